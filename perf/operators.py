@@ -230,7 +230,7 @@ def prepare(case, seed):
         S["q"], S["e"] = _encode(_activations(g, T, W, torch.bfloat16))
         S["dw"] = torch.empty(case["rows"], W, dtype=DTYPE[case["out"]], device="cuda")
         # room for partial sums and for the parts of a gradient that is not in 16 bits, kept from call to call
-        S["workspace"] = torch.empty(wgrad_room(case), dtype=torch.uint8, device="cuda")
+        S["workspace"] = torch.zeros(wgrad_room(case), dtype=torch.uint8, device="cuda")
     return S
 
 
@@ -549,7 +549,8 @@ def _held(x):
     T, W = x.shape
     x = torch.nn.functional.pad(x.double(), (0, _padded(W) - W)).unflatten(1, (-1, GROUP))
     m, k = torch.frexp(x.abs().amax(2, keepdim=True) / 127)
-    step = torch.ldexp(torch.ones_like(m), (k - (m == 0.5).int()).clamp(min=-126))
+    k = (k - (m == 0.5).int()).clamp(min=-126).long()
+    step = ((k + 1023) << 52).view(torch.float64)  # 2^k to the last bit
     return ((x / step).round() * step).flatten(1)[:, :W]
 
 
@@ -562,7 +563,7 @@ def _exact_glu(S):
 
 def _exact_wgrad(S):
     T, W = S["dy"].shape[0], S["case"]["width"]
-    step = torch.exp2(S["e"].double() - 127)
+    step = ((S["e"].long() + (1023 - 127)) << 52).view(torch.float64)
     x = (S["q"].double().view(T, -1, GROUP) * step[..., None]).flatten(1)[:, :W]
     return torch.einsum("tn,tk->nk", S["dy"].double(), x)
 
