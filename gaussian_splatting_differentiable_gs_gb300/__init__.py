@@ -91,6 +91,7 @@ def lib():
     for name in ("gs_project", "gs_bin_and_sort", "gs_workspace_status", "gs_rasterize_fwd",
                  "gs_rasterize_fwd_counted", "gs_loss_l1", "gs_rasterize_bwd", "gs_project_bwd", "gs_adam_step"):
         getattr(L, name).restype = C.c_int
+    net.declare(L)
     _lib = L
     return L
 
@@ -638,3 +639,13 @@ class TrainStep:
             self.backward(stream)
         self.update(stream)
         return self.loss
+
+
+# --------------------------------------------------------------------------
+# the network operators (include/gs_net.h)
+
+from . import net  # noqa: E402
+from .net import (Rope, act8_empty, act8_shapes, gs_act8_decode, gs_act8_encode,  # noqa: E402,F401
+                  gs_act8_wgrad, gs_act8_wgrad_workspace_bytes, gs_gated_norm_bwd,
+                  gs_gated_norm_fwd, gs_gated_norm_workspace_bytes, gs_glu_bwd, gs_glu_fwd,
+                  gs_rope)

@@ -31,8 +31,8 @@ def _sources():
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [
-        os.path.join(ROOT, "include", "gs.h"), os.path.abspath(__file__)]
+    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(
+        os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__)]
 
 
 def _compile(src, verbose):

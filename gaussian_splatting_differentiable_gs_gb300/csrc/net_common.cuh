@@ -1,0 +1,84 @@
+// net_common.cuh -- device helpers shared by the network operators.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "gs_internal.cuh"
+#include "gs_net.h"
+
+namespace gs {
+
+// N elements that move as one access of up to 16 bytes (two for 32 bytes).
+template <typename T, int N>
+struct alignas(sizeof(T) * N < 16 ? sizeof(T) * N : 16) Pack {
+  T v[N];
+};
+
+template <typename T, int N>
+__device__ __forceinline__ Pack<T, N> load_pack(const T* p) {
+  return *reinterpret_cast<const Pack<T, N>*>(p);
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_pack(T* p, const Pack<T, N>& v) {
+  *reinterpret_cast<Pack<T, N>*>(p) = v;
+}
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+
+inline int dtype_size(int32_t dtype) { return dtype == GS_F32 ? 4 : 2; }
+inline bool dtype_ok(int32_t dtype) { return dtype >= GS_BF16 && dtype <= GS_F32; }
+
+// Element alignment of a pointer, and whether every row of a matrix starts on
+// a multiple of `bytes`.
+inline bool aligned_to(const void* p, size_t bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
+}
+inline bool rows_aligned(const void* p, int64_t stride, int elem, size_t bytes) {
+  return !p || (aligned_to(p, bytes) && (stride * elem) % (int64_t)bytes == 0);
+}
+
+inline int device_sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+    return 152;
+  return n;
+}
+
+// ---- the 8-bit checkpoint's format ---------------------------------------
+// Exponent of a group from the bits of its largest magnitude: 127 = 1.984375
+// * 2^6, so a magnitude m * 2^p (1 <= m < 2) fits 127 steps of 2^(p - 6) when
+// m <= 1.984375, and of 2^(p - 5) otherwise.  255 marks a group with an
+// infinity or a NaN (magnitude bits >= 0x7f800000).
+__device__ __forceinline__ uint32_t act8_exponent(uint32_t mag_bits) {
+  if (mag_bits >= 0x7f800000u) return 255u;
+  const int e = (int)(mag_bits >> 23) - 6 + ((mag_bits & 0x7fffffu) > 0x7e0000u ? 1 : 0);
+  return e < 1 ? 1u : (uint32_t)e;
+}
+// 2^(127 - e): e = 255 gives 0 times a value, which the caller replaces by 0.
+__device__ __forceinline__ float act8_inverse(uint32_t e) {
+  return e == 255u ? 0.f : __uint_as_float((254u - e) << 23);
+}
+// The step 2^(e - 127); +inf for e = 255, so that 0 * step is the NaN that
+// such a group reads back as.
+__device__ __forceinline__ float act8_step(uint32_t e) { return __uint_as_float(e << 23); }
+
+__device__ __forceinline__ int act8_quantise(float v, float inv, uint32_t e) {
+  return e == 255u ? 0 : __float2int_rn(v * inv);
+}
+
+}  // namespace gs
