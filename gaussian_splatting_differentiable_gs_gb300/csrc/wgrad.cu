@@ -1,50 +1,712 @@
-// wgrad.cu -- gs_act8_wgrad: the weight gradient dw = dy^T x8 of a linear
-// layer from the 8-bit checkpoint of its input.
+// wgrad.cu -- gs_act8_wgrad: the weight gradient of a linear layer from the
+// 8-bit checkpoint of its input, on the tensor cores.
+//
+//   dw[n][c] = sum_t dy[t][n] * q[t][c] * 2^(e[t][c / 32] - 127)
+//
+// The product is D (channels x columns of dy) = X8^T dY, summed over tokens.
+// Both factors are read along the tokens, so both operands are "MN-major": 64
+// neighbouring channels or columns of one token are one 128-byte row of a
+// swizzled tile.  A pair of CTAs (a cluster of two) works on 256 channels x BN
+// columns with tcgen05.mma over both SMs: each CTA holds 128 channels of X8 and
+// half of the columns, so a token step costs each SM only its own half of
+// either operand.
+//
+// Warps of a CTA: one brings dy in by TMA, one the checkpoint's bytes (TMA) and
+// exponents, eight turn the bytes into bf16 (exact: at most 8 significant bits
+// times a power of two) from one ring of shared-memory stages to the next, one
+// (of the pair's first CTA) issues the products, eight add finished runs of
+// products from one half of TMEM to their registers, while the next run is
+// summed in the other half, and write the result.  The decoding warps touch shared memory only: a
+// fence or a cluster-wide release in a thread with global loads in flight
+// waits for those loads (with the bytes loaded by the decoding threads
+// themselves the same product took 2.5 times as long).
+//
+// dy enters whole in every type: bf16 by TMA as it lies in memory where its
+// rows allow it; otherwise as 1 (bf16), 2 (fp16) or 3 (fp32) bf16 terms whose
+// sum is the value (8 bits of the significand each), which a first kernel
+// writes to the workspace, and the product runs over the terms.
+//
+// Work: tiles of 256 channels x BN columns.  As many whole tiles as divide
+// evenly over the clusters are summed by one cluster each; the token steps of
+// the remaining tiles are dealt out evenly, and the partial sums of a tile
+// that several clusters share are joined in a fixed order by a second kernel.
+#include <cuda.h>
+
+#include <atomic>
+
 #include "net_common.cuh"
 
 namespace gs {
 namespace {
 
-constexpr int kTile = 64, kStep = 16;
+constexpr int kBM = 256;          // channels of a tile (two CTAs of 128)
+constexpr int kBN = 256;          // most columns of a tile
+constexpr int kBT = 64;           // tokens of a step
+constexpr int kStages = 5;        // of bf16 operands
+constexpr int kRaw = 6;           // of checkpoint bytes
+constexpr int kABytes = 128 * kBT * 2;      // a CTA's half of X8 (bf16)
+constexpr int kBBytes = kBN / 2 * kBT * 2;  // a CTA's half of dy
+constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kRawBytes = 128 * kBT;        // a CTA's 128 channels
+constexpr int kExpBytes = 4 * kBT;          // and their exponents, 4 a token
+constexpr int kBatch = 8, kBatches = 4;  // exponents: steps of a batch, batches of the ring
+constexpr int kCtrlBytes = 1024;
+constexpr int kSmem =
+    kStages * kStageBytes + kRaw * kRawBytes + kBatches * kBatch * kExpBytes + kCtrlBytes + 1024;  // + alignment
+constexpr int kDecodeWarps = 8, kTeamWarps = 4, kTeams = kDecodeWarps / kTeamWarps;
+constexpr int kItems = 4 * kBT / (32 * kTeamWarps);
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (4 + kEpiWarps + kDecodeWarps);
+// Registers a thread: the launch gives every thread kLaunchRegs, the roles
+// then share those out (sums per CTA: 61,440 at launch, 60,416 in use).
+constexpr int kLaunchRegs = 96, kCtrlRegs = 48, kEpiRegs = 160, kDecodeRegs = 56;
+static_assert(128 * kCtrlRegs + 32 * kEpiWarps * kEpiRegs + 32 * kDecodeWarps * kDecodeRegs <=
+                  kThreads * kLaunchRegs,
+              "a role would wait for registers that the launch does not have");
+// Steps that the tensor core sums on its own.  Its fp32 sum is cut, not rounded,
+// after every product of 16 tokens, so its error grows with the length: 32640
+// tokens in one run are off by 1.7e-5 of the result's norm (an fp32 product on
+// the fp32 units: 8.8e-7); in runs of 32 steps, added up in registers with
+// rounding, by 4.7e-7.
+constexpr int kChunk = 32;
+static_assert(kTeams <= kStages && kTeams <= kRaw && kBatch % kTeams == 0, "rings");
+constexpr int kMaxClusters = 128;
+constexpr size_t kPartialFloats = (size_t)128 * kBN;  // one CTA's half tile
+constexpr unsigned int kErrTimeout = 1u;
+constexpr long long kWaitNs = 2000000000ll;
 
-template <typename T, typename TO>
-__global__ void __launch_bounds__(256) wgrad_kernel(int64_t tokens, int rows, int C, const T* dy,
-                                                    int64_t dys, const int8_t* q, int64_t qs,
-                                                    const uint8_t* e, int64_t es, TO* dw,
-                                                    int64_t dws, int accumulate) {
-  __shared__ float a[kStep][kTile + 1], b[kStep][kTile + 1];
-  const int n0 = blockIdx.x * kTile, k0 = blockIdx.y * kTile;
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  float acc[4][4] = {};
-  for (int64_t t0 = 0; t0 < tokens; t0 += kStep) {
-    for (int i = threadIdx.x; i < kStep * kTile; i += 256) {
-      const int s = i / kTile, c = i % kTile;
-      const int64_t t = t0 + s;
-      a[s][c] = t < tokens && n0 + c < rows ? to_f32(dy[t * dys + n0 + c]) : 0.f;
-      b[s][c] = t < tokens && k0 + c < C
-                    ? (float)q[t * qs + k0 + c] * act8_step(e[t * es + (k0 + c) / GS_ACT8_GROUP])
-                    : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int s = 0; s < kStep; ++s)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] += a[s][ty + 16 * i] * b[s][tx + 16 * j];
-    __syncthreads();
+struct Plan {
+  int64_t tokens;
+  int32_t rows, channels;      // dw's shape
+  int32_t bn;                  // columns of a tile
+  int32_t tiles_m;             // channel tiles
+  int32_t terms;               // bf16 terms of dy
+  int64_t term_rows;           // rows of the tensor map between terms
+  int32_t steps;               // steps of a whole tile
+  int32_t clusters, waves;     // whole tiles per cluster
+  int32_t rem_tiles;           // tiles dealt out in steps
+  int64_t rem_steps, quota;    // their steps, and a cluster's share
+  int64_t dws;
+  int32_t accumulate;
+};
+
+struct Seg {
+  int tile, s0, s1;
+  int slot;  // place of a partial sum, or -1: the whole tile
+};
+
+// Calls f(seg) for the cluster's segments in order until it returns false.
+template <typename F>
+__device__ __forceinline__ void each_seg(const Plan& p, int cluster, F f) {
+  for (int w = 0; w < p.waves; ++w)
+    if (!f(Seg{w * p.clusters + cluster, 0, p.steps, -1})) return;
+  const int64_t begin = (int64_t)cluster * p.quota;
+  const int64_t end = min(begin + p.quota, p.rem_steps);
+  for (int64_t at = begin; at < end;) {
+    const int tile = (int)(at / p.steps);
+    const int64_t stop = min(end, (int64_t)(tile + 1) * p.steps);
+    Seg s;
+    s.tile = p.waves * p.clusters + tile;
+    s.s0 = (int)(at - (int64_t)tile * p.steps);
+    s.s1 = s.s0 + (int)(stop - at);
+    s.slot = s.s1 - s.s0 == p.steps ? -1 : (at == begin ? 0 : 1);
+    if (!f(s)) return;
+    at = stop;
   }
+}
+
+// The same steps one by one.
+struct Walk {
+  const Plan& p;
+  int cluster, wave, tile, k, end;
+  int64_t at, stop;
+  __device__ __forceinline__ Walk(const Plan& plan, int cl)
+      : p(plan), cluster(cl), wave(0), tile(0), k(-1), end(0) {
+    at = (int64_t)cl * p.quota;
+    stop = min(at + p.quota, p.rem_steps);
+  }
+  __device__ __forceinline__ bool next() {
+    if (++k < end) return true;
+    if (wave < p.waves) {
+      tile = wave++ * p.clusters + cluster;
+      k = 0;
+      end = p.steps;
+      return true;
+    }
+    if (at >= stop) {
+      k = end;
+      return false;
+    }
+    const int i = (int)(at / p.steps);
+    const int64_t upto = min(stop, (int64_t)(i + 1) * p.steps);
+    tile = p.waves * p.clusters + i;
+    k = (int)(at - (int64_t)i * p.steps);
+    end = k + (int)(upto - at);
+    at = upto;
+    return true;
+  }
+};
+
+__device__ __forceinline__ int64_t cluster_steps(const Plan& p, int cluster) {
+  const int64_t at = (int64_t)cluster * p.quota;
+  const int64_t dealt = min(at + p.quota, p.rem_steps) - at;
+  return (int64_t)p.waves * p.steps + (dealt > 0 ? dealt : 0);
+}
+
+// ---- mbarriers, TMA, tcgen05 (inline PTX) --------------------------------
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t in_cta0(uint32_t addr) {  // the pair's first CTA
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;"
+               ::: "memory");
+}
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {  // shared::cluster address
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// On a barrier of the pair's first CTA, for operand bytes in this CTA's own
+// shared memory: the writers' proxy fence has made them visible to the tensor
+// core, so the arrival need not order them at cluster scope.
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p;\n"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      "selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+struct Control {
+  uint64_t raw_full[kRaw], raw_empty[kRaw];      // bytes of a step
+  uint64_t exp_full[kBatches], exp_empty[kBatches];
+  uint64_t full[kStages], empty[kStages];        // both operands of both CTAs (the first's)
+  uint64_t acc_full[2], acc_empty[2];
+  uint32_t tmem;
+  volatile uint32_t abort;
+};
+
+// Waits for a barrier's phase, at most kWaitNs; false (and the status word
+// set) when that ran out or another wait of this CTA gave up.
+__device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, Control* c,
+                                            unsigned int* status) {
+  long long t0, t1;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+  while (true) {
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try(bar, parity)) return true;
+    if (c->abort) return false;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t1));
+    if (t1 - t0 > kWaitNs) {
+      c->abort = 1;
+      atomicOr(status, kErrTimeout);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, Control* c,
+                                          unsigned int* status) {
+  if (mbar_try(bar, parity)) return true;
+  return mbar_wait_slow(bar, parity, c, status);
+}
+
+__device__ __forceinline__ void tma_load_own(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                             uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+// As part of a pair's product: the barrier may be the other CTA's.
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                         uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
+// Shared-memory descriptor of an MN-major operand in 128-byte swizzled rows:
+// 64 channels are a row, 8 tokens an atom of 1024 bytes (stride between atoms
+// along the tokens), and the next 64 channels follow after kBT rows.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
+  constexpr uint64_t kMn = (uint64_t)(kBT * 128 >> 4), kTok = (uint64_t)(1024 >> 4);
+  return (uint64_t)((addr & 0x3ffff) >> 4) | (kMn << 16) | (kTok << 32) | ((uint64_t)1 << 46) |
+         ((uint64_t)2 << 61);
+}
+// Instruction descriptor: fp32 accumulator, bf16 operands, both MN-major.
+__device__ __forceinline__ uint32_t instr_desc(int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(kBM >> 4) << 24);
+}
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a), "l"(b),
+      "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+// Arrives on the same barrier of both CTAs once the products issued so far are done.
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(bar), "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_load8(uint32_t addr, float (&r)[8]) {
+  uint32_t v[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+                 "=r"(v[7])
+               : "r"(addr)
+               : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = n0 + ty + 16 * i, c = k0 + tx + 16 * j;
-      if (n < rows && c < C) {
-        TO* p = dw + n * dws + c;
-        *p = from_f32<TO>(acc[i][j] + (accumulate ? to_f32(*p) : 0.f));
+  for (int i = 0; i < 8; ++i) r[i] = __uint_as_float(v[i]);
+}
+
+template <typename TO>
+__device__ __forceinline__ void put_dw(TO* p, float v, int accumulate) {
+  *p = from_f32<TO>(accumulate ? v + to_f32(*p) : v);
+}
+
+// Four bytes of the checkpoint to four bf16 values times a step (a pair of
+// equal bf16).  A byte b = 128 s + m (two's complement: the value is m - 128 s)
+// sits in the significand of 128 + m; taking 128 (s = 0) or 256 (s = 1), whose
+// bf16 patterns differ by that very bit, from it leaves the value.  Exact.
+__device__ __forceinline__ uint32_t decode2(uint32_t bytes, __nv_bfloat162 step) {
+  const uint32_t m = (bytes & 0x007f007fu) | 0x43004300u;
+  const uint32_t c = (bytes & 0x00800080u) | 0x43004300u;
+  const __nv_bfloat162 v = __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&m),
+                                           *reinterpret_cast<const __nv_bfloat162*>(&c)),
+                                   step);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint4 decode8(uint32_t lo, uint32_t hi, __nv_bfloat162 step) {
+  uint4 r;
+  r.x = decode2(__byte_perm(lo, 0, 0x4140), step);
+  r.y = decode2(__byte_perm(lo, 0, 0x4342), step);
+  r.z = decode2(__byte_perm(hi, 0, 0x4140), step);
+  r.w = decode2(__byte_perm(hi, 0, 0x4342), step);
+  return r;
+}
+
+template <typename TO>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    wgrad_kernel(const __grid_constant__ Plan p, const __grid_constant__ CUtensorMap dy_map,
+                 const __grid_constant__ CUtensorMap q_map, const uint8_t* __restrict__ e,
+                 int64_t es, TO* dw, float* partial, unsigned int* status) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* raw_q = smem + kStages * kStageBytes;
+  uint8_t* raw_e = raw_q + kRaw * kRawBytes;
+  Control* c = (Control*)(raw_e + kBatches * kBatch * kExpBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int cluster = blockIdx.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_u32(&c->full[i]), 1 + 2 * kTeamWarps);  // dy's bytes; both CTAs' X8
+      mbar_init(smem_u32(&c->empty[i]), 1);
+    }
+    for (int i = 0; i < kRaw; ++i) {
+      mbar_init(smem_u32(&c->raw_full[i]), 1);
+      mbar_init(smem_u32(&c->raw_empty[i]), kTeamWarps);
+    }
+    for (int i = 0; i < kBatches; ++i) {
+      mbar_init(smem_u32(&c->exp_full[i]), 1);
+      mbar_init(smem_u32(&c->exp_empty[i]), kBatch * kTeamWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&c->acc_full[i]), 1);
+      mbar_init(smem_u32(&c->acc_empty[i]), 2 * kEpiWarps);
+    }
+    c->abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_u32(&c->tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  cluster_sync();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = c->tmem;
+
+  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtrlRegs));
+  if (warp == 0) {
+    // ---- dy by TMA: this CTA's half of the tile's columns ------------------
+    if (lane == 0) {
+      uint32_t it = 0;
+      const int half = p.bn / 2;
+      each_seg(p, cluster, [&](const Seg& s) {
+        const int x0 = s.tile / p.tiles_m * p.bn + (int)rank * half;
+        for (int k = s.s0; k < s.s1; ++k, ++it) {
+          const uint32_t st = it % kStages, ph = (it / kStages) & 1;
+          if (!mbar_wait(smem_u32(&c->empty[st]), ph ^ 1, c, status)) return false;
+          const uint32_t bar = smem_u32(&c->full[st]);
+          if (rank == 0) mbar_expect(bar, (uint32_t)(half * kBT * 2 * 2));
+          const uint32_t dst = smem_u32(smem + st * kStageBytes + kABytes);
+          const int y = (int)((k % p.terms) * p.term_rows) + k / p.terms * kBT;
+          for (int b = 0; b < half / 64; ++b)
+            tma_load(dst + b * (kBT * 128), &dy_map, x0 + b * 64, y, in_cta0(bar));
+        }
+        return true;
+      });
+      // the last products release the last stages: every arrival is in before this CTA ends
+      for (uint32_t back = it < kStages ? it : kStages; back > 0; --back) {
+        const uint32_t i = it - back;
+        if (!mbar_wait(smem_u32(&c->empty[i % kStages]), (i / kStages) & 1, c, status)) break;
       }
     }
+  } else if (warp == 1) {
+    // ---- products ----------------------------------------------------------
+    if (rank == 0 && lane == 0) {
+      const uint32_t idesc = instr_desc(p.bn);
+      uint32_t it = 0, chunk = 0;
+      each_seg(p, cluster, [&](const Seg& s) {
+        for (int k = s.s0; k < s.s1; ++k, ++it) {
+          const bool first = (k - s.s0) % kChunk == 0;
+          const uint32_t buf = chunk & 1;
+          if (first) {
+            if (!mbar_wait(smem_u32(&c->acc_empty[buf]), ((chunk >> 1) & 1) ^ 1, c, status))
+              return false;
+          }
+          const uint32_t st = it % kStages;
+          if (!mbar_wait(smem_u32(&c->full[st]), (it / kStages) & 1, c, status)) return false;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const uint64_t a = smem_desc(smem_u32(smem + st * kStageBytes));
+          const uint64_t b = smem_desc(smem_u32(smem + st * kStageBytes + kABytes));
+#pragma unroll
+          for (int i = 0; i < kBT / 16; ++i)  // 16 tokens are two atoms: 2048 bytes
+            mma(tmem + buf * kBN, a + (i * 2048 >> 4), b + (i * 2048 >> 4), idesc, !first || i > 0);
+          mma_commit(smem_u32(&c->empty[st]));
+          if ((k - s.s0) % kChunk == kChunk - 1 || k + 1 == s.s1) {
+            mma_commit(smem_u32(&c->acc_full[buf]));
+            ++chunk;
+          }
+        }
+        return true;
+      });
+    }
+  } else if (warp == 3) {
+    // ---- the checkpoint's bytes by TMA -------------------------------------
+    if (lane == 0) {
+      Walk w(p, cluster);
+      for (uint32_t it = 0; w.next(); ++it) {
+        const uint32_t rs = it % kRaw, bar = smem_u32(&c->raw_full[rs]);
+        if (!mbar_wait(smem_u32(&c->raw_empty[rs]), ((it / kRaw) & 1) ^ 1, c, status)) break;
+        mbar_expect(bar, kRawBytes);
+        tma_load_own(smem_u32(raw_q + rs * kRawBytes), &q_map,
+                     w.tile % p.tiles_m * kBM + (int)rank * 128, w.k / p.terms * kBT, bar);
+      }
+    }
+  } else if (warp == 2) {
+    // ---- and its exponents, kBatch steps at a time ---------------------------
+    // Exponent rows start anywhere, so they come by plain loads; the arrival
+    // that hands a batch on waits for those loads, once for kBatch steps.
+    Walk w(p, cluster);
+    const int groups = (p.channels + GS_ACT8_GROUP - 1) / GS_ACT8_GROUP;
+    const bool words = ((es | (int64_t)(uintptr_t)e) & 3) == 0;
+    const uint32_t total = (uint32_t)cluster_steps(p, cluster);
+    for (uint32_t it0 = 0; it0 < total; it0 += kBatch) {
+      uint32_t x[kBatch][2];  // four groups of tokens lane and lane + 32
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        x[i][0] = x[i][1] = 0x01010101u;
+        if (!w.next()) continue;
+        const int g = w.tile % p.tiles_m * (kBM / GS_ACT8_GROUP) + (int)rank * 4;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int64_t t = (int64_t)(w.k / p.terms) * kBT + lane + 32 * h;
+          if (t >= p.tokens) continue;
+          const uint8_t* src = e + t * es + g;
+          if (words && g + 4 <= groups) {
+            x[i][h] = __ldg(reinterpret_cast<const uint32_t*>(src));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (g + j < groups)
+                x[i][h] = (x[i][h] & ~(0xffu << 8 * j)) | (uint32_t)__ldg(src + j) << 8 * j;
+          }
+        }
+      }
+      const uint32_t n = it0 / kBatch, bs = n % kBatches;
+      if (!__all_sync(0xffffffffu,
+                      mbar_wait(smem_u32(&c->exp_empty[bs]), ((n / kBatches) & 1) ^ 1, c, status)))
+        break;
+      uint32_t* to = reinterpret_cast<uint32_t*>(raw_e + bs * kBatch * kExpBytes);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        to[i * 64 + lane] = x[i][0];
+        to[i * 64 + lane + 32] = x[i][1];
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&c->exp_full[bs]));
+    }
+  } else if (warp < 4 + kEpiWarps) {
+    // ---- chunks of the sum from TMEM into registers, then to memory ----------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
+    const int quarter = warp & 3;  // the TMEM lanes this warp may read
+    const int cols = p.bn / 2, c0 = (warp - 4) / 4 * cols;
+    const int row = quarter * 32 + lane;
+    uint32_t chunk = 0;
+    each_seg(p, cluster, [&](const Seg& s) {
+      float acc[kBN / 2];
+#pragma unroll
+      for (int j = 0; j < kBN / 2; ++j) acc[j] = 0.f;
+      for (int k = s.s0; k < s.s1; k += kChunk, ++chunk) {
+        const uint32_t buf = chunk & 1;
+        if (!__all_sync(0xffffffffu,
+                        mbar_wait(smem_u32(&c->acc_full[buf]), (chunk >> 1) & 1, c, status)))
+          return false;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t from = tmem + buf * kBN + c0 + ((uint32_t)(quarter * 32) << 16);
+#pragma unroll
+        for (int j = 0; j < kBN / 2; j += 8)
+          if (j < cols) {
+            float r[8];
+            tmem_load8(from + j, r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[j + i] += r[i];
+          }
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(in_cta0(smem_u32(&c->acc_empty[buf])));
+      }
+      const int n0 = s.tile / p.tiles_m * p.bn + c0;
+      const int ch = s.tile % p.tiles_m * kBM + (int)rank * 128 + row;
+      if (s.slot < 0) {
+        TO* to = dw + (int64_t)n0 * p.dws + ch;
+#pragma unroll
+        for (int j = 0; j < kBN / 2; ++j, to += p.dws)
+          if (ch < p.channels && j < cols && n0 + j < p.rows) put_dw<TO>(to, acc[j], p.accumulate);
+      } else {
+        float* to = partial + ((size_t)(cluster * 2 + s.slot) * 2 + rank) * kPartialFloats +
+                    c0 * 128 + row;
+#pragma unroll
+        for (int j = 0; j < kBN / 2; ++j)
+          if (j < cols) to[j * 128] = acc[j];
+      }
+      return true;
+    });
+  } else {
+    // ---- bytes to bf16 -------------------------------------------------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDecodeRegs));
+    // kTeams teams of warps take the steps in turn: a step's waits, loads and
+    // fence then overlap with those of the next steps.  A thread's items are one
+    // token and one group of 32 channels each.
+    const int team = (warp - 4 - kEpiWarps) / kTeamWarps;
+    const int id = threadIdx.x - 32 * (4 + kEpiWarps) - team * kTeamWarps * 32;
+    const int grp = id & 3;
+    const uint32_t total = (uint32_t)cluster_steps(p, cluster);
+    for (uint32_t it = team; it < total; it += kTeams) {
+      const uint32_t rs = it % kRaw, st = it % kStages, n = it / kBatch, bs = n % kBatches;
+      if (!__all_sync(0xffffffffu,
+                      mbar_wait(smem_u32(&c->exp_full[bs]), (n / kBatches) & 1, c, status) &&
+                          mbar_wait(smem_u32(&c->raw_full[rs]), (it / kRaw) & 1, c, status)))
+        break;
+      // The order of an item's two 16-byte halves: eight neighbouring lanes (two
+      // tokens, four groups) then read, and store, eight different 16-byte banks.
+      uint4 v[kItems][2];
+      __nv_bfloat162 step[kItems];
+#pragma unroll
+      for (int i = 0; i < kItems; ++i) {
+        const int tok = (id >> 2) + i * (kTeamWarps * 8), flip = (grp >> 1) ^ (tok & 1);
+        const uint4* from =
+            reinterpret_cast<const uint4*>(raw_q + rs * kRawBytes + tok * 128 + grp * 32);
+        v[i][0] = from[flip];
+        v[i][1] = from[flip ^ 1];
+        const uint32_t ex = raw_e[(it % (kBatch * kBatches)) * kExpBytes + tok * 4 + grp];
+        const uint32_t s2 = ex << 7 | ex << 23;
+        step[i] = *reinterpret_cast<const __nv_bfloat162*>(&s2);
+      }
+      if (!__all_sync(0xffffffffu,
+                      mbar_wait(smem_u32(&c->empty[st]), ((it / kStages) & 1) ^ 1, c, status)))
+        break;
+#pragma unroll
+      for (int i = 0; i < kItems; ++i) {
+        const int tok = (id >> 2) + i * (kTeamWarps * 8), flip = (grp >> 1) ^ (tok & 1);
+        uint8_t* a = smem + st * kStageBytes + (grp >> 1) * (kBT * 128) + tok * 128;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int chunk = (grp & 1) * 4 + (h ^ flip) * 2;
+          *reinterpret_cast<uint4*>(a + ((chunk ^ (tok & 7)) << 4)) =
+              decode8(v[i][h].x, v[i][h].y, step[i]);
+          *reinterpret_cast<uint4*>(a + (((chunk + 1) ^ (tok & 7)) << 4)) =
+              decode8(v[i][h].z, v[i][h].w, step[i]);
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive_pair(in_cta0(smem_u32(&c->full[st])));
+        mbar_arrive(smem_u32(&c->raw_empty[rs]));
+        mbar_arrive(smem_u32(&c->exp_empty[bs]));
+      }
+    }
+  }
+
+  // Every role is done or gave up.  After giving up, copies may still be in
+  // flight into this CTA's shared memory: leave them time to land.
+  __syncthreads();
+  __syncwarp();
+  if (c->abort)
+    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  cluster_sync();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  if (warp == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
+
+// Joins the partial sums of the tiles that several clusters share: a block
+// takes 16 columns of a CTA's half tile, a thread one channel.
+constexpr int kJoinCols = 16;
+template <typename TO>
+__global__ void __launch_bounds__(128) wgrad_join_kernel(const __grid_constant__ Plan p,
+                                                         const float* __restrict__ partial,
+                                                         TO* dw) {
+  const int per_half = p.bn / kJoinCols;
+  const int tile = blockIdx.x / (2 * per_half);
+  const int rank = blockIdx.x / per_half % 2, c0 = blockIdx.x % per_half * kJoinCols;
+  const int64_t first = (int64_t)tile * p.steps, last = first + p.steps - 1;
+  const int lo = (int)(first / p.quota), hi = (int)(last / p.quota);
+  if (lo == hi) return;  // summed by one cluster, and written by it
+  const int id = p.waves * p.clusters + tile;
+  const int n0 = id / p.tiles_m * p.bn + c0;
+  const int ch = id % p.tiles_m * kBM + rank * 128 + threadIdx.x;
+  if (ch >= p.channels) return;
+  float v[kJoinCols] = {};
+  for (int cl = lo; cl <= hi; ++cl) {
+    const int slot = (int64_t)cl * p.quota / p.steps == tile ? 0 : 1;
+    const float* from = partial + ((size_t)(cl * 2 + slot) * 2 + rank) * kPartialFloats +
+                        (size_t)c0 * 128 + threadIdx.x;
+#pragma unroll
+    for (int j = 0; j < kJoinCols; ++j) v[j] += from[j * 128];
+  }
+#pragma unroll
+  for (int j = 0; j < kJoinCols; ++j)
+    if (n0 + j < p.rows) put_dw<TO>(dw + (int64_t)(n0 + j) * p.dws + ch, v[j], p.accumulate);
+}
+
+// dy [tokens][rows] as `terms` bf16 matrices [padded tokens][ld], the next
+// 8 bits of the significand in each (cut, not rounded: the rest is exact).
+template <typename T>
+__global__ void __launch_bounds__(256) wgrad_terms_kernel(int64_t tokens, int64_t padded, int rows,
+                                                          int ld, int terms, const T* dy,
+                                                          int64_t dys, __nv_bfloat16* out) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t t = i / (ld / 2);
+  const int n = (int)(i % (ld / 2)) * 2;
+  if (t >= padded) return;
+  float v[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    v[j] = t < tokens && n + j < rows ? to_f32(dy[t * dys + n + j]) : 0.f;
+  for (int k = 0; k < terms; ++k) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t bits = __float_as_uint(v[j]);
+      uint32_t top = bits & 0xffff0000u;
+      if ((bits & 0x7fffffffu) > 0x7f800000u) top |= 0x00400000u;  // a NaN stays one
+      const bool finite = (bits & 0x7f800000u) != 0x7f800000u;
+      v[j] = finite ? v[j] - __uint_as_float(top) : 0.f;
+      w |= j ? top : top >> 16;
+    }
+    *reinterpret_cast<uint32_t*>(out + (k * padded + t) * ld + n) = w;
+  }
+}
+
+int64_t padded_tokens(int64_t tokens) { return div_up(tokens, kBT) * kBT; }
+int padded_rows(int rows) { return (int)div_up(rows, 8) * 8; }
+int terms_of(int32_t dtype) { return dtype == GS_BF16 ? 1 : dtype == GS_F16 ? 2 : 3; }
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                             const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                             const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static std::atomic<void*> fn{nullptr};
+  void* f = fn.load(std::memory_order_acquire);
+  if (!f) {
+    cudaDriverEntryPointQueryResult res;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &res) != cudaSuccess ||
+        res != cudaDriverEntryPointSuccess) {
+      (void)cudaGetLastError();
+      return nullptr;
+    }
+    fn.store(f, std::memory_order_release);
+  }
+  return (EncodeFn)f;
+}
+
+// Clusters of two that run at once on the current device (0: none).  Looked up
+// once per device, with the kernels' shared memory limits.
+int resident_clusters() {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> known[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+  int n = known[dev].load(std::memory_order_acquire);
+  if (n) return n;
+  for (const void* f : {(const void*)wgrad_kernel<float>, (const void*)wgrad_kernel<__nv_bfloat16>})
+{
+    cudaFuncAttributes a;
+    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
+        cudaFuncGetAttributes(&a, f) != cudaSuccess || a.numRegs != kLaunchRegs)
+      return 0;  // other registers at launch than the roles were given
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, wgrad_kernel<float>, &cfg) != cudaSuccess || n < 1) return 0;
+  if (n > kMaxClusters) n = kMaxClusters;
+  known[dev].store(n, std::memory_order_release);
+  return n;
+}
+
+constexpr size_t kHeader = 256;
+size_t partial_bytes() { return sizeof(float) * kPartialFloats * 4 * kMaxClusters; }
 
 }  // namespace
 }  // namespace gs
@@ -53,8 +715,10 @@ using namespace gs;
 
 extern "C" size_t gs_act8_wgrad_workspace_bytes(int64_t tokens, int32_t rows, int32_t channels,
                                                 int32_t dtype) {
-  if (tokens < 0 || rows < 1 || channels < 1 || !dtype_ok(dtype)) return 0;
-  return 256;
+  if (tokens < 0 || tokens >= ((int64_t)1 << 31) || rows < 1 || channels < 1 || !dtype_ok(dtype))
+    return 0;
+  return kHeader + partial_bytes() +
+         sizeof(__nv_bfloat16) * terms_of(dtype) * padded_tokens(tokens) * padded_rows(rows);
 }
 
 extern "C" gs_status gs_act8_wgrad(int64_t tokens, int32_t rows, int32_t channels, int32_t dtype,
@@ -68,21 +732,106 @@ extern "C" gs_status gs_act8_wgrad(int64_t tokens, int32_t rows, int32_t channel
       ws_bytes < gs_act8_wgrad_workspace_bytes(tokens, rows, channels, dtype))
     return GS_ERR_INVALID_ARG;
   if (tokens > 0 && (!dy || !q || !e || !aligned_to(dy, dtype_size(dtype)) || !aligned16(q) ||
-                     q_stride % 16))
+                     q_stride % 16 ||
+                     q_stride < div_up(channels, GS_ACT8_GROUP) * GS_ACT8_GROUP))
     return GS_ERR_INVALID_ARG;
-  const dim3 grid((unsigned)div_up(rows, kTile), (unsigned)div_up(channels, kTile));
   cudaStream_t st = (cudaStream_t)stream;
-#define GS_WGRAD(T, TO)                                                                        \
-  wgrad_kernel<T, TO><<<grid, 256, 0, st>>>(tokens, rows, channels, (const T*)dy, dy_stride, q, \
-                                            q_stride, e, e_stride, (TO*)dw, dw_stride,          \
-                                            accumulate)
-#define GS_WGRAD_OUT(T) \
-  do { if (out_dtype == GS_F32) GS_WGRAD(T, float); else GS_WGRAD(T, __nv_bfloat16); } while (0)
-  if (dtype == GS_BF16) GS_WGRAD_OUT(__nv_bfloat16);
-  else if (dtype == GS_F16) GS_WGRAD_OUT(__half);
-  else GS_WGRAD_OUT(float);
-#undef GS_WGRAD_OUT
-#undef GS_WGRAD
+  const size_t out_elem = dtype_size(out_dtype);
+  if (tokens == 0) {
+    if (!accumulate)
+      GS_CUDA(cudaMemset2DAsync(dw, dw_stride * out_elem, 0, channels * out_elem, rows, st));
+    return GS_OK;
+  }
+  const EncodeFn encode = encode_fn();
+  const int clusters = resident_clusters();
+  if (!encode || !clusters) {
+    (void)cudaGetLastError();
+    return GS_ERR_CUDA;
+  }
+
+  Plan p{};
+  p.tokens = tokens;
+  p.rows = rows;
+  p.channels = channels;
+  p.bn = rows > 128 ? 256 : 128;
+  p.dws = dw_stride;
+  p.accumulate = accumulate != 0;
+  float* partial = (float*)((char*)workspace + kHeader);
+
+  // dy as the tensor map reads it
+  const bool direct =
+      dtype == GS_BF16 && rows_aligned(dy, dy_stride, 2, 16) && dy_stride >= rows;
+  const void* src = dy;
+  int64_t height = tokens, stride = dy_stride;
+  p.terms = 1;
+  p.term_rows = 0;
+  if (!direct) {
+    p.terms = terms_of(dtype);
+    p.term_rows = padded_tokens(tokens);
+    const int ld = padded_rows(rows);
+    __nv_bfloat16* out = (__nv_bfloat16*)((char*)partial + partial_bytes());
+    const unsigned blocks = (unsigned)div_up(p.term_rows * (ld / 2), 256);
+    if (dtype == GS_BF16)
+      wgrad_terms_kernel<<<blocks, 256, 0, st>>>(tokens, p.term_rows, rows, ld, 1,
+                                                 (const __nv_bfloat16*)dy, dy_stride, out);
+    else if (dtype == GS_F16)
+      wgrad_terms_kernel<<<blocks, 256, 0, st>>>(tokens, p.term_rows, rows, ld, 2,
+                                                 (const __half*)dy, dy_stride, out);
+    else
+      wgrad_terms_kernel<<<blocks, 256, 0, st>>>(tokens, p.term_rows, rows, ld, 3,
+                                                 (const float*)dy, dy_stride, out);
+    GS_CHECK_LAUNCH();
+    src = out;
+    height = p.terms * p.term_rows;
+    stride = ld;
+  }
+  if (height > ((int64_t)1 << 31) - kBT) return GS_ERR_INVALID_ARG;
+  CUtensorMap map;
+  const cuuint64_t dims[2] = {(cuuint64_t)rows, (cuuint64_t)height};
+  const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
+  const cuuint32_t box[2] = {64, kBT}, unit[2] = {1, 1};
+  if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(src), dims, strides, box,
+             unit, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return GS_ERR_CUDA;
+
+  CUtensorMap qmap;
+  const cuuint64_t qdims[2] = {(cuuint64_t)div_up(channels, GS_ACT8_GROUP) * GS_ACT8_GROUP,
+                               (cuuint64_t)tokens};
+  const cuuint64_t qstrides[1] = {(cuuint64_t)q_stride};
+  const cuuint32_t qbox[2] = {128, kBT};
+  if (encode(&qmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(q), qdims, qstrides, qbox,
+             unit, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return GS_ERR_CUDA;
+
+  p.tiles_m = (int)div_up(channels, kBM);
+  const int64_t tiles = p.tiles_m * div_up(rows, p.bn);
+  p.steps = (int)(div_up(tokens, kBT) * p.terms);
+  p.clusters = clusters;
+  p.waves = (int)(tiles / clusters);
+  p.rem_tiles = (int)(tiles - (int64_t)p.waves * clusters);
+  p.rem_steps = (int64_t)p.rem_tiles * p.steps;
+  // A share of the dealt-out steps is worth its partial sum from kMinSteps on.
+  constexpr int64_t kMinSteps = 8;
+  p.quota = div_up(p.rem_steps, clusters);
+  if (p.quota < kMinSteps) p.quota = kMinSteps < p.steps ? kMinSteps : p.steps;
+  const int used = p.waves ? clusters : (int)div_up(p.rem_steps, p.quota);
+  unsigned int* status = (unsigned int*)((char*)workspace + kWsStatusOffset);
+  if (out_dtype == GS_F32)
+    wgrad_kernel<float><<<2 * used, kThreads, kSmem, st>>>(p, map, qmap, e, e_stride,
+                                                           (float*)dw, partial, status);
+  else
+    wgrad_kernel<__nv_bfloat16><<<2 * used, kThreads, kSmem, st>>>(
+        p, map, qmap, e, e_stride, (__nv_bfloat16*)dw, partial, status);
   GS_CHECK_LAUNCH();
+  if (p.rem_tiles && p.quota % p.steps != 0) {
+    const unsigned blocks = (unsigned)(p.rem_tiles * 2 * (p.bn / kJoinCols));
+    if (out_dtype == GS_F32)
+      wgrad_join_kernel<float><<<blocks, 128, 0, st>>>(p, partial, (float*)dw);
+    else
+      wgrad_join_kernel<__nv_bfloat16><<<blocks, 128, 0, st>>>(p, partial, (__nv_bfloat16*)dw);
+    GS_CHECK_LAUNCH();
+  }
   return GS_OK;
 }

@@ -140,7 +140,7 @@ gs_status gs_gated_norm_bwd(const gs_norm* p, const void* x_out, int64_t x_strid
  * in bf16 and fp32.  A group with an infinity or a NaN has e = 255, q = 0 and
  * reads back as NaN.  Storage: q int8 [tokens][ld], e uint8 [tokens][ld / 32]
  * with ld = C rounded up to 32 (the padding is zero); q rows are 16-byte
- * aligned (q_stride a multiple of 16). */
+ * aligned (q_stride a multiple of 16, at least ld). */
 #define GS_ACT8_GROUP 32
 
 gs_status gs_act8_encode(int64_t tokens, int32_t channels, int32_t dtype, const void* x,
