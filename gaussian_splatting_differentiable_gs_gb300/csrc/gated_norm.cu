@@ -11,13 +11,17 @@
 // and the sums over rows need two column sums only: dw_pre = sum_t dy n, and
 // per gate group e_G = sum_{t in G} d m, from which dw_post = sum_G s g_G e_G,
 // dres_scale = sum_G g_G w_post e_G and dgate_G = s w_post e_G.
+#include <atomic>
+
 #include "net_common.cuh"
 
 namespace gs {
 namespace {
 
-constexpr int kNormCtas = 304;      // row ranges of the backward (column sums)
+constexpr int kNormCtas = 304;      // most row ranges of the backward (column sums)
 constexpr int kMaxTeamWarps = 16;
+constexpr int kTeamThreads = 512;   // most threads of a CTA
+constexpr int kSmemBudget = 224 * 1024;
 
 struct NormK {
   int64_t tokens;
@@ -29,24 +33,37 @@ struct NormK {
   const int32_t* offsets;
 };
 
-// Sum of one value per thread over a team of `warps` warps, the same bits in
-// every thread.  red: two slots of kMaxTeamWarps floats per team, used in
-// turn: a slot is written again only after the barrier of the sum in between.
+// Sums of one or two values per thread over a team of `warps` warps, the same
+// bits in every thread.  red: two slots of 2 kMaxTeamWarps floats per team,
+// used in turn: a slot is written again only after the barrier of the sum in
+// between.
 struct TeamSum {
   float* red;
   int warps, warp, bar;
   int turn;
-  __device__ __forceinline__ float operator()(float v) {
+  __device__ __forceinline__ void operator()(float& a, float& b, bool both) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (warps == 1) return v;
-    float* r = red + (turn & 1) * kMaxTeamWarps;
+    for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    if (both) {
+#pragma unroll
+      for (int o = 16; o; o >>= 1) b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    if (warps == 1) return;
+    float2* r = reinterpret_cast<float2*>(red) + (turn & 1) * kMaxTeamWarps;
     ++turn;
-    if ((threadIdx.x & 31) == 0) r[warp] = v;
+    if ((threadIdx.x & 31) == 0) r[warp] = make_float2(a, b);
     asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(warps * 32) : "memory");
-    float s = 0.f;
-    for (int i = 0; i < warps; ++i) s += r[i];
-    return s;
+    a = b = 0.f;
+    for (int i = 0; i < warps; ++i) {
+      const float2 v = r[i];
+      a += v.x;
+      b += v.y;
+    }
+  }
+  __device__ __forceinline__ float operator()(float v) {
+    float none = 0.f;
+    (*this)(v, none, false);
+    return v;
   }
 };
 
@@ -60,21 +77,79 @@ __device__ __forceinline__ int find_group(const int32_t* offsets, int groups, in
   return lo;
 }
 
+// A thread's share of the rows to come.  Rows whose vectors are 4 or 16 bytes
+// are copied asynchronously into shared memory, kDepth - 1 rows ahead; every
+// thread copies what it reads itself, so nothing but its own copies is waited
+// for.  Single 16-bit values (rows that start anywhere) cannot be copied so:
+// they are held in registers, one row ahead.
 template <typename T, int VEC, int NV>
-__device__ __forceinline__ void load_row(float (&v)[VEC * NV], const T* p, int first, int step,
-                                         int C) {
+struct Rows {
+  static constexpr int kChunk = VEC * sizeof(T) >= 16 ? 16 : VEC * sizeof(T);
+  static constexpr int kPer = VEC * sizeof(T) / kChunk, kChunks = NV * kPer;
+  static constexpr bool kRing = kChunk >= 4;
+  static constexpr int kBytes = kRing ? kChunks * kChunk : 0;  // per thread and row
+
+  const T* base;  // NULL: zeros
+  int64_t stride;
+  T held[kRing ? 1 : VEC * NV];
+
+  __device__ __forceinline__ void fetch(char* slot, int64_t t, int first, int step, int C) {
+    if (!kRing || !base) return;
+    const T* p = base + t * stride;
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(slot) + threadIdx.x * kChunk;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = first + i * step;
-    if (c < C) {
-      const Pack<T, VEC> w = load_pack<T, VEC>(p + c);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) v[i * VEC + j] = to_f32(w.v[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) v[i * VEC + j] = 0.f;
+    for (int i = 0; i < kChunks; ++i) {
+      const int c = first + i / kPer * step + i % kPer * (kChunk / (int)sizeof(T));
+      if (c < C) {
+        if (kChunk == 16)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                           to + i * (int)blockDim.x * kChunk),
+                       "l"(p + c)
+                       : "memory");
+        else
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                           to + i * (int)blockDim.x * kChunk),
+                       "l"(p + c)
+                       : "memory");
+      }
     }
   }
+  __device__ __forceinline__ void hold(int64_t t, int first, int step, int C) {
+    if (kRing || !base) return;
+    const T* p = base + t * stride;
+#pragma unroll
+    for (int i = 0; i < (kRing ? 0 : VEC * NV); ++i)
+      if (first + i * step < C) held[i] = p[first + i * step];
+  }
+  __device__ __forceinline__ void read(float (&v)[VEC * NV], const char* slot, int first, int step,
+                                       int C) const {
+    constexpr int kEl = kChunk / (int)sizeof(T);
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      const int c = first + i / kPer * step + i % kPer * kEl;
+      if (base && c < C) {
+        if (kRing) {
+          const Pack<T, kEl> w = load_pack<T, kEl>(reinterpret_cast<const T*>(
+              slot + (i * (int)blockDim.x + (int)threadIdx.x) * kChunk));
+#pragma unroll
+          for (int j = 0; j < kEl; ++j) v[i * kEl + j] = to_f32(w.v[j]);
+        } else {
+          v[i] = to_f32(held[i]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < kEl; ++j) v[i * kEl + j] = 0.f;
+      }
+    }
+  }
+};
+
+template <int N>
+__device__ __forceinline__ void copies_done_but() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
 template <typename T, int VEC, int NV>
@@ -131,48 +206,94 @@ __device__ __forceinline__ void row_stats(float (&v)[VEC * NV], TeamSum& sum, co
   rstd = rsqrtf(sum(s) * k.inv_c + k.eps);
 }
 
-template <typename TB, typename TX, int VEC, int NV>
-__global__ void __launch_bounds__(512) norm_fwd_kernel(
-    NormK k, const TX* x, int64_t x_stride, const TB* block, int64_t block_stride, TX* x_out,
-    int64_t x_out_stride, TB* y, int64_t y_stride, float4* stats, int8_t* y_q, int64_t q_stride,
-    uint8_t* y_e, int64_t e_stride, int warps) {
-  __shared__ float red[16][2][kMaxTeamWarps];
+// k = res_scale * gate * w_post of a group, per channel
+template <typename TB, int VEC, int NV>
+__device__ __forceinline__ void group_weights(float (&wk)[VEC * NV], const NormK& k, int g,
+                                              int first, int step) {
+#pragma unroll
+  for (int i = 0; i < VEC * NV; ++i) wk[i] = 1.f;
+  scale_row<float, VEC, NV>(wk, k.scale, first, step, k.C);
+  if (k.post) scale_row<float, VEC, NV>(wk, k.w_post, first, step, k.C);
+  if (k.gate) scale_row<TB, VEC, NV>(wk, (const TB*)k.gate + (int64_t)g * k.C, first, step, k.C);
+}
+
+// A CTA takes rows [cta R, cta R + R); its teams take them in turn and keep the
+// weights of their channels in registers.
+template <typename TB, typename TX, int VEC, int NV, int DEPTH>
+__global__ void __launch_bounds__(kTeamThreads, VEC * NV <= 8 ? 2 : 1) norm_fwd_kernel(
+    const __grid_constant__ NormK k, const TX* x, int64_t x_stride, const TB* block,
+    int64_t block_stride, TX* x_out, int64_t x_out_stride, TB* y, int64_t y_stride, float4* stats,
+    int8_t* y_q, int64_t q_stride, uint8_t* y_e, int64_t e_stride, int64_t rows_per_cta,
+    int warps) {
+  extern __shared__ __align__(16) char smem[];
+  constexpr int E = VEC * NV;
+  using RX = Rows<TX, VEC, NV>;
+  using RB = Rows<TB, VEC, NV>;
   const int warp = threadIdx.x >> 5;
   const int team = warp / warps, teams = (blockDim.x >> 5) / warps;
-  TeamSum sum{&red[team][0][0], warps, warp - team * warps, team + 1, 0};
+  const int slot_bytes = (RX::kBytes + RB::kBytes) * blockDim.x;
+  TeamSum sum{reinterpret_cast<float*>(smem + DEPTH * slot_bytes) + team * 4 * kMaxTeamWarps, warps,
+              warp - team * warps, team + 1, 0};
   const int lane = threadIdx.x - team * warps * 32;
   const int first = lane * VEC, step = warps * 32 * VEC;
 
-  for (int64_t t = (int64_t)blockIdx.x * teams + team; t < k.tokens;
-       t += (int64_t)gridDim.x * teams) {
-    float v[VEC * NV];
+  const int64_t begin = (int64_t)blockIdx.x * rows_per_cta + team;
+  const int64_t end = min((int64_t)(blockIdx.x + 1) * rows_per_cta, k.tokens);
+  RX rx{x, x_stride};
+  RB rb{block, block_stride};
+  auto ask = [&](int s, int64_t t) {
+    if (t < end) {
+      rx.fetch(smem + s * slot_bytes, t, first, step, k.C);
+      rb.fetch(smem + s * slot_bytes + RX::kBytes * blockDim.x, t, first, step, k.C);
+    }
+    copies_commit();
+  };
+  auto hold = [&](int64_t t) {
+    if (t < end) {
+      rx.hold(t, first, step, k.C);
+      rb.hold(t, first, step, k.C);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < DEPTH - 1; ++i) ask(i, begin + (int64_t)i * teams);
+  hold(begin);
+
+  float wp[E], wk[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) wp[i] = 1.f;
+  scale_row<float, VEC, NV>(wp, k.w_pre, first, step, k.C);
+  int g = -1;
+  int64_t group_end = 0;
+
+  int s = 0;
+  for (int64_t t = begin; t < end; t += teams) {
+    copies_done_but<DEPTH - 2>();
+    float v[E], u[E];
+    rx.read(v, smem + s * slot_bytes, first, step, k.C);
+    rb.read(u, smem + s * slot_bytes + RX::kBytes * blockDim.x, first, step, k.C);
+    ask(s == 0 ? DEPTH - 1 : s - 1, t + (int64_t)(DEPTH - 1) * teams);
+    hold(t + teams);
+    s = s + 1 == DEPTH ? 0 : s + 1;
     float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
     if (block) {
-      float u[VEC * NV];
-      load_row<TB, VEC, NV>(u, block + t * block_stride, first, step, k.C);
-      load_row<TX, VEC, NV>(v, x + t * x_stride, first, step, k.C);
+      if (g < 0 || t >= group_end) {
+        g = find_group(k.offsets, k.groups, t);
+        group_end = k.offsets && g + 1 < k.groups ? k.offsets[g + 1] : k.tokens;
+        group_weights<TB, VEC, NV>(wk, k, g, first, step);
+      }
       if (k.post) {
         row_stats<VEC, NV>(u, sum, k, first, step, st.x, st.y);
 #pragma unroll
-        for (int i = 0; i < VEC * NV; ++i) u[i] *= st.y;
-        scale_row<float, VEC, NV>(u, k.w_post, first, step, k.C);
-      }
-      scale_row<float, VEC, NV>(u, k.scale, first, step, k.C);
-      if (k.gate) {
-        const int g = find_group(k.offsets, k.groups, t);
-        scale_row<TB, VEC, NV>(u, (const TB*)k.gate + (int64_t)g * k.C, first, step, k.C);
+        for (int i = 0; i < E; ++i) u[i] *= st.y;
       }
 #pragma unroll
-      for (int i = 0; i < VEC * NV; ++i) v[i] += u[i];
+      for (int i = 0; i < E; ++i) v[i] += wk[i] * u[i];
       store_row<TX, VEC, NV>(v, x_out + t * x_out_stride, first, step, k.C);
-    } else {
-      load_row<TX, VEC, NV>(v, x + t * x_stride, first, step, k.C);
     }
     if (y) {
       row_stats<VEC, NV>(v, sum, k, first, step, st.z, st.w);
 #pragma unroll
-      for (int i = 0; i < VEC * NV; ++i) v[i] *= st.w;
-      scale_row<float, VEC, NV>(v, k.w_pre, first, step, k.C);
+      for (int i = 0; i < E; ++i) v[i] *= st.w * wp[i];
       store_row<TB, VEC, NV>(v, y + t * y_stride, first, step, k.C);
       if (y_q) {
         // the checkpoint of y as stored; a group is 32 / VEC lanes of a warp
@@ -204,32 +325,75 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(
   }
 }
 
-// Work of one CTA: rows [cta R, cta R + R), cut at the groups' ends; its teams
-// take rows in turn and keep their column sums in registers.  The sums of a
-// (CTA, group) pair go to slot cta + group of part_e: along the rows either the
-// CTA or the group advances, so no two pairs share a slot.
-template <typename TB, typename TX, int VEC, int NV>
-__global__ void __launch_bounds__(512) norm_bwd_kernel(
-    NormK k, const TX* x, int64_t x_stride, const TB* block, int64_t block_stride,
-    const float4* stats, const TX* dx_out, int64_t dx_out_stride, const TB* dy, int64_t dy_stride,
-    TX* dx, int64_t dx_stride, TB* dblock, int64_t dblock_stride, float* part_pre, float* part_e,
-    int64_t rows_per_cta, int warps) {
-  extern __shared__ float smem[];
+// Rows as in the forward, cut at the groups' ends, with the column sums in
+// registers.  The sums of a (CTA, group) pair go to slot cta + group of part_e:
+// along the rows either the CTA or the group advances, so no two pairs share a
+// slot.
+template <typename TB, typename TX, int VEC, int NV, int DEPTH>
+__global__ void __launch_bounds__(kTeamThreads, 1) norm_bwd_kernel(
+    const __grid_constant__ NormK k, const TX* x, int64_t x_stride, const TB* block,
+    int64_t block_stride, const float4* stats, const TX* dx_out, int64_t dx_out_stride,
+    const TB* dy, int64_t dy_stride, TX* dx, int64_t dx_stride, TB* dblock, int64_t dblock_stride,
+    float* part_pre, float* part_e, int64_t rows_per_cta, int warps) {
+  extern __shared__ __align__(16) char smem[];
   constexpr int E = VEC * NV;
+  using RX = Rows<TX, VEC, NV>;
+  using RB = Rows<TB, VEC, NV>;
   const int warp = threadIdx.x >> 5;
   const int team = warp / warps, teams = (blockDim.x >> 5) / warps;
-  TeamSum sum{smem + team * 2 * kMaxTeamWarps, warps, warp - team * warps, team + 1, 0};
-  float* join = smem + teams * 2 * kMaxTeamWarps;  // [teams][C] column sums
+  const int xb = RX::kBytes * blockDim.x, bb = RB::kBytes * blockDim.x;
+  const int slot_bytes = 2 * (xb + bb);
+  float* red = reinterpret_cast<float*>(smem + DEPTH * slot_bytes);
+  float* join = red + teams * 4 * kMaxTeamWarps;  // [teams][C] column sums of several teams
+  TeamSum sum{red + team * 4 * kMaxTeamWarps, warps, warp - team * warps, team + 1, 0};
   const int lane = threadIdx.x - team * warps * 32;
   const int first = lane * VEC, step = warps * 32 * VEC;
 
   const int64_t begin = (int64_t)blockIdx.x * rows_per_cta;
   const int64_t end = min(begin + rows_per_cta, k.tokens);
-  float acc_pre[E], acc_e[E];
+  RX rx{dy ? x : nullptr, x_stride}, rd{dx_out, dx_out_stride};
+  RB rb{block, block_stride}, ry{dy, dy_stride};
+  auto ask = [&](int s, int64_t t) {
+    if (t < end) {
+      char* at = smem + s * slot_bytes;
+      rx.fetch(at, t, first, step, k.C);
+      rd.fetch(at + xb, t, first, step, k.C);
+      rb.fetch(at + 2 * xb, t, first, step, k.C);
+      ry.fetch(at + 2 * xb + bb, t, first, step, k.C);
+    }
+    copies_commit();
+  };
+  float4 st_next = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto hold = [&](int64_t t) {
+    if (t < end) {
+      rx.hold(t, first, step, k.C);
+      rd.hold(t, first, step, k.C);
+      rb.hold(t, first, step, k.C);
+      ry.hold(t, first, step, k.C);
+      st_next = stats[t];
+    }
+  };
 #pragma unroll
-  for (int i = 0; i < E; ++i) acc_pre[i] = acc_e[i] = 0.f;
+  for (int i = 0; i < DEPTH - 1; ++i) ask(i, begin + team + (int64_t)i * teams);
+  hold(begin + team);
+
+  float acc_pre[E], acc_e[E], wp[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    acc_pre[i] = acc_e[i] = 0.f;
+    wp[i] = 1.f;
+  }
+  scale_row<float, VEC, NV>(wp, k.w_pre, first, step, k.C);
 
   auto flush = [&](const float (&acc)[E], float* to) {
+    if (teams == 1) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+          if (first + i * step < k.C) to[first + i * step + j] = acc[i * VEC + j];
+      return;
+    }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -247,50 +411,44 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(
   };
 
   int g = find_group(k.offsets, k.groups, begin);
+  int s = 0;
+  int64_t t = begin + team;  // this team's next row
   for (int64_t at = begin; at < end;) {
     const int64_t stop =
         k.offsets && g + 1 < k.groups ? min(end, max(at, (int64_t)k.offsets[g + 1])) : end;
-    float wk[E];  // k = scale * gate * w_post of this group
-#pragma unroll
-    for (int i = 0; i < E; ++i) wk[i] = 1.f;
-    scale_row<float, VEC, NV>(wk, k.scale, first, step, k.C);
-    if (k.post) scale_row<float, VEC, NV>(wk, k.w_post, first, step, k.C);
-    if (k.gate) scale_row<TB, VEC, NV>(wk, (const TB*)k.gate + (int64_t)g * k.C, first, step, k.C);
-    for (int64_t t = at + team; t < stop; t += teams) {
-      float d[E], n[E];
-      const float4 st = stats[t];
-      if (dx_out) {
-        load_row<TX, VEC, NV>(d, dx_out + t * dx_out_stride, first, step, k.C);
-      } else {
-#pragma unroll
-        for (int i = 0; i < E; ++i) d[i] = 0.f;
-      }
+    float wk[E];
+    group_weights<TB, VEC, NV>(wk, k, g, first, step);
+    for (; t < stop; t += teams) {
+      if (DEPTH == 1) ask(0, t);
+      copies_done_but<(DEPTH > 2 ? DEPTH - 2 : 0)>();
+      float d[E], n[E], h[E], m[E];
+      const char* slot = smem + s * slot_bytes;
+      rx.read(n, slot, first, step, k.C);
+      rd.read(d, slot + xb, first, step, k.C);
+      rb.read(m, slot + 2 * xb, first, step, k.C);
+      ry.read(h, slot + 2 * xb + bb, first, step, k.C);
+      const float4 st = st_next;
+      if (DEPTH > 1) ask(s == 0 ? DEPTH - 1 : s - 1, t + (int64_t)(DEPTH - 1) * teams);
+      hold(t + teams);
+      s = s + 1 == DEPTH ? 0 : s + 1;
       if (dy) {
-        float h[E];
-        load_row<TB, VEC, NV>(h, dy + t * dy_stride, first, step, k.C);
-        load_row<TX, VEC, NV>(n, x + t * x_stride, first, step, k.C);
+        float a = 0.f, b = 0.f;
 #pragma unroll
         for (int i = 0; i < E; ++i) {
           n[i] = (n[i] - st.z) * st.w;
           acc_pre[i] += h[i] * n[i];
+          h[i] *= wp[i];
+          a += h[i] * n[i];
+          b += h[i];
         }
-        scale_row<float, VEC, NV>(h, k.w_pre, first, step, k.C);
-        float a = 0.f, b = 0.f;
-#pragma unroll
-        for (int i = 0; i < E; ++i) a += h[i] * n[i], b += h[i];
-        a = sum(a) * k.inv_c;
-        b = k.center ? sum(b) * k.inv_c : 0.f;
+        sum(a, b, k.center);
+        a *= k.inv_c;
+        b = k.center ? b * k.inv_c : 0.f;
 #pragma unroll
         for (int i = 0; i < E; ++i) d[i] += st.w * (h[i] - n[i] * a - b);
       }
       store_row<TX, VEC, NV>(d, dx + t * dx_stride, first, step, k.C);
       if (block) {
-        float m[E];
-        load_row<TB, VEC, NV>(m, block + t * block_stride, first, step, k.C);
-        if (k.post) {
-#pragma unroll
-          for (int i = 0; i < E; ++i) m[i] = (m[i] - st.x) * st.y;
-        }
         float a = 0.f, b = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
@@ -298,6 +456,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
               const int c = i * VEC + j;
+              if (k.post) m[c] = (m[c] - st.x) * st.y;
               acc_e[c] += d[c] * m[c];
               d[c] *= wk[c];
               a += d[c] * m[c];
@@ -305,8 +464,9 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(
             }
           }
         if (k.post) {
-          a = sum(a) * k.inv_c;
-          b = k.center ? sum(b) * k.inv_c : 0.f;
+          sum(a, b, k.center);
+          a *= k.inv_c;
+          b = k.center ? b * k.inv_c : 0.f;
 #pragma unroll
           for (int i = 0; i < E; ++i) d[i] = st.y * (d[i] - m[i] * a - b);
         }
@@ -426,30 +586,77 @@ struct FwdArgs {
   int64_t es;
 };
 
-template <typename TB, typename TX, int VEC, int NV>
-void fwd_launch(const FwdArgs& a, cudaStream_t st) {
-  const int warps = (int)div_up(a.k.C, 32 * VEC * NV);
-  const int teams = warps >= 4 ? 1 : 4 / warps;
-  const int64_t want = div_up(a.k.tokens, teams);
-  const unsigned blocks = (unsigned)(want < (1 << 30) ? want : (1 << 30));
-  norm_fwd_kernel<TB, TX, VEC, NV><<<blocks, teams * warps * 32, 0, st>>>(
-      a.k, (const TX*)a.x, a.xs, (const TB*)a.block, a.bs, (TX*)a.x_out, a.xos, (TB*)a.y, a.ys,
-      a.stats, a.y_q, a.qs, a.y_e, a.es, warps);
+// Rows are 8 channels a thread (16 from 4096 channels on), so a row of 1024 is
+// four warps; a CTA holds as many such teams as 512 threads and 15 named
+// barriers allow.
+struct Shape {
+  int warps, teams, threads;
+};
+template <int VEC, int NV>
+Shape norm_shape(const NormK& k) {
+  Shape s;
+  s.warps = (int)div_up(k.C, 32 * VEC * NV);
+  s.teams = kTeamThreads / 32 / s.warps;
+  if (s.teams > 8) s.teams = 8;
+  s.threads = s.teams * s.warps * 32;
+  return s;
 }
 
-// Channels per thread: up to 32, so that a row of 1024 is one warp's.
+// Row ranges: `per_sm` CTAs an SM, none without a row for each team.
+inline int64_t norm_ranges(int64_t tokens, int teams, int per_sm, int64_t* rows_per_cta) {
+  int64_t ctas = (int64_t)device_sms() * per_sm;
+  if (ctas > kNormCtas) ctas = kNormCtas;
+  const int64_t most = div_up(tokens, teams);
+  if (ctas > most) ctas = most;
+  *rows_per_cta = div_up(tokens, ctas);
+  return div_up(tokens, *rows_per_cta);
+}
+
+// Shared memory above 48 KB is asked for once per kernel and device.
+template <typename F>
+cudaError_t allow_smem(F kernel, std::atomic<uint64_t>& known) {
+  int dev = 0;
+  const cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess || dev >= 64) return err != cudaSuccess ? err : cudaErrorInvalidDevice;
+  if (known.load(std::memory_order_acquire) >> dev & 1) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget);
+  if (e == cudaSuccess) known.fetch_or(1ull << dev, std::memory_order_release);
+  return e;
+}
+
+// The deepest ring whose rows fit in shared memory (two CTAs share an SM's).
+template <typename TB, typename TX, int VEC, int NV, int DEPTH>
+cudaError_t fwd_launch(const FwdArgs& a, cudaStream_t st) {
+  constexpr int kPerSm = VEC * NV <= 8 ? 2 : 1;
+  const Shape s = norm_shape<VEC, NV>(a.k);
+  const size_t smem =
+      (size_t)DEPTH * (Rows<TX, VEC, NV>::kBytes + Rows<TB, VEC, NV>::kBytes) * s.threads +
+      sizeof(float) * s.teams * 4 * kMaxTeamWarps;
+  if constexpr (DEPTH > 2) {
+    if (smem > kSmemBudget / kPerSm) return fwd_launch<TB, TX, VEC, NV, DEPTH - 1>(a, st);
+  }
+  static std::atomic<uint64_t> known{0};
+  const auto kernel = norm_fwd_kernel<TB, TX, VEC, NV, DEPTH>;
+  const cudaError_t e = allow_smem(kernel, known);
+  if (e != cudaSuccess) return e;
+  int64_t rows = 0;
+  const int64_t ctas = norm_ranges(a.k.tokens, s.teams, kPerSm, &rows);
+  kernel<<<(unsigned)ctas, s.threads, smem, st>>>(
+      a.k, (const TX*)a.x, a.xs, (const TB*)a.block, a.bs, (TX*)a.x_out, a.xos, (TB*)a.y, a.ys,
+      a.stats, a.y_q, a.qs, a.y_e, a.es, rows, s.warps);
+  return cudaSuccess;
+}
+
 template <typename TB, typename TX, int VEC>
-void fwd_pick(const FwdArgs& a, cudaStream_t st) {
-  const int per_lane = (int)div_up(a.k.C, 32);
-  if (per_lane <= 8) fwd_launch<TB, TX, VEC, 8 / VEC>(a, st);
-  else if (per_lane <= 16) fwd_launch<TB, TX, VEC, 16 / VEC>(a, st);
-  else fwd_launch<TB, TX, VEC, 32 / VEC>(a, st);
+cudaError_t fwd_pick(const FwdArgs& a, cudaStream_t st) {
+  if (a.k.C <= 4096) return fwd_launch<TB, TX, VEC, 8 / VEC, 4>(a, st);
+  return fwd_launch<TB, TX, VEC, 16 / VEC, 4>(a, st);
 }
 
 template <typename TB, typename TX>
-void fwd_types(const FwdArgs& a, bool wide, cudaStream_t st) {
-  if (wide) fwd_pick<TB, TX, 16 / sizeof(TB)>(a, st);
-  else fwd_pick<TB, TX, 1>(a, st);
+cudaError_t fwd_types(const FwdArgs& a, bool wide, cudaStream_t st) {
+  return wide ? fwd_pick<TB, TX, 16 / sizeof(TB)>(a, st) : fwd_pick<TB, TX, 1>(a, st);
 }
 
 struct BwdArgs {
@@ -466,26 +673,42 @@ struct BwdArgs {
   int ctas;
 };
 
-template <typename TB, typename TX, int VEC, int NV>
+// As the forward; one CTA an SM (its registers hold the column sums), and no
+// rows ahead where two do not fit (more than 4096 fp32 channels).
+template <typename TB, typename TX, int VEC, int NV, int DEPTH>
 cudaError_t bwd_launch(const BwdArgs& a, cudaStream_t st) {
-  const int warps = (int)div_up(a.k.C, 32 * VEC * NV);
-  const int teams = warps >= 16 ? 1 : (16 / warps < 8 ? 16 / warps : 8);
-  const size_t smem = sizeof(float) * teams * (2 * kMaxTeamWarps + (size_t)a.k.C);
-  norm_bwd_kernel<TB, TX, VEC, NV><<<a.ctas, teams * warps * 32, smem, st>>>(
+  const Shape s = norm_shape<VEC, NV>(a.k);
+  const size_t smem =
+      (size_t)DEPTH * 2 * (Rows<TX, VEC, NV>::kBytes + Rows<TB, VEC, NV>::kBytes) * s.threads +
+      sizeof(float) * s.teams * (4 * kMaxTeamWarps + (s.teams > 1 ? (size_t)a.k.C : 0));
+  if constexpr (DEPTH > 1) {
+    if (smem > kSmemBudget) return bwd_launch<TB, TX, VEC, NV, DEPTH - 1>(a, st);
+  }
+  static std::atomic<uint64_t> known{0};
+  const auto kernel = norm_bwd_kernel<TB, TX, VEC, NV, DEPTH>;
+  const cudaError_t e = allow_smem(kernel, known);
+  if (e != cudaSuccess) return e;
+  kernel<<<(unsigned)a.ctas, s.threads, smem, st>>>(
       a.k, (const TX*)a.x, a.xs, (const TB*)a.block, a.bs, a.stats, (const TX*)a.dx_out, a.dxos,
       (const TB*)a.dy, a.dys, (TX*)a.dx, a.dxs, (TB*)a.dblock, a.dbs, a.part_pre, a.part_e,
-      a.rows_per_cta, warps);
+      a.rows_per_cta, s.warps);
   return cudaSuccess;
 }
 
+template <typename TB, typename TX, int VEC, int NV>
+cudaError_t bwd_ranges(BwdArgs& a, cudaStream_t st) {
+  a.ctas = (int)norm_ranges(a.k.tokens, norm_shape<VEC, NV>(a.k).teams, 1, &a.rows_per_cta);
+  return bwd_launch<TB, TX, VEC, NV, 4>(a, st);
+}
+
 template <typename TB, typename TX, int VEC>
-cudaError_t bwd_pick(const BwdArgs& a, cudaStream_t st) {
-  if (a.k.C <= 4096) return bwd_launch<TB, TX, VEC, 8 / VEC>(a, st);
-  return bwd_launch<TB, TX, VEC, 16 / VEC>(a, st);
+cudaError_t bwd_pick(BwdArgs& a, cudaStream_t st) {
+  if (a.k.C <= 4096) return bwd_ranges<TB, TX, VEC, 8 / VEC>(a, st);
+  return bwd_ranges<TB, TX, VEC, 16 / VEC>(a, st);
 }
 
 template <typename TB, typename TX>
-cudaError_t bwd_types(const BwdArgs& a, bool wide, cudaStream_t st) {
+cudaError_t bwd_types(BwdArgs& a, bool wide, cudaStream_t st) {
   return wide ? bwd_pick<TB, TX, 16 / sizeof(TB)>(a, st) : bwd_pick<TB, TX, 1>(a, st);
 }
 
@@ -522,7 +745,7 @@ extern "C" gs_status gs_gated_norm_fwd(const gs_norm* p, const void* x, int64_t 
   const FwdArgs a{make_norm(*p), x, block, x_out, y, x_stride, block_stride, x_out_stride,
                   y_stride, (float4*)stats, y_q, q_stride, y_e, e_stride};
   cudaStream_t st = (cudaStream_t)stream;
-  GS_NORM_TYPES(p, fwd_types, a, wide, st);
+  GS_CUDA(GS_NORM_TYPES(p, fwd_types, a, wide, st));
   GS_CHECK_LAUNCH();
   return GS_OK;
 }
@@ -565,8 +788,6 @@ extern "C" gs_status gs_gated_norm_bwd(
   if (dw_pre && dy) a.part_pre = (float*)workspace;
   if (need_e && block) a.part_e = (float*)workspace + (size_t)kNormCtas * p->channels;
   if (p->tokens > 0) {
-    a.rows_per_cta = div_up(p->tokens, kNormCtas);
-    a.ctas = (int)div_up(p->tokens, a.rows_per_cta);
     GS_CUDA(GS_NORM_TYPES(p, bwd_types, a, wide, st));
     GS_CHECK_LAUNCH();
   } else {
