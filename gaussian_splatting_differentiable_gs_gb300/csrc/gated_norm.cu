@@ -33,37 +33,37 @@ struct NormK {
   const int32_t* offsets;
 };
 
-// Sums of one or two values per thread over a team of `warps` warps, the same
-// bits in every thread.  red: two slots of 2 kMaxTeamWarps floats per team,
-// used in turn: a slot is written again only after the barrier of the sum in
-// between.
-struct TeamSum {
+// Sums of N values per thread over a team of `warps` warps, the same bits in
+// every thread.  red: two slots of kRedFloats / 2 floats per team, used in turn:
+// a slot is written again only after the barrier of the sum in between.
+constexpr int kRedFloats = 2 * 4 * kMaxTeamWarps;
+struct Team {
   float* red;
   int warps, warp, bar;
   int turn;
-  __device__ __forceinline__ void operator()(float& a, float& b, bool both) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-    if (both) {
-#pragma unroll
-      for (int o = 16; o; o >>= 1) b += __shfl_xor_sync(0xffffffffu, b, o);
-    }
-    if (warps == 1) return;
-    float2* r = reinterpret_cast<float2*>(red) + (turn & 1) * kMaxTeamWarps;
-    ++turn;
-    if ((threadIdx.x & 31) == 0) r[warp] = make_float2(a, b);
-    asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(warps * 32) : "memory");
-    a = b = 0.f;
-    for (int i = 0; i < warps; ++i) {
-      const float2 v = r[i];
-      a += v.x;
-      b += v.y;
-    }
+  __device__ __forceinline__ void sync() const {
+    if (warps == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(warps * 32) : "memory");
   }
-  __device__ __forceinline__ float operator()(float v) {
-    float none = 0.f;
-    (*this)(v, none, false);
-    return v;
+  template <int N>
+  __device__ __forceinline__ void sum(float (&v)[N]) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    if (warps == 1) return;
+    float* r = red + (turn & 1) * (kRedFloats / 2);
+    ++turn;
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) r[warp * N + i] = v[i];
+    }
+    sync();
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = 0.f;
+    for (int w = 0; w < warps; ++w)
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += r[w * N + i];
   }
 };
 
@@ -77,80 +77,92 @@ __device__ __forceinline__ int find_group(const int32_t* offsets, int groups, in
   return lo;
 }
 
-// A thread's share of the rows to come.  Rows whose vectors are 4 or 16 bytes
-// are copied asynchronously into shared memory, kDepth - 1 rows ahead; every
-// thread copies what it reads itself, so nothing but its own copies is waited
-// for.  Single 16-bit values (rows that start anywhere) cannot be copied so:
-// they are held in registers, one row ahead.
+// The rows to come are copied asynchronously (cp.async, 16 bytes at a time)
+// into shared memory while earlier rows are worked on.  Where rows start on
+// 16-byte boundaries (VEC > 1) every thread copies what it reads itself, so it
+// waits for nothing but its own copies.  Otherwise a team copies the 16-byte
+// granules that its row touches, and meets at a barrier before and after it
+// reads them; bytes of the first and last granule that are not the tensor's are
+// not read.
 template <typename T, int VEC, int NV>
 struct Rows {
-  static constexpr int kChunk = VEC * sizeof(T) >= 16 ? 16 : VEC * sizeof(T);
-  static constexpr int kPer = VEC * sizeof(T) / kChunk, kChunks = NV * kPer;
-  static constexpr bool kRing = kChunk >= 4;
-  static constexpr int kBytes = kRing ? kChunks * kChunk : 0;  // per thread and row
+  static constexpr bool kOwn = VEC > 1;
+  static constexpr int kChunk = 16, kEl = kOwn ? kChunk / (int)sizeof(T) : 1;
+  static constexpr int kPer = VEC / kEl, kChunks = NV * kPer;
+  // bytes of a row's slot for the whole CTA
+  __host__ __device__ static int slot(int threads, int teams, int C) {
+    return kOwn ? kChunks * kChunk * threads : teams * row_bytes(C);
+  }
+  __host__ __device__ static int row_bytes(int C) { return (C * (int)sizeof(T) + 31) / 16 * 16; }
 
   const T* base;  // NULL: zeros
   int64_t stride;
-  T held[kRing ? 1 : VEC * NV];
 
-  __device__ __forceinline__ void fetch(char* slot, int64_t t, int first, int step, int C) {
-    if (!kRing || !base) return;
+  __device__ __forceinline__ void fetch(char* slot, int64_t t, int first, int step, int C,
+                                        int team) const {
+    if (!base) return;
     const T* p = base + t * stride;
-    const uint32_t to = (uint32_t)__cvta_generic_to_shared(slot) + threadIdx.x * kChunk;
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(slot);
+    if (kOwn) {
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-      const int c = first + i / kPer * step + i % kPer * (kChunk / (int)sizeof(T));
-      if (c < C) {
-        if (kChunk == 16)
+      for (int i = 0; i < kChunks; ++i) {
+        const int c = first + i / kPer * step + i % kPer * kEl;
+        if (c < C)
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                           to + i * (int)blockDim.x * kChunk),
+                           to + (i * (int)blockDim.x + (int)threadIdx.x) * kChunk),
                        "l"(p + c)
                        : "memory");
-        else
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
-                           to + i * (int)blockDim.x * kChunk),
-                       "l"(p + c)
+      }
+    } else {
+      const int off = (int)((uintptr_t)p & 15), n = C * (int)sizeof(T);
+      const bool clip = t == 0 || stride < C;  // what lies before the row is not the tensor's
+      const uint32_t row = to + team * row_bytes(C);
+      for (int i = first; i * 16 < off + n; i += step) {
+        const int b0 = i * 16 - off;  // the granule's first byte within the row
+        if (b0 < 0 && clip) {
+          for (int b = 0; b < b0 + 16 && b < n; b += sizeof(T))
+            *reinterpret_cast<T*>(slot + team * row_bytes(C) + off + b) = p[b / (int)sizeof(T)];
+        } else {
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(row + i * 16),
+                       "l"((const char*)p + b0), "r"(n - b0 < 16 ? n - b0 : 16)
                        : "memory");
+        }
       }
     }
   }
-  __device__ __forceinline__ void hold(int64_t t, int first, int step, int C) {
-    if (kRing || !base) return;
-    const T* p = base + t * stride;
-#pragma unroll
-    for (int i = 0; i < (kRing ? 0 : VEC * NV); ++i)
-      if (first + i * step < C) held[i] = p[first + i * step];
-  }
-  __device__ __forceinline__ void read(float (&v)[VEC * NV], const char* slot, int first, int step,
-                                       int C) const {
-    constexpr int kEl = kChunk / (int)sizeof(T);
+  __device__ __forceinline__ void read(float (&v)[VEC * NV], const char* slot, bool live, int64_t t,
+                                       int first, int step, int C, int team) const {
+    const T* own = reinterpret_cast<const T*>(
+        slot + team * row_bytes(C) + ((uintptr_t)(base + t * stride) & 15));
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
       const int c = first + i / kPer * step + i % kPer * kEl;
-      if (base && c < C) {
-        if (kRing) {
-          const Pack<T, kEl> w = load_pack<T, kEl>(reinterpret_cast<const T*>(
-              slot + (i * (int)blockDim.x + (int)threadIdx.x) * kChunk));
+      Pack<T, kEl> w;
+      const bool in = live && base && c < C;
+      if (in)
+        w = kOwn ? load_pack<T, kEl>(reinterpret_cast<const T*>(
+                       slot + (i * (int)blockDim.x + (int)threadIdx.x) * kChunk))
+                 : load_pack<T, kEl>(own + c);
 #pragma unroll
-          for (int j = 0; j < kEl; ++j) v[i * kEl + j] = to_f32(w.v[j]);
-        } else {
-          v[i] = to_f32(held[i]);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < kEl; ++j) v[i * kEl + j] = 0.f;
-      }
+      for (int j = 0; j < kEl; ++j) v[i * kEl + j] = in ? to_f32(w.v[j]) : 0.f;
     }
   }
 };
 
-template <int N>
-__device__ __forceinline__ void copies_done_but() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// Waits until at most n of this thread's latest groups of copies are pending.
+__device__ __forceinline__ void copies_pending(int n) {
+  switch (n) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+  }
 }
 __device__ __forceinline__ void copies_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
+constexpr int kMaxDepth = 5;  // rows of a team in shared memory
 
 template <typename T, int VEC, int NV>
 __device__ __forceinline__ void store_row(const float (&v)[VEC * NV], T* p, int first, int step,
@@ -183,27 +195,39 @@ __device__ __forceinline__ void scale_row(float (&v)[VEC * NV], const T* p, int 
   }
 }
 
-// mean and 1/deviation of a row held by a team; v becomes the centred row.
-template <int VEC, int NV>
-__device__ __forceinline__ void row_stats(float (&v)[VEC * NV], TeamSum& sum, const NormK& k,
-                                          int first, int step, float& mean, float& rstd) {
-  mean = 0.f;
+// Means and 1/deviations of a team's rows; v becomes the centred rows.
+template <int VEC, int NV, int kRows>
+__device__ __forceinline__ void row_stats(float (&v)[kRows][VEC * NV], Team& team, const NormK& k,
+                                          int first, int step, float (&mean)[kRows],
+                                          float (&rstd)[kRows]) {
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) mean[r] = 0.f;
   if (k.center) {
-    float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < VEC * NV; ++i) s += v[i];
-    mean = sum(s) * k.inv_c;
+    for (int r = 0; r < kRows; ++r)
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (first + i * step < k.C) {
+      for (int i = 0; i < VEC * NV; ++i) mean[r] += v[r][i];
+    team.sum(mean);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) v[i * VEC + j] -= mean;
-      }
+    for (int r = 0; r < kRows; ++r) {
+      mean[r] *= k.inv_c;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (first + i * step < k.C) {
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) v[r][i * VEC + j] -= mean[r];
+        }
+    }
   }
-  float s = 0.f;
 #pragma unroll
-  for (int i = 0; i < VEC * NV; ++i) s += v[i] * v[i];
-  rstd = rsqrtf(sum(s) * k.inv_c + k.eps);
+  for (int r = 0; r < kRows; ++r) {
+    rstd[r] = 0.f;
+#pragma unroll
+    for (int i = 0; i < VEC * NV; ++i) rstd[r] += v[r][i] * v[r][i];
+  }
+  team.sum(rstd);
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) rstd[r] = rsqrtf(rstd[r] * k.inv_c + k.eps);
 }
 
 // k = res_scale * gate * w_post of a group, per channel
@@ -217,165 +241,187 @@ __device__ __forceinline__ void group_weights(float (&wk)[VEC * NV], const NormK
   if (k.gate) scale_row<TB, VEC, NV>(wk, (const TB*)k.gate + (int64_t)g * k.C, first, step, k.C);
 }
 
-// A CTA takes rows [cta R, cta R + R); its teams take them in turn and keep the
-// weights of their channels in registers.
-template <typename TB, typename TX, int VEC, int NV, int DEPTH>
-__global__ void __launch_bounds__(kTeamThreads, VEC * NV <= 8 ? 2 : 1) norm_fwd_kernel(
+// Work of a CTA: rows [cta R, cta R + R), cut at the groups' ends; its teams
+// take them in turn, kRows at a time, and keep the weights of their channels (and
+// the backward its column sums) in registers.
+struct Range {
+  int64_t begin, end;
+};
+__device__ __forceinline__ Range cta_rows(const NormK& k, int64_t rows_per_cta) {
+  const int64_t b = (int64_t)blockIdx.x * rows_per_cta;
+  return Range{b, min(b + rows_per_cta, k.tokens)};
+}
+
+template <typename TB, typename TX, int VEC, int NV, int kRows>
+__global__ void __launch_bounds__(kTeamThreads, 1) norm_fwd_kernel(
     const __grid_constant__ NormK k, const TX* x, int64_t x_stride, const TB* block,
     int64_t block_stride, TX* x_out, int64_t x_out_stride, TB* y, int64_t y_stride, float4* stats,
-    int8_t* y_q, int64_t q_stride, uint8_t* y_e, int64_t e_stride, int64_t rows_per_cta,
-    int warps) {
+    int8_t* y_q, int64_t q_stride, uint8_t* y_e, int64_t e_stride, int64_t rows_per_cta, int warps,
+    int depth) {
   extern __shared__ __align__(16) char smem[];
   constexpr int E = VEC * NV;
   using RX = Rows<TX, VEC, NV>;
   using RB = Rows<TB, VEC, NV>;
   const int warp = threadIdx.x >> 5;
-  const int team = warp / warps, teams = (blockDim.x >> 5) / warps;
-  const int slot_bytes = (RX::kBytes + RB::kBytes) * blockDim.x;
-  TeamSum sum{reinterpret_cast<float*>(smem + DEPTH * slot_bytes) + team * 4 * kMaxTeamWarps, warps,
-              warp - team * warps, team + 1, 0};
-  const int lane = threadIdx.x - team * warps * 32;
+  const int tm = warp / warps, teams = (blockDim.x >> 5) / warps;
+  const int xb = RX::slot(blockDim.x, teams, k.C), bb = RB::slot(blockDim.x, teams, k.C);
+  const int slot_bytes = xb + bb;
+  Team team{reinterpret_cast<float*>(smem + depth * slot_bytes) + tm * kRedFloats, warps,
+            warp - tm * warps, tm + 1, 0};
+  const int lane = threadIdx.x - tm * warps * 32;
   const int first = lane * VEC, step = warps * 32 * VEC;
 
-  const int64_t begin = (int64_t)blockIdx.x * rows_per_cta + team;
-  const int64_t end = min((int64_t)(blockIdx.x + 1) * rows_per_cta, k.tokens);
-  RX rx{x, x_stride};
-  RB rb{block, block_stride};
-  auto ask = [&](int s, int64_t t) {
-    if (t < end) {
-      rx.fetch(smem + s * slot_bytes, t, first, step, k.C);
-      rb.fetch(smem + s * slot_bytes + RX::kBytes * blockDim.x, t, first, step, k.C);
+  const Range rows = cta_rows(k, rows_per_cta);
+  const RX rx{x, x_stride};
+  const RB rb{block, block_stride};
+  int64_t next = rows.begin + tm;  // the next row to ask for
+  auto ask = [&](int s) {
+    if (next < rows.end) {
+      rx.fetch(smem + s * slot_bytes, next, first, step, k.C, tm);
+      rb.fetch(smem + s * slot_bytes + xb, next, first, step, k.C, tm);
     }
     copies_commit();
+    next += teams;
   };
-  auto hold = [&](int64_t t) {
-    if (t < end) {
-      rx.hold(t, first, step, k.C);
-      rb.hold(t, first, step, k.C);
-    }
-  };
-#pragma unroll
-  for (int i = 0; i < DEPTH - 1; ++i) ask(i, begin + (int64_t)i * teams);
-  hold(begin);
+  for (int i = 0; i < depth; ++i) ask(i);
 
   float wp[E], wk[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) wp[i] = 1.f;
   scale_row<float, VEC, NV>(wp, k.w_pre, first, step, k.C);
-  int g = -1;
-  int64_t group_end = 0;
 
-  int s = 0;
-  for (int64_t t = begin; t < end; t += teams) {
-    copies_done_but<DEPTH - 2>();
-    float v[E], u[E];
-    rx.read(v, smem + s * slot_bytes, first, step, k.C);
-    rb.read(u, smem + s * slot_bytes + RX::kBytes * blockDim.x, first, step, k.C);
-    ask(s == 0 ? DEPTH - 1 : s - 1, t + (int64_t)(DEPTH - 1) * teams);
-    hold(t + teams);
-    s = s + 1 == DEPTH ? 0 : s + 1;
-    float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (block) {
-      if (g < 0 || t >= group_end) {
-        g = find_group(k.offsets, k.groups, t);
-        group_end = k.offsets && g + 1 < k.groups ? k.offsets[g + 1] : k.tokens;
-        group_weights<TB, VEC, NV>(wk, k, g, first, step);
+  int g = find_group(k.offsets, k.groups, rows.begin), s = 0;
+  int64_t t = rows.begin + tm;
+  for (int64_t at = rows.begin; at < rows.end;) {
+    const int64_t stop =
+        k.offsets && g + 1 < k.groups ? min(rows.end, max(at, (int64_t)k.offsets[g + 1])) : rows.end;
+    if (block && t < stop) group_weights<TB, VEC, NV>(wk, k, g, first, step);
+    while (t < stop) {
+      const bool two = kRows == 2 && t + teams < stop;
+      const int s1 = s + 1 == depth ? 0 : s + 1;
+      copies_pending(depth - kRows);
+      if (!RX::kOwn) team.sync();
+      float v[kRows][E], u[kRows][E];
+      float m0[kRows] = {}, r0[kRows] = {}, m1[kRows] = {}, r1[kRows] = {};
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const char* slot = smem + (r ? s1 : s) * slot_bytes;
+        const int64_t row = t + r * teams;
+        rx.read(v[r], slot, !r || two, row, first, step, k.C, tm);
+        rb.read(u[r], slot + xb, !r || two, row, first, step, k.C, tm);
       }
-      if (k.post) {
-        row_stats<VEC, NV>(u, sum, k, first, step, st.x, st.y);
+      if (block) {
+        if (k.post) {
+          row_stats<VEC, NV, kRows>(u, team, k, first, step, m0, r0);
 #pragma unroll
-        for (int i = 0; i < E; ++i) u[i] *= st.y;
+          for (int r = 0; r < kRows; ++r)
+#pragma unroll
+            for (int i = 0; i < E; ++i) u[r][i] *= r0[r];
+        }
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+#pragma unroll
+          for (int i = 0; i < E; ++i) v[r][i] += wk[i] * u[r][i];
+          if (!r || two)
+            store_row<TX, VEC, NV>(v[r], x_out + (t + r * teams) * x_out_stride, first, step, k.C);
+        }
       }
+      if (!RX::kOwn) team.sync();
+      ask(s);
+      if (two) ask(s1);
+      if (y) {
+        row_stats<VEC, NV, kRows>(v, team, k, first, step, m1, r1);
 #pragma unroll
-      for (int i = 0; i < E; ++i) v[i] += wk[i] * u[i];
-      store_row<TX, VEC, NV>(v, x_out + t * x_out_stride, first, step, k.C);
-    }
-    if (y) {
-      row_stats<VEC, NV>(v, sum, k, first, step, st.z, st.w);
+        for (int r = 0; r < kRows; ++r) {
+          const int64_t row = t + r * teams;
 #pragma unroll
-      for (int i = 0; i < E; ++i) v[i] *= st.w * wp[i];
-      store_row<TB, VEC, NV>(v, y + t * y_stride, first, step, k.C);
-      if (y_q) {
-        // the checkpoint of y as stored; a group is 32 / VEC lanes of a warp
+          for (int i = 0; i < E; ++i) v[r][i] *= r1[r] * wp[i];
+          if (!r || two) store_row<TB, VEC, NV>(v[r], y + row * y_stride, first, step, k.C);
+          if (y_q && (!r || two)) {
+            // the checkpoint of y as stored; a group is 32 / VEC lanes of a warp
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          uint32_t mag = 0;
+            for (int i = 0; i < NV; ++i) {
+              uint32_t mag = 0;
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            v[i * VEC + j] = to_f32(from_f32<TB>(v[i * VEC + j]));
-            mag = max(mag, __float_as_uint(v[i * VEC + j]) & 0x7fffffffu);
-          }
+              for (int j = 0; j < VEC; ++j) {
+                v[r][i * VEC + j] = to_f32(from_f32<TB>(v[r][i * VEC + j]));
+                mag = max(mag, __float_as_uint(v[r][i * VEC + j]) & 0x7fffffffu);
+              }
 #pragma unroll
-          for (int o = 1; o < GS_ACT8_GROUP / VEC; o <<= 1)
-            mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, o));
-          const uint32_t e = act8_exponent(mag);
-          const float inv = act8_inverse(e);
-          const int c = first + i * step;
-          if (c < (k.C + GS_ACT8_GROUP - 1) / GS_ACT8_GROUP * GS_ACT8_GROUP) {
-            Pack<int8_t, VEC> q;
+              for (int o = 1; o < GS_ACT8_GROUP / VEC; o <<= 1)
+                mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, o));
+              const uint32_t e = act8_exponent(mag);
+              const float inv = act8_inverse(e);
+              const int c = first + i * step;
+              if (c < (k.C + GS_ACT8_GROUP - 1) / GS_ACT8_GROUP * GS_ACT8_GROUP) {
+                Pack<int8_t, VEC> q;
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) q.v[j] = (int8_t)act8_quantise(v[i * VEC + j], inv, e);
-            store_pack<int8_t, VEC>(y_q + t * q_stride + c, q);
-            if (c % GS_ACT8_GROUP == 0) y_e[t * e_stride + c / GS_ACT8_GROUP] = (uint8_t)e;
+                for (int j = 0; j < VEC; ++j)
+                  q.v[j] = (int8_t)act8_quantise(v[r][i * VEC + j], inv, e);
+                store_pack<int8_t, VEC>(y_q + row * q_stride + c, q);
+                if (c % GS_ACT8_GROUP == 0) y_e[row * e_stride + c / GS_ACT8_GROUP] = (uint8_t)e;
+              }
+            }
           }
         }
       }
+      if (lane == 0) {
+        stats[t] = make_float4(m0[0], r0[0], m1[0], r1[0]);
+        if (two) stats[t + teams] = make_float4(m0[kRows - 1], r0[kRows - 1], m1[kRows - 1], r1[kRows - 1]);
+      }
+      s = two ? (s1 + 1 == depth ? 0 : s1 + 1) : s1;
+      t += two ? 2 * teams : teams;
     }
-    if (lane == 0) stats[t] = st;
+    at = stop;
+    if (g + 1 < k.groups) ++g;
   }
 }
 
-// Rows as in the forward, cut at the groups' ends, with the column sums in
-// registers.  The sums of a (CTA, group) pair go to slot cta + group of part_e:
-// along the rows either the CTA or the group advances, so no two pairs share a
-// slot.
-template <typename TB, typename TX, int VEC, int NV, int DEPTH>
+// The sums of a (CTA, group) pair go to slot cta + group of part_e: along the
+// rows either the CTA or the group advances, so no two pairs share a slot.
+template <typename TB, typename TX, int VEC, int NV, int kRows>
 __global__ void __launch_bounds__(kTeamThreads, 1) norm_bwd_kernel(
     const __grid_constant__ NormK k, const TX* x, int64_t x_stride, const TB* block,
     int64_t block_stride, const float4* stats, const TX* dx_out, int64_t dx_out_stride,
     const TB* dy, int64_t dy_stride, TX* dx, int64_t dx_stride, TB* dblock, int64_t dblock_stride,
-    float* part_pre, float* part_e, int64_t rows_per_cta, int warps) {
+    float* part_pre, float* part_e, int64_t rows_per_cta, int warps, int depth) {
   extern __shared__ __align__(16) char smem[];
   constexpr int E = VEC * NV;
   using RX = Rows<TX, VEC, NV>;
   using RB = Rows<TB, VEC, NV>;
   const int warp = threadIdx.x >> 5;
-  const int team = warp / warps, teams = (blockDim.x >> 5) / warps;
-  const int xb = RX::kBytes * blockDim.x, bb = RB::kBytes * blockDim.x;
+  const int tm = warp / warps, teams = (blockDim.x >> 5) / warps;
+  const int xb = RX::slot(blockDim.x, teams, k.C), bb = RB::slot(blockDim.x, teams, k.C);
   const int slot_bytes = 2 * (xb + bb);
-  float* red = reinterpret_cast<float*>(smem + DEPTH * slot_bytes);
-  float* join = red + teams * 4 * kMaxTeamWarps;  // [teams][C] column sums of several teams
-  TeamSum sum{red + team * 4 * kMaxTeamWarps, warps, warp - team * warps, team + 1, 0};
-  const int lane = threadIdx.x - team * warps * 32;
+  float* red = reinterpret_cast<float*>(smem + depth * slot_bytes);
+  float* join = red + teams * kRedFloats;  // [teams][C] column sums of several teams
+  Team team{red + tm * kRedFloats, warps, warp - tm * warps, tm + 1, 0};
+  const int lane = threadIdx.x - tm * warps * 32;
   const int first = lane * VEC, step = warps * 32 * VEC;
 
-  const int64_t begin = (int64_t)blockIdx.x * rows_per_cta;
-  const int64_t end = min(begin + rows_per_cta, k.tokens);
-  RX rx{dy ? x : nullptr, x_stride}, rd{dx_out, dx_out_stride};
-  RB rb{block, block_stride}, ry{dy, dy_stride};
-  auto ask = [&](int s, int64_t t) {
-    if (t < end) {
+  const Range rows = cta_rows(k, rows_per_cta);
+  const RX rx{dy ? x : nullptr, x_stride}, rd{dx_out, dx_out_stride};
+  const RB rb{block, block_stride}, ry{dy, dy_stride};
+  int64_t next = rows.begin + tm;
+  auto ask = [&](int s) {
+    if (next < rows.end) {
       char* at = smem + s * slot_bytes;
-      rx.fetch(at, t, first, step, k.C);
-      rd.fetch(at + xb, t, first, step, k.C);
-      rb.fetch(at + 2 * xb, t, first, step, k.C);
-      ry.fetch(at + 2 * xb + bb, t, first, step, k.C);
+      rx.fetch(at, next, first, step, k.C, tm);
+      ry.fetch(at + 2 * xb + bb, next, first, step, k.C, tm);
+      rd.fetch(at + xb, next, first, step, k.C, tm);
+      rb.fetch(at + 2 * xb, next, first, step, k.C, tm);
     }
     copies_commit();
+    next += teams;
   };
-  float4 st_next = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto hold = [&](int64_t t) {
-    if (t < end) {
-      rx.hold(t, first, step, k.C);
-      rd.hold(t, first, step, k.C);
-      rb.hold(t, first, step, k.C);
-      ry.hold(t, first, step, k.C);
-      st_next = stats[t];
-    }
-  };
+  for (int i = 0; i < depth; ++i) ask(i);
+  float4 st[kRows], st_next[kRows];
+  auto ask_stats = [&](int64_t t) {
 #pragma unroll
-  for (int i = 0; i < DEPTH - 1; ++i) ask(i, begin + team + (int64_t)i * teams);
-  hold(begin + team);
+    for (int r = 0; r < kRows; ++r)
+      st_next[r] = t + r * teams < rows.end ? stats[t + r * teams] : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  ask_stats(rows.begin + tm);
 
   float acc_pre[E], acc_e[E], wp[E];
 #pragma unroll
@@ -400,7 +446,7 @@ __global__ void __launch_bounds__(kTeamThreads, 1) norm_bwd_kernel(
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         const int c = first + i * step + j;
-        if (c < k.C) join[team * k.C + c] = acc[i * VEC + j];
+        if (c < k.C) join[tm * k.C + c] = acc[i * VEC + j];
       }
     __syncthreads();
     for (int c = threadIdx.x; c < k.C; c += blockDim.x) {
@@ -410,68 +456,118 @@ __global__ void __launch_bounds__(kTeamThreads, 1) norm_bwd_kernel(
     }
   };
 
-  int g = find_group(k.offsets, k.groups, begin);
-  int s = 0;
-  int64_t t = begin + team;  // this team's next row
-  for (int64_t at = begin; at < end;) {
+  int g = find_group(k.offsets, k.groups, rows.begin), s = 0;
+  int64_t t = rows.begin + tm;  // this team's next row
+  for (int64_t at = rows.begin; at < rows.end;) {
     const int64_t stop =
-        k.offsets && g + 1 < k.groups ? min(end, max(at, (int64_t)k.offsets[g + 1])) : end;
+        k.offsets && g + 1 < k.groups ? min(rows.end, max(at, (int64_t)k.offsets[g + 1])) : rows.end;
     float wk[E];
-    group_weights<TB, VEC, NV>(wk, k, g, first, step);
-    for (; t < stop; t += teams) {
-      if (DEPTH == 1) ask(0, t);
-      copies_done_but<(DEPTH > 2 ? DEPTH - 2 : 0)>();
-      float d[E], n[E], h[E], m[E];
-      const char* slot = smem + s * slot_bytes;
-      rx.read(n, slot, first, step, k.C);
-      rd.read(d, slot + xb, first, step, k.C);
-      rb.read(m, slot + 2 * xb, first, step, k.C);
-      ry.read(h, slot + 2 * xb + bb, first, step, k.C);
-      const float4 st = st_next;
-      if (DEPTH > 1) ask(s == 0 ? DEPTH - 1 : s - 1, t + (int64_t)(DEPTH - 1) * teams);
-      hold(t + teams);
-      s = s + 1 == DEPTH ? 0 : s + 1;
-      if (dy) {
-        float a = 0.f, b = 0.f;
+    if (t < stop) group_weights<TB, VEC, NV>(wk, k, g, first, step);
+    while (t < stop) {
+      const bool two = kRows == 2 && t + teams < stop;
+      const int s1 = s + 1 == depth ? 0 : s + 1;
+      copies_pending(depth - kRows);
+      if (!RX::kOwn) team.sync();
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-          n[i] = (n[i] - st.z) * st.w;
-          acc_pre[i] += h[i] * n[i];
-          h[i] *= wp[i];
-          a += h[i] * n[i];
-          b += h[i];
-        }
-        sum(a, b, k.center);
-        a *= k.inv_c;
-        b = k.center ? b * k.inv_c : 0.f;
+      for (int r = 0; r < kRows; ++r) st[r] = st_next[r];
+      ask_stats(two ? t + 2 * teams : t + teams);
+      float d[kRows][E], part[2 * kRows];
+      {
+        float n[kRows][E], h[kRows][E];
+        if (dy) {
 #pragma unroll
-        for (int i = 0; i < E; ++i) d[i] += st.w * (h[i] - n[i] * a - b);
-      }
-      store_row<TX, VEC, NV>(d, dx + t * dx_stride, first, step, k.C);
-      if (block) {
-        float a = 0.f, b = 0.f;
+          for (int r = 0; r < kRows; ++r) {
+            const bool live = !r || two;
+            const char* slot = smem + (r ? s1 : s) * slot_bytes;
+            rx.read(n[r], slot, live, t + r * teams, first, step, k.C, tm);
+            ry.read(h[r], slot + 2 * xb + bb, live, t + r * teams, first, step, k.C, tm);
+            float a = 0.f, b = 0.f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-          if (first + i * step < k.C) {
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-              const int c = i * VEC + j;
-              if (k.post) m[c] = (m[c] - st.x) * st.y;
-              acc_e[c] += d[c] * m[c];
-              d[c] *= wk[c];
-              a += d[c] * m[c];
-              b += d[c];
+            for (int i = 0; i < E; ++i) {
+              n[r][i] = (n[r][i] - st[r].z) * st[r].w;
+              if (live) acc_pre[i] += h[r][i] * n[r][i];
+              h[r][i] *= wp[i];
+              a += h[r][i] * n[r][i];
+              b += h[r][i];
             }
+            part[r] = a;
+            part[kRows + r] = b;
           }
-        if (k.post) {
-          sum(a, b, k.center);
-          a *= k.inv_c;
-          b = k.center ? b * k.inv_c : 0.f;
+          if (k.center) {
+            team.sum(part);
+          } else {
+            float only[kRows];
 #pragma unroll
-          for (int i = 0; i < E; ++i) d[i] = st.y * (d[i] - m[i] * a - b);
+            for (int r = 0; r < kRows; ++r) only[r] = part[r];
+            team.sum(only);
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) part[r] = only[r], part[kRows + r] = 0.f;
+          }
         }
-        store_row<TB, VEC, NV>(d, dblock + t * dblock_stride, first, step, k.C);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+          const bool live = !r || two;
+          rd.read(d[r], smem + (r ? s1 : s) * slot_bytes + xb, live, t + r * teams, first, step, k.C, tm);
+          if (dy) {
+            const float a = part[r] * k.inv_c, b = part[kRows + r] * k.inv_c;
+#pragma unroll
+            for (int i = 0; i < E; ++i) d[r][i] += st[r].w * (h[r][i] - n[r][i] * a - b);
+          }
+          if (live) store_row<TX, VEC, NV>(d[r], dx + (t + r * teams) * dx_stride, first, step, k.C);
+        }
       }
+      if (block) {
+        float m[kRows][E];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+          const bool live = !r || two;
+          rb.read(m[r], smem + (r ? s1 : s) * slot_bytes + 2 * xb, live, t + r * teams, first, step, k.C,
+                  tm);
+          float a = 0.f, b = 0.f;
+#pragma unroll
+          for (int i = 0; i < NV; ++i)
+            if (first + i * step < k.C) {
+#pragma unroll
+              for (int j = 0; j < VEC; ++j) {
+                const int c = i * VEC + j;
+                if (k.post) m[r][c] = (m[r][c] - st[r].x) * st[r].y;
+                if (live) acc_e[c] += d[r][c] * m[r][c];
+                d[r][c] *= wk[c];
+                a += d[r][c] * m[r][c];
+                b += d[r][c];
+              }
+            }
+          part[r] = a;
+          part[kRows + r] = b;
+        }
+        if (k.post) {
+          if (k.center) {
+            team.sum(part);
+          } else {
+            float only[kRows];
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) only[r] = part[r];
+            team.sum(only);
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) part[r] = only[r], part[kRows + r] = 0.f;
+          }
+#pragma unroll
+          for (int r = 0; r < kRows; ++r) {
+            const float a = part[r] * k.inv_c, b = part[kRows + r] * k.inv_c;
+#pragma unroll
+            for (int i = 0; i < E; ++i) d[r][i] = st[r].y * (d[r][i] - m[r][i] * a - b);
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+          if (!r || two)
+            store_row<TB, VEC, NV>(d[r], dblock + (t + r * teams) * dblock_stride, first, step, k.C);
+      }
+      if (!RX::kOwn) team.sync();
+      ask(s);
+      if (two) ask(s1);
+      s = two ? (s1 + 1 == depth ? 0 : s1 + 1) : s1;
+      t += two ? 2 * teams : teams;
     }
     if (block && part_e && stop > at) {
       flush(acc_e, part_e + ((int64_t)blockIdx.x + g) * k.C);
@@ -484,60 +580,73 @@ __global__ void __launch_bounds__(kTeamThreads, 1) norm_bwd_kernel(
   if (part_pre) flush(acc_pre, part_pre + (int64_t)blockIdx.x * k.C);
 }
 
-// Joins the CTAs' column sums, 32 columns per block, in a fixed order.
-__global__ void __launch_bounds__(1024) norm_sums_kernel(NormK k, int64_t gate_elem,
+// Joins the CTAs' column sums, 32 columns per block, in a fixed order: the
+// block's 32 warps share out the groups (up to 32 at a time), and a group's
+// slots among its warps.
+__global__ void __launch_bounds__(1024) norm_sums_kernel(const __grid_constant__ NormK k,
                                                          int32_t gate_dtype, const float* part_pre,
                                                          const float* part_e, int64_t rows_per_cta,
                                                          int ctas, float* dw_pre, float* dw_post,
                                                          float* dgate, float* dscale) {
-  __shared__ float red[32][33];
-  const int c = blockIdx.x * 32 + threadIdx.x;
+  __shared__ float red[32][33], red2[32][33];
+  const int x = threadIdx.x, y = threadIdx.y;
+  const int c = blockIdx.x * 32 + x;
   const bool in = c < k.C;
-  auto total = [&](const float* p, int lo, int hi) {  // slots [lo, hi)
+  auto slots = [&](const float* p, int lo, int hi, int from, int by) {
     float s = 0.f;
-    if (in)
-      for (int i = lo + threadIdx.y; i < hi; i += 32) s += p[(int64_t)i * k.C + c];
-    __syncthreads();
-    red[threadIdx.y][threadIdx.x] = s;
-    __syncthreads();
-    s = red[threadIdx.x][threadIdx.y];
-#pragma unroll
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    __syncthreads();
-    if (threadIdx.x == 0) red[0][threadIdx.y] = s;
-    __syncthreads();
-    return red[0][threadIdx.x];
+    if (in && p)
+#pragma unroll 8
+      for (int i = lo + from; i < hi; i += by) s += p[(int64_t)i * k.C + c];
+    return s;
   };
-  if (dw_pre) {
-    const float s = total(part_pre, 0, part_pre ? ctas : 0);
-    if (in && threadIdx.y == 0) dw_pre[c] = s;
-  }
-  if (!dw_post && !dgate && !dscale) return;
+  red2[y][x] = dw_pre ? slots(part_pre, 0, ctas, y, 32) : 0.f;
   const float w = in && k.w_post ? k.w_post[c] : 1.f;
   const float sc = in && k.scale ? k.scale[c] : 1.f;
-  float sum_post = 0.f, sum_scale = 0.f;
-  for (int g = 0; g < k.groups; ++g) {
-    int64_t lo = k.offsets ? k.offsets[g] : 0, hi = k.offsets ? k.offsets[g + 1] : k.tokens;
-    lo = max((int64_t)0, lo);
-    hi = min(hi, k.tokens);
+  const bool sums = dw_post || dgate || dscale;
+  float post = 0.f, scale = 0.f;
+  for (int g0 = 0; g0 < (sums ? k.groups : 0); g0 += 32) {
+    const int n = min(32, k.groups - g0), per = 32 / n;
+    const int g = g0 + y / per;
     float e = 0.f;
-    if (part_e && lo < hi)  // the same for the whole block
-      e = total(part_e, (int)(lo / rows_per_cta) + g, (int)((hi - 1) / rows_per_cta) + g + 1);
-    float gv = 1.f;
-    if (in && k.gate) {
-      const int64_t at = (int64_t)g * k.C + c;
-      gv = gate_dtype == GS_F32    ? ((const float*)k.gate)[at]
-           : gate_dtype == GS_BF16 ? to_f32(((const __nv_bfloat16*)k.gate)[at])
-                                   : to_f32(((const __half*)k.gate)[at]);
+    if (y < n * per) {
+      const int64_t lo = max((int64_t)0, (int64_t)(k.offsets ? k.offsets[g] : 0));
+      const int64_t hi = min(k.tokens, k.offsets ? (int64_t)k.offsets[g + 1] : k.tokens);
+      if (lo < hi)
+        e = slots(part_e, (int)(lo / rows_per_cta) + g, (int)((hi - 1) / rows_per_cta) + g + 1,
+                  y % per, per);
     }
-    sum_post += sc * gv * e;
-    sum_scale += gv * w * e;
-    if (in && dgate && threadIdx.y == 0) dgate[(int64_t)g * k.C + c] = sc * w * e;
+    __syncthreads();
+    red[y][x] = e;
+    __syncthreads();
+    if (y < n) {  // one warp a group
+      e = 0.f;
+      for (int i = 0; i < per; ++i) e += red[y * per + i][x];
+      float gv = 1.f;
+      if (in && k.gate) {
+        const int64_t at = (int64_t)(g0 + y) * k.C + c;
+        gv = gate_dtype == GS_F32    ? ((const float*)k.gate)[at]
+             : gate_dtype == GS_BF16 ? to_f32(((const __nv_bfloat16*)k.gate)[at])
+                                     : to_f32(((const __half*)k.gate)[at]);
+      }
+      post += sc * gv * e;
+      scale += gv * w * e;
+      if (in && dgate) dgate[(int64_t)(g0 + y) * k.C + c] = sc * w * e;
+    }
   }
-  if (in && threadIdx.y == 0) {
-    if (dw_post) dw_post[c] = sum_post;
-    if (dscale) dscale[c] = sum_scale;
-  }
+  auto join = [&](float (*m)[33], float* to) {
+    __syncthreads();
+    if (y == 0 && in && to) {
+      float s = 0.f;
+      for (int i = 0; i < 32; ++i) s += m[i][x];
+      to[c] = s;
+    }
+  };
+  join(red2, dw_pre);
+  __syncthreads();
+  red[y][x] = post;
+  red2[y][x] = scale;
+  join(red, dw_post);
+  join(red2, dscale);
 }
 
 bool norm_ok(const gs_norm* p) {
@@ -625,33 +734,39 @@ cudaError_t allow_smem(F kernel, std::atomic<uint64_t>& known) {
   return e;
 }
 
-// The deepest ring whose rows fit in shared memory (two CTAs share an SM's).
-template <typename TB, typename TX, int VEC, int NV, int DEPTH>
+// Rows of a team in shared memory: as many as fit, up to kMaxDepth (5 rows of 1024
+// bf16 channels, four tensors, four teams: 160 KB), at least the ones worked on.
+int ring_depth(int slot_bytes, size_t fixed, int rows, size_t* smem) {
+  int depth = kMaxDepth;
+  while (depth > rows && depth * (size_t)slot_bytes + fixed > kSmemBudget) --depth;
+  *smem = depth * (size_t)slot_bytes + fixed;
+  return depth;
+}
+
+template <typename TB, typename TX, int VEC, int NV>
 cudaError_t fwd_launch(const FwdArgs& a, cudaStream_t st) {
-  constexpr int kPerSm = VEC * NV <= 8 ? 2 : 1;
+  constexpr int kRows = VEC * NV <= 8 ? 2 : 1;
   const Shape s = norm_shape<VEC, NV>(a.k);
-  const size_t smem =
-      (size_t)DEPTH * (Rows<TX, VEC, NV>::kBytes + Rows<TB, VEC, NV>::kBytes) * s.threads +
-      sizeof(float) * s.teams * 4 * kMaxTeamWarps;
-  if constexpr (DEPTH > 2) {
-    if (smem > kSmemBudget / kPerSm) return fwd_launch<TB, TX, VEC, NV, DEPTH - 1>(a, st);
-  }
+  size_t smem = 0;
+  const int depth = ring_depth(Rows<TX, VEC, NV>::slot(s.threads, s.teams, a.k.C) +
+                                   Rows<TB, VEC, NV>::slot(s.threads, s.teams, a.k.C),
+                               sizeof(float) * s.teams * kRedFloats, kRows, &smem);
   static std::atomic<uint64_t> known{0};
-  const auto kernel = norm_fwd_kernel<TB, TX, VEC, NV, DEPTH>;
+  const auto kernel = norm_fwd_kernel<TB, TX, VEC, NV, kRows>;
   const cudaError_t e = allow_smem(kernel, known);
   if (e != cudaSuccess) return e;
   int64_t rows = 0;
-  const int64_t ctas = norm_ranges(a.k.tokens, s.teams, kPerSm, &rows);
+  const int64_t ctas = norm_ranges(a.k.tokens, s.teams, 1, &rows);
   kernel<<<(unsigned)ctas, s.threads, smem, st>>>(
       a.k, (const TX*)a.x, a.xs, (const TB*)a.block, a.bs, (TX*)a.x_out, a.xos, (TB*)a.y, a.ys,
-      a.stats, a.y_q, a.qs, a.y_e, a.es, rows, s.warps);
+      a.stats, a.y_q, a.qs, a.y_e, a.es, rows, s.warps, depth);
   return cudaSuccess;
 }
 
 template <typename TB, typename TX, int VEC>
 cudaError_t fwd_pick(const FwdArgs& a, cudaStream_t st) {
-  if (a.k.C <= 4096) return fwd_launch<TB, TX, VEC, 8 / VEC, 4>(a, st);
-  return fwd_launch<TB, TX, VEC, 16 / VEC, 4>(a, st);
+  if (a.k.C <= 4096) return fwd_launch<TB, TX, VEC, 8 / VEC>(a, st);
+  return fwd_launch<TB, TX, VEC, 16 / VEC>(a, st);
 }
 
 template <typename TB, typename TX>
@@ -673,38 +788,32 @@ struct BwdArgs {
   int ctas;
 };
 
-// As the forward; one CTA an SM (its registers hold the column sums), and no
-// rows ahead where two do not fit (more than 4096 fp32 channels).
-template <typename TB, typename TX, int VEC, int NV, int DEPTH>
-cudaError_t bwd_launch(const BwdArgs& a, cudaStream_t st) {
+template <typename TB, typename TX, int VEC, int NV>
+cudaError_t bwd_launch(BwdArgs& a, cudaStream_t st) {
+  constexpr int kRows = 1;  // two would not fit the registers
   const Shape s = norm_shape<VEC, NV>(a.k);
-  const size_t smem =
-      (size_t)DEPTH * 2 * (Rows<TX, VEC, NV>::kBytes + Rows<TB, VEC, NV>::kBytes) * s.threads +
-      sizeof(float) * s.teams * (4 * kMaxTeamWarps + (s.teams > 1 ? (size_t)a.k.C : 0));
-  if constexpr (DEPTH > 1) {
-    if (smem > kSmemBudget) return bwd_launch<TB, TX, VEC, NV, DEPTH - 1>(a, st);
-  }
+  size_t smem = 0;
+  const int depth =
+      ring_depth(2 * (Rows<TX, VEC, NV>::slot(s.threads, s.teams, a.k.C) +
+                      Rows<TB, VEC, NV>::slot(s.threads, s.teams, a.k.C)),
+                 sizeof(float) * s.teams * (kRedFloats + (s.teams > 1 ? (size_t)a.k.C : 0)), kRows,
+                 &smem);
   static std::atomic<uint64_t> known{0};
-  const auto kernel = norm_bwd_kernel<TB, TX, VEC, NV, DEPTH>;
+  const auto kernel = norm_bwd_kernel<TB, TX, VEC, NV, kRows>;
   const cudaError_t e = allow_smem(kernel, known);
   if (e != cudaSuccess) return e;
+  a.ctas = (int)norm_ranges(a.k.tokens, s.teams, 1, &a.rows_per_cta);
   kernel<<<(unsigned)a.ctas, s.threads, smem, st>>>(
       a.k, (const TX*)a.x, a.xs, (const TB*)a.block, a.bs, a.stats, (const TX*)a.dx_out, a.dxos,
       (const TB*)a.dy, a.dys, (TX*)a.dx, a.dxs, (TB*)a.dblock, a.dbs, a.part_pre, a.part_e,
-      a.rows_per_cta, s.warps);
+      a.rows_per_cta, s.warps, depth);
   return cudaSuccess;
-}
-
-template <typename TB, typename TX, int VEC, int NV>
-cudaError_t bwd_ranges(BwdArgs& a, cudaStream_t st) {
-  a.ctas = (int)norm_ranges(a.k.tokens, norm_shape<VEC, NV>(a.k).teams, 1, &a.rows_per_cta);
-  return bwd_launch<TB, TX, VEC, NV, 4>(a, st);
 }
 
 template <typename TB, typename TX, int VEC>
 cudaError_t bwd_pick(BwdArgs& a, cudaStream_t st) {
-  if (a.k.C <= 4096) return bwd_ranges<TB, TX, VEC, 8 / VEC>(a, st);
-  return bwd_ranges<TB, TX, VEC, 16 / VEC>(a, st);
+  if (a.k.C <= 4096) return bwd_launch<TB, TX, VEC, 8 / VEC>(a, st);
+  return bwd_launch<TB, TX, VEC, 16 / VEC>(a, st);
 }
 
 template <typename TB, typename TX>
@@ -795,7 +904,7 @@ extern "C" gs_status gs_gated_norm_bwd(
   }
   if (dw_pre || need_e) {
     norm_sums_kernel<<<(unsigned)div_up(p->channels, 32), dim3(32, 32), 0, st>>>(
-        a.k, 0, p->dtype, a.part_pre, a.part_e, a.rows_per_cta, a.ctas, dw_pre, dw_post, dgate,
+        a.k, p->dtype, a.part_pre, a.part_e, a.rows_per_cta, a.ctas, dw_pre, dw_post, dgate,
         dres_scale);
     GS_CHECK_LAUNCH();
   }

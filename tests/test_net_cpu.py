@@ -9,6 +9,24 @@ import torch
 import net_plain
 
 
+class Heads(C.Structure):  # gs_heads
+    _fields_ = [("src", C.c_void_p), ("dst", C.c_void_p), ("in_token", C.c_int64),
+                ("in_head", C.c_int64), ("out_token", C.c_int64), ("out_head", C.c_int64),
+                ("heads", C.c_int32)]
+
+
+class Norm(C.Structure):  # gs_norm
+    _fields_ = [("tokens", C.c_int64), ("channels", C.c_int32), ("groups", C.c_int32),
+                ("flags", C.c_int32), ("dtype", C.c_int32), ("res_dtype", C.c_int32),
+                ("eps", C.c_float), ("w_pre", C.c_void_p), ("w_post", C.c_void_p),
+                ("res_scale", C.c_void_p), ("gate", C.c_void_p), ("group_offsets", C.c_void_p)]
+
+
+class Ckpt(C.Structure):  # gs_ckpt
+    _fields_ = [("q", C.c_void_p), ("e", C.c_void_p), ("q_stride", C.c_int64),
+                ("e_stride", C.c_int64)]
+
+
 @pytest.fixture(scope="module")
 def gs():
     import __graft_entry__
@@ -58,7 +76,7 @@ def test_rope_refusals(gs):
 
     def call(tokens=4, axes=2, dims=r._dims, turns=r.turns, pos=p, dim=16, dtype=0, src=p, dst=p,
              heads=1, n_sets=1, sets=None):
-        s = (gs.net._Heads * 2)()
+        s = (Heads * 2)()
         for h in s:
             h.src, h.dst, h.heads = src, dst, heads
             h.in_token = h.out_token = 16 * max(heads, 1)
@@ -80,7 +98,7 @@ def test_rope_refusals(gs):
 
 
 def _norm(gs, **kw):
-    p = gs.net._Norm()
+    p = Norm()
     p.tokens, p.channels, p.groups, p.eps = 4, 8, 1, 1e-6
     p.flags = gs.net.NORM_POST
     for k, v in kw.items():
@@ -144,9 +162,9 @@ def test_act8_refusals(gs):
             assert enc(fn=fn, **kw) == bad, kw
         assert enc(fn=fn, T=0, x=None, q=None, e=None) == gs.GS_OK
 
-    ck = gs.net._Ckpt(p, p, 32, 1)
-    none = gs.net._Ckpt()
-    odd = gs.net._Ckpt(p + 4, p, 32, 1)
+    ck = Ckpt(p, p, 32, 1)
+    none = Ckpt()
+    odd = Ckpt(p + 4, p, 32, 1)
 
     def fwd(act=0, gate=p, up=p, h=p, g8=ck, u8=ck, T=2):
         return L.gs_glu_fwd(T, 8, 0, act, gate, 8, up, 8, h, 8, C.byref(g8), C.byref(u8), None)
@@ -209,3 +227,15 @@ def test_plain_checkpoint_is_the_nearest_step():
     big = torch.nn.functional.pad(x, (0, 26)).view(6, 3, 32).abs().amax(2).double()
     unit = torch.exp2(e.double() - 127)
     assert (big <= 127 * unit).all() and (big > 63.5 * unit).all()
+
+
+def test_packed_structures_have_the_c_layout(gs):
+    for packed, struct in ((gs.net._HEADS, Heads), (gs.net._NORM, Norm), (gs.net._CKPT, Ckpt)):
+        assert packed.size == C.sizeof(struct)
+    p = Norm.from_buffer_copy(gs.net._NORM.pack(1 << 40, 2, 3, 4, 5, 6, 0.5, 7, 8, 9, 10, 11))
+    assert (p.tokens, p.channels, p.groups, p.flags, p.dtype, p.res_dtype, p.eps) == (1 << 40, 2, 3, 4, 5, 6, 0.5)
+    assert (p.w_pre, p.w_post, p.res_scale, p.gate, p.group_offsets) == (7, 8, 9, 10, 11)
+    h = Heads.from_buffer_copy(gs.net._HEADS.pack(1, 2, 3, 4, 5, 6, 7))
+    assert (h.src, h.dst, h.in_token, h.in_head, h.out_token, h.out_head, h.heads) == (1, 2, 3, 4, 5, 6, 7)
+    k = Ckpt.from_buffer_copy(gs.net._CKPT.pack(1, 2, 3, 4))
+    assert (k.q, k.e, k.q_stride, k.e_stride) == (1, 2, 3, 4)
