@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kTeamThreads, 1) norm_fwd_kernel(
                 Pack<int8_t, VEC> q;
 #pragma unroll
                 for (int j = 0; j < VEC; ++j)
-                  q.v[j] = (int8_t)act8_quantise(v[r][i * VEC + j], inv, e);
+                  q.v[j] = (int8_t)(act8_quantise(v[r][i * VEC + j], inv, e) & 0xff);
                 store_pack<int8_t, VEC>(y_q + row * q_stride + c, q);
                 if (c % GS_ACT8_GROUP == 0) y_e[row * e_stride + c / GS_ACT8_GROUP] = (uint8_t)e;
               }

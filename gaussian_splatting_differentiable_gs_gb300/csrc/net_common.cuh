@@ -77,8 +77,16 @@ __device__ __forceinline__ float act8_inverse(uint32_t e) {
 // such a group reads back as.
 __device__ __forceinline__ float act8_step(uint32_t e) { return __uint_as_float(e << 23); }
 
-__device__ __forceinline__ int act8_quantise(float v, float inv, uint32_t e) {
-  return e == 255u ? 0 : __float2int_rn(v * inv);
+// q in the low byte of the result: v * inv is exact (a power of two), and adding
+// 1.5 * 2^23 rounds it to the nearest whole number, ties to even.
+__device__ __forceinline__ uint32_t act8_quantise(float v, float inv, uint32_t e) {
+  const uint32_t q = __float_as_uint(__fmaf_rn(v, inv, 12582912.f));
+  return e == 255u ? 0u : q;
+}
+// The value of byte `i` of a word of checkpoint bytes, times the step: the byte
+// (its sign bit flipped) is put into the significand of 2^23 + 128 + q.
+__device__ __forceinline__ float act8_value(uint32_t flipped, int i, float step) {
+  return (__uint_as_float(__byte_perm(flipped, 0x4b000000u, 0x7440 | i)) - 8388736.f) * step;
 }
 
 }  // namespace gs

@@ -19,6 +19,7 @@ struct RopeK {
   uint64_t turns[GS_ROPE_MAX_DIM / 2];
   int32_t dims[GS_ROPE_MAX_AXES];
   int32_t n_axes, head_dim;
+  int32_t pairs;             // that rotate
   int32_t rot_units, units;  // units that rotate, and with those that copy
   int32_t head_slots, tokens_per_block;
   float sign;
@@ -31,52 +32,51 @@ struct HeadsK {
 };
 
 constexpr int kHeadBatch = 4;  // heads a thread loads before it stores any
+constexpr int kThreads = 256;
+
+// Sine and cosine of a phase in half turns, [-1, 1).  16-bit heads take the
+// fast functions (absolute error below 2^-21 on this range, a sixteenth of the
+// rounding of an fp16 result), fp32 heads the accurate ones.
+template <typename T>
+__device__ __forceinline__ void sine(float half_turns, float* s, float* c) {
+  if (sizeof(T) == 4) sincospif(half_turns, s, c);
+  else __sincosf(half_turns * 3.14159265358979f, s, c);
+}
 
 // A unit is VEC pairs (2 VEC channels) of a head; with VEC = 1 the two channels
-// move one by one, so that any stride and an odd last channel are served.
-// Threads: unit fastest (a warp reads neighbouring channels), then head slot,
-// then token.
+// move one by one, so that any stride and an odd last channel are served.  Units
+// of neighbouring pairs (INTER) may reach over the sections' ends.  Threads: unit
+// fastest (a warp reads neighbouring channels), then head slot, then token.
 template <typename T, int VEC, bool INTER>
-__global__ void __launch_bounds__(256) rope_kernel(int64_t tokens, const __grid_constant__ RopeK k,
-                                                   const __grid_constant__ HeadsK s0,
-                                                   const __grid_constant__ HeadsK s1, int heads0,
-                                                   int heads, const int32_t* __restrict__ pos) {
+__global__ void __launch_bounds__(kThreads) rope_kernel(
+    int64_t tokens, const __grid_constant__ RopeK k, const __grid_constant__ HeadsK s0,
+    const __grid_constant__ HeadsK s1, int heads0, int heads, const int32_t* __restrict__ pos) {
   const int u = threadIdx.x % k.units;
   const int y = threadIdx.x / k.units;
   const int hs = y % k.head_slots;
   const int64_t t = (int64_t)blockIdx.x * k.tokens_per_block + y / k.head_slots;
   if (t >= tokens) return;
 
-  const bool rot = u < k.rot_units;
-  int first, second;  // channel offsets of the unit's two halves
-  float co[VEC], si[VEC];
-  if (rot) {
-    int pair = u * VEC, at = 0, axis = 0, before = 0;
+  // the unit's place: its first pair's section, and its two halves' channels
+  int axis = 0, at = 0, before = 0;
+  auto seek = [&](int pair) {
     while (axis + 1 < k.n_axes && pair - before >= k.dims[axis] / 2) {
       before += k.dims[axis] / 2;
       at += k.dims[axis];
       ++axis;
     }
-    const int j = pair - before;
-    first = INTER ? at + 2 * j : at + j;
-    second = INTER ? first + VEC : first + k.dims[axis] / 2;
-    const int64_t p = pos[t * k.n_axes + axis];
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const uint64_t phase = (uint64_t)p * k.turns[pair + i];
-      const float half_turns = (float)(int32_t)(phase >> 32) * 4.656612873077393e-10f;  // 2^-31
-      sincospif(half_turns, &si[i], &co[i]);
-      si[i] *= k.sign;
-    }
-  } else {
-    first = 2 * VEC * u;
-    second = first + VEC;
+  };
+  int first = 2 * VEC * u, second = first + VEC;
+  if (!INTER && u < k.rot_units) {
+    seek(u * VEC);
+    first = at + u * VEC - before;
+    second = first + k.dims[axis] / 2;
   }
   constexpr bool kWide = INTER && VEC > 1;  // both halves in one access
   const bool two = VEC > 1 || second < k.head_dim;
 
-  for (int h0 = hs; h0 < heads; h0 += kHeadBatch * k.head_slots) {
-    Pack<T, VEC> a[kHeadBatch], b[kHeadBatch];
+  Pack<T, VEC> a[kHeadBatch], b[kHeadBatch];
+  auto load = [&](int h0) {
 #pragma unroll
     for (int i = 0; i < kHeadBatch; ++i) {
       const int h = h0 + i * k.head_slots;
@@ -98,6 +98,26 @@ __global__ void __launch_bounds__(256) rope_kernel(int64_t tokens, const __grid_
         }
       }
     }
+  };
+  load(hs);  // on its way while the angles are computed
+
+  float co[VEC], si[VEC];
+  bool rot[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    const int pair = u * VEC + i;
+    rot[i] = INTER ? pair < k.pairs : u < k.rot_units;
+    if (rot[i]) {
+      if (INTER) seek(pair);
+      const int64_t p = pos[t * k.n_axes + axis];
+      const uint64_t phase = (uint64_t)p * k.turns[pair];
+      sine<T>((float)(int32_t)(phase >> 32) * 4.656612873077393e-10f, &si[i], &co[i]);  // 2^-31
+      si[i] *= k.sign;
+    }
+  }
+
+  for (int h0 = hs; h0 < heads; h0 += kHeadBatch * k.head_slots) {
+    if (h0 != hs) load(h0);
 #pragma unroll
     for (int i = 0; i < kHeadBatch; ++i) {
       const int h = h0 + i * k.head_slots;
@@ -106,9 +126,9 @@ __global__ void __launch_bounds__(256) rope_kernel(int64_t tokens, const __grid_
         const HeadsK& s = in0 ? s0 : s1;
         T* p = reinterpret_cast<T*>(s.out + t * s.out_token +
                                     (in0 ? h : h - heads0) * s.out_head);
-        if (rot) {
 #pragma unroll
-          for (int c = 0; c < VEC; ++c) {
+        for (int c = 0; c < VEC; ++c) {
+          if (rot[c]) {
             const float x = to_f32(a[i].v[c]), z = to_f32(b[i].v[c]);
             a[i].v[c] = from_f32<T>(x * co[c] - z * si[c]);
             b[i].v[c] = from_f32<T>(x * si[c] + z * co[c]);
@@ -203,9 +223,13 @@ extern "C" gs_status gs_rope(int64_t tokens, int32_t n_axes, const int32_t* dims
   const int rest = head_dim - rot;
   int vec = 16 / elem / (interleaved ? 2 : 1);
   auto fits = [&](int v) {
-    for (int a = 0; a < n_axes; ++a)
-      if ((dims[a] / 2) % v) return false;
-    if (v > 1 && rest % (2 * v)) return false;
+    if (interleaved) {
+      if (v > 1 && head_dim % (2 * v)) return false;
+    } else {
+      for (int a = 0; a < n_axes; ++a)
+        if ((dims[a] / 2) % v) return false;
+      if (v > 1 && rest % (2 * v)) return false;
+    }
     const int64_t bytes = (int64_t)v * elem * (interleaved && v > 1 ? 2 : 1);
     for (int i = 0; i < n_sets; ++i) {
       const gs_heads& s = sets[i];
@@ -230,10 +254,11 @@ extern "C" gs_status gs_rope(int64_t tokens, int32_t n_axes, const int32_t* dims
   for (int a = 0; a < n_axes; ++a) k.dims[a] = dims[a];
   k.n_axes = n_axes;
   k.head_dim = head_dim;
-  k.rot_units = rot / 2 / vec;
-  k.units = k.rot_units + (copies ? (int)div_up(rest, 2 * vec) : 0);
+  k.pairs = rot / 2;
+  k.rot_units = (int)div_up(rot / 2, vec);
+  k.units = copies ? (int)div_up(head_dim, 2 * vec) : k.rot_units;
   k.sign = inverse ? -1.f : 1.f;
-  const int rows = 256 / k.units;  // (token, head slot) pairs of a block
+  const int rows = kThreads / k.units;  // (token, head slot) pairs of a block
   int slots = (int)div_up(heads, kHeadBatch);
   k.head_slots = slots < rows ? slots : rows;
   k.tokens_per_block = rows / k.head_slots;

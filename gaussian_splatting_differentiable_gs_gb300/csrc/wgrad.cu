@@ -590,8 +590,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // Joins the partial sums of the tiles that several clusters share: a block
-// takes 16 columns of a CTA's half tile, a thread one channel.
-constexpr int kJoinCols = 16;
+// takes four columns of a CTA's half tile, a thread one channel.
+constexpr int kJoinCols = 4;
 template <typename TO>
 __global__ void __launch_bounds__(128) wgrad_join_kernel(const __grid_constant__ Plan p,
                                                          const float* __restrict__ partial,
@@ -607,6 +607,7 @@ __global__ void __launch_bounds__(128) wgrad_join_kernel(const __grid_constant__
   const int ch = id % p.tiles_m * kBM + rank * 128 + threadIdx.x;
   if (ch >= p.channels) return;
   float v[kJoinCols] = {};
+#pragma unroll 4
   for (int cl = lo; cl <= hi; ++cl) {
     const int slot = (int64_t)cl * p.quota / p.steps == tile ? 0 : 1;
     const float* from = partial + ((size_t)(cl * 2 + slot) * 2 + rank) * kPartialFloats +
