@@ -3,19 +3,24 @@
 //
 // 32 channels share a power-of-two step, so a value q * step is exact in bf16
 // and in fp32 and the choice of q is the same in every implementation.  All
-// four kernels are single passes bound by memory.  A lane has eight channels:
-// WIDE, where rows start on 16-byte boundaries, eight neighbours (16-byte
-// accesses of 16-bit types; a group is four lanes); otherwise eight channels 32
-// apart (a warp's accesses are then runs of 32 elements at any alignment, and a
-// group is the warp).
+// four kernels are single passes bound by memory.  A lane has eight neighbouring
+// channels (a group is four lanes).  Where rows do not start on 16-byte
+// boundaries, a lane reads the aligned 16-byte granules that its channels touch
+// and shifts them into place; for stores a granule is put together from two
+// lanes, and only a run's two ends are written element by element.
 #include "net_common.cuh"
 
 namespace gs {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPer = 8;              // channels of a lane
+constexpr int kPer = 8;               // channels of a lane
 constexpr int kUnitsPerBlock = 2048;  // lanes' worth of work
+// Blocks an SM: 64 warps hide the memory latency of the aligned form (eight
+// blocks 246 us, six 250, five 261, four 275 for both directions of a gated unit
+// of 32640 x 2816 bf16); the other form needs more registers than that leaves.
+template <bool WIDE>
+constexpr int kBlocks = WIDE ? 8 : 4;
 
 struct Act8K {
   int8_t* q;
@@ -26,152 +31,235 @@ struct Act8K {
 struct RowsK {
   int64_t tokens;
   int32_t C;
-  int32_t upr;   // units (WIDE: lanes, else warps) per row, padding included
+  int32_t upr;   // units (lanes) per row, padding included
   int32_t rows;  // rows per block
 };
 
-template <bool WIDE>
-__device__ __forceinline__ int channel(int c, int j) {
-  return WIDE ? c + j : c + 32 * j;
-}
-
-// Writes eight channels' bytes and their groups' exponents.  Every lane of the
-// warp calls it; channels from `end` on are not stored.
-template <bool WIDE>
+// Writes eight channels' bytes and, once per group, the exponent.  Every lane of
+// the warp calls it; lanes with c >= end store nothing.
 __device__ __forceinline__ void put8(const float (&v)[kPer], const Act8K& k, int64_t t, int c,
                                      int end) {
-  int8_t* q = k.q + t * k.qs;
-  uint8_t* ep = k.e + t * k.es;
-  if (WIDE) {
-    uint32_t mag = 0;
+  uint32_t mag = 0;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) mag = max(mag, __float_as_uint(v[j]) & 0x7fffffffu);
-    mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
-    mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
-    if (c >= end) return;
-    const uint32_t e = act8_exponent(mag);
-    const float inv = act8_inverse(e);
-    uint32_t w[2];
+  for (int j = 0; j < kPer; ++j) mag = max(mag, __float_as_uint(v[j]) & 0x7fffffffu);
+  mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
+  mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
+  if (c >= end) return;
+  const uint32_t e = act8_exponent(mag);
+  const float inv = act8_inverse(e);
+  uint32_t w[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t lo = __byte_perm(act8_quantise(v[4 * h], inv, e),
-                                      act8_quantise(v[4 * h + 1], inv, e), 0x0040);
-      const uint32_t hi = __byte_perm(act8_quantise(v[4 * h + 2], inv, e),
-                                      act8_quantise(v[4 * h + 3], inv, e), 0x0040);
-      w[h] = __byte_perm(lo, hi, 0x5410);
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t lo =
+        __byte_perm(act8_quantise(v[4 * h], inv, e), act8_quantise(v[4 * h + 1], inv, e), 0x0040);
+    const uint32_t hi = __byte_perm(act8_quantise(v[4 * h + 2], inv, e),
+                                    act8_quantise(v[4 * h + 3], inv, e), 0x0040);
+    w[h] = __byte_perm(lo, hi, 0x5410);
+  }
+  *reinterpret_cast<uint2*>(k.q + t * k.qs + c) = make_uint2(w[0], w[1]);
+  if (c % GS_ACT8_GROUP == 0) k.e[t * k.es + c / GS_ACT8_GROUP] = (uint8_t)e;
+}
+
+// Eight channels of a checkpoint as they lie in memory: all of a unit's loads
+// are issued before the first value is used.
+struct Held8 {
+  uint2 q;
+  uint32_t e;
+};
+__device__ __forceinline__ Held8 load8(const Act8K& k, int64_t t, int c) {
+  return Held8{*reinterpret_cast<const uint2*>(k.q + t * k.qs + c),
+               k.e[t * k.es + c / GS_ACT8_GROUP]};
+}
+__device__ __forceinline__ float held8(const Held8& h, int j) {
+  return act8_value((j < 4 ? h.q.x : h.q.y) ^ 0x80808080u, j & 3, act8_step(h.e));
+}
+
+// z shifted down by s bytes (0 <= s < 16, even).
+template <int N>
+__device__ __forceinline__ void shift_down(uint32_t (&z)[N], int s) {
+#pragma unroll
+  for (int i = 0; i + 2 < N; ++i) z[i] = s & 8 ? z[i + 2] : z[i];
+#pragma unroll
+  for (int i = 0; i + 1 < N; ++i) z[i] = s & 4 ? z[i + 1] : z[i];
+#pragma unroll
+  for (int i = 0; i + 1 < N; ++i) z[i] = s & 2 ? __funnelshift_r(z[i], z[i + 1], 16) : z[i];
+}
+
+// A matrix whose rows start anywhere, or (WIDE) on 16-byte boundaries.
+template <typename T>
+struct Mat {
+  T* p;
+  int64_t stride;
+};
+
+// Element j of 32-bit words, and two values as a word (fp32: one).
+template <typename T>
+__device__ __forceinline__ float word_value(const uint32_t* w, int j);
+template <>
+__device__ __forceinline__ float word_value<float>(const uint32_t* w, int j) {
+  return __uint_as_float(w[j]);
+}
+template <>
+__device__ __forceinline__ float word_value<__nv_bfloat16>(const uint32_t* w, int j) {
+  return __uint_as_float(j & 1 ? w[j >> 1] & 0xffff0000u : w[j >> 1] << 16);
+}
+template <>
+__device__ __forceinline__ float word_value<__half>(const uint32_t* w, int j) {
+  return __half2float(__ushort_as_half((unsigned short)(j & 1 ? w[j >> 1] >> 16 : w[j >> 1])));
+}
+__device__ __forceinline__ uint32_t bits_of(float v) { return __float_as_uint(v); }
+__device__ __forceinline__ uint32_t bits_of(__nv_bfloat16 v) { return __bfloat16_as_ushort(v); }
+__device__ __forceinline__ uint32_t bits_of(__half v) { return __half_as_ushort(v); }
+
+// Eight channels of a matrix from c on (zeros from C on); c < C.
+template <typename T, bool WIDE>
+struct Held;
+template <typename T>
+struct Held<T, true> {
+  Pack<T, kPer> w;
+  __device__ __forceinline__ void load(const Mat<const T>& m, const RowsK&, int64_t t, int c) {
+    w = load_pack<T, kPer>(m.p + t * m.stride + c);
+  }
+  __device__ __forceinline__ float value(const RowsK&, int, int j) const { return to_f32(w.v[j]); }
+};
+template <typename T>
+struct Held<T, false> {
+  static constexpr int kWords = kPer * sizeof(T) / 4;
+  uint32_t w[kWords + 4];
+  __device__ __forceinline__ void load(const Mat<const T>& m, const RowsK& r, int64_t t, int c) {
+    const T* p = m.p + t * m.stride + c;
+    const int n = min(kPer, r.C - c) * (int)sizeof(T);
+    // granules reach up to 14 bytes out of the row: not out of the matrix
+    const int64_t apart = m.stride >= r.C ? m.stride * (int64_t)sizeof(T) : 0;
+    const bool inner = (c > 0 || t * apart >= 16) &&
+                       (c + 2 * kPer <= r.C || (r.tokens - 1 - t) * apart >= 16);
+    if (inner) {
+      const int d = (int)((uintptr_t)p & 15);
+      const char* g = (const char*)p - d;
+#pragma unroll
+      for (int i = 0; i <= kWords / 4; ++i) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (16 * i < d + n) v = *reinterpret_cast<const uint4*>(g + 16 * i);
+        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+      }
+      shift_down(w, d);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) w[i] = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (c + i < r.C)
+          w[i * (int)sizeof(T) / 4] |= bits_of(p[i]) << (sizeof(T) == 2 && (i & 1) ? 16 : 0);
     }
-    *reinterpret_cast<uint2*>(q + c) = make_uint2(w[0], w[1]);
-    if (c % GS_ACT8_GROUP == 0) ep[c / GS_ACT8_GROUP] = (uint8_t)e;
+  }
+  __device__ __forceinline__ float value(const RowsK& r, int c, int j) const {
+    return c + j < r.C ? word_value<T>(w, j) : 0.f;
+  }
+};
+
+// Stores eight channels from c on, those below C.  Every lane of the warp calls
+// it; `in`: c < C.
+template <typename T, bool WIDE>
+__device__ __forceinline__ void put(const float (&v)[kPer], const Mat<T>& m, const RowsK& r,
+                                    int64_t t, int c, bool in) {
+  T* p = m.p + t * m.stride + c;
+  if (WIDE) {
+    if (in) {
+      Pack<T, kPer> w;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) w.v[j] = from_f32<T>(v[j]);
+      store_pack<T, kPer>(p, w);
+    }
+    return;
+  }
+  constexpr int kWords = kPer * sizeof(T) / 4;
+  uint32_t w[kWords + 4];
+  T own[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) own[j] = from_f32<T>(v[j]);
+#pragma unroll
+  for (int i = 0; i < kWords; ++i)
+    w[4 + i] = sizeof(T) == 4 ? bits_of(own[i])
+                              : bits_of(own[2 * i % kPer]) | bits_of(own[(2 * i + 1) % kPer]) << 16;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = __shfl_up_sync(0xffffffffu, w[kWords + i], 1);
+  if (!in) return;
+  const int lane = threadIdx.x & 31;
+  const int d = (int)((uintptr_t)p & 15), n = min(kPer, r.C - c) * (int)sizeof(T);
+  // prev: the lane before has this row's channels before c; next: the lane after
+  // has enough of the row to store the granule that this lane's last bytes are in
+  const bool prev = lane > 0 && c > 0;
+  const bool next = lane < 31 && min(kPer, r.C - c - kPer) * (int)sizeof(T) >= 16 - d;
+  if (d) {
+    shift_down(w, 16 - d);
   } else {
-    uint32_t mine = 0;  // lane j keeps group j's exponent
-    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = w[4 + i];
+  }
+  char* g = (char*)p - d;  // granule i: bytes [16 i, 16 i + 16) from here
+  int lo = 0, hi = next ? n : min(n, 4 * kWords - d);  // own bytes [0, lo), [hi, n): one by one
+  if (d && !prev) lo = min(16 - d, n);
+#pragma unroll
+  for (int i = 0; i < kWords / 4; ++i) {
+    if (16 * (i + 1) - d <= n) {
+      if (i > 0 || !d || prev)
+        *reinterpret_cast<uint4*>(g + 16 * i) =
+            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    } else {
+      hi = min(hi, max(16 * i - d, 0));  // the row ends inside this granule
+    }
+  }
+  if (lo > 0 || hi < n) {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const uint32_t e =
-          act8_exponent(__reduce_max_sync(0xffffffffu, __float_as_uint(v[j]) & 0x7fffffffu));
-      if (c + 32 * j < end) q[c + 32 * j] = (int8_t)(act8_quantise(v[j], act8_inverse(e), e) & 0xff);
-      if (lane == j) mine = e;
+      const int b = j * (int)sizeof(T);
+      if (b < n && (b < lo || b >= hi)) p[j] = own[j];
     }
-    const int g = (c - lane) / GS_ACT8_GROUP + lane;
-    if (lane < kPer && g * GS_ACT8_GROUP < end) ep[g] = (uint8_t)mine;
-  }
-}
-
-template <bool WIDE>
-__device__ __forceinline__ void get8(float (&v)[kPer], const Act8K& k, int64_t t, int c, int end) {
-  const int8_t* q = k.q + t * k.qs;
-  const uint8_t* ep = k.e + t * k.es;
-  if (WIDE) {
-    if (c >= end) return;
-    const uint2 w = *reinterpret_cast<const uint2*>(q + c);
-    const float step = act8_step(ep[c / GS_ACT8_GROUP]);
-    const uint32_t x[2] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u};
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) v[j] = act8_value(x[j >> 2], j & 3, step);
-  } else {
-    uint32_t b[kPer], e[kPer];
-#pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      if (c + 32 * j < end) {
-        b[j] = (uint8_t)q[c + 32 * j];
-        e[j] = ep[(c + 32 * j) / GS_ACT8_GROUP];
-      }
-#pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      if (c + 32 * j < end) v[j] = act8_value(b[j] ^ 0x80u, 0, act8_step(e[j]));
-  }
-}
-
-template <typename T, bool WIDE>
-__device__ __forceinline__ void get(float (&v)[kPer], const T* row, int c, int C) {
-  if (WIDE) {
-    if (c >= C) return;
-    const Pack<T, kPer> w = load_pack<T, kPer>(row + c);
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) v[j] = to_f32(w.v[j]);
-  } else {
-    T w[kPer];
-#pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      if (c + 32 * j < C) w[j] = row[c + 32 * j];
-#pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      if (c + 32 * j < C) v[j] = to_f32(w[j]);
-  }
-}
-template <typename T, bool WIDE>
-__device__ __forceinline__ void put(const float (&v)[kPer], T* row, int c, int C) {
-  if (WIDE) {
-    if (c >= C) return;
-    Pack<T, kPer> w;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) w.v[j] = from_f32<T>(v[j]);
-    store_pack<T, kPer>(row + c, w);
-  } else {
-#pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      if (c + 32 * j < C) row[c + 32 * j] = from_f32<T>(v[j]);
   }
 }
 
 // Runs f(t, c, end) for the block's units, c the lane's first channel and end
 // the row's width with its padding (0 for lanes with nothing to do); whole
 // warps take part in each step.
-template <bool WIDE, typename F>
+template <typename F>
 __device__ __forceinline__ void each_unit(const RowsK& r, F f) {
   const int64_t row0 = (int64_t)blockIdx.x * r.rows;
   const int n = r.upr * (int)min((int64_t)r.rows, r.tokens - row0);
   const int end = (r.C + GS_ACT8_GROUP - 1) / GS_ACT8_GROUP * GS_ACT8_GROUP;
   const int lane = threadIdx.x & 31;
-  if (WIDE) {
-    for (int at = threadIdx.x; at - lane < n; at += kThreads) {
-      const int row = at / r.upr;
-      f(row0 + row, (at - row * r.upr) * kPer, at < n ? end : 0);
-    }
-  } else {
-    for (int at = threadIdx.x >> 5; at < n; at += kThreads / 32) {
-      const int row = at / r.upr;
-      f(row0 + row, (at - row * r.upr) * (32 * kPer) + lane, end);
-    }
+  for (int at = threadIdx.x; at - lane < n; at += kThreads) {
+    const int row = at / r.upr;
+    f(row0 + row, (at - row * r.upr) * kPer, at < n ? end : 0);
   }
 }
 
 template <typename T, bool WIDE>
-__global__ void __launch_bounds__(kThreads) encode_kernel(RowsK r, const T* x, int64_t xs,
-                                                          Act8K k) {
-  each_unit<WIDE>(r, [&](int64_t t, int c, int end) {
+__global__ void __launch_bounds__(kThreads, kBlocks<WIDE>)
+    encode_kernel(RowsK r, Mat<const T> x, Act8K k) {
+  each_unit(r, [&](int64_t t, int c, int end) {
     float v[kPer] = {};
-    get<T, WIDE>(v, x + t * xs, c, min(r.C, end));
-    put8<WIDE>(v, k, t, c, end);
+    if (c < min(r.C, end)) {
+      Held<T, WIDE> h;
+      h.load(x, r, t, c);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) v[j] = h.value(r, c, j);
+    }
+    put8(v, k, t, c, end);
   });
 }
 
 template <typename T, bool WIDE>
-__global__ void __launch_bounds__(kThreads) decode_kernel(RowsK r, Act8K k, T* x, int64_t xs) {
-  each_unit<WIDE>(r, [&](int64_t t, int c, int end) {
+__global__ void __launch_bounds__(kThreads, kBlocks<WIDE>)
+    decode_kernel(RowsK r, Act8K k, Mat<T> x) {
+  each_unit(r, [&](int64_t t, int c, int end) {
+    const bool in = c < min(r.C, end);
     float v[kPer];
-    get8<WIDE>(v, k, t, c, end);
-    put<T, WIDE>(v, x + t * xs, c, min(r.C, end));
+    if (in) {
+      const Held8 h = load8(k, t, c);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) v[j] = held8(h, j);
+    }
+    put<T, WIDE>(v, x, r, t, c, in);
   });
 }
 
@@ -211,55 +299,65 @@ __device__ __forceinline__ void act_both(float v, float& f, float& df) {
 }
 
 template <typename T, bool WIDE, int ACT, bool GATED>
-__global__ void __launch_bounds__(kThreads) glu_fwd_kernel(RowsK r, const T* gate, int64_t gs,
-                                                           const T* up, int64_t us, T* h,
-                                                           int64_t hs, Act8K g8, Act8K u8) {
-  each_unit<WIDE>(r, [&](int64_t t, int c, int end) {
-    const int C = min(r.C, end);
+__global__ void __launch_bounds__(kThreads, kBlocks<WIDE>)
+    glu_fwd_kernel(RowsK r, Mat<const T> gate, Mat<const T> up, Mat<T> h, Act8K g8, Act8K u8) {
+  each_unit(r, [&](int64_t t, int c, int end) {
+    const bool in = c < min(r.C, end);
     float g[kPer] = {}, u[kPer] = {}, o[kPer];
-    get<T, WIDE>(g, gate + t * gs, c, C);
-    if (GATED) get<T, WIDE>(u, up + t * us, c, C);
+    if (in) {
+      Held<T, WIDE> hg, hu;
+      hg.load(gate, r, t, c);
+      if (GATED) hu.load(up, r, t, c);
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) o[j] = act_value<ACT>(g[j]) * (GATED ? u[j] : 1.f);
-    put<T, WIDE>(o, h + t * hs, c, C);
-    if (g8.q) put8<WIDE>(g, g8, t, c, end);
-    if (GATED && u8.q) put8<WIDE>(u, u8, t, c, end);
+      for (int j = 0; j < kPer; ++j) {
+        g[j] = hg.value(r, c, j);
+        if (GATED) u[j] = hu.value(r, c, j);
+        o[j] = act_value<ACT>(g[j]) * (GATED ? u[j] : 1.f);
+      }
+      if (WIDE) put<T, WIDE>(o, h, r, t, c, in);
+    }
+    if (!WIDE) put<T, WIDE>(o, h, r, t, c, in);
+    if (g8.q) put8(g, g8, t, c, end);
+    if (GATED && u8.q) put8(u, u8, t, c, end);
   });
 }
 
 template <typename T, bool WIDE, int ACT, bool GATED>
-__global__ void __launch_bounds__(kThreads) glu_bwd_kernel(RowsK r, Act8K g8, Act8K u8,
-                                                           const T* dh, int64_t dhs, T* dgate,
-                                                           int64_t dgs, T* dup, int64_t dus,
-                                                           Act8K h8) {
-  each_unit<WIDE>(r, [&](int64_t t, int c, int end) {
-    const int C = min(r.C, end);
-    float g[kPer] = {}, u[kPer] = {}, d[kPer] = {};
-    get8<WIDE>(g, g8, t, c, end);
-    if (GATED) get8<WIDE>(u, u8, t, c, end);
-    get<T, WIDE>(d, dh + t * dhs, c, C);
-    float o[kPer];
+__global__ void __launch_bounds__(kThreads, kBlocks<WIDE>)
+    glu_bwd_kernel(RowsK r, Act8K g8, Act8K u8, Mat<const T> dh, Mat<T> dgate, Mat<T> dup,
+                   Act8K h8) {
+  each_unit(r, [&](int64_t t, int c, int end) {
+    const bool in = c < min(r.C, end);
+    float dg[kPer], du[kPer], o[kPer] = {};
+    if (in) {
+      const Held8 hg = load8(g8, t, c), hu = GATED ? load8(u8, t, c) : Held8{};
+      Held<T, WIDE> hd;
+      hd.load(dh, r, t, c);
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      float f, df;
-      act_both<ACT>(g[j], f, df);
-      const float w = GATED ? u[j] : 1.f;
-      o[j] = channel<WIDE>(c, j) < C ? f * w : 0.f;
-      g[j] = d[j] * w * df;
-      u[j] = d[j] * f;
+      for (int j = 0; j < kPer; ++j) {
+        float f, df;
+        act_both<ACT>(held8(hg, j), f, df);
+        const float w = GATED ? held8(hu, j) : 1.f, d = hd.value(r, c, j);
+        o[j] = WIDE || c + j < r.C ? f * w : 0.f;
+        dg[j] = d * w * df;
+        du[j] = d * f;
+      }
+      if (WIDE) {
+        put<T, WIDE>(dg, dgate, r, t, c, in);
+        if (GATED) put<T, WIDE>(du, dup, r, t, c, in);
+      }
     }
-    put<T, WIDE>(g, dgate + t * dgs, c, C);
-    if (GATED) put<T, WIDE>(u, dup + t * dus, c, C);
-    if (h8.q) put8<WIDE>(o, h8, t, c, end);
+    if (!WIDE) {
+      put<T, WIDE>(dg, dgate, r, t, c, in);
+      if (GATED) put<T, WIDE>(du, dup, r, t, c, in);
+    }
+    if (h8.q) put8(o, h8, t, c, end);
   });
 }
 
-RowsK make_rows(int64_t tokens, int32_t C, bool wide) {
-  RowsK r{tokens, C, 0, 1};
-  const int lanes = (int)div_up(C, GS_ACT8_GROUP) * (GS_ACT8_GROUP / kPer);
-  r.upr = wide ? lanes : (int)div_up(lanes, 32);
-  const int per_block = wide ? kUnitsPerBlock : kUnitsPerBlock / 32;
-  r.rows = r.upr >= per_block ? 1 : per_block / r.upr;
+RowsK make_rows(int64_t tokens, int32_t C) {
+  RowsK r{tokens, C, (int32_t)div_up(C, GS_ACT8_GROUP) * (GS_ACT8_GROUP / kPer), 1};
+  r.rows = r.upr >= kUnitsPerBlock ? 1 : kUnitsPerBlock / r.upr;
   const int64_t spread = div_up(tokens, (int64_t)device_sms() * 4);  // few tokens: use every SM
   if (r.rows > spread) r.rows = (int32_t)spread;
   return r;
@@ -306,12 +404,11 @@ extern "C" gs_status gs_act8_encode(int64_t tokens, int32_t channels, int32_t dt
   const int el = dtype_size(dtype);
   if (!x || !aligned_to(x, el) || !ckpt_ok(k, channels)) return GS_ERR_INVALID_ARG;
   const bool wide = channels % 8 == 0 && rows_aligned(x, x_stride, el, 16);
-  const RowsK r = make_rows(tokens, channels, wide);
+  const RowsK r = make_rows(tokens, channels);
   cudaStream_t st = (cudaStream_t)stream;
-  GS_ACT8_TYPES(dtype, if (wide) encode_kernel<T, true><<<blocks_of(r), kThreads, 0, st>>>(
-                           r, (const T*)x, x_stride, k);
-                else encode_kernel<T, false><<<blocks_of(r), kThreads, 0, st>>>(r, (const T*)x,
-                                                                            x_stride, k));
+  GS_ACT8_TYPES(dtype, const Mat<const T> m{(const T*)x, x_stride};
+                if (wide) encode_kernel<T, true><<<blocks_of(r), kThreads, 0, st>>>(r, m, k);
+                else encode_kernel<T, false><<<blocks_of(r), kThreads, 0, st>>>(r, m, k));
   GS_CHECK_LAUNCH();
   return GS_OK;
 }
@@ -325,12 +422,11 @@ extern "C" gs_status gs_act8_decode(int64_t tokens, int32_t channels, int32_t dt
   const int el = dtype_size(dtype);
   if (!x || !aligned_to(x, el) || !ckpt_ok(k, channels)) return GS_ERR_INVALID_ARG;
   const bool wide = channels % 8 == 0 && rows_aligned(x, x_stride, el, 16);
-  const RowsK r = make_rows(tokens, channels, wide);
+  const RowsK r = make_rows(tokens, channels);
   cudaStream_t st = (cudaStream_t)stream;
-  GS_ACT8_TYPES(dtype, if (wide) decode_kernel<T, true><<<blocks_of(r), kThreads, 0, st>>>(
-                           r, k, (T*)x, x_stride);
-                else decode_kernel<T, false><<<blocks_of(r), kThreads, 0, st>>>(r, k, (T*)x,
-                                                                            x_stride));
+  GS_ACT8_TYPES(dtype, const Mat<T> m{(T*)x, x_stride};
+                if (wide) decode_kernel<T, true><<<blocks_of(r), kThreads, 0, st>>>(r, k, m);
+                else decode_kernel<T, false><<<blocks_of(r), kThreads, 0, st>>>(r, k, m));
   GS_CHECK_LAUNCH();
   return GS_OK;
 }
@@ -349,16 +445,17 @@ extern "C" gs_status gs_glu_fwd(int64_t tokens, int32_t channels, int32_t dtype,
     return GS_ERR_INVALID_ARG;
   const bool wide = channels % 8 == 0 && rows_aligned(gate, gate_stride, el, 16) &&
                     rows_aligned(up, up_stride, el, 16) && rows_aligned(h, h_stride, el, 16);
-  const RowsK r = make_rows(tokens, channels, wide);
+  const RowsK r = make_rows(tokens, channels);
   cudaStream_t st = (cudaStream_t)stream;
 #define GS_GLU(WIDE, ACT)                                                                   \
   do {                                                                                      \
     if (up)                                                                                 \
       glu_fwd_kernel<T, WIDE, ACT, true><<<blocks_of(r), kThreads, 0, st>>>(                \
-          r, (const T*)gate, gate_stride, (const T*)up, up_stride, (T*)h, h_stride, g8, u8); \
+          r, {(const T*)gate, gate_stride}, {(const T*)up, up_stride}, {(T*)h, h_stride},   \
+          g8, u8);                                                                          \
     else                                                                                    \
       glu_fwd_kernel<T, WIDE, ACT, false><<<blocks_of(r), kThreads, 0, st>>>(               \
-          r, (const T*)gate, gate_stride, nullptr, 0, (T*)h, h_stride, g8, u8);             \
+          r, {(const T*)gate, gate_stride}, {}, {(T*)h, h_stride}, g8, u8);                 \
   } while (0)
   GS_ACT8_TYPES(dtype, if (act == GS_ACT_SILU) {
     if (wide) GS_GLU(true, GS_ACT_SILU); else GS_GLU(false, GS_ACT_SILU);
@@ -385,17 +482,17 @@ extern "C" gs_status gs_glu_bwd(int64_t tokens, int32_t channels, int32_t dtype,
   const bool wide = channels % 8 == 0 && rows_aligned(dh, dh_stride, el, 16) &&
                     rows_aligned(dgate, dgate_stride, el, 16) &&
                     rows_aligned(dup, dup_stride, el, 16);
-  const RowsK r = make_rows(tokens, channels, wide);
+  const RowsK r = make_rows(tokens, channels);
   cudaStream_t st = (cudaStream_t)stream;
 #define GS_GLU(WIDE, ACT)                                                                   \
   do {                                                                                      \
     if (dup)                                                                                \
       glu_bwd_kernel<T, WIDE, ACT, true><<<blocks_of(r), kThreads, 0, st>>>(                \
-          r, g8, u8, (const T*)dh, dh_stride, (T*)dgate, dgate_stride, (T*)dup, dup_stride, \
-          o8);                                                                              \
+          r, g8, u8, {(const T*)dh, dh_stride}, {(T*)dgate, dgate_stride},                  \
+          {(T*)dup, dup_stride}, o8);                                                       \
     else                                                                                    \
       glu_bwd_kernel<T, WIDE, ACT, false><<<blocks_of(r), kThreads, 0, st>>>(               \
-          r, g8, u8, (const T*)dh, dh_stride, (T*)dgate, dgate_stride, nullptr, 0, o8);     \
+          r, g8, u8, {(const T*)dh, dh_stride}, {(T*)dgate, dgate_stride}, {}, o8);         \
   } while (0)
   GS_ACT8_TYPES(dtype, if (act == GS_ACT_SILU) {
     if (wide) GS_GLU(true, GS_ACT_SILU); else GS_GLU(false, GS_ACT_SILU);

@@ -115,7 +115,8 @@ struct Rows {
       }
     } else {
       const int off = (int)((uintptr_t)p & 15), n = C * (int)sizeof(T);
-      const bool clip = t == 0 || stride < C;  // what lies before the row is not the tensor's
+      // whether what lies before the row is not the tensor's
+      const bool clip = stride < C || t * stride * (int64_t)sizeof(T) < 16;
       const uint32_t row = to + team * row_bytes(C);
       for (int i = first; i * 16 < off + n; i += step) {
         const int b0 = i * 16 - off;  // the granule's first byte within the row

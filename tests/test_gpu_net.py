@@ -529,6 +529,64 @@ def test_glu(gs, dt, act, gated, T, Cn, pad):
     assert torch.equal(d2, dgate)
 
 
+@pytest.mark.parametrize("dt", [torch.float16, torch.float32])
+@pytest.mark.parametrize("Cn", [1, 2, 3, 5, 7, 8, 9, 15, 16, 17, 23, 31, 33, 250, 263, 520])
+@pytest.mark.parametrize("offset,pad", [(0, 0), (1, 0), (1, 1), (3, 2), (5, 6), (8, 8), (7, 9)])
+def test_rows_at_any_alignment(gs, dt, Cn, offset, pad):
+    """Every alignment of a row: the same bits as from aligned rows, and nothing
+    but the rows is written."""
+    T = 37
+    g = _gen(Cn)
+    gate, up, dh = (torch.randn(T, Cn, generator=g).to(dt) for _ in range(3))
+    wide = -(-Cn // 32) * 32
+
+    def aligned(x):
+        v = torch.zeros(T, wide, dtype=dt, device="cuda")
+        v[:, :Cn] = x
+        return v
+
+    def room():
+        w = Cn + pad
+        flat = torch.full((T * w + offset + 40,), 7.0, dtype=dt, device="cuda")
+        return flat, flat[offset:offset + T * w].view(T, w)[:, :Cn]
+
+    def untouched(flat):
+        w = Cn + pad
+        keep = torch.ones_like(flat, dtype=torch.bool)
+        keep[offset:offset + T * w].view(T, w)[:, :Cn] = False
+        return bool((flat[keep] == 7.0).all())
+
+    ref = [torch.empty(T, wide, dtype=dt, device="cuda") for _ in range(3)]
+    r8 = gs.act8_empty(T, wide), gs.act8_empty(T, wide)
+    gs.gs_glu_fwd(aligned(gate), aligned(up), ref[0], *r8[0], *r8[1], act="gelu")
+    gs.gs_glu_bwd(*r8[0], *r8[1], aligned(dh), ref[1], ref[2], act="gelu")
+    k8 = gs.act8_empty(T, Cn), gs.act8_empty(T, Cn)
+    bufs = [room() for _ in range(4)]
+    args = [room() for _ in range(3)]
+    for (_, v), x in zip(args, (gate, up, dh)):
+        v.copy_(x)
+    gs.gs_glu_fwd(args[0][1], args[1][1], bufs[0][1], *k8[0], *k8[1], act="gelu")
+    gs.gs_glu_bwd(*k8[0], *k8[1], args[2][1], bufs[1][1], bufs[2][1], act="gelu")
+    assert all(torch.equal(a, b) for x, y in zip(k8, r8) for a, b in zip(x, y))
+    for (flat, v), want in zip(bufs, ref):
+        assert torch.equal(v, want[:, :Cn]) and untouched(flat)
+    flat, v = bufs[3]
+    gs.gs_act8_decode(*k8[0], v)
+    assert torch.equal(v.double().cpu(), plain.decode(*[z.cpu() for z in k8[0]], Cn).to(dt).double())
+    assert untouched(flat)
+    # norms: the same bits at every alignment that is not a multiple of 16 bytes
+    # (rows on such multiples are summed in another order)
+    size = gate.element_size()
+    if offset * size % 16 == 0 and (Cn + pad) * size % 16 == 0 and Cn * size % 16 == 0:
+        return
+    st, xo, y = torch.empty(T, 4, device="cuda"), room(), room()
+    gs.gs_gated_norm_fwd(args[0][1], args[1][1], xo[1], y[1], st)
+    st2, want = torch.empty(T, 4, device="cuda"), [_cuda(torch.zeros(T, Cn, dtype=dt), 1, 1) for _ in range(2)]
+    gs.gs_gated_norm_fwd(_cuda(gate, 1, 1), _cuda(up, 1, 1), *want, st2)
+    assert torch.equal(xo[1], want[0]) and torch.equal(y[1], want[1]) and torch.equal(st, st2)
+    assert untouched(xo[0]) and untouched(y[0])
+
+
 def test_glu_gradient_against_differences(gs):
     """dgate and dup against central differences of the library's forward at
     the checkpoint's values."""
