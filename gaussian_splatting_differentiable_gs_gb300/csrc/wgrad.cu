@@ -3,23 +3,24 @@
 //
 //   dw[n][c] = sum_t dy[t][n] * q[t][c] * 2^(e[t][c / 32] - 127)
 //
-// The product is D (channels x columns of dy) = X8^T dY, summed over tokens.
-// Both factors are read along the tokens, so both operands are "MN-major": 64
-// neighbouring channels or columns of one token are one 128-byte row of a
-// swizzled tile.  A pair of CTAs (a cluster of two) works on 256 channels x BN
-// columns with tcgen05.mma over both SMs: each CTA holds 128 channels of X8 and
-// half of the columns, so a token step costs each SM only its own half of
-// either operand.
+// The product is D (channels x columns of dy) = X8^T dY, summed over tokens.  A
+// pair of CTAs (a cluster of two) works on 256 channels x BN columns with
+// tcgen05.mma over both SMs: each CTA holds 128 channels of X8 and half of the
+// columns.  dy is read as it lies ("MN-major": 64 neighbouring columns of one
+// token are one 128-byte row of a swizzled tile).  X8 goes to TMEM: an operand
+// there has a channel per lane and a pair of tokens per column, and it neither
+// has to be written to nor read from shared memory, whose bandwidth is what
+// bounds this product (with X8 as a second operand in shared memory a step of 64
+// tokens took 1200 cycles, 350 of them for writing and re-reading it, against
+// 512 of the tensor cores).
 //
-// Warps of a CTA: one brings dy in by TMA, one the checkpoint's bytes (TMA) and
-// exponents, eight turn the bytes into bf16 (exact: at most 8 significant bits
-// times a power of two) from one ring of shared-memory stages to the next, one
-// (of the pair's first CTA) issues the products, eight add finished runs of
-// products from one half of TMEM to their registers, while the next run is
-// summed in the other half, and write the result.  The decoding warps touch shared memory only: a
-// fence or a cluster-wide release in a thread with global loads in flight
-// waits for those loads (with the bytes loaded by the decoding threads
-// themselves the same product took 2.5 times as long).
+// Warps of a CTA: one brings dy in by TMA, one the checkpoint's bytes (TMA), one
+// its exponents, eight turn the bytes into bf16 (exact: at most 8 significant
+// bits times a power of two) on the way from shared memory to TMEM, one (of the
+// pair's first CTA) issues the products, eight add finished runs of products
+// from TMEM to their registers and write the result.  The decoding warps touch
+// shared memory and TMEM only: a cluster-wide release or a fence in a thread
+// with global loads in flight waits for those loads.
 //
 // dy enters whole in every type: bf16 by TMA as it lies in memory where its
 // rows allow it; otherwise as 1 (bf16), 2 (fp16) or 3 (fp32) bf16 terms whose
@@ -42,24 +43,24 @@ namespace {
 constexpr int kBM = 256;          // channels of a tile (two CTAs of 128)
 constexpr int kBN = 256;          // most columns of a tile
 constexpr int kBT = 64;           // tokens of a step
-constexpr int kStages = 5;        // of bf16 operands
+constexpr int kStages = 8;        // of operands: dy in shared memory, X8 in TMEM
 constexpr int kRaw = 6;           // of checkpoint bytes
-constexpr int kABytes = 128 * kBT * 2;      // a CTA's half of X8 (bf16)
+constexpr int kAColumns = kBT / 2;          // TMEM columns of a CTA's half of X8
 constexpr int kBBytes = kBN / 2 * kBT * 2;  // a CTA's half of dy
-constexpr int kStageBytes = kABytes + kBBytes;
+static_assert(kBN + kStages * kAColumns <= 512, "TMEM");
 constexpr int kRawBytes = 128 * kBT;        // a CTA's 128 channels
-constexpr int kExpBytes = 4 * kBT;          // and their exponents, 4 a token
+constexpr int kExpBytes = 2 * 4 * kBT;      // and their steps as bf16, [4 groups][tokens]
 constexpr int kBatch = 8, kBatches = 4;  // exponents: steps of a batch, batches of the ring
 constexpr int kCtrlBytes = 1024;
 constexpr int kSmem =
-    kStages * kStageBytes + kRaw * kRawBytes + kBatches * kBatch * kExpBytes + kCtrlBytes + 1024;  // + alignment
+    kStages * kBBytes + kRaw * kRawBytes + kBatches * kBatch * kExpBytes + kCtrlBytes + 1024;  // + alignment
 constexpr int kDecodeWarps = 8, kTeamWarps = 4, kTeams = kDecodeWarps / kTeamWarps;
-constexpr int kItems = 4 * kBT / (32 * kTeamWarps);
+static_assert(kTeamWarps == 4, "a team's warps are the four quarters of TMEM's lanes");
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (4 + kEpiWarps + kDecodeWarps);
 // Registers a thread: the launch gives every thread kLaunchRegs, the roles
-// then share those out (sums per CTA: 61,440 at launch, 60,416 in use).
-constexpr int kLaunchRegs = 96, kCtrlRegs = 48, kEpiRegs = 160, kDecodeRegs = 56;
+// then share those out (61,440 a CTA).
+constexpr int kLaunchRegs = 96, kCtrlRegs = 48, kEpiRegs = 176, kDecodeRegs = 40;
 static_assert(128 * kCtrlRegs + 32 * kEpiWarps * kEpiRegs + 32 * kDecodeWarps * kDecodeRegs <=
                   kThreads * kLaunchRegs,
               "a role would wait for registers that the launch does not have");
@@ -69,7 +70,7 @@ static_assert(128 * kCtrlRegs + 32 * kEpiWarps * kEpiRegs + 32 * kDecodeWarps * 
 // the fp32 units: 8.8e-7); in runs of 32 steps, added up in registers with
 // rounding, by 4.7e-7.
 constexpr int kChunk = 32;
-static_assert(kTeams <= kStages && kTeams <= kRaw && kBatch % kTeams == 0, "rings");
+static_assert(kTeams <= kStages && kTeams <= kRaw, "rings");
 constexpr int kMaxClusters = 128;
 constexpr size_t kPartialFloats = (size_t)128 * kBN;  // one CTA's half tile
 constexpr unsigned int kErrTimeout = 1u;
@@ -115,36 +116,46 @@ __device__ __forceinline__ void each_seg(const Plan& p, int cluster, F f) {
   }
 }
 
-// The same steps one by one.
+// The same steps one by one.  Every role goes through it once per step, on the
+// latency of its own instructions: divisions are done once per segment.
 struct Walk {
   const Plan& p;
-  int cluster, wave, tile, k, end;
+  int cluster, wave, left;
   int64_t at, stop;
+  int ch0, n0;    // the tile's first channel and column
+  int ts, term;   // the step's tokens (from 64 ts on) and term of dy
   __device__ __forceinline__ Walk(const Plan& plan, int cl)
-      : p(plan), cluster(cl), wave(0), tile(0), k(-1), end(0) {
+      : p(plan), cluster(cl), wave(0), left(0), ch0(0), n0(0), ts(0), term(0) {
     at = (int64_t)cl * p.quota;
     stop = min(at + p.quota, p.rem_steps);
   }
+  __device__ __forceinline__ void begin(int tile, int first, int steps) {
+    n0 = tile / p.tiles_m * p.bn;
+    ch0 = tile % p.tiles_m * kBM;
+    ts = first / p.terms;
+    term = first - ts * p.terms;
+    left = steps - 1;
+  }
   __device__ __forceinline__ bool next() {
-    if (++k < end) return true;
-    if (wave < p.waves) {
-      tile = wave++ * p.clusters + cluster;
-      k = 0;
-      end = p.steps;
+    if (--left >= 0) {
+      if (++term == p.terms) {
+        term = 0;
+        ++ts;
+      }
       return true;
     }
-    if (at >= stop) {
-      k = end;
-      return false;
+    if (wave < p.waves) {
+      begin(wave++ * p.clusters + cluster, 0, p.steps);
+      return true;
     }
+    if (at >= stop) return false;
     const int i = (int)(at / p.steps);
     const int64_t upto = min(stop, (int64_t)(i + 1) * p.steps);
-    tile = p.waves * p.clusters + i;
-    k = (int)(at - (int64_t)i * p.steps);
-    end = k + (int)(upto - at);
+    begin(p.waves * p.clusters + i, (int)(at - (int64_t)i * p.steps), (int)(upto - at));
     at = upto;
     return true;
   }
+  __device__ __forceinline__ bool last() const { return left == 0; }  // of its segment
 };
 
 __device__ __forceinline__ int64_t cluster_steps(const Plan& p, int cluster) {
@@ -162,6 +173,12 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ uint32_t in_cta0(uint32_t addr) {  // the pair's first CTA
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
@@ -177,9 +194,9 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {  // shared::cluster address
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// On a barrier of the pair's first CTA, for operand bytes in this CTA's own
-// shared memory: the writers' proxy fence has made them visible to the tensor
-// core, so the arrival need not order them at cluster scope.
+// On a barrier of the pair's first CTA, for an operand in this CTA's own TMEM:
+// the writers' waits and tcgen05 fences order it for the tensor core, so the
+// arrival need not order memory at cluster scope.
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -206,7 +223,7 @@ struct Control {
   uint64_t raw_full[kRaw], raw_empty[kRaw];      // bytes of a step
   uint64_t exp_full[kBatches], exp_empty[kBatches];
   uint64_t full[kStages], empty[kStages];        // both operands of both CTAs (the first's)
-  uint64_t acc_full[2], acc_empty[2];
+  uint64_t acc_full, acc_empty;
   uint32_t tmem;
   volatile uint32_t abort;
 };
@@ -218,9 +235,9 @@ __device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, Co
   long long t0, t1;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
   while (true) {
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try(bar, parity)) return true;
+    if (mbar_try(bar, parity)) return true;
     if (c->abort) return false;
+    __nanosleep(50);
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t1));
     if (t1 - t0 > kWaitNs) {
       c->abort = 1;
@@ -259,15 +276,16 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
   return (uint64_t)((addr & 0x3ffff) >> 4) | (kMn << 16) | (kTok << 32) | ((uint64_t)1 << 46) |
          ((uint64_t)2 << 61);
 }
-// Instruction descriptor: fp32 accumulator, bf16 operands, both MN-major.
+// Instruction descriptor: fp32 accumulator, bf16 operands, the second MN-major.
 __device__ __forceinline__ uint32_t instr_desc(int n) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) | ((uint32_t)(n >> 3) << 17) |
+  return (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(kBM >> 4) << 24);
 }
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+// First operand in TMEM (each CTA's own), second in shared memory.
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile(
       "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a), "l"(b),
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d), "r"(a), "l"(b),
       "r"(idesc), "r"((uint32_t)add)
       : "memory");
 }
@@ -278,16 +296,42 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
       "[%0], %1;" ::"r"(bar), "h"((uint16_t)3)
       : "memory");
 }
-__device__ __forceinline__ void tmem_load8(uint32_t addr, float (&r)[8]) {
-  uint32_t v[8];
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-                 "=r"(v[7])
-               : "r"(addr)
-               : "memory");
+// 32 columns of the warp's lanes, added to acc.
+__device__ __forceinline__ void tmem_add32(uint32_t addr, float* acc) {
+  uint32_t v[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]),
+        "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]),
+        "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(addr)
+      : "memory");
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 8; ++i) r[i] = __uint_as_float(v[i]);
+  for (int i = 0; i < 32; ++i) acc[i] += __uint_as_float(v[i]);
+}
+// 16 lanes x 8 columns: thread t gives columns 2 (t % 4) and the next of lane
+// t / 4, then of lane t / 4 + 8.
+__device__ __forceinline__ void tmem_store16x8(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                               uint32_t d) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+__device__ __forceinline__ uint32_t load_shared(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 load_shared2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
 }
 
 template <typename TO>
@@ -295,25 +339,17 @@ __device__ __forceinline__ void put_dw(TO* p, float v, int accumulate) {
   *p = from_f32<TO>(accumulate ? v + to_f32(*p) : v);
 }
 
-// Four bytes of the checkpoint to four bf16 values times a step (a pair of
-// equal bf16).  A byte b = 128 s + m (two's complement: the value is m - 128 s)
+// Two bytes of the checkpoint (the low bytes of the halves) to two bf16 values
+// times two steps.  A byte b = 128 s + m (two's complement: the value is m - 128 s)
 // sits in the significand of 128 + m; taking 128 (s = 0) or 256 (s = 1), whose
 // bf16 patterns differ by that very bit, from it leaves the value.  Exact.
-__device__ __forceinline__ uint32_t decode2(uint32_t bytes, __nv_bfloat162 step) {
+__device__ __forceinline__ uint32_t decode2(uint32_t bytes, uint32_t steps) {
   const uint32_t m = (bytes & 0x007f007fu) | 0x43004300u;
   const uint32_t c = (bytes & 0x00800080u) | 0x43004300u;
   const __nv_bfloat162 v = __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&m),
                                            *reinterpret_cast<const __nv_bfloat162*>(&c)),
-                                   step);
+                                   *reinterpret_cast<const __nv_bfloat162*>(&steps));
   return *reinterpret_cast<const uint32_t*>(&v);
-}
-__device__ __forceinline__ uint4 decode8(uint32_t lo, uint32_t hi, __nv_bfloat162 step) {
-  uint4 r;
-  r.x = decode2(__byte_perm(lo, 0, 0x4140), step);
-  r.y = decode2(__byte_perm(lo, 0, 0x4342), step);
-  r.z = decode2(__byte_perm(hi, 0, 0x4140), step);
-  r.w = decode2(__byte_perm(hi, 0, 0x4342), step);
-  return r;
 }
 
 template <typename TO>
@@ -323,10 +359,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                  int64_t es, TO* dw, float* partial, unsigned int* status) {
   extern __shared__ uint8_t raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
-  uint8_t* raw_q = smem + kStages * kStageBytes;
+  uint8_t* raw_q = smem + kStages * kBBytes;
   uint8_t* raw_e = raw_q + kRaw * kRawBytes;
   Control* c = (Control*)(raw_e + kBatches * kBatch * kExpBytes);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (the same in every lane, and known to be)
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int cluster = blockIdx.x >> 1;
 
@@ -343,10 +380,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&c->exp_full[i]), 1);
       mbar_init(smem_u32(&c->exp_empty[i]), kBatch * kTeamWarps);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&c->acc_full[i]), 1);
-      mbar_init(smem_u32(&c->acc_empty[i]), 2 * kEpiWarps);
-    }
+    mbar_init(smem_u32(&c->acc_full), 1);
+    mbar_init(smem_u32(&c->acc_empty), 2 * kEpiWarps);
     c->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -365,70 +400,75 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtrlRegs));
   if (warp == 0) {
     // ---- dy by TMA: this CTA's half of the tile's columns ------------------
-    if (lane == 0) {
-      uint32_t it = 0;
-      const int half = p.bn / 2;
-      each_seg(p, cluster, [&](const Seg& s) {
-        const int x0 = s.tile / p.tiles_m * p.bn + (int)rank * half;
-        for (int k = s.s0; k < s.s1; ++k, ++it) {
-          const uint32_t st = it % kStages, ph = (it / kStages) & 1;
-          if (!mbar_wait(smem_u32(&c->empty[st]), ph ^ 1, c, status)) return false;
-          const uint32_t bar = smem_u32(&c->full[st]);
-          if (rank == 0) mbar_expect(bar, (uint32_t)(half * kBT * 2 * 2));
-          const uint32_t dst = smem_u32(smem + st * kStageBytes + kABytes);
-          const int y = (int)((k % p.terms) * p.term_rows) + k / p.terms * kBT;
-          for (int b = 0; b < half / 64; ++b)
-            tma_load(dst + b * (kBT * 128), &dy_map, x0 + b * 64, y, in_cta0(bar));
-        }
-        return true;
-      });
-      // the last products release the last stages: every arrival is in before this CTA ends
-      for (uint32_t back = it < kStages ? it : kStages; back > 0; --back) {
-        const uint32_t i = it - back;
-        if (!mbar_wait(smem_u32(&c->empty[i % kStages]), (i / kStages) & 1, c, status)) break;
+    const bool issues = elect_one();
+    const int half = p.bn / 2;
+    const uint32_t bars = in_cta0(smem_u32(&c->full[0])), bytes = (uint32_t)(half * kBT * 2 * 2);
+    const uint32_t total = (uint32_t)cluster_steps(p, cluster);
+    Walk w(p, cluster);
+    uint32_t st = 0, phase = 0;
+    for (uint32_t it = 0; it < total; ++it) {
+      w.next();
+      if (!mbar_wait(smem_u32(&c->empty[st]), phase ^ 1, c, status)) break;
+      if (issues) {
+        if (rank == 0) mbar_expect(smem_u32(&c->full[st]), bytes);
+        const uint32_t dst = smem_u32(smem) + st * kBBytes;
+        const int x = w.n0 + (int)rank * half, y = w.term * (int)p.term_rows + w.ts * kBT;
+        tma_load(dst, &dy_map, x, y, bars + st * 8);
+        if (half == 128) tma_load(dst + kBT * 128, &dy_map, x + 64, y, bars + st * 8);
       }
+      if (++st == kStages) st = 0, phase ^= 1;
     }
+    // the last products release the last stages: every arrival is in before this CTA ends
+    for (uint32_t i = total < kStages ? 0 : total - kStages; i < total; ++i)
+      if (!mbar_wait(smem_u32(&c->empty[i % kStages]), (i / kStages) & 1, c, status)) break;
   } else if (warp == 1) {
     // ---- products ----------------------------------------------------------
-    if (rank == 0 && lane == 0) {
+    // The whole warp walks the steps, so that what it computes stays in uniform
+    // registers, as the product's operands have to be; one elected lane issues.
+    if (rank == 0) {
       const uint32_t idesc = instr_desc(p.bn);
-      uint32_t it = 0, chunk = 0;
-      each_seg(p, cluster, [&](const Seg& s) {
-        for (int k = s.s0; k < s.s1; ++k, ++it) {
-          const bool first = (k - s.s0) % kChunk == 0;
-          const uint32_t buf = chunk & 1;
-          if (first) {
-            if (!mbar_wait(smem_u32(&c->acc_empty[buf]), ((chunk >> 1) & 1) ^ 1, c, status))
-              return false;
-          }
-          const uint32_t st = it % kStages;
-          if (!mbar_wait(smem_u32(&c->full[st]), (it / kStages) & 1, c, status)) return false;
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint64_t a = smem_desc(smem_u32(smem + st * kStageBytes));
-          const uint64_t b = smem_desc(smem_u32(smem + st * kStageBytes + kABytes));
+      const bool issues = elect_one();
+      const uint64_t b_first = smem_desc(smem_u32(smem));
+      const int64_t total = cluster_steps(p, cluster);
+      Walk w(p, cluster);
+      uint32_t st = 0, phase = 0, run = 0, chunk = 0;
+      for (int64_t it = 0; it < total; ++it) {
+        w.next();
+        if (run == 0 && !mbar_wait(smem_u32(&c->acc_empty), (chunk & 1) ^ 1, c, status)) break;
+        if (!mbar_wait(smem_u32(&c->full[st]), phase, c, status)) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t a = tmem + kBN + st * kAColumns;
+        const uint64_t b = b_first + st * (kBBytes >> 4);
+        ++run;
+        const bool last = run == kChunk || w.last();
+        if (issues) {
 #pragma unroll
-          for (int i = 0; i < kBT / 16; ++i)  // 16 tokens are two atoms: 2048 bytes
-            mma(tmem + buf * kBN, a + (i * 2048 >> 4), b + (i * 2048 >> 4), idesc, !first || i > 0);
+          for (int i = 0; i < kBT / 16; ++i)  // 16 tokens: 8 columns, and two atoms of 1024 bytes
+            mma(tmem, a + 8 * i, b + (i * 2048 >> 4), idesc, run > 1 || i > 0);
           mma_commit(smem_u32(&c->empty[st]));
-          if ((k - s.s0) % kChunk == kChunk - 1 || k + 1 == s.s1) {
-            mma_commit(smem_u32(&c->acc_full[buf]));
-            ++chunk;
-          }
+          if (last) mma_commit(smem_u32(&c->acc_full));
         }
-        return true;
-      });
+        if (last) {
+          run = 0;
+          ++chunk;
+        }
+        if (++st == kStages) st = 0, phase ^= 1;
+      }
     }
   } else if (warp == 3) {
     // ---- the checkpoint's bytes by TMA -------------------------------------
-    if (lane == 0) {
-      Walk w(p, cluster);
-      for (uint32_t it = 0; w.next(); ++it) {
-        const uint32_t rs = it % kRaw, bar = smem_u32(&c->raw_full[rs]);
-        if (!mbar_wait(smem_u32(&c->raw_empty[rs]), ((it / kRaw) & 1) ^ 1, c, status)) break;
+    const bool issues = elect_one();
+    Walk w(p, cluster);
+    uint32_t rs = 0, phase = 0;
+    while (w.next()) {
+      if (!mbar_wait(smem_u32(&c->raw_empty[rs]), phase ^ 1, c, status)) break;
+      if (issues) {
+        const uint32_t bar = smem_u32(&c->raw_full[rs]);
         mbar_expect(bar, kRawBytes);
-        tma_load_own(smem_u32(raw_q + rs * kRawBytes), &q_map,
-                     w.tile % p.tiles_m * kBM + (int)rank * 128, w.k / p.terms * kBT, bar);
+        tma_load_own(smem_u32(raw_q) + rs * kRawBytes, &q_map, w.ch0 + (int)rank * 128, w.ts * kBT,
+                     bar);
       }
+      if (++rs == kRaw) rs = 0, phase ^= 1;
     }
   } else if (warp == 2) {
     // ---- and its exponents, kBatch steps at a time ---------------------------
@@ -444,10 +484,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int i = 0; i < kBatch; ++i) {
         x[i][0] = x[i][1] = 0x01010101u;
         if (!w.next()) continue;
-        const int g = w.tile % p.tiles_m * (kBM / GS_ACT8_GROUP) + (int)rank * 4;
+        const int g = w.ch0 / GS_ACT8_GROUP + (int)rank * 4;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int64_t t = (int64_t)(w.k / p.terms) * kBT + lane + 32 * h;
+          const int64_t t = (int64_t)w.ts * kBT + lane + 32 * h;
           if (t >= p.tokens) continue;
           const uint8_t* src = e + t * es + g;
           if (words && g + 4 <= groups) {
@@ -464,12 +504,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!__all_sync(0xffffffffu,
                       mbar_wait(smem_u32(&c->exp_empty[bs]), ((n / kBatches) & 1) ^ 1, c, status)))
         break;
-      uint32_t* to = reinterpret_cast<uint32_t*>(raw_e + bs * kBatch * kExpBytes);
+      uint16_t* to = reinterpret_cast<uint16_t*>(raw_e + bs * kBatch * kExpBytes) + lane;
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        to[i * 64 + lane] = x[i][0];
-        to[i * 64 + lane + 32] = x[i][1];
-      }
+      for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)  // 2^(e - 127) in bf16; 255: infinity
+          to[i * 256 + (j & 3) * 64 + (j >> 2) * 32] =
+              (uint16_t)((x[i][j >> 2] >> 8 * (j & 3) & 0xffu) << 7);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&c->exp_full[bs]));
     }
@@ -478,30 +519,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
     const int quarter = warp & 3;  // the TMEM lanes this warp may read
     const int cols = p.bn / 2, c0 = (warp - 4) / 4 * cols;
-    const int row = quarter * 32 + lane;
+    // the lane's channel: see the decoding warps
+    const int row = quarter * 32 + 4 * (lane & 7) + (lane >> 3);
     uint32_t chunk = 0;
     each_seg(p, cluster, [&](const Seg& s) {
       float acc[kBN / 2];
 #pragma unroll
       for (int j = 0; j < kBN / 2; ++j) acc[j] = 0.f;
       for (int k = s.s0; k < s.s1; k += kChunk, ++chunk) {
-        const uint32_t buf = chunk & 1;
-        if (!__all_sync(0xffffffffu,
-                        mbar_wait(smem_u32(&c->acc_full[buf]), (chunk >> 1) & 1, c, status)))
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&c->acc_full), chunk & 1, c, status)))
           return false;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t from = tmem + buf * kBN + c0 + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t from = tmem + c0 + ((uint32_t)(quarter * 32) << 16);
 #pragma unroll
-        for (int j = 0; j < kBN / 2; j += 8)
-          if (j < cols) {
-            float r[8];
-            tmem_load8(from + j, r);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) acc[j + i] += r[i];
-          }
+        for (int j = 0; j < kBN / 2; j += 32)
+          if (j < cols) tmem_add32(from + j, acc + j);
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(in_cta0(smem_u32(&c->acc_empty[buf])));
+        if (lane == 0) mbar_arrive_cluster(in_cta0(smem_u32(&c->acc_empty)));
       }
       const int n0 = s.tile / p.tiles_m * p.bn + c0;
       const int ch = s.tile % p.tiles_m * kBM + (int)rank * 128 + row;
@@ -525,54 +560,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // kTeams teams of warps take the steps in turn: a step's waits, loads and
     // fence then overlap with those of the next steps.  A thread's items are one
     // token and one group of 32 channels each.
+    //
+    // A warp has a quarter of TMEM's lanes: 32 channels, one group.  Thread t takes
+    // the word of channels 4 (t / 4) .. + 3 of tokens 4 (t % 4) .. + 3 of every 16,
+    // and gives lanes t / 4 + 8 i the pairs of channel i of the four: lane r of the
+    // quarter holds channel 4 (r % 8) + r / 8.  The threads of the upper two token
+    // groups read their tokens in the order 2, 3, 0, 1: with the bytes' 16-byte
+    // chunks swizzled by the token, the warp's words then lie in 32 banks.
     const int team = (warp - 4 - kEpiWarps) / kTeamWarps;
-    const int id = threadIdx.x - 32 * (4 + kEpiWarps) - team * kTeamWarps * 32;
-    const int grp = id & 3;
+    const int quarter = warp & 3, word = lane >> 2, grp = lane & 3;
+    const bool swap = grp >= 2;
+    const uint32_t lanes = tmem + kBN + ((uint32_t)(quarter * 32) << 16);
+    uint32_t from[4];  // the four tokens' words of a stage; the next 16 tokens are 2048 bytes on
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = grp * 4 + (swap ? i ^ 2 : i);
+      from[i] = smem_u32(raw_q) + t * 128 + (((quarter * 2 + (word >> 2)) ^ (t & 7)) << 4) +
+                (word & 3) * 4;
+    }
+    const uint32_t steps = smem_u32(raw_e) + quarter * (2 * kBT) + grp * 8;
+    const uint32_t full = in_cta0(smem_u32(&c->full[0]));
     const uint32_t total = (uint32_t)cluster_steps(p, cluster);
+    uint32_t st = team, st_phase = 0, rs = team, rs_phase = 0, slot = team, slot_phase = 0;
     for (uint32_t it = team; it < total; it += kTeams) {
-      const uint32_t rs = it % kRaw, st = it % kStages, n = it / kBatch, bs = n % kBatches;
       if (!__all_sync(0xffffffffu,
-                      mbar_wait(smem_u32(&c->exp_full[bs]), (n / kBatches) & 1, c, status) &&
-                          mbar_wait(smem_u32(&c->raw_full[rs]), (it / kRaw) & 1, c, status)))
+                      mbar_wait(smem_u32(&c->exp_full[slot / kBatch]), slot_phase, c, status) &&
+                          mbar_wait(smem_u32(&c->raw_full[rs]), rs_phase, c, status) &&
+                          mbar_wait(smem_u32(&c->empty[st]), st_phase ^ 1, c, status)))
         break;
-      // The order of an item's two 16-byte halves: eight neighbouring lanes (two
-      // tokens, four groups) then read, and store, eight different 16-byte banks.
-      uint4 v[kItems][2];
-      __nv_bfloat162 step[kItems];
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint32_t bytes = rs * kRawBytes, step_at = steps + slot * kExpBytes;
+      const uint32_t to = lanes + st * kAColumns;
 #pragma unroll
-      for (int i = 0; i < kItems; ++i) {
-        const int tok = (id >> 2) + i * (kTeamWarps * 8), flip = (grp >> 1) ^ (tok & 1);
-        const uint4* from =
-            reinterpret_cast<const uint4*>(raw_q + rs * kRawBytes + tok * 128 + grp * 32);
-        v[i][0] = from[flip];
-        v[i][1] = from[flip ^ 1];
-        const uint32_t ex = raw_e[(it % (kBatch * kBatches)) * kExpBytes + tok * 4 + grp];
-        const uint32_t s2 = ex << 7 | ex << 23;
-        step[i] = *reinterpret_cast<const __nv_bfloat162*>(&s2);
+      for (int b = 0; b < kBT / 16; ++b) {  // 16 tokens: 8 columns
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = load_shared(from[i] + bytes + b * 2048);
+        const uint2 s = load_shared2(step_at + b * 32);
+        const uint32_t w0 = swap ? w[2] : w[0], w1 = swap ? w[3] : w[1];
+        const uint32_t w2 = swap ? w[0] : w[2], w3 = swap ? w[1] : w[3];
+        tmem_store16x8(to + b * 8, decode2(__byte_perm(w0, w1, 0x0400), s.x),
+                       decode2(__byte_perm(w2, w3, 0x0400), s.y),
+                       decode2(__byte_perm(w0, w1, 0x0501), s.x),
+                       decode2(__byte_perm(w2, w3, 0x0501), s.y));
+        tmem_store16x8(to + b * 8 + (16u << 16), decode2(__byte_perm(w0, w1, 0x0602), s.x),
+                       decode2(__byte_perm(w2, w3, 0x0602), s.y),
+                       decode2(__byte_perm(w0, w1, 0x0703), s.x),
+                       decode2(__byte_perm(w2, w3, 0x0703), s.y));
       }
-      if (!__all_sync(0xffffffffu,
-                      mbar_wait(smem_u32(&c->empty[st]), ((it / kStages) & 1) ^ 1, c, status)))
-        break;
-#pragma unroll
-      for (int i = 0; i < kItems; ++i) {
-        const int tok = (id >> 2) + i * (kTeamWarps * 8), flip = (grp >> 1) ^ (tok & 1);
-        uint8_t* a = smem + st * kStageBytes + (grp >> 1) * (kBT * 128) + tok * 128;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int chunk = (grp & 1) * 4 + (h ^ flip) * 2;
-          *reinterpret_cast<uint4*>(a + ((chunk ^ (tok & 7)) << 4)) =
-              decode8(v[i][h].x, v[i][h].y, step[i]);
-          *reinterpret_cast<uint4*>(a + (((chunk + 1) ^ (tok & 7)) << 4)) =
-              decode8(v[i][h].z, v[i][h].w, step[i]);
-        }
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive_pair(in_cta0(smem_u32(&c->full[st])));
+        mbar_arrive_pair(full + st * 8);
         mbar_arrive(smem_u32(&c->raw_empty[rs]));
-        mbar_arrive(smem_u32(&c->exp_empty[bs]));
+        mbar_arrive(smem_u32(&c->exp_empty[slot / kBatch]));
       }
+      if ((st += kTeams) >= kStages) st -= kStages, st_phase ^= 1;
+      if ((rs += kTeams) >= kRaw) rs -= kRaw, rs_phase ^= 1;
+      if ((slot += kTeams) >= kBatch * kBatches) slot -= kBatch * kBatches, slot_phase ^= 1;
     }
   }
 
@@ -589,35 +635,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-// Joins the partial sums of the tiles that several clusters share: a block
-// takes four columns of a CTA's half tile, a thread one channel.
-constexpr int kJoinCols = 4;
+// Joins the partial sums of the tiles that several clusters share: a warp takes
+// one column of a CTA's half tile, a thread four channels.
 template <typename TO>
 __global__ void __launch_bounds__(128) wgrad_join_kernel(const __grid_constant__ Plan p,
                                                          const float* __restrict__ partial,
                                                          TO* dw) {
-  const int per_half = p.bn / kJoinCols;
-  const int tile = blockIdx.x / (2 * per_half);
-  const int rank = blockIdx.x / per_half % 2, c0 = blockIdx.x % per_half * kJoinCols;
+  const int per_half = p.bn / 4;
+  const int tile = blockIdx.x / (2 * per_half), rank = blockIdx.x / per_half % 2;
+  const int col = blockIdx.x % per_half * 4 + (int)(threadIdx.x >> 5), in = threadIdx.x % 32 * 4;
   const int64_t first = (int64_t)tile * p.steps, last = first + p.steps - 1;
   const int lo = (int)(first / p.quota), hi = (int)(last / p.quota);
   if (lo == hi) return;  // summed by one cluster, and written by it
   const int id = p.waves * p.clusters + tile;
-  const int n0 = id / p.tiles_m * p.bn + c0;
-  const int ch = id % p.tiles_m * kBM + rank * 128 + threadIdx.x;
-  if (ch >= p.channels) return;
-  float v[kJoinCols] = {};
-#pragma unroll 4
-  for (int cl = lo; cl <= hi; ++cl) {
-    const int slot = (int64_t)cl * p.quota / p.steps == tile ? 0 : 1;
-    const float* from = partial + ((size_t)(cl * 2 + slot) * 2 + rank) * kPartialFloats +
-                        (size_t)c0 * 128 + threadIdx.x;
-#pragma unroll
-    for (int j = 0; j < kJoinCols; ++j) v[j] += from[j * 128];
+  const int n = id / p.tiles_m * p.bn + col;
+  const int ch = id % p.tiles_m * kBM + rank * 128 + in;
+  if (n >= p.rows || ch >= p.channels) return;
+  // a cluster's first segment is in its slot 0, its second in slot 1
+  const int two = (int64_t)lo * p.quota / p.steps == tile ? 0 : 1;
+  const float4* from = reinterpret_cast<const float4*>(
+      partial + ((size_t)lo * 4 + rank) * kPartialFloats + (size_t)col * 128 + in);
+  const size_t next = kPartialFloats;  // float4s from one cluster's slot 0 to the next one's
+  float4 v = from[two ? kPartialFloats / 2 : 0];
+#pragma unroll 8
+  for (int i = 1; i <= hi - lo; ++i) {
+    const float4 u = from[i * next];
+    v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
   }
+  const float r[4] = {v.x, v.y, v.z, v.w};
+  TO* to = dw + (int64_t)n * p.dws + ch;
 #pragma unroll
-  for (int j = 0; j < kJoinCols; ++j)
-    if (n0 + j < p.rows) put_dw<TO>(dw + (int64_t)(n0 + j) * p.dws + ch, v[j], p.accumulate);
+  for (int j = 0; j < 4; ++j)
+    if (ch + j < p.channels) put_dw<TO>(to + j, r[j], p.accumulate);
 }
 
 // dy [tokens][rows] as `terms` bf16 matrices [padded tokens][ld], the next
@@ -802,7 +851,7 @@ extern "C" gs_status gs_act8_wgrad(int64_t tokens, int32_t rows, int32_t channel
   const cuuint64_t qstrides[1] = {(cuuint64_t)q_stride};
   const cuuint32_t qbox[2] = {128, kBT};
   if (encode(&qmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(q), qdims, qstrides, qbox,
-             unit, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+             unit, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return GS_ERR_CUDA;
 
@@ -827,7 +876,7 @@ extern "C" gs_status gs_act8_wgrad(int64_t tokens, int32_t rows, int32_t channel
         p, map, qmap, e, e_stride, (__nv_bfloat16*)dw, partial, status);
   GS_CHECK_LAUNCH();
   if (p.rem_tiles && p.quota % p.steps != 0) {
-    const unsigned blocks = (unsigned)(p.rem_tiles * 2 * (p.bn / kJoinCols));
+    const unsigned blocks = (unsigned)(p.rem_tiles * 2 * (p.bn / 4));
     if (out_dtype == GS_F32)
       wgrad_join_kernel<float><<<blocks, 128, 0, st>>>(p, partial, (float*)dw);
     else
