@@ -18,6 +18,9 @@
 namespace gs {
 namespace {
 
+#ifndef FE
+#define FE 4096
+#endif
 constexpr int kNormCtas = 304;      // most row ranges of the backward (column sums)
 constexpr int kMaxTeamWarps = 16;
 constexpr int kTeamThreads = 512;   // most threads of a CTA
@@ -56,16 +59,26 @@ struct Team {
     ++turn;
     if ((threadIdx.x & 31) == 0) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) r[warp * N + i] = v[i];
+      for (int i = 0; i < N; ++i) r[i * kMaxTeamWarps + warp] = v[i];
     }
     sync();
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = 0.f;
-    for (int w = 0; w < warps; ++w)
+    for (int w = 0; w < warps; w += 4)  // places of warps that are not there hold zeros
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] += r[w * N + i];
+      for (int i = 0; i < N; ++i) {
+        const float4 u = *reinterpret_cast<const float4*>(r + i * kMaxTeamWarps + w);
+        v[i] += (u.x + u.y) + (u.z + u.w);
+      }
   }
 };
+
+// Zeros in the sums' places and in the slots, before any copy is asked for.
+__device__ __forceinline__ void clear_shared(char* smem, int bytes) {
+  for (int i = threadIdx.x * 16; i < bytes; i += blockDim.x * 16)
+    *reinterpret_cast<uint4*>(smem + i) = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+}
 
 __device__ __forceinline__ int find_group(const int32_t* offsets, int groups, int64_t t) {
   if (!offsets) return 0;
@@ -131,21 +144,27 @@ struct Rows {
       }
     }
   }
+  // Channels from C on and tensors that are not there read as the zeros that the
+  // slots began with.  Where a team has one row only, the second slot holds an
+  // earlier row (`live` false): finite or not, it stays in that row's sums.
   __device__ __forceinline__ void read(float (&v)[VEC * NV], const char* slot, bool live, int64_t t,
                                        int first, int step, int C, int team) const {
-    const T* own = reinterpret_cast<const T*>(
+    if (kOwn) {
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        const Pack<T, kEl> w = load_pack<T, kEl>(reinterpret_cast<const T*>(
+            slot + (i * (int)blockDim.x + (int)threadIdx.x) * kChunk));
+#pragma unroll
+        for (int j = 0; j < kEl; ++j) v[i * kEl + j] = to_f32(w.v[j]);
+      }
+      return;
+    }
+    const T* row = reinterpret_cast<const T*>(
         slot + team * row_bytes(C) + ((uintptr_t)(base + t * stride) & 15));
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-      const int c = first + i / kPer * step + i % kPer * kEl;
-      Pack<T, kEl> w;
-      const bool in = live && base && c < C;
-      if (in)
-        w = kOwn ? load_pack<T, kEl>(reinterpret_cast<const T*>(
-                       slot + (i * (int)blockDim.x + (int)threadIdx.x) * kChunk))
-                 : load_pack<T, kEl>(own + c);
-#pragma unroll
-      for (int j = 0; j < kEl; ++j) v[i * kEl + j] = in ? to_f32(w.v[j]) : 0.f;
+    for (int i = 0; i < NV; ++i) {
+      const int c = first + i * step;
+      v[i] = live && base && c < C ? to_f32(row[c]) : 0.f;
     }
   }
 };
@@ -236,7 +255,7 @@ template <typename TB, int VEC, int NV>
 __device__ __forceinline__ void group_weights(float (&wk)[VEC * NV], const NormK& k, int g,
                                               int first, int step) {
 #pragma unroll
-  for (int i = 0; i < VEC * NV; ++i) wk[i] = 1.f;
+  for (int i = 0; i < VEC * NV; ++i) wk[i] = first + i / VEC * step < k.C ? 1.f : 0.f;
   scale_row<float, VEC, NV>(wk, k.scale, first, step, k.C);
   if (k.post) scale_row<float, VEC, NV>(wk, k.w_post, first, step, k.C);
   if (k.gate) scale_row<TB, VEC, NV>(wk, (const TB*)k.gate + (int64_t)g * k.C, first, step, k.C);
@@ -284,6 +303,7 @@ __global__ void __launch_bounds__(kTeamThreads, 1) norm_fwd_kernel(
     copies_commit();
     next += teams;
   };
+  clear_shared(smem, depth * slot_bytes + teams * kRedFloats * (int)sizeof(float));
   for (int i = 0; i < depth; ++i) ask(i);
 
   float wp[E], wk[E];
@@ -415,6 +435,7 @@ __global__ void __launch_bounds__(kTeamThreads, 1) norm_bwd_kernel(
     copies_commit();
     next += teams;
   };
+  clear_shared(smem, depth * slot_bytes + teams * kRedFloats * (int)sizeof(float));
   for (int i = 0; i < depth; ++i) ask(i);
   float4 st[kRows], st_next[kRows];
   auto ask_stats = [&](int64_t t) {
@@ -526,18 +547,13 @@ __global__ void __launch_bounds__(kTeamThreads, 1) norm_bwd_kernel(
                   tm);
           float a = 0.f, b = 0.f;
 #pragma unroll
-          for (int i = 0; i < NV; ++i)
-            if (first + i * step < k.C) {
-#pragma unroll
-              for (int j = 0; j < VEC; ++j) {
-                const int c = i * VEC + j;
-                if (k.post) m[r][c] = (m[r][c] - st[r].x) * st[r].y;
-                if (live) acc_e[c] += d[r][c] * m[r][c];
-                d[r][c] *= wk[c];
-                a += d[r][c] * m[r][c];
-                b += d[r][c];
-              }
-            }
+          for (int c = 0; c < E; ++c) {  // wk is 0 from C on
+            if (k.post) m[r][c] = (m[r][c] - st[r].x) * st[r].y;
+            if (live) acc_e[c] += d[r][c] * m[r][c];
+            d[r][c] *= wk[c];
+            a += d[r][c] * m[r][c];
+            b += d[r][c];
+          }
           part[r] = a;
           part[kRows + r] = b;
         }
@@ -766,7 +782,7 @@ cudaError_t fwd_launch(const FwdArgs& a, cudaStream_t st) {
 
 template <typename TB, typename TX, int VEC>
 cudaError_t fwd_pick(const FwdArgs& a, cudaStream_t st) {
-  if (a.k.C <= 4096) return fwd_launch<TB, TX, VEC, 8 / VEC>(a, st);
+  if (a.k.C <= FE) return fwd_launch<TB, TX, VEC, 8 / VEC>(a, st);
   return fwd_launch<TB, TX, VEC, 16 / VEC>(a, st);
 }
 
