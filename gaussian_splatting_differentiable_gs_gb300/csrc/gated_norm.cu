@@ -18,12 +18,10 @@
 namespace gs {
 namespace {
 
-#ifndef FE
-#define FE 4096
-#endif
 constexpr int kNormCtas = 304;      // most row ranges of the backward (column sums)
 constexpr int kMaxTeamWarps = 16;
 constexpr int kTeamThreads = 512;   // most threads of a CTA
+constexpr int kWideThreads = 384;   // of the backward with 16 channels a thread: 168 registers
 constexpr int kSmemBudget = 224 * 1024;
 
 struct NormK {
@@ -73,16 +71,23 @@ struct Team {
   }
 };
 
-// Zeros in the sums' places and in the slots, before any copy is asked for.
-__device__ __forceinline__ void clear_shared(char* smem, int bytes) {
-  for (int i = threadIdx.x * 16; i < bytes; i += blockDim.x * 16)
+// Zeros in the sums' places, and in the slots where some of a slot is never
+// copied to, before any copy is asked for.
+__device__ __forceinline__ void clear_shared(char* smem, int slots, int bytes, bool filled) {
+  for (int i = (filled ? slots : 0) + threadIdx.x * 16; i < bytes; i += blockDim.x * 16)
     *reinterpret_cast<uint4*>(smem + i) = make_uint4(0, 0, 0, 0);
   __syncthreads();
 }
 
+// The last group that starts at or before row t.  Whole warps call it.
 __device__ __forceinline__ int find_group(const int32_t* offsets, int groups, int64_t t) {
   if (!offsets) return 0;
-  int lo = 0, hi = groups - 1;  // the last group that starts at or before t
+  if (groups <= 32) {
+    const int lane = threadIdx.x & 31;
+    const unsigned below = __ballot_sync(0xffffffffu, lane < groups && offsets[lane] <= t);
+    return below ? 31 - __clz(below) : 0;
+  }
+  int lo = 0, hi = groups - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (offsets[mid] <= t) lo = mid; else hi = mid - 1;
@@ -199,22 +204,6 @@ __device__ __forceinline__ void store_row(const float (&v)[VEC * NV], T* p, int 
   }
 }
 
-// v *= p[channel] (fp32 weights; NULL: ones)
-template <typename T, int VEC, int NV>
-__device__ __forceinline__ void scale_row(float (&v)[VEC * NV], const T* p, int first, int step,
-                                          int C) {
-  if (!p) return;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = first + i * step;
-    if (c < C) {
-      const Pack<T, VEC> w = load_pack<T, VEC>(p + c);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) v[i * VEC + j] *= to_f32(w.v[j]);
-    }
-  }
-}
-
 // Means and 1/deviations of a team's rows; v becomes the centred rows.
 template <int VEC, int NV, int kRows>
 __device__ __forceinline__ void row_stats(float (&v)[kRows][VEC * NV], Team& team, const NormK& k,
@@ -250,20 +239,47 @@ __device__ __forceinline__ void row_stats(float (&v)[kRows][VEC * NV], Team& tea
   for (int r = 0; r < kRows; ++r) rstd[r] = rsqrtf(rstd[r] * k.inv_c + k.eps);
 }
 
-// k = res_scale * gate * w_post of a group, per channel
-template <typename TB, int VEC, int NV>
-__device__ __forceinline__ void group_weights(float (&wk)[VEC * NV], const NormK& k, int g,
-                                              int first, int step) {
+// Per-channel weights in shared memory, in the order in which a team's threads
+// read them (16 bytes a thread at a time; every team reads the same): place
+// of value j of a thread's vector i.  Channels from C on have weight 0.
+template <int VEC, int NV>
+struct Weights {
+  static constexpr int kEl = VEC >= 4 ? 4 : 1;
+  __host__ __device__ static int count(int warps) { return VEC * NV * warps * 32; }
+  __device__ __forceinline__ static int place(int i, int j, int lane, int lanes) {
+    return ((i * (VEC / kEl) + j / kEl) * lanes + lane) * kEl + j % kEl;
+  }
+  // f(channel) for every channel, by the whole CTA
+  template <typename F>
+  __device__ __forceinline__ static void fill(float* w, int C, int lanes, F f) {
+    for (int c = threadIdx.x; c < VEC * NV * lanes; c += blockDim.x)
+      w[place(c / VEC / lanes, c % VEC, c / VEC % lanes, lanes)] = c < C ? f(c) : 0.f;
+  }
+  __device__ __forceinline__ static void get(float (&v)[VEC], const float* w, int i, int lane,
+                                             int lanes) {
 #pragma unroll
-  for (int i = 0; i < VEC * NV; ++i) wk[i] = first + i / VEC * step < k.C ? 1.f : 0.f;
-  scale_row<float, VEC, NV>(wk, k.scale, first, step, k.C);
-  if (k.post) scale_row<float, VEC, NV>(wk, k.w_post, first, step, k.C);
-  if (k.gate) scale_row<TB, VEC, NV>(wk, (const TB*)k.gate + (int64_t)g * k.C, first, step, k.C);
+    for (int j = 0; j < VEC; j += kEl) {
+      const Pack<float, kEl> p = load_pack<float, kEl>(w + place(i, j, lane, lanes));
+#pragma unroll
+      for (int e = 0; e < kEl; ++e) v[j + e] = p.v[e];
+    }
+  }
+};
+
+// k = res_scale * gate * w_post of a group's channel c
+template <typename TB>
+__device__ __forceinline__ float group_weight(const NormK& k, int g, int c) {
+  float w = k.scale ? k.scale[c] : 1.f;
+  if (k.post && k.w_post) w *= k.w_post[c];
+  if (k.gate) w *= to_f32(((const TB*)k.gate)[(int64_t)g * k.C + c]);
+  return w;
 }
 
 // Work of a CTA: rows [cta R, cta R + R), cut at the groups' ends; its teams
-// take them in turn, kRows at a time, and keep the weights of their channels (and
-// the backward its column sums) in registers.
+// take them in turn, kRows at a time; the backward keeps its column sums in
+// registers.  A thread has up to 32 (backward: 16) channels of a row, so that what
+// a row costs by itself (sums over the team, addresses) is spread over many: with
+// 8 the forward took 283 instructions per 8 x 32 channels and was bound by them.
 struct Range {
   int64_t begin, end;
 };
@@ -286,9 +302,11 @@ __global__ void __launch_bounds__(kTeamThreads, 1) norm_fwd_kernel(
   const int tm = warp / warps, teams = (blockDim.x >> 5) / warps;
   const int xb = RX::slot(blockDim.x, teams, k.C), bb = RB::slot(blockDim.x, teams, k.C);
   const int slot_bytes = xb + bb;
-  Team team{reinterpret_cast<float*>(smem + depth * slot_bytes) + tm * kRedFloats, warps,
-            warp - tm * warps, tm + 1, 0};
-  const int lane = threadIdx.x - tm * warps * 32;
+  float* red = reinterpret_cast<float*>(smem + depth * slot_bytes);
+  float* w_pre = red + teams * kRedFloats;
+  float* w_k = w_pre + Weights<VEC, NV>::count(warps);
+  Team team{red + tm * kRedFloats, warps, warp - tm * warps, tm + 1, 0};
+  const int lanes = warps * 32, lane = threadIdx.x - tm * lanes;
   const int first = lane * VEC, step = warps * 32 * VEC;
 
   const Range rows = cta_rows(k, rows_per_cta);
@@ -303,20 +321,24 @@ __global__ void __launch_bounds__(kTeamThreads, 1) norm_fwd_kernel(
     copies_commit();
     next += teams;
   };
-  clear_shared(smem, depth * slot_bytes + teams * kRedFloats * (int)sizeof(float));
+  clear_shared(smem, depth * slot_bytes, depth * slot_bytes + teams * kRedFloats * (int)sizeof(float),
+               !RX::kOwn || (block && k.C == VEC * NV * lanes));
   for (int i = 0; i < depth; ++i) ask(i);
 
-  float wp[E], wk[E];
-#pragma unroll
-  for (int i = 0; i < E; ++i) wp[i] = 1.f;
-  scale_row<float, VEC, NV>(wp, k.w_pre, first, step, k.C);
+  Weights<VEC, NV>::fill(w_pre, k.C, lanes,
+                         [&](int c) { return k.w_pre ? k.w_pre[c] : 1.f; });
 
   int g = find_group(k.offsets, k.groups, rows.begin), s = 0;
   int64_t t = rows.begin + tm;
   for (int64_t at = rows.begin; at < rows.end;) {
     const int64_t stop =
         k.offsets && g + 1 < k.groups ? min(rows.end, max(at, (int64_t)k.offsets[g + 1])) : rows.end;
-    if (block && t < stop) group_weights<TB, VEC, NV>(wk, k, g, first, step);
+    if (stop > at) {  // the same for the whole CTA
+      if (at > rows.begin) __syncthreads();
+      Weights<VEC, NV>::fill(w_k, k.C, lanes,
+                             [&](int c) { return group_weight<TB>(k, g, c); });
+      __syncthreads();
+    }
     while (t < stop) {
       const bool two = kRows == 2 && t + teams < stop;
       const int s1 = s + 1 == depth ? 0 : s + 1;
@@ -340,9 +362,16 @@ __global__ void __launch_bounds__(kTeamThreads, 1) norm_fwd_kernel(
             for (int i = 0; i < E; ++i) u[r][i] *= r0[r];
         }
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
+        for (int i = 0; i < NV; ++i) {
+          float w[VEC];
+          Weights<VEC, NV>::get(w, w_k, i, lane, lanes);
 #pragma unroll
-          for (int i = 0; i < E; ++i) v[r][i] += wk[i] * u[r][i];
+          for (int j = 0; j < VEC; ++j)
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) v[r][i * VEC + j] += w[j] * u[r][i * VEC + j];
+        }
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
           if (!r || two)
             store_row<TX, VEC, NV>(v[r], x_out + (t + r * teams) * x_out_stride, first, step, k.C);
         }
@@ -353,10 +382,17 @@ __global__ void __launch_bounds__(kTeamThreads, 1) norm_fwd_kernel(
       if (y) {
         row_stats<VEC, NV, kRows>(v, team, k, first, step, m1, r1);
 #pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          float w[VEC];
+          Weights<VEC, NV>::get(w, w_pre, i, lane, lanes);
+#pragma unroll
+          for (int j = 0; j < VEC; ++j)
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) v[r][i * VEC + j] *= r1[r] * w[j];
+        }
+#pragma unroll
         for (int r = 0; r < kRows; ++r) {
           const int64_t row = t + r * teams;
-#pragma unroll
-          for (int i = 0; i < E; ++i) v[r][i] *= r1[r] * wp[i];
           if (!r || two) store_row<TB, VEC, NV>(v[r], y + row * y_stride, first, step, k.C);
           if (y_q && (!r || two)) {
             // the checkpoint of y as stored; a group is 32 / VEC lanes of a warp
@@ -400,8 +436,8 @@ __global__ void __launch_bounds__(kTeamThreads, 1) norm_fwd_kernel(
 
 // The sums of a (CTA, group) pair go to slot cta + group of part_e: along the
 // rows either the CTA or the group advances, so no two pairs share a slot.
-template <typename TB, typename TX, int VEC, int NV, int kRows>
-__global__ void __launch_bounds__(kTeamThreads, 1) norm_bwd_kernel(
+template <typename TB, typename TX, int VEC, int NV, int kRows, int kMost>
+__global__ void __launch_bounds__(kMost, 1) norm_bwd_kernel(
     const __grid_constant__ NormK k, const TX* x, int64_t x_stride, const TB* block,
     int64_t block_stride, const float4* stats, const TX* dx_out, int64_t dx_out_stride,
     const TB* dy, int64_t dy_stride, TX* dx, int64_t dx_stride, TB* dblock, int64_t dblock_stride,
@@ -415,11 +451,14 @@ __global__ void __launch_bounds__(kTeamThreads, 1) norm_bwd_kernel(
   const int xb = RX::slot(blockDim.x, teams, k.C), bb = RB::slot(blockDim.x, teams, k.C);
   const int slot_bytes = 2 * (xb + bb);
   float* red = reinterpret_cast<float*>(smem + depth * slot_bytes);
-  float* join = red + teams * kRedFloats;  // [teams][C] column sums of several teams
+  float* w_pre = red + teams * kRedFloats;
+  float* w_k = w_pre + Weights<VEC, NV>::count(warps);
+  float* join = w_k + Weights<VEC, NV>::count(warps);  // [teams][C] column sums of several teams
   Team team{red + tm * kRedFloats, warps, warp - tm * warps, tm + 1, 0};
-  const int lane = threadIdx.x - tm * warps * 32;
+  const int lanes = warps * 32, lane = threadIdx.x - tm * lanes;
   const int first = lane * VEC, step = warps * 32 * VEC;
 
+  asm volatile("griddepcontrol.launch_dependents;");  // the sums' kernel waits for this one's end
   const Range rows = cta_rows(k, rows_per_cta);
   const RX rx{dy ? x : nullptr, x_stride}, rd{dx_out, dx_out_stride};
   const RB rb{block, block_stride}, ry{dy, dy_stride};
@@ -435,7 +474,8 @@ __global__ void __launch_bounds__(kTeamThreads, 1) norm_bwd_kernel(
     copies_commit();
     next += teams;
   };
-  clear_shared(smem, depth * slot_bytes + teams * kRedFloats * (int)sizeof(float));
+  clear_shared(smem, depth * slot_bytes, depth * slot_bytes + teams * kRedFloats * (int)sizeof(float),
+               !RX::kOwn || (block && dy && dx_out && k.C == VEC * NV * lanes));
   for (int i = 0; i < depth; ++i) ask(i);
   float4 st[kRows], st_next[kRows];
   auto ask_stats = [&](int64_t t) {
@@ -445,13 +485,11 @@ __global__ void __launch_bounds__(kTeamThreads, 1) norm_bwd_kernel(
   };
   ask_stats(rows.begin + tm);
 
-  float acc_pre[E], acc_e[E], wp[E];
+  float acc_pre[E], acc_e[E];
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    acc_pre[i] = acc_e[i] = 0.f;
-    wp[i] = 1.f;
-  }
-  scale_row<float, VEC, NV>(wp, k.w_pre, first, step, k.C);
+  for (int i = 0; i < E; ++i) acc_pre[i] = acc_e[i] = 0.f;
+  Weights<VEC, NV>::fill(w_pre, k.C, lanes,
+                         [&](int c) { return k.w_pre ? k.w_pre[c] : 1.f; });
 
   auto flush = [&](const float (&acc)[E], float* to) {
     if (teams == 1) {
@@ -483,8 +521,12 @@ __global__ void __launch_bounds__(kTeamThreads, 1) norm_bwd_kernel(
   for (int64_t at = rows.begin; at < rows.end;) {
     const int64_t stop =
         k.offsets && g + 1 < k.groups ? min(rows.end, max(at, (int64_t)k.offsets[g + 1])) : rows.end;
-    float wk[E];
-    if (t < stop) group_weights<TB, VEC, NV>(wk, k, g, first, step);
+    if (stop > at) {  // the same for the whole CTA
+      if (at > rows.begin) __syncthreads();
+      Weights<VEC, NV>::fill(w_k, k.C, lanes,
+                             [&](int c) { return group_weight<TB>(k, g, c); });
+      __syncthreads();
+    }
     while (t < stop) {
       const bool two = kRows == 2 && t + teams < stop;
       const int s1 = s + 1 == depth ? 0 : s + 1;
@@ -505,12 +547,18 @@ __global__ void __launch_bounds__(kTeamThreads, 1) norm_bwd_kernel(
             ry.read(h[r], slot + 2 * xb + bb, live, t + r * teams, first, step, k.C, tm);
             float a = 0.f, b = 0.f;
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-              n[r][i] = (n[r][i] - st[r].z) * st[r].w;
-              if (live) acc_pre[i] += h[r][i] * n[r][i];
-              h[r][i] *= wp[i];
-              a += h[r][i] * n[r][i];
-              b += h[r][i];
+            for (int v = 0; v < NV; ++v) {
+              float w[VEC];
+              Weights<VEC, NV>::get(w, w_pre, v, lane, lanes);
+#pragma unroll
+              for (int j = 0; j < VEC; ++j) {
+                const int i = v * VEC + j;
+                n[r][i] = (n[r][i] - st[r].z) * st[r].w;
+                if (live) acc_pre[i] += h[r][i] * n[r][i];
+                h[r][i] *= w[j];
+                a += h[r][i] * n[r][i];
+                b += h[r][i];
+              }
             }
             part[r] = a;
             part[kRows + r] = b;
@@ -547,12 +595,18 @@ __global__ void __launch_bounds__(kTeamThreads, 1) norm_bwd_kernel(
                   tm);
           float a = 0.f, b = 0.f;
 #pragma unroll
-          for (int c = 0; c < E; ++c) {  // wk is 0 from C on
-            if (k.post) m[r][c] = (m[r][c] - st[r].x) * st[r].y;
-            if (live) acc_e[c] += d[r][c] * m[r][c];
-            d[r][c] *= wk[c];
-            a += d[r][c] * m[r][c];
-            b += d[r][c];
+          for (int v = 0; v < NV; ++v) {
+            float w[VEC];  // 0 from C on
+            Weights<VEC, NV>::get(w, w_k, v, lane, lanes);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+              const int c = v * VEC + j;
+              if (k.post) m[r][c] = (m[r][c] - st[r].x) * st[r].y;
+              if (live) acc_e[c] += d[r][c] * m[r][c];
+              d[r][c] *= w[j];
+              a += d[r][c] * m[r][c];
+              b += d[r][c];
+            }
           }
           part[r] = a;
           part[kRows + r] = b;
@@ -607,6 +661,7 @@ __global__ void __launch_bounds__(1024) norm_sums_kernel(const __grid_constant__
                                                          float* dgate, float* dscale) {
   __shared__ float red[32][33], red2[32][33];
   const int x = threadIdx.x, y = threadIdx.y;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the row kernel still runs
   const int c = blockIdx.x * 32 + x;
   const bool in = c < k.C;
   auto slots = [&](const float* p, int lo, int hi, int from, int by) {
@@ -616,12 +671,25 @@ __global__ void __launch_bounds__(1024) norm_sums_kernel(const __grid_constant__
       for (int i = lo + from; i < hi; i += by) s += p[(int64_t)i * k.C + c];
     return s;
   };
-  red2[y][x] = dw_pre ? slots(part_pre, 0, ctas, y, 32) : 0.f;
+  auto join = [&](float (*m)[33], float* to) {
+    __syncthreads();
+    if (y == 0 && in && to) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) s += m[i][x];
+      to[c] = s;
+    }
+  };
+  if (blockIdx.y == 0) {  // dw_pre's blocks
+    if (!dw_pre) return;
+    red[y][x] = slots(part_pre, 0, ctas, y, 32);
+    join(red, dw_pre);
+    return;
+  }
   const float w = in && k.w_post ? k.w_post[c] : 1.f;
   const float sc = in && k.scale ? k.scale[c] : 1.f;
-  const bool sums = dw_post || dgate || dscale;
   float post = 0.f, scale = 0.f;
-  for (int g0 = 0; g0 < (sums ? k.groups : 0); g0 += 32) {
+  for (int g0 = 0; g0 < k.groups; g0 += 32) {
     const int n = min(32, k.groups - g0), per = 32 / n;
     const int g = g0 + y / per;
     float e = 0.f;
@@ -650,15 +718,6 @@ __global__ void __launch_bounds__(1024) norm_sums_kernel(const __grid_constant__
       if (in && dgate) dgate[(int64_t)(g0 + y) * k.C + c] = sc * w * e;
     }
   }
-  auto join = [&](float (*m)[33], float* to) {
-    __syncthreads();
-    if (y == 0 && in && to) {
-      float s = 0.f;
-      for (int i = 0; i < 32; ++i) s += m[i][x];
-      to[c] = s;
-    }
-  };
-  join(red2, dw_pre);
   __syncthreads();
   red[y][x] = post;
   red2[y][x] = scale;
@@ -712,18 +771,17 @@ struct FwdArgs {
   int64_t es;
 };
 
-// Rows are 8 channels a thread (16 from 4096 channels on), so a row of 1024 is
-// four warps; a CTA holds as many such teams as 512 threads and 15 named
-// barriers allow.
+// A team: the warps that a row of VEC * NV channels a thread needs; a CTA: as many
+// teams as its threads allow (16 of one warp; several warps need a named barrier).
 struct Shape {
   int warps, teams, threads;
 };
 template <int VEC, int NV>
-Shape norm_shape(const NormK& k) {
+Shape norm_shape(const NormK& k, int threads) {
   Shape s;
   s.warps = (int)div_up(k.C, 32 * VEC * NV);
-  s.teams = kTeamThreads / 32 / s.warps;
-  if (s.teams > 8) s.teams = 8;
+  s.teams = threads / 32 / s.warps;
+  if (s.teams < 1) s.teams = 1;
   s.threads = s.teams * s.warps * 32;
   return s;
 }
@@ -751,38 +809,54 @@ cudaError_t allow_smem(F kernel, std::atomic<uint64_t>& known) {
   return e;
 }
 
-// Rows of a team in shared memory: as many as fit, up to kMaxDepth (5 rows of 1024
-// bf16 channels, four tensors, four teams: 160 KB), at least the ones worked on.
-int ring_depth(int slot_bytes, size_t fixed, int rows, size_t* smem) {
-  int depth = kMaxDepth;
-  while (depth > rows && depth * (size_t)slot_bytes + fixed > kSmemBudget) --depth;
-  *smem = depth * (size_t)slot_bytes + fixed;
-  return depth;
+// Threads of a CTA and rows of a team in shared memory: 512 threads where that
+// leaves a row ahead for each team (or more, up to kMaxDepth), else fewer, as fp32 rows do.
+struct Layout {
+  Shape s;
+  int depth;
+  size_t smem;
+};
+template <typename TB, typename TX, int VEC, int NV>
+Layout norm_layout(const NormK& k, int tensors, int rows, bool join, int most) {
+  Layout l;
+  for (int threads = most;; threads /= 2) {
+    l.s = norm_shape<VEC, NV>(k, threads);
+    const size_t slot = (size_t)tensors * (Rows<TX, VEC, NV>::slot(l.s.threads, l.s.teams, k.C) +
+                                           Rows<TB, VEC, NV>::slot(l.s.threads, l.s.teams, k.C));
+    const size_t fixed =
+        sizeof(float) * ((size_t)l.s.teams * kRedFloats + 2 * Weights<VEC, NV>::count(l.s.warps) +
+                         (join && l.s.teams > 1 ? (size_t)l.s.teams * k.C : 0));
+    l.depth = kMaxDepth;
+    while (l.depth > 1 && l.depth * slot + fixed > (size_t)kSmemBudget) --l.depth;
+    l.smem = l.depth * slot + fixed;
+    if (l.depth >= rows + 1 || l.s.teams == 1) return l;
+  }
 }
 
 template <typename TB, typename TX, int VEC, int NV>
 cudaError_t fwd_launch(const FwdArgs& a, cudaStream_t st) {
-  constexpr int kRows = VEC * NV <= 8 ? 2 : 1;
-  const Shape s = norm_shape<VEC, NV>(a.k);
-  size_t smem = 0;
-  const int depth = ring_depth(Rows<TX, VEC, NV>::slot(s.threads, s.teams, a.k.C) +
-                                   Rows<TB, VEC, NV>::slot(s.threads, s.teams, a.k.C),
-                               sizeof(float) * s.teams * kRedFloats, kRows, &smem);
+  constexpr int kRows = 1;
+  const Layout l = norm_layout<TB, TX, VEC, NV>(a.k, 1, kRows, false, kTeamThreads);
   static std::atomic<uint64_t> known{0};
   const auto kernel = norm_fwd_kernel<TB, TX, VEC, NV, kRows>;
   const cudaError_t e = allow_smem(kernel, known);
   if (e != cudaSuccess) return e;
   int64_t rows = 0;
-  const int64_t ctas = norm_ranges(a.k.tokens, s.teams, 1, &rows);
-  kernel<<<(unsigned)ctas, s.threads, smem, st>>>(
+  const int64_t ctas = norm_ranges(a.k.tokens, l.s.teams, 1, &rows);
+  kernel<<<(unsigned)ctas, l.s.threads, l.smem, st>>>(
       a.k, (const TX*)a.x, a.xs, (const TB*)a.block, a.bs, (TX*)a.x_out, a.xos, (TB*)a.y, a.ys,
-      a.stats, a.y_q, a.qs, a.y_e, a.es, rows, s.warps, depth);
+      a.stats, a.y_q, a.qs, a.y_e, a.es, rows, l.s.warps, l.depth);
   return cudaSuccess;
 }
 
 template <typename TB, typename TX, int VEC>
 cudaError_t fwd_pick(const FwdArgs& a, cudaStream_t st) {
-  if (a.k.C <= FE) return fwd_launch<TB, TX, VEC, 8 / VEC>(a, st);
+  if constexpr (VEC > 1) {
+    if (a.k.C <= 256) return fwd_launch<TB, TX, VEC, 8 / VEC>(a, st);
+    if (a.k.C <= 512) return fwd_launch<TB, TX, VEC, 16 / VEC>(a, st);
+    return fwd_launch<TB, TX, VEC, 32 / VEC>(a, st);
+  }
+  if (a.k.C <= 4096) return fwd_launch<TB, TX, VEC, 8 / VEC>(a, st);  // more would not fit the registers
   return fwd_launch<TB, TX, VEC, 16 / VEC>(a, st);
 }
 
@@ -805,32 +879,30 @@ struct BwdArgs {
   int ctas;
 };
 
-template <typename TB, typename TX, int VEC, int NV>
+template <typename TB, typename TX, int VEC, int NV, int kMost>
 cudaError_t bwd_launch(BwdArgs& a, cudaStream_t st) {
-  constexpr int kRows = 1;  // two would not fit the registers
-  const Shape s = norm_shape<VEC, NV>(a.k);
-  size_t smem = 0;
-  const int depth =
-      ring_depth(2 * (Rows<TX, VEC, NV>::slot(s.threads, s.teams, a.k.C) +
-                      Rows<TB, VEC, NV>::slot(s.threads, s.teams, a.k.C)),
-                 sizeof(float) * s.teams * (kRedFloats + (s.teams > 1 ? (size_t)a.k.C : 0)), kRows,
-                 &smem);
+  constexpr int kRows = 1;
+  const Layout l = norm_layout<TB, TX, VEC, NV>(a.k, 2, kRows, true, kMost);
   static std::atomic<uint64_t> known{0};
-  const auto kernel = norm_bwd_kernel<TB, TX, VEC, NV, kRows>;
+  const auto kernel = norm_bwd_kernel<TB, TX, VEC, NV, kRows, kMost>;
   const cudaError_t e = allow_smem(kernel, known);
   if (e != cudaSuccess) return e;
-  a.ctas = (int)norm_ranges(a.k.tokens, s.teams, 1, &a.rows_per_cta);
-  kernel<<<(unsigned)a.ctas, s.threads, smem, st>>>(
+  a.ctas = (int)norm_ranges(a.k.tokens, l.s.teams, 1, &a.rows_per_cta);
+  kernel<<<(unsigned)a.ctas, l.s.threads, l.smem, st>>>(
       a.k, (const TX*)a.x, a.xs, (const TB*)a.block, a.bs, a.stats, (const TX*)a.dx_out, a.dxos,
       (const TB*)a.dy, a.dys, (TX*)a.dx, a.dxs, (TB*)a.dblock, a.dbs, a.part_pre, a.part_e,
-      a.rows_per_cta, s.warps, depth);
+      a.rows_per_cta, l.s.warps, l.depth);
   return cudaSuccess;
 }
 
+// 16 channels a thread in 384 threads where a row is that wide and aligned
+// (32640 x 1024 bf16: 96 us; 8 in 512 threads 107, 16 in 512, which spill, 119,
+// and in 256 119).
 template <typename TB, typename TX, int VEC>
 cudaError_t bwd_pick(BwdArgs& a, cudaStream_t st) {
-  if (a.k.C <= 4096) return bwd_launch<TB, TX, VEC, 8 / VEC>(a, st);
-  return bwd_launch<TB, TX, VEC, 16 / VEC>(a, st);
+  if (a.k.C > 32 * 16 * (kWideThreads / 32)) return bwd_launch<TB, TX, VEC, 16 / VEC, kTeamThreads>(a, st);
+  if (a.k.C > (VEC > 1 ? 256 : 4096)) return bwd_launch<TB, TX, VEC, 16 / VEC, kWideThreads>(a, st);
+  return bwd_launch<TB, TX, VEC, 8 / VEC, kTeamThreads>(a, st);
 }
 
 template <typename TB, typename TX>
@@ -920,9 +992,18 @@ extern "C" gs_status gs_gated_norm_bwd(
     a.part_pre = a.part_e = nullptr;
   }
   if (dw_pre || need_e) {
-    norm_sums_kernel<<<(unsigned)div_up(p->channels, 32), dim3(32, 32), 0, st>>>(
-        a.k, p->dtype, a.part_pre, a.part_e, a.rows_per_cta, a.ctas, dw_pre, dw_post, dgate,
-        dres_scale);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)div_up(p->channels, 32), need_e ? 2 : 1);
+    cfg.blockDim = dim3(32, 32);
+    cfg.stream = st;
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    GS_CUDA(cudaLaunchKernelEx(&cfg, norm_sums_kernel, a.k, p->dtype, (const float*)a.part_pre,
+                               (const float*)a.part_e, a.rows_per_cta, a.ctas, dw_pre, dw_post, dgate,
+                               dres_scale));
     GS_CHECK_LAUNCH();
   }
   return GS_OK;
