@@ -37,7 +37,7 @@ struct NormK {
 // Sums of N values per thread over a team of `warps` warps, the same bits in
 // every thread.  red: two slots of kRedFloats / 2 floats per team, used in turn:
 // a slot is written again only after the barrier of the sum in between.
-constexpr int kRedFloats = 2 * 4 * kMaxTeamWarps;
+constexpr int kRedFloats = 2 * 2 * kMaxTeamWarps;
 struct Team {
   float* red;
   int warps, warp, bar;
@@ -150,10 +150,9 @@ struct Rows {
     }
   }
   // Channels from C on and tensors that are not there read as the zeros that the
-  // slots began with.  Where a team has one row only, the second slot holds an
-  // earlier row (`live` false): finite or not, it stays in that row's sums.
-  __device__ __forceinline__ void read(float (&v)[VEC * NV], const char* slot, bool live, int64_t t,
-                                       int first, int step, int C, int team) const {
+  // slots began with.
+  __device__ __forceinline__ void read(float (&v)[VEC * NV], const char* slot, int64_t t, int first,
+                                       int step, int C, int team) const {
     if (kOwn) {
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) {
@@ -169,7 +168,7 @@ struct Rows {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = first + i * step;
-      v[i] = live && base && c < C ? to_f32(row[c]) : 0.f;
+      v[i] = base && c < C ? to_f32(row[c]) : 0.f;
     }
   }
 };
@@ -204,39 +203,29 @@ __device__ __forceinline__ void store_row(const float (&v)[VEC * NV], T* p, int 
   }
 }
 
-// Means and 1/deviations of a team's rows; v becomes the centred rows.
-template <int VEC, int NV, int kRows>
-__device__ __forceinline__ void row_stats(float (&v)[kRows][VEC * NV], Team& team, const NormK& k,
-                                          int first, int step, float (&mean)[kRows],
-                                          float (&rstd)[kRows]) {
-#pragma unroll
-  for (int r = 0; r < kRows; ++r) mean[r] = 0.f;
+// Mean and 1/deviation of a team's row; v becomes the centred row.
+template <int VEC, int NV>
+__device__ __forceinline__ void row_stats(float (&v)[VEC * NV], Team& team, const NormK& k,
+                                          int first, int step, float& mean, float& rstd) {
+  mean = 0.f;
   if (k.center) {
+    float s[1] = {0.f};
 #pragma unroll
-    for (int r = 0; r < kRows; ++r)
+    for (int i = 0; i < VEC * NV; ++i) s[0] += v[i];
+    team.sum(s);
+    mean = s[0] * k.inv_c;
 #pragma unroll
-      for (int i = 0; i < VEC * NV; ++i) mean[r] += v[r][i];
-    team.sum(mean);
+    for (int i = 0; i < NV; ++i)
+      if (first + i * step < k.C) {
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      mean[r] *= k.inv_c;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (first + i * step < k.C) {
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) v[r][i * VEC + j] -= mean[r];
-        }
-    }
+        for (int j = 0; j < VEC; ++j) v[i * VEC + j] -= mean;
+      }
   }
+  float s[1] = {0.f};
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    rstd[r] = 0.f;
-#pragma unroll
-    for (int i = 0; i < VEC * NV; ++i) rstd[r] += v[r][i] * v[r][i];
-  }
-  team.sum(rstd);
-#pragma unroll
-  for (int r = 0; r < kRows; ++r) rstd[r] = rsqrtf(rstd[r] * k.inv_c + k.eps);
+  for (int i = 0; i < VEC * NV; ++i) s[0] += v[i] * v[i];
+  team.sum(s);
+  rstd = rsqrtf(s[0] * k.inv_c + k.eps);
 }
 
 // Per-channel weights in shared memory, in the order in which a team's threads
@@ -275,9 +264,20 @@ __device__ __forceinline__ float group_weight(const NormK& k, int g, int c) {
   return w;
 }
 
+// A team's sums of part[0] and, for centred norms, part[1] (0 otherwise).
+__device__ __forceinline__ void team_sums(Team& team, float (&part)[2], bool center) {
+  if (center) {
+    team.sum(part);
+  } else {
+    float only[1] = {part[0]};
+    team.sum(only);
+    part[0] = only[0];
+    part[1] = 0.f;
+  }
+}
+
 // Work of a CTA: rows [cta R, cta R + R), cut at the groups' ends; its teams
-// take them in turn, kRows at a time; the backward keeps its column sums in
-// registers.  A thread has up to 32 (backward: 16) channels of a row, so that what
+// take them in turn; the backward keeps its column sums in registers.  A thread has up to 32 (backward: 16) channels of a row, so that what
 // a row costs by itself (sums over the team, addresses) is spread over many: with
 // 8 the forward took 283 instructions per 8 x 32 channels and was bound by them.
 struct Range {
@@ -288,7 +288,7 @@ __device__ __forceinline__ Range cta_rows(const NormK& k, int64_t rows_per_cta) 
   return Range{b, min(b + rows_per_cta, k.tokens)};
 }
 
-template <typename TB, typename TX, int VEC, int NV, int kRows>
+template <typename TB, typename TX, int VEC, int NV>
 __global__ void __launch_bounds__(kTeamThreads, 1) norm_fwd_kernel(
     const __grid_constant__ NormK k, const TX* x, int64_t x_stride, const TB* block,
     int64_t block_stride, TX* x_out, int64_t x_out_stride, TB* y, int64_t y_stride, float4* stats,
@@ -339,95 +339,69 @@ __global__ void __launch_bounds__(kTeamThreads, 1) norm_fwd_kernel(
                              [&](int c) { return group_weight<TB>(k, g, c); });
       __syncthreads();
     }
-    while (t < stop) {
-      const bool two = kRows == 2 && t + teams < stop;
-      const int s1 = s + 1 == depth ? 0 : s + 1;
-      copies_pending(depth - kRows);
+    for (; t < stop; t += teams) {
+      copies_pending(depth - 1);
       if (!RX::kOwn) team.sync();
-      float v[kRows][E], u[kRows][E];
-      float m0[kRows] = {}, r0[kRows] = {}, m1[kRows] = {}, r1[kRows] = {};
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        const char* slot = smem + (r ? s1 : s) * slot_bytes;
-        const int64_t row = t + r * teams;
-        rx.read(v[r], slot, !r || two, row, first, step, k.C, tm);
-        rb.read(u[r], slot + xb, !r || two, row, first, step, k.C, tm);
-      }
+      float v[E], u[E], m0 = 0.f, r0 = 0.f, m1 = 0.f, r1 = 0.f;
+      const char* slot = smem + s * slot_bytes;
+      rx.read(v, slot, t, first, step, k.C, tm);
+      rb.read(u, slot + xb, t, first, step, k.C, tm);
       if (block) {
         if (k.post) {
-          row_stats<VEC, NV, kRows>(u, team, k, first, step, m0, r0);
+          row_stats<VEC, NV>(u, team, k, first, step, m0, r0);
 #pragma unroll
-          for (int r = 0; r < kRows; ++r)
-#pragma unroll
-            for (int i = 0; i < E; ++i) u[r][i] *= r0[r];
+          for (int i = 0; i < E; ++i) u[i] *= r0;
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           float w[VEC];
           Weights<VEC, NV>::get(w, w_k, i, lane, lanes);
 #pragma unroll
-          for (int j = 0; j < VEC; ++j)
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) v[r][i * VEC + j] += w[j] * u[r][i * VEC + j];
+          for (int j = 0; j < VEC; ++j) v[i * VEC + j] += w[j] * u[i * VEC + j];
         }
-#pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-          if (!r || two)
-            store_row<TX, VEC, NV>(v[r], x_out + (t + r * teams) * x_out_stride, first, step, k.C);
-        }
+        store_row<TX, VEC, NV>(v, x_out + t * x_out_stride, first, step, k.C);
       }
       if (!RX::kOwn) team.sync();
       ask(s);
-      if (two) ask(s1);
+      s = s + 1 == depth ? 0 : s + 1;
       if (y) {
-        row_stats<VEC, NV, kRows>(v, team, k, first, step, m1, r1);
+        row_stats<VEC, NV>(v, team, k, first, step, m1, r1);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           float w[VEC];
           Weights<VEC, NV>::get(w, w_pre, i, lane, lanes);
 #pragma unroll
-          for (int j = 0; j < VEC; ++j)
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) v[r][i * VEC + j] *= r1[r] * w[j];
+          for (int j = 0; j < VEC; ++j) v[i * VEC + j] *= r1 * w[j];
         }
+        store_row<TB, VEC, NV>(v, y + t * y_stride, first, step, k.C);
+        if (y_q) {
+          // the checkpoint of y as stored; a group is 32 / VEC lanes of a warp
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-          const int64_t row = t + r * teams;
-          if (!r || two) store_row<TB, VEC, NV>(v[r], y + row * y_stride, first, step, k.C);
-          if (y_q && (!r || two)) {
-            // the checkpoint of y as stored; a group is 32 / VEC lanes of a warp
+          for (int i = 0; i < NV; ++i) {
+            uint32_t mag = 0;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-              uint32_t mag = 0;
+            for (int j = 0; j < VEC; ++j) {
+              v[i * VEC + j] = to_f32(from_f32<TB>(v[i * VEC + j]));
+              mag = max(mag, __float_as_uint(v[i * VEC + j]) & 0x7fffffffu);
+            }
 #pragma unroll
-              for (int j = 0; j < VEC; ++j) {
-                v[r][i * VEC + j] = to_f32(from_f32<TB>(v[r][i * VEC + j]));
-                mag = max(mag, __float_as_uint(v[r][i * VEC + j]) & 0x7fffffffu);
-              }
+            for (int o = 1; o < GS_ACT8_GROUP / VEC; o <<= 1)
+              mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, o));
+            const uint32_t e = act8_exponent(mag);
+            const float inv = act8_inverse(e);
+            const int c = first + i * step;
+            if (c < (k.C + GS_ACT8_GROUP - 1) / GS_ACT8_GROUP * GS_ACT8_GROUP) {
+              Pack<int8_t, VEC> q;
 #pragma unroll
-              for (int o = 1; o < GS_ACT8_GROUP / VEC; o <<= 1)
-                mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, o));
-              const uint32_t e = act8_exponent(mag);
-              const float inv = act8_inverse(e);
-              const int c = first + i * step;
-              if (c < (k.C + GS_ACT8_GROUP - 1) / GS_ACT8_GROUP * GS_ACT8_GROUP) {
-                Pack<int8_t, VEC> q;
-#pragma unroll
-                for (int j = 0; j < VEC; ++j)
-                  q.v[j] = (int8_t)(act8_quantise(v[r][i * VEC + j], inv, e) & 0xff);
-                store_pack<int8_t, VEC>(y_q + row * q_stride + c, q);
-                if (c % GS_ACT8_GROUP == 0) y_e[row * e_stride + c / GS_ACT8_GROUP] = (uint8_t)e;
-              }
+              for (int j = 0; j < VEC; ++j)
+                q.v[j] = (int8_t)(act8_quantise(v[i * VEC + j], inv, e) & 0xff);
+              store_pack<int8_t, VEC>(y_q + t * q_stride + c, q);
+              if (c % GS_ACT8_GROUP == 0) y_e[t * e_stride + c / GS_ACT8_GROUP] = (uint8_t)e;
             }
           }
         }
       }
-      if (lane == 0) {
-        stats[t] = make_float4(m0[0], r0[0], m1[0], r1[0]);
-        if (two) stats[t + teams] = make_float4(m0[kRows - 1], r0[kRows - 1], m1[kRows - 1], r1[kRows - 1]);
-      }
-      s = two ? (s1 + 1 == depth ? 0 : s1 + 1) : s1;
-      t += two ? 2 * teams : teams;
+      if (lane == 0) stats[t] = make_float4(m0, r0, m1, r1);
     }
     at = stop;
     if (g + 1 < k.groups) ++g;
@@ -436,7 +410,7 @@ __global__ void __launch_bounds__(kTeamThreads, 1) norm_fwd_kernel(
 
 // The sums of a (CTA, group) pair go to slot cta + group of part_e: along the
 // rows either the CTA or the group advances, so no two pairs share a slot.
-template <typename TB, typename TX, int VEC, int NV, int kRows, int kMost>
+template <typename TB, typename TX, int VEC, int NV, int kMost>
 __global__ void __launch_bounds__(kMost, 1) norm_bwd_kernel(
     const __grid_constant__ NormK k, const TX* x, int64_t x_stride, const TB* block,
     int64_t block_stride, const float4* stats, const TX* dx_out, int64_t dx_out_stride,
@@ -477,13 +451,8 @@ __global__ void __launch_bounds__(kMost, 1) norm_bwd_kernel(
   clear_shared(smem, depth * slot_bytes, depth * slot_bytes + teams * kRedFloats * (int)sizeof(float),
                !RX::kOwn || (block && dy && dx_out && k.C == VEC * NV * lanes));
   for (int i = 0; i < depth; ++i) ask(i);
-  float4 st[kRows], st_next[kRows];
-  auto ask_stats = [&](int64_t t) {
-#pragma unroll
-    for (int r = 0; r < kRows; ++r)
-      st_next[r] = t + r * teams < rows.end ? stats[t + r * teams] : make_float4(0.f, 0.f, 0.f, 0.f);
-  };
-  ask_stats(rows.begin + tm);
+  float4 st_next = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (rows.begin + tm < rows.end) st_next = stats[rows.begin + tm];
 
   float acc_pre[E], acc_e[E];
 #pragma unroll
@@ -527,118 +496,68 @@ __global__ void __launch_bounds__(kMost, 1) norm_bwd_kernel(
                              [&](int c) { return group_weight<TB>(k, g, c); });
       __syncthreads();
     }
-    while (t < stop) {
-      const bool two = kRows == 2 && t + teams < stop;
-      const int s1 = s + 1 == depth ? 0 : s + 1;
-      copies_pending(depth - kRows);
+    for (; t < stop; t += teams) {
+      copies_pending(depth - 1);
       if (!RX::kOwn) team.sync();
+      const float4 st = st_next;
+      if (t + teams < rows.end) st_next = stats[t + teams];
+      const char* slot = smem + s * slot_bytes;
+      float d[E];
+      if (dy) {
+        float n[E], h[E], part[2] = {0.f, 0.f};
+        rx.read(n, slot, t, first, step, k.C, tm);
+        ry.read(h, slot + 2 * xb + bb, t, first, step, k.C, tm);
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) st[r] = st_next[r];
-      ask_stats(two ? t + 2 * teams : t + teams);
-      float d[kRows][E], part[2 * kRows];
-      {
-        float n[kRows][E], h[kRows][E];
-        if (dy) {
+        for (int v = 0; v < NV; ++v) {
+          float w[VEC];
+          Weights<VEC, NV>::get(w, w_pre, v, lane, lanes);
 #pragma unroll
-          for (int r = 0; r < kRows; ++r) {
-            const bool live = !r || two;
-            const char* slot = smem + (r ? s1 : s) * slot_bytes;
-            rx.read(n[r], slot, live, t + r * teams, first, step, k.C, tm);
-            ry.read(h[r], slot + 2 * xb + bb, live, t + r * teams, first, step, k.C, tm);
-            float a = 0.f, b = 0.f;
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-              float w[VEC];
-              Weights<VEC, NV>::get(w, w_pre, v, lane, lanes);
-#pragma unroll
-              for (int j = 0; j < VEC; ++j) {
-                const int i = v * VEC + j;
-                n[r][i] = (n[r][i] - st[r].z) * st[r].w;
-                if (live) acc_pre[i] += h[r][i] * n[r][i];
-                h[r][i] *= w[j];
-                a += h[r][i] * n[r][i];
-                b += h[r][i];
-              }
-            }
-            part[r] = a;
-            part[kRows + r] = b;
-          }
-          if (k.center) {
-            team.sum(part);
-          } else {
-            float only[kRows];
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) only[r] = part[r];
-            team.sum(only);
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) part[r] = only[r], part[kRows + r] = 0.f;
+          for (int j = 0; j < VEC; ++j) {
+            const int i = v * VEC + j;
+            n[i] = (n[i] - st.z) * st.w;
+            acc_pre[i] += h[i] * n[i];
+            h[i] *= w[j];
+            part[0] += h[i] * n[i];
+            part[1] += h[i];
           }
         }
+        team_sums(team, part, k.center);
+        const float a = part[0] * k.inv_c, b = part[1] * k.inv_c;
+        rd.read(d, slot + xb, t, first, step, k.C, tm);
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-          const bool live = !r || two;
-          rd.read(d[r], smem + (r ? s1 : s) * slot_bytes + xb, live, t + r * teams, first, step, k.C, tm);
-          if (dy) {
-            const float a = part[r] * k.inv_c, b = part[kRows + r] * k.inv_c;
-#pragma unroll
-            for (int i = 0; i < E; ++i) d[r][i] += st[r].w * (h[r][i] - n[r][i] * a - b);
-          }
-          if (live) store_row<TX, VEC, NV>(d[r], dx + (t + r * teams) * dx_stride, first, step, k.C);
-        }
+        for (int i = 0; i < E; ++i) d[i] += st.w * (h[i] - n[i] * a - b);
+      } else {
+        rd.read(d, slot + xb, t, first, step, k.C, tm);
       }
+      store_row<TX, VEC, NV>(d, dx + t * dx_stride, first, step, k.C);
       if (block) {
-        float m[kRows][E];
+        float m[E], part[2] = {0.f, 0.f};
+        rb.read(m, slot + 2 * xb, t, first, step, k.C, tm);
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-          const bool live = !r || two;
-          rb.read(m[r], smem + (r ? s1 : s) * slot_bytes + 2 * xb, live, t + r * teams, first, step, k.C,
-                  tm);
-          float a = 0.f, b = 0.f;
+        for (int v = 0; v < NV; ++v) {
+          float w[VEC];  // 0 from C on
+          Weights<VEC, NV>::get(w, w_k, v, lane, lanes);
 #pragma unroll
-          for (int v = 0; v < NV; ++v) {
-            float w[VEC];  // 0 from C on
-            Weights<VEC, NV>::get(w, w_k, v, lane, lanes);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-              const int c = v * VEC + j;
-              if (k.post) m[r][c] = (m[r][c] - st[r].x) * st[r].y;
-              if (live) acc_e[c] += d[r][c] * m[r][c];
-              d[r][c] *= w[j];
-              a += d[r][c] * m[r][c];
-              b += d[r][c];
-            }
+          for (int j = 0; j < VEC; ++j) {
+            const int i = v * VEC + j;
+            if (k.post) m[i] = (m[i] - st.x) * st.y;
+            acc_e[i] += d[i] * m[i];
+            d[i] *= w[j];
+            part[0] += d[i] * m[i];
+            part[1] += d[i];
           }
-          part[r] = a;
-          part[kRows + r] = b;
         }
         if (k.post) {
-          if (k.center) {
-            team.sum(part);
-          } else {
-            float only[kRows];
+          team_sums(team, part, k.center);
+          const float a = part[0] * k.inv_c, b = part[1] * k.inv_c;
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) only[r] = part[r];
-            team.sum(only);
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) part[r] = only[r], part[kRows + r] = 0.f;
-          }
-#pragma unroll
-          for (int r = 0; r < kRows; ++r) {
-            const float a = part[r] * k.inv_c, b = part[kRows + r] * k.inv_c;
-#pragma unroll
-            for (int i = 0; i < E; ++i) d[r][i] = st[r].y * (d[r][i] - m[r][i] * a - b);
-          }
+          for (int i = 0; i < E; ++i) d[i] = st.y * (d[i] - m[i] * a - b);
         }
-#pragma unroll
-        for (int r = 0; r < kRows; ++r)
-          if (!r || two)
-            store_row<TB, VEC, NV>(d[r], dblock + (t + r * teams) * dblock_stride, first, step, k.C);
+        store_row<TB, VEC, NV>(d, dblock + t * dblock_stride, first, step, k.C);
       }
       if (!RX::kOwn) team.sync();
       ask(s);
-      if (two) ask(s1);
-      s = two ? (s1 + 1 == depth ? 0 : s1 + 1) : s1;
-      t += two ? 2 * teams : teams;
+      s = s + 1 == depth ? 0 : s + 1;
     }
     if (block && part_e && stop > at) {
       flush(acc_e, part_e + ((int64_t)blockIdx.x + g) * k.C);
@@ -817,8 +736,9 @@ struct Layout {
   size_t smem;
 };
 template <typename TB, typename TX, int VEC, int NV>
-Layout norm_layout(const NormK& k, int tensors, int rows, bool join, int most) {
+Layout norm_layout(const NormK& k, int tensors, bool join, int most) {
   Layout l;
+  const int sms = device_sms();
   for (int threads = most;; threads /= 2) {
     l.s = norm_shape<VEC, NV>(k, threads);
     const size_t slot = (size_t)tensors * (Rows<TX, VEC, NV>::slot(l.s.threads, l.s.teams, k.C) +
@@ -829,16 +749,16 @@ Layout norm_layout(const NormK& k, int tensors, int rows, bool join, int most) {
     l.depth = kMaxDepth;
     while (l.depth > 1 && l.depth * slot + fixed > (size_t)kSmemBudget) --l.depth;
     l.smem = l.depth * slot + fixed;
-    if (l.depth >= rows + 1 || l.s.teams == 1) return l;
+    const bool spread = k.tokens >= (int64_t)sms * l.s.teams || threads <= 128;  // every SM has work
+    if ((l.depth >= 2 && spread) || l.s.teams == 1) return l;
   }
 }
 
 template <typename TB, typename TX, int VEC, int NV>
 cudaError_t fwd_launch(const FwdArgs& a, cudaStream_t st) {
-  constexpr int kRows = 1;
-  const Layout l = norm_layout<TB, TX, VEC, NV>(a.k, 1, kRows, false, kTeamThreads);
+  const Layout l = norm_layout<TB, TX, VEC, NV>(a.k, 1, false, kTeamThreads);
   static std::atomic<uint64_t> known{0};
-  const auto kernel = norm_fwd_kernel<TB, TX, VEC, NV, kRows>;
+  const auto kernel = norm_fwd_kernel<TB, TX, VEC, NV>;
   const cudaError_t e = allow_smem(kernel, known);
   if (e != cudaSuccess) return e;
   int64_t rows = 0;
@@ -881,10 +801,9 @@ struct BwdArgs {
 
 template <typename TB, typename TX, int VEC, int NV, int kMost>
 cudaError_t bwd_launch(BwdArgs& a, cudaStream_t st) {
-  constexpr int kRows = 1;
-  const Layout l = norm_layout<TB, TX, VEC, NV>(a.k, 2, kRows, true, kMost);
+  const Layout l = norm_layout<TB, TX, VEC, NV>(a.k, 2, true, kMost);
   static std::atomic<uint64_t> known{0};
-  const auto kernel = norm_bwd_kernel<TB, TX, VEC, NV, kRows, kMost>;
+  const auto kernel = norm_bwd_kernel<TB, TX, VEC, NV, kMost>;
   const cudaError_t e = allow_smem(kernel, known);
   if (e != cudaSuccess) return e;
   a.ctas = (int)norm_ranges(a.k.tokens, l.s.teams, 1, &a.rows_per_cta);
