@@ -18,10 +18,9 @@
 namespace gs {
 namespace {
 
-constexpr int kNormCtas = 304;      // most row ranges of the backward (column sums)
+constexpr int kNormCtas = 304;      // most row ranges (places for their column sums)
 constexpr int kMaxTeamWarps = 16;
 constexpr int kTeamThreads = 512;   // most threads of a CTA
-constexpr int kWideThreads = 384;   // of the backward with 16 channels a thread: 168 registers
 constexpr int kSmemBudget = 224 * 1024;
 
 struct NormK {
@@ -410,8 +409,8 @@ __global__ void __launch_bounds__(kTeamThreads, 1) norm_fwd_kernel(
 
 // The sums of a (CTA, group) pair go to slot cta + group of part_e: along the
 // rows either the CTA or the group advances, so no two pairs share a slot.
-template <typename TB, typename TX, int VEC, int NV, int kMost>
-__global__ void __launch_bounds__(kMost, 1) norm_bwd_kernel(
+template <typename TB, typename TX, int VEC, int NV>
+__global__ void __launch_bounds__(kTeamThreads, 1) norm_bwd_kernel(
     const __grid_constant__ NormK k, const TX* x, int64_t x_stride, const TB* block,
     int64_t block_stride, const float4* stats, const TX* dx_out, int64_t dx_out_stride,
     const TB* dy, int64_t dy_stride, TX* dx, int64_t dx_stride, TB* dblock, int64_t dblock_stride,
@@ -672,12 +671,6 @@ NormK make_norm(const gs_norm& p) {
   return k;
 }
 
-// 16-byte rows everywhere: the wide accesses may be used.
-bool norm_wide(const gs_norm& p, int vec) {
-  return p.channels % vec == 0 && aligned16(p.w_pre) && aligned16(p.w_post) &&
-         aligned16(p.res_scale) && aligned16(p.gate);
-}
-
 struct FwdArgs {
   NormK k;
   const void *x, *block;
@@ -705,9 +698,9 @@ Shape norm_shape(const NormK& k, int threads) {
   return s;
 }
 
-// Row ranges: `per_sm` CTAs an SM, none without a row for each team.
-inline int64_t norm_ranges(int64_t tokens, int teams, int per_sm, int64_t* rows_per_cta) {
-  int64_t ctas = (int64_t)device_sms() * per_sm;
+// Row ranges: one CTA an SM, none without a row for each team.
+inline int64_t norm_ranges(int64_t tokens, int teams, int64_t* rows_per_cta) {
+  int64_t ctas = device_sms();
   if (ctas > kNormCtas) ctas = kNormCtas;
   const int64_t most = div_up(tokens, teams);
   if (ctas > most) ctas = most;
@@ -736,10 +729,10 @@ struct Layout {
   size_t smem;
 };
 template <typename TB, typename TX, int VEC, int NV>
-Layout norm_layout(const NormK& k, int tensors, bool join, int most) {
+Layout norm_layout(const NormK& k, int tensors, bool join) {
   Layout l;
   const int sms = device_sms();
-  for (int threads = most;; threads /= 2) {
+  for (int threads = kTeamThreads;; threads /= 2) {
     l.s = norm_shape<VEC, NV>(k, threads);
     const size_t slot = (size_t)tensors * (Rows<TX, VEC, NV>::slot(l.s.threads, l.s.teams, k.C) +
                                            Rows<TB, VEC, NV>::slot(l.s.threads, l.s.teams, k.C));
@@ -756,13 +749,13 @@ Layout norm_layout(const NormK& k, int tensors, bool join, int most) {
 
 template <typename TB, typename TX, int VEC, int NV>
 cudaError_t fwd_launch(const FwdArgs& a, cudaStream_t st) {
-  const Layout l = norm_layout<TB, TX, VEC, NV>(a.k, 1, false, kTeamThreads);
+  const Layout l = norm_layout<TB, TX, VEC, NV>(a.k, 1, false);
   static std::atomic<uint64_t> known{0};
   const auto kernel = norm_fwd_kernel<TB, TX, VEC, NV>;
   const cudaError_t e = allow_smem(kernel, known);
   if (e != cudaSuccess) return e;
   int64_t rows = 0;
-  const int64_t ctas = norm_ranges(a.k.tokens, l.s.teams, 1, &rows);
+  const int64_t ctas = norm_ranges(a.k.tokens, l.s.teams, &rows);
   kernel<<<(unsigned)ctas, l.s.threads, l.smem, st>>>(
       a.k, (const TX*)a.x, a.xs, (const TB*)a.block, a.bs, (TX*)a.x_out, a.xos, (TB*)a.y, a.ys,
       a.stats, a.y_q, a.qs, a.y_e, a.es, rows, l.s.warps, l.depth);
@@ -799,14 +792,14 @@ struct BwdArgs {
   int ctas;
 };
 
-template <typename TB, typename TX, int VEC, int NV, int kMost>
+template <typename TB, typename TX, int VEC, int NV>
 cudaError_t bwd_launch(BwdArgs& a, cudaStream_t st) {
-  const Layout l = norm_layout<TB, TX, VEC, NV>(a.k, 2, true, kMost);
+  const Layout l = norm_layout<TB, TX, VEC, NV>(a.k, 2, true);
   static std::atomic<uint64_t> known{0};
-  const auto kernel = norm_bwd_kernel<TB, TX, VEC, NV, kMost>;
+  const auto kernel = norm_bwd_kernel<TB, TX, VEC, NV>;
   const cudaError_t e = allow_smem(kernel, known);
   if (e != cudaSuccess) return e;
-  a.ctas = (int)norm_ranges(a.k.tokens, l.s.teams, 1, &a.rows_per_cta);
+  a.ctas = (int)norm_ranges(a.k.tokens, l.s.teams, &a.rows_per_cta);
   kernel<<<(unsigned)a.ctas, l.s.threads, l.smem, st>>>(
       a.k, (const TX*)a.x, a.xs, (const TB*)a.block, a.bs, a.stats, (const TX*)a.dx_out, a.dxos,
       (const TB*)a.dy, a.dys, (TX*)a.dx, a.dxs, (TB*)a.dblock, a.dbs, a.part_pre, a.part_e,
@@ -814,14 +807,13 @@ cudaError_t bwd_launch(BwdArgs& a, cudaStream_t st) {
   return cudaSuccess;
 }
 
-// 16 channels a thread in 384 threads where a row is that wide and aligned
-// (32640 x 1024 bf16: 96 us; 8 in 512 threads 107, 16 in 512, which spill, 119,
-// and in 256 119).
+// 16 channels a thread where rows are aligned and that wide (32640 x 1024 bf16: 85 us,
+// with 8 a thread 107 us); 8 for rows that start anywhere, where 16 cost more in
+// single accesses than they save (5003 x 997 fp32: 49 us, 87 us).
 template <typename TB, typename TX, int VEC>
 cudaError_t bwd_pick(BwdArgs& a, cudaStream_t st) {
-  if (a.k.C > 32 * 16 * (kWideThreads / 32)) return bwd_launch<TB, TX, VEC, 16 / VEC, kTeamThreads>(a, st);
-  if (a.k.C > (VEC > 1 ? 256 : 4096)) return bwd_launch<TB, TX, VEC, 16 / VEC, kWideThreads>(a, st);
-  return bwd_launch<TB, TX, VEC, 8 / VEC, kTeamThreads>(a, st);
+  if (a.k.C <= (VEC > 1 ? 256 : 4096)) return bwd_launch<TB, TX, VEC, 8 / VEC>(a, st);
+  return bwd_launch<TB, TX, VEC, 16 / VEC>(a, st);
 }
 
 template <typename TB, typename TX>
@@ -856,7 +848,7 @@ extern "C" gs_status gs_gated_norm_fwd(const gs_norm* p, const void* x, int64_t 
   if (y_q && (!aligned16(y_q) || q_stride % 16 ||
               q_stride < div_up(p->channels, GS_ACT8_GROUP) * GS_ACT8_GROUP)) return GS_ERR_INVALID_ARG;
   const int vec = 16 / eb;
-  const bool wide = norm_wide(*p, vec) && rows_aligned(x, x_stride, ex, 16) &&
+  const bool wide = p->channels % vec == 0 && rows_aligned(x, x_stride, ex, 16) &&
                     rows_aligned(block, block_stride, eb, 16) &&
                     rows_aligned(x_out, x_out_stride, ex, 16) && rows_aligned(y, y_stride, eb, 16);
   const FwdArgs a{make_norm(*p), x, block, x_out, y, x_stride, block_stride, x_out_stride,
@@ -894,7 +886,7 @@ extern "C" gs_status gs_gated_norm_bwd(
        ws_bytes < gs_gated_norm_workspace_bytes(p->channels, p->groups)))
     return GS_ERR_INVALID_ARG;
   const int vec = 16 / eb;
-  const bool wide = norm_wide(*p, vec) && rows_aligned(x_out, x_stride, ex, 16) &&
+  const bool wide = p->channels % vec == 0 && rows_aligned(x_out, x_stride, ex, 16) &&
                     rows_aligned(block, block_stride, eb, 16) &&
                     rows_aligned(dx_out, dx_out_stride, ex, 16) &&
                     rows_aligned(dy, dy_stride, eb, 16) && rows_aligned(dx, dx_stride, ex, 16) &&
