@@ -31,7 +31,13 @@ struct HeadsK {
   int64_t in_token, in_head, out_token, out_head;  // bytes
 };
 
-constexpr int kHeadBatch = 4;  // heads a thread loads before it stores any
+#ifndef HBX
+#define HBX 2
+#define MB 1
+#endif
+// Heads a thread loads before it stores any.
+template <typename T, int VEC>
+constexpr int kBatchOf = VEC * sizeof(T) >= 8 && sizeof(T) == 2 ? HBX : 4;
 constexpr int kThreads = 256;
 
 // Sine and cosine of a phase in half turns, [-1, 1).  16-bit heads take the
@@ -48,9 +54,10 @@ __device__ __forceinline__ void sine(float half_turns, float* s, float* c) {
 // of neighbouring pairs (INTER) may reach over the sections' ends.  Threads: unit
 // fastest (a warp reads neighbouring channels), then head slot, then token.
 template <typename T, int VEC, bool INTER>
-__global__ void __launch_bounds__(kThreads) rope_kernel(
+__global__ void __launch_bounds__(kThreads, VEC * sizeof(T) >= 8 && sizeof(T) == 2 ? MB : 1) rope_kernel(
     int64_t tokens, const __grid_constant__ RopeK k, const __grid_constant__ HeadsK s0,
     const __grid_constant__ HeadsK s1, int heads0, int heads, const int32_t* __restrict__ pos) {
+  constexpr int kHeadBatch = kBatchOf<T, VEC>;
   const int u = threadIdx.x % k.units;
   const int y = threadIdx.x / k.units;
   const int hs = y % k.head_slots;
@@ -259,7 +266,7 @@ extern "C" gs_status gs_rope(int64_t tokens, int32_t n_axes, const int32_t* dims
   k.units = copies ? (int)div_up(head_dim, 2 * vec) : k.rot_units;
   k.sign = inverse ? -1.f : 1.f;
   const int rows = kThreads / k.units;  // (token, head slot) pairs of a block
-  int slots = (int)div_up(heads, kHeadBatch);
+  int slots = (int)div_up(heads, elem == 2 && vec >= 4 ? kBatchOf<__half, 4> : 4);
   k.head_slots = slots < rows ? slots : rows;
   k.tokens_per_block = rows / k.head_slots;
   const int threads = k.units * k.head_slots * k.tokens_per_block;

@@ -83,7 +83,7 @@ struct Plan {
   int32_t tiles_m;             // channel tiles
   int32_t terms;               // bf16 terms of dy
   int64_t term_rows;           // rows of the tensor map between terms
-  int32_t steps;               // steps of a whole tile
+  int32_t token_steps, steps;  // steps over the tokens; of a whole tile
   int32_t clusters, waves;     // whole tiles per cluster
   int32_t rem_tiles;           // tiles dealt out in steps
   int64_t rem_steps, quota;    // their steps, and a cluster's share
@@ -91,71 +91,64 @@ struct Plan {
   int32_t accumulate;
 };
 
-struct Seg {
-  int tile, s0, s1;
-  int slot;  // place of a partial sum, or -1: the whole tile
-};
-
-// Calls f(seg) for the cluster's segments in order until it returns false.
-template <typename F>
-__device__ __forceinline__ void each_seg(const Plan& p, int cluster, F f) {
-  for (int w = 0; w < p.waves; ++w)
-    if (!f(Seg{w * p.clusters + cluster, 0, p.steps, -1})) return;
-  const int64_t begin = (int64_t)cluster * p.quota;
-  const int64_t end = min(begin + p.quota, p.rem_steps);
-  for (int64_t at = begin; at < end;) {
-    const int tile = (int)(at / p.steps);
-    const int64_t stop = min(end, (int64_t)(tile + 1) * p.steps);
-    Seg s;
-    s.tile = p.waves * p.clusters + tile;
-    s.s0 = (int)(at - (int64_t)tile * p.steps);
-    s.s1 = s.s0 + (int)(stop - at);
-    s.slot = s.s1 - s.s0 == p.steps ? -1 : (at == begin ? 0 : 1);
-    if (!f(s)) return;
-    at = stop;
-  }
-}
-
-// The same steps one by one.  Every role goes through it once per step, on the
-// latency of its own instructions: divisions are done once per segment.
+// A cluster's steps one by one: its whole tiles, then its share of the dealt-out
+// steps.  Within a tile the steps run over blocks of kChunk token steps, all of
+// them for one term of dy after the other, so that a run of products that the
+// tensor core sums on its own has terms of one size.  Every role goes through
+// this once per step, on the latency of its own instructions: divisions are done
+// once per segment (the steps of one tile).
 struct Walk {
   const Plan& p;
   int cluster, wave, left;
   int64_t at, stop;
-  int ch0, n0;    // the tile's first channel and column
-  int ts, term;   // the step's tokens (from 64 ts on) and term of dy
+  int ch0, n0;            // the tile's first channel and column
+  int slot;               // place of the segment's partial sum, or -1: the whole tile
+  int ts, term;           // the step's tokens (from 64 ts on) and term of dy
+  int block, block_end;   // the block of token steps it is in
   __device__ __forceinline__ Walk(const Plan& plan, int cl)
-      : p(plan), cluster(cl), wave(0), left(0), ch0(0), n0(0), ts(0), term(0) {
+      : p(plan), cluster(cl), wave(0), left(0), ch0(0), n0(0), slot(-1), ts(0), term(0), block(0),
+        block_end(0) {
     at = (int64_t)cl * p.quota;
     stop = min(at + p.quota, p.rem_steps);
   }
   __device__ __forceinline__ void begin(int tile, int first, int steps) {
     n0 = tile / p.tiles_m * p.bn;
     ch0 = tile % p.tiles_m * kBM;
-    ts = first / p.terms;
-    term = first - ts * p.terms;
+    block = first / (kChunk * p.terms) * kChunk;
+    block_end = min(block + kChunk, p.token_steps);
+    const int in = first - block * p.terms, size = block_end - block;
+    term = in / size;
+    ts = block + in - term * size;
     left = steps - 1;
   }
   __device__ __forceinline__ bool next() {
     if (--left >= 0) {
-      if (++term == p.terms) {
-        term = 0;
-        ++ts;
+      if (++ts == block_end) {
+        if (++term == p.terms) {
+          term = 0;
+          block = block_end;
+          block_end = min(block + kChunk, p.token_steps);
+        }
+        ts = block;
       }
       return true;
     }
     if (wave < p.waves) {
+      slot = -1;
       begin(wave++ * p.clusters + cluster, 0, p.steps);
       return true;
     }
     if (at >= stop) return false;
     const int i = (int)(at / p.steps);
     const int64_t upto = min(stop, (int64_t)(i + 1) * p.steps);
-    begin(p.waves * p.clusters + i, (int)(at - (int64_t)i * p.steps), (int)(upto - at));
+    const int n = (int)(upto - at);
+    slot = n == p.steps ? -1 : at == (int64_t)cluster * p.quota ? 0 : 1;
+    begin(p.waves * p.clusters + i, (int)(at - (int64_t)i * p.steps), n);
     at = upto;
     return true;
   }
-  __device__ __forceinline__ bool last() const { return left == 0; }  // of its segment
+  __device__ __forceinline__ bool segment_ends() const { return left == 0; }
+  __device__ __forceinline__ bool run_ends() const { return left == 0 || ts + 1 == block_end; }
 };
 
 __device__ __forceinline__ int64_t cluster_steps(const Plan& p, int cluster) {
@@ -431,27 +424,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint64_t b_first = smem_desc(smem_u32(smem));
       const int64_t total = cluster_steps(p, cluster);
       Walk w(p, cluster);
-      uint32_t st = 0, phase = 0, run = 0, chunk = 0;
+      uint32_t st = 0, phase = 0, acc_phase = 1;
+      bool begins = true;  // a run of products
       for (int64_t it = 0; it < total; ++it) {
         w.next();
-        if (run == 0 && !mbar_wait(smem_u32(&c->acc_empty), (chunk & 1) ^ 1, c, status)) break;
+        if (begins) {
+          if (!mbar_wait(smem_u32(&c->acc_empty), acc_phase, c, status)) break;
+          acc_phase ^= 1;
+        }
         if (!mbar_wait(smem_u32(&c->full[st]), phase, c, status)) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint32_t a = tmem + kBN + st * kAColumns;
         const uint64_t b = b_first + st * (kBBytes >> 4);
-        ++run;
-        const bool last = run == kChunk || w.last();
+        const bool ends = w.run_ends();
         if (issues) {
 #pragma unroll
           for (int i = 0; i < kBT / 16; ++i)  // 16 tokens: 8 columns, and two atoms of 1024 bytes
-            mma(tmem, a + 8 * i, b + (i * 2048 >> 4), idesc, run > 1 || i > 0);
+            mma(tmem, a + 8 * i, b + (i * 2048 >> 4), idesc, !begins || i > 0);
           mma_commit(smem_u32(&c->empty[st]));
-          if (last) mma_commit(smem_u32(&c->acc_full));
+          if (ends) mma_commit(smem_u32(&c->acc_full));
         }
-        if (last) {
-          run = 0;
-          ++chunk;
-        }
+        begins = ends;
         if (++st == kStages) st = 0, phase ^= 1;
       }
     }
@@ -521,39 +514,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int cols = p.bn / 2, c0 = (warp - 4) / 4 * cols;
     // the lane's channel: see the decoding warps
     const int row = quarter * 32 + 4 * (lane & 7) + (lane >> 3);
-    uint32_t chunk = 0;
-    each_seg(p, cluster, [&](const Seg& s) {
-      float acc[kBN / 2];
+    uint32_t phase = 0;
+    float acc[kBN / 2];
 #pragma unroll
-      for (int j = 0; j < kBN / 2; ++j) acc[j] = 0.f;
-      for (int k = s.s0; k < s.s1; k += kChunk, ++chunk) {
-        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&c->acc_full), chunk & 1, c, status)))
-          return false;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t from = tmem + c0 + ((uint32_t)(quarter * 32) << 16);
+    for (int j = 0; j < kBN / 2; ++j) acc[j] = 0.f;
+    Walk w(p, cluster);
+    while (w.next()) {
+      if (!w.run_ends()) continue;
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&c->acc_full), phase, c, status))) break;
+      phase ^= 1;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint32_t from = tmem + c0 + ((uint32_t)(quarter * 32) << 16);
 #pragma unroll
-        for (int j = 0; j < kBN / 2; j += 32)
-          if (j < cols) tmem_add32(from + j, acc + j);
-        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(in_cta0(smem_u32(&c->acc_empty)));
-      }
-      const int n0 = s.tile / p.tiles_m * p.bn + c0;
-      const int ch = s.tile % p.tiles_m * kBM + (int)rank * 128 + row;
-      if (s.slot < 0) {
+      for (int j = 0; j < kBN / 2; j += 32)
+        if (j < cols) tmem_add32(from + j, acc + j);
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(in_cta0(smem_u32(&c->acc_empty)));
+      if (!w.segment_ends()) continue;
+      const int n0 = w.n0 + c0, ch = w.ch0 + (int)rank * 128 + row;
+      if (w.slot < 0) {
         TO* to = dw + (int64_t)n0 * p.dws + ch;
 #pragma unroll
         for (int j = 0; j < kBN / 2; ++j, to += p.dws)
           if (ch < p.channels && j < cols && n0 + j < p.rows) put_dw<TO>(to, acc[j], p.accumulate);
       } else {
-        float* to = partial + ((size_t)(cluster * 2 + s.slot) * 2 + rank) * kPartialFloats +
+        float* to = partial + ((size_t)(cluster * 2 + w.slot) * 2 + rank) * kPartialFloats +
                     c0 * 128 + row;
 #pragma unroll
         for (int j = 0; j < kBN / 2; ++j)
           if (j < cols) to[j * 128] = acc[j];
       }
-      return true;
-    });
+#pragma unroll
+      for (int j = 0; j < kBN / 2; ++j) acc[j] = 0.f;
+    }
   } else {
     // ---- bytes to bf16 -------------------------------------------------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDecodeRegs));
@@ -857,7 +851,8 @@ extern "C" gs_status gs_act8_wgrad(int64_t tokens, int32_t rows, int32_t channel
 
   p.tiles_m = (int)div_up(channels, kBM);
   const int64_t tiles = p.tiles_m * div_up(rows, p.bn);
-  p.steps = (int)(div_up(tokens, kBT) * p.terms);
+  p.token_steps = (int)div_up(tokens, kBT);
+  p.steps = p.token_steps * p.terms;
   p.clusters = clusters;
   p.waves = (int)(tiles / clusters);
   p.rem_tiles = (int)(tiles - (int64_t)p.waves * clusters);
