@@ -5,8 +5,16 @@
 // pass (the rotation is orthogonal).  Angles are phases in 64-bit fractions of
 // a turn: position * turns modulo 2^64, whose top 32 bits are the signed phase
 // in [-1/2, 1/2), so a large position loses nothing and the sine never needs a
-// range reduction.  The angle is the same for every head of a token: a thread
-// keeps the sines of its pairs and walks heads.
+// range reduction.  The angle is the same for every head of a token: a block
+// computes the sines of its tokens once, a thread keeps those of its channels and
+// walks heads.
+//
+// Bound by memory: one read and one write of the heads.  A thread has a few pairs
+// of a head, as vectors of up to 16 bytes, and finds their places once: blocks
+// walk over the tokens.  (With a block per group of tokens, every thread computing
+// its own sines, 32640 tokens of 20 heads of 64 in bf16 took 53 us, most of them
+// in that set-up.  Vectors of 16 neighbouring bytes, whatever the sections, with
+// the partners read a second time, took 62 us.)
 #include <math.h>
 #include <string.h>
 
@@ -18,10 +26,7 @@ namespace {
 struct RopeK {
   uint64_t turns[GS_ROPE_MAX_DIM / 2];
   int32_t dims[GS_ROPE_MAX_AXES];
-  int32_t n_axes, head_dim;
-  int32_t pairs;             // that rotate
-  int32_t rot_units, units;  // units that rotate, and with those that copy
-  int32_t head_slots, tokens_per_block;
+  int32_t n_axes, head_dim, rot;  // rot: channels that turn
   float sign;
 };
 
@@ -29,17 +34,24 @@ struct HeadsK {
   const char* in;
   char* out;
   int64_t in_token, in_head, out_token, out_head;  // bytes
+  int32_t heads;
+  int32_t units;                  // of VEC pairs of a head: those that turn, or all
+  int32_t slots, block_tokens;    // threads: units x slots x block_tokens
 };
 
-#ifndef HBX
-#define HBX 2
-#define MB 1
-#endif
-// Heads a thread loads before it stores any.
-template <typename T, int VEC>
-constexpr int kBatchOf = VEC * sizeof(T) >= 8 && sizeof(T) == 2 ? HBX : 4;
+// Heads a thread loads before it stores any, and blocks an SM that leave it the
+// registers for that (32640 tokens, 20 heads of 64 in bf16: 4 heads and 3 blocks
+// 45 us, 4 and 4 47, 4 and 2 52, 2 and 4 45; pairs of neighbours, 16 heads of 96
+// in fp16: 2 and 4 51 us, 4 and 3 57).
+template <typename T, int VEC, bool INTER>
+constexpr int kBatchOf = INTER && VEC * sizeof(T) == 8 && sizeof(T) == 2 ? 2 : 4;
+template <typename T, int VEC, bool INTER>
+constexpr int kBlocksOf = kBatchOf<T, VEC, INTER> == 2 ? 4 : 3;
+// Most pairs a thread: 16 bytes of an fp32 head or of neighbours; of either half
+// of a 16-bit head 8 bytes, as 16 take so many registers that less is in flight
+// (the same heads in sections of 32: 8 bytes 45 us, 16 bytes 49 to 105).
+constexpr int most_pairs(int elem, bool interleaved) { return elem == 4 && interleaved ? 2 : 4; }
 constexpr int kThreads = 256;
-
 // Sine and cosine of a phase in half turns, [-1, 1).  16-bit heads take the
 // fast functions (absolute error below 2^-21 on this range, a sixteenth of the
 // rounding of an fp16 result), fp32 heads the accurate ones.
@@ -49,127 +61,119 @@ __device__ __forceinline__ void sine(float half_turns, float* s, float* c) {
   else __sincosf(half_turns * 3.14159265358979f, s, c);
 }
 
-// A unit is VEC pairs (2 VEC channels) of a head; with VEC = 1 the two channels
-// move one by one, so that any stride and an odd last channel are served.  Units
-// of neighbouring pairs (INTER) may reach over the sections' ends.  Threads: unit
-// fastest (a warp reads neighbouring channels), then head slot, then token.
+// VEC pairs a thread: two vectors of VEC channels, or (neighbours, INTER) one of
+// 2 VEC; with VEC = 1 the two channels move one by one, so that any stride and an
+// odd last channel are served.  Threads: vector fastest, then head slot, then
+// token.
 template <typename T, int VEC, bool INTER>
-__global__ void __launch_bounds__(kThreads, VEC * sizeof(T) >= 8 && sizeof(T) == 2 ? MB : 1) rope_kernel(
-    int64_t tokens, const __grid_constant__ RopeK k, const __grid_constant__ HeadsK s0,
-    const __grid_constant__ HeadsK s1, int heads0, int heads, const int32_t* __restrict__ pos) {
-  constexpr int kHeadBatch = kBatchOf<T, VEC>;
-  const int u = threadIdx.x % k.units;
-  const int y = threadIdx.x / k.units;
-  const int hs = y % k.head_slots;
-  const int64_t t = (int64_t)blockIdx.x * k.tokens_per_block + y / k.head_slots;
-  if (t >= tokens) return;
+__global__ void __launch_bounds__(kThreads, kBlocksOf<T, VEC, INTER>) rope_kernel(
+    int64_t tokens, const __grid_constant__ RopeK k, const __grid_constant__ HeadsK q,
+    const __grid_constant__ HeadsK kk, const int32_t* __restrict__ pos) {
+  constexpr bool kOne = INTER && VEC > 1;  // both channels in one vector
+  constexpr int kHeadBatch = kBatchOf<T, VEC, INTER>;
+  __shared__ float2 angles[2][kThreads * VEC];  // [token][pair]: cosine, sine
+  const HeadsK& s = blockIdx.y ? kk : q;
+  const int threads = s.units * s.slots * s.block_tokens;
+  if ((int)threadIdx.x >= threads) return;  // (the larger set's blocks have more)
+  const int u = threadIdx.x % s.units, y = threadIdx.x / s.units;
+  const int hs = y % s.slots, tok = y / s.slots;
+  const int pairs = k.rot / 2;
 
-  // the unit's place: its first pair's section, and its two halves' channels
-  int axis = 0, at = 0, before = 0;
-  auto seek = [&](int pair) {
-    while (axis + 1 < k.n_axes && pair - before >= k.dims[axis] / 2) {
-      before += k.dims[axis] / 2;
-      at += k.dims[axis];
-      ++axis;
-    }
-  };
-  int first = 2 * VEC * u, second = first + VEC;
-  if (!INTER && u < k.rot_units) {
-    seek(u * VEC);
-    first = at + u * VEC - before;
+  // the unit's place: its pairs, and its two halves' channels
+  const int pair = u * VEC;
+  int first = 2 * VEC * u, second = first + (kOne ? 0 : VEC);
+  if (!INTER && pair < pairs) {
+    int axis = 0, at = 0;
+    while (pair - at / 2 >= k.dims[axis] / 2) at += k.dims[axis++];
+    first = at + pair - at / 2;
     second = first + k.dims[axis] / 2;
   }
-  constexpr bool kWide = INTER && VEC > 1;  // both halves in one access
   const bool two = VEC > 1 || second < k.head_dim;
-
-  Pack<T, VEC> a[kHeadBatch], b[kHeadBatch];
-  auto load = [&](int h0) {
-#pragma unroll
-    for (int i = 0; i < kHeadBatch; ++i) {
-      const int h = h0 + i * k.head_slots;
-      if (h < heads) {
-        const bool in0 = h < heads0;
-        const HeadsK& s = in0 ? s0 : s1;
-        const T* p = reinterpret_cast<const T*>(s.in + t * s.in_token +
-                                                (in0 ? h : h - heads0) * s.in_head);
-        if (kWide) {
-          const Pack<T, 2 * VEC> w = load_pack<T, 2 * VEC>(p + first);
-#pragma unroll
-          for (int c = 0; c < VEC; ++c) {
-            a[i].v[c] = w.v[2 * c];
-            b[i].v[c] = w.v[2 * c + 1];
-          }
-        } else {
-          a[i] = load_pack<T, VEC>(p + first);
-          if (two) b[i] = load_pack<T, VEC>(p + second);
-        }
-      }
-    }
+  // the angle that this thread computes for the block (and every `threads`-th after it)
+  auto axis_of = [&](int j) {
+    int axis = 0;
+    while (j >= k.dims[axis] / 2) j -= k.dims[axis++] / 2;
+    return axis;
   };
-  load(hs);  // on its way while the angles are computed
+  const int a_tok = threadIdx.x / pairs, a_pair = threadIdx.x - a_tok * pairs;
+  const int a_axis = axis_of(a_pair);
+  auto compute = [&](float2* to, int64_t row, int axis, int j) {
+    if (row >= tokens) return;
+    const int64_t p = pos[row * k.n_axes + axis];
+    const uint64_t phase = (uint64_t)p * k.turns[j];
+    float2 a;
+    sine<T>((float)(int32_t)(phase >> 32) * 4.656612873077393e-10f, &a.y, &a.x);  // 2^-31
+    a.y *= k.sign;
+    *to = a;
+  };
 
-  float co[VEC], si[VEC];
-  bool rot[VEC];
+  const int64_t in_step = s.in_head * s.slots, out_step = s.out_head * s.slots;
+  int turn = 0;
+  for (int64_t t0 = (int64_t)blockIdx.x * s.block_tokens; t0 < tokens;
+       t0 += (int64_t)gridDim.x * s.block_tokens, turn ^= 1) {
+    const int64_t t = t0 + tok;
+    const char* in = s.in + t * s.in_token + hs * s.in_head;
+    char* out = s.out + t * s.out_token + hs * s.out_head;
+    Pack<T, kOne ? 2 * VEC : VEC> a[kHeadBatch], b[kOne ? 1 : kHeadBatch];
+    auto load = [&](int left) {
+      const char* p = in;
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    const int pair = u * VEC + i;
-    rot[i] = INTER ? pair < k.pairs : u < k.rot_units;
-    if (rot[i]) {
-      if (INTER) seek(pair);
-      const int64_t p = pos[t * k.n_axes + axis];
-      const uint64_t phase = (uint64_t)p * k.turns[pair];
-      sine<T>((float)(int32_t)(phase >> 32) * 4.656612873077393e-10f, &si[i], &co[i]);  // 2^-31
-      si[i] *= k.sign;
+      for (int i = 0; i < kHeadBatch; ++i, p += in_step)
+        if (i * s.slots < left) {
+          a[i] = load_pack<T, kOne ? 2 * VEC : VEC>(reinterpret_cast<const T*>(p) + first);
+          if (!kOne && two)
+            b[kOne ? 0 : i] = load_pack<T, kOne ? 2 * VEC : VEC>(reinterpret_cast<const T*>(p) + second);
+        }
+    };
+    int left = t < tokens ? s.heads - hs : 0;  // heads from this thread's on
+    load(left);  // on its way while the angles are computed
+    float2* angle = angles[turn];
+    if (a_tok < s.block_tokens) compute(angle + threadIdx.x, t0 + a_tok, a_axis, a_pair);
+    for (int i = threadIdx.x + threads; i < s.block_tokens * pairs; i += threads) {
+      const int j = i % pairs;
+      compute(angle + i, t0 + i / pairs, axis_of(j), j);
     }
-  }
-
-  for (int h0 = hs; h0 < heads; h0 += kHeadBatch * k.head_slots) {
-    if (h0 != hs) load(h0);
+    // (two tables in turn: one barrier a round is enough)
+    asm volatile("bar.sync 1, %0;" ::"r"((threads + 31) / 32 * 32) : "memory");
+    float2 cs[VEC];
 #pragma unroll
-    for (int i = 0; i < kHeadBatch; ++i) {
-      const int h = h0 + i * k.head_slots;
-      if (h < heads) {
-        const bool in0 = h < heads0;
-        const HeadsK& s = in0 ? s0 : s1;
-        T* p = reinterpret_cast<T*>(s.out + t * s.out_token +
-                                    (in0 ? h : h - heads0) * s.out_head);
+    for (int c = 0; c < VEC; ++c)
+      cs[c] = pair + c < pairs ? angle[tok * pairs + pair + c] : make_float2(1.f, 0.f);
+    while (left > 0) {
+      char* p = out;
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) {
-          if (rot[c]) {
-            const float x = to_f32(a[i].v[c]), z = to_f32(b[i].v[c]);
-            a[i].v[c] = from_f32<T>(x * co[c] - z * si[c]);
-            b[i].v[c] = from_f32<T>(x * si[c] + z * co[c]);
-          }
+      for (int i = 0; i < kHeadBatch; ++i, p += out_step)
+        if (i * s.slots < left) {
+#pragma unroll
+          for (int c = 0; c < VEC; ++c)
+            if (pair + c < pairs) {
+              T& x = a[i].v[kOne ? 2 * c : c];
+              T& z = kOne ? a[i].v[kOne ? 2 * c + 1 : 0] : b[kOne ? 0 : i].v[c];
+              const float u0 = to_f32(x), v0 = to_f32(z);
+              x = from_f32<T>(u0 * cs[c].x - v0 * cs[c].y);
+              z = from_f32<T>(u0 * cs[c].y + v0 * cs[c].x);
+            }
+          store_pack(reinterpret_cast<T*>(p) + first, a[i]);
+          if (!kOne && two) store_pack(reinterpret_cast<T*>(p) + second, b[kOne ? 0 : i]);
         }
-        if (kWide) {
-          Pack<T, 2 * VEC> w;
-#pragma unroll
-          for (int c = 0; c < VEC; ++c) {
-            w.v[2 * c] = a[i].v[c];
-            w.v[2 * c + 1] = b[i].v[c];
-          }
-          store_pack<T, 2 * VEC>(p + first, w);
-        } else {
-          store_pack<T, VEC>(p + first, a[i]);
-          if (two) store_pack<T, VEC>(p + second, b[i]);
-        }
-      }
+      left -= kHeadBatch * s.slots;
+      in += kHeadBatch * in_step;
+      out += kHeadBatch * out_step;
+      load(left);
     }
   }
 }
 
 template <typename T, bool INTER>
 void rope_launch(int vec, dim3 grid, int threads, int64_t tokens, const RopeK& k, const HeadsK& s0,
-                 const HeadsK& s1, int heads0, int heads, const int32_t* pos, cudaStream_t st) {
-  constexpr int kMax = 16 / (int)sizeof(T) / (INTER ? 2 : 1);
-  if (kMax >= 8 && vec == 8)
-    rope_kernel<T, kMax >= 8 ? 8 : 1, INTER><<<grid, threads, 0, st>>>(tokens, k, s0, s1, heads0, heads, pos);
-  else if (kMax >= 4 && vec == 4)
-    rope_kernel<T, kMax >= 4 ? 4 : 1, INTER><<<grid, threads, 0, st>>>(tokens, k, s0, s1, heads0, heads, pos);
+                 const HeadsK& s1, const int32_t* pos, cudaStream_t st) {
+  constexpr int kMost = most_pairs(sizeof(T), INTER);
+  if (kMost == 4 && vec == 4)
+    rope_kernel<T, kMost, INTER><<<grid, threads, 0, st>>>(tokens, k, s0, s1, pos);
   else if (vec == 2)
-    rope_kernel<T, 2, INTER><<<grid, threads, 0, st>>>(tokens, k, s0, s1, heads0, heads, pos);
+    rope_kernel<T, 2, INTER><<<grid, threads, 0, st>>>(tokens, k, s0, s1, pos);
   else
-    rope_kernel<T, 1, INTER><<<grid, threads, 0, st>>>(tokens, k, s0, s1, heads0, heads, pos);
+    rope_kernel<T, 1, INTER><<<grid, threads, 0, st>>>(tokens, k, s0, s1, pos);
 }
 
 bool dims_ok(int32_t n_axes, const int32_t* dims, int* sum) {
@@ -225,19 +229,21 @@ extern "C" gs_status gs_rope(int64_t tokens, int32_t n_axes, const int32_t* dims
   if (tokens == 0 || heads == 0) return GS_OK;
   if (!positions || !aligned4(positions)) return GS_ERR_INVALID_ARG;
 
-  // Pairs per unit: the widest that the sections, the strides and the
-  // alignment of every set allow, up to 16 bytes per access.
+  // Pairs per unit: the widest that the sections, the strides and the alignment
+  // of every set allow, up to 16 bytes per access.
   const int rest = head_dim - rot;
-  int vec = 16 / elem / (interleaved ? 2 : 1);
+  bool copies = false;
+  int vec = most_pairs(elem, interleaved);
   auto fits = [&](int v) {
+    if (v == 1) return true;
     if (interleaved) {
-      if (v > 1 && head_dim % (2 * v)) return false;
+      if (head_dim % (2 * v)) return false;
     } else {
       for (int a = 0; a < n_axes; ++a)
         if ((dims[a] / 2) % v) return false;
-      if (v > 1 && rest % (2 * v)) return false;
+      if (rest % (2 * v)) return false;
     }
-    const int64_t bytes = (int64_t)v * elem * (interleaved && v > 1 ? 2 : 1);
+    const int64_t bytes = (int64_t)v * elem * (interleaved ? 2 : 1);
     for (int i = 0; i < n_sets; ++i) {
       const gs_heads& s = sets[i];
       if (!s.heads) continue;
@@ -247,8 +253,7 @@ extern "C" gs_status gs_rope(int64_t tokens, int32_t n_axes, const int32_t* dims
     }
     return true;
   };
-  while (vec > 1 && !fits(vec)) vec /= 2;
-  bool copies = false;
+  while (!fits(vec)) vec /= 2;
   for (int i = 0; i < n_sets; ++i) {
     const gs_heads& s = sets[i];
     if (!s.heads) continue;
@@ -256,36 +261,45 @@ extern "C" gs_status gs_rope(int64_t tokens, int32_t n_axes, const int32_t* dims
       return GS_ERR_INVALID_ARG;
     copies |= s.in != s.out;
   }
+
   RopeK k{};
   memcpy(k.turns, turns, sizeof(uint64_t) * (rot / 2));
   for (int a = 0; a < n_axes; ++a) k.dims[a] = dims[a];
   k.n_axes = n_axes;
   k.head_dim = head_dim;
-  k.pairs = rot / 2;
-  k.rot_units = (int)div_up(rot / 2, vec);
-  k.units = copies ? (int)div_up(head_dim, 2 * vec) : k.rot_units;
+  k.rot = rot;
   k.sign = inverse ? -1.f : 1.f;
-  const int rows = kThreads / k.units;  // (token, head slot) pairs of a block
-  int slots = (int)div_up(heads, elem == 2 && vec >= 4 ? kBatchOf<__half, 4> : 4);
-  k.head_slots = slots < rows ? slots : rows;
-  k.tokens_per_block = rows / k.head_slots;
-  const int threads = k.units * k.head_slots * k.tokens_per_block;
-  const int64_t blocks = div_up(tokens, k.tokens_per_block);
-  auto make = [&](const gs_heads& s) {
-    return HeadsK{(const char*)s.in, (char*)s.out, s.in_token * elem, s.in_head * elem,
-                  s.out_token * elem, s.out_head * elem};
-  };
-  const HeadsK s0 = make(sets[0]), s1 = make(sets[n_sets - 1]);
-  const dim3 grid((unsigned)blocks);
+  const int sms = device_sms();
+  HeadsK h[2] = {};
+  int n = 0, threads = 32;
+  int64_t blocks = 1;
+  for (int i = 0; i < n_sets; ++i) {
+    const gs_heads& s = sets[i];
+    if (!s.heads) continue;
+    HeadsK& d = h[n++];
+    d = HeadsK{(const char*)s.in, (char*)s.out, s.in_token * elem, s.in_head * elem,
+               s.out_token * elem, s.out_head * elem, s.heads, 0, 0, 0};
+    d.units = (int)div_up(copies ? head_dim : rot, 2 * vec);
+    const int rows = kThreads / d.units;  // (token, head slot) pairs of a block
+    d.slots = (int)div_up(s.heads, interleaved && elem == 2 && vec == 4 ? 2 : 4);  // as kBatchOf
+    if (d.slots > rows) d.slots = rows;
+    d.block_tokens = rows / d.slots;
+    const int64_t spread = div_up(tokens, sms);  // few tokens: use every SM
+    if (d.block_tokens > spread) d.block_tokens = (int)spread;
+    const int need = (int)div_up(d.units * d.slots * d.block_tokens, 32) * 32;
+    if (need > threads) threads = need;
+    const int64_t want = div_up(tokens, d.block_tokens);
+    if (want > blocks) blocks = want;
+  }
+  // blocks of both sets together: as many as run at once
+  const int64_t most = (int64_t)sms * (2048 / threads < 32 ? 2048 / threads : 32) / n;
+  if (blocks > most) blocks = most;
+  const dim3 grid((unsigned)blocks, n);
   cudaStream_t st = (cudaStream_t)stream;
-#define GS_ROPE(T)                                                                            \
-  do {                                                                                        \
-    if (interleaved)                                                                          \
-      rope_launch<T, true>(vec, grid, threads, tokens, k, s0, s1, sets[0].heads, (int)heads,  \
-                           positions, st);                                                    \
-    else                                                                                      \
-      rope_launch<T, false>(vec, grid, threads, tokens, k, s0, s1, sets[0].heads, (int)heads, \
-                            positions, st);                                                   \
+#define GS_ROPE(T)                                                                                 \
+  do {                                                                                             \
+    if (interleaved) rope_launch<T, true>(vec, grid, threads, tokens, k, h[0], h[1], positions, st); \
+    else rope_launch<T, false>(vec, grid, threads, tokens, k, h[0], h[1], positions, st);          \
   } while (0)
   if (dtype == GS_BF16) GS_ROPE(__nv_bfloat16);
   else if (dtype == GS_F16) GS_ROPE(__half);
