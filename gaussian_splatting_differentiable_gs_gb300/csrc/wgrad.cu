@@ -200,6 +200,8 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                : "memory");
 }
+// The thread sleeps until the phase ends, for 20 us at most: polling without that
+// took issue slots from the decoding warps (279 us instead of 252).
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -230,7 +232,6 @@ __device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, Co
   while (true) {
     if (mbar_try(bar, parity)) return true;
     if (c->abort) return false;
-    __nanosleep(50);
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t1));
     if (t1 - t0 > kWaitNs) {
       c->abort = 1;
@@ -530,7 +531,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (j < cols) tmem_add32(from + j, acc + j);
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(in_cta0(smem_u32(&c->acc_empty)));
+      if (lane == 0) mbar_arrive_pair(in_cta0(smem_u32(&c->acc_empty)));
       if (!w.segment_ends()) continue;
       const int n0 = w.n0 + c0, ch = w.ch0 + (int)rank * 128 + row;
       if (w.slot < 0) {
