@@ -9,10 +9,10 @@
 // columns.  dy is read as it lies ("MN-major": 64 neighbouring columns of one
 // token are one 128-byte row of a swizzled tile).  X8 goes to TMEM: an operand
 // there has a channel per lane and a pair of tokens per column, and it neither
-// has to be written to nor read from shared memory, whose bandwidth is what
-// bounds this product (with X8 as a second operand in shared memory a step of 64
-// tokens took 1200 cycles, 350 of them for writing and re-reading it, against
-// 512 of the tensor cores).
+// has to be written to nor read from shared memory, which would otherwise be the
+// bound: per step of 64 tokens an SM would move 80 KB or more through it (dy in
+// and out, the bytes in and out, X8 in and out), 640 cycles at 128 bytes each,
+// against 570 of the tensor cores.
 //
 // Warps of a CTA: one brings dy in by TMA, one the checkpoint's bytes (TMA), one
 // its exponents, eight turn the bytes into bf16 (exact: at most 8 significant
@@ -184,12 +184,10 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {  // shared::cluster address
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// On a barrier of the pair's first CTA, for an operand in this CTA's own TMEM:
-// the writers' waits and tcgen05 fences order it for the tensor core, so the
-// arrival need not order memory at cluster scope.
+// On a barrier of the pair's first CTA, for what this CTA did with its own TMEM:
+// the waits and tcgen05 fences around it order that for the tensor core, so the
+// arrival need not order memory at cluster scope (a release at that scope costs
+// the arriving warp several hundred cycles).
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -390,6 +388,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = c->tmem;
+  asm volatile("griddepcontrol.launch_dependents;");      // the join's blocks wait for this one's end
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // dy's terms, and all before, are there
 
   if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtrlRegs));
   if (warp == 0) {
@@ -473,7 +473,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const bool words = ((es | (int64_t)(uintptr_t)e) & 3) == 0;
     const uint32_t total = (uint32_t)cluster_steps(p, cluster);
     for (uint32_t it0 = 0; it0 < total; it0 += kBatch) {
-      uint32_t x[kBatch][2];  // four groups of tokens lane and lane + 32
+      uint32_t x[kBatch][2];  // four groups of tokens 2 lane and 2 lane + 1
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         x[i][0] = x[i][1] = 0x01010101u;
@@ -481,7 +481,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int g = w.ch0 / GS_ACT8_GROUP + (int)rank * 4;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int64_t t = (int64_t)w.ts * kBT + lane + 32 * h;
+          const int64_t t = (int64_t)w.ts * kBT + 2 * lane + h;
           if (t >= p.tokens) continue;
           const uint8_t* src = e + t * es + g;
           if (words && g + 4 <= groups) {
@@ -498,13 +498,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!__all_sync(0xffffffffu,
                       mbar_wait(smem_u32(&c->exp_empty[bs]), ((n / kBatches) & 1) ^ 1, c, status)))
         break;
-      uint16_t* to = reinterpret_cast<uint16_t*>(raw_e + bs * kBatch * kExpBytes) + lane;
+      uint32_t* to = reinterpret_cast<uint32_t*>(raw_e + bs * kBatch * kExpBytes) + lane;
 #pragma unroll
       for (int i = 0; i < kBatch; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)  // 2^(e - 127) in bf16; 255: infinity
-          to[i * 256 + (j & 3) * 64 + (j >> 2) * 32] =
-              (uint16_t)((x[i][j >> 2] >> 8 * (j & 3) & 0xffu) << 7);
+        for (int j = 0; j < 4; ++j)  // 2^(e - 127) in bf16, of two tokens; 255: infinity
+          to[i * 128 + j * 32] =
+              __byte_perm(x[i][0] >> 8 * j, x[i][1] >> 8 * j, 0x5410) << 7 & 0x7f807f80u;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&c->exp_full[bs]));
     }
@@ -552,9 +552,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else {
     // ---- bytes to bf16 -------------------------------------------------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDecodeRegs));
-    // kTeams teams of warps take the steps in turn: a step's waits, loads and
-    // fence then overlap with those of the next steps.  A thread's items are one
-    // token and one group of 32 channels each.
+    // kTeams teams of warps take the steps in turn: a step's waits and loads then
+    // overlap with the next one's (three or four teams, with fewer registers each,
+    // gain nothing: 32640 x 5632 x 1024 in 249 and 252 us, with two 248).
     //
     // A warp has a quarter of TMEM's lanes: 32 channels, one group.  Thread t takes
     // the word of channels 4 (t / 4) .. + 3 of tokens 4 (t % 4) .. + 3 of every 16,
@@ -636,6 +636,7 @@ template <typename TO>
 __global__ void __launch_bounds__(128) wgrad_join_kernel(const __grid_constant__ Plan p,
                                                          const float* __restrict__ partial,
                                                          TO* dw) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the products still run
   const int per_half = p.bn / 4;
   const int tile = blockIdx.x / (2 * per_half), rank = blockIdx.x / per_half % 2;
   const int col = blockIdx.x % per_half * 4 + (int)(threadIdx.x >> 5), in = threadIdx.x % 32 * 4;
@@ -670,6 +671,7 @@ template <typename T>
 __global__ void __launch_bounds__(256) wgrad_terms_kernel(int64_t tokens, int64_t padded, int rows,
                                                           int ld, int terms, const T* dy,
                                                           int64_t dys, __nv_bfloat16* out) {
+  asm volatile("griddepcontrol.launch_dependents;");
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t t = i / (ld / 2);
   const int n = (int)(i % (ld / 2)) * 2;
@@ -864,20 +866,32 @@ extern "C" gs_status gs_act8_wgrad(int64_t tokens, int32_t rows, int32_t channel
   if (p.quota < kMinSteps) p.quota = kMinSteps < p.steps ? kMinSteps : p.steps;
   const int used = p.waves ? clusters : (int)div_up(p.rem_steps, p.quota);
   unsigned int* status = (unsigned int*)((char*)workspace + kWsStatusOffset);
+  // Both kernels may start while the one before them still runs: their set-up
+  // overlaps with it, and they wait for its end before they touch memory.
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(2 * used);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
   if (out_dtype == GS_F32)
-    wgrad_kernel<float><<<2 * used, kThreads, kSmem, st>>>(p, map, qmap, e, e_stride,
-                                                           (float*)dw, partial, status);
+    GS_CUDA(cudaLaunchKernelEx(&cfg, wgrad_kernel<float>, p, map, qmap, e, e_stride, (float*)dw, partial, status));
   else
-    wgrad_kernel<__nv_bfloat16><<<2 * used, kThreads, kSmem, st>>>(
-        p, map, qmap, e, e_stride, (__nv_bfloat16*)dw, partial, status);
-  GS_CHECK_LAUNCH();
+    GS_CUDA(cudaLaunchKernelEx(&cfg, wgrad_kernel<__nv_bfloat16>, p, map, qmap, e, e_stride,
+                               (__nv_bfloat16*)dw, partial, status));
   if (p.rem_tiles && p.quota % p.steps != 0) {
-    const unsigned blocks = (unsigned)(p.rem_tiles * 2 * (p.bn / 4));
+    cfg.gridDim = dim3((unsigned)(p.rem_tiles * 2 * (p.bn / 4)));
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 0;
     if (out_dtype == GS_F32)
-      wgrad_join_kernel<float><<<blocks, 128, 0, st>>>(p, partial, (float*)dw);
+      GS_CUDA(cudaLaunchKernelEx(&cfg, wgrad_join_kernel<float>, p, (const float*)partial, (float*)dw));
     else
-      wgrad_join_kernel<__nv_bfloat16><<<blocks, 128, 0, st>>>(p, partial, (__nv_bfloat16*)dw);
-    GS_CHECK_LAUNCH();
+      GS_CUDA(cudaLaunchKernelEx(&cfg, wgrad_join_kernel<__nv_bfloat16>, p, (const float*)partial,
+                                 (__nv_bfloat16*)dw));
   }
   return GS_OK;
 }
