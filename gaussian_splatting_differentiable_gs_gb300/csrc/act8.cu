@@ -3,11 +3,18 @@
 //
 // 32 channels share a power-of-two step, so a value q * step is exact in bf16
 // and in fp32 and the choice of q is the same in every implementation.  All
-// four kernels are single passes bound by memory.  A lane has eight neighbouring
-// channels (a group is four lanes).  Where rows do not start on 16-byte
-// boundaries, a lane reads the aligned 16-byte granules that its channels touch
-// and shifts them into place; for stores a granule is put together from two
-// lanes, and only a run's two ends are written element by element.
+// four kernels are single passes.  A lane has eight neighbouring channels (a group
+// is four lanes).  Where rows start on 16-byte boundaries the kernels are bound by
+// memory (a gated unit of 32640 x 2816 bf16, both directions: 232 us, 6.4 TB/s).
+// Where they do not, a lane reads the aligned 16-byte granules that its channels
+// touch and shifts them into place; for stores a granule is put together from two
+// lanes, and only a run's two ends are written element by element.  That form is
+// bound by instructions (8160 x 1361 fp16: 78 us, of which storing is 20, the
+// checkpoints 14 and the error function 10).  Loads of single words in place of
+// granules: no change; a warp that walks along a row and keeps its last lane's
+// words, so that only rows' ends are split: 80 us.
+#include <type_traits>
+
 #include "net_common.cuh"
 
 namespace gs {
@@ -16,11 +23,12 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPer = 8;               // channels of a lane
 constexpr int kUnitsPerBlock = 2048;  // lanes' worth of work
-// Blocks an SM: 64 warps hide the memory latency of the aligned form (eight
-// blocks 246 us, six 250, five 261, four 275 for both directions of a gated unit
-// of 32640 x 2816 bf16); the other form needs more registers than that leaves.
+// Blocks an SM: 48 warps or more hide the memory latency of the aligned form (six
+// and eight blocks 232 us, five 242, four 259 for both directions of a gated unit
+// of 32640 x 2816 bf16); the other form needs more registers than that leaves
+// (8160 x 1361 fp16: five 78 us, four 80, six 95).
 template <bool WIDE>
-constexpr int kBlocks = WIDE ? 8 : 4;
+constexpr int kBlocks = WIDE ? 8 : 5;
 
 struct Act8K {
   int8_t* q;
@@ -35,26 +43,35 @@ struct RowsK {
   int32_t rows;  // rows per block
 };
 
+// The larger one; a NaN if there is one (whose bits, without the sign, are above
+// any number's).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+
 // Writes eight channels' bytes and, once per group, the exponent.  Every lane of
 // the warp calls it; lanes with c >= end store nothing.
 __device__ __forceinline__ void put8(const float (&v)[kPer], const Act8K& k, int64_t t, int c,
                                      int end) {
-  uint32_t mag = 0;
+  float top = fabsf(v[0]);
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) mag = max(mag, __float_as_uint(v[j]) & 0x7fffffffu);
+  for (int j = 1; j < kPer; ++j) top = max_nan(top, fabsf(v[j]));
+  uint32_t mag = __float_as_uint(top);
   mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
   mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
   if (c >= end) return;
   const uint32_t e = act8_exponent(mag);
   const float inv = act8_inverse(e);
+  const uint32_t keep = e == 255u ? 0u : 0xffffffffu;
   uint32_t w[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const uint32_t lo =
-        __byte_perm(act8_quantise(v[4 * h], inv, e), act8_quantise(v[4 * h + 1], inv, e), 0x0040);
-    const uint32_t hi = __byte_perm(act8_quantise(v[4 * h + 2], inv, e),
-                                    act8_quantise(v[4 * h + 3], inv, e), 0x0040);
-    w[h] = __byte_perm(lo, hi, 0x5410);
+    const uint32_t lo = __byte_perm(act8_round(v[4 * h], inv), act8_round(v[4 * h + 1], inv), 0x0040);
+    const uint32_t hi =
+        __byte_perm(act8_round(v[4 * h + 2], inv), act8_round(v[4 * h + 3], inv), 0x0040);
+    w[h] = __byte_perm(lo, hi, 0x5410) & keep;
   }
   *reinterpret_cast<uint2*>(k.q + t * k.qs + c) = make_uint2(w[0], w[1]);
   if (c % GS_ACT8_GROUP == 0) k.e[t * k.es + c / GS_ACT8_GROUP] = (uint8_t)e;
@@ -74,22 +91,24 @@ __device__ __forceinline__ float held8(const Held8& h, int j) {
   return act8_value((j < 4 ? h.q.x : h.q.y) ^ 0x80808080u, j & 3, act8_step(h.e));
 }
 
-// z shifted down by s bytes (0 <= s < 16, even).
+// The first N words of z (N + 4 words) shifted down by s bytes (0 <= s < 16, even).
 template <int N>
-__device__ __forceinline__ void shift_down(uint32_t (&z)[N], int s) {
+__device__ __forceinline__ void shift_down(uint32_t (&z)[N + 4], int s) {
 #pragma unroll
-  for (int i = 0; i + 2 < N; ++i) z[i] = s & 8 ? z[i + 2] : z[i];
+  for (int i = 0; i < N + 2; ++i) z[i] = s & 8 ? z[i + 2] : z[i];
 #pragma unroll
-  for (int i = 0; i + 1 < N; ++i) z[i] = s & 4 ? z[i + 1] : z[i];
+  for (int i = 0; i < N + 1; ++i) z[i] = s & 4 ? z[i + 1] : z[i];
+  const int bits = (s & 2) * 8;
 #pragma unroll
-  for (int i = 0; i + 1 < N; ++i) z[i] = s & 2 ? __funnelshift_r(z[i], z[i + 1], 16) : z[i];
+  for (int i = 0; i < N; ++i) z[i] = __funnelshift_r(z[i], z[i + 1], bits);
 }
 
-// A matrix whose rows start anywhere, or (WIDE) on 16-byte boundaries.
+// A matrix whose rows start anywhere, or (WIDE) on 16-byte boundaries.  `edge`:
+// that many first and last rows may lie within 16 bytes of the matrix' ends.
 template <typename T>
 struct Mat {
   T* p;
-  int64_t stride;
+  int64_t stride, edge;
 };
 
 // Element j of 32-bit words, and two values as a word (fp32: one).
@@ -111,49 +130,73 @@ __device__ __forceinline__ uint32_t bits_of(float v) { return __float_as_uint(v)
 __device__ __forceinline__ uint32_t bits_of(__nv_bfloat16 v) { return __bfloat16_as_ushort(v); }
 __device__ __forceinline__ uint32_t bits_of(__half v) { return __half_as_ushort(v); }
 
+// Two values as the words of their bits.
+template <typename T>
+__device__ __forceinline__ uint32_t pair_word(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pair_word<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pair_word<__half>(float a, float b) {
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <typename T>
+__device__ __forceinline__ void words_of(const float (&v)[kPer], uint32_t* w) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) w[j] = __float_as_uint(v[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kPer / 2; ++j) w[j] = pair_word<T>(v[2 * j], v[2 * j + 1]);
+  }
+}
+
 // Eight channels of a matrix from c on (zeros from C on); c < C.
 template <typename T, bool WIDE>
-struct Held;
-template <typename T>
-struct Held<T, true> {
-  Pack<T, kPer> w;
-  __device__ __forceinline__ void load(const Mat<const T>& m, const RowsK&, int64_t t, int c) {
-    w = load_pack<T, kPer>(m.p + t * m.stride + c);
-  }
-  __device__ __forceinline__ float value(const RowsK&, int, int j) const { return to_f32(w.v[j]); }
-};
-template <typename T>
-struct Held<T, false> {
+struct Held {
   static constexpr int kWords = kPer * sizeof(T) / 4;
-  uint32_t w[kWords + 4];
+  uint32_t w[kWords + (WIDE ? 0 : 4)];
   __device__ __forceinline__ void load(const Mat<const T>& m, const RowsK& r, int64_t t, int c) {
     const T* p = m.p + t * m.stride + c;
-    const int n = min(kPer, r.C - c) * (int)sizeof(T);
-    // granules reach up to 14 bytes out of the row: not out of the matrix
-    const int64_t apart = m.stride >= r.C ? m.stride * (int64_t)sizeof(T) : 0;
-    const bool inner = (c > 0 || t * apart >= 16) &&
-                       (c + 2 * kPer <= r.C || (r.tokens - 1 - t) * apart >= 16);
-    if (inner) {
-      const int d = (int)((uintptr_t)p & 15);
-      const char* g = (const char*)p - d;
+    if constexpr (WIDE) {
 #pragma unroll
-      for (int i = 0; i <= kWords / 4; ++i) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (16 * i < d + n) v = *reinterpret_cast<const uint4*>(g + 16 * i);
-        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
-      }
-      shift_down(w, d);
+      for (int i = 0; i < kWords; i += 4) granule(i, reinterpret_cast<const uint4*>(p) + i / 4);
     } else {
+      const int n = min(kPer, r.C - c) * (int)sizeof(T);
+      // granules reach up to 14 bytes out of the row: not out of the matrix
+      if ((c > 0 || t >= m.edge) && (c + 2 * kPer <= r.C || t < r.tokens - m.edge)) {
+        const int d = (int)((uintptr_t)p & 15);
+        const char* g = (const char*)p - d;
 #pragma unroll
-      for (int i = 0; i < kWords; ++i) w[i] = 0;
+        for (int i = 0; i < kWords + 4; i += 4) {
+          w[i] = w[i + 1] = w[i + 2] = w[i + 3] = 0;
+          if (4 * i < d + n) granule(i, reinterpret_cast<const uint4*>(g) + i / 4);
+        }
+        shift_down<kWords>(w, d);
+        if (n < 4 * kWords) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (c + i < r.C)
-          w[i * (int)sizeof(T) / 4] |= bits_of(p[i]) << (sizeof(T) == 2 && (i & 1) ? 16 : 0);
+          for (int i = 0; i < kWords; ++i)
+            w[i] = 4 * i + 4 <= n ? w[i] : 4 * i < n ? w[i] & 0xffffu : 0u;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          if (c + i < r.C)
+            w[i * (int)sizeof(T) / 4] |= bits_of(p[i]) << (sizeof(T) == 2 && (i & 1) ? 16 : 0);
+      }
     }
   }
-  __device__ __forceinline__ float value(const RowsK& r, int c, int j) const {
-    return c + j < r.C ? word_value<T>(w, j) : 0.f;
+  __device__ __forceinline__ float value(int j) const { return word_value<T>(w, j); }
+
+ private:
+  __device__ __forceinline__ void granule(int i, const uint4* g) {
+    const uint4 v = *g;
+    w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
   }
 };
 
@@ -162,25 +205,22 @@ struct Held<T, false> {
 template <typename T, bool WIDE>
 __device__ __forceinline__ void put(const float (&v)[kPer], const Mat<T>& m, const RowsK& r,
                                     int64_t t, int c, bool in) {
+  constexpr int kWords = kPer * sizeof(T) / 4;
   T* p = m.p + t * m.stride + c;
-  if (WIDE) {
+  if constexpr (WIDE) {
     if (in) {
-      Pack<T, kPer> w;
+      uint32_t w[kWords];
+      words_of<T>(v, w);
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) w.v[j] = from_f32<T>(v[j]);
-      store_pack<T, kPer>(p, w);
+      for (int i = 0; i < kWords; i += 4)
+        reinterpret_cast<uint4*>(p)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
     }
     return;
   }
-  constexpr int kWords = kPer * sizeof(T) / 4;
-  uint32_t w[kWords + 4];
-  T own[kPer];
+  uint32_t own[kWords], w[kWords + 4];
+  words_of<T>(v, own);
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) own[j] = from_f32<T>(v[j]);
-#pragma unroll
-  for (int i = 0; i < kWords; ++i)
-    w[4 + i] = sizeof(T) == 4 ? bits_of(own[i])
-                              : bits_of(own[2 * i % kPer]) | bits_of(own[(2 * i + 1) % kPer]) << 16;
+  for (int i = 0; i < kWords; ++i) w[4 + i] = own[i];
 #pragma unroll
   for (int i = 0; i < 4; ++i) w[i] = __shfl_up_sync(0xffffffffu, w[kWords + i], 1);
   if (!in) return;
@@ -191,10 +231,10 @@ __device__ __forceinline__ void put(const float (&v)[kPer], const Mat<T>& m, con
   const bool prev = lane > 0 && c > 0;
   const bool next = lane < 31 && min(kPer, r.C - c - kPer) * (int)sizeof(T) >= 16 - d;
   if (d) {
-    shift_down(w, 16 - d);
+    shift_down<kWords>(w, 16 - d);
   } else {
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = w[4 + i];
+    for (int i = 0; i < kWords; ++i) w[i] = own[i];
   }
   char* g = (char*)p - d;  // granule i: bytes [16 i, 16 i + 16) from here
   int lo = 0, hi = next ? n : min(n, 4 * kWords - d);  // own bytes [0, lo), [hi, n): one by one
@@ -210,10 +250,12 @@ __device__ __forceinline__ void put(const float (&v)[kPer], const Mat<T>& m, con
     }
   }
   if (lo > 0 || hi < n) {
+    using U = typename std::conditional<sizeof(T) == 4, uint32_t, uint16_t>::type;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int b = j * (int)sizeof(T);
-      if (b < n && (b < lo || b >= hi)) p[j] = own[j];
+      if (b < n && (b < lo || b >= hi))
+        reinterpret_cast<U*>(p)[j] = (U)(own[b / 4] >> (b % 4 * 8));
     }
   }
 }
@@ -227,9 +269,13 @@ __device__ __forceinline__ void each_unit(const RowsK& r, F f) {
   const int n = r.upr * (int)min((int64_t)r.rows, r.tokens - row0);
   const int end = (r.C + GS_ACT8_GROUP - 1) / GS_ACT8_GROUP * GS_ACT8_GROUP;
   const int lane = threadIdx.x & 31;
+  const int rows = kThreads / r.upr, units = kThreads - rows * r.upr;  // of one step
+  int row = (int)threadIdx.x / r.upr, unit = (int)threadIdx.x - row * r.upr;
   for (int at = threadIdx.x; at - lane < n; at += kThreads) {
-    const int row = at / r.upr;
-    f(row0 + row, (at - row * r.upr) * kPer, at < n ? end : 0);
+    f(row0 + row, unit * kPer, at < n ? end : 0);
+    row += rows;
+    unit += units;
+    if (unit >= r.upr) unit -= r.upr, ++row;
   }
 }
 
@@ -242,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<WIDE>)
       Held<T, WIDE> h;
       h.load(x, r, t, c);
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) v[j] = h.value(r, c, j);
+      for (int j = 0; j < kPer; ++j) v[j] = h.value(j);
     }
     put8(v, k, t, c, end);
   });
@@ -263,6 +309,19 @@ __global__ void __launch_bounds__(kThreads, kBlocks<WIDE>)
   });
 }
 
+// 2^v and 1 / v as the hardware's single instructions; results and arguments below
+// 2^-126 count as zero, which is below the error of every use here.
+__device__ __forceinline__ float power2(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float reciprocal(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 // act(v) and its derivative.  Phi comes from Abramowitz and Stegun's formula
 // 7.1.26 for the error function (absolute error below 1.5e-7, half of that in
 // Phi), which needs the one exponential that the derivative has too.
@@ -271,8 +330,8 @@ struct Phi {
 };
 __device__ __forceinline__ Phi normal(float v) {
   const float z = fabsf(v) * 0.70710678118654752f;
-  const float t = __fdividef(1.f, fmaf(0.3275911f, z, 1.f));
-  const float ex = __expf(-z * z);
+  const float t = reciprocal(fmaf(0.3275911f, z, 1.f));
+  const float ex = power2(z * z * -1.4426950408889634f);
   float q = fmaf(1.061405429f, t, -1.453152027f);
   q = fmaf(q, t, 1.421413741f);
   q = fmaf(q, t, -0.284496736f);
@@ -280,15 +339,17 @@ __device__ __forceinline__ Phi normal(float v) {
   const float tail = 0.5f * q * t * ex;
   return Phi{v < 0.f ? tail : 1.f - tail, ex * 0.39894228040143268f};
 }
+__device__ __forceinline__ float sigmoid(float v) {
+  return reciprocal(1.f + power2(v * -1.4426950408889634f));
+}
 template <int ACT>
 __device__ __forceinline__ float act_value(float v) {
-  if (ACT == GS_ACT_SILU) return __fdividef(v, 1.f + __expf(-v));
-  return v * normal(v).p;
+  return v * (ACT == GS_ACT_SILU ? sigmoid(v) : normal(v).p);
 }
 template <int ACT>
 __device__ __forceinline__ void act_both(float v, float& f, float& df) {
   if (ACT == GS_ACT_SILU) {
-    const float s = __fdividef(1.f, 1.f + __expf(-v));
+    const float s = sigmoid(v);
     f = v * s;
     df = s * (1.f + v * (1.f - s));
   } else {
@@ -310,8 +371,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks<WIDE>)
       if (GATED) hu.load(up, r, t, c);
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
-        g[j] = hg.value(r, c, j);
-        if (GATED) u[j] = hu.value(r, c, j);
+        g[j] = hg.value(j);
+        if (GATED) u[j] = hu.value(j);
         o[j] = act_value<ACT>(g[j]) * (GATED ? u[j] : 1.f);
       }
       if (WIDE) put<T, WIDE>(o, h, r, t, c, in);
@@ -337,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<WIDE>)
       for (int j = 0; j < kPer; ++j) {
         float f, df;
         act_both<ACT>(held8(hg, j), f, df);
-        const float w = GATED ? held8(hu, j) : 1.f, d = hd.value(r, c, j);
+        const float w = GATED ? held8(hu, j) : 1.f, d = hd.value(j);
         o[j] = WIDE || c + j < r.C ? f * w : 0.f;
         dg[j] = d * w * df;
         du[j] = d * f;
@@ -376,6 +437,12 @@ Act8K ckpt_of(const gs_ckpt* c) {
   return c ? Act8K{c->q, c->e, c->q_stride, c->e_stride} : Act8K{nullptr, nullptr, 0, 0};
 }
 
+template <typename T>
+Mat<T> mat_of(T* p, int64_t stride, int32_t C) {
+  const int64_t apart = stride >= C ? stride * (int64_t)sizeof(T) : 0;
+  return {p, stride, apart ? div_up(16, apart) : (int64_t)1 << 31};
+}
+
 #define GS_ACT8_TYPES(dtype, ...)                     \
   do {                                                \
     if ((dtype) == GS_BF16) {                         \
@@ -406,7 +473,7 @@ extern "C" gs_status gs_act8_encode(int64_t tokens, int32_t channels, int32_t dt
   const bool wide = channels % 8 == 0 && rows_aligned(x, x_stride, el, 16);
   const RowsK r = make_rows(tokens, channels);
   cudaStream_t st = (cudaStream_t)stream;
-  GS_ACT8_TYPES(dtype, const Mat<const T> m{(const T*)x, x_stride};
+  GS_ACT8_TYPES(dtype, const Mat<const T> m = mat_of((const T*)x, x_stride, channels);
                 if (wide) encode_kernel<T, true><<<blocks_of(r), kThreads, 0, st>>>(r, m, k);
                 else encode_kernel<T, false><<<blocks_of(r), kThreads, 0, st>>>(r, m, k));
   GS_CHECK_LAUNCH();
@@ -424,7 +491,7 @@ extern "C" gs_status gs_act8_decode(int64_t tokens, int32_t channels, int32_t dt
   const bool wide = channels % 8 == 0 && rows_aligned(x, x_stride, el, 16);
   const RowsK r = make_rows(tokens, channels);
   cudaStream_t st = (cudaStream_t)stream;
-  GS_ACT8_TYPES(dtype, const Mat<T> m{(T*)x, x_stride};
+  GS_ACT8_TYPES(dtype, const Mat<T> m = mat_of((T*)x, x_stride, channels);
                 if (wide) decode_kernel<T, true><<<blocks_of(r), kThreads, 0, st>>>(r, k, m);
                 else decode_kernel<T, false><<<blocks_of(r), kThreads, 0, st>>>(r, k, m));
   GS_CHECK_LAUNCH();
@@ -447,15 +514,17 @@ extern "C" gs_status gs_glu_fwd(int64_t tokens, int32_t channels, int32_t dtype,
                     rows_aligned(up, up_stride, el, 16) && rows_aligned(h, h_stride, el, 16);
   const RowsK r = make_rows(tokens, channels);
   cudaStream_t st = (cudaStream_t)stream;
-#define GS_GLU(WIDE, ACT)                                                                   \
-  do {                                                                                      \
-    if (up)                                                                                 \
-      glu_fwd_kernel<T, WIDE, ACT, true><<<blocks_of(r), kThreads, 0, st>>>(                \
-          r, {(const T*)gate, gate_stride}, {(const T*)up, up_stride}, {(T*)h, h_stride},   \
-          g8, u8);                                                                          \
-    else                                                                                    \
-      glu_fwd_kernel<T, WIDE, ACT, false><<<blocks_of(r), kThreads, 0, st>>>(               \
-          r, {(const T*)gate, gate_stride}, {}, {(T*)h, h_stride}, g8, u8);                 \
+#define GS_GLU(WIDE, ACT)                                                                    \
+  do {                                                                                       \
+    const Mat<const T> mg = mat_of((const T*)gate, gate_stride, channels);                   \
+    const Mat<const T> mu = mat_of((const T*)up, up_stride, channels);                       \
+    const Mat<T> mh = mat_of((T*)h, h_stride, channels);                                     \
+    if (up)                                                                                  \
+      glu_fwd_kernel<T, WIDE, ACT, true><<<blocks_of(r), kThreads, 0, st>>>(r, mg, mu, mh, g8, \
+                                                                            u8);             \
+    else                                                                                     \
+      glu_fwd_kernel<T, WIDE, ACT, false><<<blocks_of(r), kThreads, 0, st>>>(r, mg, mu, mh,  \
+                                                                             g8, u8);        \
   } while (0)
   GS_ACT8_TYPES(dtype, if (act == GS_ACT_SILU) {
     if (wide) GS_GLU(true, GS_ACT_SILU); else GS_GLU(false, GS_ACT_SILU);
@@ -484,15 +553,17 @@ extern "C" gs_status gs_glu_bwd(int64_t tokens, int32_t channels, int32_t dtype,
                     rows_aligned(dup, dup_stride, el, 16);
   const RowsK r = make_rows(tokens, channels);
   cudaStream_t st = (cudaStream_t)stream;
-#define GS_GLU(WIDE, ACT)                                                                   \
-  do {                                                                                      \
-    if (dup)                                                                                \
-      glu_bwd_kernel<T, WIDE, ACT, true><<<blocks_of(r), kThreads, 0, st>>>(                \
-          r, g8, u8, {(const T*)dh, dh_stride}, {(T*)dgate, dgate_stride},                  \
-          {(T*)dup, dup_stride}, o8);                                                       \
-    else                                                                                    \
-      glu_bwd_kernel<T, WIDE, ACT, false><<<blocks_of(r), kThreads, 0, st>>>(               \
-          r, g8, u8, {(const T*)dh, dh_stride}, {(T*)dgate, dgate_stride}, {}, o8);         \
+#define GS_GLU(WIDE, ACT)                                                                    \
+  do {                                                                                       \
+    const Mat<const T> md = mat_of((const T*)dh, dh_stride, channels);                       \
+    const Mat<T> mg = mat_of((T*)dgate, dgate_stride, channels);                             \
+    const Mat<T> mu = mat_of((T*)dup, dup_stride, channels);                                 \
+    if (dup)                                                                                 \
+      glu_bwd_kernel<T, WIDE, ACT, true><<<blocks_of(r), kThreads, 0, st>>>(r, g8, u8, md, mg, \
+                                                                            mu, o8);         \
+    else                                                                                     \
+      glu_bwd_kernel<T, WIDE, ACT, false><<<blocks_of(r), kThreads, 0, st>>>(r, g8, u8, md,  \
+                                                                             mg, mu, o8);    \
   } while (0)
   GS_ACT8_TYPES(dtype, if (act == GS_ACT_SILU) {
     if (wide) GS_GLU(true, GS_ACT_SILU); else GS_GLU(false, GS_ACT_SILU);

@@ -77,11 +77,14 @@ __device__ __forceinline__ float act8_inverse(uint32_t e) {
 // such a group reads back as.
 __device__ __forceinline__ float act8_step(uint32_t e) { return __uint_as_float(e << 23); }
 
-// q in the low byte of the result: v * inv is exact (a power of two), and adding
-// 1.5 * 2^23 rounds it to the nearest whole number, ties to even.
+// q in the low byte of the result (anything where v is not finite): v * inv is exact
+// (a power of two), and adding 1.5 * 2^23 rounds it to the nearest whole number, ties
+// to even.
+__device__ __forceinline__ uint32_t act8_round(float v, float inv) {
+  return __float_as_uint(__fmaf_rn(v, inv, 12582912.f));
+}
 __device__ __forceinline__ uint32_t act8_quantise(float v, float inv, uint32_t e) {
-  const uint32_t q = __float_as_uint(__fmaf_rn(v, inv, 12582912.f));
-  return e == 255u ? 0u : q;
+  return e == 255u ? 0u : act8_round(v, inv);
 }
 // The value of byte `i` of a word of checkpoint bytes, times the step: the byte
 // (its sign bit flipped) is put into the significand of 2^23 + 128 + q.
