@@ -5,14 +5,14 @@
 // and in fp32 and the choice of q is the same in every implementation.  All
 // four kernels are single passes.  A lane has eight neighbouring channels (a group
 // is four lanes).  Where rows start on 16-byte boundaries the kernels are bound by
-// memory (a gated unit of 32640 x 2816 bf16, both directions: 232 us, 6.4 TB/s).
+// memory (a gated unit of 32640 x 2816 bf16, both directions: 229 us, 6.5 TB/s).
 // Where they do not, a lane reads the aligned 16-byte granules that its channels
 // touch and shifts them into place; for stores a granule is put together from two
 // lanes, and only a run's two ends are written element by element.  That form is
-// bound by instructions (8160 x 1361 fp16: 78 us, of which storing is 20, the
+// bound by instructions (8160 x 1361 fp16: 75 us, of which storing is 20, the
 // checkpoints 14 and the error function 10).  Loads of single words in place of
 // granules: no change; a warp that walks along a row and keeps its last lane's
-// words, so that only rows' ends are split: 80 us.
+// words, so that only rows' ends are split: 2 us more.
 #include <type_traits>
 
 #include "net_common.cuh"
@@ -25,7 +25,7 @@ constexpr int kPer = 8;               // channels of a lane
 constexpr int kUnitsPerBlock = 2048;  // lanes' worth of work
 // Blocks an SM: 48 warps or more hide the memory latency of the aligned form (six
 // and eight blocks 232 us, five 242, four 259 for both directions of a gated unit
-// of 32640 x 2816 bf16); the other form needs more registers than that leaves
+// of 32640 x 2816 bf16, launches not overlapped); the other form needs more registers than that leaves
 // (8160 x 1361 fp16: five 78 us, four 80, six 95).
 template <bool WIDE>
 constexpr int kBlocks = WIDE ? 8 : 5;
@@ -265,6 +265,8 @@ __device__ __forceinline__ void put(const float (&v)[kPer], const Mat<T>& m, con
 // warps take part in each step.
 template <typename F>
 __device__ __forceinline__ void each_unit(const RowsK& r, F f) {
+  launch_dependents();
+  wait_for_previous();
   const int64_t row0 = (int64_t)blockIdx.x * r.rows;
   const int n = r.upr * (int)min((int64_t)r.rows, r.tokens - row0);
   const int end = (r.C + GS_ACT8_GROUP - 1) / GS_ACT8_GROUP * GS_ACT8_GROUP;
@@ -474,9 +476,8 @@ extern "C" gs_status gs_act8_encode(int64_t tokens, int32_t channels, int32_t dt
   const RowsK r = make_rows(tokens, channels);
   cudaStream_t st = (cudaStream_t)stream;
   GS_ACT8_TYPES(dtype, const Mat<const T> m = mat_of((const T*)x, x_stride, channels);
-                if (wide) encode_kernel<T, true><<<blocks_of(r), kThreads, 0, st>>>(r, m, k);
-                else encode_kernel<T, false><<<blocks_of(r), kThreads, 0, st>>>(r, m, k));
-  GS_CHECK_LAUNCH();
+                GS_CUDA(launch_overlapped(wide ? encode_kernel<T, true> : encode_kernel<T, false>,
+                                          blocks_of(r), kThreads, 0, st, r, m, k)));
   return GS_OK;
 }
 
@@ -492,9 +493,8 @@ extern "C" gs_status gs_act8_decode(int64_t tokens, int32_t channels, int32_t dt
   const RowsK r = make_rows(tokens, channels);
   cudaStream_t st = (cudaStream_t)stream;
   GS_ACT8_TYPES(dtype, const Mat<T> m = mat_of((T*)x, x_stride, channels);
-                if (wide) decode_kernel<T, true><<<blocks_of(r), kThreads, 0, st>>>(r, k, m);
-                else decode_kernel<T, false><<<blocks_of(r), kThreads, 0, st>>>(r, k, m));
-  GS_CHECK_LAUNCH();
+                GS_CUDA(launch_overlapped(wide ? decode_kernel<T, true> : decode_kernel<T, false>,
+                                          blocks_of(r), kThreads, 0, st, r, k, m)));
   return GS_OK;
 }
 
@@ -519,12 +519,9 @@ extern "C" gs_status gs_glu_fwd(int64_t tokens, int32_t channels, int32_t dtype,
     const Mat<const T> mg = mat_of((const T*)gate, gate_stride, channels);                   \
     const Mat<const T> mu = mat_of((const T*)up, up_stride, channels);                       \
     const Mat<T> mh = mat_of((T*)h, h_stride, channels);                                     \
-    if (up)                                                                                  \
-      glu_fwd_kernel<T, WIDE, ACT, true><<<blocks_of(r), kThreads, 0, st>>>(r, mg, mu, mh, g8, \
-                                                                            u8);             \
-    else                                                                                     \
-      glu_fwd_kernel<T, WIDE, ACT, false><<<blocks_of(r), kThreads, 0, st>>>(r, mg, mu, mh,  \
-                                                                             g8, u8);        \
+    GS_CUDA(launch_overlapped(up ? glu_fwd_kernel<T, WIDE, ACT, true>                        \
+                                  : glu_fwd_kernel<T, WIDE, ACT, false>,                     \
+                              blocks_of(r), kThreads, 0, st, r, mg, mu, mh, g8, u8));        \
   } while (0)
   GS_ACT8_TYPES(dtype, if (act == GS_ACT_SILU) {
     if (wide) GS_GLU(true, GS_ACT_SILU); else GS_GLU(false, GS_ACT_SILU);
@@ -532,7 +529,6 @@ extern "C" gs_status gs_glu_fwd(int64_t tokens, int32_t channels, int32_t dtype,
     if (wide) GS_GLU(true, GS_ACT_GELU); else GS_GLU(false, GS_ACT_GELU);
   });
 #undef GS_GLU
-  GS_CHECK_LAUNCH();
   return GS_OK;
 }
 
@@ -558,12 +554,9 @@ extern "C" gs_status gs_glu_bwd(int64_t tokens, int32_t channels, int32_t dtype,
     const Mat<const T> md = mat_of((const T*)dh, dh_stride, channels);                       \
     const Mat<T> mg = mat_of((T*)dgate, dgate_stride, channels);                             \
     const Mat<T> mu = mat_of((T*)dup, dup_stride, channels);                                 \
-    if (dup)                                                                                 \
-      glu_bwd_kernel<T, WIDE, ACT, true><<<blocks_of(r), kThreads, 0, st>>>(r, g8, u8, md, mg, \
-                                                                            mu, o8);         \
-    else                                                                                     \
-      glu_bwd_kernel<T, WIDE, ACT, false><<<blocks_of(r), kThreads, 0, st>>>(r, g8, u8, md,  \
-                                                                             mg, mu, o8);    \
+    GS_CUDA(launch_overlapped(dup ? glu_bwd_kernel<T, WIDE, ACT, true>                       \
+                                   : glu_bwd_kernel<T, WIDE, ACT, false>,                    \
+                              blocks_of(r), kThreads, 0, st, r, g8, u8, md, mg, mu, o8));    \
   } while (0)
   GS_ACT8_TYPES(dtype, if (act == GS_ACT_SILU) {
     if (wide) GS_GLU(true, GS_ACT_SILU); else GS_GLU(false, GS_ACT_SILU);
@@ -571,6 +564,5 @@ extern "C" gs_status gs_glu_bwd(int64_t tokens, int32_t channels, int32_t dtype,
     if (wide) GS_GLU(true, GS_ACT_GELU); else GS_GLU(false, GS_ACT_GELU);
   });
 #undef GS_GLU
-  GS_CHECK_LAUNCH();
   return GS_OK;
 }

@@ -276,9 +276,10 @@ __device__ __forceinline__ void team_sums(Team& team, float (&part)[2], bool cen
 }
 
 // Work of a CTA: rows [cta R, cta R + R), cut at the groups' ends; its teams
-// take them in turn; the backward keeps its column sums in registers.  A thread has up to 32 (backward: 16) channels of a row, so that what
-// a row costs by itself (sums over the team, addresses) is spread over many: with
-// 8 the forward took 283 instructions per 8 x 32 channels and was bound by them.
+// take them in turn; the backward keeps its column sums in registers.  A thread has
+// up to 32 (backward: 16) channels of a row, so that what a row costs by itself
+// (sums over the team, addresses) is spread over many: with 8 the forward took 283
+// instructions per 8 x 32 channels and was bound by them.
 struct Range {
   int64_t begin, end;
 };
@@ -308,6 +309,7 @@ __global__ void __launch_bounds__(kTeamThreads, 1) norm_fwd_kernel(
   const int lanes = warps * 32, lane = threadIdx.x - tm * lanes;
   const int first = lane * VEC, step = warps * 32 * VEC;
 
+  launch_dependents();
   const Range rows = cta_rows(k, rows_per_cta);
   const RX rx{x, x_stride};
   const RB rb{block, block_stride};
@@ -322,6 +324,7 @@ __global__ void __launch_bounds__(kTeamThreads, 1) norm_fwd_kernel(
   };
   clear_shared(smem, depth * slot_bytes, depth * slot_bytes + teams * kRedFloats * (int)sizeof(float),
                !RX::kOwn || (block && k.C == VEC * NV * lanes));
+  wait_for_previous();
   for (int i = 0; i < depth; ++i) ask(i);
 
   Weights<VEC, NV>::fill(w_pre, k.C, lanes,
@@ -431,7 +434,7 @@ __global__ void __launch_bounds__(kTeamThreads, 1) norm_bwd_kernel(
   const int lanes = warps * 32, lane = threadIdx.x - tm * lanes;
   const int first = lane * VEC, step = warps * 32 * VEC;
 
-  asm volatile("griddepcontrol.launch_dependents;");  // the sums' kernel waits for this one's end
+  launch_dependents();
   const Range rows = cta_rows(k, rows_per_cta);
   const RX rx{dy ? x : nullptr, x_stride}, rd{dx_out, dx_out_stride};
   const RB rb{block, block_stride}, ry{dy, dy_stride};
@@ -449,6 +452,7 @@ __global__ void __launch_bounds__(kTeamThreads, 1) norm_bwd_kernel(
   };
   clear_shared(smem, depth * slot_bytes, depth * slot_bytes + teams * kRedFloats * (int)sizeof(float),
                !RX::kOwn || (block && dy && dx_out && k.C == VEC * NV * lanes));
+  wait_for_previous();
   for (int i = 0; i < depth; ++i) ask(i);
   float4 st_next = make_float4(0.f, 0.f, 0.f, 0.f);
   if (rows.begin + tm < rows.end) st_next = stats[rows.begin + tm];
@@ -579,7 +583,7 @@ __global__ void __launch_bounds__(1024) norm_sums_kernel(const __grid_constant__
                                                          float* dgate, float* dscale) {
   __shared__ float red[32][33], red2[32][33];
   const int x = threadIdx.x, y = threadIdx.y;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the row kernel still runs
+  launch_dependents();
   const int c = blockIdx.x * 32 + x;
   const bool in = c < k.C;
   auto slots = [&](const float* p, int lo, int hi, int from, int by) {
@@ -600,41 +604,51 @@ __global__ void __launch_bounds__(1024) norm_sums_kernel(const __grid_constant__
   };
   if (blockIdx.y == 0) {  // dw_pre's blocks
     if (!dw_pre) return;
+    wait_for_previous();
     red[y][x] = slots(part_pre, 0, ctas, y, 32);
     join(red, dw_pre);
     return;
   }
+  // What is not the row kernel's is read while that still runs: it began after all
+  // that came before.
   const float w = in && k.w_post ? k.w_post[c] : 1.f;
   const float sc = in && k.scale ? k.scale[c] : 1.f;
+  int64_t lo = 0, hi = 0;  // rows of the group whose slots this warp adds up
+  float gv = 1.f;          // gate of the group that it joins
+  auto ahead = [&](int g0) {
+    const int n = min(32, k.groups - g0), per = 32 / n, g = g0 + y / per;
+    lo = 0, hi = y < n * per ? k.tokens : 0;
+    if (k.offsets && y < n * per) {
+      lo = max(lo, (int64_t)k.offsets[g]);
+      hi = min(hi, (int64_t)k.offsets[g + 1]);
+    }
+    if (y < n && in && k.gate) {
+      const int64_t at = (int64_t)(g0 + y) * k.C + c;
+      gv = gate_dtype == GS_F32    ? ((const float*)k.gate)[at]
+           : gate_dtype == GS_BF16 ? to_f32(((const __nv_bfloat16*)k.gate)[at])
+                                   : to_f32(((const __half*)k.gate)[at]);
+    }
+  };
+  ahead(0);
+  wait_for_previous();
   float post = 0.f, scale = 0.f;
   for (int g0 = 0; g0 < k.groups; g0 += 32) {
-    const int n = min(32, k.groups - g0), per = 32 / n;
-    const int g = g0 + y / per;
+    const int n = min(32, k.groups - g0), per = 32 / n, g = g0 + y / per;
     float e = 0.f;
-    if (y < n * per) {
-      const int64_t lo = max((int64_t)0, (int64_t)(k.offsets ? k.offsets[g] : 0));
-      const int64_t hi = min(k.tokens, k.offsets ? (int64_t)k.offsets[g + 1] : k.tokens);
-      if (lo < hi)
-        e = slots(part_e, (int)(lo / rows_per_cta) + g, (int)((hi - 1) / rows_per_cta) + g + 1,
-                  y % per, per);
-    }
+    if (lo < hi)
+      e = slots(part_e, (int)(lo / rows_per_cta) + g, (int)((hi - 1) / rows_per_cta) + g + 1,
+                y % per, per);
     __syncthreads();
     red[y][x] = e;
     __syncthreads();
     if (y < n) {  // one warp a group
       e = 0.f;
       for (int i = 0; i < per; ++i) e += red[y * per + i][x];
-      float gv = 1.f;
-      if (in && k.gate) {
-        const int64_t at = (int64_t)(g0 + y) * k.C + c;
-        gv = gate_dtype == GS_F32    ? ((const float*)k.gate)[at]
-             : gate_dtype == GS_BF16 ? to_f32(((const __nv_bfloat16*)k.gate)[at])
-                                     : to_f32(((const __half*)k.gate)[at]);
-      }
       post += sc * gv * e;
       scale += gv * w * e;
       if (in && dgate) dgate[(int64_t)(g0 + y) * k.C + c] = sc * w * e;
     }
+    if (g0 + 32 < k.groups) ahead(g0 + 32);
   }
   __syncthreads();
   red[y][x] = post;
@@ -756,10 +770,9 @@ cudaError_t fwd_launch(const FwdArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   int64_t rows = 0;
   const int64_t ctas = norm_ranges(a.k.tokens, l.s.teams, &rows);
-  kernel<<<(unsigned)ctas, l.s.threads, l.smem, st>>>(
-      a.k, (const TX*)a.x, a.xs, (const TB*)a.block, a.bs, (TX*)a.x_out, a.xos, (TB*)a.y, a.ys,
-      a.stats, a.y_q, a.qs, a.y_e, a.es, rows, l.s.warps, l.depth);
-  return cudaSuccess;
+  return launch_overlapped(kernel, (unsigned)ctas, l.s.threads, l.smem, st, a.k, (const TX*)a.x,
+                           a.xs, (const TB*)a.block, a.bs, (TX*)a.x_out, a.xos, (TB*)a.y, a.ys,
+                           a.stats, a.y_q, a.qs, a.y_e, a.es, rows, l.s.warps, l.depth);
 }
 
 template <typename TB, typename TX, int VEC>
@@ -800,11 +813,10 @@ cudaError_t bwd_launch(BwdArgs& a, cudaStream_t st) {
   const cudaError_t e = allow_smem(kernel, known);
   if (e != cudaSuccess) return e;
   a.ctas = (int)norm_ranges(a.k.tokens, l.s.teams, &a.rows_per_cta);
-  kernel<<<(unsigned)a.ctas, l.s.threads, l.smem, st>>>(
-      a.k, (const TX*)a.x, a.xs, (const TB*)a.block, a.bs, a.stats, (const TX*)a.dx_out, a.dxos,
-      (const TB*)a.dy, a.dys, (TX*)a.dx, a.dxs, (TB*)a.dblock, a.dbs, a.part_pre, a.part_e,
-      a.rows_per_cta, l.s.warps, l.depth);
-  return cudaSuccess;
+  return launch_overlapped(kernel, (unsigned)a.ctas, l.s.threads, l.smem, st, a.k, (const TX*)a.x,
+                           a.xs, (const TB*)a.block, a.bs, a.stats, (const TX*)a.dx_out, a.dxos,
+                           (const TB*)a.dy, a.dys, (TX*)a.dx, a.dxs, (TB*)a.dblock, a.dbs,
+                           a.part_pre, a.part_e, a.rows_per_cta, l.s.warps, l.depth);
 }
 
 // 16 channels a thread where rows are aligned and that wide (32640 x 1024 bf16: 85 us,
@@ -855,7 +867,6 @@ extern "C" gs_status gs_gated_norm_fwd(const gs_norm* p, const void* x, int64_t 
                   y_stride, (float4*)stats, y_q, q_stride, y_e, e_stride};
   cudaStream_t st = (cudaStream_t)stream;
   GS_CUDA(GS_NORM_TYPES(p, fwd_types, a, wide, st));
-  GS_CHECK_LAUNCH();
   return GS_OK;
 }
 
@@ -898,24 +909,13 @@ extern "C" gs_status gs_gated_norm_bwd(
   if (need_e && block) a.part_e = (float*)workspace + (size_t)kNormCtas * p->channels;
   if (p->tokens > 0) {
     GS_CUDA(GS_NORM_TYPES(p, bwd_types, a, wide, st));
-    GS_CHECK_LAUNCH();
   } else {
     a.part_pre = a.part_e = nullptr;
   }
   if (dw_pre || need_e) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)div_up(p->channels, 32), need_e ? 2 : 1);
-    cfg.blockDim = dim3(32, 32);
-    cfg.stream = st;
-    cudaLaunchAttribute early{};
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
-    GS_CUDA(cudaLaunchKernelEx(&cfg, norm_sums_kernel, a.k, p->dtype, (const float*)a.part_pre,
-                               (const float*)a.part_e, a.rows_per_cta, a.ctas, dw_pre, dw_post, dgate,
-                               dres_scale));
-    GS_CHECK_LAUNCH();
+    GS_CUDA(launch_overlapped(norm_sums_kernel, dim3((unsigned)div_up(p->channels, 32), need_e ? 2 : 1),
+                              dim3(32, 32), 0, st, a.k, p->dtype, a.part_pre, a.part_e,
+                              a.rows_per_cta, a.ctas, dw_pre, dw_post, dgate, dres_scale));
   }
   return GS_OK;
 }

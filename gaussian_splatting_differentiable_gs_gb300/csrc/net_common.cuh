@@ -51,6 +51,34 @@ inline bool rows_aligned(const void* p, int64_t stride, int elem, size_t bytes) 
   return !p || (aligned_to(p, bytes) && (stride * elem) % (int64_t)bytes == 0);
 }
 
+// Kernels that begin while the one before on their stream ends: launched by
+// launch_overlapped, a kernel touches global memory only after wait_for_previous,
+// which returns when that kernel and all before it have ended and their writes are
+// there.  launch_dependents lets the next one be set up.  Back to back on 32640 x
+// 1024 in bf16, the norms take 50.8 us forward and 82.2 us backward, and 53.2 and
+// 84.6 us without it.
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;");
+}
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
+                              cudaStream_t stream, A... args) {
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 inline int device_sms() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||

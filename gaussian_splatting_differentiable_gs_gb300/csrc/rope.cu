@@ -68,7 +68,7 @@ __device__ __forceinline__ void sine(float half_turns, float* s, float* c) {
 template <typename T, int VEC, bool INTER>
 __global__ void __launch_bounds__(kThreads, kBlocksOf<T, VEC, INTER>) rope_kernel(
     int64_t tokens, const __grid_constant__ RopeK k, const __grid_constant__ HeadsK q,
-    const __grid_constant__ HeadsK kk, const int32_t* __restrict__ pos) {
+    const __grid_constant__ HeadsK kk, const int32_t* pos) {
   constexpr bool kOne = INTER && VEC > 1;  // both channels in one vector
   constexpr int kHeadBatch = kBatchOf<T, VEC, INTER>;
   __shared__ float2 angles[2][kThreads * VEC];  // [token][pair]: cosine, sine
@@ -107,6 +107,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksOf<T, VEC, INTER>) rope_kerne
     *to = a;
   };
 
+  launch_dependents();
+  wait_for_previous();
   const int64_t in_step = s.in_head * s.slots, out_step = s.out_head * s.slots;
   int turn = 0;
   for (int64_t t0 = (int64_t)blockIdx.x * s.block_tokens; t0 < tokens;
@@ -165,15 +167,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksOf<T, VEC, INTER>) rope_kerne
 }
 
 template <typename T, bool INTER>
-void rope_launch(int vec, dim3 grid, int threads, int64_t tokens, const RopeK& k, const HeadsK& s0,
-                 const HeadsK& s1, const int32_t* pos, cudaStream_t st) {
+cudaError_t rope_launch(int vec, dim3 grid, int threads, int64_t tokens, const RopeK& k,
+                        const HeadsK& s0, const HeadsK& s1, const int32_t* pos, cudaStream_t st) {
   constexpr int kMost = most_pairs(sizeof(T), INTER);
   if (kMost == 4 && vec == 4)
-    rope_kernel<T, kMost, INTER><<<grid, threads, 0, st>>>(tokens, k, s0, s1, pos);
-  else if (vec == 2)
-    rope_kernel<T, 2, INTER><<<grid, threads, 0, st>>>(tokens, k, s0, s1, pos);
-  else
-    rope_kernel<T, 1, INTER><<<grid, threads, 0, st>>>(tokens, k, s0, s1, pos);
+    return launch_overlapped(rope_kernel<T, kMost, INTER>, grid, threads, 0, st, tokens, k, s0, s1, pos);
+  if (vec == 2)
+    return launch_overlapped(rope_kernel<T, 2, INTER>, grid, threads, 0, st, tokens, k, s0, s1, pos);
+  return launch_overlapped(rope_kernel<T, 1, INTER>, grid, threads, 0, st, tokens, k, s0, s1, pos);
 }
 
 bool dims_ok(int32_t n_axes, const int32_t* dims, int* sum) {
@@ -296,15 +297,12 @@ extern "C" gs_status gs_rope(int64_t tokens, int32_t n_axes, const int32_t* dims
   if (blocks > most) blocks = most;
   const dim3 grid((unsigned)blocks, n);
   cudaStream_t st = (cudaStream_t)stream;
-#define GS_ROPE(T)                                                                                 \
-  do {                                                                                             \
-    if (interleaved) rope_launch<T, true>(vec, grid, threads, tokens, k, h[0], h[1], positions, st); \
-    else rope_launch<T, false>(vec, grid, threads, tokens, k, h[0], h[1], positions, st);          \
-  } while (0)
+#define GS_ROPE(T)                                                                         \
+  GS_CUDA((interleaved ? rope_launch<T, true> : rope_launch<T, false>)(                    \
+      vec, grid, threads, tokens, k, h[0], h[1], positions, st))
   if (dtype == GS_BF16) GS_ROPE(__nv_bfloat16);
   else if (dtype == GS_F16) GS_ROPE(__half);
   else GS_ROPE(float);
 #undef GS_ROPE
-  GS_CHECK_LAUNCH();
   return GS_OK;
 }

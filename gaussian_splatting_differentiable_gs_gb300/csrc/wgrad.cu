@@ -347,7 +347,7 @@ __device__ __forceinline__ uint32_t decode2(uint32_t bytes, uint32_t steps) {
 template <typename TO>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     wgrad_kernel(const __grid_constant__ Plan p, const __grid_constant__ CUtensorMap dy_map,
-                 const __grid_constant__ CUtensorMap q_map, const uint8_t* __restrict__ e,
+                 const __grid_constant__ CUtensorMap q_map, const uint8_t* e,
                  int64_t es, TO* dw, float* partial, unsigned int* status) {
   extern __shared__ uint8_t raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
@@ -388,8 +388,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = c->tmem;
-  asm volatile("griddepcontrol.launch_dependents;");      // the join's blocks wait for this one's end
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // dy's terms, and all before, are there
+  launch_dependents();
+  wait_for_previous();  // dy's terms, and all before, are there
 
   if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtrlRegs));
   if (warp == 0) {
@@ -634,9 +634,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // one column of a CTA's half tile, a thread four channels.
 template <typename TO>
 __global__ void __launch_bounds__(128) wgrad_join_kernel(const __grid_constant__ Plan p,
-                                                         const float* __restrict__ partial,
+                                                         const float* partial,
                                                          TO* dw) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the products still run
+  launch_dependents();
+  wait_for_previous();
   const int per_half = p.bn / 4;
   const int tile = blockIdx.x / (2 * per_half), rank = blockIdx.x / per_half % 2;
   const int col = blockIdx.x % per_half * 4 + (int)(threadIdx.x >> 5), in = threadIdx.x % 32 * 4;
@@ -671,7 +672,8 @@ template <typename T>
 __global__ void __launch_bounds__(256) wgrad_terms_kernel(int64_t tokens, int64_t padded, int rows,
                                                           int ld, int terms, const T* dy,
                                                           int64_t dys, __nv_bfloat16* out) {
-  asm volatile("griddepcontrol.launch_dependents;");
+  launch_dependents();
+  wait_for_previous();
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t t = i / (ld / 2);
   const int n = (int)(i % (ld / 2)) * 2;
@@ -819,15 +821,14 @@ extern "C" gs_status gs_act8_wgrad(int64_t tokens, int32_t rows, int32_t channel
     __nv_bfloat16* out = (__nv_bfloat16*)((char*)partial + partial_bytes());
     const unsigned blocks = (unsigned)div_up(p.term_rows * (ld / 2), 256);
     if (dtype == GS_BF16)
-      wgrad_terms_kernel<<<blocks, 256, 0, st>>>(tokens, p.term_rows, rows, ld, 1,
-                                                 (const __nv_bfloat16*)dy, dy_stride, out);
+      GS_CUDA(launch_overlapped(wgrad_terms_kernel<__nv_bfloat16>, blocks, 256, 0, st, tokens,
+                                p.term_rows, rows, ld, 1, (const __nv_bfloat16*)dy, dy_stride, out));
     else if (dtype == GS_F16)
-      wgrad_terms_kernel<<<blocks, 256, 0, st>>>(tokens, p.term_rows, rows, ld, 2,
-                                                 (const __half*)dy, dy_stride, out);
+      GS_CUDA(launch_overlapped(wgrad_terms_kernel<__half>, blocks, 256, 0, st, tokens, p.term_rows,
+                                rows, ld, 2, (const __half*)dy, dy_stride, out));
     else
-      wgrad_terms_kernel<<<blocks, 256, 0, st>>>(tokens, p.term_rows, rows, ld, 3,
-                                                 (const float*)dy, dy_stride, out);
-    GS_CHECK_LAUNCH();
+      GS_CUDA(launch_overlapped(wgrad_terms_kernel<float>, blocks, 256, 0, st, tokens, p.term_rows,
+                                rows, ld, 3, (const float*)dy, dy_stride, out));
     src = out;
     height = p.terms * p.term_rows;
     stride = ld;
@@ -866,32 +867,19 @@ extern "C" gs_status gs_act8_wgrad(int64_t tokens, int32_t rows, int32_t channel
   if (p.quota < kMinSteps) p.quota = kMinSteps < p.steps ? kMinSteps : p.steps;
   const int used = p.waves ? clusters : (int)div_up(p.rem_steps, p.quota);
   unsigned int* status = (unsigned int*)((char*)workspace + kWsStatusOffset);
-  // Both kernels may start while the one before them still runs: their set-up
-  // overlaps with it, and they wait for its end before they touch memory.
-  cudaLaunchAttribute early{};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.stream = st;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
-  cfg.gridDim = dim3(2 * used);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
   if (out_dtype == GS_F32)
-    GS_CUDA(cudaLaunchKernelEx(&cfg, wgrad_kernel<float>, p, map, qmap, e, e_stride, (float*)dw, partial, status));
+    GS_CUDA(launch_overlapped(wgrad_kernel<float>, 2 * used, kThreads, kSmem, st, p, map, qmap, e,
+                              e_stride, (float*)dw, partial, status));
   else
-    GS_CUDA(cudaLaunchKernelEx(&cfg, wgrad_kernel<__nv_bfloat16>, p, map, qmap, e, e_stride,
-                               (__nv_bfloat16*)dw, partial, status));
+    GS_CUDA(launch_overlapped(wgrad_kernel<__nv_bfloat16>, 2 * used, kThreads, kSmem, st, p, map,
+                              qmap, e, e_stride, (__nv_bfloat16*)dw, partial, status));
   if (p.rem_tiles && p.quota % p.steps != 0) {
-    cfg.gridDim = dim3((unsigned)(p.rem_tiles * 2 * (p.bn / 4)));
-    cfg.blockDim = dim3(128);
-    cfg.dynamicSmemBytes = 0;
+    const unsigned blocks = (unsigned)(p.rem_tiles * 2 * (p.bn / 4));
     if (out_dtype == GS_F32)
-      GS_CUDA(cudaLaunchKernelEx(&cfg, wgrad_join_kernel<float>, p, (const float*)partial, (float*)dw));
+      GS_CUDA(launch_overlapped(wgrad_join_kernel<float>, blocks, 128, 0, st, p, partial, (float*)dw));
     else
-      GS_CUDA(cudaLaunchKernelEx(&cfg, wgrad_join_kernel<__nv_bfloat16>, p, (const float*)partial,
-                                 (__nv_bfloat16*)dw));
+      GS_CUDA(launch_overlapped(wgrad_join_kernel<__nv_bfloat16>, blocks, 128, 0, st, p, partial,
+                                (__nv_bfloat16*)dw));
   }
   return GS_OK;
 }
