@@ -130,19 +130,6 @@ __device__ __forceinline__ uint32_t bits_of(float v) { return __float_as_uint(v)
 __device__ __forceinline__ uint32_t bits_of(__nv_bfloat16 v) { return __bfloat16_as_ushort(v); }
 __device__ __forceinline__ uint32_t bits_of(__half v) { return __half_as_ushort(v); }
 
-// Two values as the words of their bits.
-template <typename T>
-__device__ __forceinline__ uint32_t pair_word(float a, float b);
-template <>
-__device__ __forceinline__ uint32_t pair_word<__nv_bfloat16>(float a, float b) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-template <>
-__device__ __forceinline__ uint32_t pair_word<__half>(float a, float b) {
-  const __half2 v = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
 template <typename T>
 __device__ __forceinline__ void words_of(const float (&v)[kPer], uint32_t* w) {
   if constexpr (sizeof(T) == 4) {

@@ -195,11 +195,27 @@ __device__ __forceinline__ void store_row(const float (&v)[VEC * NV], T* p, int 
     const int c = first + i * step;
     if (c < C) {
       Pack<T, VEC> w;
+      if constexpr (sizeof(T) == 2 && VEC > 1) {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) w.v[j] = from_f32<T>(v[i * VEC + j]);
+        for (int j = 0; j < VEC; j += 2)
+          reinterpret_cast<uint32_t*>(&w)[j / 2] = pair_word<T>(v[i * VEC + j], v[i * VEC + j + 1]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) w.v[j] = from_f32<T>(v[i * VEC + j]);
+      }
       store_pack<T, VEC>(p + c, w);
     }
   }
+}
+
+// Channels i and i + 1 of a thread's.
+template <int E>
+__device__ __forceinline__ float2 pair(const float (&v)[E], int i) {
+  return make_float2(v[i], v[i + 1]);
+}
+template <int E>
+__device__ __forceinline__ void put_pair(float (&v)[E], int i, float2 a) {
+  v[i] = a.x, v[i + 1] = a.y;
 }
 
 // Mean and 1/deviation of a team's row; v becomes the centred row.
@@ -208,9 +224,10 @@ __device__ __forceinline__ void row_stats(float (&v)[VEC * NV], Team& team, cons
                                           int first, int step, float& mean, float& rstd) {
   mean = 0.f;
   if (k.center) {
-    float s[1] = {0.f};
+    float2 all = both(0.f);
 #pragma unroll
-    for (int i = 0; i < VEC * NV; ++i) s[0] += v[i];
+    for (int i = 0; i < VEC * NV; i += 2) all = add2(all, pair(v, i));
+    float s[1] = {all.x + all.y};
     team.sum(s);
     mean = s[0] * k.inv_c;
 #pragma unroll
@@ -220,9 +237,10 @@ __device__ __forceinline__ void row_stats(float (&v)[VEC * NV], Team& team, cons
         for (int j = 0; j < VEC; ++j) v[i * VEC + j] -= mean;
       }
   }
-  float s[1] = {0.f};
+  float2 all = both(0.f);
 #pragma unroll
-  for (int i = 0; i < VEC * NV; ++i) s[0] += v[i] * v[i];
+  for (int i = 0; i < VEC * NV; i += 2) all = fma2(pair(v, i), pair(v, i), all);
+  float s[1] = {all.x + all.y};
   team.sum(s);
   rstd = rsqrtf(s[0] * k.inv_c + k.eps);
 }
@@ -250,6 +268,16 @@ struct Weights {
       const Pack<float, kEl> p = load_pack<float, kEl>(w + place(i, j, lane, lanes));
 #pragma unroll
       for (int e = 0; e < kEl; ++e) v[j + e] = p.v[e];
+    }
+  }
+  __device__ __forceinline__ static void get_all(float (&v)[VEC * NV], const float* w, int lane,
+                                                 int lanes) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float u[VEC];
+      get(u, w, i, lane, lanes);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) v[i * VEC + j] = u[j];
     }
   }
 };
@@ -352,15 +380,12 @@ __global__ void __launch_bounds__(kTeamThreads, 1) norm_fwd_kernel(
         if (k.post) {
           row_stats<VEC, NV>(u, team, k, first, step, m0, r0);
 #pragma unroll
-          for (int i = 0; i < E; ++i) u[i] *= r0;
+          for (int i = 0; i < E; i += 2) put_pair(u, i, mul2(pair(u, i), both(r0)));
         }
+        float w[E];
+        Weights<VEC, NV>::get_all(w, w_k, lane, lanes);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          float w[VEC];
-          Weights<VEC, NV>::get(w, w_k, i, lane, lanes);
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) v[i * VEC + j] += w[j] * u[i * VEC + j];
-        }
+        for (int i = 0; i < E; i += 2) put_pair(v, i, fma2(pair(w, i), pair(u, i), pair(v, i)));
         store_row<TX, VEC, NV>(v, x_out + t * x_out_stride, first, step, k.C);
       }
       if (!RX::kOwn) team.sync();
@@ -368,13 +393,11 @@ __global__ void __launch_bounds__(kTeamThreads, 1) norm_fwd_kernel(
       s = s + 1 == depth ? 0 : s + 1;
       if (y) {
         row_stats<VEC, NV>(v, team, k, first, step, m1, r1);
+        float w[E];
+        Weights<VEC, NV>::get_all(w, w_pre, lane, lanes);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          float w[VEC];
-          Weights<VEC, NV>::get(w, w_pre, i, lane, lanes);
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) v[i * VEC + j] *= r1 * w[j];
-        }
+        for (int i = 0; i < E; i += 2)
+          put_pair(v, i, mul2(mul2(both(r1), pair(w, i)), pair(v, i)));
         store_row<TB, VEC, NV>(v, y + t * y_stride, first, step, k.C);
         if (y_q) {
           // the checkpoint of y as stored; a group is 32 / VEC lanes of a warp
@@ -507,54 +530,67 @@ __global__ void __launch_bounds__(kTeamThreads, 1) norm_bwd_kernel(
       const char* slot = smem + s * slot_bytes;
       float d[E];
       if (dy) {
-        float n[E], h[E], part[2] = {0.f, 0.f};
+        float n[E], h[E], w[E];
         rx.read(n, slot, t, first, step, k.C, tm);
         ry.read(h, slot + 2 * xb + bb, t, first, step, k.C, tm);
+        Weights<VEC, NV>::get_all(w, w_pre, lane, lanes);
+        float2 hn = both(0.f), h1 = both(0.f);
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          float w[VEC];
-          Weights<VEC, NV>::get(w, w_pre, v, lane, lanes);
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            const int i = v * VEC + j;
-            n[i] = (n[i] - st.z) * st.w;
-            acc_pre[i] += h[i] * n[i];
-            h[i] *= w[j];
-            part[0] += h[i] * n[i];
-            part[1] += h[i];
-          }
+        for (int i = 0; i < E; i += 2) {
+          const float2 ni = mul2(add2(pair(n, i), both(-st.z)), both(st.w)), hi = pair(h, i);
+          put_pair(acc_pre, i, fma2(hi, ni, pair(acc_pre, i)));
+          const float2 hw = mul2(hi, pair(w, i));
+          hn = fma2(hw, ni, hn);
+          put_pair(n, i, ni);
+          put_pair(h, i, hw);
         }
-        team_sums(team, part, k.center);
-        const float a = part[0] * k.inv_c, b = part[1] * k.inv_c;
-        rd.read(d, slot + xb, t, first, step, k.C, tm);
+        if (k.center)
 #pragma unroll
-        for (int i = 0; i < E; ++i) d[i] += st.w * (h[i] - n[i] * a - b);
+          for (int i = 0; i < E; i += 2) h1 = add2(h1, pair(h, i));
+        float part[2] = {hn.x + hn.y, h1.x + h1.y};
+        team_sums(team, part, k.center);
+        const float2 a = both(-part[0] * k.inv_c), b = both(-part[1] * k.inv_c);
+        rd.read(d, slot + xb, t, first, step, k.C, tm);
+        if (k.center)
+#pragma unroll
+          for (int i = 0; i < E; i += 2) put_pair(h, i, add2(pair(h, i), b));
+#pragma unroll
+        for (int i = 0; i < E; i += 2)
+          put_pair(d, i, fma2(both(st.w), fma2(pair(n, i), a, pair(h, i)), pair(d, i)));
       } else {
         rd.read(d, slot + xb, t, first, step, k.C, tm);
       }
       store_row<TX, VEC, NV>(d, dx + t * dx_stride, first, step, k.C);
       if (block) {
-        float m[E], part[2] = {0.f, 0.f};
+        float m[E], w[E];  // weights: 0 from C on
         rb.read(m, slot + 2 * xb, t, first, step, k.C, tm);
+        Weights<VEC, NV>::get_all(w, w_k, lane, lanes);
+        if (k.post)
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          float w[VEC];  // 0 from C on
-          Weights<VEC, NV>::get(w, w_k, v, lane, lanes);
+          for (int i = 0; i < E; i += 2)
+            put_pair(m, i, mul2(add2(pair(m, i), both(-st.x)), both(st.y)));
+        float2 dm = both(0.f), d1 = both(0.f);
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            const int i = v * VEC + j;
-            if (k.post) m[i] = (m[i] - st.x) * st.y;
-            acc_e[i] += d[i] * m[i];
-            d[i] *= w[j];
-            part[0] += d[i] * m[i];
-            part[1] += d[i];
-          }
+        for (int i = 0; i < E; i += 2) {
+          const float2 mi = pair(m, i), di = pair(d, i);
+          put_pair(acc_e, i, fma2(di, mi, pair(acc_e, i)));
+          const float2 dw = mul2(di, pair(w, i));
+          dm = fma2(dw, mi, dm);
+          put_pair(d, i, dw);
         }
         if (k.post) {
-          team_sums(team, part, k.center);
-          const float a = part[0] * k.inv_c, b = part[1] * k.inv_c;
+          if (k.center)
 #pragma unroll
-          for (int i = 0; i < E; ++i) d[i] = st.y * (d[i] - m[i] * a - b);
+            for (int i = 0; i < E; i += 2) d1 = add2(d1, pair(d, i));
+          float part[2] = {dm.x + dm.y, d1.x + d1.y};
+          team_sums(team, part, k.center);
+          const float2 a = both(-part[0] * k.inv_c), b = both(-part[1] * k.inv_c);
+          if (k.center)
+#pragma unroll
+            for (int i = 0; i < E; i += 2) put_pair(d, i, add2(pair(d, i), b));
+#pragma unroll
+          for (int i = 0; i < E; i += 2)
+            put_pair(d, i, mul2(both(st.y), fma2(pair(m, i), a, pair(d, i))));
         }
         store_row<TB, VEC, NV>(d, dblock + t * dblock_stride, first, step, k.C);
       }
