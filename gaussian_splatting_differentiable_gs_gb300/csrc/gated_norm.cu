@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(kTeamThreads, 1) norm_bwd_kernel(
   float* red = reinterpret_cast<float*>(smem + depth * slot_bytes);
   float* w_pre = red + teams * kRedFloats;
   float* w_k = w_pre + Weights<VEC, NV>::count(warps);
-  float* join = w_k + Weights<VEC, NV>::count(warps);  // [teams][C] column sums of several teams
+  float* join = w_k + Weights<VEC, NV>::count(warps);  // column sums of several teams, in places
   Team team{red + tm * kRedFloats, warps, warp - tm * warps, tm + 1, 0};
   const int lanes = warps * 32, lane = threadIdx.x - tm * lanes;
   const int first = lane * VEC, step = warps * 32 * VEC;
@@ -495,19 +495,27 @@ __global__ void __launch_bounds__(kTeamThreads, 1) norm_bwd_kernel(
           if (first + i * step < k.C) to[first + i * step + j] = acc[i * VEC + j];
       return;
     }
+    using W = Weights<VEC, NV>;
+    using P = Pack<float, W::kEl>;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < E; i += W::kEl) {
+      P p;
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const int c = first + i * step + j;
-        if (c < k.C) join[tm * k.C + c] = acc[i * VEC + j];
+      for (int j = 0; j < W::kEl; ++j) p.v[j] = acc[i + j];
+      store_pack<float, W::kEl>(join + tm * E * lanes + W::place(i / VEC, i % VEC, lane, lanes), p);
+    }
+    __syncthreads();
+    for (int q = threadIdx.x; q < E / W::kEl * lanes; q += blockDim.x) {
+      P sum = load_pack<float, W::kEl>(join + q * W::kEl);
+      for (int i = 1; i < teams; ++i) {
+        const P p = load_pack<float, W::kEl>(join + i * E * lanes + q * W::kEl);
+#pragma unroll
+        for (int j = 0; j < W::kEl; ++j) sum.v[j] += p.v[j];
       }
-    __syncthreads();
-    for (int c = threadIdx.x; c < k.C; c += blockDim.x) {
-      float s = 0.f;
-      for (int i = 0; i < teams; ++i) s += join[i * k.C + c];
-      to[c] = s;
+      constexpr int kIn = VEC / W::kEl;  // packs of a vector
+      const int r = q / lanes, c = (r / kIn * lanes + q % lanes) * VEC + r % kIn * W::kEl;
+      if (c < k.C) store_pack<float, W::kEl>(to + c, sum);
     }
   };
 
@@ -629,20 +637,19 @@ __global__ void __launch_bounds__(1024) norm_sums_kernel(const __grid_constant__
       for (int i = lo + from; i < hi; i += by) s += p[(int64_t)i * k.C + c];
     return s;
   };
-  auto join = [&](float (*m)[33], float* to) {
-    __syncthreads();
-    if (y == 0 && in && to) {
-      float s = 0.f;
+  auto join = [&](float (*m)[33], float* to) {  // one warp
+    if (!in || !to) return;
+    float s = 0.f;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) s += m[i][x];
-      to[c] = s;
-    }
+    for (int i = 0; i < 32; ++i) s += m[i][x];
+    to[c] = s;
   };
   if (blockIdx.y == 0) {  // dw_pre's blocks
     if (!dw_pre) return;
     wait_for_previous();
     red[y][x] = slots(part_pre, 0, ctas, y, 32);
-    join(red, dw_pre);
+    __syncthreads();
+    if (y == 0) join(red, dw_pre);
     return;
   }
   // What is not the row kernel's is read while that still runs: it began after all
@@ -689,8 +696,9 @@ __global__ void __launch_bounds__(1024) norm_sums_kernel(const __grid_constant__
   __syncthreads();
   red[y][x] = post;
   red2[y][x] = scale;
-  join(red, dw_post);
-  join(red2, dscale);
+  __syncthreads();
+  if (y == 0) join(red, dw_post);
+  if (y == 1) join(red2, dscale);
 }
 
 bool norm_ok(const gs_norm* p) {
@@ -788,7 +796,7 @@ Layout norm_layout(const NormK& k, int tensors, bool join) {
                                            Rows<TB, VEC, NV>::slot(l.s.threads, l.s.teams, k.C));
     const size_t fixed =
         sizeof(float) * ((size_t)l.s.teams * kRedFloats + 2 * Weights<VEC, NV>::count(l.s.warps) +
-                         (join && l.s.teams > 1 ? (size_t)l.s.teams * k.C : 0));
+                         (join && l.s.teams > 1 ? (size_t)l.s.teams * Weights<VEC, NV>::count(l.s.warps) : 0));
     l.depth = kMaxDepth;
     while (l.depth > 1 && l.depth * slot + fixed > (size_t)kSmemBudget) --l.depth;
     l.smem = l.depth * slot + fixed;
