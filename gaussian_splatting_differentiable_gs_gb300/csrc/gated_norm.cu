@@ -132,20 +132,19 @@ struct Rows {
       }
     } else {
       const int off = (int)((uintptr_t)p & 15), n = C * (int)sizeof(T);
-      // whether what lies before the row is not the tensor's
-      const bool clip = stride < C || t * stride * (int64_t)sizeof(T) < 16;
-      const uint32_t row = to + team * row_bytes(C);
-      for (int i = first; i * 16 < off + n; i += step) {
-        const int b0 = i * 16 - off;  // the granule's first byte within the row
-        if (b0 < 0 && clip) {
-          for (int b = 0; b < b0 + 16 && b < n; b += sizeof(T))
-            *reinterpret_cast<T*>(slot + team * row_bytes(C) + off + b) = p[b / (int)sizeof(T)];
-        } else {
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(row + i * 16),
-                       "l"((const char*)p + b0), "r"(n - b0 < 16 ? n - b0 : 16)
-                       : "memory");
-        }
+      int b = first * 16 - off;  // the granule's first byte within the row
+      uint32_t at = to + team * row_bytes(C) + first * 16;
+      // what lies before the row may not be the tensor's
+      if (b < 0 && (stride < C || t * stride * (int64_t)sizeof(T) < 16)) {
+        for (int j = 0; j < b + 16 && j < n; j += sizeof(T))
+          *reinterpret_cast<T*>(slot + team * row_bytes(C) + off + j) = p[j / (int)sizeof(T)];
+        b += step * 16, at += step * 16;
       }
+      const char* from = (const char*)p + b;
+      for (; b < n; b += step * 16, at += step * 16, from += step * 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(from),
+                     "r"(min(n - b, 16))
+                     : "memory");
     }
   }
   // Channels from C on and tensors that are not there read as the zeros that the
