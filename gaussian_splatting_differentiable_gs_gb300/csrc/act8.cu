@@ -5,11 +5,11 @@
 // and in fp32 and the choice of q is the same in every implementation.  All
 // four kernels are single passes.  A lane has eight neighbouring channels (a group
 // is four lanes).  Where rows start on 16-byte boundaries the kernels are bound by
-// memory (a gated unit of 32640 x 2816 bf16, both directions: 229 us, 6.5 TB/s).
+// memory (a gated unit of 32640 x 2816 bf16, both directions: 230 us, 6.4 TB/s).
 // Where they do not, a lane reads the aligned 16-byte granules that its channels
 // touch and shifts them into place; for stores a granule is put together from two
 // lanes, and only a run's two ends are written element by element.  That form is
-// bound by instructions (8160 x 1361 fp16: 75 us, of which storing is 20, the
+// bound by instructions (8160 x 1361 fp16: 72 us, of which storing is 20, the
 // checkpoints 14 and the error function 10).  Loads of single words in place of
 // granules: no change; a warp that walks along a row and keeps its last lane's
 // words, so that only rows' ends are split: 2 us more.
@@ -23,12 +23,12 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPer = 8;               // channels of a lane
 constexpr int kUnitsPerBlock = 2048;  // lanes' worth of work
-// Blocks an SM: 48 warps or more hide the memory latency of the aligned form (six
-// and eight blocks 232 us, five 242, four 259 for both directions of a gated unit
-// of 32640 x 2816 bf16, launches not overlapped); the other form needs more registers than that leaves
-// (8160 x 1361 fp16: five 78 us, four 80, six 95).
+// Blocks an SM: 48 warps hide the memory latency of the aligned form (both directions
+// of a gated unit of 32640 x 2816 bf16: six blocks 230 us, eight 232, five 242); the
+// other form needs more registers than that leaves (8160 x 1361 fp16: five 78 us,
+// four 80, six 95).
 template <bool WIDE>
-constexpr int kBlocks = WIDE ? 8 : 5;
+constexpr int kBlocks = WIDE ? 6 : 5;
 
 struct Act8K {
   int8_t* q;
@@ -311,40 +311,47 @@ __device__ __forceinline__ float reciprocal(float v) {
   return r;
 }
 
-// act(v) and its derivative.  Phi comes from Abramowitz and Stegun's formula
-// 7.1.26 for the error function (absolute error below 1.5e-7, half of that in
-// Phi), which needs the one exponential that the derivative has too.
+// act(v) and its derivative for two values.  Phi comes from Abramowitz and
+// Stegun's formula 7.1.26 for the error function (absolute error below 1.5e-7, half
+// of that in Phi), which needs the one exponential that the derivative has too; its
+// arithmetic takes two values an instruction (8160 x 1361 fp16: 72 us, 75 without).
+// The same elsewhere in these kernels costs the aligned form registers, and thereby
+// warps: 238 us in place of 230 at 32640 x 2816 bf16.
 struct Phi {
-  float p, density;  // Phi(v), phi(v)
+  float2 p, density;  // Phi(v), phi(v)
 };
-__device__ __forceinline__ Phi normal(float v) {
-  const float z = fabsf(v) * 0.70710678118654752f;
-  const float t = reciprocal(fmaf(0.3275911f, z, 1.f));
-  const float ex = power2(z * z * -1.4426950408889634f);
-  float q = fmaf(1.061405429f, t, -1.453152027f);
-  q = fmaf(q, t, 1.421413741f);
-  q = fmaf(q, t, -0.284496736f);
-  q = fmaf(q, t, 0.254829592f);
-  const float tail = 0.5f * q * t * ex;
-  return Phi{v < 0.f ? tail : 1.f - tail, ex * 0.39894228040143268f};
+__device__ __forceinline__ Phi normal(float2 v) {
+  const float2 z = make_float2(fabsf(v.x) * 0.70710678118654752f, fabsf(v.y) * 0.70710678118654752f);
+  const float2 y = fma2(both(0.3275911f), z, both(1.f));
+  const float2 t = make_float2(reciprocal(y.x), reciprocal(y.y));
+  const float2 w = mul2(mul2(z, z), both(-1.4426950408889634f));
+  const float2 ex = make_float2(power2(w.x), power2(w.y));
+  float2 q = fma2(both(0.5f * 1.061405429f), t, both(0.5f * -1.453152027f));
+  q = fma2(q, t, both(0.5f * 1.421413741f));
+  q = fma2(q, t, both(0.5f * -0.284496736f));
+  q = fma2(q, t, both(0.5f * 0.254829592f));
+  const float2 tail = mul2(mul2(q, t), ex), rest = fma2(tail, both(-1.f), both(1.f));
+  return Phi{make_float2(v.x < 0.f ? tail.x : rest.x, v.y < 0.f ? tail.y : rest.y),
+             mul2(ex, both(0.39894228040143268f))};
 }
 __device__ __forceinline__ float sigmoid(float v) {
   return reciprocal(1.f + power2(v * -1.4426950408889634f));
 }
 template <int ACT>
-__device__ __forceinline__ float act_value(float v) {
-  return v * (ACT == GS_ACT_SILU ? sigmoid(v) : normal(v).p);
+__device__ __forceinline__ float2 act_value(float2 v) {
+  if (ACT == GS_ACT_SILU) return make_float2(v.x * sigmoid(v.x), v.y * sigmoid(v.y));
+  return mul2(v, normal(v).p);
 }
 template <int ACT>
-__device__ __forceinline__ void act_both(float v, float& f, float& df) {
+__device__ __forceinline__ void act_both(float2 v, float2& f, float2& df) {
   if (ACT == GS_ACT_SILU) {
-    const float s = sigmoid(v);
-    f = v * s;
-    df = s * (1.f + v * (1.f - s));
+    const float s = sigmoid(v.x), u = sigmoid(v.y);
+    f = make_float2(v.x * s, v.y * u);
+    df = make_float2(s * (1.f + v.x * (1.f - s)), u * (1.f + v.y * (1.f - u)));
   } else {
     const Phi n = normal(v);
-    f = v * n.p;
-    df = fmaf(v, n.density, n.p);
+    f = mul2(v, n.p);
+    df = fma2(v, n.density, n.p);
   }
 }
 
@@ -359,10 +366,16 @@ __global__ void __launch_bounds__(kThreads, kBlocks<WIDE>)
       hg.load(gate, r, t, c);
       if (GATED) hu.load(up, r, t, c);
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        g[j] = hg.value(j);
-        if (GATED) u[j] = hu.value(j);
-        o[j] = act_value<ACT>(g[j]) * (GATED ? u[j] : 1.f);
+      for (int j = 0; j < kPer; j += 2) {
+        const float2 a = make_float2(hg.value(j), hg.value(j + 1));
+        float2 f = act_value<ACT>(a);
+        g[j] = a.x, g[j + 1] = a.y;
+        if (GATED) {
+          const float2 b = make_float2(hu.value(j), hu.value(j + 1));
+          u[j] = b.x, u[j + 1] = b.y;
+          f.x *= b.x, f.y *= b.y;
+        }
+        o[j] = f.x, o[j + 1] = f.y;
       }
       if (WIDE) put<T, WIDE>(o, h, r, t, c, in);
     }
@@ -384,13 +397,15 @@ __global__ void __launch_bounds__(kThreads, kBlocks<WIDE>)
       Held<T, WIDE> hd;
       hd.load(dh, r, t, c);
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        float f, df;
-        act_both<ACT>(held8(hg, j), f, df);
-        const float w = GATED ? held8(hu, j) : 1.f, d = hd.value(j);
-        o[j] = WIDE || c + j < r.C ? f * w : 0.f;
-        dg[j] = d * w * df;
-        du[j] = d * f;
+      for (int j = 0; j < kPer; j += 2) {
+        float2 f, df;
+        act_both<ACT>(make_float2(held8(hg, j), held8(hg, j + 1)), f, df);
+        const float2 d = make_float2(hd.value(j), hd.value(j + 1));
+        const float2 w = GATED ? make_float2(held8(hu, j), held8(hu, j + 1)) : both(1.f);
+        o[j] = WIDE || c + j < r.C ? f.x * w.x : 0.f;
+        o[j + 1] = WIDE || c + j + 1 < r.C ? f.y * w.y : 0.f;
+        dg[j] = d.x * w.x * df.x, dg[j + 1] = d.y * w.y * df.y;
+        du[j] = d.x * f.x, du[j + 1] = d.y * f.y;
       }
       if (WIDE) {
         put<T, WIDE>(dg, dgate, r, t, c, in);

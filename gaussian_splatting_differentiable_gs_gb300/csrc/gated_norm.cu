@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kTeamThreads, 1) norm_fwd_kernel(
               Pack<int8_t, VEC> q;
 #pragma unroll
               for (int j = 0; j < VEC; ++j)
-                q.v[j] = (int8_t)(act8_quantise(v[i * VEC + j], inv, e) & 0xff);
+                q.v[j] = (int8_t)(e == 255u ? 0u : act8_round(v[i * VEC + j], inv) & 0xff);
               store_pack<int8_t, VEC>(y_q + t * q_stride + c, q);
               if (c % GS_ACT8_GROUP == 0) y_e[t * e_stride + c / GS_ACT8_GROUP] = (uint8_t)e;
             }
@@ -863,8 +863,9 @@ cudaError_t bwd_launch(BwdArgs& a, cudaStream_t st) {
 }
 
 // 16 channels a thread where rows are aligned and that wide (32640 x 1024 bf16: 85 us,
-// with 8 a thread 107 us); 8 for rows that start anywhere, where 16 cost more in
-// single accesses than they save (5003 x 997 fp32: 49 us, 87 us).
+// with 8 a thread 107 us, when that was measured; 76 us now); 8 for rows that start
+// anywhere, where 16 cost more in single accesses than they save (5003 x 997 fp32:
+// 49 us, 87 us; 44 us now).
 template <typename TB, typename TX, int VEC>
 cudaError_t bwd_pick(BwdArgs& a, cudaStream_t st) {
   if (a.k.C <= (VEC > 1 ? 256 : 4096)) return bwd_launch<TB, TX, VEC, 8 / VEC>(a, st);
