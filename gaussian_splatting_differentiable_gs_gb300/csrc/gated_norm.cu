@@ -626,9 +626,12 @@ __global__ void __launch_bounds__(1024) norm_sums_kernel(const __grid_constant__
                                                          float* dgate, float* dscale) {
   __shared__ float red[32][33], red2[32][33];
   const int x = threadIdx.x, y = threadIdx.y;
-  launch_dependents();
   const int c = blockIdx.x * 32 + x;
   const bool in = c < k.C;
+  launch_dependents();
+  // Before anything is read, the weights and offsets too: the row kernel begins early
+  // itself, so when this one begins, what runs before that may still be writing them.
+  wait_for_previous();
   auto slots = [&](const float* p, int lo, int hi, int from, int by) {
     float s = 0.f;
     if (in && p)
@@ -645,14 +648,11 @@ __global__ void __launch_bounds__(1024) norm_sums_kernel(const __grid_constant__
   };
   if (blockIdx.y == 0) {  // dw_pre's blocks
     if (!dw_pre) return;
-    wait_for_previous();
     red[y][x] = slots(part_pre, 0, ctas, y, 32);
     __syncthreads();
     if (y == 0) join(red, dw_pre);
     return;
   }
-  // What is not the row kernel's is read while that still runs: it began after all
-  // that came before.
   const float w = in && k.w_post ? k.w_post[c] : 1.f;
   const float sc = in && k.scale ? k.scale[c] : 1.f;
   int64_t lo = 0, hi = 0;  // rows of the group whose slots this warp adds up
@@ -672,7 +672,6 @@ __global__ void __launch_bounds__(1024) norm_sums_kernel(const __grid_constant__
     }
   };
   ahead(0);
-  wait_for_previous();
   float post = 0.f, scale = 0.f;
   for (int g0 = 0; g0 < k.groups; g0 += 32) {
     const int n = min(32, k.groups - g0), per = 32 / n, g = g0 + y / per;
