@@ -285,7 +285,7 @@ struct Weights {
 template <typename TB>
 __device__ __forceinline__ float group_weight(const NormK& k, int g, int c) {
   float w = k.scale ? k.scale[c] : 1.f;
-  if (k.post && k.w_post) w *= k.w_post[c];
+  if (k.w_post) w *= k.w_post[c];
   if (k.gate) w *= to_f32(((const TB*)k.gate)[(int64_t)g * k.C + c]);
   return w;
 }
@@ -685,7 +685,7 @@ __global__ void __launch_bounds__(1024) norm_sums_kernel(const __grid_constant__
     if (y < n) {  // one warp a group
       e = 0.f;
       for (int i = 0; i < per; ++i) e += red[y * per + i][x];
-      post += sc * gv * e;
+      if (k.post) post += sc * gv * e;  // else u does not depend on w_post
       scale += gv * w * e;
       if (in && dgate) dgate[(int64_t)(g0 + y) * k.C + c] = sc * w * e;
     }
@@ -720,7 +720,7 @@ NormK make_norm(const gs_norm& p) {
   k.eps = p.eps;
   k.inv_c = (float)(1.0 / p.channels);
   k.w_pre = p.w_pre;
-  k.w_post = p.w_post;
+  k.w_post = k.post ? p.w_post : nullptr;  // no norm after the block: no weight
   k.scale = p.res_scale;
   k.gate = p.gate;
   k.offsets = p.gate ? p.group_offsets : nullptr;

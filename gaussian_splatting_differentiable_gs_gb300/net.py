@@ -234,7 +234,7 @@ def gs_gated_norm_fwd(x, block, x_out, y, stats, w_pre=None, w_post=None, gate=N
                       center=False, eps=1e-6, stream=None):
     """x_out = x + res_scale * gate[group] * (w_post * norm(block)), y = w_pre
     * norm(x_out).  block, x_out None: y = w_pre * norm(x) only; y None: the
-    sum only; post False: no norm of the block.  gate [groups, channels] with
+    sum only; post False: no norm of the block, and no w_post.  gate [groups, channels] with
     group_offsets int32 [groups + 1] (one group: None).  stats: float32
     [tokens, 4] for the backward.  y_q, y_e: y's 8-bit checkpoint."""
     shape, res_code = _first(x, "x")

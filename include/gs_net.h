@@ -74,7 +74,7 @@ gs_status gs_rope(int64_t tokens, int32_t n_axes, const int32_t* dims, const uin
 /* ---------------------------------------------------------------------- */
 /* The join of two blocks of a residual network, per token (row) with C
  * channels:
- *   u  = w_post * norm(block)      (post; u = block without)
+ *   u  = w_post * norm(block)      (post; u = block without, whatever w_post)
  *   x' = x + res_scale * gate[g] * u
  *   y  = w_pre * norm(x')
  * norm(v) = v * rsqrt(mean(v^2) + eps), or with GS_NORM_CENTER
@@ -116,7 +116,8 @@ gs_status gs_gated_norm_fwd(const gs_norm* p, const void* x, int64_t x_stride, c
 /* gs_gated_norm_bwd -- with d = dx_out + (gradient through norm(x')):
  *   dx = d, dblock = gradient through gate, scale and norm, and the sums over
  *   rows dw_pre, dw_post, dres_scale [C], dgate [groups][C] (fp32 outputs,
- *   overwritten, NULL where not wanted; the order of summation is fixed).
+ *   overwritten, NULL where not wanted; the order of summation is fixed;
+ *   without GS_NORM_POST dw_post is zeros).
  *   x_out    [tokens][C] x' as the forward wrote it
  *   block, stats  the forward's; block NULL as there (dblock NULL)
  *   dx_out   gradient of x' from the rest of the network, or NULL (0)
