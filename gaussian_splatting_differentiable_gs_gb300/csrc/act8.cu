@@ -87,8 +87,15 @@ __device__ __forceinline__ Held8 load8(const Act8K& k, int64_t t, int c) {
   return Held8{*reinterpret_cast<const uint2*>(k.q + t * k.qs + c),
                k.e[t * k.es + c / GS_ACT8_GROUP]};
 }
-__device__ __forceinline__ float held8(const Held8& h, int j) {
-  return act8_value((j < 4 ? h.q.x : h.q.y) ^ 0x80808080u, j & 3, act8_step(h.e));
+__device__ __forceinline__ float held8(const Held8& h, int j, float step) {
+  return act8_value((j < 4 ? h.q.x : h.q.y) ^ 0x80808080u, j & 3, step);
+}
+// The step for arithmetic in fp32.  From kAct8Top on it is the next number below, which
+// makes 64 steps of 2^122 fp32's largest number in place of an infinity (whose product
+// with a derivative of 0 would be a NaN); other values of such a group lose a last place
+// at most.
+__device__ __forceinline__ float held_step(const Held8& h) {
+  return __uint_as_float((h.e << 23) - (h.e >= kAct8Top<float> && h.e < 255u ? 1u : 0u));
 }
 
 // The first N words of z (N + 4 words) shifted down by s bytes (0 <= s < 16, even).
@@ -292,7 +299,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks<WIDE>)
     if (in) {
       const Held8 h = load8(k, t, c);
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) v[j] = held8(h, j);
+      for (int j = 0; j < kPer; ++j) v[j] = held8(h, j, act8_step(h.e));
+      if (h.e >= kAct8Top<T> && h.e < 255u) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) v[j] = act8_within<T>(v[j], held8(h, j, 1.f), act8_step(h.e));
+      }
     }
     put<T, WIDE>(v, x, r, t, c, in);
   });
@@ -394,14 +405,15 @@ __global__ void __launch_bounds__(kThreads, kBlocks<WIDE>)
     float dg[kPer], du[kPer], o[kPer] = {};
     if (in) {
       const Held8 hg = load8(g8, t, c), hu = GATED ? load8(u8, t, c) : Held8{};
+      const float sg = held_step(hg), su = held_step(hu);
       Held<T, WIDE> hd;
       hd.load(dh, r, t, c);
 #pragma unroll
       for (int j = 0; j < kPer; j += 2) {
         float2 f, df;
-        act_both<ACT>(make_float2(held8(hg, j), held8(hg, j + 1)), f, df);
+        act_both<ACT>(make_float2(held8(hg, j, sg), held8(hg, j + 1, sg)), f, df);
         const float2 d = make_float2(hd.value(j), hd.value(j + 1));
-        const float2 w = GATED ? make_float2(held8(hu, j), held8(hu, j + 1)) : both(1.f);
+        const float2 w = GATED ? make_float2(held8(hu, j, su), held8(hu, j + 1, su)) : both(1.f);
         o[j] = WIDE || c + j < r.C ? f.x * w.x : 0.f;
         o[j + 1] = WIDE || c + j + 1 < r.C ? f.y * w.y : 0.f;
         dg[j] = d.x * w.x * df.x, dg[j + 1] = d.y * w.y * df.y;

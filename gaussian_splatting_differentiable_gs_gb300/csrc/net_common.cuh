@@ -146,6 +146,29 @@ __device__ __forceinline__ float act8_inverse(uint32_t e) {
 // such a group reads back as.
 __device__ __forceinline__ float act8_step(uint32_t e) { return __uint_as_float(e << 23); }
 
+// Where rounding to 64 steps carried a value past the largest number of the type that
+// it is read in (a magnitude above 127 / 128 of the power of two beyond fp16's, bf16's
+// or fp32's range), it reads as that number.  Only groups with an exponent from here on
+// can hold such a value: fp16 holds 127 * 2^9, bf16 and fp32 127 * 2^121.
+template <typename T>
+constexpr uint32_t kAct8Top = 249u;
+template <>
+constexpr uint32_t kAct8Top<__half> = 137u;
+template <typename T>
+__device__ __forceinline__ float largest();
+template <>
+__device__ __forceinline__ float largest<float>() { return __uint_as_float(0x7f7fffffu); }
+template <>
+__device__ __forceinline__ float largest<__nv_bfloat16>() { return __uint_as_float(0x7f7f0000u); }
+template <>
+__device__ __forceinline__ float largest<__half>() { return 65504.f; }
+// v = q * step, q not 0: what half a step less would still hold was not beyond the type.
+template <typename T>
+__device__ __forceinline__ float act8_within(float v, float q, float step) {
+  const float top = largest<T>();
+  return fabsf(v) > top && (fabsf(q) - 0.5f) * step <= top ? copysignf(top, v) : v;
+}
+
 // q in the low byte of the result (anything where v is not finite): v * inv is exact
 // (a power of two), and adding 1.5 * 2^23 rounds it to the nearest whole number, ties
 // to even.

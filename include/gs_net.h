@@ -138,8 +138,10 @@ gs_status gs_gated_norm_bwd(const gs_norm* p, const void* x_out, int64_t x_strid
  * one exponent e; a value is q * 2^(e - 127), with e the smallest exponent
  * >= 1 for which the group's largest magnitude is at most 127 * 2^(e - 127)
  * and q rounded to nearest (ties to even), |q| <= 127.  Such a value is exact
- * in bf16 and fp32.  A group with an infinity or a NaN has e = 255, q = 0 and
- * reads back as NaN.  Storage: q int8 [tokens][ld], e uint8 [tokens][ld / 32]
+ * in bf16 and fp32; where only that rounding carried it past the largest number
+ * of the type that it is read in, gs_act8_decode and gs_glu_bwd (fp32) read that
+ * number (above 65024 in fp16, above 127 * 2^121 in bf16 and fp32).  Only a group with an infinity or a NaN,
+ * which has e = 255 and q = 0, reads back as NaN.  Storage: q int8 [tokens][ld], e uint8 [tokens][ld / 32]
  * with ld = C rounded up to 32 (the padding is zero); q rows are 16-byte
  * aligned (q_stride a multiple of 16, at least ld). */
 #define GS_ACT8_GROUP 32
@@ -181,6 +183,9 @@ gs_status gs_glu_bwd(int64_t tokens, int32_t channels, int32_t dtype, int32_t ac
  * k < channels, summed in fp32; accumulate != 0 adds to dw (the sum is
  * formed in fp32 and rounded once).
  *   dy          [tokens][rows] of type dtype; used exactly in every type
+ *   q, e        the checkpoint; its values are used exactly, as bf16 (64
+ *               steps of 2^122, a magnitude above 127 * 2^121 that was
+ *               rounded up, are an infinity there)
  *   dw          [rows][channels] of type out_dtype (GS_F32 or GS_BF16)
  *   workspace   gs_act8_wgrad_workspace_bytes(...) bytes, 16-byte aligned;
  *               its first 256 bytes must be zero before the first call

@@ -56,3 +56,71 @@ def test_norm_weight_after_the_block_counts_only_with_the_norm(gs, center):
              torch.stack([(terms * scale.double()).abs()[of == i].sum(0) for i in range(G)]))):
         err = (results[0][name].double().cpu() - want).abs()
         assert (err <= 2 * (T + 4) * U * mag).all(), name  # T terms, then the factors
+
+
+TOP = {torch.float16: 65504.0, torch.bfloat16: float(torch.finfo(torch.bfloat16).max),
+       torch.float32: float(torch.finfo(torch.float32).max)}
+
+
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("C", [32, 40, 33])
+def test_checkpoint_of_the_largest_numbers_reads_back_finite(gs, dt, C):
+    """The step nearest to a type's largest numbers can lie above them: such a value
+    reads as the type's largest number, everything else as it is held."""
+    top = TOP[dt]
+    x = torch.full((4, C), 0.0)
+    x[0, 0], x[0, 5] = top, -top
+    x[1] = top * 0.994          # above 127 / 128 of the power of two
+    x[2, ::2], x[2, 1::2] = -top, top * 0.7
+    x[3] = top * 0.25
+    x = x.to(dt)
+    q, e = gs.act8_empty(4, C)
+    gs.gs_act8_encode(x.cuda(), q, e)
+    wq, we = plain.encode(x)
+    assert torch.equal(q.cpu(), wq) and torch.equal(e.cpu(), we)
+    held = plain.decode(wq, we, C)
+    back = torch.empty(4, C, dtype=dt, device="cuda")
+    gs.gs_act8_decode(q, e, back)
+    want = held.clamp(-top, top)
+    assert torch.equal(back.double().cpu(), want)
+    # read in the other types: finite where the type holds the value before rounding
+    for other in (torch.bfloat16, torch.float32):
+        out = torch.empty(4, C, dtype=other, device="cuda")
+        gs.gs_act8_decode(q, e, out)
+        assert torch.equal(out.double().cpu(), held.clamp(-TOP[other], TOP[other]))
+
+
+def test_checkpoint_above_a_type_reads_as_infinity(gs):
+    """Values that a type does not hold, whatever their rounding, convert as ever."""
+    x = torch.tensor([[1e5, -7e4, 66100.0, 65000.0] + [1.0] * 28, [3e38, 1e30, -1e20, 1.0] + [0.0] * 28])
+    q, e = gs.act8_empty(2, 32)
+    gs.gs_act8_encode(x.cuda(), q, e)
+    out = torch.empty(2, 32, dtype=torch.float16, device="cuda")
+    gs.gs_act8_decode(q, e, out)
+    step = torch.exp2(e.cpu().double() - 127)
+    held = plain.decode(q.cpu(), e.cpu(), 32)
+    want = held.float().half()
+    within = (held.abs() - 0.5 * step <= 65504) & torch.isinf(want)
+    want = torch.where(within, torch.sign(held) * 65504, want.double())
+    assert torch.equal(out.double().cpu(), want)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("C", [64, 37])
+def test_gated_unit_at_the_largest_numbers(gs, act, dt, C):
+    """At a type's largest numbers act is v or 0 and its derivative 1 or 0: no NaN."""
+    top = TOP[dt]
+    gate = torch.where(torch.arange(C) % 2 == 0, torch.tensor(top), torch.tensor(-top)).to(dt)[None].repeat(3, 1)
+    up, dh = torch.full((3, C), 0.5).to(dt), torch.full((3, C), 0.25).to(dt)
+    h = torch.empty(3, C, dtype=dt, device="cuda")
+    g8, u8 = gs.act8_empty(3, C), gs.act8_empty(3, C)
+    gs.gs_glu_fwd(gate.cuda(), up.cuda(), h, *g8, *u8, act=act)
+    on = (gate > 0).double()
+    assert torch.equal(h.double().cpu().abs(), on * float(torch.tensor(top).to(dt).double() * 0.5))
+    dg, du = torch.empty_like(h), torch.empty_like(h)
+    gs.gs_glu_bwd(*g8, *u8, dh.cuda(), dg, du, act=act)
+    assert torch.equal(dg.double().cpu().abs(), on * 0.125)
+    held = torch.finfo(torch.float32).max  # the checkpoint's values are taken in fp32
+    want = (torch.tensor(held) * 0.25).to(dt).double()
+    assert torch.equal(du.double().cpu().abs(), on * want)
