@@ -488,12 +488,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (t >= p.tokens) continue;
           const uint8_t* src = e + t * es + g;
           if (words && g + 4 <= groups) {
-            x[i][h] = __ldg(reinterpret_cast<const uint32_t*>(src));
+            x[i][h] = *reinterpret_cast<const uint32_t*>(src);
           } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               if (g + j < groups)
-                x[i][h] = (x[i][h] & ~(0xffu << 8 * j)) | (uint32_t)__ldg(src + j) << 8 * j;
+                x[i][h] = (x[i][h] & ~(0xffu << 8 * j)) | (uint32_t)src[j] << 8 * j;
           }
         }
       }

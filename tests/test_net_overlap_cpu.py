@@ -97,3 +97,11 @@ def test_nothing_is_read_before_the_wait(file, name, sig, body):
         if re.search(r"\b%s\s*\(" % fn, code) and _reads(text, pointers):
             found.append("%s()" % fn)
     assert not found, "%s touches global memory before its wait: %s" % (name, found)
+
+
+@pytest.mark.parametrize("file", sorted({k[0] for k in KERNELS} | {"net_common.cuh"}))
+def test_no_loads_of_data_that_never_changes(file):
+    """Such loads (__ldg, ld.global.nc, const __restrict__) are for data that nobody writes
+    while the kernel runs; what the kernel before writes is not, as that may still run."""
+    found = re.findall(r"__ldg|\.nc\b|__restrict__|__ldcs|__ldlu", _source(os.path.join(CSRC, file)))
+    assert not found, (file, found)
