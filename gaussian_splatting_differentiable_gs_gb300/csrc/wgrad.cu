@@ -74,7 +74,7 @@ static_assert(kTeams <= kStages && kTeams <= kRaw, "rings");
 constexpr int kMaxClusters = 128;
 constexpr size_t kPartialFloats = (size_t)128 * kBN;  // one CTA's half tile
 constexpr unsigned int kErrTimeout = 1u;
-constexpr long long kWaitNs = 2000000000ll;
+constexpr int64_t kWaitNs = 2000000000;
 
 struct Plan {
   int64_t tokens;
@@ -89,6 +89,8 @@ struct Plan {
   int64_t rem_steps, quota;    // their steps, and a cluster's share
   int64_t dws;
   int32_t accumulate;
+  uint32_t exp_steps;  // steps whose exponents are brought: all, but in the self-test
+  int64_t wait_ns;     // after which a wait gives up
 };
 
 // A cluster's steps one by one: its whole tiles, then its share of the dealt-out
@@ -218,30 +220,90 @@ struct Control {
   uint64_t full[kStages], empty[kStages];        // both operands of both CTAs (the first's)
   uint64_t acc_full, acc_empty;
   uint32_t tmem;
-  volatile uint32_t abort;
+  // when a role ends: steps whose copies and products it asked for, runs, steps decoded
+  uint32_t dy_steps, raw_steps, products, runs, decoded[kDecodeWarps];
+  volatile uint32_t abort;                       // a wait of the pair gave up
 };
 
-// Waits for a barrier's phase, at most kWaitNs; false (and the status word
-// set) when that ran out or another wait of this CTA gave up.
+__device__ __forceinline__ int64_t now_ns() {
+  int64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+// A word of the Control of the pair's CTA `rank`.
+__device__ __forceinline__ uint32_t load_pair(const volatile uint32_t* word, uint32_t rank) {
+  uint32_t v;
+  asm volatile(
+      "{\n.reg .b32 a;\nmapa.shared::cluster.u32 a, %1, %2;\nld.shared::cluster.u32 %0, [a];\n}"
+      : "=r"(v)
+      : "r"(smem_u32((const void*)word)), "r"(rank)
+      : "memory");
+  return v;
+}
+__device__ __forceinline__ void store_pair(volatile uint32_t* word, uint32_t rank, uint32_t v) {
+  asm volatile("{\n.reg .b32 a;\nmapa.shared::cluster.u32 a, %0, %1;\nst.shared::cluster.u32 [a], %2;\n}" ::"r"(
+                   smem_u32((const void*)word)),
+               "r"(rank), "r"(v)
+               : "memory");
+}
+
+// Waits for a barrier's phase, at most p.wait_ns; false (and the status word set) when
+// that ran out or another wait of the pair gave up.
 __device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, Control* c,
-                                            unsigned int* status) {
-  long long t0, t1;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+                                               const Plan& p, unsigned int* status) {
+  const int64_t t0 = now_ns();
   while (true) {
     if (mbar_try(bar, parity)) return true;
     if (c->abort) return false;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t1));
-    if (t1 - t0 > kWaitNs) {
-      c->abort = 1;
+    if (now_ns() - t0 > p.wait_ns) {
+      store_pair(&c->abort, 0, 1);
+      store_pair(&c->abort, 1, 1);
       atomicOr(status, kErrTimeout);
       return false;
     }
   }
 }
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, Control* c,
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, Control* c, const Plan& p,
                                           unsigned int* status) {
   if (mbar_try(bar, parity)) return true;
-  return mbar_wait_slow(bar, parity, c, status);
+  return mbar_wait_slow(bar, parity, c, p, status);
+}
+
+// After giving up: one thread of each CTA waits, at most p.wait_ns in all, until nothing
+// of the pair is under way that writes shared memory or TMEM: copies of bytes and of dy,
+// products, and the arrivals at their end.  Every role of both CTAs has ended, so the
+// steps that were asked for are known.
+__device__ __forceinline__ void drain(Control* c, const Plan& p, uint32_t rank) {
+  const int64_t until = now_ns() + p.wait_ns;
+  auto wait = [&](uint64_t* ring, int places, uint32_t step) {  // the phase that `step` ends
+    while (!mbar_try(smem_u32(&ring[step % places]), step / places & 1) && now_ns() < until) {}
+  };
+  auto last = [&](uint64_t* ring, int places, uint32_t steps) {
+    for (uint32_t i = steps < places ? 0 : steps - places; i < steps; ++i) wait(ring, places, i);
+  };
+  last(c->raw_full, kRaw, c->raw_steps);
+  last(c->empty, kStages, load_pair(&c->products, 0));
+  if (const uint32_t runs = load_pair(&c->runs, 0)) wait(&c->acc_full, 1, runs - 1);
+  if (rank) return;
+  // dy's copies of both CTAs end at the first one's barriers, at whose steps what else was
+  // to arrive is made up for: X8 of decoding warps that gave up, and dy's other half where
+  // only one CTA asked for its own.
+  const uint32_t own = c->dy_steps, other = load_pair(&c->dy_steps, 1), steps = max(own, other);
+  const uint32_t half = (uint32_t)(p.bn / 2 * kBT * 2);
+  for (uint32_t i = steps < kStages ? 0 : steps - kStages; i < steps; ++i) {
+    const uint32_t bar = smem_u32(&c->full[i % kStages]);
+    uint32_t missing = 0;
+    for (uint32_t w = i % kTeams * kTeamWarps, n = 0; n < kTeamWarps; ++w, ++n)
+      missing += (c->decoded[w] <= i) + (load_pair(&c->decoded[w], 1) <= i);
+    if (i >= own) mbar_expect(bar, half);
+    if (i >= other)
+      asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cluster.b64 [%0], %1;" ::"r"(in_cta0(bar)),
+                   "r"(half)
+                   : "memory");
+    if (missing)
+      asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(missing) : "memory");
+  }
+  last(c->full, kStages, steps);
 }
 
 __device__ __forceinline__ void tma_load_own(uint32_t dst, const CUtensorMap* map, int x, int y,
@@ -377,6 +439,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     mbar_init(smem_u32(&c->acc_full), 1);
     mbar_init(smem_u32(&c->acc_empty), 2 * kEpiWarps);
+    c->dy_steps = c->raw_steps = c->products = c->runs = 0;
     c->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -402,10 +465,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t bars = in_cta0(smem_u32(&c->full[0])), bytes = (uint32_t)(half * kBT * 2 * 2);
     const uint32_t total = (uint32_t)cluster_steps(p, cluster);
     Walk w(p, cluster);
-    uint32_t st = 0, phase = 0;
-    for (uint32_t it = 0; it < total; ++it) {
+    uint32_t st = 0, phase = 0, it = 0;
+    for (; it < total; ++it) {
       w.next();
-      if (!mbar_wait(smem_u32(&c->empty[st]), phase ^ 1, c, status)) break;
+      if (!mbar_wait(smem_u32(&c->empty[st]), phase ^ 1, c, p, status)) break;
       if (issues) {
         if (rank == 0) mbar_expect(smem_u32(&c->full[st]), bytes);
         const uint32_t dst = smem_u32(smem) + st * kBBytes;
@@ -415,9 +478,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (++st == kStages) st = 0, phase ^= 1;
     }
+    if (issues) c->dy_steps = it;
     // the last products release the last stages: every arrival is in before this CTA ends
     for (uint32_t i = total < kStages ? 0 : total - kStages; i < total; ++i)
-      if (!mbar_wait(smem_u32(&c->empty[i % kStages]), (i / kStages) & 1, c, status)) break;
+      if (!mbar_wait(smem_u32(&c->empty[i % kStages]), (i / kStages) & 1, c, p, status)) break;
   } else if (warp == 1) {
     // ---- products ----------------------------------------------------------
     // The whole warp walks the steps, so that what it computes stays in uniform
@@ -428,15 +492,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint64_t b_first = smem_desc(smem_u32(smem));
       const int64_t total = cluster_steps(p, cluster);
       Walk w(p, cluster);
-      uint32_t st = 0, phase = 0, acc_phase = 1;
+      uint32_t st = 0, phase = 0, acc_phase = 1, runs = 0;
       bool begins = true;  // a run of products
-      for (int64_t it = 0; it < total; ++it) {
+      int64_t it = 0;
+      for (; it < total; ++it) {
         w.next();
         if (begins) {
-          if (!mbar_wait(smem_u32(&c->acc_empty), acc_phase, c, status)) break;
+          if (!mbar_wait(smem_u32(&c->acc_empty), acc_phase, c, p, status)) break;
           acc_phase ^= 1;
         }
-        if (!mbar_wait(smem_u32(&c->full[st]), phase, c, status)) break;
+        if (!mbar_wait(smem_u32(&c->full[st]), phase, c, p, status)) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint32_t a = tmem + kBN + st * kAColumns;
         const uint64_t b = b_first + st * (kBBytes >> 4);
@@ -449,24 +514,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (ends) mma_commit(smem_u32(&c->acc_full));
         }
         begins = ends;
+        runs += ends;
         if (++st == kStages) st = 0, phase ^= 1;
       }
+      if (issues) c->products = (uint32_t)it, c->runs = runs;
     }
   } else if (warp == 3) {
     // ---- the checkpoint's bytes by TMA -------------------------------------
     const bool issues = elect_one();
     Walk w(p, cluster);
-    uint32_t rs = 0, phase = 0;
+    uint32_t rs = 0, phase = 0, steps = 0;
     while (w.next()) {
-      if (!mbar_wait(smem_u32(&c->raw_empty[rs]), phase ^ 1, c, status)) break;
+      if (!mbar_wait(smem_u32(&c->raw_empty[rs]), phase ^ 1, c, p, status)) break;
       if (issues) {
         const uint32_t bar = smem_u32(&c->raw_full[rs]);
         mbar_expect(bar, kRawBytes);
         tma_load_own(smem_u32(raw_q) + rs * kRawBytes, &q_map, w.ch0 + (int)rank * 128, w.ts * kBT,
                      bar);
       }
+      ++steps;
       if (++rs == kRaw) rs = 0, phase ^= 1;
     }
+    if (issues) c->raw_steps = steps;
   } else if (warp == 2) {
     // ---- and its exponents, kBatch steps at a time ---------------------------
     // Exponent rows start anywhere, so they come by plain loads; the arrival
@@ -474,7 +543,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     Walk w(p, cluster);
     const int groups = (p.channels + GS_ACT8_GROUP - 1) / GS_ACT8_GROUP;
     const bool words = ((es | (int64_t)(uintptr_t)e) & 3) == 0;
-    const uint32_t total = (uint32_t)cluster_steps(p, cluster);
+    const uint32_t total = min((uint32_t)cluster_steps(p, cluster), p.exp_steps);
     for (uint32_t it0 = 0; it0 < total; it0 += kBatch) {
       uint32_t x[kBatch][2];  // four groups of tokens 2 lane and 2 lane + 1
 #pragma unroll
@@ -499,7 +568,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       const uint32_t n = it0 / kBatch, bs = n % kBatches;
       if (!__all_sync(0xffffffffu,
-                      mbar_wait(smem_u32(&c->exp_empty[bs]), ((n / kBatches) & 1) ^ 1, c, status)))
+                      mbar_wait(smem_u32(&c->exp_empty[bs]), ((n / kBatches) & 1) ^ 1, c, p, status)))
         break;
       uint32_t* to = reinterpret_cast<uint32_t*>(raw_e + bs * kBatch * kExpBytes) + lane;
 #pragma unroll
@@ -525,7 +594,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     Walk w(p, cluster);
     while (w.next()) {
       if (!w.run_ends()) continue;
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&c->acc_full), phase, c, status))) break;
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&c->acc_full), phase, c, p, status))) break;
       phase ^= 1;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t from = tmem + c0 + ((uint32_t)(quarter * 32) << 16);
@@ -580,11 +649,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t full = in_cta0(smem_u32(&c->full[0]));
     const uint32_t total = (uint32_t)cluster_steps(p, cluster);
     uint32_t st = team, st_phase = 0, rs = team, rs_phase = 0, slot = team, slot_phase = 0;
-    for (uint32_t it = team; it < total; it += kTeams) {
+    uint32_t it = team;
+    for (; it < total; it += kTeams) {
       if (!__all_sync(0xffffffffu,
-                      mbar_wait(smem_u32(&c->exp_full[slot / kBatch]), slot_phase, c, status) &&
-                          mbar_wait(smem_u32(&c->raw_full[rs]), rs_phase, c, status) &&
-                          mbar_wait(smem_u32(&c->empty[st]), st_phase ^ 1, c, status)))
+                      mbar_wait(smem_u32(&c->exp_full[slot / kBatch]), slot_phase, c, p, status) &&
+                          mbar_wait(smem_u32(&c->raw_full[rs]), rs_phase, c, p, status) &&
+                          mbar_wait(smem_u32(&c->empty[st]), st_phase ^ 1, c, p, status)))
         break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t bytes = rs * kRawBytes, step_at = steps + slot * kExpBytes;
@@ -618,16 +688,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if ((rs += kTeams) >= kRaw) rs -= kRaw, rs_phase ^= 1;
       if ((slot += kTeams) >= kBatch * kBatches) slot -= kBatch * kBatches, slot_phase ^= 1;
     }
+    if (lane == 0) c->decoded[warp - 4 - kEpiWarps] = it;
   }
 
-  // Every role is done or gave up.  After giving up, copies may still be in
-  // flight into this CTA's shared memory: leave them time to land.
+  // Every role of both CTAs is done, or gave up: then both know.
   __syncthreads();
   __syncwarp();
-  if (c->abort)
-    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   cluster_sync();
+  if (c->abort) {
+    if (threadIdx.x == 0) drain(c, p, rank);
+    __syncthreads();
+    __syncwarp();
+    cluster_sync();  // neither CTA ends while the other looks at it
+  }
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   if (warp == 2)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
@@ -773,11 +847,14 @@ extern "C" size_t gs_act8_wgrad_workspace_bytes(int64_t tokens, int32_t rows, in
          sizeof(__nv_bfloat16) * terms_of(dtype) * padded_tokens(tokens) * padded_rows(rows);
 }
 
-extern "C" gs_status gs_act8_wgrad(int64_t tokens, int32_t rows, int32_t channels, int32_t dtype,
-                                   const void* dy, int64_t dy_stride, const int8_t* q,
-                                   int64_t q_stride, const uint8_t* e, int64_t e_stride, void* dw,
-                                   int64_t dw_stride, int32_t out_dtype, int32_t accumulate,
-                                   void* workspace, size_t ws_bytes, void* stream) {
+namespace {
+
+// exp_steps, wait_ns: see Plan.
+gs_status weight_gradient(int64_t tokens, int32_t rows, int32_t channels, int32_t dtype,
+                          const void* dy, int64_t dy_stride, const int8_t* q, int64_t q_stride,
+                          const uint8_t* e, int64_t e_stride, void* dw, int64_t dw_stride,
+                          int32_t out_dtype, int32_t accumulate, void* workspace, size_t ws_bytes,
+                          uint32_t exp_steps, int64_t wait_ns, void* stream) {
   if (tokens < 0 || tokens >= ((int64_t)1 << 31) || rows < 1 || channels < 1 || !dtype_ok(dtype) ||
       (out_dtype != GS_F32 && out_dtype != GS_BF16) || !dw ||
       !aligned_to(dw, dtype_size(out_dtype)) || !workspace || !aligned16(workspace) ||
@@ -808,6 +885,8 @@ extern "C" gs_status gs_act8_wgrad(int64_t tokens, int32_t rows, int32_t channel
   p.bn = rows > 128 ? 256 : 128;
   p.dws = dw_stride;
   p.accumulate = accumulate != 0;
+  p.exp_steps = exp_steps;
+  p.wait_ns = wait_ns;
   float* partial = (float*)((char*)workspace + kHeader);
 
   // dy as the tensor map reads it
@@ -885,4 +964,30 @@ extern "C" gs_status gs_act8_wgrad(int64_t tokens, int32_t rows, int32_t channel
                                 (__nv_bfloat16*)dw));
   }
   return GS_OK;
+}
+
+}  // namespace
+
+extern "C" gs_status gs_act8_wgrad(int64_t tokens, int32_t rows, int32_t channels, int32_t dtype,
+                                   const void* dy, int64_t dy_stride, const int8_t* q,
+                                   int64_t q_stride, const uint8_t* e, int64_t e_stride, void* dw,
+                                   int64_t dw_stride, int32_t out_dtype, int32_t accumulate,
+                                   void* workspace, size_t ws_bytes, void* stream) {
+  return weight_gradient(tokens, rows, channels, dtype, dy, dy_stride, q, q_stride, e, e_stride, dw,
+                         dw_stride, out_dtype, accumulate, workspace, ws_bytes, UINT32_MAX, kWaitNs,
+                         stream);
+}
+
+extern "C" gs_status gs_selftest_wgrad_timeout(int64_t tokens, int32_t rows, int32_t channels,
+                                               const void* dy, const int8_t* q, const uint8_t* e,
+                                               void* dw, void* workspace, size_t ws_bytes,
+                                               int32_t steps, void* stream) {
+  // The exponents stop after `steps` steps of 64 tokens (a multiple of kBatch), so that the
+  // decoding warps, and with them every other role, wait for what never comes: 20 ms.
+  if (steps < 0) return GS_ERR_INVALID_ARG;
+  const int64_t ld = div_up(channels, GS_ACT8_GROUP) * GS_ACT8_GROUP;
+  const gs_status s = weight_gradient(tokens, rows, channels, GS_BF16, dy, rows, q, ld, e,
+                                      ld / GS_ACT8_GROUP, dw, channels, GS_F32, 0, workspace,
+                                      ws_bytes, (uint32_t)steps, 20000000, stream);
+  return s != GS_OK ? s : gs_workspace_status(workspace, stream);
 }

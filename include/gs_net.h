@@ -199,6 +199,16 @@ gs_status gs_act8_wgrad(int64_t tokens, int32_t rows, int32_t channels, int32_t 
                         int32_t out_dtype, int32_t accumulate, void* workspace, size_t ws_bytes,
                         void* stream);
 
+/* Self-test of gs_act8_wgrad's bounded waits: the call in bf16 with contiguous
+ * arrays and an fp32 dw, whose exponents stop after `steps` steps of 64 tokens
+ * per pair of SMs (in eights), so that its waits run out, after 20 ms instead of
+ * two seconds; the kernel waits for its copies under way, flags the error and
+ * ends, and the call synchronises and returns GS_ERR_TIMEOUT (GS_OK where
+ * `steps` were enough).  dw is left undefined, the context stays usable. */
+gs_status gs_selftest_wgrad_timeout(int64_t tokens, int32_t rows, int32_t channels,
+                                    const void* dy, const int8_t* q, const uint8_t* e, void* dw,
+                                    void* workspace, size_t ws_bytes, int32_t steps, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
