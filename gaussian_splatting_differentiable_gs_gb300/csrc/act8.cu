@@ -322,45 +322,56 @@ __device__ __forceinline__ float reciprocal(float v) {
   return r;
 }
 
-// act(v) and its derivative for two values.  Phi comes from Abramowitz and
-// Stegun's formula 7.1.26 for the error function (absolute error below 1.5e-7, half
-// of that in Phi), which needs the one exponential that the derivative has too; its
-// arithmetic takes two values an instruction (8160 x 1361 fp16: 72 us, 75 without).
-// The same elsewhere in these kernels costs the aligned form registers, and thereby
-// warps: 238 us in place of 230 at 32640 x 2816 bf16.
+// Phi and its density for two values.  16-bit types take Abramowitz and Stegun's formula
+// 7.1.26 for the error function, which needs the one exponential that the derivative has
+// too; in this arithmetic Phi is off by up to 2.6e-7, a thousandth of fp16's rounding of
+// values near 1 (in the tail, where Phi is small, by up to a third of itself: below that
+// rounding of v Phi's terms).  It takes two values an instruction (8160 x 1361 fp16: 72 us,
+// 75 without).  The same elsewhere in these kernels costs the aligned form registers, and
+// thereby warps: 238 us in place of 230 at 32640 x 2816 bf16.  fp32 takes the complementary
+// error function, which keeps its relative accuracy in the tail.
 struct Phi {
   float2 p, density;  // Phi(v), phi(v)
 };
+template <typename T>
 __device__ __forceinline__ Phi normal(float2 v) {
-  const float2 z = make_float2(fabsf(v.x) * 0.70710678118654752f, fabsf(v.y) * 0.70710678118654752f);
-  const float2 y = fma2(both(0.3275911f), z, both(1.f));
-  const float2 t = make_float2(reciprocal(y.x), reciprocal(y.y));
-  const float2 w = mul2(mul2(z, z), both(-1.4426950408889634f));
-  const float2 ex = make_float2(power2(w.x), power2(w.y));
-  float2 q = fma2(both(0.5f * 1.061405429f), t, both(0.5f * -1.453152027f));
-  q = fma2(q, t, both(0.5f * 1.421413741f));
-  q = fma2(q, t, both(0.5f * -0.284496736f));
-  q = fma2(q, t, both(0.5f * 0.254829592f));
-  const float2 tail = mul2(mul2(q, t), ex), rest = fma2(tail, both(-1.f), both(1.f));
-  return Phi{make_float2(v.x < 0.f ? tail.x : rest.x, v.y < 0.f ? tail.y : rest.y),
-             mul2(ex, both(0.39894228040143268f))};
+  if constexpr (sizeof(T) == 4) {
+    const float2 w = mul2(mul2(v, v), both(-0.72134752044448170f));  // -v^2 / 2 in powers of two
+    return Phi{make_float2(0.5f * erfcf(v.x * -0.70710678118654752f),
+                           0.5f * erfcf(v.y * -0.70710678118654752f)),
+               mul2(make_float2(power2(w.x), power2(w.y)), both(0.39894228040143268f))};
+  } else {
+    const float2 z = make_float2(fabsf(v.x) * 0.70710678118654752f, fabsf(v.y) * 0.70710678118654752f);
+    const float2 y = fma2(both(0.3275911f), z, both(1.f));
+    const float2 t = make_float2(reciprocal(y.x), reciprocal(y.y));
+    const float2 w = mul2(mul2(z, z), both(-1.4426950408889634f));
+    const float2 ex = make_float2(power2(w.x), power2(w.y));
+    float2 q = fma2(both(0.5f * 1.061405429f), t, both(0.5f * -1.453152027f));
+    q = fma2(q, t, both(0.5f * 1.421413741f));
+    q = fma2(q, t, both(0.5f * -0.284496736f));
+    q = fma2(q, t, both(0.5f * 0.254829592f));
+    const float2 tail = mul2(mul2(q, t), ex), rest = fma2(tail, both(-1.f), both(1.f));
+    return Phi{make_float2(v.x < 0.f ? tail.x : rest.x, v.y < 0.f ? tail.y : rest.y),
+               mul2(ex, both(0.39894228040143268f))};
+  }
 }
+// act(v) and its derivative for two values.
 __device__ __forceinline__ float sigmoid(float v) {
   return reciprocal(1.f + power2(v * -1.4426950408889634f));
 }
-template <int ACT>
+template <typename T, int ACT>
 __device__ __forceinline__ float2 act_value(float2 v) {
   if (ACT == GS_ACT_SILU) return make_float2(v.x * sigmoid(v.x), v.y * sigmoid(v.y));
-  return mul2(v, normal(v).p);
+  return mul2(v, normal<T>(v).p);
 }
-template <int ACT>
+template <typename T, int ACT>
 __device__ __forceinline__ void act_both(float2 v, float2& f, float2& df) {
   if (ACT == GS_ACT_SILU) {
     const float s = sigmoid(v.x), u = sigmoid(v.y);
     f = make_float2(v.x * s, v.y * u);
     df = make_float2(s * (1.f + v.x * (1.f - s)), u * (1.f + v.y * (1.f - u)));
   } else {
-    const Phi n = normal(v);
+    const Phi n = normal<T>(v);
     f = mul2(v, n.p);
     df = fma2(v, n.density, n.p);
   }
@@ -379,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<WIDE>)
 #pragma unroll
       for (int j = 0; j < kPer; j += 2) {
         const float2 a = make_float2(hg.value(j), hg.value(j + 1));
-        float2 f = act_value<ACT>(a);
+        float2 f = act_value<T, ACT>(a);
         g[j] = a.x, g[j + 1] = a.y;
         if (GATED) {
           const float2 b = make_float2(hu.value(j), hu.value(j + 1));
@@ -411,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<WIDE>)
 #pragma unroll
       for (int j = 0; j < kPer; j += 2) {
         float2 f, df;
-        act_both<ACT>(make_float2(held8(hg, j, sg), held8(hg, j + 1, sg)), f, df);
+        act_both<T, ACT>(make_float2(held8(hg, j, sg), held8(hg, j + 1, sg)), f, df);
         const float2 d = make_float2(hd.value(j), hd.value(j + 1));
         const float2 w = GATED ? make_float2(held8(hu, j, su), held8(hu, j + 1, su)) : both(1.f);
         o[j] = WIDE || c + j < r.C ? f.x * w.x : 0.f;

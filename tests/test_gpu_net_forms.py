@@ -124,3 +124,42 @@ def test_gated_unit_at_the_largest_numbers(gs, act, dt, C):
     held = torch.finfo(torch.float32).max  # the checkpoint's values are taken in fp32
     want = (torch.tensor(held) * 0.25).to(dt).double()
     assert torch.equal(du.double().cpu().abs(), on * want)
+
+
+def test_fp32_gelu_keeps_its_relative_accuracy(gs):
+    """gelu(v) = v Phi(v) in fp32, in the tail too.  Phi is half the complementary error
+    function of -v / sqrt 2: 4 units in the last place (8 u) of the function, 2 u for the
+    halving's and product's roundings; the argument's rounding (constant and product, 2 u
+    relative) moves Phi by at most (v^2 + 1) times that where v < 0."""
+    v = torch.cat([-torch.logspace(-4, 0.9, 3000, dtype=torch.float64), torch.zeros(1, dtype=torch.float64),
+                   torch.logspace(-4, 1.5, 3000, dtype=torch.float64)]).float()
+    v = torch.cat([v, v[:7]])[:6008 // 8 * 8].view(8, -1)
+    tail = (v.double() ** 2 + 1) * (v < 0)
+    for width in (v.shape[1], v.shape[1] - 1):  # rows on 16-byte boundaries, and not
+        x = v[:, :width].cuda().contiguous()
+        h = torch.empty_like(x)
+        gs.gs_glu_fwd(x, None, h, act="gelu")
+        want = x.double() * 0.5 * torch.special.erfc(-x.double() / 2 ** 0.5)
+        err = (h.double() - want).abs().cpu()
+        bound = want.abs().cpu() * (12 + 2 * tail[:, :width]) * U + 1e-38
+        assert (err <= bound).all(), float((err / want.abs().cpu().clamp_min(1e-300) / U).max())
+
+
+def test_fp32_gelu_derivative(gs):
+    """dgate = dh (Phi + v phi) at the held values: the roundings above on Phi, and on
+    v phi those of its exponential (argument v^2 / 2 at 3 u, 4 u of its own) and of two products."""
+    q0 = torch.arange(-127, 128)
+    T, C = 8, 256
+    q = torch.zeros(T, C, dtype=torch.int8)
+    q[:, :255] = q0.to(torch.int8)
+    e = torch.empty(T, C // 32, dtype=torch.uint8)
+    for t in range(T):
+        e[t] = 127 - 4 - t  # steps 1/16 and finer
+    v = plain.decode(q, e, C)
+    dg = torch.empty(T, C, device="cuda")
+    gs.gs_glu_bwd(q.cuda(), e.cuda(), None, None, torch.ones(T, C, device="cuda"), dg, None, act="gelu")
+    phi = torch.exp(-0.5 * v * v) * (0.5 / torch.pi) ** 0.5
+    big = 0.5 * torch.special.erfc(-v / 2 ** 0.5)
+    bound = (big * (12 + 2 * (v * v + 1) * (v < 0)) + (v * phi).abs() * (8 + 2 * v * v)) * U + 2 * U * (big + v * phi).abs()
+    err = (dg.double().cpu() - (big + v * phi)).abs()
+    assert (err <= bound + 1e-38).all(), float((err / bound).max())
