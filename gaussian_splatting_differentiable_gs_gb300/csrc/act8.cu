@@ -95,7 +95,9 @@ __device__ __forceinline__ float held8(const Held8& h, int j, float step) {
 // with a derivative of 0 would be a NaN); other values of such a group lose a last place
 // at most.
 __device__ __forceinline__ float held_step(const Held8& h) {
-  return __uint_as_float((h.e << 23) - (h.e >= kAct8Top<float> && h.e < 255u ? 1u : 0u));
+  // signed, with one more in the exponent: 255 (a NaN) is the least then, and stays
+  const int bits = (int)((h.e + 1) << 23), top = (int)((kAct8Top<float> + 1) << 23) - 1;
+  return __int_as_float(min(bits, top) - (1 << 23));
 }
 
 // The first N words of z (N + 4 words) shifted down by s bytes (0 <= s < 16, even).

@@ -163,3 +163,21 @@ def test_fp32_gelu_derivative(gs):
     bound = (big * (12 + 2 * (v * v + 1) * (v < 0)) + (v * phi).abs() * (8 + 2 * v * v)) * U + 2 * U * (big + v * phi).abs()
     err = (dg.double().cpu() - (big + v * phi)).abs()
     assert (err <= bound + 1e-38).all(), float((err / bound).max())
+
+
+@pytest.mark.parametrize("C", [96, 70])
+def test_gated_unit_of_groups_that_are_not_numbers(gs, C):
+    """Such a group gives NaN in both gradients, its neighbours do not."""
+    gate, up, dh = (torch.randn(4, C, generator=_gen(i)) for i in range(3))
+    gate[1, 40], up[2, 3] = float("nan"), float("inf")
+    g8, u8 = gs.act8_empty(4, C), gs.act8_empty(4, C)
+    gs.gs_act8_encode(gate.cuda(), *g8)
+    gs.gs_act8_encode(up.cuda(), *u8)
+    dg, du = torch.empty(4, C, device="cuda"), torch.empty(4, C, device="cuda")
+    for act in ("silu", "gelu"):
+        gs.gs_glu_bwd(*g8, *u8, dh.cuda(), dg, du, act=act)
+        want = torch.zeros(4, C, dtype=torch.bool)
+        want[1, 32:64] = True
+        assert torch.equal(torch.isnan(du.cpu()), want)
+        want[2, :32] = True
+        assert torch.equal(torch.isnan(dg.cpu()), want)
