@@ -82,3 +82,25 @@ def test_norm_backward_after_the_calls_that_write_its_weights(gs, graph):
                              (o["dres_scale"], (gt * w * e).sum(0), (gt.abs() * w * mag).sum(0)),
                              (o["dw_post"], (gt * s * e).sum(0), (gt.abs() * s * mag).sum(0))):
             assert ((got.double().cpu() - want).abs() <= bound * m + 1e-30).all(), i
+
+
+def test_weight_gradient_after_the_calls_that_write_its_checkpoint(gs):
+    """Encoded into the same arrays each round, by the call right before."""
+    T, N, K, rounds = 300, 70, 96, 10
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(rounds, T, K, generator=g, device="cuda") * torch.exp2(
+        torch.randint(-8, 8, (rounds, T, 1), generator=g, device="cuda").float())
+    dy = torch.randn(T, N, generator=g, device="cuda").bfloat16()
+    ws = torch.zeros(gs.gs_act8_wgrad_workspace_bytes(T, N, K), dtype=torch.uint8, device="cuda")
+    want, got = (torch.empty(rounds, N, K, device="cuda") for _ in range(2))
+    for i in range(rounds):  # each with a checkpoint of its own, and a pause
+        q, e = gs.act8_empty(T, K)
+        gs.gs_act8_encode(x[i], q, e)
+        torch.cuda.synchronize()
+        gs.gs_act8_wgrad(dy, q, e, want[i], ws)
+        torch.cuda.synchronize()
+    q, e = gs.act8_empty(T, K)
+    for i in range(rounds):
+        gs.gs_act8_encode(x[i], q, e)
+        gs.gs_act8_wgrad(dy, q, e, got[i], ws)
+    assert torch.equal(got, want)
