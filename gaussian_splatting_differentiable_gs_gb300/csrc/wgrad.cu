@@ -831,6 +831,13 @@ int resident_clusters() {
   return n;
 }
 
+// dy's terms one after the other have to fit a tensor map's 32-bit coordinates, with the
+// rows that the last step reads beyond them.
+bool shape_ok(int64_t tokens, int32_t rows, int32_t channels, int32_t dtype) {
+  return tokens >= 0 && tokens < ((int64_t)1 << 31) && rows >= 1 && channels >= 1 &&
+         dtype_ok(dtype) && terms_of(dtype) * padded_tokens(tokens) <= ((int64_t)1 << 31) - kBT;
+}
+
 constexpr size_t kHeader = 256;
 size_t partial_bytes() { return sizeof(float) * kPartialFloats * 4 * kMaxClusters; }
 
@@ -841,8 +848,7 @@ using namespace gs;
 
 extern "C" size_t gs_act8_wgrad_workspace_bytes(int64_t tokens, int32_t rows, int32_t channels,
                                                 int32_t dtype) {
-  if (tokens < 0 || tokens >= ((int64_t)1 << 31) || rows < 1 || channels < 1 || !dtype_ok(dtype))
-    return 0;
+  if (!shape_ok(tokens, rows, channels, dtype)) return 0;
   return kHeader + partial_bytes() +
          sizeof(__nv_bfloat16) * terms_of(dtype) * padded_tokens(tokens) * padded_rows(rows);
 }
@@ -855,7 +861,7 @@ gs_status weight_gradient(int64_t tokens, int32_t rows, int32_t channels, int32_
                           const uint8_t* e, int64_t e_stride, void* dw, int64_t dw_stride,
                           int32_t out_dtype, int32_t accumulate, void* workspace, size_t ws_bytes,
                           uint32_t exp_steps, int64_t wait_ns, void* stream) {
-  if (tokens < 0 || tokens >= ((int64_t)1 << 31) || rows < 1 || channels < 1 || !dtype_ok(dtype) ||
+  if (!shape_ok(tokens, rows, channels, dtype) ||
       (out_dtype != GS_F32 && out_dtype != GS_BF16) || !dw ||
       !aligned_to(dw, dtype_size(out_dtype)) || !workspace || !aligned16(workspace) ||
       ws_bytes < gs_act8_wgrad_workspace_bytes(tokens, rows, channels, dtype))
@@ -915,7 +921,6 @@ gs_status weight_gradient(int64_t tokens, int32_t rows, int32_t channels, int32_
     height = p.terms * p.term_rows;
     stride = ld;
   }
-  if (height > ((int64_t)1 << 31) - kBT) return GS_ERR_INVALID_ARG;
   CUtensorMap map;
   const cuuint64_t dims[2] = {(cuuint64_t)rows, (cuuint64_t)height};
   const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};

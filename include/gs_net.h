@@ -187,7 +187,9 @@ gs_status gs_glu_bwd(int64_t tokens, int32_t channels, int32_t dtype, int32_t ac
  *               steps of 2^122, a magnitude above 127 * 2^121 that was
  *               rounded up, are an infinity there)
  *   dw          [rows][channels] of type out_dtype (GS_F32 or GS_BF16)
- *   workspace   gs_act8_wgrad_workspace_bytes(...) bytes, 16-byte aligned;
+ *   tokens      times the bf16 terms of dy's type (1 bf16, 2 fp16, 3 fp32) at
+ *               most 2^31 - 64 when rounded up to 64
+ *   workspace   gs_act8_wgrad_workspace_bytes(...) bytes (0: refused), 16-byte aligned;
  *               its first 256 bytes must be zero before the first call
  *               (gs_workspace_status reads them) and calls on one workspace
  *               must not overlap */

@@ -1,0 +1,29 @@
+"""CPU checks of the network operators' arguments at the C ABI: what is refused is refused
+before anything is enqueued (here nothing can be: there is no GPU)."""
+import ctypes as C
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def gs():
+    import __graft_entry__
+    __graft_entry__.build()
+    import gaussian_splatting_differentiable_gs_gb300 as gs
+    return gs
+
+
+def _aligned(size=1 << 16):
+    buf = C.create_string_buffer(size)
+    return buf, (C.addressof(buf) + 15) & ~15
+
+
+@pytest.mark.parametrize("dtype,tokens", [(2, 1 << 30), (1, 1 << 30), (0, (1 << 31) - 32), (2, 715827904)])
+def test_wgrad_refuses_lengths_beyond_the_tensor_map_first(gs, dtype, tokens):
+    """Two bf16 terms of an fp16 gradient, three of an fp32 one: 2^31 - 64 rows in all."""
+    keep, p = _aligned()
+    L = gs.lib()
+    call = lambda size: L.gs_act8_wgrad(tokens, 8, 8, dtype, p, 8, p, 32, p, 1, p, 8, 2, 0, p, size, None)  # noqa: E731
+    assert call(1 << 62) == gs.GS_ERR_INVALID_ARG
+    assert L.gs_act8_wgrad_workspace_bytes(tokens, 8, 8, dtype) == 0
+    assert L.gs_act8_wgrad_workspace_bytes(tokens // 4, 8, 8, dtype) > 0
