@@ -260,6 +260,10 @@ extern "C" gs_status gs_rope(int64_t tokens, int32_t n_axes, const int32_t* dims
     if (!s.heads) continue;
     if (!s.in || !s.out || !aligned_to(s.in, elem) || !aligned_to(s.out, elem))
       return GS_ERR_INVALID_ARG;
+    // in place with other strides, a head would be written before another one is read there
+    if (s.in == s.out && ((tokens > 1 && s.in_token != s.out_token) ||
+                          (s.heads > 1 && s.in_head != s.out_head)))
+      return GS_ERR_INVALID_ARG;
     copies |= s.in != s.out;
   }
 

@@ -53,7 +53,7 @@ gs_status gs_rope_turns(int32_t n_axes, const int32_t* dims, const double* base,
                         const double* scale, uint64_t* turns);
 
 /* One set of heads (queries, or keys): in and out [tokens][heads][head_dim].
- * out may equal in with the same strides (in place). */
+ * out may equal in with the same strides (in place; others are refused). */
 typedef struct gs_heads {
   const void* in;
   void* out;
@@ -64,7 +64,7 @@ typedef struct gs_heads {
 /* gs_rope -- rotates one or two sets of heads in one launch.
  *   dims, turns  (host) as given to and by gs_rope_turns
  *   positions    [tokens][n_axes] int32, any values
- *   sets         (host) n_sets = 1 or 2 sets, heads >= 0
+ *   sets         (host) n_sets = 1 or 2 sets, 0 <= heads <= 65536
  *   dtype        gs_dtype of the heads; the rotation is computed in fp32 */
 gs_status gs_rope(int64_t tokens, int32_t n_axes, const int32_t* dims, const uint64_t* turns,
                   int32_t interleaved, int32_t inverse, const int32_t* positions,

@@ -181,3 +181,21 @@ def test_gated_unit_of_groups_that_are_not_numbers(gs, C):
         assert torch.equal(torch.isnan(du.cpu()), want)
         want[2, :32] = True
         assert torch.equal(torch.isnan(dg.cpu()), want)
+
+
+def test_rope_in_place_where_a_stride_is_never_taken(gs):
+    """One token, or one head: the stride between them does not matter."""
+    import ctypes as C
+    rope = gs.Rope([8])
+    pos = torch.tensor([[3]] * 4, dtype=torch.int32).cuda()
+    x = torch.randn(4, 4, 8, generator=_gen(8)).cuda()
+    want = torch.empty_like(x)
+    gs.gs_rope(rope, pos, x, q_out=want)
+    for tokens, heads, strides in ((1, 4, (32, 8, 999, 8)), (4, 1, (32, 8, 32, 999)), (4, 4, (32, 8, 32, 8))):
+        y = x.clone()
+        sets = gs.net._HEADS.pack(y.data_ptr(), y.data_ptr(), *strides, heads)
+        assert gs.lib().gs_rope(tokens, 1, rope._dims, rope.turns, 0, 0, pos.data_ptr(), 8, 2, sets, 1,
+                                torch.cuda.current_stream().cuda_stream) == gs.GS_OK
+        assert torch.equal(y[:tokens, :heads], want[:tokens, :heads])
+        y[:tokens, :heads] = x[:tokens, :heads]
+        assert torch.equal(y, x)

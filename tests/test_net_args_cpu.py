@@ -27,3 +27,21 @@ def test_wgrad_refuses_lengths_beyond_the_tensor_map_first(gs, dtype, tokens):
     assert call(1 << 62) == gs.GS_ERR_INVALID_ARG
     assert L.gs_act8_wgrad_workspace_bytes(tokens, 8, 8, dtype) == 0
     assert L.gs_act8_wgrad_workspace_bytes(tokens // 4, 8, 8, dtype) > 0
+
+
+class Heads(C.Structure):  # gs_heads
+    _fields_ = [("src", C.c_void_p), ("dst", C.c_void_p), ("in_token", C.c_int64),
+                ("in_head", C.c_int64), ("out_token", C.c_int64), ("out_head", C.c_int64),
+                ("heads", C.c_int32)]
+
+
+def test_rope_refuses_in_place_with_other_strides(gs):
+    keep, p = _aligned()
+    r = gs.Rope([8])
+
+    def call(strides):
+        s = (Heads * 1)(Heads(p, p, *strides, 2))
+        return gs.lib().gs_rope(3, 1, r._dims, r.turns, 0, 0, p, 8, 0, s, 1, None)
+
+    assert call((32, 8, 16, 8)) == gs.GS_ERR_INVALID_ARG     # another stride between tokens
+    assert call((32, 8, 32, 16)) == gs.GS_ERR_INVALID_ARG    # between heads
