@@ -167,7 +167,8 @@ def _heads(src, dst, name, like):
     if (i1 != 1 or o1 != 1) and shape[2] > 1 and src.numel():
         raise ValueError("%s: the last axis must be contiguous" % name)
     a, b = src.data_ptr(), dst.data_ptr()
-    if a == b and (it != ot or ih != oh):
+    # (tensors without entries have no address)
+    if a == b and a and ((it != ot and shape[0] > 1) or (ih != oh and shape[1] > 1)):
         raise ValueError("%s: in place with other strides" % name)
     return _HEADS.pack(a, b, it, ih, ot, oh, shape[1])
 
