@@ -458,9 +458,8 @@ unsigned blocks_of(const RowsK& r) { return (unsigned)div_up(r.tokens, r.rows); 
 bool shape_ok(int64_t tokens, int32_t C, int32_t dtype) {
   return tokens >= 0 && tokens < ((int64_t)1 << 31) && C >= 1 && C <= (1 << 24) && dtype_ok(dtype);
 }
-bool ckpt_ok(const Act8K& k, int32_t C) {
-  return k.q && k.e && aligned16(k.q) && k.qs % 16 == 0 &&
-         k.qs >= div_up(C, GS_ACT8_GROUP) * GS_ACT8_GROUP;
+bool ckpt_ok(const Act8K& k, int64_t tokens, int32_t C) {
+  return gs::ckpt_ok(tokens, C, k.q, k.qs, k.e, k.es);
 }
 Act8K ckpt_of(const gs_ckpt* c) {
   return c ? Act8K{c->q, c->e, c->q_stride, c->e_stride} : Act8K{nullptr, nullptr, 0, 0};
@@ -498,7 +497,7 @@ extern "C" gs_status gs_act8_encode(int64_t tokens, int32_t channels, int32_t dt
   if (tokens == 0) return GS_OK;
   const Act8K k{q, e, q_stride, e_stride};
   const int el = dtype_size(dtype);
-  if (!x || !aligned_to(x, el) || !ckpt_ok(k, channels)) return GS_ERR_INVALID_ARG;
+  if (!x || !aligned_to(x, el) || !ckpt_ok(k, tokens, channels)) return GS_ERR_INVALID_ARG;
   const bool wide = channels % 8 == 0 && rows_aligned(x, x_stride, el, 16);
   const RowsK r = make_rows(tokens, channels);
   cudaStream_t st = (cudaStream_t)stream;
@@ -515,7 +514,7 @@ extern "C" gs_status gs_act8_decode(int64_t tokens, int32_t channels, int32_t dt
   if (tokens == 0) return GS_OK;
   const Act8K k{const_cast<int8_t*>(q), const_cast<uint8_t*>(e), q_stride, e_stride};
   const int el = dtype_size(dtype);
-  if (!x || !aligned_to(x, el) || !ckpt_ok(k, channels)) return GS_ERR_INVALID_ARG;
+  if (!x || !aligned_to(x, el) || !ckpt_ok(k, tokens, channels)) return GS_ERR_INVALID_ARG;
   const bool wide = channels % 8 == 0 && rows_aligned(x, x_stride, el, 16);
   const RowsK r = make_rows(tokens, channels);
   cudaStream_t st = (cudaStream_t)stream;
@@ -535,7 +534,7 @@ extern "C" gs_status gs_glu_fwd(int64_t tokens, int32_t channels, int32_t dtype,
   const Act8K g8 = ckpt_of(gate8), u8 = ckpt_of(up8);
   const int el = dtype_size(dtype);
   if (!gate || !h || !aligned_to(gate, el) || !aligned_to(up, el) || !aligned_to(h, el) ||
-      (g8.q && !ckpt_ok(g8, channels)) || (u8.q && (!up || !ckpt_ok(u8, channels))))
+      (g8.q && !ckpt_ok(g8, tokens, channels)) || (u8.q && (!up || !ckpt_ok(u8, tokens, channels))))
     return GS_ERR_INVALID_ARG;
   const bool wide = channels % 8 == 0 && rows_aligned(gate, gate_stride, el, 16) &&
                     rows_aligned(up, up_stride, el, 16) && rows_aligned(h, h_stride, el, 16);
@@ -568,7 +567,7 @@ extern "C" gs_status gs_glu_bwd(int64_t tokens, int32_t channels, int32_t dtype,
   if (tokens == 0) return GS_OK;
   const Act8K g8 = ckpt_of(gate8), u8 = ckpt_of(up8), o8 = ckpt_of(h8);
   const int el = dtype_size(dtype);
-  if (!ckpt_ok(g8, channels) || (u8.q && !ckpt_ok(u8, channels)) || (o8.q && !ckpt_ok(o8, channels)) || (!u8.q != !dup) ||
+  if (!ckpt_ok(g8, tokens, channels) || (u8.q && !ckpt_ok(u8, tokens, channels)) || (o8.q && !ckpt_ok(o8, tokens, channels)) || (!u8.q != !dup) ||
       !dh || !dgate || !aligned_to(dh, el) || !aligned_to(dgate, el) || !aligned_to(dup, el))
     return GS_ERR_INVALID_ARG;
   const bool wide = channels % 8 == 0 && rows_aligned(dh, dh_stride, el, 16) &&

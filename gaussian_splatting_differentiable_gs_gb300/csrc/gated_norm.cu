@@ -900,8 +900,7 @@ extern "C" gs_status gs_gated_norm_fwd(const gs_norm* p, const void* x, int64_t 
       !aligned16(stats) || !aligned_to(x, ex) || !aligned_to(block, eb) ||
       !aligned_to(x_out, ex) || !aligned_to(y, eb))
     return GS_ERR_INVALID_ARG;
-  if (y_q && (!aligned16(y_q) || q_stride % 16 ||
-              q_stride < div_up(p->channels, GS_ACT8_GROUP) * GS_ACT8_GROUP)) return GS_ERR_INVALID_ARG;
+  if (y_q && !ckpt_ok(p->tokens, p->channels, y_q, q_stride, y_e, e_stride)) return GS_ERR_INVALID_ARG;
   const int vec = 16 / eb;
   const bool wide = p->channels % vec == 0 && rows_aligned(x, x_stride, ex, 16) &&
                     rows_aligned(block, block_stride, eb, 16) &&

@@ -130,6 +130,14 @@ inline int device_sms() {
   return n;
 }
 
+// A checkpoint's arrays: whole groups of bytes, rows that do not overlap.
+inline bool ckpt_ok(int64_t tokens, int32_t channels, const int8_t* q, int64_t q_stride,
+                    const uint8_t* e, int64_t e_stride) {
+  const int64_t groups = div_up(channels, GS_ACT8_GROUP);
+  return q && e && aligned16(q) && q_stride % 16 == 0 && q_stride >= groups * GS_ACT8_GROUP &&
+         (tokens < 2 || e_stride >= groups);
+}
+
 // ---- the 8-bit checkpoint's format ---------------------------------------
 // Exponent of a group from the bits of its largest magnitude: 127 = 1.984375
 // * 2^6, so a magnitude m * 2^p (1 <= m < 2) fits 127 steps of 2^(p - 6) when

@@ -866,9 +866,8 @@ gs_status weight_gradient(int64_t tokens, int32_t rows, int32_t channels, int32_
       !aligned_to(dw, dtype_size(out_dtype)) || !workspace || !aligned16(workspace) ||
       ws_bytes < gs_act8_wgrad_workspace_bytes(tokens, rows, channels, dtype))
     return GS_ERR_INVALID_ARG;
-  if (tokens > 0 && (!dy || !q || !e || !aligned_to(dy, dtype_size(dtype)) || !aligned16(q) ||
-                     q_stride % 16 ||
-                     q_stride < div_up(channels, GS_ACT8_GROUP) * GS_ACT8_GROUP))
+  if (tokens > 0 && (!dy || !aligned_to(dy, dtype_size(dtype)) ||
+                     !ckpt_ok(tokens, channels, q, q_stride, e, e_stride)))
     return GS_ERR_INVALID_ARG;
   cudaStream_t st = (cudaStream_t)stream;
   const size_t out_elem = dtype_size(out_dtype);

@@ -143,7 +143,7 @@ gs_status gs_gated_norm_bwd(const gs_norm* p, const void* x_out, int64_t x_strid
  * number (above 65024 in fp16, above 127 * 2^121 in bf16 and fp32).  Only a group with an infinity or a NaN,
  * which has e = 255 and q = 0, reads back as NaN.  Storage: q int8 [tokens][ld], e uint8 [tokens][ld / 32]
  * with ld = C rounded up to 32 (the padding is zero); q rows are 16-byte
- * aligned (q_stride a multiple of 16, at least ld). */
+ * aligned (q_stride a multiple of 16, at least ld; e_stride at least ld / 32). */
 #define GS_ACT8_GROUP 32
 
 gs_status gs_act8_encode(int64_t tokens, int32_t channels, int32_t dtype, const void* x,

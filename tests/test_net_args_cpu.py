@@ -45,3 +45,34 @@ def test_rope_refuses_in_place_with_other_strides(gs):
 
     assert call((32, 8, 16, 8)) == gs.GS_ERR_INVALID_ARG     # another stride between tokens
     assert call((32, 8, 32, 16)) == gs.GS_ERR_INVALID_ARG    # between heads
+
+
+class Norm(C.Structure):  # gs_norm
+    _fields_ = [("tokens", C.c_int64), ("channels", C.c_int32), ("groups", C.c_int32),
+                ("flags", C.c_int32), ("dtype", C.c_int32), ("res_dtype", C.c_int32),
+                ("eps", C.c_float), ("w_pre", C.c_void_p), ("w_post", C.c_void_p),
+                ("res_scale", C.c_void_p), ("gate", C.c_void_p), ("group_offsets", C.c_void_p)]
+
+
+class Ckpt(C.Structure):  # gs_ckpt
+    _fields_ = [("q", C.c_void_p), ("e", C.c_void_p), ("q_stride", C.c_int64),
+                ("e_stride", C.c_int64)]
+
+
+@pytest.mark.parametrize("es", [0, 1, -2])
+def test_exponent_rows_must_not_overlap(gs, es):
+    """40 channels: two exponents a row."""
+    keep, p = _aligned()
+    L, bad = gs.lib(), gs.GS_ERR_INVALID_ARG
+    ws = gs.gs_act8_wgrad_workspace_bytes(2, 8, 40)
+    good, short = Ckpt(p, p, 64, 2), Ckpt(p, p, 64, es)
+    r = C.byref
+    assert L.gs_act8_encode(2, 40, 0, p, 40, p, 64, p, es, None) == bad
+    assert L.gs_act8_decode(2, 40, 0, p, 64, p, es, p, 40, None) == bad
+    assert L.gs_glu_fwd(2, 40, 0, 0, p, 40, p, 40, p, 40, r(short), r(good), None) == bad
+    assert L.gs_glu_fwd(2, 40, 0, 0, p, 40, p, 40, p, 40, r(good), r(short), None) == bad
+    for cks in ((short, good, good), (good, short, good), (good, good, short)):
+        assert L.gs_glu_bwd(2, 40, 0, 0, r(cks[0]), r(cks[1]), p, 40, p, 40, p, 40, r(cks[2]), None) == bad
+    n = Norm(2, 40, 1, 1, 0, 0, 1e-6)
+    assert L.gs_gated_norm_fwd(r(n), p, 40, p, 40, p, 40, p, 40, p, p, 64, p, es, None) == bad
+    assert L.gs_act8_wgrad(2, 8, 40, 0, p, 8, p, 64, p, es, p, 40, 2, 0, p, ws, None) == bad
