@@ -47,15 +47,17 @@ _HEADS = struct.Struct("PPqqqqi4x")
 _CKPT = struct.Struct("PPqq")
 _NO_CKPT = _CKPT.pack(0, 0, 0, 0)
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _stream(stream, t):
-    """The given stream, or the current one of the tensor's device."""
-    return _raw_stream(t.get_device()) if stream is None else stream.cuda_stream
+    """The given stream, or the current one; kernels run on the current device."""
+    device = t.get_device()
+    if device != _current_device():
+        raise ValueError("tensors on cuda:%d, but the current device is cuda:%d"
+                         % (device, _current_device()))
+    return _raw_stream(device) if stream is None else stream.cuda_stream
 
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
 
 
 def _refuse_mat(t, name, shape, dtype):

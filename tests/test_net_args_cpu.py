@@ -76,3 +76,23 @@ def test_exponent_rows_must_not_overlap(gs, es):
     n = Norm(2, 40, 1, 1, 0, 0, 1e-6)
     assert L.gs_gated_norm_fwd(r(n), p, 40, p, 40, p, 40, p, 40, p, p, 64, p, es, None) == bad
     assert L.gs_act8_wgrad(2, 8, 40, 0, p, 8, p, 64, p, es, p, 40, 2, 0, p, ws, None) == bad
+
+
+def test_tensors_of_another_device_than_the_current_one_are_refused(gs, monkeypatch):
+    """The library launches on the current device, so that is whose stream is taken."""
+    class Tensor:
+        def __init__(self, device):
+            self.device = device
+
+        def get_device(self):
+            return self.device
+
+    class Stream:
+        cuda_stream = 77
+
+    monkeypatch.setattr(gs.net, "_current_device", lambda: 1)
+    monkeypatch.setattr(gs.net, "_raw_stream", lambda device: 1000 + device)
+    assert gs.net._stream(None, Tensor(1)) == 1001 and gs.net._stream(Stream, Tensor(1)) == 77
+    for stream in (None, Stream):
+        with pytest.raises(ValueError, match="current device"):
+            gs.net._stream(stream, Tensor(0))
