@@ -7,6 +7,7 @@ gaussian_splatting_differentiable_gs_gb300/_build/ (git-ignored).
 import concurrent.futures as cf
 import glob
 import os
+import re
 import subprocess
 import sys
 
@@ -35,12 +36,28 @@ def _deps():
         os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__)]
 
 
+def _check_registers(src, log):
+    """A kernel whose warps share out the registers of its launch states their number
+    (kLaunchRegs, in the file of <file>_kernel); the library refuses to launch it with
+    any other.  Raises here if the compiler gave another number."""
+    want = re.search(r"kLaunchRegs = (\d+)", open(src).read())
+    if not want:
+        return
+    kernel = os.path.basename(src)[:-3] + "_kernel"
+    used = [int(n) for n in re.findall(
+        r"Compiling entry function '\w*?\d%s\w*'(?:(?!Compiling)[\s\S])*?Used (\d+) registers" % kernel, log)]
+    if not used or set(used) != {int(want.group(1))}:
+        raise RuntimeError("%s: %s was given %s registers a thread, its launch needs %s"
+                           % (src, kernel, sorted(set(used)) or "no known number of", want.group(1)))
+
+
 def _compile(src, verbose):
     obj = os.path.join(OUT, os.path.basename(src) + ".o")
-    cmd = [_nvcc()] + ARCH + FLAGS + (["-Xptxas", "-v"] if verbose else []) + ["-c", src, "-o", obj]
+    cmd = [_nvcc()] + ARCH + FLAGS + ["-Xptxas", "-v", "-c", src, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("nvcc failed for %s:\n%s%s" % (src, r.stdout, r.stderr))
+    _check_registers(src, r.stderr)
     return obj, r.stderr
 
 

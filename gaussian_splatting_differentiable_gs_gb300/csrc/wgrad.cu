@@ -808,12 +808,11 @@ int resident_clusters() {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
   int n = known[dev].load(std::memory_order_acquire);
   if (n) return n;
-  for (const void* f : {(const void*)wgrad_kernel<float>, (const void*)wgrad_kernel<__nv_bfloat16>})
-{
+  for (const void* f : {(const void*)wgrad_kernel<float>, (const void*)wgrad_kernel<__nv_bfloat16>}) {
     cudaFuncAttributes a;
     if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
         cudaFuncGetAttributes(&a, f) != cudaSuccess || a.numRegs != kLaunchRegs)
-      return 0;  // other registers at launch than the roles were given
+      return 0;  // (the build checks the registers that the roles share out)
   }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(2);

@@ -59,7 +59,6 @@ def _stream(stream, t):
     return _raw_stream(device) if stream is None else stream.cuda_stream
 
 
-
 def _refuse_mat(t, name, shape, dtype):
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2:
         raise ValueError("%s must be a CUDA matrix" % name)
