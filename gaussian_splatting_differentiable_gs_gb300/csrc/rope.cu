@@ -177,6 +177,68 @@ cudaError_t rope_launch(int vec, dim3 grid, int threads, int64_t tokens, const R
   return launch_overlapped(rope_kernel<T, 1, INTER>, grid, threads, 0, st, tokens, k, s0, s1, pos);
 }
 
+// ---- frequencies (host) ----------------------------------------------------
+// A number as the sum of two doubles, for about 100 bits: a double's 53 would leave a
+// frequency off by 2^-56 of a turn, and the angle at position 2^31 by 1.5e-6.  Sums by
+// Knuth's exact addition, products by fma (a rounded product too: one that the compiler
+// could fuse with the sum after it would spoil that).
+struct Wide {
+  double hi, lo;
+};
+Wide sum2(double a, double b) {  // exact
+  const double s = a + b, t = s - a;
+  return {s, (a - (s - t)) + (b - t)};
+}
+Wide operator+(Wide a, Wide b) {
+  const Wide s = sum2(a.hi, b.hi);
+  return sum2(s.hi, s.lo + (a.lo + b.lo));
+}
+Wide operator*(Wide a, Wide b) {
+  const double p = fma(a.hi, b.hi, 0.0);
+  return sum2(p, fma(a.hi, b.lo, fma(a.lo, b.hi, fma(a.hi, b.hi, -p))));
+}
+Wide operator/(Wide a, double b) {
+  const double q = a.hi / b;
+  return sum2(q, (fma(-q, b, a.hi) + a.lo) / b);
+}
+
+// e^x: x less whole powers of two, e^r - 1 = y by its series for r / 512, then nine times
+// y (2 + y) for twice the argument.
+Wide exp_wide(Wide x) {
+  constexpr Wide kLn2{0.6931471805599453, 2.3190468138462996e-17};
+  const double k = nearbyint(x.hi / kLn2.hi);
+  const Wide part = kLn2 * Wide{-k, 0.0}, r0 = x + part, r{r0.hi / 512.0, r0.lo / 512.0};
+  Wide p = r / 9.0 + Wide{1.0, 0.0};  // 1 + r / n (1 + r / (n + 1) (...)), |r| < 7e-4
+  for (int n = 8; n >= 2; --n) p = r * p / n + Wide{1.0, 0.0};
+  Wide y = r * p;
+  for (int i = 0; i < 9; ++i) y = y * (y + Wide{2.0, 0.0});
+  y = y + Wide{1.0, 0.0};
+  return {ldexp(y.hi, (int)k), ldexp(y.lo, (int)k)};
+}
+// ln x: the double's logarithm y and, as x e^-y is 1 + d with a small d, d - d^2 / 2.
+Wide log_wide(double x) {
+  const Wide y{log(x), 0.0};
+  // e^-y in two factors: each stays a normal number wherever x is
+  const Wide half = exp_wide(Wide{-0.5 * y.hi, 0.0});
+  const Wide d = half * (half * Wide{x, 0.0}) + Wide{-1.0, 0.0};
+  return y + d + Wide{fma(-0.5 * d.hi, d.hi, 0.0), 0.0};
+}
+
+// |scale| base^(-2 j / dim) / 2 pi in turns, times 2^64, modulo 2^64; false where it is not
+// a finite number.
+bool turns_of(double scale, Wide log_base, int j, int dim, uint64_t* turns) {
+  constexpr Wide kTurn{0.15915494309189535, -9.839338337591243e-18};  // 1 / 2 pi
+  const Wide e = log_base * Wide{-2.0 * j, 0.0} / dim;
+  if (!(fabs(e.hi) < 700.0)) return false;
+  const Wide f = exp_wide(e) * (kTurn * Wide{fabs(scale), 0.0});
+  if (!isfinite(f.hi)) return false;
+  const double part = ldexp(f.hi - floor(f.hi), 32), hi = floor(part);  // both exact
+  const double lo = nearbyint(ldexp((part - hi) + ldexp(f.lo, 32), 32));
+  const uint64_t t = ((uint64_t)hi << 32) + (uint64_t)(int64_t)lo;
+  *turns = scale < 0.0 ? 0 - t : t;
+  return true;
+}
+
 bool dims_ok(int32_t n_axes, const int32_t* dims, int* sum) {
   if (n_axes < 1 || n_axes > GS_ROPE_MAX_AXES || !dims) return false;
   int64_t s = 0;
@@ -200,15 +262,11 @@ extern "C" gs_status gs_rope_turns(int32_t n_axes, const int32_t* dims, const do
   for (int a = 0; a < n_axes; ++a)
     if (!(base[a] > 0.0) || !isfinite(base[a]) || !isfinite(scale[a])) return GS_ERR_INVALID_ARG;
   int at = 0;
-  for (int a = 0; a < n_axes; ++a)
-    for (int j = 0; j < dims[a] / 2; ++j) {
-      double f = scale[a] * pow(base[a], -2.0 * j / dims[a]) / (2.0 * M_PI);
-      if (!isfinite(f)) return GS_ERR_INVALID_ARG;
-      f -= floor(f);  // whole turns do not matter
-      const double hi = floor(ldexp(f, 32));
-      const double lo = nearbyint(ldexp(ldexp(f, 32) - hi, 32));
-      turns[at++] = ((uint64_t)hi << 32) + (uint64_t)lo;
-    }
+  for (int a = 0; a < n_axes; ++a) {
+    const Wide log_base = log_wide(base[a]);
+    for (int j = 0; j < dims[a] / 2; ++j)
+      if (!turns_of(scale[a], log_base, j, dims[a], &turns[at++])) return GS_ERR_INVALID_ARG;
+  }
   return GS_OK;
 }
 

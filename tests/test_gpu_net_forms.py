@@ -199,3 +199,29 @@ def test_rope_in_place_where_a_stride_is_never_taken(gs):
         assert torch.equal(y[:tokens, :heads], want[:tokens, :heads])
         y[:tokens, :heads] = x[:tokens, :heads]
         assert torch.equal(y, x)
+
+
+@pytest.mark.parametrize("scale", [1.0, -3.0])
+def test_rope_far_positions_lose_nothing(gs, scale):
+    """The angle of a position up to 2^31 in either direction is good to fp32's rounding:
+    the bound is that of small positions, with angles from 60 digits."""
+    import math
+    from decimal import Decimal, getcontext
+    getcontext().prec = 60
+    two_pi = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494")
+    at = [2 ** 31 - 1, -2 ** 31, 123456789, -987654321, 2 ** 30 + 1, 7]
+    x = torch.randn(len(at), 2, 64, generator=_gen(1))
+    got = torch.empty(len(at), 2, 64, device="cuda")
+    gs.gs_rope(gs.Rope([64], scale=scale), torch.tensor(at, dtype=torch.int32)[:, None].cuda(), x.cuda(), q_out=got)
+    ang = torch.empty(len(at), 32, dtype=torch.float64)
+    for j in range(32):
+        f = Decimal(scale) * (Decimal(10000).ln() * Decimal(-2 * j) / 64).exp() / two_pi
+        for i, p in enumerate(at):
+            t = p * f
+            ang[i, j] = float(t - t.to_integral_value()) * 2 * math.pi
+    u, v = x[..., :32].double(), x[..., 32:].double()
+    c, s = ang.cos()[:, None], ang.sin()[:, None]
+    want = torch.cat([u * c - v * s, u * s + v * c], -1)
+    pair = torch.cat([u.abs() + v.abs()] * 2, -1)
+    err = (got.double().cpu() - want).abs()
+    assert (err <= 10 * U * pair + U * want.abs()).all(), float((err / pair).max() / U)

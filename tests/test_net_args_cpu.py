@@ -96,3 +96,31 @@ def test_tensors_of_another_device_than_the_current_one_are_refused(gs, monkeypa
     for stream in (None, Stream):
         with pytest.raises(ValueError, match="current device"):
             gs.net._stream(stream, Tensor(0))
+
+
+def _turns(dims, base, scale):
+    """Each pair's frequency in turns times 2^64, modulo 2^64, to 60 digits."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 90
+    two_pi = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899862803482534211706798")
+    out = []
+    for d, b, s in zip(dims, base, scale):
+        for j in range(d // 2):
+            f = Decimal(s) * (Decimal(b).ln() * Decimal(-2 * j) / Decimal(d)).exp() / two_pi * 2 ** 64
+            out.append(f % 2 ** 64)
+    return out
+
+
+@pytest.mark.parametrize("dims,base,scale", [
+    ([64], [10000.0], [1.0]), ([128], [500000.0], [0.25]), ([16, 24, 24], [10000.0, 100.0, 7.5], [1.0, 0.5, 2.0]),
+    ([6, 10], [1.0, 1e6], [-1.0, 3.0]), ([256], [1e4], [-0.125]), ([2, 30], [0.5, 0.001], [7.0, 1e-3]),
+    ([34], [1e300], [1e-9]), ([22], [3.0], [12345.678]), ([8], [1e4], [0.0])])
+def test_rope_turns_to_the_last_of_their_bits(gs, dims, base, scale):
+    """64 bits of each frequency: a position times it, modulo 2^64, is off by 2^-64 of a turn
+    times the position."""
+    r = gs.Rope(dims, base=base, scale=scale)
+    want = _turns(dims, base, scale)
+    assert len(want) == sum(dims) // 2
+    for got, f in zip(r.turns, want):
+        off = abs(int(got) - f)
+        assert min(off, 2 ** 64 - off) <= 1, (int(got), f)
