@@ -229,7 +229,6 @@ Wide log_wide(double x) {
 bool turns_of(double scale, Wide log_base, int j, int dim, uint64_t* turns) {
   constexpr Wide kTurn{0.15915494309189535, -9.839338337591243e-18};  // 1 / 2 pi
   const Wide e = log_base * Wide{-2.0 * j, 0.0} / dim;
-  if (!(fabs(e.hi) < 700.0)) return false;
   const Wide f = exp_wide(e) * (kTurn * Wide{fabs(scale), 0.0});
   if (!isfinite(f.hi)) return false;
   const double part = ldexp(f.hi - floor(f.hi), 32), hi = floor(part);  // both exact

@@ -47,8 +47,9 @@ typedef enum gs_dtype { GS_BF16 = 0, GS_F16 = 1, GS_F32 = 2 } gs_dtype;
 /* gs_rope_turns -- turns[] (host, sum(dims) / 2 entries): each pair's
  * frequency as a 64-bit fraction of a turn, f / 2 pi * 2^64 mod 2^64 to within
  * 1.  A position times this, modulo 2^64, is the angle's phase, off by 2^-64 of
- * a turn for each unit of the position.  1 <= n_axes <= GS_ROPE_MAX_AXES, dims[a] even and >= 0,
- * 2 <= sum(dims) <= GS_ROPE_MAX_DIM, base[a] > 0, scale[a] finite. */
+ * a turn for each unit of the position.  1 <= n_axes <= GS_ROPE_MAX_AXES,
+ * dims[a] even and >= 0, 2 <= sum(dims) <= GS_ROPE_MAX_DIM, base[a] > 0,
+ * scale[a] and every frequency finite. */
 gs_status gs_rope_turns(int32_t n_axes, const int32_t* dims, const double* base,
                         const double* scale, uint64_t* turns);
 

@@ -124,3 +124,14 @@ def test_rope_turns_to_the_last_of_their_bits(gs, dims, base, scale):
     for got, f in zip(r.turns, want):
         off = abs(int(got) - f)
         assert min(off, 2 ** 64 - off) <= 1, (int(got), f)
+
+
+def test_rope_turns_at_the_ends_of_the_bases(gs):
+    """Frequencies that are next to nothing, and one that is no finite number."""
+    for base in (1.7e308, 1e308):
+        r = gs.Rope([256], base=base)
+        want = _turns([256], [base], [1.0])
+        assert all(abs(int(got) - f) <= 1 for got, f in zip(r.turns, want))
+    assert gs.Rope([4], base=5e-324, scale=0.0).turns[1] == 0
+    with pytest.raises(gs.GSError, match="invalid argument"):
+        gs.Rope([64], base=1e-310, scale=1e30)
