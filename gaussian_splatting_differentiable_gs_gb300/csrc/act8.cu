@@ -567,8 +567,11 @@ extern "C" gs_status gs_glu_bwd(int64_t tokens, int32_t channels, int32_t dtype,
   if (tokens == 0) return GS_OK;
   const Act8K g8 = ckpt_of(gate8), u8 = ckpt_of(up8), o8 = ckpt_of(h8);
   const int el = dtype_size(dtype);
-  if (!ckpt_ok(g8, tokens, channels) || (u8.q && !ckpt_ok(u8, tokens, channels)) || (o8.q && !ckpt_ok(o8, tokens, channels)) || (!u8.q != !dup) ||
-      !dh || !dgate || !aligned_to(dh, el) || !aligned_to(dgate, el) || !aligned_to(dup, el))
+  if (!ckpt_ok(g8, tokens, channels) || (u8.q && !ckpt_ok(u8, tokens, channels)) ||
+      (o8.q && !ckpt_ok(o8, tokens, channels)) || (!u8.q != !dup) || !dh || !dgate ||
+      !aligned_to(dh, el) || !aligned_to(dgate, el) || !aligned_to(dup, el) ||
+      !in_place_ok(tokens, dh, dh_stride, dgate, dgate_stride) ||
+      !in_place_ok(tokens, dh, dh_stride, dup, dup_stride))
     return GS_ERR_INVALID_ARG;
   const bool wide = channels % 8 == 0 && rows_aligned(dh, dh_stride, el, 16) &&
                     rows_aligned(dgate, dgate_stride, el, 16) &&

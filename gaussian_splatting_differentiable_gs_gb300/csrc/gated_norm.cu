@@ -898,7 +898,8 @@ extern "C" gs_status gs_gated_norm_fwd(const gs_norm* p, const void* x, int64_t 
   const int eb = dtype_size(p->dtype), ex = dtype_size(p->res_dtype);
   if (!x || !stats || (!block != !x_out) || (!block && !y) || (!y_q != !y_e) || (y_q && !y) ||
       !aligned16(stats) || !aligned_to(x, ex) || !aligned_to(block, eb) ||
-      !aligned_to(x_out, ex) || !aligned_to(y, eb))
+      !aligned_to(x_out, ex) || !aligned_to(y, eb) ||
+      !in_place_ok(p->tokens, x, x_stride, x_out, x_out_stride))
     return GS_ERR_INVALID_ARG;
   if (y_q && !ckpt_ok(p->tokens, p->channels, y_q, q_stride, y_e, e_stride)) return GS_ERR_INVALID_ARG;
   const int vec = 16 / eb;
@@ -932,7 +933,9 @@ extern "C" gs_status gs_gated_norm_bwd(
   if (p->tokens > 0 && (!x_out || !stats || !dx || (!dx_out && !dy) || !aligned16(stats) ||
                         !aligned_to(x_out, ex) || !aligned_to(block, eb) ||
                         !aligned_to(dx_out, ex) || !aligned_to(dy, eb) || !aligned_to(dx, ex) ||
-                        !aligned_to(dblock, eb)))
+                        !aligned_to(dblock, eb) ||
+                        !in_place_ok(p->tokens, dx_out, dx_out_stride, dx, dx_stride) ||
+                        !in_place_ok(p->tokens, dy, dy_stride, dblock, dblock_stride)))
     return GS_ERR_INVALID_ARG;
   if ((dw_pre || need_e) &&
       (!workspace || !aligned16(workspace) ||

@@ -92,6 +92,13 @@ inline bool rows_aligned(const void* p, int64_t stride, int elem, size_t bytes) 
   return !p || (aligned_to(p, bytes) && (stride * elem) % (int64_t)bytes == 0);
 }
 
+// An output at its input's address: the same rows, or some would be written before
+// others are read there.
+inline bool in_place_ok(int64_t tokens, const void* in, int64_t in_stride, const void* out,
+                        int64_t out_stride) {
+  return in != out || !in || tokens < 2 || in_stride == out_stride;
+}
+
 // Kernels that begin while the one before on their stream ends: launched by
 // launch_overlapped, a kernel touches global memory only after wait_for_previous,
 // which returns when that kernel and all before it have ended and their writes are

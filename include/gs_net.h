@@ -104,7 +104,7 @@ typedef struct gs_norm {
  *   x, block    [tokens][C]; block NULL: no sum, y = w_pre * norm(x) (x_out
  *               NULL)
  *   x_out, y    outputs; y NULL: no norm before (the network's last sum);
- *               x_out may equal x
+ *               x_out may equal x (same strides)
  *   stats       [tokens][4] fp32 output: mean and 1/deviation of block, mean
  *               and 1/deviation of x' (0 where not computed)
  *   y_q, y_e    y's checkpoint (see gs_act8_encode; the bytes are those of
@@ -160,7 +160,8 @@ gs_status gs_act8_decode(int64_t tokens, int32_t channels, int32_t dtype, const 
  * takes the derivative at the values that the checkpoints hold:
  *   dgate = dh * up * act'(gate), dup = dh * act(gate)
  * and, with h_q and h_e, writes the checkpoint of h at those values, from
- * which the next product's weight gradient is taken.  dgate may equal dh. */
+ * which the next product's weight gradient is taken.  dgate may equal dh
+ * (same strides). */
 #define GS_ACT_SILU 0
 #define GS_ACT_GELU 1
 

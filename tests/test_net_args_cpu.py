@@ -135,3 +135,16 @@ def test_rope_turns_at_the_ends_of_the_bases(gs):
     assert gs.Rope([4], base=5e-324, scale=0.0).turns[1] == 0
     with pytest.raises(gs.GSError, match="invalid argument"):
         gs.Rope([64], base=1e-310, scale=1e30)
+
+
+def test_matrices_in_place_with_other_strides_are_refused(gs):
+    """Rows would be written before others are read there."""
+    keep, p = _aligned()
+    L, bad, r = gs.lib(), gs.GS_ERR_INVALID_ARG, C.byref
+    ck, other = Ckpt(p, p, 32, 1), p + 4096
+    assert L.gs_glu_bwd(2, 8, 0, 0, r(ck), r(ck), p, 8, p, 16, other, 8, None, None) == bad
+    n = Norm(2, 8, 1, 1, 0, 0, 1e-6)
+    assert L.gs_gated_norm_fwd(r(n), p, 8, other, 8, p, 16, other, 8, other, None, 0, None, 0, None) == bad
+    bwd = lambda dx, dxs, db, dbs: L.gs_gated_norm_bwd(  # noqa: E731
+        r(n), other, 8, other, 8, other, p, 8, p + 2048, 8, dx, dxs, db, dbs, None, None, None, None, None, 0, None)
+    assert bwd(p, 16, other, 8) == bad and bwd(other, 8, p + 2048, 16) == bad
