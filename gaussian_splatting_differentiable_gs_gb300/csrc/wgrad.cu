@@ -986,11 +986,11 @@ extern "C" gs_status gs_selftest_wgrad_timeout(int64_t tokens, int32_t rows, int
                                                void* dw, void* workspace, size_t ws_bytes,
                                                int32_t steps, void* stream) {
   // The exponents stop after `steps` steps of 64 tokens (a multiple of kBatch), so that the
-  // decoding warps, and with them every other role, wait for what never comes: 20 ms.
+  // decoding warps, and with them every other role, wait for what never comes: 100 ms.
   if (steps < 0) return GS_ERR_INVALID_ARG;
   const int64_t ld = div_up(channels, GS_ACT8_GROUP) * GS_ACT8_GROUP;
   const gs_status s = weight_gradient(tokens, rows, channels, GS_BF16, dy, rows, q, ld, e,
                                       ld / GS_ACT8_GROUP, dw, channels, GS_F32, 0, workspace,
-                                      ws_bytes, (uint32_t)steps, 20000000, stream);
+                                      ws_bytes, (uint32_t)steps, 100000000, stream);
   return s != GS_OK ? s : gs_workspace_status(workspace, stream);
 }

@@ -184,7 +184,8 @@ gs_status gs_glu_bwd(int64_t tokens, int32_t channels, int32_t dtype, int32_t ac
  * checkpoint of its input: dw[n][k] = sum_t dy[t][n] * x8[t][k], n < rows,
  * k < channels, summed in fp32; accumulate != 0 adds to dw (the sum is
  * formed in fp32 and rounded once).
- *   dy          [tokens][rows] of type dtype; used exactly in every type
+ *   dy          [tokens][rows] of type dtype; used exactly in every type (of
+ *               an fp32 gradient what lies below 2^-133 is cut)
  *   q, e        the checkpoint; its values are used exactly, as bf16 (64
  *               steps of 2^122, a magnitude above 127 * 2^121 that was
  *               rounded up, are an infinity there)
@@ -205,7 +206,7 @@ gs_status gs_act8_wgrad(int64_t tokens, int32_t rows, int32_t channels, int32_t 
 
 /* Self-test of gs_act8_wgrad's bounded waits: the call in bf16 with contiguous
  * arrays and an fp32 dw, whose exponents stop after `steps` steps of 64 tokens
- * per pair of SMs (in eights), so that its waits run out, after 20 ms instead of
+ * per pair of SMs (in eights), so that its waits run out, after 100 ms instead of
  * two seconds; the kernel waits for its copies under way, flags the error and
  * ends, and the call synchronises and returns GS_ERR_TIMEOUT (GS_OK where
  * `steps` were enough).  dw is left undefined, the context stays usable. */

@@ -225,3 +225,20 @@ def test_rope_far_positions_lose_nothing(gs, scale):
     pair = torch.cat([u.abs() + v.abs()] * 2, -1)
     err = (got.double().cpu() - want).abs()
     assert (err <= 10 * U * pair + U * want.abs()).all(), float((err / pair).max() / U)
+
+
+def test_weight_gradient_of_the_smallest_numbers(gs):
+    """A wide gradient's terms reach down to bf16's smallest step, 2^-133: one token, so
+    that dw = dy x to fp32's rounding (three terms, their sum) but for what lies below it."""
+    N, K = 120, 64
+    big = 2.0 ** 100
+    dy = torch.randn(1, N, generator=_gen(3)) * torch.logspace(-30, -39, N)
+    x = torch.full((1, K), big)
+    q, e = gs.act8_empty(1, K)
+    gs.gs_act8_encode(x.cuda(), q, e)
+    ws = torch.zeros(gs.gs_act8_wgrad_workspace_bytes(1, N, K, torch.float32), dtype=torch.uint8, device="cuda")
+    dw = torch.empty(N, K, device="cuda")
+    gs.gs_act8_wgrad(dy.cuda(), q, e, dw, ws)
+    want = dy.double().t() * big
+    err = (dw.double().cpu() - want).abs()
+    assert (err <= 4 * U * want.abs() + 2.0 ** -133 * big).all(), float((err / big).max() * 2 ** 133)
