@@ -864,7 +864,7 @@ cudaError_t bwd_launch(BwdArgs& a, cudaStream_t st) {
 // 16 channels a thread where rows are aligned and that wide (32640 x 1024 bf16: 85 us,
 // with 8 a thread 107 us, when that was measured; 76 us now); 8 for rows that start
 // anywhere, where 16 cost more in single accesses than they save (5003 x 997 fp32:
-// 49 us, 87 us; 44 us now).
+// 49 us, 87 us; 45 us now).
 template <typename TB, typename TX, int VEC>
 cudaError_t bwd_pick(BwdArgs& a, cudaStream_t st) {
   if (a.k.C <= (VEC > 1 ? 256 : 4096)) return bwd_launch<TB, TX, VEC, 8 / VEC>(a, st);

@@ -9,7 +9,11 @@
 // computes the sines of its tokens once, a thread keeps those of its channels and
 // walks heads.
 //
-// Bound by memory: one read and one write of the heads.  A thread has a few pairs
+// One read and one write of the heads.  fp32 heads run at 99 % of the copy rate
+// (32640 tokens of 24 heads of 80: 75.6 us).  16-bit heads do not: 32640 tokens of 20
+// heads of 64 in bf16 take 43 us where the copy rate would allow 25, with DRAM busy for
+// 35 % of it and 53 % of the issue slots used; 72 registers a thread leave 22 warps an
+// SM, whose largest stall is the wait for their loads.  A thread has a few pairs
 // of a head, as vectors of up to 16 bytes, and finds their places once: blocks
 // walk over the tokens.  (With a block per group of tokens, every thread computing
 // its own sines, 32640 tokens of 20 heads of 64 in bf16 took 53 us, most of them

@@ -4,7 +4,12 @@ from views.  As in the package itself, each gs_* function only checks and
 marshals its arguments and calls the C ABI function of the same name.
 
 Matrices are CUDA tensors [tokens, channels] whose last axis is contiguous;
-rows may have any stride (a slice of a packed projection, say)."""
+rows may have any stride (a slice of a packed projection, say).
+
+Results go into the tensors that the caller gives.  The calls are not autograd
+functions: a tensor that requires a gradient is taken as it is and gets none; each
+operator's backward pass is a call of its own (examples/predict_gaussians.py chains
+them)."""
 import ctypes as C
 import struct
 
