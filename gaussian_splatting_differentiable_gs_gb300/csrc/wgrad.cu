@@ -31,11 +31,9 @@
 // evenly over the clusters are summed by one cluster each; the token steps of
 // the remaining tiles are dealt out evenly, and the partial sums of a tile
 // that several clusters share are joined in a fixed order by a second kernel.
-#include <cuda.h>
-
 #include <atomic>
 
-#include "net_common.cuh"
+#include "tensor_core.cuh"
 
 namespace gs {
 namespace {
@@ -159,61 +157,6 @@ __device__ __forceinline__ int64_t cluster_steps(const Plan& p, int cluster) {
   return (int64_t)p.waves * p.steps + (dealt > 0 ? dealt : 0);
 }
 
-// ---- mbarriers, TMA, tcgen05 (inline PTX) --------------------------------
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-  return (uint32_t)__cvta_generic_to_shared(p);
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile(
-      "{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(r));
-  return r != 0;
-}
-__device__ __forceinline__ uint32_t in_cta0(uint32_t addr) {  // the pair's first CTA
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;"
-               ::: "memory");
-}
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-// On a barrier of the pair's first CTA, for what this CTA did with its own TMEM:
-// the waits and tcgen05 fences around it order that for the tensor core, so the
-// arrival need not order memory at cluster scope (a release at that scope costs
-// the arriving warp several hundred cycles).
-__device__ __forceinline__ void mbar_arrive_pair(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-               : "memory");
-}
-// The thread sleeps until the phase ends, for 20 us at most: polling without that
-// took issue slots from the decoding warps (279 us instead of 252).
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n.reg .pred p;\n"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-      "selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 struct Control {
   uint64_t raw_full[kRaw], raw_empty[kRaw];      // bytes of a step
   uint64_t exp_full[kBatches], exp_empty[kBatches];
@@ -224,28 +167,6 @@ struct Control {
   uint32_t dy_steps, raw_steps, products, runs, decoded[kDecodeWarps];
   volatile uint32_t abort;                       // a wait of the pair gave up
 };
-
-__device__ __forceinline__ int64_t now_ns() {
-  int64_t t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-// A word of the Control of the pair's CTA `rank`.
-__device__ __forceinline__ uint32_t load_pair(const volatile uint32_t* word, uint32_t rank) {
-  uint32_t v;
-  asm volatile(
-      "{\n.reg .b32 a;\nmapa.shared::cluster.u32 a, %1, %2;\nld.shared::cluster.u32 %0, [a];\n}"
-      : "=r"(v)
-      : "r"(smem_u32((const void*)word)), "r"(rank)
-      : "memory");
-  return v;
-}
-__device__ __forceinline__ void store_pair(volatile uint32_t* word, uint32_t rank, uint32_t v) {
-  asm volatile("{\n.reg .b32 a;\nmapa.shared::cluster.u32 a, %0, %1;\nst.shared::cluster.u32 [a], %2;\n}" ::"r"(
-                   smem_u32((const void*)word)),
-               "r"(rank), "r"(v)
-               : "memory");
-}
 
 // Waits for a barrier's phase, at most p.wait_ns; false (and the status word set) when
 // that ran out or another wait of the pair gave up.
@@ -306,22 +227,6 @@ __device__ __forceinline__ void drain(Control* c, const Plan& p, uint32_t rank) 
   last(c->full, kStages, steps);
 }
 
-__device__ __forceinline__ void tma_load_own(uint32_t dst, const CUtensorMap* map, int x, int y,
-                                             uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar)
-      : "memory");
-}
-// As part of a pair's product: the barrier may be the other CTA's.
-__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y,
-                                         uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar)
-      : "memory");
-}
-
 // Shared-memory descriptor of an MN-major operand in 128-byte swizzled rows:
 // 64 channels are a row, 8 tokens an atom of 1024 bytes (stride between atoms
 // along the tokens), and the next 64 channels follow after kBT rows.
@@ -341,13 +246,6 @@ __device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint64_t b, uint32_t
       "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
       "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d), "r"(a), "l"(b),
       "r"(idesc), "r"((uint32_t)add)
-      : "memory");
-}
-// Arrives on the same barrier of both CTAs once the products issued so far are done.
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-      "[%0], %1;" ::"r"(bar), "h"((uint16_t)3)
       : "memory");
 }
 // 32 columns of the warp's lanes, added to acc.
@@ -777,27 +675,6 @@ __global__ void __launch_bounds__(256) wgrad_terms_kernel(int64_t tokens, int64_
 int64_t padded_tokens(int64_t tokens) { return div_up(tokens, kBT) * kBT; }
 int padded_rows(int rows) { return (int)div_up(rows, 8) * 8; }
 int terms_of(int32_t dtype) { return dtype == GS_BF16 ? 1 : dtype == GS_F16 ? 2 : 3; }
-
-typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                             const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                             const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encode_fn() {
-  static std::atomic<void*> fn{nullptr};
-  void* f = fn.load(std::memory_order_acquire);
-  if (!f) {
-    cudaDriverEntryPointQueryResult res;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &res) != cudaSuccess ||
-        res != cudaDriverEntryPointSuccess) {
-      (void)cudaGetLastError();
-      return nullptr;
-    }
-    fn.store(f, std::memory_order_release);
-  }
-  return (EncodeFn)f;
-}
 
 // Clusters of two that run at once on the current device (0: none).  Looked up
 // once per device, with the kernels' shared memory limits.

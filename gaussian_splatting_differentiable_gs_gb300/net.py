@@ -1,6 +1,6 @@
 """Network operators (include/gs_net.h): multi-axis rotary positions, gated
-norms and 8-bit activation checkpoints, for a network that predicts Gaussians
-from views.  As in the package itself, each gs_* function only checks and
+norms, 8-bit activation checkpoints, the gated feed-forward block and linear
+attention with decays, for a network that predicts Gaussians from views.  As in the package itself, each gs_* function only checks and
 marshals its arguments and calls the C ABI function of the same name.
 
 Matrices are CUDA tensors [tokens, channels] whose last axis is contiguous;
@@ -41,6 +41,16 @@ def declare(L):
     L.gs_act8_wgrad_workspace_bytes.restype = sz
     L.gs_act8_wgrad.argtypes = [i64, i32, i32, i32, vp, i64, vp, i64, vp, i64, vp, i64, i32, i32,
                                 vp, sz, vp]
+    L.gs_ffn_workspace_bytes.argtypes = [i64, i32, i32, i32]
+    L.gs_ffn_workspace_bytes.restype = sz
+    L.gs_ffn_fwd.argtypes = [i64, i32, i32, i32, i32, vp, i64, vp, i64, vp, i64, vp, sz, vp]
+    L.gs_ffn_bwd.argtypes = [i64, i32, i32, i32, i32, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64,
+                             i32, i32, vp, sz, vp]
+    L.gs_linear_attn_workspace_bytes.argtypes = [vp, i32]
+    L.gs_linear_attn_workspace_bytes.restype = sz
+    L.gs_linear_attn_fwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.gs_linear_attn_bwd.argtypes = [vp] * 11 + [sz, vp]
+    L.gs_linear_attn_step.argtypes = [vp] * 7
 
 
 from . import _check, lib  # noqa: E402  (the package defines these first)
@@ -51,6 +61,8 @@ _NORM = struct.Struct("qiiiiifPPPPP")
 _HEADS = struct.Struct("PPqqqqi4x")
 _CKPT = struct.Struct("PPqq")
 _NO_CKPT = _CKPT.pack(0, 0, 0, 0)
+_ATTN = struct.Struct("qiiiiiifPPP")
+_ATTN_HEADS = struct.Struct("Pqq")
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 
@@ -365,3 +377,154 @@ def gs_act8_wgrad(dy, q, e, dw, workspace, accumulate=False, stream=None):
         tokens, rows, c, code, dy.data_ptr(), dy.stride(0), q, qs, e, es, dw.data_ptr(),
         dw.stride(0), out_code, 1 if accumulate else 0,
         _vec(workspace, "workspace", size, torch.uint8), size, _stream(stream, dy)))
+
+
+# --------------------------------------------------------------------------
+# the gated feed-forward block
+
+
+def _on_one_device(*tensors):
+    device = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError("tensors on cuda:%d and cuda:%d" % (device, t.get_device()))
+
+
+def gs_ffn_workspace_bytes(tokens, channels, hidden, backward=True):
+    return int(lib().gs_ffn_workspace_bytes(tokens, channels, hidden, 1 if backward else 0))
+
+
+def _ffn_args(x, w, h, name, workspace, act):
+    """Checks what both directions have: the C call's arguments up to h's, and the workspace's."""
+    (tokens, c), code = _first(x, "x")
+    if code == 2:
+        raise ValueError("x: bfloat16 or float16")
+    if getattr(w, "dim", int)() != 2 or w.shape[0] % 2 or not w.shape[0]:
+        raise ValueError("w must be [2 * hidden, channels]")
+    hidden = w.shape[0] // 2
+    _mat(w, "w", (2 * hidden, c), x.dtype)
+    _mat(h, name, (tokens, hidden), x.dtype)
+    if act not in ACTS:
+        raise ValueError("act: one of %s" % ", ".join(ACTS))
+    size = workspace.numel()
+    return ((tokens, c, hidden, code, ACTS[act], x.data_ptr(), x.stride(0), w.data_ptr(), w.stride(0),
+             h.data_ptr(), h.stride(0)), (_vec(workspace, "workspace", size, torch.uint8), size))
+
+
+def gs_ffn_fwd(x, w, h, workspace, act="silu", stream=None):
+    """h [tokens, hidden] = act(x w_gate^T) * (x w_up^T) in one kernel, with w [2 * hidden,
+    channels] the gate's rows and then up's; bfloat16 or float16.  workspace: uint8,
+    gs_ffn_workspace_bytes() bytes, its first 256 zero before the first call."""
+    args, ws = _ffn_args(x, w, h, "h", workspace, act)
+    _on_one_device(x, w, h, workspace)
+    _check("gs_ffn_fwd", lib().gs_ffn_fwd(*args, *ws, _stream(stream, x)))
+
+
+def gs_ffn_bwd(x, w, dh, dx, dw, workspace, act="silu", accumulate=False, stream=None):
+    """From dh, the gradient of h: dx [tokens, channels] and dw [2 * hidden, channels] (of
+    x's type or float32; accumulate adds to it); either may be None.  Gate and up are
+    formed again from x, so that nothing else is kept from the forward pass."""
+    args, ws = _ffn_args(x, w, dh, "dh", workspace, act)
+    d, ds = _opt(dx, "dx", x.shape, x.dtype)
+    g, gs_, code = None, 0, args[3]
+    if dw is not None:
+        if dw.dtype is not x.dtype and dw.dtype is not torch.float32:
+            raise ValueError("dw: type %s" % dw.dtype)
+        _mat(dw, "dw", w.shape, dw.dtype)
+        g, gs_, code = dw.data_ptr(), dw.stride(0), DTYPES[dw.dtype]
+    _on_one_device(x, w, dh, dx, dw, workspace)
+    _check("gs_ffn_bwd", lib().gs_ffn_bwd(*args, d, ds, g, gs_, code, 1 if accumulate else 0, *ws,
+                                          _stream(stream, x)))
+
+
+# --------------------------------------------------------------------------
+# linear attention
+
+
+def _attn(q, k, v, log_decay, group_offsets, state, scale):
+    """Checks what every call has: (the packed gs_linear_attn, q's, k's and v's packed
+    heads, shape of the outputs, shape of the states)."""
+    code = DTYPES.get(getattr(q, "dtype", None))
+    if code is None or code == 2 or q.dim() != 3:
+        raise ValueError("q must be a CUDA [tokens, heads, dim] tensor of bfloat16 or float16")
+    tokens, hq, dim = q.shape
+    if getattr(k, "dim", int)() != 3 or getattr(v, "dim", int)() != 3:
+        raise ValueError("k and v must be CUDA [tokens, heads, dim] tensors")
+    hk, vdim = k.shape[1], v.shape[2]
+    if not hk or not hq or hq % hk:
+        raise ValueError("%d query heads do not share %d key heads evenly" % (hq, hk))
+    groups = 1
+    if group_offsets is not None:
+        groups = group_offsets.numel() - 1
+        if groups < 1:
+            raise ValueError("group_offsets must have groups + 1 entries")
+    states = (groups, hq, dim, vdim)
+    packed = _ATTN.pack(tokens, hq, hk, dim, vdim, groups, code, dim ** -0.5 if scale is None else scale,
+                        _vec(log_decay, "log_decay", hq),
+                        _vec(group_offsets, "group_offsets", groups + 1, torch.int32),
+                        _states(state, "state", states))
+    return (packed, _attn_heads(q, "q", (tokens, hq, dim), q), _attn_heads(k, "k", (tokens, hk, dim), q),
+            _attn_heads(v, "v", (tokens, hk, vdim), q), (tokens, hq, vdim), states)
+
+
+def _attn_heads(t, name, shape, like):
+    if (getattr(t, "shape", None) != shape or t.dtype is not like.dtype
+            or t.get_device() != like.get_device() or not t.is_cuda):
+        raise ValueError("%s must be a %s tensor %s on q's device" % (name, like.dtype, list(shape)))
+    a, b, c = t.stride()
+    if c != 1 and shape[2] > 1 and t.numel():
+        raise ValueError("%s: the last axis must be contiguous" % name)
+    return _ATTN_HEADS.pack(t.data_ptr(), a, b)
+
+
+def _states(t, name, shape):
+    if t is None:
+        return 0
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), shape))
+    return _vec(t, name, shape[0] * shape[1] * shape[2] * shape[3])
+
+
+def gs_linear_attn_workspace_bytes(tokens, q_heads, k_heads, dim, vdim, groups=1, backward=True):
+    return int(lib().gs_linear_attn_workspace_bytes(
+        _ATTN.pack(tokens, q_heads, k_heads, dim, vdim, groups, 0, 1.0, 0, 0, 0), 1 if backward else 0))
+
+
+def gs_linear_attn_fwd(q, k, v, log_decay, out, group_offsets=None, state=None, state_out=None, scale=None,
+                       workspace=None, stream=None):
+    """out [tokens, q_heads, vdim]: S <- e^log_decay S + k v^T, out = scale q S token after
+    token (scale: dim ** -0.5 where none is given), for q [tokens, q_heads, dim], k [tokens,
+    k_heads, dim], v [tokens, k_heads, vdim] of bfloat16 or float16 and log_decay float32
+    [q_heads], 0 or less.  Groups of tokens (group_offsets int32 [groups + 1]; None: one)
+    each go from their state to state_out, float32 [groups, q_heads, dim, vdim] (None: zeros;
+    not wanted).  workspace: uint8, gs_linear_attn_workspace_bytes() bytes."""
+    a, qh, kh, vh, shape, states = _attn(q, k, v, log_decay, group_offsets, state, scale)
+    size = 0 if workspace is None else workspace.numel()
+    _on_one_device(q, log_decay, group_offsets, state, state_out, workspace)
+    _check("gs_linear_attn_fwd", lib().gs_linear_attn_fwd(
+        a, qh, kh, vh, _attn_heads(out, "out", shape, q), _states(state_out, "state_out", states),
+        _vec(workspace, "workspace", size, torch.uint8), size, _stream(stream, q)))
+
+
+def gs_linear_attn_bwd(q, k, v, log_decay, dout, dq, dk, dv, group_offsets=None, state=None, dstate_out=None,
+                       dstate=None, scale=None, workspace=None, stream=None):
+    """Backward of gs_linear_attn_fwd from its inputs, dout and (None: zeros) the gradient of
+    its last states: dq, dk, dv and, where given, dstate, the gradient of the first states."""
+    a, qh, kh, vh, shape, states = _attn(q, k, v, log_decay, group_offsets, state, scale)
+    size = 0 if workspace is None else workspace.numel()
+    _on_one_device(q, log_decay, group_offsets, state, dstate_out, dstate, workspace)
+    _check("gs_linear_attn_bwd", lib().gs_linear_attn_bwd(
+        a, qh, kh, vh, _attn_heads(dout, "dout", shape, q), _attn_heads(dq, "dq", q.shape, q),
+        _attn_heads(dk, "dk", k.shape, q), _attn_heads(dv, "dv", v.shape, q),
+        _states(dstate_out, "dstate_out", states), _states(dstate, "dstate", states),
+        _vec(workspace, "workspace", size, torch.uint8), size, _stream(stream, q)))
+
+
+def gs_linear_attn_step(q, k, v, log_decay, state, out, scale=None, stream=None):
+    """One token of each of q.shape[0] streams: updates state, float32 [streams, q_heads, dim,
+    vdim], in place and writes out [streams, q_heads, vdim]."""
+    a, qh, kh, vh, shape, _ = _attn(q, k, v, log_decay, None, None, scale)
+    states = (shape[0], shape[1], q.shape[2], shape[2])
+    _on_one_device(q, log_decay, state)
+    _check("gs_linear_attn_step", lib().gs_linear_attn_step(
+        a, qh, kh, vh, _attn_heads(out, "out", shape, q), _states(state, "state", states), _stream(stream, q)))

@@ -11,6 +11,10 @@
  *                           residual sum and norm before the next block
  *   gs_act8_*, gs_glu_*     activation checkpoints in 8 bits and their use in
  *                           the backward pass
+ *   gs_ffn_fwd/_bwd         the gated feed-forward block: both projections,
+ *                           the activation and the product in one kernel
+ *   gs_linear_attn_*        linear attention with a decay for each head, in
+ *                           chunks or token by token
  *
  * Conventions as in gs.h: the caller owns every buffer; pointers are device
  * pointers unless marked (host); work is enqueued on `stream`; arguments are
@@ -213,6 +217,111 @@ gs_status gs_act8_wgrad(int64_t tokens, int32_t rows, int32_t channels, int32_t 
 gs_status gs_selftest_wgrad_timeout(int64_t tokens, int32_t rows, int32_t channels,
                                     const void* dy, const int8_t* q, const uint8_t* e, void* dw,
                                     void* workspace, size_t ws_bytes, int32_t steps, void* stream);
+
+/* ---------------------------------------------------------------------- */
+/* The gated feed-forward block: both projections, the activation and the
+ * product in one kernel on the tensor cores.  With w [2 hidden][channels],
+ * the gate's rows and then up's:
+ *   gate = x w_gate^T, up = x w_up^T, h = act(gate) * up
+ * Neither gate nor up is written; gs_ffn_bwd forms them again from x.  x, w,
+ * h, dh and dx are of one type, GS_BF16 or GS_F16; sums are fp32.  h may not
+ * overlap the inputs, nor may dx or dw.
+ *   workspace   gs_ffn_workspace_bytes(...) bytes (0: refused), 16-byte
+ *               aligned; its first 256 bytes must be zero before the first
+ *               call (gs_workspace_status reads them) and calls on one
+ *               workspace must not overlap
+ * tokens <= 2^31 - 512; channels, hidden <= 2^20. */
+size_t gs_ffn_workspace_bytes(int64_t tokens, int32_t channels, int32_t hidden, int32_t backward);
+gs_status gs_ffn_fwd(int64_t tokens, int32_t channels, int32_t hidden, int32_t dtype, int32_t act,
+                     const void* x, int64_t x_stride, const void* w, int64_t w_stride, void* h,
+                     int64_t h_stride, void* workspace, size_t ws_bytes, void* stream);
+
+/* gs_ffn_bwd -- from the gradient of h:
+ *   dgate = dh * up * act'(gate), dup = dh * act(gate)  (rounded to dtype)
+ *   dx = dgate w_gate + dup w_up,  dw = [dgate | dup]^T x
+ *   dx        [tokens][channels], or NULL where not wanted
+ *   dw        [2 hidden][channels] of type dw_dtype (dtype or GS_F32), or
+ *             NULL; accumulate != 0 adds to dw (the sum is formed in fp32
+ *             and rounded once).  The order of summation is fixed. */
+gs_status gs_ffn_bwd(int64_t tokens, int32_t channels, int32_t hidden, int32_t dtype, int32_t act,
+                     const void* x, int64_t x_stride, const void* w, int64_t w_stride,
+                     const void* dh, int64_t dh_stride, void* dx, int64_t dx_stride, void* dw,
+                     int64_t dw_stride, int32_t dw_dtype, int32_t accumulate, void* workspace,
+                     size_t ws_bytes, void* stream);
+
+/* Self-test of the block's bounded waits: the forward call in bf16 (silu) with
+ * contiguous arrays, whose operands stop after `steps` steps of 64 channels per
+ * pair of SMs, so that its waits run out, after 100 ms instead of two seconds;
+ * the kernel waits for its copies under way, flags the error and ends, and the
+ * call synchronises and returns GS_ERR_TIMEOUT (GS_OK where `steps` were
+ * enough).  h is left undefined, the context stays usable. */
+gs_status gs_selftest_ffn_timeout(int64_t tokens, int32_t channels, int32_t hidden, const void* x,
+                                  const void* w, void* h, void* workspace, size_t ws_bytes,
+                                  int32_t steps, void* stream);
+
+/* ---------------------------------------------------------------------- */
+/* Linear attention with a decay for each head.  A head has a state S
+ * [dim][vdim], and from token to token
+ *   S_t = d S_{t-1} + k_t v_t^T,  o_t = scale * q_t S_t,  d = e^log_decay
+ * Tokens come in groups (views, streams): group g is the tokens
+ * [group_offsets[g], group_offsets[g + 1]) and goes from its state to its
+ * last state.  Query head h reads key (and value) head h / (q_heads /
+ * k_heads), and has a decay and a state of its own.  Tokens outside the
+ * groups (behind the last one) are neither read nor written.
+ * q, k, v and what is written for them are of one type, GS_BF16 or GS_F16;
+ * states and sums are fp32.  In fp16, products scale * q k and dout v (and
+ * outputs) beyond 65504 become infinities; an infinity or a NaN in a token
+ * spreads to the outputs and gradients of its group, some of those before it
+ * among them.  1 <= dim, vdim <= GS_LINEAR_ATTN_MAX_DIM. */
+#define GS_LINEAR_ATTN_MAX_DIM 128
+
+typedef struct gs_linear_attn {
+  int64_t tokens;
+  int32_t q_heads, k_heads;      /* k_heads divides q_heads                   */
+  int32_t dim, vdim;             /* channels of queries and keys, of values   */
+  int32_t groups;                /* 1 without offsets                         */
+  int32_t dtype;
+  float scale;
+  const float* log_decay;        /* [q_heads], 0 or less                      */
+  const int32_t* group_offsets;  /* [groups + 1] ascending from 0, or NULL    */
+  const float* state;            /* [groups][q_heads][dim][vdim], or NULL (0) */
+} gs_linear_attn;
+
+typedef struct gs_attn_heads {   /* [tokens][heads][channels]                 */
+  void* p;
+  int64_t token, head;           /* strides, elements                         */
+} gs_attn_heads;
+
+/* gs_linear_attn_fwd -- all tokens of the groups, in chunks.
+ *   state_out   [groups][q_heads][dim][vdim] fp32: the states after the
+ *               groups' last tokens (a group's own state where it has none),
+ *               or NULL; may equal state
+ *   workspace   gs_linear_attn_workspace_bytes(a, backward) bytes, 16-byte
+ *               aligned, no initialisation; calls on one workspace must not
+ *               overlap */
+size_t gs_linear_attn_workspace_bytes(const gs_linear_attn* a, int32_t backward);
+gs_status gs_linear_attn_fwd(const gs_linear_attn* a, const gs_attn_heads* q,
+                             const gs_attn_heads* k, const gs_attn_heads* v,
+                             const gs_attn_heads* out, float* state_out, void* workspace,
+                             size_t ws_bytes, void* stream);
+
+/* gs_linear_attn_bwd -- from the gradients of the outputs and (dstate_out, or
+ * NULL: 0) of the last states: dq, dk, dv (summed over the query heads that
+ * share a key head) and dstate, the gradient of the first states (or NULL; may
+ * equal dstate_out).  The decays get no gradient. */
+gs_status gs_linear_attn_bwd(const gs_linear_attn* a, const gs_attn_heads* q,
+                             const gs_attn_heads* k, const gs_attn_heads* v,
+                             const gs_attn_heads* dout, const gs_attn_heads* dq,
+                             const gs_attn_heads* dk, const gs_attn_heads* dv,
+                             const float* dstate_out, float* dstate, void* workspace,
+                             size_t ws_bytes, void* stream);
+
+/* gs_linear_attn_step -- one token of each of a->tokens streams: state
+ * [tokens][q_heads][dim][vdim] fp32, read and updated in place; a->state,
+ * a->groups and a->group_offsets are not used (groups: 1). */
+gs_status gs_linear_attn_step(const gs_linear_attn* a, const gs_attn_heads* q,
+                              const gs_attn_heads* k, const gs_attn_heads* v,
+                              const gs_attn_heads* out, float* state, void* stream);
 
 #ifdef __cplusplus
 }
