@@ -410,6 +410,7 @@ struct Part {
   Side key, value;
   float mul;
   int32_t back, shift;  // tokens from the last to the first
+  int32_t exact;        // its last states are handed on
   float* to;            // [slots][heads][Dp][Ep]
 };
 struct PartsArgs {
@@ -458,8 +459,11 @@ __global__ void __launch_bounds__(kThreads<KD>, 256 / KD) attn_parts_kernel(cons
     __syncthreads();
     if (c + 1 < chunks) load(c + 1);
     const uint32_t set = (c & 1) * kSet * 2;
-    add_tokens<T, KD, std::is_same<T, __half>::value ? 2 : 3>(st, power2(a * (float)min(kL, s.n - c * kL)), keys + set,
-                                                               values + set, weights, d16);
+    const float decay = power2(a * (float)min(kL, s.n - c * kL));
+    if (std::is_same<T, __half>::value || !part.exact)
+      add_tokens<T, KD, 2>(st, decay, keys + set, values + set, weights, d16);
+    else
+      add_tokens<T, KD, 3>(st, decay, keys + set, values + set, weights, d16);
   }
   float* to = part.to + (((int64_t)blockIdx.x * p.heads + h) * p.Dp + warp * 16 + (lane >> 2)) * p.Ep + e0 + (lane & 3) * 2;
 #pragma unroll
@@ -492,21 +496,21 @@ __global__ void __launch_bounds__(kScanThreads) attn_scan_kernel(const __grid_co
   launch_dependents();
   wait_for_previous();
   const Scan& k = p.scan[blockIdx.z];
-  const int size = p.Dp * p.Ep, per = size / kScanThreads;
+  const int per = (p.D * p.E + kScanThreads - 1) / kScanThreads, size = p.Dp * p.Ep;
   const int h = blockIdx.y, g = blockIdx.x / per, i = blockIdx.x % per * kScanThreads + threadIdx.x;
-  const int row = i / p.Ep, col = i % p.Ep;
+  if (i >= p.D * p.E) return;
+  const int row = i / p.E, col = i % p.E;
   const float a = log2_decay(p.log_decay, h);
   const int64_t begin = offset_of(p.split, g), end = offset_of(p.split, g + 1);
   const int64_t first = begin / p.split.seg + g;
   const int slots = end > begin ? (int)((end - begin + p.split.seg - 1) / p.split.seg) : 0;
   const int tail = (int)(end - begin - (int64_t)(slots - 1) * p.split.seg);
-  const int64_t mat = ((int64_t)g * p.heads + h) * p.D * p.E + (int64_t)row * p.E + col;
-  const bool in = row < p.D && col < p.E;
-  float s = k.edge && in ? k.edge[mat] : 0.f;
+  const int64_t mat = ((int64_t)g * p.heads + h) * p.D * p.E + i;
+  float s = k.edge ? k.edge[mat] : 0.f;
   const float full = power2(a * (float)p.split.seg), rest = power2(a * (float)tail);
   const int last = slots - 1;
   const int64_t stride = (k.back ? -1 : 1) * (int64_t)p.heads * size;
-  float* at = k.parts + ((first + (k.back ? last : 0)) * p.heads + h) * size + i;
+  float* at = k.parts + ((first + (k.back ? last : 0)) * p.heads + h) * size + row * p.Ep + col;
   for (int b = 0; b < slots; b += AHEAD) {
     float u[AHEAD];
 #pragma unroll
@@ -519,7 +523,7 @@ __global__ void __launch_bounds__(kScanThreads) attn_scan_kernel(const __grid_co
       s = s * ((k.back ? b + j == 0 : b + j == last) ? rest : full) + u[j];
     }
   }
-  if (k.last && in) k.last[mat] = s;
+  if (k.last) k.last[mat] = s;
 }
 
 // ---- outputs -----------------------------------------------------------------
@@ -665,13 +669,13 @@ struct KvArgs {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads<64>, 3) attn_kv_kernel(const __grid_constant__ KvArgs p) {
+__global__ void __launch_bounds__(kThreads<64>, 4) attn_kv_kernel(const __grid_constant__ KvArgs p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   launch_dependents();
   wait_for_previous();
-  constexpr int kTile = kL * 64, kSet = 4 * kTile, kB = kTile * 2;  // keys, values, queries, douts
+  constexpr int kTile = kL * 64, kB = kTile * 2;  // keys, values, queries, douts
   T* tiles = (T*)smem;
-  const uint32_t state = smem_at(tiles + 2 * kSet);
+  const uint32_t state = smem_at(tiles + 4 * kTile);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, rt = warp;
   const Span s = span_of(p.split, blockIdx.x);
   if (s.n == 0) return;
@@ -685,7 +689,7 @@ __global__ void __launch_bounds__(kThreads<64>, 3) attn_kv_kernel(const __grid_c
     const int h = blockIdx.y * p.rep + r;
     const float a = log2_decay(p.log_decay, h);
     auto load = [&](int c) {
-      T* to = tiles + (c & 1) * kSet;
+      T* to = tiles;
       const int n = min(kL, s.n - c * kL);
       const int64_t at = from - (int64_t)c * kL;
       load_tile<T, 64, kThreads<64>>(to, head_at<T>(p.k, h, p.rep, at), -p.k.token, n, p.k.dim);
@@ -705,10 +709,9 @@ __global__ void __launch_bounds__(kThreads<64>, 3) attn_kv_kernel(const __grid_c
 
     for (int c = 0; c < chunks; ++c) {
       const int n = min(kL, s.n - c * kL), pad = kL - n;
-      const uint32_t set = (c & 1) * kSet * 2;
       float unscale = 1.f, rescale = 1.f;
       if constexpr (std::is_same<T, __half>::value) {
-        const int e = state_exponent(st, reinterpret_cast<float*>(tiles + ((c + 1) & 1) * kSet + 2 * kTile), kWarps<64>,
+        const int e = state_exponent(st, reinterpret_cast<float*>(tiles + 5 * kTile), kWarps<64>,
                                      warp, lane);
         rescale = power_of_two(-e);
         unscale = power_of_two(e);
@@ -716,7 +719,6 @@ __global__ void __launch_bounds__(kThreads<64>, 3) attn_kv_kernel(const __grid_c
       put_state<T>(state, st, warp, g, t, rescale);
       copies_wait<0>();
       __syncthreads();
-      if (c + 1 < chunks) load(c + 1);
       const float f0 = unscale * power2(a * (float)max(rt * 16 + g - pad, 0));
       const float f1 = unscale * power2(a * (float)max(rt * 16 + g + 8 - pad, 0));
       const int64_t tok = from - (int64_t)c * kL;
@@ -724,7 +726,7 @@ __global__ void __launch_bounds__(kThreads<64>, 3) attn_kv_kernel(const __grid_c
       uint32_t f[4][4];
       {  // dv: keys times R, and keys times queries times douts
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ldm4(f[i], (rows + set + own) ^ (i * 32));
+        for (int i = 0; i < 4; ++i) ldm4(f[i], (rows + own) ^ (i * 32));
         float o[8][4] = {};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -737,15 +739,15 @@ __global__ void __launch_bounds__(kThreads<64>, 3) attn_kv_kernel(const __grid_c
           }
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i][0] *= f0, o[i][1] *= f0, o[i][2] *= f1, o[i][3] *= f1;
-        add_inner<T, 64, 64>(o, f, cols + set + 2 * kB, rows + set + 3 * kB, rt, powers);
+        add_inner<T, 64, 64>(o, f, cols + 2 * kB, rows + 3 * kB, rt, powers);
         if (p.rep > 1) sum_heads<64>(o, p.sums[1] + sum, sum_step, rt, pad, g, t, r == 0, r + 1 == p.rep);
         if (r + 1 == p.rep)
-          put_rows<T, 64, 64>(smem_at(tiles) + set, o, rt, 0, head_at<T>(p.dv, h, p.rep, tok), -p.dv.token, pad,
+          put_rows<T, 64, 64>(smem_at(tiles), o, rt, 0, head_at<T>(p.dv, h, p.rep, tok), -p.dv.token, pad,
                               p.dv.dim, p.dv.wide, lane);
       }
       {  // dk: values times R^T, and values times douts times queries
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ldm4(f[i], (rows + set + kB + own) ^ (i * 32));
+        for (int i = 0; i < 4; ++i) ldm4(f[i], (rows + kB + own) ^ (i * 32));
         float o[8][4] = {};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -758,16 +760,17 @@ __global__ void __launch_bounds__(kThreads<64>, 3) attn_kv_kernel(const __grid_c
           }
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i][0] *= f0, o[i][1] *= f0, o[i][2] *= f1, o[i][3] *= f1;
-        add_inner<T, 64, 64>(o, f, cols + set + 3 * kB, rows + set + 2 * kB, rt, powers);
+        add_inner<T, 64, 64>(o, f, cols + 3 * kB, rows + 2 * kB, rt, powers);
         if (p.rep > 1) sum_heads<64>(o, p.sums[0] + sum, sum_step, rt, pad, g, t, r == 0, r + 1 == p.rep);
         if (r + 1 == p.rep)
-          put_rows<T, 64, 64>(smem_at(tiles) + set + kB, o, rt, 0, head_at<T>(p.dk, h, p.rep, tok), -p.dk.token, pad,
+          put_rows<T, 64, 64>(smem_at(tiles) + kB, o, rt, 0, head_at<T>(p.dk, h, p.rep, tok), -p.dk.token, pad,
                               p.dk.dim, p.dk.wide, lane);
       }
       if (c + 1 < chunks)
-        add_tokens<T, 64, 2>(st, power2(a * (float)n), (cols + set + 2 * kB) ^ (warp * 32), rows + set + 3 * kB, weights,
+        add_tokens<T, 64, 2>(st, power2(a * (float)n), (cols + 2 * kB) ^ (warp * 32), rows + 3 * kB, weights,
                              powers.d16);
       __syncthreads();  // the state and the tiles have been read
+      if (c + 1 < chunks) load(c + 1);
     }
   }
 }
@@ -872,8 +875,9 @@ int padded_dim(int32_t dim) { return dim <= 64 ? 64 : 128; }
 // segment costs about two chunks more for its state (32640 tokens, 16 heads of 64: forward
 // MEASURED).
 int32_t segment_tokens(const gs_linear_attn* a, bool backward) {
-  const int64_t chunks = div_up(a->tokens, kL), resident = (int64_t)device_sms() * (256 / padded_dim(a->dim));
-  const int64_t blocks = (int64_t)a->q_heads * (padded_dim(a->vdim) / kV);
+  // (the groups' lengths are on the device: taken as equal)
+  const int64_t chunks = div_up(div_up(a->tokens, a->groups), kL), resident = (int64_t)device_sms() * (256 / padded_dim(a->dim));
+  const int64_t blocks = (int64_t)a->groups * a->q_heads * (padded_dim(a->vdim) / kV);
   const int least = backward ? 2 : 1, most = 32;
   int best = least;
   int64_t cost = INT64_MAX;
@@ -995,7 +999,7 @@ gs_status run_parts(const PartsArgs& p, int64_t slots, int parts, cudaStream_t s
   return GS_OK;
 }
 gs_status run_scan(const ScanArgs& p, cudaStream_t st) {
-  const int64_t blocks = (int64_t)p.split.groups * (p.Dp * p.Ep / kScanThreads);
+  const int64_t blocks = p.split.groups * div_up(p.D * p.E, kScanThreads);
   if (blocks > INT32_MAX) return GS_ERR_INVALID_ARG;
   GS_CUDA(launch_overlapped(attn_scan_kernel<16>, dim3((unsigned)blocks, p.heads, p.scans), dim3(kScanThreads), 0, st,
                             p));
@@ -1013,7 +1017,7 @@ gs_status run_out_of(const OutArgs& p, int64_t slots, cudaStream_t st) {
                             dim3(kThreads<KD>), kOutSmem<KD>, st, p));
   return GS_OK;
 }
-constexpr int kKvSmem = 9 * kL * 64 * 2;
+constexpr int kKvSmem = 5 * kL * 64 * 2 + 64;  // four tiles, the state, a number a warp
 template <typename T>
 gs_status run_kv(const KvArgs& p, int64_t slots, cudaStream_t st) {
   static std::atomic<uint64_t> known{0};
@@ -1060,7 +1064,7 @@ gs_status forward(const gs_linear_attn* a, const Call& c, Side (&s)[4], float* s
   const gs_status copied = copy_rows(a, s, 3, room, st);
   if (copied != GS_OK) return copied;
   if (scan) {
-    const gs_status r = states_of<T>(a, c, {Part{s[1], s[2], 1.f, 0, 0, room.states}, Part{}},
+    const gs_status r = states_of<T>(a, c, {Part{s[1], s[2], 1.f, 0, 0, state_out != nullptr, room.states}, Part{}},
                                      {Scan{a->state, state_out, room.states, 0}, Scan{}}, 1, st);
     if (r != GS_OK) return r;
   }
@@ -1090,7 +1094,8 @@ gs_status backward(const gs_linear_attn* a, const Call& c, Side (&s)[7], const f
   const bool scan = a->tokens > c.split.seg || dstate;
   if (scan) {
     const gs_status r =
-        states_of<T>(a, c, {Part{k, v, 1.f, 0, 0, room.states}, Part{q, g, a->scale, 1, 1, room.grads}},
+        states_of<T>(a, c, {Part{k, v, 1.f, 0, 0, 0, room.states},
+                          Part{q, g, a->scale, 1, 1, dstate != nullptr, room.grads}},
                      {Scan{a->state, nullptr, room.states, 0}, Scan{dstate_out, dstate, room.grads, 1}}, 2, st);
     if (r != GS_OK) return r;
   }
