@@ -65,8 +65,7 @@ struct Job {
   int64_t out_stride;
   int32_t out_wide;            // rows of out start on 16-byte boundaries
   const void* dh;              // kRecompute
-  int64_t dh_stride;
-  int32_t dh_wide;
+  int64_t dh_stride;           // (rows on 16-byte boundaries)
   int32_t hidden, hidden_ld;   // hidden, rounded up to 8: columns of dgate in the workspace
   int32_t accumulate;
   uint32_t load_steps;  // steps whose operands are brought: all, but in the self-test
@@ -264,39 +263,30 @@ __device__ __forceinline__ void rows_out(const uint8_t* room, T* to, int64_t str
         if (c < cols) to[r * stride + c] = *reinterpret_cast<const T*>(room + granule_at(r, c >> 3) + (c & 7) * 2);
   }
 }
-// Zeros where the matrix has nothing.
+// Rows on 16-byte boundaries; zeros where the matrix has nothing (from granules that
+// hold any of it).
 template <typename T>
-__device__ __forceinline__ void rows_in(uint8_t* room, const T* from, int64_t stride, int rows, int cols,
-                                        bool wide, int lane) {
-  if (wide) {
-    const int g = lane & 7;
-    uint4 v[8];
+__device__ __forceinline__ void rows_in(uint8_t* room, const T* from, int64_t stride, int rows, int cols, int lane) {
+  const int g = lane & 7;
+  uint4 v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = i * 4 + (lane >> 3);
-      v[i] = make_uint4(0, 0, 0, 0);
-      if (r >= rows || g * 8 >= cols) continue;
-      const T* p = from + r * stride + g * 8;
-      if (g * 8 + 8 <= cols) {
-        v[i] = *reinterpret_cast<const uint4*>(p);
-      } else {
-        Pack<T, 8> e;
+  for (int i = 0; i < 8; ++i) {
+    const int r = i * 4 + (lane >> 3);
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (r >= rows || g * 8 >= cols) continue;
+    const T* p = from + r * stride + g * 8;
+    if (g * 8 + 8 <= cols) {
+      v[i] = *reinterpret_cast<const uint4*>(p);
+    } else {
+      Pack<T, 8> e;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) e.v[j] = g * 8 + j < cols ? p[j] : from_f32<T>(0.f);
-        v[i] = *reinterpret_cast<const uint4*>(&e);
-      }
+      for (int j = 0; j < 8; ++j) e.v[j] = g * 8 + j < cols ? p[j] : from_f32<T>(0.f);
+      v[i] = *reinterpret_cast<const uint4*>(&e);
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      *reinterpret_cast<uint4*>(room + granule_at(i * 4 + (lane >> 3), g)) = v[i];
-  } else {
-#pragma unroll 8
-    for (int r = 0; r < 32; ++r)
-#pragma unroll
-      for (int c = lane; c < 64; c += 32)
-        *reinterpret_cast<T*>(room + granule_at(r, c >> 3) + (c & 7) * 2) =
-            r < rows && c < cols ? from[r * stride + c] : from_f32<T>(0.f);
   }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    *reinterpret_cast<uint4*>(room + granule_at(i * 4 + (lane >> 3), g)) = v[i];
 }
 // Words 16 c .. 16 c + 15 (32 elements) of the thread's own row.
 __device__ __forceinline__ void own_row_put(uint8_t* room, int lane, int c, const uint32_t* w) {
@@ -316,6 +306,20 @@ template <typename T>
 __device__ __forceinline__ float2 two_of(uint32_t w) {
   const Pack<T, 2> e = *reinterpret_cast<const Pack<T, 2>*>(&w);
   return make_float2(to_f32(e.v[0]), to_f32(e.v[1]));
+}
+
+// mma.sync, 16 x 8 x 16.
+template <typename T>
+__device__ __forceinline__ void mma_rows(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  if constexpr (std::is_same<T, __half>::value)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 template <typename TO>
@@ -457,7 +461,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t from = lanes + sum * kTile;
       if (MODE == kRecompute) {
         const int col0 = tn * kHalf + half * 64, cols = (int)min((int64_t)64, p.cols - col0);
-        rows_in<T>(room, (const T*)p.dh + row0 * p.dh_stride + col0, p.dh_stride, rows, cols, p.dh_wide, lane);
+        rows_in<T>(room, (const T*)p.dh + row0 * p.dh_stride + col0, p.dh_stride, rows, cols, lane);
         __syncwarp();
       }
       if (!__all_sync(0xffffffffu, wait(smem_u32(&c->sum_full[sum]), phase, c, p, status))) break;
@@ -511,6 +515,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           rows_out<T>(room, to, p.out_stride, rows, cols, true, lane);
         }
         __syncwarp();
+      } else if (MODE == kDx && w.slot >= 0) {
+        float* to = partial + ((size_t)(cluster * 2 + w.slot) * 2 + rank) * kPartialFloats +
+                    (quarter * 32 + lane) * kTile + half * kHalf;
+#pragma unroll 1
+        for (int b = 0; b < 4; ++b) {
+          float v[32];
+          tmem_load32(from + half * kHalf + b * 32, v);
+          tmem_wait(v);
+          if (b == 3) release();
+#pragma unroll
+          for (int j = 0; j < 32; j += 4)
+            *reinterpret_cast<float4*>(to + b * 32 + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+        }
       } else if (MODE == kDx) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -574,54 +591,156 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-// Joins the partial sums of dW's tiles that several clusters share, in the clusters'
-// order: a warp takes one column of a CTA's half tile, a thread four channels.
-template <typename TO>
+// Joins the partial sums of the tiles that several clusters share, in the clusters' order.
+// dW's lie column by column, 128 channels each: a warp takes a column of a CTA's half tile,
+// a thread four channels.  dx's lie row by row: a warp takes a row, a thread eight columns.
+template <typename TO, bool DX>
 __global__ void __launch_bounds__(128) ffn_join_kernel(const __grid_constant__ Job p, const float* partial) {
   launch_dependents();
   wait_for_previous();
-  constexpr int kPerHalf = kTile / 4;
+  constexpr int kLines = DX ? kHalf : kTile, kPerHalf = kLines / 4, kPer = DX ? 8 : 4;
   const int tile = blockIdx.x / (2 * kPerHalf), rank = blockIdx.x / kPerHalf % 2;
-  const int col = blockIdx.x % kPerHalf * 4 + (int)(threadIdx.x >> 5), in = threadIdx.x % 32 * 4;
+  const int line = blockIdx.x % kPerHalf * 4 + (int)(threadIdx.x >> 5), in = threadIdx.x % 32 * kPer;
   const int64_t first = (int64_t)tile * p.steps, last = first + p.steps - 1;
   const int lo = (int)(first / p.quota), hi = (int)(last / p.quota);
   if (lo == hi) return;  // summed by one cluster, and written by it
   const int id = p.waves * p.clusters + tile;
-  const int64_t n = (int64_t)(id % p.tiles_n) * kTile + col, ch = (int64_t)(id / p.tiles_n) * kTile + rank * kHalf + in;
-  const int64_t row = n < p.cols ? dw_row(p, n) : -1;
-  if (row < 0 || ch >= p.rows) return;
+  const int64_t m = (int64_t)(id / p.tiles_n) * kTile + rank * kHalf + (DX ? line : in);
+  const int64_t n = (int64_t)(id % p.tiles_n) * kTile + (DX ? in : line);
+  const int64_t row = DX ? m : n < p.cols ? dw_row(p, n) : -1;
+  if (row < 0 || m >= p.rows || n >= p.cols) return;
   // a cluster's first segment is in its slot 0, its second in slot 1
   const int two = (int64_t)lo * p.quota / p.steps == tile ? 0 : 1;
   const float4* from = reinterpret_cast<const float4*>(partial + ((size_t)lo * 4 + rank) * kPartialFloats +
-                                                       (size_t)col * kHalf + in);
+                                                       (size_t)line * (DX ? kTile : kHalf) + in);
   const size_t next = kPartialFloats;  // float4s from one cluster's slot 0 to the next one's
-  float4 v = from[two ? kPartialFloats / 2 : 0];
-#pragma unroll 8
-  for (int i = 1; i <= hi - lo; ++i) {
-    const float4 u = from[i * next];
-    v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
-  }
-  const float r[4] = {v.x, v.y, v.z, v.w};
-  TO* to = (TO*)p.out + row * p.out_stride + ch;
+  float r[kPer];
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (ch + j < p.rows) put_dw<TO>(to + j, r[j], p.accumulate);
+  for (int q = 0; q < kPer / 4; ++q) {
+    float4 v = from[(two ? kPartialFloats / 2 : 0) + q];
+#pragma unroll 8
+    for (int i = 1; i <= hi - lo; ++i) {
+      const float4 u = from[i * next + q];
+      v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+    }
+    r[4 * q] = v.x, r[4 * q + 1] = v.y, r[4 * q + 2] = v.z, r[4 * q + 3] = v.w;
+  }
+  TO* to = (TO*)p.out + row * p.out_stride + (DX ? n : m);
+  const int64_t left = DX ? p.cols - n : p.rows - m;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j)
+    if (j < left) put_dw<TO>(to + j, r[j], p.accumulate);
 }
 
-// Rows that start anywhere, copied to rows of `ld` elements (a multiple of 8) that TMA
-// can read; the padding is zeros.
+// Rows that start anywhere, copied to padded rows that TMA can read (`granules` of eight
+// elements each); the padding is zeros.
+struct Copies {
+  int count;
+  struct {
+    const void* from;
+    void* to;
+    int64_t rows, stride, to_stride;
+    int32_t cols, granules;
+  } c[3];
+};
 template <typename W>
-__global__ void __launch_bounds__(256) ffn_rows_kernel(int64_t rows, int cols, int ld, const W* from,
-                                                       int64_t stride, W* to) {
+__global__ void __launch_bounds__(256) ffn_rows_kernel(const __grid_constant__ Copies p) {
   launch_dependents();
   wait_for_previous();
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, r = i / (ld / 8);
-  const int c = (int)(i % (ld / 8)) * 8;
-  if (r >= rows) return;
+  const auto& k = p.c[blockIdx.y];
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, r = i / k.granules;
+  const int c = (int)(i % k.granules) * 8;
+  if (r >= k.rows) return;
+  const W* from = (const W*)k.from + r * k.stride;
   Pack<W, 8> v;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v.v[j] = c + j < cols ? from[r * stride + c + j] : W(0);
-  store_pack<W, 8>(to + r * ld + c, v);
+  for (int j = 0; j < 8; ++j) v.v[j] = c + j < k.cols ? from[c + j] : W(0);
+  store_pack<W, 8>((W*)k.to + r * k.to_stride + c, v);
+}
+
+// ---- few tokens -----------------------------------------------------------------
+// Up to 8 NT tokens: the weights' bytes bound the call, so each is read once, straight
+// from memory into the operands' registers (mma.sync).  A block has 8 hidden channels:
+// the first operand's 16 rows are their 8 rows of Wg and 8 of Wu, so that a thread holds
+// gate and up of the same channel and token; its warps share out the channels of x.  A
+// thread takes 16 bytes of a row at a time: the sum's terms in another order than the
+// instruction's, the same one in both operands.  (1024 x 2816 bf16,
+// one token: 3.7 us, 3.1 TB/s.)
+constexpr int kFewWarps = 8;
+constexpr int kFewRows = 8;
+
+template <typename T, bool WIDE>
+__device__ __forceinline__ uint4 eight_of(const T* row, int k, int channels) {
+  if (WIDE && k + 8 <= channels) return *reinterpret_cast<const uint4*>(row + k);
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (k + j < channels) w[j / 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(row + k + j) << (j % 2 * 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+struct Few {
+  int32_t tokens, channels, hidden;
+  const void *x, *w;
+  int64_t x_stride, w_stride;
+  void* h;
+  int64_t h_stride;
+};
+
+template <typename T, int ACT, int NT, bool WIDE>
+__global__ void __launch_bounds__(32 * kFewWarps) ffn_few_kernel(const __grid_constant__ Few p) {
+  launch_dependents();
+  wait_for_previous();
+  __shared__ float sums[kFewWarps][NT * 4][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int f = blockIdx.x * kFewRows + g;
+  const T* gate = (const T*)p.w + (int64_t)min(f, p.hidden - 1) * p.w_stride;
+  const T* up = gate + (int64_t)p.hidden * p.w_stride;
+  float c[NT][4] = {};
+  constexpr int kAhead = NT > 2 ? 2 : 4;  // blocks of 32 channels under way
+  for (int b = warp; b * 32 < p.channels; b += kFewWarps * kAhead) {
+    uint4 a0[kAhead], a1[kAhead], x[kAhead][NT];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int k = (b + i * kFewWarps) * 32 + t * 8;
+      a0[i] = a1[i] = make_uint4(0, 0, 0, 0);
+      if (k < p.channels) {
+        a0[i] = eight_of<T, WIDE>(gate, k, p.channels);
+        a1[i] = eight_of<T, WIDE>(up, k, p.channels);
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        x[i][n] = make_uint4(0, 0, 0, 0);
+        if (k < p.channels && n * 8 + g < p.tokens)
+          x[i][n] = eight_of<T, WIDE>((const T*)p.x + (n * 8 + g) * p.x_stride, k, p.channels);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        mma_rows<T>(c[n], a0[i].x, a1[i].x, a0[i].y, a1[i].y, x[i][n].x, x[i][n].y);
+        mma_rows<T>(c[n], a0[i].z, a1[i].z, a0[i].w, a1[i].w, x[i][n].z, x[i][n].w);
+      }
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sums[warp][n * 4 + j][lane] = c[n][j];
+  __syncthreads();
+  if (warp >= NT) return;
+  float v[4];  // gate of tokens 2t, 2t + 1, up of the same
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[j] = sums[0][warp * 4 + j][lane];
+#pragma unroll
+    for (int i = 1; i < kFewWarps; ++i) v[j] += sums[i][warp * 4 + j][lane];
+  }
+  const float2 a = act_value<T, ACT>(make_float2(v[0], v[1]));
+  const int token = warp * 8 + 2 * t;
+  T* to = (T*)p.h + token * p.h_stride + f;
+  if (f < p.hidden && token < p.tokens) to[0] = from_f32<T>(a.x * v[2]);
+  if (f < p.hidden && token + 1 < p.tokens) to[p.h_stride] = from_f32<T>(a.y * v[3]);
 }
 
 // ---- host ------------------------------------------------------------------
@@ -735,23 +854,34 @@ struct Room {  // the workspace's parts
   }
 };
 
-// The matrix itself, or its copy in padded rows, as TMA reads it.
+// The matrix itself, or (then to be copied) its copy in padded rows, as TMA reads it.
 struct Rows {
   const void* p;
   int64_t stride;
 };
-gs_status readable(Rows* out, int64_t rows, int32_t cols, const void* p, int64_t stride, void* room,
-                   cudaStream_t st) {
+bool readable(const void* p, int64_t rows, int64_t cols, int64_t stride) {
+  return aligned16(p) && (rows < 2 || (stride % 8 == 0 && stride >= cols));
+}
+void copy_rows(Copies* c, const void* from, int64_t rows, int32_t cols, int64_t stride, void* to, int64_t to_stride) {
+  auto& k = c->c[c->count++];
+  k.from = from, k.to = to;
+  k.rows = rows, k.stride = stride, k.to_stride = to_stride;
+  k.cols = cols, k.granules = (int32_t)(padded(cols) / 8);
+}
+Rows rows_of(Copies* c, const void* p, int64_t rows, int32_t cols, int64_t stride, void* room) {
   const int64_t ld = padded(cols);
-  if (aligned16(p) && (rows < 2 || (stride % 8 == 0 && stride >= cols))) {
-    *out = Rows{p, rows < 2 ? ld : stride};
-    return GS_OK;
-  }
-  const int64_t blocks = div_up(rows * (ld / 8), 256);
+  if (readable(p, rows, cols, stride)) return Rows{p, rows < 2 ? ld : stride};
+  copy_rows(c, p, rows, cols, stride, room, ld);
+  return Rows{room, ld};
+}
+gs_status run_copies(const Copies& c, cudaStream_t st) {
+  int64_t most = 0;
+  for (int i = 0; i < c.count; ++i)
+    if (c.c[i].rows * c.c[i].granules > most) most = c.c[i].rows * c.c[i].granules;
+  if (!most) return GS_OK;
+  const int64_t blocks = div_up(most, 256);
   if (blocks > INT32_MAX) return GS_ERR_INVALID_ARG;
-  GS_CUDA(launch_overlapped(ffn_rows_kernel<uint16_t>, dim3((unsigned)blocks), dim3(256), 0, st, rows, cols,
-                            (int)ld, (const uint16_t*)p, stride, (uint16_t*)room));
-  *out = Rows{room, ld};
+  GS_CUDA(launch_overlapped(ffn_rows_kernel<uint16_t>, dim3((unsigned)blocks, c.count), dim3(256), 0, st, c));
   return GS_OK;
 }
 
@@ -763,11 +893,11 @@ void deal(Job* p, int64_t tiles, int clusters, bool split) {
   const int64_t rem = tiles - (int64_t)p->waves * clusters;
   p->rem_steps = rem * p->steps;
   p->quota = p->steps;
-  if (split && rem) {
-    constexpr int64_t kMinSteps = 8;  // that a share is worth its partial sum
-    p->quota = div_up(p->rem_steps, clusters);
-    if (p->quota < kMinSteps) p->quota = kMinSteps < p->steps ? kMinSteps : p->steps;
-  }
+  // A share is worth its partial sum from 8 steps on; the join takes as long as 12 steps
+  // and one more for every third tile (32640 x 5632 x 1024, dx: its 56 remaining tiles
+  // of 88 steps whole 206 us, in shares 205 and 10 for the join).
+  const int64_t share = div_up(p->rem_steps, clusters), quota = share > 8 ? share : 8;
+  if (split && rem && quota + 12 + rem / 3 < p->steps) p->quota = quota;
 }
 
 gs_status launch(const void* kernel, const Job& p, const CUtensorMap& a, const CUtensorMap& b, float* partial,
@@ -779,6 +909,14 @@ gs_status launch(const void* kernel, const Job& p, const CUtensorMap& a, const C
   return GS_OK;
 }
 
+template <typename TO, bool DX>
+gs_status join(const Job& p, int64_t tiles, const Room& room, cudaStream_t st) {
+  const int64_t rem = tiles - (int64_t)p.waves * p.clusters;
+  if (!rem || p.quota % p.steps == 0) return GS_OK;
+  GS_CUDA(launch_overlapped(ffn_join_kernel<TO, DX>, dim3((unsigned)(rem * 2 * (DX ? kHalf / 4 : kTile / 4))), dim3(128),
+                            0, st, p, room.partial));
+  return GS_OK;
+}
 const void* pick(int32_t dtype, int mode, int act, bool f32 = false) {
   return dtype == GS_BF16 ? kernel_of<__nv_bfloat16>(mode, act, f32) : kernel_of<__half>(mode, act, f32);
 }
@@ -815,6 +953,32 @@ gs_status project(const Args& a, const Rows& x, const Rows& w, const Job& job, i
   return launch(pick(a.dtype, mode, a.act), p, am, bm, room.partial, room.status, st);
 }
 
+template <typename T, int ACT, int NT>
+gs_status few_of(const Few& p, bool wide, cudaStream_t st) {
+  const dim3 grid((unsigned)div_up(p.hidden, kFewRows)), block(32 * kFewWarps);
+  GS_CUDA(wide ? launch_overlapped(ffn_few_kernel<T, ACT, NT, true>, grid, block, 0, st, p)
+               : launch_overlapped(ffn_few_kernel<T, ACT, NT, false>, grid, block, 0, st, p));
+  return GS_OK;
+}
+template <typename T, int ACT>
+gs_status few_of(const Few& p, bool wide, cudaStream_t st) {
+  return p.tokens <= 8 ? few_of<T, ACT, 1>(p, wide, st) : p.tokens <= 16 ? few_of<T, ACT, 2>(p, wide, st)
+                                                                         : few_of<T, ACT, 4>(p, wide, st);
+}
+// (1024 x 2816, 16 and 32 tokens: 5.7 and 7.9 us, on the tensor cores' tiles 8.9;
+// 2048 x 5632: 14.4 and 19.7, 14.0)
+bool few(const Args& a) {
+  return a.tokens <= 16 || (a.tokens <= 32 && (int64_t)a.channels * a.hidden <= (1 << 22));
+}
+gs_status few_tokens(const Args& a, void* h, int64_t h_stride, cudaStream_t st) {
+  const Few p{(int32_t)a.tokens, a.channels, a.hidden, a.x, a.w, a.x_stride, a.w_stride, h, h_stride};
+  const bool wide = rows_aligned(a.x, a.tokens < 2 ? 0 : a.x_stride, 2, 16) && rows_aligned(a.w, a.w_stride, 2, 16);
+  if (a.dtype == GS_BF16)
+    return a.act == GS_ACT_SILU ? few_of<__nv_bfloat16, GS_ACT_SILU>(p, wide, st)
+                                : few_of<__nv_bfloat16, GS_ACT_GELU>(p, wide, st);
+  return a.act == GS_ACT_SILU ? few_of<__half, GS_ACT_SILU>(p, wide, st) : few_of<__half, GS_ACT_GELU>(p, wide, st);
+}
+
 gs_status forward(const Args& a, void* h, int64_t h_stride, void* workspace, size_t ws_bytes,
                   uint32_t load_steps, int64_t wait_ns, cudaStream_t st) {
   if (!args_ok(a)) return GS_ERR_INVALID_ARG;
@@ -822,14 +986,16 @@ gs_status forward(const Args& a, void* h, int64_t h_stride, void* workspace, siz
   if (!workspace || !aligned16(workspace) || ws_bytes < room.bytes) return GS_ERR_INVALID_ARG;
   if (a.tokens == 0) return GS_OK;
   if (!matrix_ok(h, a.tokens, a.hidden, h_stride, 2, true)) return GS_ERR_INVALID_ARG;
+  if (few(a) && load_steps == UINT32_MAX) return few_tokens(a, h, h_stride, st);
   const int clusters = resident_clusters();
   if (!clusters) {
     (void)cudaGetLastError();
     return GS_ERR_CUDA;
   }
-  Rows x, w;
-  gs_status s = readable(&x, a.tokens, a.channels, a.x, a.x_stride, room.x, st);
-  if (s == GS_OK) s = readable(&w, 2 * (int64_t)a.hidden, a.channels, a.w, a.w_stride, room.w, st);
+  Copies copies{};
+  const Rows x = rows_of(&copies, a.x, a.tokens, a.channels, a.x_stride, room.x);
+  const Rows w = rows_of(&copies, a.w, 2 * (int64_t)a.hidden, a.channels, a.w_stride, room.w);
+  const gs_status s = run_copies(copies, st);
   if (s != GS_OK) return s;
   Job p{};
   p.out = h;
@@ -865,12 +1031,18 @@ gs_status backward(const Args& a, const void* dh, int64_t dh_stride, void* dx, i
     (void)cudaGetLastError();
     return GS_ERR_CUDA;
   }
-  Rows x, w;
-  gs_status s = readable(&x, a.tokens, a.channels, a.x, a.x_stride, room.x, st);
-  if (s == GS_OK) s = readable(&w, rows, a.channels, a.w, a.w_stride, room.w, st);
+  Copies copies{};
+  const Rows x = rows_of(&copies, a.x, a.tokens, a.channels, a.x_stride, room.x);
+  const Rows w = rows_of(&copies, a.w, rows, a.channels, a.w_stride, room.w);
+  // odd rows of dh are copied to where dup will be: a warp reads its block of dh before it
+  // writes that of dup
+  const int64_t ld = padded(a.hidden);
+  const bool dh_wide = rows_aligned(dh, a.tokens < 2 ? 0 : dh_stride, 2, 16);
+  uint16_t* dh_room = (uint16_t*)room.grads + ld;
+  if (!dh_wide) copy_rows(&copies, dh, a.tokens, a.hidden, dh_stride, dh_room, 2 * ld);
+  gs_status s = run_copies(copies, st);
   if (s != GS_OK) return s;
 
-  const int64_t ld = padded(a.hidden);
   Job p{};
   p.hidden = a.hidden;
   p.hidden_ld = (int)ld;
@@ -880,9 +1052,8 @@ gs_status backward(const Args& a, const void* dh, int64_t dh_stride, void* dx, i
     Job q = p;
     q.out = room.grads;
     q.out_stride = 2 * ld;
-    q.dh = dh;
-    q.dh_stride = dh_stride;
-    q.dh_wide = rows_aligned(dh, a.tokens < 2 ? 0 : dh_stride, 2, 16);
+    q.dh = dh_wide ? dh : dh_room;
+    q.dh_stride = dh_wide ? dh_stride : 2 * ld;
     s = project(a, x, w, q, kRecompute, clusters, room, st);
     if (s != GS_OK) return s;
   }
@@ -897,13 +1068,16 @@ gs_status backward(const Args& a, const void* dh, int64_t dh_stride, void* dx, i
     q.tiles_n = (int)div_up(a.channels, kTile);
     q.part_steps = (int)div_up(a.hidden, kStep);
     q.steps = 2 * q.part_steps;
-    deal(&q, div_up(a.tokens, kTile) * q.tiles_n, clusters, false);
+    const int64_t tiles = div_up(a.tokens, kTile) * q.tiles_n;
+    deal(&q, tiles, clusters, true);
     const int64_t ad[3] = {a.hidden, a.tokens, 2}, as[2] = {2 * ld, ld};
     const int64_t bd[3] = {a.channels, a.hidden, 2}, bs[2] = {w.stride, w.stride * a.hidden};
     const int ab[3] = {kStep, kHalf, 1}, bb[3] = {64, kStep, 1};
     if (!make_map(&am, a.dtype, room.grads, 3, ad, as, ab) || !make_map(&bm, a.dtype, w.p, 3, bd, bs, bb))
       return GS_ERR_CUDA;
     s = launch(pick(a.dtype, kDx, 0), q, am, bm, room.partial, room.status, st);
+    if (s == GS_OK)
+      s = a.dtype == GS_BF16 ? join<__nv_bfloat16, true>(q, tiles, room, st) : join<__half, true>(q, tiles, room, st);
     if (s != GS_OK) return s;
   }
   if (dw) {
@@ -925,16 +1099,9 @@ gs_status backward(const Args& a, const void* dh, int64_t dh_stride, void* dx, i
     const bool f32 = dw_dtype == GS_F32;
     s = launch(pick(a.dtype, kDw, 0, f32), q, am, bm, room.partial, room.status, st);
     if (s != GS_OK) return s;
-    const int64_t rem = tiles - (int64_t)q.waves * clusters;
-    if (rem && q.quota % q.steps != 0) {
-      const dim3 grid((unsigned)(rem * 2 * (kTile / 4)));
-      if (f32)
-        GS_CUDA(launch_overlapped(ffn_join_kernel<float>, grid, dim3(128), 0, st, q, room.partial));
-      else if (a.dtype == GS_BF16)
-        GS_CUDA(launch_overlapped(ffn_join_kernel<__nv_bfloat16>, grid, dim3(128), 0, st, q, room.partial));
-      else
-        GS_CUDA(launch_overlapped(ffn_join_kernel<__half>, grid, dim3(128), 0, st, q, room.partial));
-    }
+    s = f32 ? join<float, false>(q, tiles, room, st)
+            : a.dtype == GS_BF16 ? join<__nv_bfloat16, false>(q, tiles, room, st) : join<__half, false>(q, tiles, room, st);
+    if (s != GS_OK) return s;
   }
   return GS_OK;
 }

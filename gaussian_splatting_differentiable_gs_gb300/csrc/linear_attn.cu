@@ -870,10 +870,11 @@ constexpr int64_t kMaxTokens = ((int64_t)1 << 31) - 1;
 
 int padded_dim(int32_t dim) { return dim <= 64 ? 64 : 128; }
 
-// Chunks of a segment.  The kernels run in waves of as many blocks as the SMs hold (four
-// of four warps each, two of eight), a wave takes as long as a segment, and each
-// segment costs about two chunks more for its state (32640 tokens, 16 heads of 64: forward
-// MEASURED).
+// Tokens of a segment.  The kernels run in waves of as many blocks as the SMs hold (four
+// of four warps each, two of eight), a wave takes as long as a segment, and each segment
+// costs about two chunks more for its state.  Where a group is one segment its states need
+// neither a sum nor a scan: those two kernels' start is worth about five chunks, and their
+// work half of the outputs'.
 int32_t segment_tokens(const gs_linear_attn* a, bool backward) {
   // (the groups' lengths are on the device: taken as equal)
   const int64_t chunks = div_up(div_up(a->tokens, a->groups), kL), resident = (int64_t)device_sms() * (256 / padded_dim(a->dim));
@@ -882,7 +883,8 @@ int32_t segment_tokens(const gs_linear_attn* a, bool backward) {
   int best = least;
   int64_t cost = INT64_MAX;
   for (int m = least; m <= most; ++m) {
-    const int64_t c = div_up(div_up(chunks, m) * blocks, resident) * (m + 2);
+    const int64_t waves = div_up(div_up(chunks, m) * blocks, resident);
+    const int64_t c = chunks <= m ? 2 * waves * (chunks + 2) : 3 * waves * (m + 2) + 10;
     if (c < cost) cost = c, best = m;
   }
   return best * kL;

@@ -382,12 +382,24 @@ def gs_act8_wgrad(dy, q, e, dw, workspace, accumulate=False, stream=None):
 # --------------------------------------------------------------------------
 # the gated feed-forward block
 
+# (a tensor's device is -1 on the CPU, so that one comparison says both that it is on a
+# GPU and on which)
 
-def _on_one_device(*tensors):
-    device = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and t.get_device() != device:
-            raise ValueError("tensors on cuda:%d and cuda:%d" % (device, t.get_device()))
+
+def _refuse_device(t, name, device):
+    raise ValueError("%s is on %s, not on cuda:%d" % (name, getattr(t, "device", "no device"), device))
+
+
+def _workspace(t, device):
+    """(pointer, size) of a workspace."""
+    try:
+        if t.dtype is torch.uint8 and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr(), t.numel()
+    except AttributeError:
+        pass
+    if t is None:
+        return 0, 0
+    raise ValueError("workspace must be a contiguous uint8 tensor on cuda:%d" % device)
 
 
 def gs_ffn_workspace_bytes(tokens, channels, hidden, backward=True):
@@ -396,19 +408,37 @@ def gs_ffn_workspace_bytes(tokens, channels, hidden, backward=True):
 
 def _ffn_args(x, w, h, name, workspace, act):
     """Checks what both directions have: the C call's arguments up to h's, and the workspace's."""
+    try:
+        dt, device = x.dtype, x.get_device()
+        tokens, c = x.shape
+        rows, wc = w.shape
+        (xs, x1), (ws, w1), (hs, h1) = x.stride(), w.stride(), h.stride()
+        hidden = rows // 2
+        if ((dt is torch.bfloat16 or dt is torch.float16) and w.dtype is dt and h.dtype is dt and wc == c
+                and rows > 0 and not rows & 1 and h.shape == (tokens, hidden)
+                and device == w.get_device() == h.get_device() >= 0
+                and (x1 == 1 or c == 1 or not tokens) and (w1 == 1 or c == 1)
+                and (h1 == 1 or hidden == 1 or not tokens)):
+            return ((tokens, c, hidden, DTYPES[dt], ACTS[act], x.data_ptr(), xs, w.data_ptr(), ws, h.data_ptr(), hs),
+                    _workspace(workspace, device))
+    except (AttributeError, TypeError, KeyError):
+        if act not in ACTS:
+            raise ValueError("act: one of %s" % ", ".join(ACTS)) from None
+    except ValueError as e:
+        if "unpack" not in str(e):
+            raise
+    # something is wrong: say what
     (tokens, c), code = _first(x, "x")
     if code == 2:
         raise ValueError("x: bfloat16 or float16")
     if getattr(w, "dim", int)() != 2 or w.shape[0] % 2 or not w.shape[0]:
         raise ValueError("w must be [2 * hidden, channels]")
-    hidden = w.shape[0] // 2
-    _mat(w, "w", (2 * hidden, c), x.dtype)
-    _mat(h, name, (tokens, hidden), x.dtype)
-    if act not in ACTS:
-        raise ValueError("act: one of %s" % ", ".join(ACTS))
-    size = workspace.numel()
-    return ((tokens, c, hidden, code, ACTS[act], x.data_ptr(), x.stride(0), w.data_ptr(), w.stride(0),
-             h.data_ptr(), h.stride(0)), (_vec(workspace, "workspace", size, torch.uint8), size))
+    _mat(w, "w", (w.shape[0], c), x.dtype)
+    _mat(h, name, (tokens, w.shape[0] // 2), x.dtype)
+    for t, n in ((w, "w"), (h, name)):
+        if t.get_device() != x.get_device():
+            _refuse_device(t, n, x.get_device())
+    raise ValueError("x, w, %s: not as documented" % name)
 
 
 def gs_ffn_fwd(x, w, h, workspace, act="silu", stream=None):
@@ -416,8 +446,9 @@ def gs_ffn_fwd(x, w, h, workspace, act="silu", stream=None):
     channels] the gate's rows and then up's; bfloat16 or float16.  workspace: uint8,
     gs_ffn_workspace_bytes() bytes, its first 256 zero before the first call."""
     args, ws = _ffn_args(x, w, h, "h", workspace, act)
-    _on_one_device(x, w, h, workspace)
-    _check("gs_ffn_fwd", lib().gs_ffn_fwd(*args, *ws, _stream(stream, x)))
+    status = lib().gs_ffn_fwd(*args, *ws, _stream(stream, x))
+    if status:
+        _check("gs_ffn_fwd", status)
 
 
 def gs_ffn_bwd(x, w, dh, dx, dw, workspace, act="silu", accumulate=False, stream=None):
@@ -432,7 +463,10 @@ def gs_ffn_bwd(x, w, dh, dx, dw, workspace, act="silu", accumulate=False, stream
             raise ValueError("dw: type %s" % dw.dtype)
         _mat(dw, "dw", w.shape, dw.dtype)
         g, gs_, code = dw.data_ptr(), dw.stride(0), DTYPES[dw.dtype]
-    _on_one_device(x, w, dh, dx, dw, workspace)
+    device = x.get_device()
+    for t, n in ((dx, "dx"), (dw, "dw")):
+        if t is not None and t.get_device() != device:
+            _refuse_device(t, n, device)
     _check("gs_ffn_bwd", lib().gs_ffn_bwd(*args, d, ds, g, gs_, code, 1 if accumulate else 0, *ws,
                                           _stream(stream, x)))
 
@@ -443,49 +477,61 @@ def gs_ffn_bwd(x, w, dh, dx, dw, workspace, act="silu", accumulate=False, stream
 
 def _attn(q, k, v, log_decay, group_offsets, state, scale):
     """Checks what every call has: (the packed gs_linear_attn, q's, k's and v's packed
-    heads, shape of the outputs, shape of the states)."""
-    code = DTYPES.get(getattr(q, "dtype", None))
-    if code is None or code == 2 or q.dim() != 3:
-        raise ValueError("q must be a CUDA [tokens, heads, dim] tensor of bfloat16 or float16")
-    tokens, hq, dim = q.shape
-    if getattr(k, "dim", int)() != 3 or getattr(v, "dim", int)() != 3:
-        raise ValueError("k and v must be CUDA [tokens, heads, dim] tensors")
-    hk, vdim = k.shape[1], v.shape[2]
+    heads, shape of the outputs, shape of the states, q's device)."""
+    try:
+        code = DTYPES[q.dtype]
+        tokens, hq, dim = q.shape
+        hk, vdim = k.shape[1], v.shape[2]
+    except (AttributeError, KeyError, ValueError, IndexError, TypeError):
+        raise ValueError("q, k and v must be CUDA [tokens, heads, dim] tensors of bfloat16 or float16") from None
+    if code == 2:
+        raise ValueError("q must be bfloat16 or float16")
     if not hk or not hq or hq % hk:
         raise ValueError("%d query heads do not share %d key heads evenly" % (hq, hk))
-    groups = 1
+    device, groups, offsets = q.get_device(), 1, 0
     if group_offsets is not None:
         groups = group_offsets.numel() - 1
         if groups < 1:
             raise ValueError("group_offsets must have groups + 1 entries")
+        offsets = _entries(group_offsets, "group_offsets", (groups + 1,), torch.int32, device)
     states = (groups, hq, dim, vdim)
     packed = _ATTN.pack(tokens, hq, hk, dim, vdim, groups, code, dim ** -0.5 if scale is None else scale,
-                        _vec(log_decay, "log_decay", hq),
-                        _vec(group_offsets, "group_offsets", groups + 1, torch.int32),
-                        _states(state, "state", states))
-    return (packed, _attn_heads(q, "q", (tokens, hq, dim), q), _attn_heads(k, "k", (tokens, hk, dim), q),
-            _attn_heads(v, "v", (tokens, hk, vdim), q), (tokens, hq, vdim), states)
+                        _entries(log_decay, "log_decay", (hq,), torch.float32, device), offsets,
+                        0 if state is None else _entries(state, "state", states, torch.float32, device))
+    dt = q.dtype
+    return (packed, _attn_heads(q, "q", (tokens, hq, dim), dt, device),
+            _attn_heads(k, "k", (tokens, hk, dim), dt, device),
+            _attn_heads(v, "v", (tokens, hk, vdim), dt, device), (tokens, hq, vdim), states, device)
 
 
-def _attn_heads(t, name, shape, like):
-    if (getattr(t, "shape", None) != shape or t.dtype is not like.dtype
-            or t.get_device() != like.get_device() or not t.is_cuda):
-        raise ValueError("%s must be a %s tensor %s on q's device" % (name, like.dtype, list(shape)))
-    a, b, c = t.stride()
-    if c != 1 and shape[2] > 1 and t.numel():
+def _attn_heads(t, name, shape, dtype, device):
+    try:
+        a, b, c = t.stride()
+        if (t.shape == shape and t.dtype is dtype and t.get_device() == device >= 0
+                and (c == 1 or shape[2] == 1 or not t.numel())):
+            return _ATTN_HEADS.pack(t.data_ptr(), a, b)
+    except (AttributeError, ValueError, TypeError):
+        pass
+    if getattr(t, "shape", None) == shape and t.dtype is dtype and t.is_cuda:
+        if t.get_device() != device:
+            _refuse_device(t, name, device)
         raise ValueError("%s: the last axis must be contiguous" % name)
-    return _ATTN_HEADS.pack(t.data_ptr(), a, b)
+    raise ValueError("%s must be a CUDA %s tensor %s" % (name, dtype, list(shape)))
 
 
-def _states(t, name, shape):
-    if t is None:
-        return 0
-    if t.shape != shape:
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), shape))
-    return _vec(t, name, shape[0] * shape[1] * shape[2] * shape[3])
+def _entries(t, name, shape, dtype, device):
+    """The pointer of a contiguous tensor of that shape; 0 for None."""
+    try:
+        if t.shape == shape and t.dtype is dtype and t.get_device() == device >= 0 and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        if t is None:
+            return 0
+    raise ValueError("%s must be a contiguous %s tensor %s on q's device" % (name, dtype, list(shape)))
 
 
 def gs_linear_attn_workspace_bytes(tokens, q_heads, k_heads, dim, vdim, groups=1, backward=True):
+    """What a call needs at most (0: refused); less where every row starts on a 16-byte boundary."""
     return int(lib().gs_linear_attn_workspace_bytes(
         _ATTN.pack(tokens, q_heads, k_heads, dim, vdim, groups, 0, 1.0, 0, 0, 0), 1 if backward else 0))
 
@@ -498,33 +544,34 @@ def gs_linear_attn_fwd(q, k, v, log_decay, out, group_offsets=None, state=None, 
     [q_heads], 0 or less.  Groups of tokens (group_offsets int32 [groups + 1]; None: one)
     each go from their state to state_out, float32 [groups, q_heads, dim, vdim] (None: zeros;
     not wanted).  workspace: uint8, gs_linear_attn_workspace_bytes() bytes."""
-    a, qh, kh, vh, shape, states = _attn(q, k, v, log_decay, group_offsets, state, scale)
-    size = 0 if workspace is None else workspace.numel()
-    _on_one_device(q, log_decay, group_offsets, state, state_out, workspace)
-    _check("gs_linear_attn_fwd", lib().gs_linear_attn_fwd(
-        a, qh, kh, vh, _attn_heads(out, "out", shape, q), _states(state_out, "state_out", states),
-        _vec(workspace, "workspace", size, torch.uint8), size, _stream(stream, q)))
+    a, qh, kh, vh, shape, states, device = _attn(q, k, v, log_decay, group_offsets, state, scale)
+    status = lib().gs_linear_attn_fwd(
+        a, qh, kh, vh, _attn_heads(out, "out", shape, q.dtype, device),
+        0 if state_out is None else _entries(state_out, "state_out", states, torch.float32, device),
+        *_workspace(workspace, device), _stream(stream, q))
+    if status:
+        _check("gs_linear_attn_fwd", status)
 
 
 def gs_linear_attn_bwd(q, k, v, log_decay, dout, dq, dk, dv, group_offsets=None, state=None, dstate_out=None,
                        dstate=None, scale=None, workspace=None, stream=None):
     """Backward of gs_linear_attn_fwd from its inputs, dout and (None: zeros) the gradient of
     its last states: dq, dk, dv and, where given, dstate, the gradient of the first states."""
-    a, qh, kh, vh, shape, states = _attn(q, k, v, log_decay, group_offsets, state, scale)
-    size = 0 if workspace is None else workspace.numel()
-    _on_one_device(q, log_decay, group_offsets, state, dstate_out, dstate, workspace)
+    a, qh, kh, vh, shape, states, device = _attn(q, k, v, log_decay, group_offsets, state, scale)
+    dt, f32 = q.dtype, torch.float32
     _check("gs_linear_attn_bwd", lib().gs_linear_attn_bwd(
-        a, qh, kh, vh, _attn_heads(dout, "dout", shape, q), _attn_heads(dq, "dq", q.shape, q),
-        _attn_heads(dk, "dk", k.shape, q), _attn_heads(dv, "dv", v.shape, q),
-        _states(dstate_out, "dstate_out", states), _states(dstate, "dstate", states),
-        _vec(workspace, "workspace", size, torch.uint8), size, _stream(stream, q)))
+        a, qh, kh, vh, _attn_heads(dout, "dout", shape, dt, device), _attn_heads(dq, "dq", q.shape, dt, device),
+        _attn_heads(dk, "dk", k.shape, dt, device), _attn_heads(dv, "dv", v.shape, dt, device),
+        _entries(dstate_out, "dstate_out", states, f32, device), _entries(dstate, "dstate", states, f32, device),
+        *_workspace(workspace, device), _stream(stream, q)))
 
 
 def gs_linear_attn_step(q, k, v, log_decay, state, out, scale=None, stream=None):
     """One token of each of q.shape[0] streams: updates state, float32 [streams, q_heads, dim,
     vdim], in place and writes out [streams, q_heads, vdim]."""
-    a, qh, kh, vh, shape, _ = _attn(q, k, v, log_decay, None, None, scale)
-    states = (shape[0], shape[1], q.shape[2], shape[2])
-    _on_one_device(q, log_decay, state)
-    _check("gs_linear_attn_step", lib().gs_linear_attn_step(
-        a, qh, kh, vh, _attn_heads(out, "out", shape, q), _states(state, "state", states), _stream(stream, q)))
+    a, qh, kh, vh, shape, states, device = _attn(q, k, v, log_decay, None, None, scale)
+    status = lib().gs_linear_attn_step(
+        a, qh, kh, vh, _attn_heads(out, "out", shape, q.dtype, device),
+        _entries(state, "state", (shape[0],) + states[1:], torch.float32, device), _stream(stream, q))
+    if status:
+        _check("gs_linear_attn_step", status)

@@ -99,6 +99,12 @@ SHAPES = [  # tokens, channels, hidden, padding of the rows, offset of the first
     (257, 130, 257, 0, 3),
     (600, 520, 300, 64, 0),
     (1000, 64, 2000, 0, 0),
+    (8, 1000, 100, 0, 0),      # few tokens, on either side of the steps between their forms
+    (9, 1031, 24, 0, 0),
+    (31, 2056, 16, 0, 2),
+    (32, 520, 40, 8, 0),
+    (33, 520, 40, 8, 0),
+    (300, 300, 3001, 0, 0),    # dx's sums split over several pairs
 ]
 
 
