@@ -649,4 +649,5 @@ from .net import (Rope, act8_empty, act8_shapes, gs_act8_decode, gs_act8_encode,
                   gs_act8_wgrad, gs_act8_wgrad_workspace_bytes, gs_ffn_bwd, gs_ffn_fwd,
                   gs_ffn_workspace_bytes, gs_gated_norm_bwd, gs_gated_norm_fwd,
                   gs_gated_norm_workspace_bytes, gs_glu_bwd, gs_glu_fwd, gs_linear_attn_bwd,
-                  gs_linear_attn_fwd, gs_linear_attn_step, gs_linear_attn_workspace_bytes, gs_rope)
+                  gs_linear_attn_fwd, gs_linear_attn_status, gs_linear_attn_step,
+                  gs_linear_attn_workspace_bytes, gs_rope)

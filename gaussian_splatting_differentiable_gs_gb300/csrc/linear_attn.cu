@@ -3,7 +3,7 @@
 //
 //   S_t = d S_{t-1} + k_t v_t^T,  o_t = scale q_t S_t,  d = e^log_decay
 //
-// In chunks of 64 tokens (n of them, i and j counted from a chunk's start, S its state
+// In chunks of 128 tokens (n of them, i and j counted from a chunk's start, S its state
 // at the start):
 //   o_i = scale (d^(i+1) q_i S + sum_{j <= i} d^(i-j) (q_i k_j) v_j)
 //   S'  = d^n S + sum_j d^(n-1-j) k_j v_j^T
@@ -22,29 +22,28 @@
 // and a group's last state, a third one forms the outputs, segment by segment, with the
 // state in registers (fp32) between a segment's chunks.
 //
-// Products are on the tensor cores (mma.sync: chains of products of 16 x 64 results per
-// warp whose operands come from one another's registers), sums and states fp32.  What is
+// Products are on the tensor cores (tcgen05, 128 rows), sums and states fp32.  What is
 // rounded to the inputs' type on the way: the decayed products q_i k_j, and the state
 // where it is multiplied by a query (not where it is kept); each of the two parts of an
 // output is rounded once there and once more as the output.  The decayed keys of a
 // state's sum are taken as 3 (bf16) or 2 (fp16) terms, exact to fp32's rounding, for the
-// states that are handed on, and as 2 terms for those inside a segment.
+// states that are handed on, and as 2 terms for the others.
 #include <atomic>
 #include <type_traits>
 
 #include "activation.cuh"
+#include "tensor_core.cuh"
 
 namespace gs {
 namespace {
 
-constexpr int kL = 64;  // tokens of a chunk
-constexpr int kTilesOfRows = kL / 16;
-constexpr int kV = 64;  // values' channels of a block: wider heads take two blocks
-// The keys' channels, padded to KD = 64 or 128, set the warps: each has 16 rows of the state.
-template <int KD>
-constexpr int kWarps = KD / 16;
-template <int KD>
-constexpr int kThreads = 32 * kWarps<KD>;
+constexpr int kL = 128;  // tokens of a chunk: the rows of a product
+constexpr int kV = 64;   // values' channels of a block: wider heads take two blocks
+constexpr int kThreads = 256;
+constexpr int kBlock = kL * 128;  // bytes of 64 channels of a chunk
+constexpr unsigned int kErrTimeout = 1u;
+constexpr int64_t kWaitNs = 2000000000;
+// The keys' channels are padded to KD = 64 or 128.
 
 struct Side {  // heads that are read or written
   void* p;
@@ -85,319 +84,330 @@ __device__ __forceinline__ Span span_of(const Split& s, int64_t slot) {
   return Span{lo, start, in < 0 || left <= 0 ? 0 : (int)(left < s.seg ? left : s.seg)};
 }
 
-// ---- mma.sync and its operands ---------------------------------------------
-__device__ __forceinline__ uint32_t smem_at(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+// Set where a wait for the tensor core ran out (gs_linear_attn_status).
+__device__ unsigned int attn_timeouts;
+
+// ---- tcgen05 on one SM ------------------------------------------------------------
+// Descriptors of operands in 128-byte swizzled rows (64 channels of a token, the granules
+// of 16 bytes exchanged by the token's last three bits).  K-major: the channels are the
+// sum's terms, 16 on are 32 bytes.  MN-major: the tokens are the sum's terms, 16 on are
+// 2048 bytes; the next 64 channels follow a block later.
+template <bool MN>
+__device__ __forceinline__ uint64_t operand(uint32_t addr) {
+  constexpr uint64_t kLead = MN ? (uint64_t)(kBlock >> 4) : 1, kAtom = (uint64_t)(1024 >> 4);
+  return (uint64_t)((addr & 0x3ffff) >> 4) | (kLead << 16) | (kAtom << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
 template <typename T>
-__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if constexpr (std::is_same<T, __half>::value)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+__device__ __forceinline__ constexpr uint32_t instruction(int m, int n, bool a_mn, bool b_mn) {
+  const uint32_t type = std::is_same<T, __half>::value ? 0u : 1u;
+  return (1u << 4) | (type << 7) | (type << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
-__device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+      "r"((uint32_t)add)
+      : "memory");
 }
-__device__ __forceinline__ void ldm4t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
+// The first operand in TMEM: a row a lane, two terms a column.
+__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+      "r"((uint32_t)add)
+      : "memory");
 }
-// Tiles in shared memory: rows of W 16-bit elements, whose 16-byte granules are swizzled by
-// the row's last three bits: granule i of row r is at place i ^ (r % 8).  Tiles begin on
-// 256-byte boundaries, so that 16 elements on are an exclusive or with 32.
-//
-// The lane's row address for the four 8 x 8 matrices of a 16 x 16 block at column 0 of the
-// rows from r0 on (a multiple of 8): rows first (r0, r0 + 8 at column 0, then at 8) ...
-template <int W>
-__device__ __forceinline__ uint32_t rows_first(uint32_t tile, int r0, int lane) {
-  return tile + (r0 + (lane & 15)) * (W * 2) + (((lane >> 4) ^ (lane & 7)) << 4);
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-// ... or columns first.
-template <int W>
-__device__ __forceinline__ uint32_t cols_first(uint32_t tile, int r0, int lane) {
-  return tile + (r0 + (lane & 7) + (lane >> 4) * 8) * (W * 2) + (((lane >> 3 & 1) ^ (lane & 7)) << 4);
+__device__ __forceinline__ void before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// What this thread wrote to shared memory is there for the tensor core (after a barrier).
+__device__ __forceinline__ void publish() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+struct Control {
+  uint64_t done[2];
+  uint32_t tmem;
+  volatile uint32_t abort;
+  float top[2][kThreads / 32];
+  alignas(16) float decay[64];  // mul d^(31 - i), then zeros
+};
+static_assert(sizeof(Control) <= 1024, "control");
+// Waits for products; at most two seconds in all, after which nothing is waited for any
+// more, the results are undefined and the error is on record.
+__device__ __forceinline__ void wait_done(Control* c, int which, uint32_t parity) {
+  const uint32_t bar = smem_u32(&c->done[which]);
+  const int64_t t0 = now_ns();
+  while (!mbar_try(bar, parity) && !c->abort)
+    if (now_ns() - t0 > kWaitNs) {
+      c->abort = 1;
+      atomicOr(&attn_timeouts, kErrTimeout);
+    }
+  __syncwarp();  // the warp's accesses to TMEM are in step
+}
+template <int COLUMNS>
+__device__ __forceinline__ uint32_t begin(Control* c) {
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&c->done[0]), 1);
+    mbar_init(smem_u32(&c->done[1]), 1);
+    c->abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (threadIdx.x >> 5 == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&c->tmem)),
+                 "n"(COLUMNS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  before_sync();
+  __syncthreads();
+  after_sync();
+  return c->tmem;
+}
+template <int COLUMNS>
+__device__ __forceinline__ void end(uint32_t tmem) {
+  before_sync();
+  __syncthreads();
+  after_sync();
+  if (threadIdx.x >> 5 == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(COLUMNS));
 }
 
-// A chunk's tile.  A chunk of n < kL tokens has them in its last n rows and zeros before
-// them, so that a row's distance to the chunk's end is the same in every chunk.  Columns
-// from dim on (a multiple of 8) are zeros.
-template <typename T, int W, int THREADS>
-__device__ __forceinline__ void load_tile(T* tile, const T* from, int64_t stride, int n, int dim) {
-  constexpr int kG = W / 8, kRows = THREADS / kG;
-  const int r0 = threadIdx.x / kG, c = threadIdx.x % kG, pad = kL - n;
-  uint32_t to = smem_at(tile) + r0 * (W * 2) + ((c ^ (r0 & 7)) << 4);
-  const T* p = from + (r0 - pad) * stride + c * 8;
-  const bool in = c * 8 < dim;
+// 32 columns of the thread's lane; the values are there after loaded().
+__device__ __forceinline__ void load32(uint32_t addr, float (&f)[32]) {
+  uint32_t(&v)[32] = reinterpret_cast<uint32_t(&)[32]>(f);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+        "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(addr)
+      : "memory");
+}
+// 16 lanes x 32 columns: thread t has columns 8 i + 2 (t % 4) and the next of lane t / 4
+// in f[4 i], f[4 i + 1], and of lane t / 4 + 8 in the two after.
+__device__ __forceinline__ void load16x32(uint32_t addr, float (&f)[16]) {
+  uint32_t(&v)[16] = reinterpret_cast<uint32_t(&)[16]>(f);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(addr)
+      : "memory");
+}
+// Ties loaded values to the wait, so that no use of them moves before it.
+template <int N>
+__device__ __forceinline__ void loaded(float (&f)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < kL / kRows; ++i) {
-    const bool there = in && r0 + i * kRows >= pad;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + i * kRows * W * 2),
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(f[i]));
+}
+// 32 terms (16 words) of the thread's row.
+__device__ __forceinline__ void store16(uint32_t addr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+// ---- tiles ------------------------------------------------------------------------
+// A chunk's tile of W = 64 or 128 channels, in blocks of 64.  A chunk of n < kL tokens has
+// them in its last n rows and zeros before them, so that a row's distance to the chunk's
+// end is the same in every chunk.  Columns from dim on (a multiple of 8) are zeros.  A
+// thread brings one granule of every kRows-th row.
+template <int W>
+struct Rows {
+  static constexpr int kG = W / 8, kRows = kThreads / kG, kCount = kL / kRows;
+  int r0, c;
+  uint32_t at;  // of the thread's first granule; the next ones are kRows * 128 bytes on
+  __device__ __forceinline__ Rows()
+      : r0(threadIdx.x / kG), c(threadIdx.x % kG), at(c / 8 * kBlock + r0 * 128 + (((c & 7) ^ (r0 & 7)) << 4)) {}
+};
+template <typename T, int W>
+__device__ __forceinline__ void load_tile(uint32_t tile, const T* from, int64_t stride, int n, int dim) {
+  const Rows<W> k;
+  const int pad = kL - n;
+  const T* p = from + (k.r0 - pad) * stride + k.c * 8;
+  const bool in = k.c * 8 < dim;
+  const int64_t next = k.kRows * stride;
+#pragma unroll
+  for (int i = 0; i < k.kCount; ++i) {
+    const bool there = in && k.r0 + i * k.kRows >= pad;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tile + k.at + i * k.kRows * 128),
                  "l"(there ? p : from), "r"(there ? 16 : 0)
                  : "memory");
-    p += kRows * stride;
+    p += next;
   }
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+__device__ __forceinline__ uint4 get_granule(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void put_granule(uint32_t at, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
 
 // log2 of a head's decay; one that leaves nothing after a token counts as 2^-1000.
 __device__ __forceinline__ float log2_decay(const float* log_decay, int h) {
   const float a = log_decay[h] * 1.4426950408889634f;
   return a < -1000.f ? -1000.f : a;
 }
-
 template <typename T>
 __device__ __forceinline__ float2 unpack(uint32_t w) {
   const Pack<T, 2> e = *reinterpret_cast<const Pack<T, 2>*>(&w);
   return make_float2(to_f32(e.v[0]), to_f32(e.v[1]));
 }
-
-// What a thread needs of a decay's powers: the weights of the keys in a chunk's last 16
-// rows (tokens 2t, 2t + 1, 2t + 8, 2t + 9), mul d^(15 - token + shift).
-struct Weights {
-  float w[4];
-  float top;  // the largest
-  __device__ __forceinline__ Weights(float a, int t, int shift, float mul) : top(mul * power2(a * (float)shift)) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      w[j] = mul * power2(a * (float)(15 - 2 * t - (j & 1) - (j >> 1) * 8 + shift));
-  }
-};
-
-// 16 rows of the state past a chunk: st <- decay st + sum_j weight_j key_j value_j^T, the
-// weighted keys as TERMS terms.  keys: columns first at the warp's 16 of the keys' channels;
-// values: rows first.  In fp16 keys and state take a power of two meanwhile, so that the
-// largest key with the largest weight is near 2^13: the terms of small ones would be below
-// fp16's range.
-template <typename T, int KD, int TERMS>
-__device__ __forceinline__ void add_tokens(float (&st)[kV / 8][4], float decay, uint32_t keys, uint32_t values,
-                                           const Weights& weights, float d16) {
-  float w[4] = {weights.w[0], weights.w[1], weights.w[2], weights.w[3]};
-  float back = 1.f;
-  if constexpr (std::is_same<T, __half>::value) {
-    uint32_t top = 0;  // magnitudes compare as whole numbers
-#pragma unroll
-    for (int ks = 0; ks < kL / 16; ++ks) {
-      uint32_t raw[4];
-      ldm4t(raw, keys + ks * 16 * KD * 2);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) top = max(top, max(raw[r] & 0x7fffu, raw[r] >> 16 & 0x7fffu));
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float m = __half2float(__ushort_as_half((unsigned short)top)) * fabsf(weights.top);
-    const int e = m > 0.f ? min(max((int)(__float_as_uint(m) >> 23) - 127 - 13, -100), 100) : 0;
-    back = __uint_as_float((uint32_t)(127 + e) << 23);
-    const float fit = __uint_as_float((uint32_t)(127 - e) << 23);
-    decay *= fit;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] *= fit;
-  }
-#pragma unroll
-  for (int i = 0; i < kV / 8; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) st[i][j] *= decay;
-#pragma unroll
-  for (int ks = kL / 16 - 1; ks >= 0; --ks) {
-    uint32_t raw[4];
-    // (row g, tokens 2t..), (g + 8, 2t..), (g, 2t + 8..), (g + 8, 2t + 8..)
-    ldm4t(raw, keys + ks * 16 * KD * 2);
-    uint32_t term[TERMS][4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      float2 x = mul2(unpack<T>(raw[r]), r < 2 ? make_float2(w[0], w[1]) : make_float2(w[2], w[3]));
-#pragma unroll
-      for (int i = 0; i < TERMS; ++i) {
-        term[i][r] = pair_word<T>(x.x, x.y);
-        if (i + 1 < TERMS) x = fma2(unpack<T>(term[i][r]), both(-1.f), x);
-      }
-    }
-#pragma unroll
-    for (int c = 0; c < kV; c += 16) {
-      uint32_t b[4];
-      ldm4t(b, (values ^ (c * 2)) + ks * 16 * kV * 2);
-#pragma unroll
-      for (int i = 0; i < TERMS; ++i) {
-        mma16<T>(st[c / 8], term[i], b[0], b[1]);
-        mma16<T>(st[c / 8 + 1], term[i], b[2], b[3]);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] *= d16;
-  }
-  if constexpr (std::is_same<T, __half>::value) {
-#pragma unroll
-    for (int i = 0; i < kV / 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) st[i][j] *= back;
-  }
-}
-
-// Powers between rows g, g + 8 and columns 2t, 2t + 1 of a 16 x 16 block, times mul.
-struct Powers {
-  float b0, b1;  // d^(g - 2t + 8), d^(g - 2t + 7)
-  float d0, d1;  // d^(g - 2t), d^(g - 2t - 1) on the diagonal
-  float d8, d16;
-  bool in0, in1;
-  __device__ __forceinline__ Powers(float a, int g, int t, float mul) {
-    b0 = mul * power2(a * (float)(g - 2 * t + 8));
-    b1 = mul * power2(a * (float)(g - 2 * t + 7));
-    in0 = g >= 2 * t;
-    in1 = g >= 2 * t + 1;
-    d0 = mul * power2(a * (float)max(g - 2 * t, 0));
-    d1 = mul * power2(a * (float)max(g - 2 * t - 1, 0));
-    d8 = power2(a * 8.f);
-    d16 = power2(a * 16.f);
-  }
-};
-
-// o += (queries times keys, decayed, up to the diagonal) times values, for the 16 rows rt.
-// keys: columns first; values: rows first, at the warp's columns.
-template <typename T, int KD, int WIDTH>
-__device__ __forceinline__ void add_inner(float (&o)[WIDTH / 8][4], const uint32_t (&qf)[KD / 16][4], uint32_t keys,
-                                          uint32_t values, int rt, const Powers& p) {
-  float far = 1.f;  // d^(16 (rt - jb - 1))
-#pragma unroll 1
-  for (int jb = rt; jb >= 0; --jb) {
-    float w[2][4] = {};
-    const uint32_t k = keys + jb * (16 * KD * 2), v = values + jb * (16 * kV * 2);
-#pragma unroll
-    for (int i = 0; i < KD / 16; ++i) {
-      uint32_t b[4];
-      ldm4(b, k ^ (i * 32));
-      mma16<T>(w[0], qf[i], b[0], b[1]);
-      mma16<T>(w[1], qf[i], b[2], b[3]);
-    }
-    uint32_t pf[4];
-    if (jb == rt) {
-      pf[0] = pair_word<T>(p.in0 ? w[0][0] * p.d0 : 0.f, p.in1 ? w[0][1] * p.d1 : 0.f);
-      pf[1] = pair_word<T>(w[0][2] * p.b0, w[0][3] * p.b1);
-      pf[2] = 0;
-      pf[3] = pair_word<T>(p.in0 ? w[1][2] * p.d0 : 0.f, p.in1 ? w[1][3] * p.d1 : 0.f);
-    } else {
-      const float c0 = p.b0 * far, c1 = p.b1 * far, e0 = c0 * p.d8, e1 = c1 * p.d8;
-      pf[0] = pair_word<T>(w[0][0] * e0, w[0][1] * e1);
-      pf[1] = pair_word<T>(w[0][2] * (e0 * p.d8), w[0][3] * (e1 * p.d8));
-      pf[2] = pair_word<T>(w[1][0] * c0, w[1][1] * c1);
-      pf[3] = pair_word<T>(w[1][2] * e0, w[1][3] * e1);
-      far *= p.d16;
-    }
-#pragma unroll
-    for (int x = 0; x < WIDTH; x += 16) {
-      uint32_t b[4];
-      ldm4t(b, v ^ (x * 2));
-      mma16<T>(o[x / 8], pf, b[0], b[1]);
-      mma16<T>(o[x / 8 + 1], pf, b[2], b[3]);
-    }
-  }
-}
-
-// The state as the products take it.  rescale: a power of two.
-template <typename T>
-__device__ __forceinline__ void put_state(uint32_t tile, const float (&st)[kV / 8][4], int warp, int g, int t,
-                                          float rescale) {
-  const uint32_t row = tile + (warp * 16 + g) * (kV * 2) + t * 4;
-#pragma unroll
-  for (int i = 0; i < kV / 8; ++i) {
-    const uint32_t to = row + ((i ^ g) << 4);
-    asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(pair_word<T>(st[i][0] * rescale, st[i][1] * rescale)) : "memory");
-    asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + 8 * kV * 2),
-                 "r"(pair_word<T>(st[i][2] * rescale, st[i][3] * rescale))
-                 : "memory");
-  }
-}
-// fp16: the power of two that brings the block's largest entry of the state near 2^13, as
-// an exponent.  top: room for a number a warp, which nobody uses until the next barrier.
-__device__ __forceinline__ int state_exponent(const float (&st)[kV / 8][4], float* top, int warps, int warp, int lane) {
-  float m = 0.f;
-#pragma unroll
-  for (int i = 0; i < kV / 8; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) m = fmaxf(m, fabsf(st[i][j]));
-#pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) top[warp] = m;
-  __syncthreads();
-  for (int i = 0; i < warps; ++i) m = fmaxf(m, top[i]);
-  return min(max((int)(__float_as_uint(m) >> 23) - 127 - 13, -100), 100);
-}
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+// The exponent that brings m near 2^13 when it is taken away.
+__device__ __forceinline__ int exponent_of(float m) {
+  return m > 0.f ? min(max((int)(__float_as_uint(m) >> 23) - 127 - 13, -100), 100) : 0;
+}
 
-// 16 rows of the state from memory: entry (row, col) at src[row * rs + col * cs].
-__device__ __forceinline__ void get_state(float (&st)[kV / 8][4], const float* src, int64_t rs, int64_t cs, int row0,
-                                          int col0, int rows, int cols, int g, int t) {
+// The tile's keys, weighted by d^(127 - row + shift) mul, as TERMS terms of T in as many
+// tiles of the same layout one after the other.  Each thread takes the granules that it
+// brought itself.
+template <typename T, int KD, int TERMS>
+__device__ __forceinline__ void weigh(uint32_t keys, uint32_t terms, float a, int shift, float mul) {
+  const Rows<KD> k;
+  constexpr uint32_t kTermBytes = KD / 64 * kBlock;
+  float w = mul * power2(a * (float)(kL - 1 - (k.r0 + (k.kCount - 1) * k.kRows) + shift));
+  const float next = power2(a * (float)k.kRows);
 #pragma unroll
-  for (int i = 0; i < kV / 8; ++i)
+  for (int i = k.kCount - 1; i >= 0; --i) {
+    const uint32_t at = k.at + i * k.kRows * 128;
+    const uint4 raw = get_granule(keys + at);
+    const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
+    uint32_t out[TERMS][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int row = row0 + g + (j >> 1) * 8, col = col0 + i * 8 + 2 * t + (j & 1);
-      st[i][j] = src && row < rows && col < cols ? src[row * rs + col * cs] : 0.f;
+      float2 x = mul2(unpack<T>(in[j]), both(w));
+#pragma unroll
+      for (int t = 0; t < TERMS; ++t) {
+        out[t][j] = pair_word<T>(x.x, x.y);
+        if (t + 1 < TERMS) x = fma2(unpack<T>(out[t][j]), both(-1.f), x);
+      }
     }
+#pragma unroll
+    for (int t = 0; t < TERMS; ++t)
+      put_granule(terms + t * kTermBytes + at, make_uint4(out[t][0], out[t][1], out[t][2], out[t][3]));
+    w *= next;
+  }
+}
+// fp16: the largest magnitude among the thread's own granules of the keys, in the warp.
+template <int KD>
+__device__ __forceinline__ float top_key(uint32_t keys) {
+  const Rows<KD> k;
+  uint32_t top = 0;  // magnitudes compare as whole numbers
+#pragma unroll
+  for (int i = 0; i < k.kCount; ++i) {
+    const uint4 v = get_granule(keys + k.at + i * k.kRows * 128);
+    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top = max(top, max(in[j] & 0x7fffu, in[j] >> 16 & 0x7fffu));
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  return __half2float(__ushort_as_half((unsigned short)top));
 }
 
-// The warp's 16 rows of outputs through its own rows of a tile (of W columns, whose
-// contents it alone uses and needs no more) to memory; the rows from `pad` on are there.
-template <typename T, int W, int WIDTH>
-__device__ __forceinline__ void put_rows(uint32_t tile, const float (&o)[WIDTH / 8][4], int rt, int col0, T* to,
-                                         int64_t stride, int pad, int dim, bool wide, int lane) {
-  const int g = lane >> 2, t = lane & 3;
-  const uint32_t row = tile + (rt * 16 + g) * (W * 2) + t * 4;
-  __syncwarp();
-#pragma unroll
-  for (int i = 0; i < WIDTH / 8; ++i) {
-    const uint32_t at = row + (((col0 / 8 + i) ^ g) << 4);
-    asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(pair_word<T>(o[i][0], o[i][1])) : "memory");
-    asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 8 * W * 2), "r"(pair_word<T>(o[i][2], o[i][3])) : "memory");
+// ---- the state: [KD][64] in the products' layout, half of the columns a half of the warps.
+// KD = 64: a warp has 16 rows; 128: twice 16.
+template <int KD>
+struct State {
+  static constexpr int kM = KD / 64;
+  float v[kM][16];
+  int row0, col0, g, t;
+  uint32_t lanes;
+  __device__ __forceinline__ State() {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    row0 = (warp & 3) * (KD / 4);
+    col0 = (warp >> 2) * 32;
+    g = lane >> 2, t = lane & 3;
+    lanes = (uint32_t)((warp & 3) * 32) << 16;
   }
-  __syncwarp();
-  constexpr int kG = WIDTH / 8, kRows = 32 / kG;
-  const int r0 = rt * 16 + lane / kG, c = col0 / 8 + lane % kG;
+  __device__ __forceinline__ int row(int m, int j) const { return row0 + m * 16 + g + (j >> 1 & 1) * 8; }
+  __device__ __forceinline__ int col(int j) const { return col0 + (j >> 2) * 8 + 2 * t + (j & 1); }
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-  for (int i = 0; i < 16 / kRows; ++i) {
-    const int r = r0 + i * kRows;
-    if (r < pad || c * 8 >= dim) continue;
-    uint32_t w[4];
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "r"(tile + r * (W * 2) + ((c ^ (r & 7)) << 4))
-                 : "memory");
-    T* x = to + (r - pad) * stride + c * 8;
-    if (wide) {
-      *reinterpret_cast<uint4*>(x) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
+    for (int m = 0; m < kM; ++m)
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (c * 8 + j < dim) reinterpret_cast<uint16_t*>(x)[j] = (uint16_t)(w[j / 2] >> (j % 2 * 16));
-    }
+      for (int j = 0; j < 16; ++j) v[m][j] = 0.f;
   }
-}
-// fp32 sums over a key head's query heads, one head after the other: o += what the heads
-// before left, and unless this is the last one, o stays there.
-template <int WIDTH>
-__device__ __forceinline__ void sum_heads(float (&o)[WIDTH / 8][4], float* to, int64_t stride, int rt, int pad, int g,
-                                          int t, bool first, bool last) {
+  // Entry (row, e0 + col) from src[row * rs + (e0 + col) * cs].
+  __device__ __forceinline__ void get(const float* src, int64_t rs, int64_t cs, int e0, int rows, int cols) {
 #pragma unroll
-  for (int i = 0; i < WIDTH / 8; ++i)
+    for (int m = 0; m < kM; ++m)
 #pragma unroll
-    for (int j = 0; j < 4; j += 2) {
-      const int r = rt * 16 + g + (j >> 1) * 8;
-      if (r < pad) continue;
-      float2* x = reinterpret_cast<float2*>(to + (r - pad) * stride + i * 8 + 2 * t);
-      if (!first) {
-        const float2 y = *x;
-        o[i][j] += y.x, o[i][j + 1] += y.y;
+      for (int j = 0; j < 16; ++j) {
+        const int r = row(m, j), c = e0 + col(j);
+        v[m][j] = src && r < rows && c < cols ? src[r * rs + c * cs] : 0.f;
       }
-      if (!last) *x = make_float2(o[i][j], o[i][j + 1]);
+  }
+  __device__ __forceinline__ void put(float* to, int64_t stride) const {
+#pragma unroll
+    for (int m = 0; m < kM; ++m)
+#pragma unroll
+      for (int j = 0; j < 16; j += 2)
+        *reinterpret_cast<float2*>(to + row(m, j) * stride + col(j)) = make_float2(v[m][j], v[m][j + 1]);
+  }
+  __device__ __forceinline__ float top() const {
+    float x = 0.f;
+#pragma unroll
+    for (int m = 0; m < kM; ++m)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) x = fmaxf(x, fabsf(v[m][j]));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+  }
+  // As the products take it: rows of 64 T.
+  template <typename T>
+  __device__ __forceinline__ void to_tile(uint32_t tile, float scale) const {
+#pragma unroll
+    for (int m = 0; m < kM; ++m) {
+      const uint32_t at = tile + (row0 + m * 16 + g) * 128 + ((col0 / 8 ^ g) << 4) + t * 4;
+#pragma unroll
+      for (int j = 0; j < 16; j += 2)
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"((at ^ (j >> 2 << 4)) + (j >> 1 & 1) * 1024),
+                     "r"(pair_word<T>(v[m][j] * scale, v[m][j + 1] * scale))
+                     : "memory");
     }
+  }
+  // v <- decay v + back (what the tensor core summed at `sum`)
+  __device__ __forceinline__ void update(uint32_t sum, float decay, float back) {
+    float u[kM][16];
+#pragma unroll
+    for (int m = 0; m < kM; ++m) load16x32(sum + lanes + ((uint32_t)(m * 16) << 16) + col0, u[m]);
+#pragma unroll
+    for (int m = 0; m < kM; ++m) {
+      loaded(u[m]);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[m][j] = v[m][j] * decay + u[m][j] * back;
+    }
+  }
+};
+// terms^T values: the products of a state's update, by one thread.
+template <typename T, int KD, int TERMS>
+__device__ __forceinline__ void mma_state(uint32_t d, uint32_t terms, uint32_t values) {
+  const uint32_t idesc = instruction<T>(KD, kV, true, true);
+  const uint64_t b = operand<true>(values);
+#pragma unroll
+  for (int t = 0; t < TERMS; ++t) {
+    const uint64_t a = operand<true>(terms + t * (KD / 64 * kBlock));
+#pragma unroll
+    for (int i = 0; i < kL / 16; ++i) mma(d, a + i * (2048 >> 4), b + i * (2048 >> 4), idesc, t > 0 || i > 0);
+  }
 }
 
 template <typename T>
@@ -410,7 +420,6 @@ struct Part {
   Side key, value;
   float mul;
   int32_t back, shift;  // tokens from the last to the first
-  int32_t exact;        // its last states are handed on
   float* to;            // [slots][heads][Dp][Ep]
 };
 struct PartsArgs {
@@ -418,59 +427,73 @@ struct PartsArgs {
   int32_t heads, rep;
   int32_t Dp, Ep;  // channels, rounded up to 64
   const float* log_decay;
-  Part part[2];
+  Part part;
 };
 
-template <typename T, int KD>
-__global__ void __launch_bounds__(kThreads<KD>, 256 / KD) attn_parts_kernel(const __grid_constant__ PartsArgs p) {
+template <int KD, int TERMS>
+constexpr int kPartsSmem = 2 * (KD / 64 + 1) * kBlock + TERMS * (KD / 64) * kBlock + 1024;
+
+template <typename T, int KD, int TERMS>
+__global__ void __launch_bounds__(kThreads, 128 / KD) attn_parts_kernel(const __grid_constant__ PartsArgs p) {
   extern __shared__ __align__(1024) uint8_t smem[];
+  constexpr bool kHalfType = std::is_same<T, __half>::value;
+  constexpr uint32_t kSet = (KD / 64 + 1) * kBlock;  // keys, values
+  const uint32_t tiles = smem_u32(smem), terms = tiles + 2 * kSet;
+  Control* c = (Control*)(smem + 2 * kSet + TERMS * (KD / 64) * kBlock);
+  const uint32_t tmem = begin<64>(c);
   launch_dependents();
   wait_for_previous();
-  constexpr int kSet = kL * (KD + kV);  // keys, values
-  T* tiles = (T*)smem;
-  const int h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int blocks = p.Ep / kV, e0 = blockIdx.z % blocks * kV;
-  const Part& part = p.part[blockIdx.z / blocks];
+  const int h = blockIdx.y, e0 = blockIdx.z * kV, warp = threadIdx.x >> 5;
+  const Part& part = p.part;
   const Span s = span_of(p.split, blockIdx.x);
-  if (s.n == 0) return;
   const float a = log2_decay(p.log_decay, h);
   const int64_t from = part.back ? s.start + s.n - 1 : s.start;
   const int64_t step = part.back ? -1 : 1;
   const T* k = head_at<T>(part.key, h, p.rep, from);
   const T* v = head_at<T>(part.value, h, p.rep, from) + e0;
-  auto load = [&](int c) {
-    T* to = tiles + (c & 1) * kSet;
-    const int n = min(kL, s.n - c * kL);
-    const int64_t at = step * c * kL;
-    load_tile<T, KD, kThreads<KD>>(to, k + at * part.key.token, step * part.key.token, n, part.key.dim);
-    load_tile<T, kV, kThreads<KD>>(to + kL * KD, v + at * part.value.token, step * part.value.token, n,
-                                   part.value.dim - e0);
+  auto load = [&](int i) {
+    const uint32_t to = tiles + (i & 1) * kSet;
+    const int n = min(kL, s.n - i * kL);
+    const int64_t at = step * i * kL;
+    load_tile<T, KD>(to, k + at * part.key.token, step * part.key.token, n, part.key.dim);
+    load_tile<T, kV>(to + KD / 64 * kBlock, v + at * part.value.token, step * part.value.token, n, part.value.dim - e0);
     copies_commit();
   };
-  float st[kV / 8][4] = {};
   const int chunks = (s.n + kL - 1) / kL;
-  const Weights weights(a, lane & 3, part.shift, part.mul);
-  const float d16 = power2(a * 16.f);
-  const uint32_t keys = cols_first<KD>(smem_at(tiles), 0, lane) ^ (warp * 32);
-  const uint32_t values = rows_first<kV>(smem_at(tiles) + kL * KD * 2, 0, lane);
-  load(0);
-  for (int c = 0; c < chunks; ++c) {
-    copies_wait<0>();
-    __syncthreads();
-    if (c + 1 < chunks) load(c + 1);
-    const uint32_t set = (c & 1) * kSet * 2;
-    const float decay = power2(a * (float)min(kL, s.n - c * kL));
-    if (std::is_same<T, __half>::value || !part.exact)
-      add_tokens<T, KD, 2>(st, decay, keys + set, values + set, weights, d16);
-    else
-      add_tokens<T, KD, 3>(st, decay, keys + set, values + set, weights, d16);
-  }
-  float* to = part.to + (((int64_t)blockIdx.x * p.heads + h) * p.Dp + warp * 16 + (lane >> 2)) * p.Ep + e0 + (lane & 3) * 2;
+  State<KD> st;
+  st.zero();
+  if (chunks) load(0);
+  for (int i = 0; i < chunks; ++i) {
+    const uint32_t set = tiles + (i & 1) * kSet;
+    copies_wait();
+    float mul = part.mul, back = 1.f;
+    if constexpr (kHalfType) {
+      const float m = top_key<KD>(set);
+      if ((threadIdx.x & 31) == 0) c->top[i & 1][warp] = m;
+      __syncthreads();
+      float x = 0.f;
 #pragma unroll
-  for (int i = 0; i < kV / 8; ++i) {
-    *reinterpret_cast<float2*>(to + i * 8) = make_float2(st[i][0], st[i][1]);
-    *reinterpret_cast<float2*>(to + 8 * p.Ep + i * 8) = make_float2(st[i][2], st[i][3]);
+      for (int w = 0; w < kThreads / 32; ++w) x = fmaxf(x, c->top[i & 1][w]);
+      const int e = exponent_of(x * fabsf(part.mul) * power2(a * (float)part.shift));
+      mul *= power_of_two(-e);
+      back = power_of_two(e);
+    }
+    weigh<T, KD, TERMS>(set, terms, a, part.shift, mul);
+    publish();
+    before_sync();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      after_sync();
+      mma_state<T, KD, TERMS>(tmem, terms, set + KD / 64 * kBlock);
+      commit(smem_u32(&c->done[0]));
+    }
+    if (i + 1 < chunks) load(i + 1);
+    wait_done(c, 0, i & 1);
+    after_sync();
+    st.update(tmem, power2(a * (float)min(kL, s.n - i * kL)), back);
   }
+  if (s.n) st.put(part.to + ((int64_t)blockIdx.x * p.heads + h) * p.Dp * p.Ep + e0, p.Ep);
+  end<64>(tmem);
 }
 
 // ---- the states at the segments' starts, in place of their parts ---------------
@@ -527,6 +550,174 @@ __global__ void __launch_bounds__(kScanThreads) attn_scan_kernel(const __grid_co
 }
 
 // ---- outputs -----------------------------------------------------------------
+// TMEM: the products of queries and keys; the decayed ones as the next product's operand;
+// their product with the values; in the first one's place then queries times the state,
+// and the state's update.
+constexpr uint32_t kScores = 0, kDecayed = 128, kInner = 192, kOuter = 0, kUpdate = 64;
+
+// Where a state is read from: a segment's, or without those the group's own.
+struct Stored {
+  const float* p;
+  int64_t rs, cs;  // between rows and columns as they are used
+};
+__device__ __forceinline__ Stored stored(const float* states, const float* edge, int Kp, int Vp, int kdim, int vdim,
+                                         int transposed, int64_t slot, int64_t group) {
+  const float* p = states ? states + slot * Kp * Vp : edge ? edge + group * kdim * vdim : nullptr;
+  const int ks = states ? Kp : kdim, vs = states ? Vp : vdim;
+  return transposed ? Stored{p, 1, ks} : Stored{p, vs, 1};
+}
+
+// scores = queries keys^T, by one thread.
+template <typename T, int KD>
+__device__ __forceinline__ void mma_scores(uint32_t tmem, uint32_t queries, uint32_t keys) {
+  const uint32_t idesc = instruction<T>(kL, kL, false, false);
+  const uint64_t a = operand<false>(queries), b = operand<false>(keys);
+#pragma unroll
+  for (int i = 0; i < KD / 16; ++i) {
+    const uint64_t at = (i / 4 * kBlock + i % 4 * 32) >> 4;
+    mma(tmem + kScores, a + at, b + at, idesc, i > 0);
+  }
+}
+// inner = decayed values, outer = queries state (TRANSPOSED: state^T, of 64 x 64).
+template <typename T, int KD, bool TRANSPOSED>
+__device__ __forceinline__ void mma_outputs(uint32_t tmem, uint32_t queries, uint32_t values, uint32_t state) {
+  const uint64_t v = operand<true>(values);
+  const uint32_t inner = instruction<T>(kL, kV, false, true);
+#pragma unroll
+  for (int i = 0; i < kL / 16; ++i) mma_tmem(tmem + kInner, tmem + kDecayed + 8 * i, v + i * (2048 >> 4), inner, i > 0);
+  const uint64_t q = operand<false>(queries), s = operand<!TRANSPOSED>(state);
+  const uint32_t outer = instruction<T>(kL, kV, false, !TRANSPOSED);
+#pragma unroll
+  for (int i = 0; i < KD / 16; ++i)
+    mma(tmem + kOuter, q + ((i / 4 * kBlock + i % 4 * 32) >> 4), s + i * (TRANSPOSED ? 32 >> 4 : 2048 >> 4), outer, i > 0);
+}
+
+// The scores' decay and mask: a thread has a row, and of its four blocks of 32 columns
+// every second one.  Row and column are l and x in their blocks: below the diagonal
+// d^(32 (row block - column block) + l - 31) d^(31 - x), on it d^(l - x) where x <= l.
+template <typename T>
+__device__ __forceinline__ void decay_scores(uint32_t tmem, const Control* c, float a) {
+  const int warp = threadIdx.x >> 5, l = threadIdx.x & 31, rb = warp & 3;
+  const uint32_t lanes = tmem + ((uint32_t)(rb * 32) << 16);
+#pragma unroll 1
+  for (int b = warp >> 2; b < 4; b += 2) {
+    uint32_t o[16];
+    if (b > rb) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) o[j] = 0;
+    } else {
+      float s[32];
+      load32(lanes + kScores + 32 * b, s);
+      if (b < rb) {
+        const float2 f = both(power2(a * (float)(32 * (rb - b) + l - 31)));
+        loaded(s);
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          const float4 d = *reinterpret_cast<const float4*>(c->decay + j);
+          const float2 x = mul2(mul2(make_float2(s[j], s[j + 1]), make_float2(d.x, d.y)), f);
+          const float2 y = mul2(mul2(make_float2(s[j + 2], s[j + 3]), make_float2(d.z, d.w)), f);
+          o[j / 2] = pair_word<T>(x.x, x.y);
+          o[j / 2 + 1] = pair_word<T>(y.x, y.y);
+        }
+      } else {
+        const float* d = c->decay + 31 - l;
+        loaded(s);
+#pragma unroll
+        for (int j = 0; j < 32; j += 2)
+          o[j / 2] = pair_word<T>(j <= l ? s[j] * d[j] : 0.f, j + 1 <= l ? s[j + 1] * d[j + 1] : 0.f);
+      }
+    }
+    store16(lanes + kDecayed + 16 * b, o);
+  }
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+struct Output {
+  void* p;              // of the chunk's first token and the block's first channel
+  int64_t stride;       // between the chunk's tokens
+  int32_t dim, wide;    // channels from there on; whole granules on 16-byte boundaries
+  float* sums;          // fp32 sums over a key head's query heads, or NULL
+  int64_t sum_stride;
+  bool first, last;     // of those heads
+};
+// inner + f outer, by way of `room` (a tile that nothing uses) to memory; the rows from pad
+// on are there.  A thread has a row's half; a warp stores its 32 rows' halves.
+template <typename T>
+__device__ __forceinline__ void put_outputs(uint32_t tmem, uint32_t room, float f, const Output& out, int pad) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = warp >> 2, row = (warp & 3) * 32 + lane;
+  const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * 32;
+  float x[32], y[32];
+  load32(lanes + kInner, x);
+  load32(lanes + kOuter, y);
+  loaded(x);
+  loaded(y);
+#pragma unroll
+  for (int j = 0; j < 32; j += 2) {
+    const float2 v = fma2(make_float2(y[j], y[j + 1]), both(f), make_float2(x[j], x[j + 1]));
+    x[j] = v.x, x[j + 1] = v.y;
+  }
+  if (out.sums) {
+    float4* to = reinterpret_cast<float4*>(out.sums + (row - pad) * out.sum_stride + half * 32);
+    if (row >= pad)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (!out.first) {
+          const float4 v = to[j];
+          x[4 * j] += v.x, x[4 * j + 1] += v.y, x[4 * j + 2] += v.z, x[4 * j + 3] += v.w;
+        }
+        if (!out.last) to[j] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+      }
+    if (!out.last) return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    put_granule(room + row * 128 + (((half * 4 + j) ^ (row & 7)) << 4),
+                make_uint4(pair_word<T>(x[8 * j], x[8 * j + 1]), pair_word<T>(x[8 * j + 2], x[8 * j + 3]),
+                           pair_word<T>(x[8 * j + 4], x[8 * j + 5]), pair_word<T>(x[8 * j + 6], x[8 * j + 7])));
+  __syncwarp();
+  const int g = half * 4 + (lane & 3);
+  if (g * 8 < out.dim) {
+    const int r0 = (warp & 3) * 32 + (lane >> 2);
+    T* to = (T*)out.p + (r0 - pad) * out.stride + g * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i, to += 8 * out.stride) {
+      const int r = r0 + i * 8;
+      if (r < pad) continue;
+      const uint4 v = get_granule(room + r * 128 + ((g ^ (r & 7)) << 4));
+      if (out.wide) {
+        *reinterpret_cast<uint4*>(to) = v;
+      } else {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (g * 8 + j < out.dim) reinterpret_cast<uint16_t*>(to)[j] = (uint16_t)(w[j / 2] >> (j % 2 * 16));
+      }
+    }
+  }
+  __syncwarp();
+}
+
+// fp16: powers of two that keep the state and the weighted keys in range, from the block's
+// largest ones; nothing for bf16.  Takes a barrier.
+struct Fit {
+  float state, state_back, key, key_back;
+};
+template <typename T, int KD>
+__device__ __forceinline__ Fit fit_of(Control* c, const State<KD>& st, uint32_t keys, float top_weight) {
+  Fit f{1.f, 1.f, 1.f, 1.f};
+  if constexpr (std::is_same<T, __half>::value) {
+    const float s = st.top(), k = top_key<KD>(keys);
+    if ((threadIdx.x & 31) == 0) c->top[0][threadIdx.x >> 5] = s, c->top[1][threadIdx.x >> 5] = k;
+    __syncthreads();
+    float x = 0.f, y = 0.f;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) x = fmaxf(x, c->top[0][w]), y = fmaxf(y, c->top[1][w]);
+    const int e = exponent_of(x), ke = exponent_of(y * fabsf(top_weight));
+    f = Fit{power_of_two(-e), power_of_two(e), power_of_two(-ke), power_of_two(ke)};
+  }
+  return f;
+}
+
 struct OutArgs {
   Split split;
   int32_t heads, rep;    // query heads
@@ -541,121 +732,99 @@ struct OutArgs {
   float mul_inner, mul_state, mul_key;
   float* sums;           // [tokens][key heads][Vp], where shared and rep > 1
 };
-
-// Where a state is read from: a segment's, or without those the group's own.
-struct Stored {
-  const float* p;
-  int64_t rs, cs;  // between rows and columns as they are used
-};
-__device__ __forceinline__ Stored stored(const float* states, const float* edge, int Kp, int Vp, int kdim, int vdim,
-                                         int transposed, int64_t slot, int64_t group) {
-  const float* p = states ? states + slot * Kp * Vp : edge ? edge + group * kdim * vdim : nullptr;
-  const int ks = states ? Kp : kdim, vs = states ? Vp : vdim;
-  return transposed ? Stored{p, 1, ks} : Stored{p, vs, 1};
-}
+template <int KD>
+constexpr int kOutSmem = (4 * (KD / 64) + 1) * kBlock + KD * 128 + 1024;
 
 template <typename T, int KD>
-__global__ void __launch_bounds__(kThreads<KD>, 256 / KD) attn_out_kernel(const __grid_constant__ OutArgs p) {
+__global__ void __launch_bounds__(kThreads, 128 / KD) attn_out_kernel(const __grid_constant__ OutArgs p) {
   extern __shared__ __align__(1024) uint8_t smem[];
+  constexpr uint32_t kKeys = KD / 64 * kBlock;
+  const uint32_t queries = smem_u32(smem), keys = queries + kKeys, values = keys + kKeys, terms = values + kBlock;
+  const uint32_t state = terms + 2 * kKeys;
+  Control* c = (Control*)(smem + 4 * kKeys + kBlock + KD * 128);
+  const uint32_t tmem = begin<256>(c);
   launch_dependents();
   wait_for_previous();
-  constexpr int kKeys = kL * KD, kValues = kL * kV, kSet = 2 * kKeys + kValues;
-  constexpr int kSplits = kWarps<KD> / kTilesOfRows;  // of the values' channels over warps
-  constexpr int kWidth = kV / kSplits;
-  T* tiles = (T*)smem;                          // [2] queries, keys, values
-  const uint32_t state = smem_at(tiles + 2 * kSet);  // [KD][kV]
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int rt = warp % kTilesOfRows, col0 = warp / kTilesOfRows * kWidth;
   const Span s = span_of(p.split, blockIdx.x);
-  if (s.n == 0) return;
   const int64_t from = p.back ? s.start + s.n - 1 : s.start, step = p.back ? -1 : 1;
-  const int chunks = (s.n + kL - 1) / kL, e0 = blockIdx.z * kV;
-  const int reps = p.shared ? p.rep : 1;
-  const uint32_t queries = rows_first<KD>(smem_at(tiles), rt * 16, lane);
-  const uint32_t keys = cols_first<KD>(smem_at(tiles) + kKeys * 2, 0, lane);
-  const uint32_t values = rows_first<kV>(smem_at(tiles) + 4 * kKeys, 0, lane);
-  const uint32_t state_rows = rows_first<kV>(state, 0, lane) ^ (col0 * 2);
+  const int chunks = (s.n + kL - 1) / kL, e0 = blockIdx.z * kV, reps = p.shared ? p.rep : 1;
+  const int row = ((int)threadIdx.x >> 5 & 3) * 32 + ((int)threadIdx.x & 31);
+  uint32_t phase = 0;
 
-  for (int r = 0; r < reps; ++r) {
+  for (int r = 0; r < (s.n ? reps : 0); ++r) {
     const int h = p.shared ? blockIdx.y * p.rep + r : blockIdx.y;
     const float a = log2_decay(p.log_decay, h);
     const T* q = head_at<T>(p.query, h, p.rep, from);
     const T* k = head_at<T>(p.key, h, p.rep, from);
     const T* v = head_at<T>(p.value, h, p.rep, from) + e0;
-    auto load = [&](int c) {
-      T* to = tiles + (c & 1) * kSet;
-      const int n = min(kL, s.n - c * kL);
-      const int64_t at = step * c * kL;
-      load_tile<T, KD, kThreads<KD>>(to, q + at * p.query.token, step * p.query.token, n, p.query.dim);
-      load_tile<T, KD, kThreads<KD>>(to + kKeys, k + at * p.key.token, step * p.key.token, n, p.key.dim);
-      load_tile<T, kV, kThreads<KD>>(to + 2 * kKeys, v + at * p.value.token, step * p.value.token, n, p.value.dim - e0);
+    auto load = [&](int i) {
+      const int n = min(kL, s.n - i * kL);
+      const int64_t at = step * i * kL;
+      load_tile<T, KD>(queries, q + at * p.query.token, step * p.query.token, n, p.query.dim);
+      load_tile<T, KD>(keys, k + at * p.key.token, step * p.key.token, n, p.key.dim);
+      load_tile<T, kV>(values, v + at * p.value.token, step * p.value.token, n, p.value.dim - e0);
       copies_commit();
     };
-    __syncthreads();
     load(0);
-    float st[kV / 8][4];  // 16 rows (keys' channels) a warp
-    const Stored from_memory = stored(p.states, p.edge, p.Kp, p.Vp, p.K, p.V, p.transposed,
-                                      ((int64_t)blockIdx.x * p.heads + h), ((int64_t)s.group * p.heads + h));
-    get_state(st, from_memory.p, from_memory.rs, from_memory.cs, warp * 16, e0, p.K, p.V, g, t);
-    const Powers powers(a, g, t, p.mul_inner);
-    const Weights weights(a, t, p.shift, p.mul_key);
+    if (threadIdx.x < 64) c->decay[threadIdx.x] = threadIdx.x < 32 ? p.mul_inner * power2(a * (float)(31 - (int)threadIdx.x)) : 0.f;
+    State<KD> st;
+    const Stored src = stored(p.states, p.edge, p.Kp, p.Vp, p.K, p.V, p.transposed, (int64_t)blockIdx.x * p.heads + h,
+                              (int64_t)s.group * p.heads + h);
+    st.get(src.p, src.rs, src.cs, e0, p.K, p.V);
+    const float top_weight = p.mul_key * power2(a * (float)p.shift);
 
-    for (int c = 0; c < chunks; ++c) {
-      const int n = min(kL, s.n - c * kL), pad = kL - n;
-      const uint32_t set = (c & 1) * kSet * 2;
-      float unscale = 1.f, rescale = 1.f;
-      if constexpr (std::is_same<T, __half>::value) {
-        // (in the other set's values, which are read no more and not yet on their way)
-        const int e = state_exponent(st, reinterpret_cast<float*>(tiles + ((c + 1) & 1) * kSet + 2 * kKeys), kWarps<KD>,
-                                     warp, lane);
-        rescale = power_of_two(-e);
-        unscale = power_of_two(e);
-      }
-      put_state<T>(state, st, warp, g, t, rescale);
-      copies_wait<0>();
+    for (int i = 0; i < chunks; ++i, phase ^= 1) {
+      const int n = min(kL, s.n - i * kL), pad = kL - n;
+      copies_wait();
+      const Fit fit = fit_of<T, KD>(c, st, keys, top_weight);
+      st.template to_tile<T>(state, fit.state);
+      publish();
+      before_sync();
       __syncthreads();
-      if (c + 1 < chunks) load(c + 1);
-
-      // queries times the state
-      uint32_t qf[KD / 16][4];
-#pragma unroll
-      for (int i = 0; i < KD / 16; ++i) ldm4(qf[i], (queries + set) ^ (i * 32));
-      float o[kWidth / 8][4] = {};
-#pragma unroll
-      for (int i = 0; i < KD / 16; ++i)
-#pragma unroll
-        for (int x = 0; x < kWidth; x += 16) {
-          uint32_t b[4];
-          ldm4t(b, (state_rows ^ (x * 2)) + i * 16 * kV * 2);
-          mma16<T>(o[x / 8], qf[i], b[0], b[1]);
-          mma16<T>(o[x / 8 + 1], qf[i], b[2], b[3]);
-        }
+      if (threadIdx.x == 0) {
+        after_sync();
+        mma_scores<T, KD>(tmem, queries, keys);
+        commit(smem_u32(&c->done[0]));
+      }
+      const bool more = i + 1 < chunks;
+      if (more) weigh<T, KD, 2>(keys, terms, a, p.shift, p.mul_key * fit.key);
+      wait_done(c, 0, phase);
+      after_sync();
+      decay_scores<T>(tmem, c, a);
+      publish();
+      before_sync();
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        after_sync();
+        mma_outputs<T, KD, false>(tmem, queries, values, state);
+        if (more) mma_state<T, KD, 2>(tmem + kUpdate, terms, values);
+        commit(smem_u32(&c->done[1]));
+      }
+      wait_done(c, 1, phase);
+      after_sync();
+      if (more) {
+        load(i + 1);
+        st.update(tmem + kUpdate, power2(a * (float)n), fit.key_back);
+      }
+      const int64_t tok = from + step * i * kL;
+      const int64_t key_heads = p.heads / p.rep;
+      const Output out{(T*)p.out.p + (int64_t)blockIdx.y * p.out.head + tok * p.out.token + e0, step * p.out.token,
+                       p.out.dim - e0, p.out.wide,
+                       reps > 1 ? p.sums + (tok * key_heads + blockIdx.y) * p.Vp + e0 : nullptr,
+                       step * key_heads * p.Vp, r == 0, r + 1 == reps};
       // (rows before the chunk's first token are not there)
-      const float f0 = p.mul_state * unscale * power2(a * (float)max(rt * 16 + g + 1 - p.shift - pad, 0));
-      const float f1 = p.mul_state * unscale * power2(a * (float)max(rt * 16 + g + 9 - p.shift - pad, 0));
-#pragma unroll
-      for (int i = 0; i < kWidth / 8; ++i) o[i][0] *= f0, o[i][1] *= f0, o[i][2] *= f1, o[i][3] *= f1;
-      add_inner<T, KD, kWidth>(o, qf, keys + set, (values + set) ^ (col0 * 2), rt, powers);
-
-      if (c + 1 < chunks)
-        add_tokens<T, KD, 2>(st, power2(a * (float)n), (keys + set) ^ (warp * 32), values + set, weights, powers.d16);
-      const int64_t tok = from + step * c * kL;
-      if (reps > 1)
-        sum_heads<kWidth>(o, p.sums + (tok * (p.heads / p.rep) + blockIdx.y) * p.Vp + e0 + col0,
-                          step * (p.heads / p.rep) * p.Vp, rt, pad, g, t, r == 0, r + 1 == reps);
-      __syncthreads();  // the state, the queries and the keys have been read
-      if (r + 1 == reps)
-        put_rows<T, KD, kWidth>(smem_at(tiles) + set, o, rt, col0,
-                                (T*)p.out.p + (int64_t)blockIdx.y * p.out.head + tok * p.out.token + e0,
-                                step * p.out.token, pad, p.out.dim - e0, p.out.wide, lane);
+      put_outputs<T>(tmem, terms, p.mul_state * fit.state_back * power2(a * (float)max(row + 1 - p.shift - pad, 0)), out,
+                     pad);
     }
+    __syncthreads();  // the next head's loads and decays follow
   }
+  end<256>(tmem);
 }
 
 // ---- the gradients of keys and values together -----------------------------------
 // Heads of up to 64 channels: both go through the tokens backwards with the same state R
 // [dim][vdim] (the gradient of the state), which is read as it lies for dv and transposed
-// for dk, and updated once.  queries, keys, values, douts as in the call.
+// for dk, and updated once.
 struct KvArgs {
   Split split;
   int32_t heads, rep;
@@ -667,112 +836,92 @@ struct KvArgs {
   float scale;
   float* sums[2];       // [tokens][key heads][64], where rep > 1: of dk, of dv
 };
+constexpr int kKvSmem = 6 * kBlock + 64 * 128 + 1024;
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads<64>, 4) attn_kv_kernel(const __grid_constant__ KvArgs p) {
+__global__ void __launch_bounds__(kThreads, 2) attn_kv_kernel(const __grid_constant__ KvArgs p) {
   extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t keys = smem_u32(smem), values = keys + kBlock, queries = values + kBlock, douts = queries + kBlock;
+  const uint32_t terms = douts + kBlock, state = terms + 2 * kBlock;
+  Control* c = (Control*)(smem + 6 * kBlock + 64 * 128);
+  const uint32_t tmem = begin<256>(c);
   launch_dependents();
   wait_for_previous();
-  constexpr int kTile = kL * 64, kB = kTile * 2;  // keys, values, queries, douts
-  T* tiles = (T*)smem;
-  const uint32_t state = smem_at(tiles + 4 * kTile);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, rt = warp;
   const Span s = span_of(p.split, blockIdx.x);
-  if (s.n == 0) return;
-  const int64_t from = s.start + s.n - 1;
-  const int chunks = (s.n + kL - 1) / kL, key_heads = p.heads / p.rep;
-  const uint32_t rows = rows_first<64>(smem_at(tiles), 0, lane), cols = cols_first<64>(smem_at(tiles), 0, lane);
-  const uint32_t own = rt * 16 * 128;
-  const uint32_t state_rows = rows_first<64>(state, 0, lane), state_cols = cols_first<64>(state, 0, lane);
+  const int64_t from = s.start + s.n - 1, key_heads = p.heads / p.rep;
+  const int chunks = (s.n + kL - 1) / kL;
+  const int row = ((int)threadIdx.x >> 5 & 3) * 32 + ((int)threadIdx.x & 31);
 
-  for (int r = 0; r < p.rep; ++r) {
+  for (int r = 0; r < (s.n ? p.rep : 0); ++r) {
     const int h = blockIdx.y * p.rep + r;
     const float a = log2_decay(p.log_decay, h);
-    auto load = [&](int c) {
-      T* to = tiles;
-      const int n = min(kL, s.n - c * kL);
-      const int64_t at = from - (int64_t)c * kL;
-      load_tile<T, 64, kThreads<64>>(to, head_at<T>(p.k, h, p.rep, at), -p.k.token, n, p.k.dim);
-      load_tile<T, 64, kThreads<64>>(to + kTile, head_at<T>(p.v, h, p.rep, at), -p.v.token, n, p.v.dim);
-      load_tile<T, 64, kThreads<64>>(to + 2 * kTile, head_at<T>(p.q, h, p.rep, at), -p.q.token, n, p.q.dim);
-      load_tile<T, 64, kThreads<64>>(to + 3 * kTile, head_at<T>(p.g, h, p.rep, at), -p.g.token, n, p.g.dim);
+    auto load = [&](int i) {
+      const int n = min(kL, s.n - i * kL);
+      const int64_t at = from - (int64_t)i * kL;
+      load_tile<T, 64>(keys, head_at<T>(p.k, h, p.rep, at), -p.k.token, n, p.k.dim);
+      load_tile<T, 64>(values, head_at<T>(p.v, h, p.rep, at), -p.v.token, n, p.v.dim);
+      load_tile<T, 64>(queries, head_at<T>(p.q, h, p.rep, at), -p.q.token, n, p.q.dim);
+      load_tile<T, 64>(douts, head_at<T>(p.g, h, p.rep, at), -p.g.token, n, p.g.dim);
       copies_commit();
     };
-    __syncthreads();
     load(0);
-    float st[kV / 8][4];
-    const Stored from_memory = stored(p.states, p.edge, 64, 64, p.D, p.E, 0, ((int64_t)blockIdx.x * p.heads + h),
-                                      ((int64_t)s.group * p.heads + h));
-    get_state(st, from_memory.p, from_memory.rs, from_memory.cs, warp * 16, 0, p.D, p.E, g, t);
-    const Powers powers(a, g, t, p.scale);
-    const Weights weights(a, t, 1, p.scale);
+    if (threadIdx.x < 64) c->decay[threadIdx.x] = threadIdx.x < 32 ? p.scale * power2(a * (float)(31 - (int)threadIdx.x)) : 0.f;
+    State<64> st;
+    const Stored src = stored(p.states, p.edge, 64, 64, p.D, p.E, 0, (int64_t)blockIdx.x * p.heads + h,
+                              (int64_t)s.group * p.heads + h);
+    st.get(src.p, src.rs, src.cs, 0, p.D, p.E);
+    const float top_weight = p.scale * power2(a);
 
-    for (int c = 0; c < chunks; ++c) {
-      const int n = min(kL, s.n - c * kL), pad = kL - n;
-      float unscale = 1.f, rescale = 1.f;
-      if constexpr (std::is_same<T, __half>::value) {
-        const int e = state_exponent(st, reinterpret_cast<float*>(tiles + 5 * kTile), kWarps<64>,
-                                     warp, lane);
-        rescale = power_of_two(-e);
-        unscale = power_of_two(e);
-      }
-      put_state<T>(state, st, warp, g, t, rescale);
-      copies_wait<0>();
+    for (int i = 0; i < chunks; ++i) {
+      const int n = min(kL, s.n - i * kL), pad = kL - n;
+      const bool more = i + 1 < chunks;
+      copies_wait();
+      const Fit fit = fit_of<T, 64>(c, st, queries, top_weight);
+      st.template to_tile<T>(state, fit.state);
+      publish();
+      before_sync();
       __syncthreads();
-      const float f0 = unscale * power2(a * (float)max(rt * 16 + g - pad, 0));
-      const float f1 = unscale * power2(a * (float)max(rt * 16 + g + 8 - pad, 0));
-      const int64_t tok = from - (int64_t)c * kL;
-      const int64_t sum = (tok * key_heads + blockIdx.y) * 64, sum_step = -(int64_t)key_heads * 64;
-      uint32_t f[4][4];
-      {  // dv: keys times R, and keys times queries times douts
+      const float f = fit.state_back * power2(a * (float)max(row - pad, 0));
+      const int64_t tok = from - (int64_t)i * kL;
+      const bool sums = p.rep > 1;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ldm4(f[i], (rows + own) ^ (i * 32));
-        float o[8][4] = {};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int x = 0; x < 64; x += 16) {
-            uint32_t b[4];
-            ldm4t(b, (state_rows ^ (x * 2)) + i * 16 * 128);
-            mma16<T>(o[x / 8], f[i], b[0], b[1]);
-            mma16<T>(o[x / 8 + 1], f[i], b[2], b[3]);
-          }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i][0] *= f0, o[i][1] *= f0, o[i][2] *= f1, o[i][3] *= f1;
-        add_inner<T, 64, 64>(o, f, cols + 2 * kB, rows + 3 * kB, rt, powers);
-        if (p.rep > 1) sum_heads<64>(o, p.sums[1] + sum, sum_step, rt, pad, g, t, r == 0, r + 1 == p.rep);
-        if (r + 1 == p.rep)
-          put_rows<T, 64, 64>(smem_at(tiles), o, rt, 0, head_at<T>(p.dv, h, p.rep, tok), -p.dv.token, pad,
-                              p.dv.dim, p.dv.wide, lane);
+      for (int ph = 0; ph < 2; ++ph) {  // dv, dk: each barrier is used twice a chunk
+        if (threadIdx.x == 0) {
+          after_sync();
+          if (ph == 0) mma_scores<T, 64>(tmem, keys, queries);
+          else mma_scores<T, 64>(tmem, values, douts);
+          commit(smem_u32(&c->done[0]));
+        }
+        if (ph == 0 && more) weigh<T, 64, 2>(queries, terms, a, 1, p.scale * fit.key);
+        wait_done(c, 0, ph);
+        after_sync();
+        decay_scores<T>(tmem, c, a);
+        publish();
+        before_sync();
+        __syncthreads();
+        if (threadIdx.x == 0) {
+          after_sync();
+          if (ph == 0) mma_outputs<T, 64, false>(tmem, keys, douts, state);
+          else mma_outputs<T, 64, true>(tmem, values, queries, state);
+          if (ph == 1 && more) mma_state<T, 64, 2>(tmem + kUpdate, terms, douts);
+          commit(smem_u32(&c->done[1]));
+        }
+        wait_done(c, 1, ph);
+        after_sync();
+        const Side& side = ph ? p.dk : p.dv;
+        const Output out{head_at<T>(side, h, p.rep, tok), -side.token, side.dim, side.wide,
+                         sums ? p.sums[1 - ph] + (tok * key_heads + blockIdx.y) * 64 : nullptr, -key_heads * 64, r == 0,
+                         r + 1 == p.rep};
+        // dv through the keys' tile, which nothing uses any more, dk through the values'
+        if (ph == 1 && more) st.update(tmem + kUpdate, power2(a * (float)n), fit.key_back);
+        put_outputs<T>(tmem, ph ? values : keys, f, out, pad);
+        before_sync();
+        __syncthreads();  // the sums in TMEM and the tiles have been read
       }
-      {  // dk: values times R^T, and values times douts times queries
-#pragma unroll
-        for (int i = 0; i < 4; ++i) ldm4(f[i], (rows + kB + own) ^ (i * 32));
-        float o[8][4] = {};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int x = 0; x < 64; x += 16) {
-            uint32_t b[4];
-            ldm4(b, (state_cols ^ (i * 32)) + x * 128);
-            mma16<T>(o[x / 8], f[i], b[0], b[1]);
-            mma16<T>(o[x / 8 + 1], f[i], b[2], b[3]);
-          }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i][0] *= f0, o[i][1] *= f0, o[i][2] *= f1, o[i][3] *= f1;
-        add_inner<T, 64, 64>(o, f, cols + 3 * kB, rows + 2 * kB, rt, powers);
-        if (p.rep > 1) sum_heads<64>(o, p.sums[0] + sum, sum_step, rt, pad, g, t, r == 0, r + 1 == p.rep);
-        if (r + 1 == p.rep)
-          put_rows<T, 64, 64>(smem_at(tiles) + kB, o, rt, 0, head_at<T>(p.dk, h, p.rep, tok), -p.dk.token, pad,
-                              p.dk.dim, p.dk.wide, lane);
-      }
-      if (c + 1 < chunks)
-        add_tokens<T, 64, 2>(st, power2(a * (float)n), (cols + 2 * kB) ^ (warp * 32), rows + 3 * kB, weights,
-                             powers.d16);
-      __syncthreads();  // the state and the tiles have been read
-      if (c + 1 < chunks) load(c + 1);
+      if (more) load(i + 1);
     }
   }
+  end<256>(tmem);
 }
 
 // ---- rows that start anywhere, copied to padded rows --------------------------------
@@ -870,21 +1019,20 @@ constexpr int64_t kMaxTokens = ((int64_t)1 << 31) - 1;
 
 int padded_dim(int32_t dim) { return dim <= 64 ? 64 : 128; }
 
-// Tokens of a segment.  The kernels run in waves of as many blocks as the SMs hold (four
-// of four warps each, two of eight), a wave takes as long as a segment, and each segment
-// costs about two chunks more for its state.  Where a group is one segment its states need
-// neither a sum nor a scan: those two kernels' start is worth about five chunks, and their
-// work half of the outputs'.
-int32_t segment_tokens(const gs_linear_attn* a, bool backward) {
+// Tokens of a segment.  The kernels run in waves of as many blocks as the SMs hold (two
+// with up to 64 channels of queries and keys, else one), a wave takes as long as a segment,
+// and each segment costs about one chunk more for its state.  Where a group is one segment
+// its states need neither a sum nor a scan: those two kernels' start is worth about three
+// chunks, and their work half of the outputs'.
+int32_t segment_tokens(const gs_linear_attn* a) {
   // (the groups' lengths are on the device: taken as equal)
-  const int64_t chunks = div_up(div_up(a->tokens, a->groups), kL), resident = (int64_t)device_sms() * (256 / padded_dim(a->dim));
+  const int64_t chunks = div_up(div_up(a->tokens, a->groups), kL), resident = (int64_t)device_sms() * (128 / padded_dim(a->dim));
   const int64_t blocks = (int64_t)a->groups * a->q_heads * (padded_dim(a->vdim) / kV);
-  const int least = backward ? 2 : 1, most = 32;
-  int best = least;
+  int best = 1;
   int64_t cost = INT64_MAX;
-  for (int m = least; m <= most; ++m) {
+  for (int m = 1; m <= 16; ++m) {
     const int64_t waves = div_up(div_up(chunks, m) * blocks, resident);
-    const int64_t c = chunks <= m ? 2 * waves * (chunks + 2) : 3 * waves * (m + 2) + 10;
+    const int64_t c = chunks <= m ? 2 * waves * (chunks + 1) : 3 * waves * (m + 1) + 6;
     if (c < cost) cost = c, best = m;
   }
   return best * kL;
@@ -944,11 +1092,6 @@ bool side(Side* s, const gs_linear_attn* a, const gs_attn_heads* h, int32_t dim,
   return true;
 }
 
-template <int KD>
-constexpr int kPartsSmem = 2 * kL * (KD + kV) * 2;
-template <int KD>
-constexpr int kOutSmem = (2 * kL * (2 * KD + kV) + KD * kV) * 2;
-
 // Dynamic shared memory beyond 48 KB, asked for once per kernel and device.
 template <typename F>
 bool allow_smem(F kernel, std::atomic<uint64_t>& known, int bytes) {
@@ -989,16 +1132,23 @@ gs_status copy_rows(const gs_linear_attn* a, Side* s, int n, const Room& room, c
   return GS_OK;
 }
 
-template <typename T, int KD>
-gs_status run_parts(const PartsArgs& p, int64_t slots, int parts, cudaStream_t st) {
+template <typename T, int KD, int TERMS>
+gs_status run_parts_of(const PartsArgs& p, int64_t slots, cudaStream_t st) {
   static std::atomic<uint64_t> known{0};
-  if (!allow_smem(attn_parts_kernel<T, KD>, known, kPartsSmem<KD>)) {
+  if (!allow_smem(attn_parts_kernel<T, KD, TERMS>, known, kPartsSmem<KD, TERMS>)) {
     (void)cudaGetLastError();
     return GS_ERR_CUDA;
   }
-  GS_CUDA(launch_overlapped(attn_parts_kernel<T, KD>, dim3((unsigned)slots, p.heads, parts * (p.Ep / kV)),
-                            dim3(kThreads<KD>), kPartsSmem<KD>, st, p));
+  GS_CUDA(launch_overlapped(attn_parts_kernel<T, KD, TERMS>, dim3((unsigned)slots, p.heads, p.Ep / kV), dim3(kThreads),
+                            kPartsSmem<KD, TERMS>, st, p));
   return GS_OK;
+}
+// exact: the last states are handed on.
+template <typename T>
+gs_status run_parts(const PartsArgs& p, int64_t slots, bool exact, cudaStream_t st) {
+  constexpr int kExact = std::is_same<T, __half>::value ? 2 : 3;
+  if (exact) return p.Dp == 64 ? run_parts_of<T, 64, kExact>(p, slots, st) : run_parts_of<T, 128, kExact>(p, slots, st);
+  return p.Dp == 64 ? run_parts_of<T, 64, 2>(p, slots, st) : run_parts_of<T, 128, 2>(p, slots, st);
 }
 gs_status run_scan(const ScanArgs& p, cudaStream_t st) {
   const int64_t blocks = p.split.groups * div_up(p.D * p.E, kScanThreads);
@@ -1016,10 +1166,9 @@ gs_status run_out_of(const OutArgs& p, int64_t slots, cudaStream_t st) {
   }
   GS_CUDA(launch_overlapped(attn_out_kernel<T, KD>,
                             dim3((unsigned)slots, p.shared ? p.heads / p.rep : p.heads, p.Vp / kV),
-                            dim3(kThreads<KD>), kOutSmem<KD>, st, p));
+                            dim3(kThreads), kOutSmem<KD>, st, p));
   return GS_OK;
 }
-constexpr int kKvSmem = 5 * kL * 64 * 2 + 64;  // four tiles, the state, a number a warp
 template <typename T>
 gs_status run_kv(const KvArgs& p, int64_t slots, cudaStream_t st) {
   static std::atomic<uint64_t> known{0};
@@ -1027,8 +1176,7 @@ gs_status run_kv(const KvArgs& p, int64_t slots, cudaStream_t st) {
     (void)cudaGetLastError();
     return GS_ERR_CUDA;
   }
-  GS_CUDA(launch_overlapped(attn_kv_kernel<T>, dim3((unsigned)slots, p.heads / p.rep), dim3(kThreads<64>), kKvSmem, st,
-                            p));
+  GS_CUDA(launch_overlapped(attn_kv_kernel<T>, dim3((unsigned)slots, p.heads / p.rep), dim3(kThreads), kKvSmem, st, p));
   return GS_OK;
 }
 template <typename T>
@@ -1040,8 +1188,8 @@ struct Call {
   Split split;
   int64_t slots;
   int Dp, Ep, rep;
-  Call(const gs_linear_attn* a, bool backward) {
-    split = Split{a->tokens, a->group_offsets, a->groups, segment_tokens(a, backward)};
+  explicit Call(const gs_linear_attn* a) {
+    split = Split{a->tokens, a->group_offsets, a->groups, segment_tokens(a)};
     slots = a->tokens / split.seg + a->groups;
     Dp = padded_dim(a->dim);
     Ep = padded_dim(a->vdim);
@@ -1053,9 +1201,11 @@ struct Call {
 template <typename T>
 gs_status states_of(const gs_linear_attn* a, const Call& c, const Part (&part)[2], const Scan (&scan)[2], int n,
                     cudaStream_t st) {
-  const PartsArgs p{c.split, a->q_heads, c.rep, c.Dp, c.Ep, a->log_decay, {part[0], part[1]}};
-  const gs_status r = c.Dp == 64 ? run_parts<T, 64>(p, c.slots, n, st) : run_parts<T, 128>(p, c.slots, n, st);
-  if (r != GS_OK) return r;
+  for (int i = 0; i < n; ++i) {
+    const PartsArgs p{c.split, a->q_heads, c.rep, c.Dp, c.Ep, a->log_decay, part[i]};
+    const gs_status r = run_parts<T>(p, c.slots, scan[i].last != nullptr, st);
+    if (r != GS_OK) return r;
+  }
   return run_scan(ScanArgs{c.split, a->q_heads, a->dim, a->vdim, c.Dp, c.Ep, a->log_decay, {scan[0], scan[1]}, n}, st);
 }
 
@@ -1066,7 +1216,7 @@ gs_status forward(const gs_linear_attn* a, const Call& c, Side (&s)[4], float* s
   const gs_status copied = copy_rows(a, s, 3, room, st);
   if (copied != GS_OK) return copied;
   if (scan) {
-    const gs_status r = states_of<T>(a, c, {Part{s[1], s[2], 1.f, 0, 0, state_out != nullptr, room.states}, Part{}},
+    const gs_status r = states_of<T>(a, c, {Part{s[1], s[2], 1.f, 0, 0, room.states}, Part{}},
                                      {Scan{a->state, state_out, room.states, 0}, Scan{}}, 1, st);
     if (r != GS_OK) return r;
   }
@@ -1096,8 +1246,7 @@ gs_status backward(const gs_linear_attn* a, const Call& c, Side (&s)[7], const f
   const bool scan = a->tokens > c.split.seg || dstate;
   if (scan) {
     const gs_status r =
-        states_of<T>(a, c, {Part{k, v, 1.f, 0, 0, 0, room.states},
-                          Part{q, g, a->scale, 1, 1, dstate != nullptr, room.grads}},
+        states_of<T>(a, c, {Part{k, v, 1.f, 0, 0, room.states}, Part{q, g, a->scale, 1, 1, room.grads}},
                      {Scan{a->state, nullptr, room.states, 0}, Scan{dstate_out, dstate, room.grads, 1}}, 2, st);
     if (r != GS_OK) return r;
   }
@@ -1151,7 +1300,7 @@ using namespace gs;
 
 extern "C" size_t gs_linear_attn_workspace_bytes(const gs_linear_attn* a, int32_t backward) {
   if (!a || !shape_ok(a)) return 0;
-  const Call c(a, backward != 0);
+  const Call c(a);
   return Room(nullptr, a, c.slots, backward != 0, backward ? 15 : 7).bytes;
 }
 
@@ -1159,7 +1308,7 @@ extern "C" gs_status gs_linear_attn_fwd(const gs_linear_attn* a, const gs_attn_h
                                         const gs_attn_heads* v, const gs_attn_heads* out, float* state_out,
                                         void* workspace, size_t ws_bytes, void* stream) {
   if (!a || !shape_ok(a) || !aligned_or_none(a) || (!a->group_offsets && a->groups != 1)) return GS_ERR_INVALID_ARG;
-  const Call c(a, false);
+  const Call c(a);
   Side s[4] = {};
   if (a->tokens > 0 && (!side(&s[0], a, q, a->dim, false, false) || !side(&s[1], a, k, a->dim, true, false) ||
                         !side(&s[2], a, v, a->vdim, true, false) || !side(&s[3], a, out, a->vdim, false, true)))
@@ -1182,7 +1331,7 @@ extern "C" gs_status gs_linear_attn_bwd(const gs_linear_attn* a, const gs_attn_h
                                         const float* dstate_out, float* dstate, void* workspace, size_t ws_bytes,
                                         void* stream) {
   if (!a || !shape_ok(a) || !aligned_or_none(a) || (!a->group_offsets && a->groups != 1)) return GS_ERR_INVALID_ARG;
-  const Call c(a, true);
+  const Call c(a);
   Side s[7] = {};
   if (a->tokens > 0 &&
       (!side(&s[0], a, q, a->dim, false, false) || !side(&s[1], a, k, a->dim, true, false) ||
@@ -1200,6 +1349,18 @@ extern "C" gs_status gs_linear_attn_bwd(const gs_linear_attn* a, const gs_attn_h
   }
   return a->dtype == GS_BF16 ? backward<__nv_bfloat16>(a, c, s, dstate_out, dstate, room, st)
                              : backward<__half>(a, c, s, dstate_out, dstate, room, st);
+}
+
+extern "C" gs_status gs_linear_attn_status(void* stream) {
+  unsigned int found = 0;
+  const unsigned int none = 0;
+  cudaStream_t st = (cudaStream_t)stream;
+  GS_CUDA(cudaMemcpyFromSymbolAsync(&found, attn_timeouts, sizeof(found), 0, cudaMemcpyDeviceToHost, st));
+  GS_CUDA(cudaStreamSynchronize(st));
+  if (!found) return GS_OK;
+  GS_CUDA(cudaMemcpyToSymbolAsync(attn_timeouts, &none, sizeof(none), 0, cudaMemcpyHostToDevice, st));
+  GS_CUDA(cudaStreamSynchronize(st));
+  return GS_ERR_TIMEOUT;
 }
 
 extern "C" gs_status gs_linear_attn_step(const gs_linear_attn* a, const gs_attn_heads* q, const gs_attn_heads* k,

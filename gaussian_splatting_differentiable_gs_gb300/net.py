@@ -51,6 +51,7 @@ def declare(L):
     L.gs_linear_attn_fwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, sz, vp]
     L.gs_linear_attn_bwd.argtypes = [vp] * 11 + [sz, vp]
     L.gs_linear_attn_step.argtypes = [vp] * 7
+    L.gs_linear_attn_status.argtypes = [vp]
 
 
 from . import _check, lib  # noqa: E402  (the package defines these first)
@@ -575,3 +576,9 @@ def gs_linear_attn_step(q, k, v, log_decay, state, out, scale=None, stream=None)
         _entries(state, "state", (shape[0],) + states[1:], torch.float32, device), _stream(stream, q))
     if status:
         _check("gs_linear_attn_step", status)
+
+
+def gs_linear_attn_status(stream=None):
+    """Synchronises, and raises if a wait for the tensor cores ran out on the current device."""
+    s = torch.cuda.current_stream() if stream is None else stream
+    _check("gs_linear_attn_status", lib().gs_linear_attn_status(s.cuda_stream))

@@ -316,6 +316,12 @@ gs_status gs_linear_attn_bwd(const gs_linear_attn* a, const gs_attn_heads* q,
                              const float* dstate_out, float* dstate, void* workspace,
                              size_t ws_bytes, void* stream);
 
+/* Every wait of these kernels for the tensor cores is bounded (two seconds a
+ * block, after which results are undefined).  gs_linear_attn_status
+ * synchronises the stream and returns GS_ERR_TIMEOUT if one ran out on the
+ * current device since the last such call. */
+gs_status gs_linear_attn_status(void* stream);
+
 /* gs_linear_attn_step -- one token of each of a->tokens streams: state
  * [tokens][q_heads][dim][vdim] fp32, read and updated in place; a->state,
  * a->groups and a->group_offsets are not used (groups: 1). */
