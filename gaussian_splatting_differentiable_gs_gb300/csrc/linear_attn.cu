@@ -138,12 +138,14 @@ static_assert(sizeof(Control) <= 1024, "control");
 // more, the results are undefined and the error is on record.
 __device__ __forceinline__ void wait_done(Control* c, int which, uint32_t parity) {
   const uint32_t bar = smem_u32(&c->done[which]);
-  const int64_t t0 = now_ns();
-  while (!mbar_try(bar, parity) && !c->abort)
-    if (now_ns() - t0 > kWaitNs) {
-      c->abort = 1;
-      atomicOr(&attn_timeouts, kErrTimeout);
-    }
+  if (!mbar_try(bar, parity)) {
+    const int64_t t0 = now_ns();
+    while (!mbar_try(bar, parity) && !c->abort)
+      if (now_ns() - t0 > kWaitNs) {
+        c->abort = 1;
+        atomicOr(&attn_timeouts, kErrTimeout);
+      }
+  }
   __syncwarp();  // the warp's accesses to TMEM are in step
 }
 template <int COLUMNS>
@@ -235,19 +237,32 @@ __device__ __forceinline__ void load_tile(uint32_t tile, const T* from, int64_t 
   const Rows<W> k;
   const int pad = kL - n;
   const T* p = from + (k.r0 - pad) * stride + k.c * 8;
-  const bool in = k.c * 8 < dim;
-  const int64_t next = k.kRows * stride;
+  uint32_t bytes = k.c * 8 < dim ? 16 : 0;
+  int64_t next = k.kRows * stride;
+  if (pad == 0) {
+    if (!bytes) p = from, next = 0;  // (nothing is read there)
 #pragma unroll
-  for (int i = 0; i < k.kCount; ++i) {
-    const bool there = in && k.r0 + i * k.kRows >= pad;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tile + k.at + i * k.kRows * 128),
-                 "l"(there ? p : from), "r"(there ? 16 : 0)
-                 : "memory");
-    p += next;
+    for (int i = 0; i < k.kCount; ++i) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tile + k.at + i * k.kRows * 128), "l"(p),
+                   "r"(bytes)
+                   : "memory");
+      p += next;
+    }
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < k.kCount; ++i) {
+      const bool there = bytes && k.r0 + i * k.kRows >= pad;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tile + k.at + i * k.kRows * 128),
+                   "l"(there ? p : from), "r"(there ? 16 : 0)
+                   : "memory");
+      p += next;
+    }
   }
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+// All but the last N groups of copies are there.
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 __device__ __forceinline__ uint4 get_granule(uint32_t at) {
   uint4 v;
@@ -277,6 +292,9 @@ __device__ __forceinline__ int exponent_of(float m) {
 // The tile's keys, weighted by d^(127 - row + shift) mul, as TERMS terms of T in as many
 // tiles of the same layout one after the other.  Each thread takes the granules that it
 // brought itself.
+//
+// bf16 in two terms: with the weight w = wh + wl in two, hi = k wh + k wl rounded once and
+// lo = (k wh - hi) + k wl, off by 2^-17 of the value; two elements an instruction.
 template <typename T, int KD, int TERMS>
 __device__ __forceinline__ void weigh(uint32_t keys, uint32_t terms, float a, int shift, float mul) {
   const Rows<KD> k;
@@ -289,13 +307,25 @@ __device__ __forceinline__ void weigh(uint32_t keys, uint32_t terms, float a, in
     const uint4 raw = get_granule(keys + at);
     const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
     uint32_t out[TERMS][4];
+    if constexpr (!std::is_same<T, __half>::value && TERMS == 2) {
+      const __nv_bfloat16 first = __float2bfloat16_rn(w);
+      const __nv_bfloat162 wh(first, first), wl = __float2bfloat162_rn(w - __bfloat162float(first));
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float2 x = mul2(unpack<T>(in[j]), both(w));
+      for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&in[j]), t = __hmul2(x, wl);
+        const __nv_bfloat162 hi = __hfma2(x, wh, t), lo = __hadd2(__hfma2(x, wh, __hneg2(hi)), t);
+        out[0][j] = *reinterpret_cast<const uint32_t*>(&hi);
+        out[1][j] = *reinterpret_cast<const uint32_t*>(&lo);
+      }
+    } else {
 #pragma unroll
-      for (int t = 0; t < TERMS; ++t) {
-        out[t][j] = pair_word<T>(x.x, x.y);
-        if (t + 1 < TERMS) x = fma2(unpack<T>(out[t][j]), both(-1.f), x);
+      for (int j = 0; j < 4; ++j) {
+        float2 x = mul2(unpack<T>(in[j]), both(w));
+#pragma unroll
+        for (int t = 0; t < TERMS; ++t) {
+          out[t][j] = pair_word<T>(x.x, x.y);
+          if (t + 1 < TERMS) x = fma2(unpack<T>(out[t][j]), both(-1.f), x);
+        }
       }
     }
 #pragma unroll
@@ -465,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 128 / KD) attn_parts_kernel(const __
   if (chunks) load(0);
   for (int i = 0; i < chunks; ++i) {
     const uint32_t set = tiles + (i & 1) * kSet;
-    copies_wait();
+    copies_wait<0>();
     float mul = part.mul, back = 1.f;
     if constexpr (kHalfType) {
       const float m = top_key<KD>(set);
@@ -551,9 +581,9 @@ __global__ void __launch_bounds__(kScanThreads) attn_scan_kernel(const __grid_co
 
 // ---- outputs -----------------------------------------------------------------
 // TMEM: the products of queries and keys; the decayed ones as the next product's operand;
-// their product with the values; in the first one's place then queries times the state,
+// queries times the state; in the first one's place then the decayed ones times the values
 // and the state's update.
-constexpr uint32_t kScores = 0, kDecayed = 128, kInner = 192, kOuter = 0, kUpdate = 64;
+constexpr uint32_t kScores = 0, kDecayed = 128, kOuter = 192, kInner = 0, kUpdate = 64;
 
 // Where a state is read from: a segment's, or without those the group's own.
 struct Stored {
@@ -567,29 +597,28 @@ __device__ __forceinline__ Stored stored(const float* states, const float* edge,
   return transposed ? Stored{p, 1, ks} : Stored{p, vs, 1};
 }
 
-// scores = queries keys^T, by one thread.
-template <typename T, int KD>
-__device__ __forceinline__ void mma_scores(uint32_t tmem, uint32_t queries, uint32_t keys) {
-  const uint32_t idesc = instruction<T>(kL, kL, false, false);
-  const uint64_t a = operand<false>(queries), b = operand<false>(keys);
+// scores = queries keys^T, outer = queries state (TRANSPOSED: state^T, of 64 x 64), by one
+// thread.
+template <typename T, int KD, bool TRANSPOSED>
+__device__ __forceinline__ void mma_scores(uint32_t tmem, uint32_t queries, uint32_t keys, uint32_t state) {
+  const uint64_t q = operand<false>(queries), k = operand<false>(keys), s = operand<!TRANSPOSED>(state);
+  const uint32_t scores = instruction<T>(kL, kL, false, false), outer = instruction<T>(kL, kV, false, !TRANSPOSED);
 #pragma unroll
   for (int i = 0; i < KD / 16; ++i) {
     const uint64_t at = (i / 4 * kBlock + i % 4 * 32) >> 4;
-    mma(tmem + kScores, a + at, b + at, idesc, i > 0);
+    mma(tmem + kScores, q + at, k + at, scores, i > 0);
   }
+#pragma unroll
+  for (int i = 0; i < KD / 16; ++i)
+    mma(tmem + kOuter, q + ((i / 4 * kBlock + i % 4 * 32) >> 4), s + i * (TRANSPOSED ? 32 >> 4 : 2048 >> 4), outer, i > 0);
 }
-// inner = decayed values, outer = queries state (TRANSPOSED: state^T, of 64 x 64).
-template <typename T, int KD, bool TRANSPOSED>
-__device__ __forceinline__ void mma_outputs(uint32_t tmem, uint32_t queries, uint32_t values, uint32_t state) {
+// inner = decayed values
+template <typename T>
+__device__ __forceinline__ void mma_inner(uint32_t tmem, uint32_t values) {
   const uint64_t v = operand<true>(values);
   const uint32_t inner = instruction<T>(kL, kV, false, true);
 #pragma unroll
   for (int i = 0; i < kL / 16; ++i) mma_tmem(tmem + kInner, tmem + kDecayed + 8 * i, v + i * (2048 >> 4), inner, i > 0);
-  const uint64_t q = operand<false>(queries), s = operand<!TRANSPOSED>(state);
-  const uint32_t outer = instruction<T>(kL, kV, false, !TRANSPOSED);
-#pragma unroll
-  for (int i = 0; i < KD / 16; ++i)
-    mma(tmem + kOuter, q + ((i / 4 * kBlock + i % 4 * 32) >> 4), s + i * (TRANSPOSED ? 32 >> 4 : 2048 >> 4), outer, i > 0);
 }
 
 // The scores' decay and mask: a thread has a row, and of its four blocks of 32 columns
@@ -623,8 +652,8 @@ __device__ __forceinline__ void decay_scores(uint32_t tmem, const Control* c, fl
         const float* d = c->decay + 31 - l;
         loaded(s);
 #pragma unroll
-        for (int j = 0; j < 32; j += 2)
-          o[j / 2] = pair_word<T>(j <= l ? s[j] * d[j] : 0.f, j + 1 <= l ? s[j + 1] * d[j + 1] : 0.f);
+        for (int j = 0; j < 32; j += 2)  // (what the mask takes out may be a NaN)
+          o[j / 2] = pair_word<T>(s[j] * d[j], s[j + 1] * d[j + 1]) & (j < l ? 0xffffffffu : j == l ? 0xffffu : 0u);
       }
     }
     store16(lanes + kDecayed + 16 * b, o);
@@ -733,15 +762,18 @@ struct OutArgs {
   float* sums;           // [tokens][key heads][Vp], where shared and rep > 1
 };
 template <int KD>
-constexpr int kOutSmem = (4 * (KD / 64) + 1) * kBlock + KD * 128 + 1024;
+constexpr int kOutSmem = (4 * (KD / 64) + 2) * kBlock + KD * 128 + 1024;
 
 template <typename T, int KD>
 __global__ void __launch_bounds__(kThreads, 128 / KD) attn_out_kernel(const __grid_constant__ OutArgs p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   constexpr uint32_t kKeys = KD / 64 * kBlock;
-  const uint32_t queries = smem_u32(smem), keys = queries + kKeys, values = keys + kKeys, terms = values + kBlock;
+  // Values in two tiles in turn, so that the next chunk comes while this one's outputs are
+  // formed, which need no queries or keys any more.
+  const uint32_t queries = smem_u32(smem), keys = queries + kKeys, both_values = keys + kKeys;
+  const uint32_t terms = both_values + 2 * kBlock;
   const uint32_t state = terms + 2 * kKeys;
-  Control* c = (Control*)(smem + 4 * kKeys + kBlock + KD * 128);
+  Control* c = (Control*)(smem + 4 * kKeys + 2 * kBlock + KD * 128);
   const uint32_t tmem = begin<256>(c);
   launch_dependents();
   wait_for_previous();
@@ -762,7 +794,9 @@ __global__ void __launch_bounds__(kThreads, 128 / KD) attn_out_kernel(const __gr
       const int64_t at = step * i * kL;
       load_tile<T, KD>(queries, q + at * p.query.token, step * p.query.token, n, p.query.dim);
       load_tile<T, KD>(keys, k + at * p.key.token, step * p.key.token, n, p.key.dim);
-      load_tile<T, kV>(values, v + at * p.value.token, step * p.value.token, n, p.value.dim - e0);
+      copies_commit();
+      load_tile<T, kV>(both_values + (i & 1) * kBlock, v + at * p.value.token, step * p.value.token, n,
+                       p.value.dim - e0);
       copies_commit();
     };
     load(0);
@@ -775,7 +809,8 @@ __global__ void __launch_bounds__(kThreads, 128 / KD) attn_out_kernel(const __gr
 
     for (int i = 0; i < chunks; ++i, phase ^= 1) {
       const int n = min(kL, s.n - i * kL), pad = kL - n;
-      copies_wait();
+      const uint32_t values = both_values + (i & 1) * kBlock;
+      copies_wait<1>();  // (the values may be on their way)
       const Fit fit = fit_of<T, KD>(c, st, keys, top_weight);
       st.template to_tile<T>(state, fit.state);
       publish();
@@ -783,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 128 / KD) attn_out_kernel(const __gr
       __syncthreads();
       if (threadIdx.x == 0) {
         after_sync();
-        mma_scores<T, KD>(tmem, queries, keys);
+        mma_scores<T, KD, false>(tmem, queries, keys, state);
         commit(smem_u32(&c->done[0]));
       }
       const bool more = i + 1 < chunks;
@@ -791,21 +826,20 @@ __global__ void __launch_bounds__(kThreads, 128 / KD) attn_out_kernel(const __gr
       wait_done(c, 0, phase);
       after_sync();
       decay_scores<T>(tmem, c, a);
+      copies_wait<0>();
       publish();
       before_sync();
       __syncthreads();
+      if (more) load(i + 1);
       if (threadIdx.x == 0) {
         after_sync();
-        mma_outputs<T, KD, false>(tmem, queries, values, state);
+        mma_inner<T>(tmem, values);
         if (more) mma_state<T, KD, 2>(tmem + kUpdate, terms, values);
         commit(smem_u32(&c->done[1]));
       }
       wait_done(c, 1, phase);
       after_sync();
-      if (more) {
-        load(i + 1);
-        st.update(tmem + kUpdate, power2(a * (float)n), fit.key_back);
-      }
+      if (more) st.update(tmem + kUpdate, power2(a * (float)n), fit.key_back);
       const int64_t tok = from + step * i * kL;
       const int64_t key_heads = p.heads / p.rep;
       const Output out{(T*)p.out.p + (int64_t)blockIdx.y * p.out.head + tok * p.out.token + e0, step * p.out.token,
@@ -859,9 +893,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv_kernel(const __grid_const
       const int n = min(kL, s.n - i * kL);
       const int64_t at = from - (int64_t)i * kL;
       load_tile<T, 64>(keys, head_at<T>(p.k, h, p.rep, at), -p.k.token, n, p.k.dim);
-      load_tile<T, 64>(values, head_at<T>(p.v, h, p.rep, at), -p.v.token, n, p.v.dim);
       load_tile<T, 64>(queries, head_at<T>(p.q, h, p.rep, at), -p.q.token, n, p.q.dim);
+      copies_commit();
       load_tile<T, 64>(douts, head_at<T>(p.g, h, p.rep, at), -p.g.token, n, p.g.dim);
+      load_tile<T, 64>(values, head_at<T>(p.v, h, p.rep, at), -p.v.token, n, p.v.dim);
       copies_commit();
     };
     load(0);
@@ -875,7 +910,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv_kernel(const __grid_const
     for (int i = 0; i < chunks; ++i) {
       const int n = min(kL, s.n - i * kL), pad = kL - n;
       const bool more = i + 1 < chunks;
-      copies_wait();
+      copies_wait<1>();  // (values and douts may be on their way)
       const Fit fit = fit_of<T, 64>(c, st, queries, top_weight);
       st.template to_tile<T>(state, fit.state);
       publish();
@@ -888,21 +923,21 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv_kernel(const __grid_const
       for (int ph = 0; ph < 2; ++ph) {  // dv, dk: each barrier is used twice a chunk
         if (threadIdx.x == 0) {
           after_sync();
-          if (ph == 0) mma_scores<T, 64>(tmem, keys, queries);
-          else mma_scores<T, 64>(tmem, values, douts);
+          if (ph == 0) mma_scores<T, 64, false>(tmem, keys, queries, state);
+          else mma_scores<T, 64, true>(tmem, values, douts, state);
           commit(smem_u32(&c->done[0]));
         }
         if (ph == 0 && more) weigh<T, 64, 2>(queries, terms, a, 1, p.scale * fit.key);
         wait_done(c, 0, ph);
         after_sync();
         decay_scores<T>(tmem, c, a);
+        if (ph == 0) copies_wait<0>();
         publish();
         before_sync();
         __syncthreads();
         if (threadIdx.x == 0) {
           after_sync();
-          if (ph == 0) mma_outputs<T, 64, false>(tmem, keys, douts, state);
-          else mma_outputs<T, 64, true>(tmem, values, queries, state);
+          mma_inner<T>(tmem, ph ? queries : douts);
           if (ph == 1 && more) mma_state<T, 64, 2>(tmem + kUpdate, terms, douts);
           commit(smem_u32(&c->done[1]));
         }
@@ -1022,17 +1057,20 @@ int padded_dim(int32_t dim) { return dim <= 64 ? 64 : 128; }
 // Tokens of a segment.  The kernels run in waves of as many blocks as the SMs hold (two
 // with up to 64 channels of queries and keys, else one), a wave takes as long as a segment,
 // and each segment costs about one chunk more for its state.  Where a group is one segment
-// its states need neither a sum nor a scan: those two kernels' start is worth about three
-// chunks, and their work half of the outputs'.
+// its states need neither a sum nor a scan (unless the last ones are wanted): those two
+// kernels' start is worth about three chunks, and their work half of the outputs'.  The
+// groups' lengths are on the device: they are taken as equal, but for the longest one,
+// which a lone segment each has to wait for.
 int32_t segment_tokens(const gs_linear_attn* a) {
-  // (the groups' lengths are on the device: taken as equal)
-  const int64_t chunks = div_up(div_up(a->tokens, a->groups), kL), resident = (int64_t)device_sms() * (128 / padded_dim(a->dim));
+  const int64_t mean = div_up(a->tokens, a->groups), chunks = div_up(mean, kL);
+  const int64_t longest = div_up(mean * (a->groups > 1 ? 2 : 1), kL);
+  const int64_t resident = (int64_t)device_sms() * (128 / padded_dim(a->dim));
   const int64_t blocks = (int64_t)a->groups * a->q_heads * (padded_dim(a->vdim) / kV);
   int best = 1;
   int64_t cost = INT64_MAX;
   for (int m = 1; m <= 16; ++m) {
     const int64_t waves = div_up(div_up(chunks, m) * blocks, resident);
-    const int64_t c = chunks <= m ? 2 * waves * (chunks + 1) : 3 * waves * (m + 1) + 6;
+    const int64_t c = longest <= m ? 2 * waves * (longest + 1) : 3 * waves * (m + 1) + 6;
     if (c < cost) cost = c, best = m;
   }
   return best * kL;
