@@ -290,15 +290,15 @@ __device__ __forceinline__ int exponent_of(float m) {
 }
 
 // The tile's keys, weighted by d^(127 - row + shift) mul, as TERMS terms of T in as many
-// tiles of the same layout one after the other.  Each thread takes the granules that it
-// brought itself.
+// tiles of the same layout, `next_term` bytes after one another (the first may be
+// the keys' own tile).  Each thread takes the granules that it brought itself.
 //
 // bf16 in two terms: with the weight w = wh + wl in two, hi = k wh + k wl rounded once and
 // lo = (k wh - hi) + k wl, off by 2^-17 of the value; two elements an instruction.
 template <typename T, int KD, int TERMS>
-__device__ __forceinline__ void weigh(uint32_t keys, uint32_t terms, float a, int shift, float mul) {
+__device__ __forceinline__ void weigh(uint32_t keys, uint32_t first_term, uint32_t next_term, float a, int shift,
+                                      float mul) {
   const Rows<KD> k;
-  constexpr uint32_t kTermBytes = KD / 64 * kBlock;
   float w = mul * power2(a * (float)(kL - 1 - (k.r0 + (k.kCount - 1) * k.kRows) + shift));
   const float next = power2(a * (float)k.kRows);
 #pragma unroll
@@ -330,7 +330,7 @@ __device__ __forceinline__ void weigh(uint32_t keys, uint32_t terms, float a, in
     }
 #pragma unroll
     for (int t = 0; t < TERMS; ++t)
-      put_granule(terms + t * kTermBytes + at, make_uint4(out[t][0], out[t][1], out[t][2], out[t][3]));
+      put_granule(first_term + t * next_term + at, make_uint4(out[t][0], out[t][1], out[t][2], out[t][3]));
     w *= next;
   }
 }
@@ -429,12 +429,12 @@ struct State {
 };
 // terms^T values: the products of a state's update, by one thread.
 template <typename T, int KD, int TERMS>
-__device__ __forceinline__ void mma_state(uint32_t d, uint32_t terms, uint32_t values) {
+__device__ __forceinline__ void mma_state(uint32_t d, uint32_t first_term, uint32_t next_term, uint32_t values) {
   const uint32_t idesc = instruction<T>(KD, kV, true, true);
   const uint64_t b = operand<true>(values);
 #pragma unroll
   for (int t = 0; t < TERMS; ++t) {
-    const uint64_t a = operand<true>(terms + t * (KD / 64 * kBlock));
+    const uint64_t a = operand<true>(first_term + t * next_term);
 #pragma unroll
     for (int i = 0; i < kL / 16; ++i) mma(d, a + i * (2048 >> 4), b + i * (2048 >> 4), idesc, t > 0 || i > 0);
   }
@@ -481,21 +481,32 @@ __global__ void __launch_bounds__(kThreads, 128 / KD) attn_parts_kernel(const __
   const int64_t step = part.back ? -1 : 1;
   const T* k = head_at<T>(part.key, h, p.rep, from);
   const T* v = head_at<T>(part.value, h, p.rep, from) + e0;
-  auto load = [&](int i) {
-    const uint32_t to = tiles + (i & 1) * kSet;
-    const int n = min(kL, s.n - i * kL);
-    const int64_t at = step * i * kL;
-    load_tile<T, KD>(to, k + at * part.key.token, step * part.key.token, n, part.key.dim);
-    load_tile<T, kV>(to + KD / 64 * kBlock, v + at * part.value.token, step * part.value.token, n, part.value.dim - e0);
+  const int chunks = (s.n + kL - 1) / kL;
+  constexpr uint32_t kTerm = KD / 64 * kBlock;
+  // Two chunks ahead: a chunk's keys make room when they have been weighed (each thread
+  // brings the granules that it weighs), its values when they have been multiplied.
+  auto load_keys = [&](int i) {
+    if (i < chunks)
+      load_tile<T, KD>(tiles + (i & 1) * kSet, k + step * i * kL * part.key.token, step * part.key.token,
+                       min(kL, s.n - i * kL), part.key.dim);
     copies_commit();
   };
-  const int chunks = (s.n + kL - 1) / kL;
+  auto load_values = [&](int i) {
+    if (i < chunks)
+      load_tile<T, kV>(tiles + (i & 1) * kSet + kTerm, v + step * i * kL * part.value.token, step * part.value.token,
+                       min(kL, s.n - i * kL), part.value.dim - e0);
+    copies_commit();
+  };
   State<KD> st;
   st.zero();
-  if (chunks) load(0);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    load_keys(i);
+    load_values(i);
+  }
   for (int i = 0; i < chunks; ++i) {
     const uint32_t set = tiles + (i & 1) * kSet;
-    copies_wait<0>();
+    copies_wait<2>();
     float mul = part.mul, back = 1.f;
     if constexpr (kHalfType) {
       const float m = top_key<KD>(set);
@@ -508,18 +519,19 @@ __global__ void __launch_bounds__(kThreads, 128 / KD) attn_parts_kernel(const __
       mul *= power_of_two(-e);
       back = power_of_two(e);
     }
-    weigh<T, KD, TERMS>(set, terms, a, part.shift, mul);
+    weigh<T, KD, TERMS>(set, terms, kTerm, a, part.shift, mul);
     publish();
     before_sync();
     __syncthreads();
     if (threadIdx.x == 0) {
       after_sync();
-      mma_state<T, KD, TERMS>(tmem, terms, set + KD / 64 * kBlock);
+      mma_state<T, KD, TERMS>(tmem, terms, kTerm, set + kTerm);
       commit(smem_u32(&c->done[0]));
     }
-    if (i + 1 < chunks) load(i + 1);
+    load_keys(i + 2);
     wait_done(c, 0, i & 1);
     after_sync();
+    load_values(i + 2);
     st.update(tmem, power2(a * (float)min(kL, s.n - i * kL)), back);
   }
   if (s.n) st.put(part.to + ((int64_t)blockIdx.x * p.heads + h) * p.Dp * p.Ep + e0, p.Ep);
@@ -762,18 +774,18 @@ struct OutArgs {
   float* sums;           // [tokens][key heads][Vp], where shared and rep > 1
 };
 template <int KD>
-constexpr int kOutSmem = (4 * (KD / 64) + 2) * kBlock + KD * 128 + 1024;
+constexpr int kOutSmem = 2 * (2 * (KD / 64) + 1) * kBlock + KD * 128 + 1024;
 
 template <typename T, int KD>
 __global__ void __launch_bounds__(kThreads, 128 / KD) attn_out_kernel(const __grid_constant__ OutArgs p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   constexpr uint32_t kKeys = KD / 64 * kBlock;
-  // Values in two tiles in turn, so that the next chunk comes while this one's outputs are
-  // formed, which need no queries or keys any more.
-  const uint32_t queries = smem_u32(smem), keys = queries + kKeys, both_values = keys + kKeys;
-  const uint32_t terms = both_values + 2 * kBlock;
-  const uint32_t state = terms + 2 * kKeys;
-  Control* c = (Control*)(smem + 4 * kKeys + 2 * kBlock + KD * 128);
+  // Two sets of tiles in turn, so that a chunk comes while the one before is worked on: the
+  // weighted keys' terms take the places of the keys and of the queries when these have
+  // been multiplied, the outputs leave through the keys'.
+  constexpr uint32_t kSet = 2 * kKeys + kBlock;  // queries, keys, values
+  const uint32_t tiles = smem_u32(smem), state = tiles + 2 * kSet;
+  Control* c = (Control*)(smem + 2 * kSet + KD * 128);
   const uint32_t tmem = begin<256>(c);
   launch_dependents();
   wait_for_previous();
@@ -792,11 +804,10 @@ __global__ void __launch_bounds__(kThreads, 128 / KD) attn_out_kernel(const __gr
     auto load = [&](int i) {
       const int n = min(kL, s.n - i * kL);
       const int64_t at = step * i * kL;
-      load_tile<T, KD>(queries, q + at * p.query.token, step * p.query.token, n, p.query.dim);
-      load_tile<T, KD>(keys, k + at * p.key.token, step * p.key.token, n, p.key.dim);
-      copies_commit();
-      load_tile<T, kV>(both_values + (i & 1) * kBlock, v + at * p.value.token, step * p.value.token, n,
-                       p.value.dim - e0);
+      const uint32_t to = tiles + (i & 1) * kSet;
+      load_tile<T, KD>(to, q + at * p.query.token, step * p.query.token, n, p.query.dim);
+      load_tile<T, KD>(to + kKeys, k + at * p.key.token, step * p.key.token, n, p.key.dim);
+      load_tile<T, kV>(to + 2 * kKeys, v + at * p.value.token, step * p.value.token, n, p.value.dim - e0);
       copies_commit();
     };
     load(0);
@@ -809,8 +820,8 @@ __global__ void __launch_bounds__(kThreads, 128 / KD) attn_out_kernel(const __gr
 
     for (int i = 0; i < chunks; ++i, phase ^= 1) {
       const int n = min(kL, s.n - i * kL), pad = kL - n;
-      const uint32_t values = both_values + (i & 1) * kBlock;
-      copies_wait<1>();  // (the values may be on their way)
+      const uint32_t queries = tiles + (i & 1) * kSet, keys = queries + kKeys, values = keys + kKeys;
+      copies_wait<0>();
       const Fit fit = fit_of<T, KD>(c, st, keys, top_weight);
       st.template to_tile<T>(state, fit.state);
       publish();
@@ -822,19 +833,18 @@ __global__ void __launch_bounds__(kThreads, 128 / KD) attn_out_kernel(const __gr
         commit(smem_u32(&c->done[0]));
       }
       const bool more = i + 1 < chunks;
-      if (more) weigh<T, KD, 2>(keys, terms, a, p.shift, p.mul_key * fit.key);
+      if (more) load(i + 1);
       wait_done(c, 0, phase);
       after_sync();
+      if (more) weigh<T, KD, 2>(keys, keys, queries - keys, a, p.shift, p.mul_key * fit.key);
       decay_scores<T>(tmem, c, a);
-      copies_wait<0>();
       publish();
       before_sync();
       __syncthreads();
-      if (more) load(i + 1);
       if (threadIdx.x == 0) {
         after_sync();
         mma_inner<T>(tmem, values);
-        if (more) mma_state<T, KD, 2>(tmem + kUpdate, terms, values);
+        if (more) mma_state<T, KD, 2>(tmem + kUpdate, keys, queries - keys, values);
         commit(smem_u32(&c->done[1]));
       }
       wait_done(c, 1, phase);
@@ -847,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 128 / KD) attn_out_kernel(const __gr
                        reps > 1 ? p.sums + (tok * key_heads + blockIdx.y) * p.Vp + e0 : nullptr,
                        step * key_heads * p.Vp, r == 0, r + 1 == reps};
       // (rows before the chunk's first token are not there)
-      put_outputs<T>(tmem, terms, p.mul_state * fit.state_back * power2(a * (float)max(row + 1 - p.shift - pad, 0)), out,
+      put_outputs<T>(tmem, keys, p.mul_state * fit.state_back * power2(a * (float)max(row + 1 - p.shift - pad, 0)), out,
                      pad);
     }
     __syncthreads();  // the next head's loads and decays follow
@@ -870,13 +880,15 @@ struct KvArgs {
   float scale;
   float* sums[2];       // [tokens][key heads][64], where rep > 1: of dk, of dv
 };
-constexpr int kKvSmem = 6 * kBlock + 64 * 128 + 1024;
+constexpr int kKvSmem = 6 * kBlock + 64 * 128 + 1024;  // keys and queries twice, values, douts; the state
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) attn_kv_kernel(const __grid_constant__ KvArgs p) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  const uint32_t keys = smem_u32(smem), values = keys + kBlock, queries = values + kBlock, douts = queries + kBlock;
-  const uint32_t terms = douts + kBlock, state = terms + 2 * kBlock;
+  // Keys and queries in two pairs of tiles in turn: the next chunk's come while this one is
+  // worked on, its values and douts while its first scores are.  The weighted queries'
+  // terms take the places of keys and values when these have been multiplied.
+  const uint32_t pairs = smem_u32(smem), values = pairs + 4 * kBlock, douts = values + kBlock, state = douts + kBlock;
   Control* c = (Control*)(smem + 6 * kBlock + 64 * 128);
   const uint32_t tmem = begin<256>(c);
   launch_dependents();
@@ -889,17 +901,23 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv_kernel(const __grid_const
   for (int r = 0; r < (s.n ? p.rep : 0); ++r) {
     const int h = blockIdx.y * p.rep + r;
     const float a = log2_decay(p.log_decay, h);
-    auto load = [&](int i) {
+    auto load_pair = [&](int i) {
       const int n = min(kL, s.n - i * kL);
       const int64_t at = from - (int64_t)i * kL;
-      load_tile<T, 64>(keys, head_at<T>(p.k, h, p.rep, at), -p.k.token, n, p.k.dim);
-      load_tile<T, 64>(queries, head_at<T>(p.q, h, p.rep, at), -p.q.token, n, p.q.dim);
+      const uint32_t to = pairs + (i & 1) * 2 * kBlock;
+      load_tile<T, 64>(to, head_at<T>(p.k, h, p.rep, at), -p.k.token, n, p.k.dim);
+      load_tile<T, 64>(to + kBlock, head_at<T>(p.q, h, p.rep, at), -p.q.token, n, p.q.dim);
       copies_commit();
+    };
+    auto load_others = [&](int i) {
+      const int n = min(kL, s.n - i * kL);
+      const int64_t at = from - (int64_t)i * kL;
       load_tile<T, 64>(douts, head_at<T>(p.g, h, p.rep, at), -p.g.token, n, p.g.dim);
       load_tile<T, 64>(values, head_at<T>(p.v, h, p.rep, at), -p.v.token, n, p.v.dim);
       copies_commit();
     };
-    load(0);
+    load_pair(0);
+    load_others(0);
     if (threadIdx.x < 64) c->decay[threadIdx.x] = threadIdx.x < 32 ? p.scale * power2(a * (float)(31 - (int)threadIdx.x)) : 0.f;
     State<64> st;
     const Stored src = stored(p.states, p.edge, 64, 64, p.D, p.E, 0, (int64_t)blockIdx.x * p.heads + h,
@@ -910,6 +928,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv_kernel(const __grid_const
     for (int i = 0; i < chunks; ++i) {
       const int n = min(kL, s.n - i * kL), pad = kL - n;
       const bool more = i + 1 < chunks;
+      const uint32_t keys = pairs + (i & 1) * 2 * kBlock, queries = keys + kBlock;
       copies_wait<1>();  // (values and douts may be on their way)
       const Fit fit = fit_of<T, 64>(c, st, queries, top_weight);
       st.template to_tile<T>(state, fit.state);
@@ -927,18 +946,22 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv_kernel(const __grid_const
           else mma_scores<T, 64, true>(tmem, values, douts, state);
           commit(smem_u32(&c->done[0]));
         }
-        if (ph == 0 && more) weigh<T, 64, 2>(queries, terms, a, 1, p.scale * fit.key);
+        if (ph == 0) {
+          if (more) load_pair(i + 1);
+          else copies_commit();
+        }
         wait_done(c, 0, ph);
         after_sync();
+        if (ph == 1 && more) weigh<T, 64, 2>(queries, keys, values - keys, a, 1, p.scale * fit.key);
         decay_scores<T>(tmem, c, a);
-        if (ph == 0) copies_wait<0>();
+        if (ph == 0) copies_wait<1>();  // values and douts are there
         publish();
         before_sync();
         __syncthreads();
         if (threadIdx.x == 0) {
           after_sync();
           mma_inner<T>(tmem, ph ? queries : douts);
-          if (ph == 1 && more) mma_state<T, 64, 2>(tmem + kUpdate, terms, douts);
+          if (ph == 1 && more) mma_state<T, 64, 2>(tmem + kUpdate, keys, values - keys, douts);
           commit(smem_u32(&c->done[1]));
         }
         wait_done(c, 1, ph);
@@ -953,7 +976,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv_kernel(const __grid_const
         before_sync();
         __syncthreads();  // the sums in TMEM and the tiles have been read
       }
-      if (more) load(i + 1);
+      if (more) load_others(i + 1);
     }
   }
   end<256>(tmem);
