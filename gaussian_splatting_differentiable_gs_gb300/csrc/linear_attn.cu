@@ -716,24 +716,27 @@ __device__ __forceinline__ void put_outputs(uint32_t tmem, uint32_t room, float 
                 make_uint4(pair_word<T>(x[8 * j], x[8 * j + 1]), pair_word<T>(x[8 * j + 2], x[8 * j + 3]),
                            pair_word<T>(x[8 * j + 4], x[8 * j + 5]), pair_word<T>(x[8 * j + 6], x[8 * j + 7])));
   __syncwarp();
-  const int g = half * 4 + (lane & 3);
-  if (g * 8 < out.dim) {
-    const int r0 = (warp & 3) * 32 + (lane >> 2);
+  if (out.wide) {
+    // (rows r and r + 4 together: their granules lie in different banks)
+    const int g = half * 4 + (lane & 3), r0 = (warp & 3) * 32 + (lane >> 3) + (lane & 4);
     T* to = (T*)out.p + (r0 - pad) * out.stride + g * 8;
+    if (g * 8 < out.dim)
 #pragma unroll
-    for (int i = 0; i < 4; ++i, to += 8 * out.stride) {
-      const int r = r0 + i * 8;
-      if (r < pad) continue;
-      const uint4 v = get_granule(room + r * 128 + ((g ^ (r & 7)) << 4));
-      if (out.wide) {
-        *reinterpret_cast<uint4*>(to) = v;
-      } else {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (g * 8 + j < out.dim) reinterpret_cast<uint16_t*>(to)[j] = (uint16_t)(w[j / 2] >> (j % 2 * 16));
+      for (int i = 0; i < 4; ++i, to += 8 * out.stride) {
+        const int r = r0 + i * 8;
+        if (r >= pad) *reinterpret_cast<uint4*>(to) = get_granule(room + r * 128 + ((g ^ (r & 7)) << 4));
       }
-    }
+  } else {
+    const int col = half * 32 + lane;
+    if (col < out.dim)
+      for (int r = max((warp & 3) * 32, pad); r < (warp & 3) * 32 + 32; ++r) {
+        uint16_t v;
+        asm volatile("ld.shared.u16 %0, [%1];"
+                     : "=h"(v)
+                     : "r"(room + r * 128 + (((col >> 3) ^ (r & 7)) << 4) + (col & 7) * 2)
+                     : "memory");
+        reinterpret_cast<uint16_t*>(out.p)[(r - pad) * out.stride + col] = v;
+      }
   }
   __syncwarp();
 }
@@ -774,18 +777,22 @@ struct OutArgs {
   float* sums;           // [tokens][key heads][Vp], where shared and rep > 1
 };
 template <int KD>
-constexpr int kOutSmem = 2 * (2 * (KD / 64) + 1) * kBlock + KD * 128 + 1024;
+constexpr int kOutSets = KD == 64 ? 2 : 1;
+template <int KD>
+constexpr int kOutSmem = kOutSets<KD> * (2 * (KD / 64) + 1) * kBlock + KD * 128 + 1024;
 
 template <typename T, int KD>
-__global__ void __launch_bounds__(kThreads, 128 / KD) attn_out_kernel(const __grid_constant__ OutArgs p) {
+__global__ void __launch_bounds__(kThreads, 2) attn_out_kernel(const __grid_constant__ OutArgs p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   constexpr uint32_t kKeys = KD / 64 * kBlock;
-  // Two sets of tiles in turn, so that a chunk comes while the one before is worked on: the
-  // weighted keys' terms take the places of the keys and of the queries when these have
-  // been multiplied, the outputs leave through the keys'.
-  constexpr uint32_t kSet = 2 * kKeys + kBlock;  // queries, keys, values
-  const uint32_t tiles = smem_u32(smem), state = tiles + 2 * kSet;
-  Control* c = (Control*)(smem + 2 * kSet + KD * 128);
+  // The weighted keys' terms take the places of the keys and of the queries when these have
+  // been multiplied, the outputs leave through the keys'.  Up to 64 channels there is room
+  // for two sets of tiles in turn, so that a chunk comes while the one before is worked on
+  // (32640 tokens, 16 heads of 64: 59 us, with a set and a half 58, one 65); with 128 one
+  // set leaves room for two blocks an SM instead.
+  constexpr uint32_t kSets = kOutSets<KD>, kSet = 2 * kKeys + kBlock;  // queries, keys, values
+  const uint32_t tiles = smem_u32(smem), state = tiles + kSets * kSet;
+  Control* c = (Control*)(smem + kSets * kSet + KD * 128);
   const uint32_t tmem = begin<256>(c);
   launch_dependents();
   wait_for_previous();
@@ -804,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 128 / KD) attn_out_kernel(const __gr
     auto load = [&](int i) {
       const int n = min(kL, s.n - i * kL);
       const int64_t at = step * i * kL;
-      const uint32_t to = tiles + (i & 1) * kSet;
+      const uint32_t to = tiles + i % kSets * kSet;
       load_tile<T, KD>(to, q + at * p.query.token, step * p.query.token, n, p.query.dim);
       load_tile<T, KD>(to + kKeys, k + at * p.key.token, step * p.key.token, n, p.key.dim);
       load_tile<T, kV>(to + 2 * kKeys, v + at * p.value.token, step * p.value.token, n, p.value.dim - e0);
@@ -820,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 128 / KD) attn_out_kernel(const __gr
 
     for (int i = 0; i < chunks; ++i, phase ^= 1) {
       const int n = min(kL, s.n - i * kL), pad = kL - n;
-      const uint32_t queries = tiles + (i & 1) * kSet, keys = queries + kKeys, values = keys + kKeys;
+      const uint32_t queries = tiles + i % kSets * kSet, keys = queries + kKeys, values = keys + kKeys;
       copies_wait<0>();
       const Fit fit = fit_of<T, KD>(c, st, keys, top_weight);
       st.template to_tile<T>(state, fit.state);
@@ -833,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, 128 / KD) attn_out_kernel(const __gr
         commit(smem_u32(&c->done[0]));
       }
       const bool more = i + 1 < chunks;
-      if (more) load(i + 1);
+      if (more && kSets == 2) load(i + 1);
       wait_done(c, 0, phase);
       after_sync();
       if (more) weigh<T, KD, 2>(keys, keys, queries - keys, a, p.shift, p.mul_key * fit.key);
@@ -859,6 +866,10 @@ __global__ void __launch_bounds__(kThreads, 128 / KD) attn_out_kernel(const __gr
       // (rows before the chunk's first token are not there)
       put_outputs<T>(tmem, keys, p.mul_state * fit.state_back * power2(a * (float)max(row + 1 - p.shift - pad, 0)), out,
                      pad);
+      if (more && kSets == 1) {
+        __syncthreads();  // the outputs have left the keys' tile
+        load(i + 1);
+      }
     }
     __syncthreads();  // the next head's loads and decays follow
   }
@@ -1078,22 +1089,31 @@ constexpr int64_t kMaxTokens = ((int64_t)1 << 31) - 1;
 int padded_dim(int32_t dim) { return dim <= 64 ? 64 : 128; }
 
 // Tokens of a segment.  The kernels run in waves of as many blocks as the SMs hold (two
-// with up to 64 channels of queries and keys, else one), a wave takes as long as a segment,
-// and each segment costs about one chunk more for its state.  Where a group is one segment
-// its states need neither a sum nor a scan (unless the last ones are wanted): those two
-// kernels' start is worth about three chunks, and their work half of the outputs'.  The
-// groups' lengths are on the device: they are taken as equal, but for the longest one,
-// which a lone segment each has to wait for.
-int32_t segment_tokens(const gs_linear_attn* a) {
-  const int64_t mean = div_up(a->tokens, a->groups), chunks = div_up(mean, kL);
-  const int64_t longest = div_up(mean * (a->groups > 1 ? 2 : 1), kL);
-  const int64_t resident = (int64_t)device_sms() * (128 / padded_dim(a->dim));
-  const int64_t blocks = (int64_t)a->groups * a->q_heads * (padded_dim(a->vdim) / kV);
+// each), and a wave takes as long as a segment: about a chunk's time for each of its chunks
+// and one more for its state.  A chunk of the outputs or of the queries' gradients costs
+// two units, of the states' sums one, of the keys' and values' gradients four for each query
+// head of a key head; the sums' and the scan's start costs six.  Where a group is one
+// segment and its last state is not wanted, there are neither.  The groups' lengths are on
+// the device: they are taken as equal, and a lone segment as long as two of them.
+int32_t segment_tokens(const gs_linear_attn* a, bool backward, bool states) {
+  const int64_t chunks = div_up(div_up(a->tokens, a->groups), kL);
+  const int64_t longest = a->groups > 1 ? 2 * chunks : chunks;
+  const int64_t resident = (int64_t)device_sms() * 2, rep = a->q_heads / a->k_heads;
+  const int64_t tiles = padded_dim(a->vdim) / kV, key_tiles = padded_dim(a->dim) / kV;
   int best = 1;
   int64_t cost = INT64_MAX;
   for (int m = 1; m <= 16; ++m) {
-    const int64_t waves = div_up(div_up(chunks, m) * blocks, resident);
-    const int64_t c = longest <= m ? 2 * waves * (longest + 1) : 3 * waves * (m + 1) + 6;
+    const bool alone = longest <= m;
+    const int64_t n = alone ? longest : m, segments = a->groups * (alone ? 1 : div_up(chunks, m));
+    const int64_t wave = div_up(segments * a->q_heads * tiles, resident);
+    int64_t c = 0;
+    if (!alone || states) c += (backward ? 2 : 1) * wave * (n + 1) + 6;
+    if (backward) {
+      c += 2 * div_up(segments * a->q_heads * key_tiles, resident) * (n + 1);
+      c += 4 * div_up(segments * a->k_heads * key_tiles * tiles, resident) * (n * rep + 1);
+    } else {
+      c += 2 * wave * (n + 1);
+    }
     if (c < cost) cost = c, best = m;
   }
   return best * kL;
@@ -1214,7 +1234,7 @@ gs_status run_parts(const PartsArgs& p, int64_t slots, bool exact, cudaStream_t 
 gs_status run_scan(const ScanArgs& p, cudaStream_t st) {
   const int64_t blocks = p.split.groups * div_up(p.D * p.E, kScanThreads);
   if (blocks > INT32_MAX) return GS_ERR_INVALID_ARG;
-  GS_CUDA(launch_overlapped(attn_scan_kernel<16>, dim3((unsigned)blocks, p.heads, p.scans), dim3(kScanThreads), 0, st,
+  GS_CUDA(launch_overlapped(attn_scan_kernel<8>, dim3((unsigned)blocks, p.heads, p.scans), dim3(kScanThreads), 0, st,
                             p));
   return GS_OK;
 }
@@ -1249,8 +1269,8 @@ struct Call {
   Split split;
   int64_t slots;
   int Dp, Ep, rep;
-  explicit Call(const gs_linear_attn* a) {
-    split = Split{a->tokens, a->group_offsets, a->groups, segment_tokens(a)};
+  Call(const gs_linear_attn* a, bool backward, bool states) {
+    split = Split{a->tokens, a->group_offsets, a->groups, segment_tokens(a, backward, states)};
     slots = a->tokens / split.seg + a->groups;
     Dp = padded_dim(a->dim);
     Ep = padded_dim(a->vdim);
@@ -1361,15 +1381,20 @@ using namespace gs;
 
 extern "C" size_t gs_linear_attn_workspace_bytes(const gs_linear_attn* a, int32_t backward) {
   if (!a || !shape_ok(a)) return 0;
-  const Call c(a);
-  return Room(nullptr, a, c.slots, backward != 0, backward ? 15 : 7).bytes;
+  size_t most = 0;
+  for (int states = 0; states < 2; ++states) {
+    const Call c(a, backward != 0, states != 0);
+    const size_t n = Room(nullptr, a, c.slots, backward != 0, backward ? 15 : 7).bytes;
+    if (n > most) most = n;
+  }
+  return most;
 }
 
 extern "C" gs_status gs_linear_attn_fwd(const gs_linear_attn* a, const gs_attn_heads* q, const gs_attn_heads* k,
                                         const gs_attn_heads* v, const gs_attn_heads* out, float* state_out,
                                         void* workspace, size_t ws_bytes, void* stream) {
   if (!a || !shape_ok(a) || !aligned_or_none(a) || (!a->group_offsets && a->groups != 1)) return GS_ERR_INVALID_ARG;
-  const Call c(a);
+  const Call c(a, false, state_out != nullptr);
   Side s[4] = {};
   if (a->tokens > 0 && (!side(&s[0], a, q, a->dim, false, false) || !side(&s[1], a, k, a->dim, true, false) ||
                         !side(&s[2], a, v, a->vdim, true, false) || !side(&s[3], a, out, a->vdim, false, true)))
@@ -1392,7 +1417,7 @@ extern "C" gs_status gs_linear_attn_bwd(const gs_linear_attn* a, const gs_attn_h
                                         const float* dstate_out, float* dstate, void* workspace, size_t ws_bytes,
                                         void* stream) {
   if (!a || !shape_ok(a) || !aligned_or_none(a) || (!a->group_offsets && a->groups != 1)) return GS_ERR_INVALID_ARG;
-  const Call c(a);
+  const Call c(a, true, dstate != nullptr);
   Side s[7] = {};
   if (a->tokens > 0 &&
       (!side(&s[0], a, q, a->dim, false, false) || !side(&s[1], a, k, a->dim, true, false) ||
