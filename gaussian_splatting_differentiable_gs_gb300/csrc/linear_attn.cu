@@ -1157,7 +1157,7 @@ bool aligned_or_none(const gs_linear_attn* a) {
 }
 
 bool side(Side* s, const gs_linear_attn* a, const gs_attn_heads* h, int32_t dim, bool of_key, bool output) {
-  if (!h || !h->p || !aligned_to(h->p, 2)) return false;
+  if (!h->p || !aligned_to(h->p, 2)) return false;
   constexpr int64_t kMost = (int64_t)1 << 40;
   if (h->token >= kMost || h->token <= -kMost || h->head >= kMost || h->head <= -kMost) return false;
   const int32_t heads = of_key ? a->k_heads : a->q_heads;
@@ -1390,14 +1390,13 @@ extern "C" size_t gs_linear_attn_workspace_bytes(const gs_linear_attn* a, int32_
   return most;
 }
 
-extern "C" gs_status gs_linear_attn_fwd(const gs_linear_attn* a, const gs_attn_heads* q, const gs_attn_heads* k,
-                                        const gs_attn_heads* v, const gs_attn_heads* out, float* state_out,
+extern "C" gs_status gs_linear_attn_fwd(const gs_linear_attn* a, const gs_attn_heads* heads, float* state_out,
                                         void* workspace, size_t ws_bytes, void* stream) {
-  if (!a || !shape_ok(a) || !aligned_or_none(a) || (!a->group_offsets && a->groups != 1)) return GS_ERR_INVALID_ARG;
+  if (!a || !heads || !shape_ok(a) || !aligned_or_none(a) || (!a->group_offsets && a->groups != 1)) return GS_ERR_INVALID_ARG;
   const Call c(a, false, state_out != nullptr);
   Side s[4] = {};
-  if (a->tokens > 0 && (!side(&s[0], a, q, a->dim, false, false) || !side(&s[1], a, k, a->dim, true, false) ||
-                        !side(&s[2], a, v, a->vdim, true, false) || !side(&s[3], a, out, a->vdim, false, true)))
+  if (a->tokens > 0 && (!side(&s[0], a, &heads[0], a->dim, false, false) || !side(&s[1], a, &heads[1], a->dim, true, false) ||
+                        !side(&s[2], a, &heads[2], a->vdim, true, false) || !side(&s[3], a, &heads[3], a->vdim, false, true)))
     return GS_ERR_INVALID_ARG;
   const Room room(workspace, a, c.slots, false, a->tokens > 0 ? to_copy(s, 3) : 0);
   if (!workspace || !aligned16(workspace) || ws_bytes < room.bytes) return GS_ERR_INVALID_ARG;
@@ -1411,19 +1410,17 @@ extern "C" gs_status gs_linear_attn_fwd(const gs_linear_attn* a, const gs_attn_h
                              : forward<__half>(a, c, s, state_out, room, st);
 }
 
-extern "C" gs_status gs_linear_attn_bwd(const gs_linear_attn* a, const gs_attn_heads* q, const gs_attn_heads* k,
-                                        const gs_attn_heads* v, const gs_attn_heads* dout,
-                                        const gs_attn_heads* dq, const gs_attn_heads* dk, const gs_attn_heads* dv,
+extern "C" gs_status gs_linear_attn_bwd(const gs_linear_attn* a, const gs_attn_heads* heads,
                                         const float* dstate_out, float* dstate, void* workspace, size_t ws_bytes,
                                         void* stream) {
-  if (!a || !shape_ok(a) || !aligned_or_none(a) || (!a->group_offsets && a->groups != 1)) return GS_ERR_INVALID_ARG;
+  if (!a || !heads || !shape_ok(a) || !aligned_or_none(a) || (!a->group_offsets && a->groups != 1)) return GS_ERR_INVALID_ARG;
   const Call c(a, true, dstate != nullptr);
   Side s[7] = {};
   if (a->tokens > 0 &&
-      (!side(&s[0], a, q, a->dim, false, false) || !side(&s[1], a, k, a->dim, true, false) ||
-       !side(&s[2], a, v, a->vdim, true, false) || !side(&s[3], a, dout, a->vdim, false, false) ||
-       !side(&s[4], a, dq, a->dim, false, true) || !side(&s[5], a, dk, a->dim, true, true) ||
-       !side(&s[6], a, dv, a->vdim, true, true)))
+      (!side(&s[0], a, &heads[0], a->dim, false, false) || !side(&s[1], a, &heads[1], a->dim, true, false) ||
+       !side(&s[2], a, &heads[2], a->vdim, true, false) || !side(&s[3], a, &heads[3], a->vdim, false, false) ||
+       !side(&s[4], a, &heads[4], a->dim, false, true) || !side(&s[5], a, &heads[5], a->dim, true, true) ||
+       !side(&s[6], a, &heads[6], a->vdim, true, true)))
     return GS_ERR_INVALID_ARG;
   const Room room(workspace, a, c.slots, true, a->tokens > 0 ? to_copy(s, 4) : 0);
   if (!workspace || !aligned16(workspace) || ws_bytes < room.bytes) return GS_ERR_INVALID_ARG;
@@ -1449,15 +1446,14 @@ extern "C" gs_status gs_linear_attn_status(void* stream) {
   return GS_ERR_TIMEOUT;
 }
 
-extern "C" gs_status gs_linear_attn_step(const gs_linear_attn* a, const gs_attn_heads* q, const gs_attn_heads* k,
-                                         const gs_attn_heads* v, const gs_attn_heads* out, float* state,
+extern "C" gs_status gs_linear_attn_step(const gs_linear_attn* a, const gs_attn_heads* heads, float* state,
                                          void* stream) {
-  if (!a || !shape_ok(a) || !aligned_or_none(a)) return GS_ERR_INVALID_ARG;
+  if (!a || !heads || !shape_ok(a) || !aligned_or_none(a)) return GS_ERR_INVALID_ARG;
   if (a->tokens == 0) return GS_OK;
   StepArgs p{};
-  if (!state || !aligned_to(state, 4) || !side(&p.q, a, q, a->dim, false, false) ||
-      !side(&p.k, a, k, a->dim, true, false) || !side(&p.v, a, v, a->vdim, true, false) ||
-      !side(&p.out, a, out, a->vdim, false, true))
+  if (!state || !aligned_to(state, 4) || !side(&p.q, a, &heads[0], a->dim, false, false) ||
+      !side(&p.k, a, &heads[1], a->dim, true, false) || !side(&p.v, a, &heads[2], a->vdim, true, false) ||
+      !side(&p.out, a, &heads[3], a->vdim, false, true))
     return GS_ERR_INVALID_ARG;
   p.heads = a->q_heads;
   p.rep = a->q_heads / a->k_heads;

@@ -48,9 +48,9 @@ def declare(L):
                              i32, i32, vp, sz, vp]
     L.gs_linear_attn_workspace_bytes.argtypes = [vp, i32]
     L.gs_linear_attn_workspace_bytes.restype = sz
-    L.gs_linear_attn_fwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, sz, vp]
-    L.gs_linear_attn_bwd.argtypes = [vp] * 11 + [sz, vp]
-    L.gs_linear_attn_step.argtypes = [vp] * 7
+    L.gs_linear_attn_fwd.argtypes = [vp, vp, vp, vp, sz, vp]
+    L.gs_linear_attn_bwd.argtypes = [vp, vp, vp, vp, vp, sz, vp]
+    L.gs_linear_attn_step.argtypes = [vp, vp, vp, vp]
     L.gs_linear_attn_status.argtypes = [vp]
 
 
@@ -63,7 +63,7 @@ _HEADS = struct.Struct("PPqqqqi4x")
 _CKPT = struct.Struct("PPqq")
 _NO_CKPT = _CKPT.pack(0, 0, 0, 0)
 _ATTN = struct.Struct("qiiiiiifPPP")
-_ATTN_HEADS = struct.Struct("Pqq")
+_ATTN_HEADS4, _ATTN_HEADS7 = struct.Struct("Pqq" * 4), struct.Struct("Pqq" * 7)
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 
@@ -476,41 +476,58 @@ def gs_ffn_bwd(x, w, dh, dx, dw, workspace, act="silu", accumulate=False, stream
 # linear attention
 
 
-def _attn(q, k, v, log_decay, group_offsets, state, scale):
-    """Checks what every call has: (the packed gs_linear_attn, q's, k's and v's packed
-    heads, shape of the outputs, shape of the states, q's device)."""
+def _attn(q, k, v, out, name, log_decay, group_offsets, state, scale):
+    """Checks what every call has: (the packed gs_linear_attn, pointers and strides of q, k,
+    v and out, shape of the states, device)."""
     try:
-        code = DTYPES[q.dtype]
+        dt, device = q.dtype, q.get_device()
         tokens, hq, dim = q.shape
-        hk, vdim = k.shape[1], v.shape[2]
-    except (AttributeError, KeyError, ValueError, IndexError, TypeError):
-        raise ValueError("q, k and v must be CUDA [tokens, heads, dim] tensors of bfloat16 or float16") from None
-    if code == 2:
-        raise ValueError("q must be bfloat16 or float16")
+        tk, hk, dk = k.shape
+        tv, hv, vdim = v.shape
+        (qa, qb, q1), (ka, kb, k1), (va, vb, v1), (oa, ob, o1) = q.stride(), k.stride(), v.stride(), out.stride()
+        if ((dt is torch.bfloat16 or dt is torch.float16) and k.dtype is dt and v.dtype is dt and out.dtype is dt
+                and tk == tokens == tv and dk == dim and hk == hv and hk and hq and not hq % hk
+                and out.shape == (tokens, hq, vdim)
+                and device == k.get_device() == v.get_device() == out.get_device() >= 0
+                and ((q1 == k1 == v1 == o1 == 1) or not tokens
+                     or ((q1 == k1 == 1 or dim == 1) and (v1 == o1 == 1 or vdim == 1)))):
+            groups = 1 if group_offsets is None else group_offsets.numel() - 1
+            if groups < 1:
+                raise ValueError("group_offsets must have groups + 1 entries")
+            states = (groups, hq, dim, vdim)
+            return (_ATTN.pack(tokens, hq, hk, dim, vdim, groups, DTYPES[dt], dim ** -0.5 if scale is None else scale,
+                               _entries(log_decay, "log_decay", (hq,), torch.float32, device),
+                               0 if group_offsets is None else
+                               _entries(group_offsets, "group_offsets", (groups + 1,), torch.int32, device),
+                               0 if state is None else _entries(state, "state", states, torch.float32, device)),
+                    (q.data_ptr(), qa, qb, k.data_ptr(), ka, kb, v.data_ptr(), va, vb, out.data_ptr(), oa, ob),
+                    states, device)
+    except (AttributeError, TypeError):
+        pass
+    except ValueError as e:
+        if "unpack" not in str(e):
+            raise
+    # something is wrong: say what
+    for t, n in ((q, "q"), (k, "k"), (v, "v")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 3 or not t.is_cuda or DTYPES.get(t.dtype, 2) == 2:
+            raise ValueError("%s must be a CUDA [tokens, heads, dim] tensor of bfloat16 or float16" % n)
+    tokens, hq, dim = q.shape
+    hk, vdim = k.shape[1], v.shape[2]
     if not hk or not hq or hq % hk:
         raise ValueError("%d query heads do not share %d key heads evenly" % (hq, hk))
-    device, groups, offsets = q.get_device(), 1, 0
-    if group_offsets is not None:
-        groups = group_offsets.numel() - 1
-        if groups < 1:
-            raise ValueError("group_offsets must have groups + 1 entries")
-        offsets = _entries(group_offsets, "group_offsets", (groups + 1,), torch.int32, device)
-    states = (groups, hq, dim, vdim)
-    packed = _ATTN.pack(tokens, hq, hk, dim, vdim, groups, code, dim ** -0.5 if scale is None else scale,
-                        _entries(log_decay, "log_decay", (hq,), torch.float32, device), offsets,
-                        0 if state is None else _entries(state, "state", states, torch.float32, device))
-    dt = q.dtype
-    return (packed, _attn_heads(q, "q", (tokens, hq, dim), dt, device),
-            _attn_heads(k, "k", (tokens, hk, dim), dt, device),
-            _attn_heads(v, "v", (tokens, hk, vdim), dt, device), (tokens, hq, vdim), states, device)
+    for t, n, shape in ((q, "q", (tokens, hq, dim)), (k, "k", (tokens, hk, dim)), (v, "v", (tokens, hk, vdim)),
+                        (out, name, (tokens, hq, vdim))):
+        _attn_heads(t, n, shape, q.dtype, q.get_device())
+    raise ValueError("q, k, v, %s: not as documented" % name)
 
 
 def _attn_heads(t, name, shape, dtype, device):
+    """(pointer, stride between tokens, between heads)."""
     try:
         a, b, c = t.stride()
         if (t.shape == shape and t.dtype is dtype and t.get_device() == device >= 0
-                and (c == 1 or shape[2] == 1 or not t.numel())):
-            return _ATTN_HEADS.pack(t.data_ptr(), a, b)
+                and (c == 1 or shape[2] == 1 or not shape[0])):
+            return t.data_ptr(), a, b
     except (AttributeError, ValueError, TypeError):
         pass
     if getattr(t, "shape", None) == shape and t.dtype is dtype and t.is_cuda:
@@ -523,7 +540,7 @@ def _attn_heads(t, name, shape, dtype, device):
 def _entries(t, name, shape, dtype, device):
     """The pointer of a contiguous tensor of that shape; 0 for None."""
     try:
-        if t.shape == shape and t.dtype is dtype and t.get_device() == device >= 0 and t.is_contiguous():
+        if t.shape == shape and t.dtype is dtype and t.get_device() == device and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
         if t is None:
@@ -545,9 +562,9 @@ def gs_linear_attn_fwd(q, k, v, log_decay, out, group_offsets=None, state=None, 
     [q_heads], 0 or less.  Groups of tokens (group_offsets int32 [groups + 1]; None: one)
     each go from their state to state_out, float32 [groups, q_heads, dim, vdim] (None: zeros;
     not wanted).  workspace: uint8, gs_linear_attn_workspace_bytes() bytes."""
-    a, qh, kh, vh, shape, states, device = _attn(q, k, v, log_decay, group_offsets, state, scale)
+    a, heads, states, device = _attn(q, k, v, out, "out", log_decay, group_offsets, state, scale)
     status = lib().gs_linear_attn_fwd(
-        a, qh, kh, vh, _attn_heads(out, "out", shape, q.dtype, device),
+        a, _ATTN_HEADS4.pack(*heads),
         0 if state_out is None else _entries(state_out, "state_out", states, torch.float32, device),
         *_workspace(workspace, device), _stream(stream, q))
     if status:
@@ -558,11 +575,11 @@ def gs_linear_attn_bwd(q, k, v, log_decay, dout, dq, dk, dv, group_offsets=None,
                        dstate=None, scale=None, workspace=None, stream=None):
     """Backward of gs_linear_attn_fwd from its inputs, dout and (None: zeros) the gradient of
     its last states: dq, dk, dv and, where given, dstate, the gradient of the first states."""
-    a, qh, kh, vh, shape, states, device = _attn(q, k, v, log_decay, group_offsets, state, scale)
+    a, heads, states, device = _attn(q, k, v, dout, "dout", log_decay, group_offsets, state, scale)
     dt, f32 = q.dtype, torch.float32
     _check("gs_linear_attn_bwd", lib().gs_linear_attn_bwd(
-        a, qh, kh, vh, _attn_heads(dout, "dout", shape, dt, device), _attn_heads(dq, "dq", q.shape, dt, device),
-        _attn_heads(dk, "dk", k.shape, dt, device), _attn_heads(dv, "dv", v.shape, dt, device),
+        a, _ATTN_HEADS7.pack(*heads, *_attn_heads(dq, "dq", q.shape, dt, device),
+                             *_attn_heads(dk, "dk", k.shape, dt, device), *_attn_heads(dv, "dv", v.shape, dt, device)),
         _entries(dstate_out, "dstate_out", states, f32, device), _entries(dstate, "dstate", states, f32, device),
         *_workspace(workspace, device), _stream(stream, q)))
 
@@ -570,10 +587,10 @@ def gs_linear_attn_bwd(q, k, v, log_decay, dout, dq, dk, dv, group_offsets=None,
 def gs_linear_attn_step(q, k, v, log_decay, state, out, scale=None, stream=None):
     """One token of each of q.shape[0] streams: updates state, float32 [streams, q_heads, dim,
     vdim], in place and writes out [streams, q_heads, vdim]."""
-    a, qh, kh, vh, shape, states, device = _attn(q, k, v, log_decay, None, None, scale)
+    a, heads, states, device = _attn(q, k, v, out, "out", log_decay, None, None, scale)
     status = lib().gs_linear_attn_step(
-        a, qh, kh, vh, _attn_heads(out, "out", shape, q.dtype, device),
-        _entries(state, "state", (shape[0],) + states[1:], torch.float32, device), _stream(stream, q))
+        a, _ATTN_HEADS4.pack(*heads),
+        _entries(state, "state", (q.shape[0],) + states[1:], torch.float32, device), _stream(stream, q))
     if status:
         _check("gs_linear_attn_step", status)
 

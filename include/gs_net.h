@@ -293,41 +293,39 @@ typedef struct gs_attn_heads {   /* [tokens][heads][channels]                 */
 } gs_attn_heads;
 
 /* gs_linear_attn_fwd -- all tokens of the groups, in chunks.
+ *   heads       (host) four: q, k, v, out; out may not overlap the inputs
  *   state_out   [groups][q_heads][dim][vdim] fp32: the states after the
  *               groups' last tokens (a group's own state where it has none),
  *               or NULL; may equal state
- *   workspace   gs_linear_attn_workspace_bytes(a, backward) bytes, 16-byte
- *               aligned, no initialisation; calls on one workspace must not
- *               overlap */
+ *   workspace   at most gs_linear_attn_workspace_bytes(a, backward) bytes (0:
+ *               refused; rows of q, k, v and dout that do not start on 16-byte
+ *               boundaries, or are no multiple of 8 long, are copied there
+ *               first), 16-byte aligned, no initialisation; calls on one
+ *               workspace must not overlap */
 size_t gs_linear_attn_workspace_bytes(const gs_linear_attn* a, int32_t backward);
-gs_status gs_linear_attn_fwd(const gs_linear_attn* a, const gs_attn_heads* q,
-                             const gs_attn_heads* k, const gs_attn_heads* v,
-                             const gs_attn_heads* out, float* state_out, void* workspace,
-                             size_t ws_bytes, void* stream);
+gs_status gs_linear_attn_fwd(const gs_linear_attn* a, const gs_attn_heads* heads,
+                             float* state_out, void* workspace, size_t ws_bytes, void* stream);
 
-/* gs_linear_attn_bwd -- from the gradients of the outputs and (dstate_out, or
- * NULL: 0) of the last states: dq, dk, dv (summed over the query heads that
- * share a key head) and dstate, the gradient of the first states (or NULL; may
- * equal dstate_out).  The decays get no gradient. */
-gs_status gs_linear_attn_bwd(const gs_linear_attn* a, const gs_attn_heads* q,
-                             const gs_attn_heads* k, const gs_attn_heads* v,
-                             const gs_attn_heads* dout, const gs_attn_heads* dq,
-                             const gs_attn_heads* dk, const gs_attn_heads* dv,
+/* gs_linear_attn_bwd -- heads (host): q, k, v, dout, dq, dk, dv.  From the
+ * gradients of the outputs and (dstate_out, or NULL: 0) of the last states: dq,
+ * dk, dv (summed over the query heads that share a key head) and dstate, the
+ * gradient of the first states (or NULL; may equal dstate_out).  The decays get
+ * no gradient. */
+gs_status gs_linear_attn_bwd(const gs_linear_attn* a, const gs_attn_heads* heads,
                              const float* dstate_out, float* dstate, void* workspace,
                              size_t ws_bytes, void* stream);
 
-/* Every wait of these kernels for the tensor cores is bounded (two seconds a
- * block, after which results are undefined).  gs_linear_attn_status
+/* gs_linear_attn_step -- one token of each of a->tokens streams; heads (host):
+ * q, k, v, out; state [tokens][q_heads][dim][vdim] fp32, read and updated in
+ * place.  a->state and a->group_offsets are not used. */
+gs_status gs_linear_attn_step(const gs_linear_attn* a, const gs_attn_heads* heads, float* state,
+                              void* stream);
+
+/* Every wait of the chunked kernels for the tensor cores is bounded (two seconds
+ * a block, after which results are undefined).  gs_linear_attn_status
  * synchronises the stream and returns GS_ERR_TIMEOUT if one ran out on the
  * current device since the last such call. */
 gs_status gs_linear_attn_status(void* stream);
-
-/* gs_linear_attn_step -- one token of each of a->tokens streams: state
- * [tokens][q_heads][dim][vdim] fp32, read and updated in place; a->state,
- * a->groups and a->group_offsets are not used (groups: 1). */
-gs_status gs_linear_attn_step(const gs_linear_attn* a, const gs_attn_heads* q,
-                              const gs_attn_heads* k, const gs_attn_heads* v,
-                              const gs_attn_heads* out, float* state, void* stream);
 
 #ifdef __cplusplus
 }
