@@ -15,9 +15,16 @@ passes over all tokens in between is the library's:
   gs_act8_wgrad           every weight gradient, from the 8-bit checkpoints
 
 so that between the two directions a block keeps bytes, not 16-bit activations
-(the residual stream and the block outputs stay as they are).
+(the residual stream and the block outputs stay as they are).  Two more take the
+place of torch products:
 
-  python examples/predict_gaussians.py [--steps 20]
+  gs_linear_attn_fwd/bwd  (--linear) linear attention over all views' tokens as one
+                          stream, a decay for each head, instead of the softmax
+                          over every pair of tokens
+  gs_ffn_fwd/bwd          (--fused) the gated unit with its input projection in one
+                          kernel, which keeps nothing but its input
+
+  python examples/predict_gaussians.py [--steps 20] [--linear] [--fused]
 """
 import argparse
 import os
@@ -43,7 +50,7 @@ class Kept:
 class Network:
     """width = heads * 64; `groups`: the views, each with its own gates."""
 
-    def __init__(self, views, rows, cols, width=256, blocks=2, per_token=2, seed=0):
+    def __init__(self, views, rows, cols, width=256, blocks=2, per_token=2, seed=0, linear=False, fused=False):
         g = torch.Generator(device="cuda").manual_seed(seed)
         self.T, self.C, self.F, self.V = views * rows * cols, width, 2 * width, views
         self.H, self.blocks, self.per_token = width // 64, blocks, per_token
@@ -72,6 +79,13 @@ class Network:
         room = max(gs.gs_act8_wgrad_workspace_bytes(self.T, w.shape[0], w.shape[1], dt)
                    for w in self.w.values() if w.dim() == 2 for dt in (DT, torch.float32))
         self.wgrad_ws = torch.zeros(room, dtype=torch.uint8, device="cuda")
+        self.linear, self.fused = linear, fused
+        if linear:
+            self.log_decay = -torch.exp2(-8.0 * torch.arange(1, self.H + 1, device="cuda") / self.H)
+            self.attn_ws = torch.empty(gs.gs_linear_attn_workspace_bytes(self.T, self.H, self.H, 64, 64),
+                                       dtype=torch.uint8, device="cuda")
+        if fused:
+            self.ffn_ws = torch.zeros(gs.gs_ffn_workspace_bytes(self.T, C, F), dtype=torch.uint8, device="cuda")
 
     # ---- pieces ------------------------------------------------------------
     def _mat(self, c, dt=DT):
@@ -124,6 +138,17 @@ class Network:
                              workspace=self.norm_ws)
         return dxi, db
 
+    def _attend_linear(self, qkv):
+        out = torch.empty_like(qkv[:, 0])
+        gs.gs_linear_attn_fwd(*qkv.unbind(1), self.log_decay, out, workspace=self.attn_ws)
+        return out.flatten(1)
+
+    def _attend_linear_back(self, qkv, da):
+        dqkv = torch.empty_like(qkv)
+        gs.gs_linear_attn_bwd(*qkv.unbind(1), self.log_decay, da.view(self.T, self.H, 64), *dqkv.unbind(1),
+                              workspace=self.attn_ws)
+        return dqkv
+
     @staticmethod
     def _attend(qkv):
         q, k, v = (t.transpose(0, 1) for t in qkv.unbind(1))  # [heads, tokens, 64]
@@ -142,16 +167,23 @@ class Network:
             self.saved.append(s)
             qkv = self._linear(y, "qkv%d" % b).view(T, 3, H, 64)
             gs.gs_rope(self.rope, self.positions, qkv[:, 0], qkv[:, 1])
-            a = self._attend(qkv)
+            a = self._attend_linear(qkv) if self.linear else self._attend(qkv)
             kept = Kept(T, self.C)
             gs.gs_act8_encode(a, kept.q, kept.e)
             self.saved.append((qkv, kept))
             x, y, s = self._join(x, self._linear(a, "out%d" % b), 2 * b + 1)
             self.saved.append(s)
-            gu, h = self._linear(y, "up%d" % b), self._mat(self.F)
-            g8, u8 = Kept(T, self.F), Kept(T, self.F)
-            gs.gs_glu_fwd(gu[:, :self.F], gu[:, self.F:], h, g8.q, g8.e, u8.q, u8.e)
-            self.saved.append((g8, u8))
+            h = self._mat(self.F)
+            if self.fused:
+                gs.gs_ffn_fwd(y, self.w["up%d" % b].to(DT), h, self.ffn_ws)
+                h8 = Kept(T, self.F)
+                gs.gs_act8_encode(h, h8.q, h8.e)
+                self.saved.append((y, h8))
+            else:
+                gu = self._linear(y, "up%d" % b)
+                g8, u8 = Kept(T, self.F), Kept(T, self.F)
+                gs.gs_glu_fwd(gu[:, :self.F], gu[:, self.F:], h, g8.q, g8.e, u8.q, u8.e)
+                self.saved.append((g8, u8))
             x, y, s = self._join(x, self._linear(h, "down%d" % b), 2 * b + 2)
         self.saved.append(s)
         return self._linear(y, "head").float()
@@ -164,19 +196,30 @@ class Network:
         dx = None
         for b in reversed(range(self.blocks)):
             dx, db = self._join_back(dx, dy, s, 2 * b + 2, grads)
-            g8, u8 = saved.pop()
-            h8, dgu = Kept(T, self.F), self._mat(2 * self.F)
-            gs.gs_glu_bwd(g8.q, g8.e, u8.q, u8.e, db @ self.w["down%d" % b].to(DT),
-                          dgu[:, :self.F], dgu[:, self.F:], h8.q, h8.e)
-            self._linear_back(db, h8, "down%d" % b, grads, need_dx=False)
-            s = saved.pop()
-            dy = self._linear_back(dgu, s[3], "up%d" % b, grads)
+            dh = db @ self.w["down%d" % b].to(DT)
+            if self.fused:
+                y, h8 = saved.pop()
+                up, dy = self.w["up%d" % b], self._mat(self.C)
+                grads["up%d" % b] = torch.empty_like(up)
+                gs.gs_ffn_bwd(y, up.to(DT), dh, dy, grads["up%d" % b], self.ffn_ws)
+                self._linear_back(db, h8, "down%d" % b, grads, need_dx=False)
+                s = saved.pop()
+            else:
+                g8, u8 = saved.pop()
+                h8, dgu = Kept(T, self.F), self._mat(2 * self.F)
+                gs.gs_glu_bwd(g8.q, g8.e, u8.q, u8.e, dh, dgu[:, :self.F], dgu[:, self.F:], h8.q, h8.e)
+                self._linear_back(db, h8, "down%d" % b, grads, need_dx=False)
+                s = saved.pop()
+                dy = self._linear_back(dgu, s[3], "up%d" % b, grads)
             dx, db = self._join_back(dx, dy, s, 2 * b + 1, grads)
             qkv, kept = saved.pop()
             da = self._linear_back(db, kept, "out%d" % b, grads)
-            qkv = qkv.detach().requires_grad_(True)
-            with torch.enable_grad():
-                dqkv, = torch.autograd.grad(self._attend(qkv), qkv, da)
+            if self.linear:
+                dqkv = self._attend_linear_back(qkv, da)
+            else:
+                qkv = qkv.detach().requires_grad_(True)
+                with torch.enable_grad():
+                    dqkv, = torch.autograd.grad(self._attend(qkv), qkv, da)
             gs.gs_rope(self.rope, self.positions, dqkv[:, 0], dqkv[:, 1], inverse=True)
             s = saved.pop()
             dy = self._linear_back(dqkv.reshape(T, 3 * self.C), s[3], "qkv%d" % b, grads)
@@ -248,14 +291,19 @@ def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--steps", type=int, default=20)
     ap.add_argument("--size", type=int, default=256)
+    ap.add_argument("--linear", action="store_true", help="linear attention with decays")
+    ap.add_argument("--fused", action="store_true", help="the gated unit with its projection in one kernel")
     a = ap.parse_args()
     cams = [scenes.camera(np.eye(3), [-0.2 * v, 0, 0], a.size, a.size, a.size / 2, a.size / 2, a.size, a.size)
             for v in range(2)]
-    tr = Trainer(smooth_images(len(cams), a.size), cams)
+    tr = Trainer(smooth_images(len(cams), a.size), cams, linear=a.linear, fused=a.fused)
     for i in range(a.steps):
         loss = tr.step()
         print("step %d  loss %.5f" % (i, loss.item()))
     assert gs.gs_workspace_status(tr.net.wgrad_ws) == gs.GS_OK
+    if a.fused:
+        assert gs.gs_workspace_status(tr.net.ffn_ws) == gs.GS_OK
+    gs.gs_linear_attn_status()
 
 
 if __name__ == "__main__":
