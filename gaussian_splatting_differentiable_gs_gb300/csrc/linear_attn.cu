@@ -450,6 +450,7 @@ struct Part {
   Side key, value;
   float mul;
   int32_t back, shift;  // tokens from the last to the first
+  int32_t exact;        // its last states are handed on
   float* to;            // [slots][heads][Dp][Ep]
 };
 struct PartsArgs {
@@ -457,24 +458,19 @@ struct PartsArgs {
   int32_t heads, rep;
   int32_t Dp, Ep;  // channels, rounded up to 64
   const float* log_decay;
-  Part part;
+  Part part[2];
 };
 
 template <int KD, int TERMS>
-constexpr int kPartsSmem = 2 * (KD / 64 + 1) * kBlock + TERMS * (KD / 64) * kBlock + 1024;
+constexpr int kPartsSmem = 1024 + 2 * (KD / 64 + 1) * kBlock + TERMS * (KD / 64) * kBlock;
 
 template <typename T, int KD, int TERMS>
-__global__ void __launch_bounds__(kThreads, 128 / KD) attn_parts_kernel(const __grid_constant__ PartsArgs p) {
-  extern __shared__ __align__(1024) uint8_t smem[];
+__device__ __forceinline__ void sum_part(const PartsArgs& p, const Part& part, int e0, Control* c, uint32_t tiles,
+                                         uint32_t tmem) {
   constexpr bool kHalfType = std::is_same<T, __half>::value;
   constexpr uint32_t kSet = (KD / 64 + 1) * kBlock;  // keys, values
-  const uint32_t tiles = smem_u32(smem), terms = tiles + 2 * kSet;
-  Control* c = (Control*)(smem + 2 * kSet + TERMS * (KD / 64) * kBlock);
-  const uint32_t tmem = begin<64>(c);
-  launch_dependents();
-  wait_for_previous();
-  const int h = blockIdx.y, e0 = blockIdx.z * kV, warp = threadIdx.x >> 5;
-  const Part& part = p.part;
+  const uint32_t terms = tiles + 2 * kSet;
+  const int h = blockIdx.y, warp = threadIdx.x >> 5;
   const Span s = span_of(p.split, blockIdx.x);
   const float a = log2_decay(p.log_decay, h);
   const int64_t from = part.back ? s.start + s.n - 1 : s.start;
@@ -535,8 +531,23 @@ __global__ void __launch_bounds__(kThreads, 128 / KD) attn_parts_kernel(const __
     st.update(tmem, power2(a * (float)min(kL, s.n - i * kL)), back);
   }
   if (s.n) st.put(part.to + ((int64_t)blockIdx.x * p.heads + h) * p.Dp * p.Ep + e0, p.Ep);
+}
+
+// TERMS: the most that a part's keys are taken as.
+template <typename T, int KD, int TERMS>
+__global__ void __launch_bounds__(kThreads, 128 / KD) attn_parts_kernel(const __grid_constant__ PartsArgs p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Control* c = (Control*)smem;
+  const uint32_t tmem = begin<64>(c);
+  launch_dependents();
+  wait_for_previous();
+  const int blocks = p.Ep / kV, e0 = blockIdx.z % blocks * kV;
+  const Part& part = p.part[blockIdx.z / blocks];
+  if (TERMS == 2 || !part.exact) sum_part<T, KD, 2>(p, part, e0, c, smem_u32(smem) + 1024, tmem);
+  else sum_part<T, KD, TERMS>(p, part, e0, c, smem_u32(smem) + 1024, tmem);
   end<64>(tmem);
 }
+
 
 // ---- the states at the segments' starts, in place of their parts ---------------
 struct Scan {
@@ -779,11 +790,11 @@ struct OutArgs {
 template <int KD>
 constexpr int kOutSets = KD == 64 ? 2 : 1;
 template <int KD>
-constexpr int kOutSmem = kOutSets<KD> * (2 * (KD / 64) + 1) * kBlock + KD * 128 + 1024;
+constexpr int kOutSmem = 1024 + kOutSets<KD> * (2 * (KD / 64) + 1) * kBlock + KD * 128;
 
 template <typename T, int KD>
-__global__ void __launch_bounds__(kThreads, 2) attn_out_kernel(const __grid_constant__ OutArgs p) {
-  extern __shared__ __align__(1024) uint8_t smem[];
+__device__ __forceinline__ void form_outputs(const OutArgs& p, int slot, int y, int e0, Control* c, uint32_t tiles,
+                                             uint32_t tmem) {
   constexpr uint32_t kKeys = KD / 64 * kBlock;
   // The weighted keys' terms take the places of the keys and of the queries when these have
   // been multiplied, the outputs leave through the keys'.  Up to 64 channels there is room
@@ -791,19 +802,15 @@ __global__ void __launch_bounds__(kThreads, 2) attn_out_kernel(const __grid_cons
   // (32640 tokens, 16 heads of 64: 59 us, with a set and a half 58, one 65); with 128 one
   // set leaves room for two blocks an SM instead.
   constexpr uint32_t kSets = kOutSets<KD>, kSet = 2 * kKeys + kBlock;  // queries, keys, values
-  const uint32_t tiles = smem_u32(smem), state = tiles + kSets * kSet;
-  Control* c = (Control*)(smem + kSets * kSet + KD * 128);
-  const uint32_t tmem = begin<256>(c);
-  launch_dependents();
-  wait_for_previous();
-  const Span s = span_of(p.split, blockIdx.x);
+  const uint32_t state = tiles + kSets * kSet;
+  const Span s = span_of(p.split, slot);
   const int64_t from = p.back ? s.start + s.n - 1 : s.start, step = p.back ? -1 : 1;
-  const int chunks = (s.n + kL - 1) / kL, e0 = blockIdx.z * kV, reps = p.shared ? p.rep : 1;
+  const int chunks = (s.n + kL - 1) / kL, reps = p.shared ? p.rep : 1;
   const int row = ((int)threadIdx.x >> 5 & 3) * 32 + ((int)threadIdx.x & 31);
   uint32_t phase = 0;
 
   for (int r = 0; r < (s.n ? reps : 0); ++r) {
-    const int h = p.shared ? blockIdx.y * p.rep + r : blockIdx.y;
+    const int h = p.shared ? y * p.rep + r : y;
     const float a = log2_decay(p.log_decay, h);
     const T* q = head_at<T>(p.query, h, p.rep, from);
     const T* k = head_at<T>(p.key, h, p.rep, from);
@@ -820,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_out_kernel(const __grid_cons
     load(0);
     if (threadIdx.x < 64) c->decay[threadIdx.x] = threadIdx.x < 32 ? p.mul_inner * power2(a * (float)(31 - (int)threadIdx.x)) : 0.f;
     State<KD> st;
-    const Stored src = stored(p.states, p.edge, p.Kp, p.Vp, p.K, p.V, p.transposed, (int64_t)blockIdx.x * p.heads + h,
+    const Stored src = stored(p.states, p.edge, p.Kp, p.Vp, p.K, p.V, p.transposed, (int64_t)slot * p.heads + h,
                               (int64_t)s.group * p.heads + h);
     st.get(src.p, src.rs, src.cs, e0, p.K, p.V);
     const float top_weight = p.mul_key * power2(a * (float)p.shift);
@@ -859,9 +866,9 @@ __global__ void __launch_bounds__(kThreads, 2) attn_out_kernel(const __grid_cons
       if (more) st.update(tmem + kUpdate, power2(a * (float)n), fit.key_back);
       const int64_t tok = from + step * i * kL;
       const int64_t key_heads = p.heads / p.rep;
-      const Output out{(T*)p.out.p + (int64_t)blockIdx.y * p.out.head + tok * p.out.token + e0, step * p.out.token,
+      const Output out{(T*)p.out.p + (int64_t)y * p.out.head + tok * p.out.token + e0, step * p.out.token,
                        p.out.dim - e0, p.out.wide,
-                       reps > 1 ? p.sums + (tok * key_heads + blockIdx.y) * p.Vp + e0 : nullptr,
+                       reps > 1 ? p.sums + (tok * key_heads + y) * p.Vp + e0 : nullptr,
                        step * key_heads * p.Vp, r == 0, r + 1 == reps};
       // (rows before the chunk's first token are not there)
       put_outputs<T>(tmem, keys, p.mul_state * fit.state_back * power2(a * (float)max(row + 1 - p.shift - pad, 0)), out,
@@ -873,6 +880,16 @@ __global__ void __launch_bounds__(kThreads, 2) attn_out_kernel(const __grid_cons
     }
     __syncthreads();  // the next head's loads and decays follow
   }
+}
+
+template <typename T, int KD>
+__global__ void __launch_bounds__(kThreads, 2) attn_out_kernel(const __grid_constant__ OutArgs p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Control* c = (Control*)smem;
+  const uint32_t tmem = begin<256>(c);
+  launch_dependents();
+  wait_for_previous();
+  form_outputs<T, KD>(p, blockIdx.x, blockIdx.y, blockIdx.z * kV, c, smem_u32(smem) + 1024, tmem);
   end<256>(tmem);
 }
 
@@ -891,26 +908,21 @@ struct KvArgs {
   float scale;
   float* sums[2];       // [tokens][key heads][64], where rep > 1: of dk, of dv
 };
-constexpr int kKvSmem = 6 * kBlock + 64 * 128 + 1024;  // keys and queries twice, values, douts; the state
+constexpr int kKvSmem = 1024 + 6 * kBlock + 64 * 128;  // keys and queries twice, values, douts; the state
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) attn_kv_kernel(const __grid_constant__ KvArgs p) {
-  extern __shared__ __align__(1024) uint8_t smem[];
+__device__ __forceinline__ void form_kv(const KvArgs& p, int slot, int y, Control* c, uint32_t tiles, uint32_t tmem) {
   // Keys and queries in two pairs of tiles in turn: the next chunk's come while this one is
   // worked on, its values and douts while its first scores are.  The weighted queries'
   // terms take the places of keys and values when these have been multiplied.
-  const uint32_t pairs = smem_u32(smem), values = pairs + 4 * kBlock, douts = values + kBlock, state = douts + kBlock;
-  Control* c = (Control*)(smem + 6 * kBlock + 64 * 128);
-  const uint32_t tmem = begin<256>(c);
-  launch_dependents();
-  wait_for_previous();
-  const Span s = span_of(p.split, blockIdx.x);
+  const uint32_t pairs = tiles, values = pairs + 4 * kBlock, douts = values + kBlock, state = douts + kBlock;
+  const Span s = span_of(p.split, slot);
   const int64_t from = s.start + s.n - 1, key_heads = p.heads / p.rep;
   const int chunks = (s.n + kL - 1) / kL;
   const int row = ((int)threadIdx.x >> 5 & 3) * 32 + ((int)threadIdx.x & 31);
 
   for (int r = 0; r < (s.n ? p.rep : 0); ++r) {
-    const int h = blockIdx.y * p.rep + r;
+    const int h = y * p.rep + r;
     const float a = log2_decay(p.log_decay, h);
     auto load_pair = [&](int i) {
       const int n = min(kL, s.n - i * kL);
@@ -931,7 +943,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv_kernel(const __grid_const
     load_others(0);
     if (threadIdx.x < 64) c->decay[threadIdx.x] = threadIdx.x < 32 ? p.scale * power2(a * (float)(31 - (int)threadIdx.x)) : 0.f;
     State<64> st;
-    const Stored src = stored(p.states, p.edge, 64, 64, p.D, p.E, 0, (int64_t)blockIdx.x * p.heads + h,
+    const Stored src = stored(p.states, p.edge, 64, 64, p.D, p.E, 0, (int64_t)slot * p.heads + h,
                               (int64_t)s.group * p.heads + h);
     st.get(src.p, src.rs, src.cs, 0, p.D, p.E);
     const float top_weight = p.scale * power2(a);
@@ -979,7 +991,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv_kernel(const __grid_const
         after_sync();
         const Side& side = ph ? p.dk : p.dv;
         const Output out{head_at<T>(side, h, p.rep, tok), -side.token, side.dim, side.wide,
-                         sums ? p.sums[1 - ph] + (tok * key_heads + blockIdx.y) * 64 : nullptr, -key_heads * 64, r == 0,
+                         sums ? p.sums[1 - ph] + (tok * key_heads + y) * 64 : nullptr, -key_heads * 64, r == 0,
                          r + 1 == p.rep};
         // dv through the keys' tile, which nothing uses any more, dk through the values'
         if (ph == 1 && more) st.update(tmem + kUpdate, power2(a * (float)n), fit.key_back);
@@ -989,6 +1001,43 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv_kernel(const __grid_const
       }
       if (more) load_others(i + 1);
     }
+  }
+}
+
+// ---- all gradients in one launch ------------------------------------------------------
+// Two or three kinds of blocks, the ones that take longest first: an SM's two blocks are
+// then of different kinds, and few are left alone at the end (5003 tokens in 7 groups, heads
+// of 72 and 41: 91 us in three launches, 59 in one).  ED, EE: dim and vdim, padded.
+struct GradArgs {
+  int32_t slots, q_heads, k_heads;
+  int32_t first, second;  // where the blocks of a kind end
+  OutArgs dq, dk, dv;
+  KvArgs both;            // dk and dv of heads of up to 64 channels
+};
+template <int ED, int EE>
+constexpr int kGradSmem = ED == 64 && EE == 64 ? (kKvSmem > kOutSmem<64> ? kKvSmem : kOutSmem<64>)
+                                               : (kOutSmem<64> > kOutSmem<128> ? kOutSmem<64> : kOutSmem<128>);
+
+template <typename T, int ED, int EE>
+__global__ void __launch_bounds__(kThreads, 2) attn_grad_kernel(const __grid_constant__ GradArgs p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Control* c = (Control*)smem;
+  const uint32_t tmem = begin<256>(c), tiles = smem_u32(smem) + 1024;
+  launch_dependents();
+  wait_for_previous();
+  const int b = blockIdx.x;
+  if (b < p.first) {
+    const int at = b / p.slots, y = at % p.k_heads;
+    if constexpr (ED == 64 && EE == 64) form_kv<T>(p.both, b % p.slots, y, c, tiles, tmem);
+    else form_outputs<T, EE>(p.dk, b % p.slots, y, at / p.k_heads * kV, c, tiles, tmem);
+  } else if (b < p.second) {
+    if constexpr (ED != 64 || EE != 64) {
+      const int at = (b - p.first) / p.slots;
+      form_outputs<T, ED>(p.dv, (b - p.first) % p.slots, at % p.k_heads, at / p.k_heads * kV, c, tiles, tmem);
+    }
+  } else {
+    const int at = (b - p.second) / p.slots;
+    form_outputs<T, EE>(p.dq, (b - p.second) % p.slots, at % p.q_heads, at / p.q_heads * kV, c, tiles, tmem);
   }
   end<256>(tmem);
 }
@@ -1088,13 +1137,15 @@ constexpr int64_t kMaxTokens = ((int64_t)1 << 31) - 1;
 
 int padded_dim(int32_t dim) { return dim <= 64 ? 64 : 128; }
 
-// Tokens of a segment.  The kernels run in waves of as many blocks as the SMs hold (two
-// each), and a wave takes as long as a segment: about a chunk's time for each of its chunks
-// and one more for its state.  A chunk of the outputs or of the queries' gradients costs
-// two units, of the states' sums one, of the keys' and values' gradients four for each query
-// head of a key head; the sums' and the scan's start costs six.  Where a group is one
-// segment and its last state is not wanted, there are neither.  The groups' lengths are on
-// the device: they are taken as equal, and a lone segment as long as two of them.
+// Tokens of a segment.  A chunk of the outputs or of the queries' gradients costs two units
+// of time, of the states' sums one, of the keys' and values' gradients four for each query
+// head of a key head; each segment costs one chunk more for its start and its state.  With
+// two blocks an SM, blocks of one kind run in waves; of several kinds about as long as their
+// work takes and half of the longest.  The sums' and the scan's start costs six; where a
+// group is one segment and its last state is not wanted, there are neither.  The groups'
+// lengths are on the device: they are taken as equal, and a lone segment as long as two of
+// them.  (Backward, 32640 tokens, 16 heads of 64: segments of 7 chunks, as chosen, 234 us, of
+// 15 232; 5003 tokens in 7 groups, 8 and 4 heads of 72 and 41: of 2, as chosen, 90, of 3 99.)
 int32_t segment_tokens(const gs_linear_attn* a, bool backward, bool states) {
   const int64_t chunks = div_up(div_up(a->tokens, a->groups), kL);
   const int64_t longest = a->groups > 1 ? 2 * chunks : chunks;
@@ -1105,14 +1156,16 @@ int32_t segment_tokens(const gs_linear_attn* a, bool backward, bool states) {
   for (int m = 1; m <= 16; ++m) {
     const bool alone = longest <= m;
     const int64_t n = alone ? longest : m, segments = a->groups * (alone ? 1 : div_up(chunks, m));
-    const int64_t wave = div_up(segments * a->q_heads * tiles, resident);
+    const int64_t sums = segments * a->q_heads * tiles * (backward ? 2 : 1);
     int64_t c = 0;
-    if (!alone || states) c += (backward ? 2 : 1) * wave * (n + 1) + 6;
+    if (!alone || states) c += div_up(sums, resident) * (n + 1) + 6;
     if (backward) {
-      c += 2 * div_up(segments * a->q_heads * key_tiles, resident) * (n + 1);
-      c += 4 * div_up(segments * a->k_heads * key_tiles * tiles, resident) * (n * rep + 1);
+      const int64_t q = 2 * (n + 1), kv = 4 * (n * rep + 1);
+      const int64_t work = segments * (a->q_heads * key_tiles * q + a->k_heads * key_tiles * tiles * kv);
+      const int64_t spread = div_up(work, resident) + kv / 2;
+      c += spread > kv ? spread : kv;
     } else {
-      c += 2 * wave * (n + 1);
+      c += 2 * div_up(sums, resident) * (n + 1);
     }
     if (c < cost) cost = c, best = m;
   }
@@ -1213,31 +1266,25 @@ gs_status copy_rows(const gs_linear_attn* a, Side* s, int n, const Room& room, c
   return GS_OK;
 }
 
-template <typename T, int KD, int TERMS>
-gs_status run_parts_of(const PartsArgs& p, int64_t slots, cudaStream_t st) {
+template <typename T, int KD>
+gs_status run_parts_of(const PartsArgs& p, int64_t slots, int parts, cudaStream_t st) {
+  constexpr int kTerms = std::is_same<T, __half>::value ? 2 : 3;
   static std::atomic<uint64_t> known{0};
-  if (!allow_smem(attn_parts_kernel<T, KD, TERMS>, known, kPartsSmem<KD, TERMS>)) {
+  if (!allow_smem(attn_parts_kernel<T, KD, kTerms>, known, kPartsSmem<KD, kTerms>)) {
     (void)cudaGetLastError();
     return GS_ERR_CUDA;
   }
-  GS_CUDA(launch_overlapped(attn_parts_kernel<T, KD, TERMS>, dim3((unsigned)slots, p.heads, p.Ep / kV), dim3(kThreads),
-                            kPartsSmem<KD, TERMS>, st, p));
+  GS_CUDA(launch_overlapped(attn_parts_kernel<T, KD, kTerms>, dim3((unsigned)slots, p.heads, parts * (p.Ep / kV)),
+                            dim3(kThreads), kPartsSmem<KD, kTerms>, st, p));
   return GS_OK;
-}
-// exact: the last states are handed on.
-template <typename T>
-gs_status run_parts(const PartsArgs& p, int64_t slots, bool exact, cudaStream_t st) {
-  constexpr int kExact = std::is_same<T, __half>::value ? 2 : 3;
-  if (exact) return p.Dp == 64 ? run_parts_of<T, 64, kExact>(p, slots, st) : run_parts_of<T, 128, kExact>(p, slots, st);
-  return p.Dp == 64 ? run_parts_of<T, 64, 2>(p, slots, st) : run_parts_of<T, 128, 2>(p, slots, st);
 }
 gs_status run_scan(const ScanArgs& p, cudaStream_t st) {
   const int64_t blocks = p.split.groups * div_up(p.D * p.E, kScanThreads);
   if (blocks > INT32_MAX) return GS_ERR_INVALID_ARG;
-  GS_CUDA(launch_overlapped(attn_scan_kernel, dim3((unsigned)blocks, p.heads, p.scans), dim3(kScanThreads), 0, st,
-                            p));
+  GS_CUDA(launch_overlapped(attn_scan_kernel, dim3((unsigned)blocks, p.heads, p.scans), dim3(kScanThreads), 0, st, p));
   return GS_OK;
 }
+
 template <typename T, int KD>
 gs_status run_out_of(const OutArgs& p, int64_t slots, cudaStream_t st) {
   static std::atomic<uint64_t> known{0};
@@ -1245,24 +1292,20 @@ gs_status run_out_of(const OutArgs& p, int64_t slots, cudaStream_t st) {
     (void)cudaGetLastError();
     return GS_ERR_CUDA;
   }
-  GS_CUDA(launch_overlapped(attn_out_kernel<T, KD>,
-                            dim3((unsigned)slots, p.shared ? p.heads / p.rep : p.heads, p.Vp / kV),
-                            dim3(kThreads), kOutSmem<KD>, st, p));
+  GS_CUDA(launch_overlapped(attn_out_kernel<T, KD>, dim3((unsigned)slots, p.heads, p.Vp / kV), dim3(kThreads),
+                            kOutSmem<KD>, st, p));
   return GS_OK;
 }
-template <typename T>
-gs_status run_kv(const KvArgs& p, int64_t slots, cudaStream_t st) {
+template <typename T, int ED, int EE>
+gs_status run_grad_of(const GradArgs& p, int64_t blocks, cudaStream_t st) {
   static std::atomic<uint64_t> known{0};
-  if (!allow_smem(attn_kv_kernel<T>, known, kKvSmem)) {
+  if (!allow_smem(attn_grad_kernel<T, ED, EE>, known, kGradSmem<ED, EE>)) {
     (void)cudaGetLastError();
     return GS_ERR_CUDA;
   }
-  GS_CUDA(launch_overlapped(attn_kv_kernel<T>, dim3((unsigned)slots, p.heads / p.rep), dim3(kThreads), kKvSmem, st, p));
+  GS_CUDA(launch_overlapped(attn_grad_kernel<T, ED, EE>, dim3((unsigned)blocks), dim3(kThreads), kGradSmem<ED, EE>, st,
+                            p));
   return GS_OK;
-}
-template <typename T>
-gs_status run_out(const OutArgs& p, int64_t slots, cudaStream_t st) {
-  return p.Kp == 64 ? run_out_of<T, 64>(p, slots, st) : run_out_of<T, 128>(p, slots, st);
 }
 
 struct Call {
@@ -1282,11 +1325,9 @@ struct Call {
 template <typename T>
 gs_status states_of(const gs_linear_attn* a, const Call& c, const Part (&part)[2], const Scan (&scan)[2], int n,
                     cudaStream_t st) {
-  for (int i = 0; i < n; ++i) {
-    const PartsArgs p{c.split, a->q_heads, c.rep, c.Dp, c.Ep, a->log_decay, part[i]};
-    const gs_status r = run_parts<T>(p, c.slots, scan[i].last != nullptr, st);
-    if (r != GS_OK) return r;
-  }
+  const PartsArgs p{c.split, a->q_heads, c.rep, c.Dp, c.Ep, a->log_decay, {part[0], part[1]}};
+  const gs_status r = c.Dp == 64 ? run_parts_of<T, 64>(p, c.slots, n, st) : run_parts_of<T, 128>(p, c.slots, n, st);
+  if (r != GS_OK) return r;
   return run_scan(ScanArgs{c.split, a->q_heads, a->dim, a->vdim, c.Dp, c.Ep, a->log_decay, {scan[0], scan[1]}, n}, st);
 }
 
@@ -1297,7 +1338,7 @@ gs_status forward(const gs_linear_attn* a, const Call& c, Side (&s)[4], float* s
   const gs_status copied = copy_rows(a, s, 3, room, st);
   if (copied != GS_OK) return copied;
   if (scan) {
-    const gs_status r = states_of<T>(a, c, {Part{s[1], s[2], 1.f, 0, 0, room.states}, Part{}},
+    const gs_status r = states_of<T>(a, c, {Part{s[1], s[2], 1.f, 0, 0, state_out != nullptr, room.states}, Part{}},
                                      {Scan{a->state, state_out, room.states, 0}, Scan{}}, 1, st);
     if (r != GS_OK) return r;
   }
@@ -1315,7 +1356,7 @@ gs_status forward(const gs_linear_attn* a, const Call& c, Side (&s)[4], float* s
   o.K = a->dim, o.V = a->vdim, o.Kp = c.Dp, o.Vp = c.Ep;
   o.mul_inner = o.mul_state = a->scale;
   o.mul_key = 1.f;
-  return run_out<T>(o, c.slots, st);
+  return c.Dp == 64 ? run_out_of<T, 64>(o, c.slots, st) : run_out_of<T, 128>(o, c.slots, st);
 }
 
 template <typename T>
@@ -1327,7 +1368,7 @@ gs_status backward(const gs_linear_attn* a, const Call& c, Side (&s)[7], const f
   const bool scan = a->tokens > c.split.seg || dstate;
   if (scan) {
     const gs_status r =
-        states_of<T>(a, c, {Part{k, v, 1.f, 0, 0, room.states}, Part{q, g, a->scale, 1, 1, room.grads}},
+        states_of<T>(a, c, {Part{k, v, 1.f, 0, 0, 0, room.states}, Part{q, g, a->scale, 1, 1, dstate != nullptr, room.grads}},
                      {Scan{a->state, nullptr, room.states, 0}, Scan{dstate_out, dstate, room.grads, 1}}, 2, st);
     if (r != GS_OK) return r;
   }
@@ -1337,41 +1378,39 @@ gs_status backward(const gs_linear_attn* a, const Call& c, Side (&s)[7], const f
   o.rep = c.rep;
   o.log_decay = a->log_decay;
   o.mul_inner = a->scale;
-  {
-    OutArgs x = o;  // dq
-    x.query = g, x.key = v, x.value = k, x.out = s[4];
-    x.K = a->vdim, x.V = a->dim, x.Kp = c.Ep, x.Vp = c.Dp;
-    x.states = scan ? room.states : nullptr;
-    x.edge = a->state;
-    x.transposed = 1;
-    x.mul_state = a->scale;
-    x.mul_key = 1.f;
-    const gs_status r = run_out<T>(x, c.slots, st);
-    if (r != GS_OK) return r;
-  }
-  if (c.Dp == 64 && c.Ep == 64)
-    return run_kv<T>(KvArgs{c.split, a->q_heads, c.rep, q, k, v, g, s[5], s[6], a->dim, a->vdim, a->log_decay,
-                            scan ? room.grads : nullptr, dstate_out, a->scale, {room.sums[0], room.sums[1]}},
-                     c.slots, st);
+  OutArgs dq = o;
+  dq.query = g, dq.key = v, dq.value = k, dq.out = s[4];
+  dq.K = a->vdim, dq.V = a->dim, dq.Kp = c.Ep, dq.Vp = c.Dp;
+  dq.states = scan ? room.states : nullptr;
+  dq.edge = a->state;
+  dq.transposed = 1;
+  dq.mul_state = a->scale;
+  dq.mul_key = 1.f;
   o.back = o.shift = o.shared = 1;
   o.mul_state = 1.f;
   o.mul_key = a->scale;
   o.states = scan ? room.grads : nullptr;
   o.edge = dstate_out;
-  {
-    OutArgs x = o;  // dk
-    x.query = v, x.key = g, x.value = q, x.out = s[5];
-    x.K = a->vdim, x.V = a->dim, x.Kp = c.Ep, x.Vp = c.Dp;
-    x.transposed = 1;
-    x.sums = room.sums[0];
-    const gs_status r = run_out<T>(x, c.slots, st);
-    if (r != GS_OK) return r;
-  }
-  OutArgs x = o;  // dv
-  x.query = k, x.key = q, x.value = g, x.out = s[6];
-  x.K = a->dim, x.V = a->vdim, x.Kp = c.Dp, x.Vp = c.Ep;
-  x.sums = room.sums[1];
-  return run_out<T>(x, c.slots, st);
+  OutArgs dk = o, dv = o;
+  dk.query = v, dk.key = g, dk.value = q, dk.out = s[5];
+  dk.K = a->vdim, dk.V = a->dim, dk.Kp = c.Ep, dk.Vp = c.Dp;
+  dk.transposed = 1;
+  dk.sums = room.sums[0];
+  dv.query = k, dv.key = q, dv.value = g, dv.out = s[6];
+  dv.K = a->dim, dv.V = a->vdim, dv.Kp = c.Dp, dv.Vp = c.Ep;
+  dv.sums = room.sums[1];
+
+  const bool small = c.Dp == 64 && c.Ep == 64;
+  const int64_t first = c.slots * a->k_heads * (small ? 1 : c.Dp / kV);
+  const int64_t second = first + (small ? 0 : c.slots * a->k_heads * (c.Ep / kV));
+  const int64_t blocks = second + c.slots * a->q_heads * (c.Dp / kV);
+  if (blocks > INT32_MAX) return GS_ERR_INVALID_ARG;
+  const GradArgs p{(int32_t)c.slots, a->q_heads, a->k_heads, (int32_t)first, (int32_t)second, dq, dk, dv,
+                   KvArgs{c.split, a->q_heads, c.rep, q, k, v, g, s[5], s[6], a->dim, a->vdim, a->log_decay, o.states,
+                          o.edge, a->scale, {room.sums[0], room.sums[1]}}};
+  if (c.Dp == 64)
+    return c.Ep == 64 ? run_grad_of<T, 64, 64>(p, blocks, st) : run_grad_of<T, 64, 128>(p, blocks, st);
+  return c.Ep == 64 ? run_grad_of<T, 128, 64>(p, blocks, st) : run_grad_of<T, 128, 128>(p, blocks, st);
 }
 
 }  // namespace
