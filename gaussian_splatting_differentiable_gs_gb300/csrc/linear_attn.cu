@@ -127,7 +127,7 @@ __device__ __forceinline__ void after_sync() { asm volatile("tcgen05.fence::afte
 __device__ __forceinline__ void publish() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 struct Control {
-  uint64_t done[2];
+  uint64_t done[3];
   uint32_t tmem;
   volatile uint32_t abort;
   float top[2][kThreads / 32];
@@ -151,8 +151,7 @@ __device__ __forceinline__ void wait_done(Control* c, int which, uint32_t parity
 template <int COLUMNS>
 __device__ __forceinline__ uint32_t begin(Control* c) {
   if (threadIdx.x == 0) {
-    mbar_init(smem_u32(&c->done[0]), 1);
-    mbar_init(smem_u32(&c->done[1]), 1);
+    for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&c->done[i]), 1);
     c->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -688,14 +687,16 @@ struct Output {
   void* p;              // of the chunk's first token and the block's first channel
   int64_t stride;       // between the chunk's tokens
   int32_t dim, wide;    // channels from there on; whole granules on 16-byte boundaries
-  float* sums;          // fp32 sums over a key head's query heads, or NULL
-  int64_t sum_stride;
+};
+struct Sums {  // fp32 sums over a key head's query heads, or NULL
+  float* p;             // as Output::p
+  int64_t stride;
   bool first, last;     // of those heads
 };
-// inner + f outer, by way of `room` (a tile that nothing uses) to memory; the rows from pad
-// on are there.  A thread has a row's half; a warp stores its 32 rows' halves.
+// inner + f outer of half a row as 32 T; what the heads before summed is added, and unless
+// this is the last head the sum goes back.
 template <typename T>
-__device__ __forceinline__ void put_outputs(uint32_t tmem, uint32_t room, float f, const Output& out, int pad) {
+__device__ __forceinline__ void get_outputs(uint32_t tmem, float f, const Sums& sums, int pad, uint32_t (&w)[16]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = warp >> 2, row = (warp & 3) * 32 + lane;
   const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * 32;
   float x[32], y[32];
@@ -708,24 +709,30 @@ __device__ __forceinline__ void put_outputs(uint32_t tmem, uint32_t room, float 
     const float2 v = fma2(make_float2(y[j], y[j + 1]), both(f), make_float2(x[j], x[j + 1]));
     x[j] = v.x, x[j + 1] = v.y;
   }
-  if (out.sums) {
-    float4* to = reinterpret_cast<float4*>(out.sums + (row - pad) * out.sum_stride + half * 32);
-    if (row >= pad)
+  if (sums.p && row >= pad) {
+    float4* to = reinterpret_cast<float4*>(sums.p + (row - pad) * sums.stride + half * 32);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (!out.first) {
-          const float4 v = to[j];
-          x[4 * j] += v.x, x[4 * j + 1] += v.y, x[4 * j + 2] += v.z, x[4 * j + 3] += v.w;
-        }
-        if (!out.last) to[j] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+    for (int j = 0; j < 8; ++j) {
+      if (!sums.first) {
+        const float4 v = to[j];
+        x[4 * j] += v.x, x[4 * j + 1] += v.y, x[4 * j + 2] += v.z, x[4 * j + 3] += v.w;
       }
-    if (!out.last) return;
+      if (!sums.last) to[j] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+    }
   }
+#pragma unroll
+  for (int j = 0; j < 16; ++j) w[j] = pair_word<T>(x[2 * j], x[2 * j + 1]);
+}
+// These to memory, by way of `room` (a tile whose rows of the warp nothing uses); the rows
+// from pad on are there.  A warp stores its 32 rows' halves.
+template <typename T>
+__device__ __forceinline__ void put_outputs(uint32_t room, const uint32_t (&w)[16], const Output& out, int pad) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = warp >> 2, row = (warp & 3) * 32 + lane;
+  __syncwarp();
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     put_granule(room + row * 128 + (((half * 4 + j) ^ (row & 7)) << 4),
-                make_uint4(pair_word<T>(x[8 * j], x[8 * j + 1]), pair_word<T>(x[8 * j + 2], x[8 * j + 3]),
-                           pair_word<T>(x[8 * j + 4], x[8 * j + 5]), pair_word<T>(x[8 * j + 6], x[8 * j + 7])));
+                make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]));
   __syncwarp();
   if (out.wide) {
     // (rows r and r + 4 together: their granules lie in different banks)
@@ -790,24 +797,25 @@ struct OutArgs {
 template <int KD>
 constexpr int kOutSets = KD == 64 ? 2 : 1;
 template <int KD>
-constexpr int kOutSmem = 1024 + kOutSets<KD> * (2 * (KD / 64) + 1) * kBlock + KD * 128;
+constexpr int kOutSmem = 1024 + kOutSets<KD> * (2 * (KD / 64) + 1) * kBlock + KD * 128 + (KD == 64 ? 0 : kBlock);
 
 template <typename T, int KD>
 __device__ __forceinline__ void form_outputs(const OutArgs& p, int slot, int y, int e0, Control* c, uint32_t tiles,
                                              uint32_t tmem) {
   constexpr uint32_t kKeys = KD / 64 * kBlock;
   // The weighted keys' terms take the places of the keys and of the queries when these have
-  // been multiplied, the outputs leave through the keys'.  Up to 64 channels there is room
-  // for two sets of tiles in turn, so that a chunk comes while the one before is worked on
-  // (32640 tokens, 16 heads of 64: 59 us, with a set and a half 58, one 65); with 128 one
-  // set leaves room for two blocks an SM instead.
+  // been multiplied.  Up to 64 channels there is room for two sets of tiles in turn, so that
+  // a chunk comes while the one before is worked on, whose outputs leave through its keys'
+  // tile while the next one's scores are formed; with 128 one set, and a tile for the
+  // outputs, leave room for two blocks an SM instead.
   constexpr uint32_t kSets = kOutSets<KD>, kSet = 2 * kKeys + kBlock;  // queries, keys, values
   const uint32_t state = tiles + kSets * kSet;
   const Span s = span_of(p.split, slot);
   const int64_t from = p.back ? s.start + s.n - 1 : s.start, step = p.back ? -1 : 1;
   const int chunks = (s.n + kL - 1) / kL, reps = p.shared ? p.rep : 1;
   const int row = ((int)threadIdx.x >> 5 & 3) * 32 + ((int)threadIdx.x & 31);
-  uint32_t phase = 0;
+  const int64_t key_heads = p.heads / p.rep;
+  uint32_t phase = 0, update_phase = 0;
 
   for (int r = 0; r < (s.n ? reps : 0); ++r) {
     const int h = p.shared ? y * p.rep + r : y;
@@ -815,16 +823,21 @@ __device__ __forceinline__ void form_outputs(const OutArgs& p, int slot, int y, 
     const T* q = head_at<T>(p.query, h, p.rep, from);
     const T* k = head_at<T>(p.key, h, p.rep, from);
     const T* v = head_at<T>(p.value, h, p.rep, from) + e0;
-    auto load = [&](int i) {
+    auto load_keys = [&](int i) {
+      load_tile<T, KD>(tiles + i % kSets * kSet + kKeys, k + step * i * kL * p.key.token, step * p.key.token,
+                       min(kL, s.n - i * kL), p.key.dim);
+      copies_commit();
+    };
+    auto load_others = [&](int i) {
       const int n = min(kL, s.n - i * kL);
       const int64_t at = step * i * kL;
       const uint32_t to = tiles + i % kSets * kSet;
       load_tile<T, KD>(to, q + at * p.query.token, step * p.query.token, n, p.query.dim);
-      load_tile<T, KD>(to + kKeys, k + at * p.key.token, step * p.key.token, n, p.key.dim);
       load_tile<T, kV>(to + 2 * kKeys, v + at * p.value.token, step * p.value.token, n, p.value.dim - e0);
       copies_commit();
     };
-    load(0);
+    load_keys(0);
+    load_others(0);
     if (threadIdx.x < 64) c->decay[threadIdx.x] = threadIdx.x < 32 ? p.mul_inner * power2(a * (float)(31 - (int)threadIdx.x)) : 0.f;
     State<KD> st;
     const Stored src = stored(p.states, p.edge, p.Kp, p.Vp, p.K, p.V, p.transposed, (int64_t)slot * p.heads + h,
@@ -832,9 +845,18 @@ __device__ __forceinline__ void form_outputs(const OutArgs& p, int slot, int y, 
     st.get(src.p, src.rs, src.cs, e0, p.K, p.V);
     const float top_weight = p.mul_key * power2(a * (float)p.shift);
 
+    const bool last = r + 1 == reps;
+    auto room = [&](int i) { return kSets == 2 ? tiles + (i & 1) * kSet + kKeys : state + KD * 128; };
+    auto put = [&](int i, const uint32_t(&w)[16], int pad) {
+      const int64_t tok = from + step * i * kL;
+      put_outputs<T>(room(i), w, Output{(T*)p.out.p + (int64_t)y * p.out.head + tok * p.out.token + e0,
+                                        step * p.out.token, p.out.dim - e0, p.out.wide}, pad);
+    };
+    uint32_t w[16];
     for (int i = 0; i < chunks; ++i, phase ^= 1) {
       const int n = min(kL, s.n - i * kL), pad = kL - n;
       const uint32_t queries = tiles + i % kSets * kSet, keys = queries + kKeys, values = keys + kKeys;
+      const bool more = i + 1 < chunks;
       copies_wait<0>();
       const Fit fit = fit_of<T, KD>(c, st, keys, top_weight);
       st.template to_tile<T>(state, fit.state);
@@ -846,8 +868,8 @@ __device__ __forceinline__ void form_outputs(const OutArgs& p, int slot, int y, 
         mma_scores<T, KD, false>(tmem, queries, keys, state);
         commit(smem_u32(&c->done[0]));
       }
-      const bool more = i + 1 < chunks;
-      if (more && kSets == 2) load(i + 1);
+      if (more && kSets == 2) load_others(i + 1);
+      if (i > 0 && last) put(i - 1, w, 0);
       wait_done(c, 0, phase);
       after_sync();
       if (more) weigh<T, KD, 2>(keys, keys, queries - keys, a, p.shift, p.mul_key * fit.key);
@@ -858,26 +880,33 @@ __device__ __forceinline__ void form_outputs(const OutArgs& p, int slot, int y, 
       if (threadIdx.x == 0) {
         after_sync();
         mma_inner<T>(tmem, values);
-        if (more) mma_state<T, KD, 2>(tmem + kUpdate, keys, queries - keys, values);
         commit(smem_u32(&c->done[1]));
+        if (more) {
+          mma_state<T, KD, 2>(tmem + kUpdate, keys, queries - keys, values);
+          commit(smem_u32(&c->done[2]));
+        }
       }
+      if (more && kSets == 2) load_keys(i + 1);
       wait_done(c, 1, phase);
       after_sync();
-      if (more) st.update(tmem + kUpdate, power2(a * (float)n), fit.key_back);
       const int64_t tok = from + step * i * kL;
-      const int64_t key_heads = p.heads / p.rep;
-      const Output out{(T*)p.out.p + (int64_t)y * p.out.head + tok * p.out.token + e0, step * p.out.token,
-                       p.out.dim - e0, p.out.wide,
-                       reps > 1 ? p.sums + (tok * key_heads + y) * p.Vp + e0 : nullptr,
-                       step * key_heads * p.Vp, r == 0, r + 1 == reps};
+      const Sums sums{reps > 1 ? p.sums + (tok * key_heads + y) * p.Vp + e0 : nullptr, step * key_heads * p.Vp, r == 0,
+                      last};
       // (rows before the chunk's first token are not there)
-      put_outputs<T>(tmem, keys, p.mul_state * fit.state_back * power2(a * (float)max(row + 1 - p.shift - pad, 0)), out,
-                     pad);
-      if (more && kSets == 1) {
-        __syncthreads();  // the outputs have left the keys' tile
-        load(i + 1);
+      get_outputs<T>(tmem, p.mul_state * fit.state_back * power2(a * (float)max(row + 1 - p.shift - pad, 0)), sums, pad,
+                     w);
+      if (more) {
+        wait_done(c, 2, update_phase);
+        update_phase ^= 1;
+        after_sync();
+        if (kSets == 1) {
+          load_keys(i + 1);
+          load_others(i + 1);
+        }
+        st.update(tmem + kUpdate, power2(a * (float)n), fit.key_back);
       }
     }
+    if (last) put(chunks - 1, w, kL - (s.n - (chunks - 1) * kL));
     __syncthreads();  // the next head's loads and decays follow
   }
 }
@@ -912,24 +941,28 @@ constexpr int kKvSmem = 1024 + 6 * kBlock + 64 * 128;  // keys and queries twice
 
 template <typename T>
 __device__ __forceinline__ void form_kv(const KvArgs& p, int slot, int y, Control* c, uint32_t tiles, uint32_t tmem) {
-  // Keys and queries in two pairs of tiles in turn: the next chunk's come while this one is
-  // worked on, its values and douts while its first scores are.  The weighted queries'
-  // terms take the places of keys and values when these have been multiplied.
+  // Keys and queries in two pairs of tiles in turn: the next chunk's come while this one's
+  // last products are formed, its values and douts while its first scores are.  The weighted
+  // queries' terms take the places of keys and values when these have been multiplied.  dv
+  // and dk leave through a keys' tile that is not in use while the next scores are formed.
   const uint32_t pairs = tiles, values = pairs + 4 * kBlock, douts = values + kBlock, state = douts + kBlock;
   const Span s = span_of(p.split, slot);
   const int64_t from = s.start + s.n - 1, key_heads = p.heads / p.rep;
   const int chunks = (s.n + kL - 1) / kL;
   const int row = ((int)threadIdx.x >> 5 & 3) * 32 + ((int)threadIdx.x & 31);
+  uint32_t update_phase = 0;
 
   for (int r = 0; r < (s.n ? p.rep : 0); ++r) {
     const int h = y * p.rep + r;
     const float a = log2_decay(p.log_decay, h);
-    auto load_pair = [&](int i) {
-      const int n = min(kL, s.n - i * kL);
-      const int64_t at = from - (int64_t)i * kL;
-      const uint32_t to = pairs + (i & 1) * 2 * kBlock;
-      load_tile<T, 64>(to, head_at<T>(p.k, h, p.rep, at), -p.k.token, n, p.k.dim);
-      load_tile<T, 64>(to + kBlock, head_at<T>(p.q, h, p.rep, at), -p.q.token, n, p.q.dim);
+    auto load_keys = [&](int i) {
+      load_tile<T, 64>(pairs + (i & 1) * 2 * kBlock, head_at<T>(p.k, h, p.rep, from - (int64_t)i * kL), -p.k.token,
+                       min(kL, s.n - i * kL), p.k.dim);
+      copies_commit();
+    };
+    auto load_queries = [&](int i) {
+      load_tile<T, 64>(pairs + (i & 1) * 2 * kBlock + kBlock, head_at<T>(p.q, h, p.rep, from - (int64_t)i * kL),
+                       -p.q.token, min(kL, s.n - i * kL), p.q.dim);
       copies_commit();
     };
     auto load_others = [&](int i) {
@@ -939,7 +972,8 @@ __device__ __forceinline__ void form_kv(const KvArgs& p, int slot, int y, Contro
       load_tile<T, 64>(values, head_at<T>(p.v, h, p.rep, at), -p.v.token, n, p.v.dim);
       copies_commit();
     };
-    load_pair(0);
+    load_queries(0);
+    load_keys(0);
     load_others(0);
     if (threadIdx.x < 64) c->decay[threadIdx.x] = threadIdx.x < 32 ? p.scale * power2(a * (float)(31 - (int)threadIdx.x)) : 0.f;
     State<64> st;
@@ -948,10 +982,16 @@ __device__ __forceinline__ void form_kv(const KvArgs& p, int slot, int y, Contro
     st.get(src.p, src.rs, src.cs, 0, p.D, p.E);
     const float top_weight = p.scale * power2(a);
 
+    const bool last = r + 1 == p.rep;
+    auto put = [&](int i, const uint32_t(&w)[16], const Side& side, uint32_t room, int pad) {
+      put_outputs<T>(room, w, Output{head_at<T>(side, h, p.rep, from - (int64_t)i * kL), -side.token, side.dim, side.wide},
+                     pad);
+    };
+    uint32_t w[16];
     for (int i = 0; i < chunks; ++i) {
       const int n = min(kL, s.n - i * kL), pad = kL - n;
       const bool more = i + 1 < chunks;
-      const uint32_t keys = pairs + (i & 1) * 2 * kBlock, queries = keys + kBlock;
+      const uint32_t keys = pairs + (i & 1) * 2 * kBlock, queries = keys + kBlock, other = pairs + (~i & 1) * 2 * kBlock;
       copies_wait<1>();  // (values and douts may be on their way)
       const Fit fit = fit_of<T, 64>(c, st, queries, top_weight);
       st.template to_tile<T>(state, fit.state);
@@ -959,10 +999,9 @@ __device__ __forceinline__ void form_kv(const KvArgs& p, int slot, int y, Contro
       before_sync();
       __syncthreads();
       const float f = fit.state_back * power2(a * (float)max(row - pad, 0));
-      const int64_t tok = from - (int64_t)i * kL;
-      const bool sums = p.rep > 1;
+      const int64_t sum = ((from - (int64_t)i * kL) * key_heads + y) * 64;
 #pragma unroll
-      for (int ph = 0; ph < 2; ++ph) {  // dv, dk: each barrier is used twice a chunk
+      for (int ph = 0; ph < 2; ++ph) {  // dv, dk: the first two barriers are used twice a chunk
         if (threadIdx.x == 0) {
           after_sync();
           if (ph == 0) mma_scores<T, 64, false>(tmem, keys, queries, state);
@@ -970,37 +1009,45 @@ __device__ __forceinline__ void form_kv(const KvArgs& p, int slot, int y, Contro
           commit(smem_u32(&c->done[0]));
         }
         if (ph == 0) {
-          if (more) load_pair(i + 1);
+          if (more) load_queries(i + 1);
           else copies_commit();
         }
+        if (last && (ph || i > 0)) put(ph ? i : i - 1, w, ph ? p.dv : p.dk, other, ph ? pad : 0);
         wait_done(c, 0, ph);
         after_sync();
         if (ph == 1 && more) weigh<T, 64, 2>(queries, keys, values - keys, a, 1, p.scale * fit.key);
         decay_scores<T>(tmem, c, a);
-        if (ph == 0) copies_wait<1>();  // values and douts are there
+        if (ph == 0) copies_wait<1>();  // they are there, the next queries may be on their way
         publish();
         before_sync();
         __syncthreads();
         if (threadIdx.x == 0) {
           after_sync();
           mma_inner<T>(tmem, ph ? queries : douts);
-          if (ph == 1 && more) mma_state<T, 64, 2>(tmem + kUpdate, keys, values - keys, douts);
           commit(smem_u32(&c->done[1]));
+          if (ph == 1 && more) {
+            mma_state<T, 64, 2>(tmem + kUpdate, keys, values - keys, douts);
+            commit(smem_u32(&c->done[2]));
+          }
         }
+        if (ph == 1 && more) load_keys(i + 1);
         wait_done(c, 1, ph);
         after_sync();
-        const Side& side = ph ? p.dk : p.dv;
-        const Output out{head_at<T>(side, h, p.rep, tok), -side.token, side.dim, side.wide,
-                         sums ? p.sums[1 - ph] + (tok * key_heads + y) * 64 : nullptr, -key_heads * 64, r == 0,
-                         r + 1 == p.rep};
-        // dv through the keys' tile, which nothing uses any more, dk through the values'
-        if (ph == 1 && more) st.update(tmem + kUpdate, power2(a * (float)n), fit.key_back);
-        put_outputs<T>(tmem, ph ? values : keys, f, out, pad);
-        before_sync();
-        __syncthreads();  // the sums in TMEM and the tiles have been read
+        get_outputs<T>(tmem, f, Sums{p.rep > 1 ? p.sums[1 - ph] + sum : nullptr, -key_heads * 64, r == 0, last}, pad, w);
+        if (ph == 0) {
+          before_sync();
+          __syncthreads();  // the sums in TMEM have been read
+        } else if (more) {
+          wait_done(c, 2, update_phase);
+          update_phase ^= 1;
+          after_sync();
+          load_others(i + 1);
+          st.update(tmem + kUpdate, power2(a * (float)n), fit.key_back);
+        }
       }
-      if (more) load_others(i + 1);
     }
+    if (last) put(chunks - 1, w, p.dk, pairs + (~chunks & 1) * 2 * kBlock, kL - (s.n - (chunks - 1) * kL));
+    __syncthreads();  // the next head's loads and decays follow
   }
 }
 
