@@ -48,7 +48,7 @@ constexpr int kRowsOut = 32 * 128;         // a warp's room for 32 rows of 128 b
 constexpr int kCtrlBytes = 1024;
 constexpr int kSmem = kStages * kStage + kEpiWarps * kRowsOut + kCtrlBytes + 1024;  // + alignment
 static_assert(kSmem <= 227 * 1024, "shared memory");
-constexpr int kMaxClusters = 128;
+constexpr int kMaxClusters = 96;
 constexpr size_t kPartialFloats = (size_t)kHalf * kTile;  // one CTA's half tile
 constexpr unsigned int kErrTimeout = 1u;
 constexpr int64_t kWaitNs = 2000000000;
@@ -66,7 +66,7 @@ struct Job {
   int32_t out_wide;            // rows of out start on 16-byte boundaries
   const void* dh;              // kRecompute
   int64_t dh_stride;           // (rows on 16-byte boundaries)
-  int32_t hidden, hidden_ld;   // hidden, rounded up to 8: columns of dgate in the workspace
+  int32_t hidden, hidden_ld;   // hidden, padded: columns of dgate in the workspace
   int32_t accumulate;
   uint32_t load_steps;  // steps whose operands are brought: all, but in the self-test
   int64_t wait_ns;      // after which a wait gives up
@@ -517,7 +517,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
       } else if (MODE == kDx && w.slot >= 0) {
         float* to = partial + ((size_t)(cluster * 2 + w.slot) * 2 + rank) * kPartialFloats +
-                    (quarter * 32 + lane) * kTile + half * kHalf;
+                    half * kHalf * kHalf + (quarter * 32 + lane) * 4;
 #pragma unroll 1
         for (int b = 0; b < 4; ++b) {
           float v[32];
@@ -526,7 +526,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (b == 3) release();
 #pragma unroll
           for (int j = 0; j < 32; j += 4)
-            *reinterpret_cast<float4*>(to + b * 32 + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+            *reinterpret_cast<float4*>(to + (b * 32 + j) * kHalf) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
         }
       } else if (MODE == kDx) {
 #pragma unroll
@@ -593,43 +593,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // Joins the partial sums of the tiles that several clusters share, in the clusters' order.
 // dW's lie column by column, 128 channels each: a warp takes a column of a CTA's half tile,
-// a thread four channels.  dx's lie row by row: a warp takes a row, a thread eight columns.
+// a thread four channels.  dx's lie by fours of columns, 128 rows each: a warp takes 32
+// rows, a thread eight columns of one.
 template <typename TO, bool DX>
-__global__ void __launch_bounds__(128) ffn_join_kernel(const __grid_constant__ Job p, const float* partial) {
-  launch_dependents();
-  wait_for_previous();
+__device__ __forceinline__ void join_partials(const Job& p, const float* partial, int block) {
   constexpr int kLines = DX ? kHalf : kTile, kPerHalf = kLines / 4, kPer = DX ? 8 : 4;
-  const int tile = blockIdx.x / (2 * kPerHalf), rank = blockIdx.x / kPerHalf % 2;
-  const int line = blockIdx.x % kPerHalf * 4 + (int)(threadIdx.x >> 5), in = threadIdx.x % 32 * kPer;
+  const int tile = block / (2 * kPerHalf), rank = block / kPerHalf % 2;
+  const int line = block % kPerHalf * 4 + (int)(threadIdx.x >> 5), lane = threadIdx.x % 32;
+  // the thread's row and column of the half tile
+  const int mi = DX ? line % 4 * 32 + lane : lane * 4, ni = DX ? line / 4 * 8 : line;
   const int64_t first = (int64_t)tile * p.steps, last = first + p.steps - 1;
   const int lo = (int)(first / p.quota), hi = (int)(last / p.quota);
   if (lo == hi) return;  // summed by one cluster, and written by it
   const int id = p.waves * p.clusters + tile;
-  const int64_t m = (int64_t)(id / p.tiles_n) * kTile + rank * kHalf + (DX ? line : in);
-  const int64_t n = (int64_t)(id % p.tiles_n) * kTile + (DX ? in : line);
+  const int64_t m = (int64_t)(id / p.tiles_n) * kTile + rank * kHalf + mi;
+  const int64_t n = (int64_t)(id % p.tiles_n) * kTile + ni;
   const int64_t row = DX ? m : n < p.cols ? dw_row(p, n) : -1;
   if (row < 0 || m >= p.rows || n >= p.cols) return;
   // a cluster's first segment is in its slot 0, its second in slot 1
   const int two = (int64_t)lo * p.quota / p.steps == tile ? 0 : 1;
   const float4* from = reinterpret_cast<const float4*>(partial + ((size_t)lo * 4 + rank) * kPartialFloats +
-                                                       (size_t)line * (DX ? kTile : kHalf) + in);
+                                                       (size_t)ni * kHalf + (DX ? mi * 4 : mi));
   const size_t next = kPartialFloats;  // float4s from one cluster's slot 0 to the next one's
-  float r[kPer];
+  float4 v[kPer / 4];
 #pragma unroll
-  for (int q = 0; q < kPer / 4; ++q) {
-    float4 v = from[(two ? kPartialFloats / 2 : 0) + q];
-#pragma unroll 8
-    for (int i = 1; i <= hi - lo; ++i) {
-      const float4 u = from[i * next + q];
-      v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+  for (int q = 0; q < kPer / 4; ++q) v[q] = from[(two ? kPartialFloats / 2 : 0) + q * kHalf];
+#pragma unroll 4
+  for (int i = 1; i <= hi - lo; ++i)
+#pragma unroll
+    for (int q = 0; q < kPer / 4; ++q) {
+      const float4 u = from[i * next + q * kHalf];
+      v[q].x += u.x, v[q].y += u.y, v[q].z += u.z, v[q].w += u.w;
     }
-    r[4 * q] = v.x, r[4 * q + 1] = v.y, r[4 * q + 2] = v.z, r[4 * q + 3] = v.w;
-  }
+  Pack<TO, kPer> r;
   TO* to = (TO*)p.out + row * p.out_stride + (DX ? n : m);
   const int64_t left = DX ? p.cols - n : p.rows - m;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j)
-    if (j < left) put_dw<TO>(to + j, r[j], p.accumulate);
+  for (int j = 0; j < kPer; ++j) {
+    const float x = (&v[j / 4].x)[j % 4];
+    r.v[j] = from_f32<TO>(p.accumulate && j < left ? x + to_f32(to[j]) : x);
+  }
+  if (p.out_wide && left >= kPer) {
+    store_pack<TO, kPer>(to, r);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (j < left) to[j] = r.v[j];
+  }
+}
+// Both in one launch: dx's blocks, then dW's.
+struct Joins {
+  Job dx, dw;
+  int32_t dx_blocks;
+  const float *dx_partial, *dw_partial;
+};
+template <typename T, typename TO>
+__global__ void __launch_bounds__(128) ffn_join_kernel(const __grid_constant__ Joins p) {
+  launch_dependents();
+  wait_for_previous();
+  if ((int)blockIdx.x < p.dx_blocks) join_partials<T, true>(p.dx, p.dx_partial, blockIdx.x);
+  else join_partials<TO, false>(p.dw, p.dw_partial, blockIdx.x - p.dx_blocks);
 }
 
 // Rows that start anywhere, copied to padded rows that TMA can read (`granules` of eight
@@ -816,7 +839,10 @@ bool make_map(CUtensorMap* map, int32_t dtype, const void* p, int rank, const in
 
 constexpr int64_t kMaxTokens = ((int64_t)1 << 31) - 2 * kTile;
 constexpr int32_t kMaxWidth = 1 << 20;
-int64_t padded(int64_t n) { return div_up(n, 8) * 8; }
+// Rows in the workspace: whole lines of 128 bytes, as a row of a tile is.  (Tensors whose
+// rows start elsewhere in a line cost L2 a half more: 5000 x 1000 x 1360 as they lie forward
+// 27 us, 4864 x 1024 x 1408, the same number of tiles, 18.5.)
+int64_t padded(int64_t n) { return div_up(n, 64) * 64; }
 bool shape_ok(int64_t tokens, int32_t channels, int32_t hidden) {
   return tokens >= 0 && tokens <= kMaxTokens && channels >= 1 && channels <= kMaxWidth && hidden >= 1 &&
          hidden <= kMaxWidth && div_up(tokens, kTile) * div_up(hidden, kHalf) < ((int64_t)1 << 31) &&
@@ -834,7 +860,7 @@ constexpr size_t kPartialBytes = sizeof(float) * kPartialFloats * 4 * kMaxCluste
 
 struct Room {  // the workspace's parts
   char *x, *w, *grads;
-  float* partial;
+  float *partial, *dw_partial;  // of dx, of dW
   unsigned int* status;
   size_t bytes;
   Room(void* ws, int64_t tokens, int32_t channels, int32_t hidden, bool backward) {
@@ -850,6 +876,7 @@ struct Room {  // the workspace's parts
     w = take((size_t)2 * hidden * padded(channels) * 2);
     grads = take(backward ? (size_t)tokens * 2 * padded(hidden) * 2 : 0);
     partial = (float*)take(backward ? kPartialBytes : 0);
+    dw_partial = (float*)take(backward ? kPartialBytes : 0);
     bytes = at;
   }
 };
@@ -909,13 +936,10 @@ gs_status launch(const void* kernel, const Job& p, const CUtensorMap& a, const C
   return GS_OK;
 }
 
-template <typename TO, bool DX>
-gs_status join(const Job& p, int64_t tiles, const Room& room, cudaStream_t st) {
+// Blocks that join a product's shared tiles (0: there are none).
+int64_t join_blocks(const Job& p, int64_t tiles, bool dx) {
   const int64_t rem = tiles - (int64_t)p.waves * p.clusters;
-  if (!rem || p.quota % p.steps == 0) return GS_OK;
-  GS_CUDA(launch_overlapped(ffn_join_kernel<TO, DX>, dim3((unsigned)(rem * 2 * (DX ? kHalf / 4 : kTile / 4))), dim3(128),
-                            0, st, p, room.partial));
-  return GS_OK;
+  return !rem || p.quota % p.steps == 0 ? 0 : rem * 2 * (dx ? kHalf / 4 : kTile / 4);
 }
 const void* pick(int32_t dtype, int mode, int act, bool f32 = false) {
   return dtype == GS_BF16 ? kernel_of<__nv_bfloat16>(mode, act, f32) : kernel_of<__half>(mode, act, f32);
@@ -1057,6 +1081,8 @@ gs_status backward(const Args& a, const void* dh, int64_t dh_stride, void* dx, i
     s = project(a, x, w, q, kRecompute, clusters, room, st);
     if (s != GS_OK) return s;
   }
+  Joins joins{};
+  int64_t blocks = 0;
   CUtensorMap am, bm;
   if (dx) {
     Job q = p;
@@ -1076,9 +1102,9 @@ gs_status backward(const Args& a, const void* dh, int64_t dh_stride, void* dx, i
     if (!make_map(&am, a.dtype, room.grads, 3, ad, as, ab) || !make_map(&bm, a.dtype, w.p, 3, bd, bs, bb))
       return GS_ERR_CUDA;
     s = launch(pick(a.dtype, kDx, 0), q, am, bm, room.partial, room.status, st);
-    if (s == GS_OK)
-      s = a.dtype == GS_BF16 ? join<__nv_bfloat16, true>(q, tiles, room, st) : join<__half, true>(q, tiles, room, st);
     if (s != GS_OK) return s;
+    joins.dx = q;
+    joins.dx_blocks = (int32_t)join_blocks(q, tiles, true);
   }
   if (dw) {
     Job q = p;
@@ -1086,6 +1112,7 @@ gs_status backward(const Args& a, const void* dh, int64_t dh_stride, void* dx, i
     q.cols = 2 * ld;
     q.out = dw;
     q.out_stride = dw_stride;
+    q.out_wide = rows_aligned(dw, dw_stride, dtype_size(dw_dtype), 16);
     q.accumulate = accumulate != 0;
     q.tiles_n = (int)div_up(2 * ld, kTile);
     q.steps = q.part_steps = (int)div_up(a.tokens, kStep);
@@ -1097,11 +1124,21 @@ gs_status backward(const Args& a, const void* dh, int64_t dh_stride, void* dx, i
     if (!make_map(&am, a.dtype, x.p, 2, ad, as, box) || !make_map(&bm, a.dtype, room.grads, 2, bd, bs, box))
       return GS_ERR_CUDA;
     const bool f32 = dw_dtype == GS_F32;
-    s = launch(pick(a.dtype, kDw, 0, f32), q, am, bm, room.partial, room.status, st);
+    s = launch(pick(a.dtype, kDw, 0, f32), q, am, bm, room.dw_partial, room.status, st);
     if (s != GS_OK) return s;
-    s = f32 ? join<float, false>(q, tiles, room, st)
-            : a.dtype == GS_BF16 ? join<__nv_bfloat16, false>(q, tiles, room, st) : join<__half, false>(q, tiles, room, st);
-    if (s != GS_OK) return s;
+    joins.dw = q;
+    blocks = join_blocks(q, tiles, false);
+  }
+  if (blocks += joins.dx_blocks) {
+    joins.dx_partial = room.partial, joins.dw_partial = room.dw_partial;
+    const dim3 grid((unsigned)blocks), block(128);
+    if (a.dtype == GS_BF16)
+      GS_CUDA(dw && dw_dtype == GS_F32
+                  ? launch_overlapped(ffn_join_kernel<__nv_bfloat16, float>, grid, block, 0, st, joins)
+                  : launch_overlapped(ffn_join_kernel<__nv_bfloat16, __nv_bfloat16>, grid, block, 0, st, joins));
+    else
+      GS_CUDA(dw && dw_dtype == GS_F32 ? launch_overlapped(ffn_join_kernel<__half, float>, grid, block, 0, st, joins)
+                                       : launch_overlapped(ffn_join_kernel<__half, __half>, grid, block, 0, st, joins));
   }
   return GS_OK;
 }
