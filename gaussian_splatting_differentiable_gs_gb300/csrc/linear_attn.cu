@@ -460,15 +460,19 @@ struct PartsArgs {
   Part part[2];
 };
 
+// Up to 64 channels two sets of keys and values, and the terms: loads are two chunks ahead.
+// With 128 one set, in which the first term takes the keys' place, so that an SM has two
+// blocks (4 groups of 2040 tokens, 8 heads of 128: 16 us; two sets, one block 22).
 template <int KD, int TERMS>
-constexpr int kPartsSmem = 1024 + 2 * (KD / 64 + 1) * kBlock + TERMS * (KD / 64) * kBlock;
+constexpr int kPartsSmem = 1024 + (KD == 64 ? 2 * 2 + TERMS : 3 + 2 * (TERMS - 1)) * kBlock;
 
 template <typename T, int KD, int TERMS>
 __device__ __forceinline__ void sum_part(const PartsArgs& p, const Part& part, int e0, Control* c, uint32_t tiles,
                                          uint32_t tmem) {
   constexpr bool kHalfType = std::is_same<T, __half>::value;
-  constexpr uint32_t kSet = (KD / 64 + 1) * kBlock;  // keys, values
-  const uint32_t terms = tiles + 2 * kSet;
+  constexpr int kSets = KD == 64 ? 2 : 1;
+  constexpr uint32_t kTerm = KD / 64 * kBlock, kSet = kTerm + kBlock;
+  const uint32_t terms = kSets == 2 ? tiles + 2 * kSet : tiles;
   const int h = blockIdx.y, warp = threadIdx.x >> 5;
   const Span s = span_of(p.split, blockIdx.x);
   const float a = log2_decay(p.log_decay, h);
@@ -477,34 +481,35 @@ __device__ __forceinline__ void sum_part(const PartsArgs& p, const Part& part, i
   const T* k = head_at<T>(part.key, h, p.rep, from);
   const T* v = head_at<T>(part.value, h, p.rep, from) + e0;
   const int chunks = (s.n + kL - 1) / kL;
-  constexpr uint32_t kTerm = KD / 64 * kBlock;
-  // Two chunks ahead: a chunk's keys make room when they have been weighed (each thread
-  // brings the granules that it weighs), its values when they have been multiplied.
+  // Two sets: a chunk's keys make room when they have been weighed (each thread brings the
+  // granules that it weighs), its values when they have been multiplied.
+  auto keys_of = [&](int i) { return kSets == 2 ? tiles + (i & 1) * kSet : tiles; };
+  auto values_of = [&](int i) { return kSets == 2 ? tiles + (i & 1) * kSet + kTerm : tiles + TERMS * kTerm; };
   auto load_keys = [&](int i) {
     if (i < chunks)
-      load_tile<T, KD>(tiles + (i & 1) * kSet, k + step * i * kL * part.key.token, step * part.key.token,
-                       min(kL, s.n - i * kL), part.key.dim);
+      load_tile<T, KD>(keys_of(i), k + step * i * kL * part.key.token, step * part.key.token, min(kL, s.n - i * kL),
+                       part.key.dim);
     copies_commit();
   };
   auto load_values = [&](int i) {
     if (i < chunks)
-      load_tile<T, kV>(tiles + (i & 1) * kSet + kTerm, v + step * i * kL * part.value.token, step * part.value.token,
+      load_tile<T, kV>(values_of(i), v + step * i * kL * part.value.token, step * part.value.token,
                        min(kL, s.n - i * kL), part.value.dim - e0);
     copies_commit();
   };
   State<KD> st;
   st.zero();
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < kSets; ++i) {
     load_keys(i);
     load_values(i);
   }
   for (int i = 0; i < chunks; ++i) {
-    const uint32_t set = tiles + (i & 1) * kSet;
-    copies_wait<2>();
+    const uint32_t keys = keys_of(i);
+    copies_wait<2 * (kSets - 1)>();
     float mul = part.mul, back = 1.f;
     if constexpr (kHalfType) {
-      const float m = top_key<KD>(set);
+      const float m = top_key<KD>(keys);
       if ((threadIdx.x & 31) == 0) c->top[i & 1][warp] = m;
       __syncthreads();
       float x = 0.f;
@@ -514,19 +519,20 @@ __device__ __forceinline__ void sum_part(const PartsArgs& p, const Part& part, i
       mul *= power_of_two(-e);
       back = power_of_two(e);
     }
-    weigh<T, KD, TERMS>(set, terms, kTerm, a, part.shift, mul);
+    weigh<T, KD, TERMS>(keys, terms, kTerm, a, part.shift, mul);
     publish();
     before_sync();
     __syncthreads();
     if (threadIdx.x == 0) {
       after_sync();
-      mma_state<T, KD, TERMS>(tmem, terms, kTerm, set + kTerm);
+      mma_state<T, KD, TERMS>(tmem, terms, kTerm, values_of(i));
       commit(smem_u32(&c->done[0]));
     }
-    load_keys(i + 2);
+    if (kSets == 2) load_keys(i + kSets);
     wait_done(c, 0, i & 1);
     after_sync();
-    load_values(i + 2);
+    if (kSets == 1) load_keys(i + kSets);
+    load_values(i + kSets);
     st.update(tmem, power2(a * (float)min(kL, s.n - i * kL)), back);
   }
   if (s.n) st.put(part.to + ((int64_t)blockIdx.x * p.heads + h) * p.Dp * p.Ep + e0, p.Ep);
@@ -534,7 +540,7 @@ __device__ __forceinline__ void sum_part(const PartsArgs& p, const Part& part, i
 
 // TERMS: the most that a part's keys are taken as.
 template <typename T, int KD, int TERMS>
-__global__ void __launch_bounds__(kThreads, 128 / KD) attn_parts_kernel(const __grid_constant__ PartsArgs p) {
+__global__ void __launch_bounds__(kThreads, 2) attn_parts_kernel(const __grid_constant__ PartsArgs p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   Control* c = (Control*)smem;
   const uint32_t tmem = begin<64>(c);
@@ -563,42 +569,49 @@ struct ScanArgs {
   int32_t scans;
 };
 
-// One element of the state a thread, so that there are enough of them to hide the latency
-// of the parts' loads, kAhead of them under way (19 segments of 16 heads of 64: 7.5 us, the
-// same with vectors of four elements 29; half as many under way: 13).
-constexpr int kScanThreads = 256, kAhead = 16;
+// VEC neighbouring elements of the state in a row a thread, AHEAD segments' loads under
+// way.
+constexpr int kScanThreads = 256;
+template <int VEC, int AHEAD>
 __global__ void __launch_bounds__(kScanThreads) attn_scan_kernel(const __grid_constant__ ScanArgs p) {
   launch_dependents();
   wait_for_previous();
   const Scan& k = p.scan[blockIdx.z];
-  const int per = (p.D * p.E + kScanThreads - 1) / kScanThreads, size = p.Dp * p.Ep;
+  const int across = (p.E + VEC - 1) / VEC, per = (p.D * across + kScanThreads - 1) / kScanThreads;
   const int h = blockIdx.y, g = blockIdx.x / per, i = blockIdx.x % per * kScanThreads + threadIdx.x;
-  if (i >= p.D * p.E) return;
-  const int row = i / p.E, col = i % p.E;
+  if (i >= p.D * across) return;
+  const int row = i / across, col = i % across * VEC, size = p.Dp * p.Ep;
   const float a = log2_decay(p.log_decay, h);
   const int64_t begin = offset_of(p.split, g), end = offset_of(p.split, g + 1);
   const int64_t first = begin / p.split.seg + g;
   const int slots = end > begin ? (int)((end - begin + p.split.seg - 1) / p.split.seg) : 0;
   const int tail = (int)(end - begin - (int64_t)(slots - 1) * p.split.seg);
-  const int64_t mat = ((int64_t)g * p.heads + h) * p.D * p.E + i;
-  float s = k.edge ? k.edge[mat] : 0.f;
+  const int64_t mat = ((int64_t)g * p.heads + h) * p.D * p.E + row * p.E + col;
+  Pack<float, VEC> s;
+#pragma unroll
+  for (int x = 0; x < VEC; ++x) s.v[x] = k.edge && col + x < p.E ? k.edge[mat + x] : 0.f;
   const float full = power2(a * (float)p.split.seg), rest = power2(a * (float)tail);
   const int last = slots - 1;
   const int64_t stride = (k.back ? -1 : 1) * (int64_t)p.heads * size;
   float* at = k.parts + ((first + (k.back ? last : 0)) * p.heads + h) * size + row * p.Ep + col;
-  for (int b = 0; b < slots; b += kAhead) {
-    float u[kAhead];
+  for (int b = 0; b < slots; b += AHEAD) {
+    Pack<float, VEC> u[AHEAD];  // (a part's columns go on to a whole vector)
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j)
-      if (b + j < slots) u[j] = at[stride * (b + j)];
+    for (int j = 0; j < AHEAD; ++j)
+      if (b + j < slots) u[j] = load_pack<float, VEC>(at + stride * (b + j));
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
+    for (int j = 0; j < AHEAD; ++j) {
       if (b + j >= slots) break;
-      at[stride * (b + j)] = s;
-      s = s * ((k.back ? b + j == 0 : b + j == last) ? rest : full) + u[j];
+      store_pack<float, VEC>(at + stride * (b + j), s);
+      const float d = (k.back ? b + j == 0 : b + j == last) ? rest : full;
+#pragma unroll
+      for (int x = 0; x < VEC; ++x) s.v[x] = s.v[x] * d + u[j].v[x];
     }
   }
-  if (k.last) k.last[mat] = s;
+  if (k.last)
+#pragma unroll
+    for (int x = 0; x < VEC; ++x)
+      if (col + x < p.E) k.last[mat + x] = s.v[x];
 }
 
 // ---- outputs -----------------------------------------------------------------
@@ -1325,10 +1338,18 @@ gs_status run_parts_of(const PartsArgs& p, int64_t slots, int parts, cudaStream_
                             dim3(kThreads), kPartsSmem<KD, kTerms>, st, p));
   return GS_OK;
 }
+// A thread has one element while those are fewer than the threads that the machine holds:
+// the loads' latency counts, and 40 of them under way hide it (one group, 19 segments of 16
+// heads of 64: 7 us, with 16 loads 8, with 8 13; with four elements a thread 29).  With more elements
+// the instructions count, and a thread has four (4 groups, 5 segments each, 8 heads of
+// 128: 11.3 us, with one 16).
 gs_status run_scan(const ScanArgs& p, cudaStream_t st) {
-  const int64_t blocks = p.split.groups * div_up(p.D * p.E, kScanThreads);
+  const bool vec = (int64_t)p.split.groups * p.heads * p.D * p.E * p.scans > (int64_t)device_sms() * 2048;
+  const int64_t blocks = p.split.groups * div_up(p.D * div_up(p.E, vec ? 4 : 1), kScanThreads);
   if (blocks > INT32_MAX) return GS_ERR_INVALID_ARG;
-  GS_CUDA(launch_overlapped(attn_scan_kernel, dim3((unsigned)blocks, p.heads, p.scans), dim3(kScanThreads), 0, st, p));
+  const dim3 grid((unsigned)blocks, p.heads, p.scans);
+  GS_CUDA(vec ? launch_overlapped(attn_scan_kernel<4, 8>, grid, dim3(kScanThreads), 0, st, p)
+              : launch_overlapped(attn_scan_kernel<1, 40>, grid, dim3(kScanThreads), 0, st, p));
   return GS_OK;
 }
 
