@@ -538,7 +538,10 @@ __device__ __forceinline__ void sum_part(const PartsArgs& p, const Part& part, i
   if (s.n) st.put(part.to + ((int64_t)blockIdx.x * p.heads + h) * p.Dp * p.Ep + e0, p.Ep);
 }
 
-// TERMS: the most that a part's keys are taken as.
+// TERMS: the most that a part's keys are taken as.  Bound by the loads of rows of 128 bytes:
+// 32640 tokens, 16 heads of 64, bf16, 14 chunks a segment: 33 us for 134 MB (2 terms 27);
+// with neither the weighing nor the products 28, without one of them 29.  Halves of a chunk
+// in turn, one weighed while the other is multiplied, gained nothing (35).
 template <typename T, int KD, int TERMS>
 __global__ void __launch_bounds__(kThreads, 2) attn_parts_kernel(const __grid_constant__ PartsArgs p) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -812,6 +815,10 @@ constexpr int kOutSets = KD == 64 ? 2 : 1;
 template <int KD>
 constexpr int kOutSmem = 1024 + kOutSets<KD> * (2 * (KD / 64) + 1) * kBlock + KD * 128 + (KD == 64 ? 0 : kBlock);
 
+// One pass over a segment's queries, keys and values.  32640 tokens, 16 heads of 64, bf16,
+// forward: 57 us for 273 MB, 4.8 TB/s; no part of the work bounds it alone: taken out by
+// itself, the stores of the outputs are worth 8 us, the decay, the weighing and the state's
+// products 4 or 5 each.  Shared memory is busy for three quarters of a chunk's time.
 template <typename T, int KD>
 __device__ __forceinline__ void form_outputs(const OutArgs& p, int slot, int y, int e0, Control* c, uint32_t tiles,
                                              uint32_t tmem) {
@@ -1065,9 +1072,11 @@ __device__ __forceinline__ void form_kv(const KvArgs& p, int slot, int y, Contro
 }
 
 // ---- all gradients in one launch ------------------------------------------------------
-// Two or three kinds of blocks, the ones that take longest first: an SM's two blocks are
-// then of different kinds, and few are left alone at the end (5003 tokens in 7 groups, heads
-// of 72 and 41: 91 us in three launches, 59 in one).  ED, EE: dim and vdim, padded.
+// Two or three kinds of blocks, the ones that take longest first, so that few are left alone
+// at the end (5003 tokens in 7 groups, heads of 72 and 41: 91 us in three launches, 51 in
+// one).  A segment's blocks next to one another read a quarter less from memory (32640
+// tokens, 16 heads of 64, bf16: 351 MB, as it is 486) and take longer all the same, 195 us
+// instead of 160: the long ones at the end.  ED, EE: dim and vdim, padded.
 struct GradArgs {
   int32_t slots, q_heads, k_heads;
   int32_t first, second;  // where the blocks of a kind end
@@ -1136,7 +1145,8 @@ struct StepArgs {
 
 // One head of one token a block: VEC neighbouring columns of the state a thread, whose
 // rows the block's threads share out; read, updated, written and multiplied by the query
-// in one pass.  Bound by the state's bytes.
+// in one pass.  Bound by the state's bytes: 256 tokens, 16 heads of 64, bf16, 136 MB in 22.9
+// us, 5.9 TB/s; one token 2.3 us, of the call's 7 to 8.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(128) attn_step_kernel(const __grid_constant__ StepArgs p) {
   launch_dependents();
@@ -1340,9 +1350,9 @@ gs_status run_parts_of(const PartsArgs& p, int64_t slots, int parts, cudaStream_
 }
 // A thread has one element while those are fewer than the threads that the machine holds:
 // the loads' latency counts, and 40 of them under way hide it (one group, 19 segments of 16
-// heads of 64: 7 us, with 16 loads 8, with 8 13; with four elements a thread 29).  With more elements
-// the instructions count, and a thread has four (4 groups, 5 segments each, 8 heads of
-// 128: 11.3 us, with one 16).
+// heads of 64: 6 us, with 16 loads 9, with 8 13; with four elements a thread 29).  With
+// more elements the instructions count, and a thread has four (4 groups, 5 segments each, 8
+// heads of 128: 11 us, with one 16).
 gs_status run_scan(const ScanArgs& p, cudaStream_t st) {
   const bool vec = (int64_t)p.split.groups * p.heads * p.D * p.E * p.scans > (int64_t)device_sms() * 2048;
   const int64_t blocks = p.split.groups * div_up(p.D * div_up(p.E, vec ? 4 : 1), kScanThreads);
