@@ -406,6 +406,40 @@ def test_many_groups(gs):
             assert (out[b:e].double().cpu() - want).norm() <= 2 * EPS[q.dtype] * want.norm()
 
 
+@pytest.mark.parametrize("E", [41, 44])
+def test_many_states(gs, E):
+    """More elements of the states than the machine has threads, a group of many segments among short ones."""
+    G, H, D = 60, 4, 40
+    gen = torch.Generator().manual_seed(E)
+    n = torch.randint(0, 90, (G,), generator=gen)
+    n[3], n[17], n[41] = 0, 3001, 300
+    off = torch.cat([torch.zeros(1, dtype=torch.long), n.cumsum(0)])
+    T = int(off[-1])
+    q, k = (_rand(T, H, D, seed=i) for i in range(2))
+    v, do = (_rand(T, H, E, seed=i) for i in (2, 3))
+    a = torch.tensor([-0.2, 0.0, -0.01, -0.001], device="cuda")
+    s0, ds, s, d0 = (torch.randn(G, H, D, E, device="cuda") for _ in range(4))
+    out, dq, dk, dv = (torch.empty_like(t) for t in (v, q, k, v))
+    ws = _attn_ws(gs, T, H, H, D, E, G)
+    kw = dict(group_offsets=off.to(torch.int32).cuda(), state=s0, workspace=ws)
+    gs.gs_linear_attn_fwd(q, k, v, a, out, state_out=s, **kw)
+    gs.gs_linear_attn_bwd(q, k, v, a, do, dq, dk, dv, dstate_out=ds, dstate=d0, **kw)
+    for g in (0, 2, 3, 16, 17, 18, 41, G - 1):
+        b, e = int(off[g]), int(off[g + 1])
+        ins = [t[b:e].double().cpu().requires_grad_(True) for t in (q, k, v)]
+        first = s0[g:g + 1].double().cpu().requires_grad_(True)
+        want, last = plain.attn(*ins, a.cpu(), [0, e - b], first, D ** -0.5)
+        total = (want * do[b:e].double().cpu()).sum() + (last * ds[g:g + 1].double().cpu()).sum()
+        grads = torch.autograd.grad(total, ins + [first], allow_unused=True)
+        # states: keys in two terms or more, 2^-17 each at most, and sums in fp32
+        for x, y in ((s[g], last[0].detach()), (d0[g], grads[3][0])):
+            assert (x.double().cpu() - y).norm() <= 2.0 ** -16 * y.norm()
+        # three roundings to 16 bits that know nothing of one another: sqrt(3) half steps
+        for x, y in ((out, want.detach()), (dq, grads[0]), (dk, grads[1]), (dv, grads[2])):
+            if e > b:
+                assert (x[b:e].double().cpu() - y).norm() <= 2 * EPS[q.dtype] * y.norm()
+
+
 # --------------------------------------------------------------------------
 # waits
 
