@@ -585,10 +585,11 @@ __global__ void __launch_bounds__(kScanThreads) attn_scan_kernel(const __grid_co
   if (i >= p.D * across) return;
   const int row = i / across, col = i % across * VEC, size = p.Dp * p.Ep;
   const float a = log2_decay(p.log_decay, h);
-  const int64_t begin = offset_of(p.split, g), end = offset_of(p.split, g + 1);
-  const int64_t first = begin / p.split.seg + g;
-  const int slots = end > begin ? (int)((end - begin + p.split.seg - 1) / p.split.seg) : 0;
-  const int tail = (int)(end - begin - (int64_t)(slots - 1) * p.split.seg);
+  const uint32_t begin = (uint32_t)offset_of(p.split, g), end = (uint32_t)offset_of(p.split, g + 1);
+  const uint32_t seg = p.split.seg;
+  const int64_t first = begin / seg + g;
+  const int slots = end > begin ? (end - begin + seg - 1) / seg : 0;
+  const int tail = (int)(end - begin - (slots - 1) * seg);
   const int64_t mat = ((int64_t)g * p.heads + h) * p.D * p.E + row * p.E + col;
   Pack<float, VEC> s;
 #pragma unroll
