@@ -1,7 +1,8 @@
 """Network operators (include/gs_net.h): multi-axis rotary positions, gated
 norms, 8-bit activation checkpoints, the gated feed-forward block and linear
-attention with decays, for a network that predicts Gaussians from views.  As in the package itself, each gs_* function only checks and
-marshals its arguments and calls the C ABI function of the same name.
+attention with decays, for a network that predicts Gaussians from views.  As in
+the package itself, each gs_* function only checks and marshals its arguments and
+calls the C ABI function of the same name.
 
 Matrices are CUDA tensors [tokens, channels] whose last axis is contiguous;
 rows may have any stride (a slice of a packed projection, say).
