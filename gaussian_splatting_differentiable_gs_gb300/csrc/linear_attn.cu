@@ -705,15 +705,13 @@ struct Output {
   int64_t stride;       // between the chunk's tokens
   int32_t dim, wide;    // channels from there on; whole granules on 16-byte boundaries
 };
-struct Sums {  // fp32 sums over a key head's query heads, or NULL
+struct Whole {  // outputs in fp32, or NULL
   float* p;             // as Output::p
   int64_t stride;
-  bool first, last;     // of those heads
 };
-// inner + f outer of half a row as 32 T; what the heads before summed is added, and unless
-// this is the last head the sum goes back.
+// inner + f outer of half a row: to memory in fp32, or as 32 T.
 template <typename T>
-__device__ __forceinline__ void get_outputs(uint32_t tmem, float f, const Sums& sums, int pad, uint32_t (&w)[16]) {
+__device__ __forceinline__ void get_outputs(uint32_t tmem, float f, const Whole& whole, int pad, uint32_t (&w)[16]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = warp >> 2, row = (warp & 3) * 32 + lane;
   const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * 32;
   float x[32], y[32];
@@ -726,16 +724,12 @@ __device__ __forceinline__ void get_outputs(uint32_t tmem, float f, const Sums& 
     const float2 v = fma2(make_float2(y[j], y[j + 1]), both(f), make_float2(x[j], x[j + 1]));
     x[j] = v.x, x[j + 1] = v.y;
   }
-  if (sums.p && row >= pad) {
-    float4* to = reinterpret_cast<float4*>(sums.p + (row - pad) * sums.stride + half * 32);
+  if (whole.p) {
+    float4* to = reinterpret_cast<float4*>(whole.p + (row - pad) * whole.stride + half * 32);
+    if (row >= pad)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (!sums.first) {
-        const float4 v = to[j];
-        x[4 * j] += v.x, x[4 * j + 1] += v.y, x[4 * j + 2] += v.z, x[4 * j + 3] += v.w;
-      }
-      if (!sums.last) to[j] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
-    }
+      for (int j = 0; j < 8; ++j) to[j] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+    return;
   }
 #pragma unroll
   for (int j = 0; j < 16; ++j) w[j] = pair_word<T>(x[2 * j], x[2 * j + 1]);
@@ -800,7 +794,6 @@ __device__ __forceinline__ Fit fit_of(Control* c, const State<KD>& st, uint32_t 
 struct OutArgs {
   Split split;
   int32_t heads, rep;    // query heads
-  int32_t shared;        // outputs are summed over the rep query heads of a key head
   Side query, key, value, out;
   const float* log_decay;
   int32_t K, V, Kp, Vp;  // keys' and values' channels, and rounded up to 64 or 128
@@ -809,7 +802,7 @@ struct OutArgs {
   int32_t transposed;    // states are stored [values' channels][keys' channels] (and [Vp][Kp])
   int32_t back, shift;
   float mul_inner, mul_state, mul_key;
-  float* sums;           // [tokens][key heads][Vp], where shared and rep > 1
+  float* whole;          // [tokens][heads][Vp]: instead of out, in fp32, or NULL
 };
 template <int KD>
 constexpr int kOutSets = KD == 64 ? 2 : 1;
@@ -820,8 +813,9 @@ constexpr int kOutSmem = 1024 + kOutSets<KD> * (2 * (KD / 64) + 1) * kBlock + KD
 // forward: 57 us for 273 MB, 4.8 TB/s; no part of the work bounds it alone: taken out by
 // itself, the stores of the outputs are worth 8 us, the decay, the weighing and the state's
 // products 4 or 5 each.  Shared memory is busy for three quarters of a chunk's time.
-template <typename T, int KD>
-__device__ __forceinline__ void form_outputs(const OutArgs& p, int slot, int y, int e0, Control* c, uint32_t tiles,
+// WHOLE: they may be wanted in fp32.
+template <typename T, int KD, bool WHOLE>
+__device__ __forceinline__ void form_outputs(const OutArgs& p, int slot, int h, int e0, Control* c, uint32_t tiles,
                                              uint32_t tmem) {
   constexpr uint32_t kKeys = KD / 64 * kBlock;
   // The weighted keys' terms take the places of the keys and of the queries when these have
@@ -833,103 +827,98 @@ __device__ __forceinline__ void form_outputs(const OutArgs& p, int slot, int y, 
   const uint32_t state = tiles + kSets * kSet;
   const Span s = span_of(p.split, slot);
   const int64_t from = p.back ? s.start + s.n - 1 : s.start, step = p.back ? -1 : 1;
-  const int chunks = (s.n + kL - 1) / kL, reps = p.shared ? p.rep : 1;
+  const int chunks = (s.n + kL - 1) / kL;
   const int row = ((int)threadIdx.x >> 5 & 3) * 32 + ((int)threadIdx.x & 31);
-  const int64_t key_heads = p.heads / p.rep;
+  const bool fp32 = WHOLE && p.whole;
   uint32_t phase = 0, update_phase = 0;
+  if (!s.n) return;
 
-  for (int r = 0; r < (s.n ? reps : 0); ++r) {
-    const int h = p.shared ? y * p.rep + r : y;
-    const float a = log2_decay(p.log_decay, h);
-    const T* q = head_at<T>(p.query, h, p.rep, from);
-    const T* k = head_at<T>(p.key, h, p.rep, from);
-    const T* v = head_at<T>(p.value, h, p.rep, from) + e0;
-    auto load_keys = [&](int i) {
-      load_tile<T, KD>(tiles + i % kSets * kSet + kKeys, k + step * i * kL * p.key.token, step * p.key.token,
-                       min(kL, s.n - i * kL), p.key.dim);
-      copies_commit();
-    };
-    auto load_others = [&](int i) {
-      const int n = min(kL, s.n - i * kL);
-      const int64_t at = step * i * kL;
-      const uint32_t to = tiles + i % kSets * kSet;
-      load_tile<T, KD>(to, q + at * p.query.token, step * p.query.token, n, p.query.dim);
-      load_tile<T, kV>(to + 2 * kKeys, v + at * p.value.token, step * p.value.token, n, p.value.dim - e0);
-      copies_commit();
-    };
-    load_keys(0);
-    load_others(0);
-    if (threadIdx.x < 64) c->decay[threadIdx.x] = threadIdx.x < 32 ? p.mul_inner * power2(a * (float)(31 - (int)threadIdx.x)) : 0.f;
-    State<KD> st;
-    const Stored src = stored(p.states, p.edge, p.Kp, p.Vp, p.K, p.V, p.transposed, (int64_t)slot * p.heads + h,
-                              (int64_t)s.group * p.heads + h);
-    st.get(src.p, src.rs, src.cs, e0, p.K, p.V);
-    const float top_weight = p.mul_key * power2(a * (float)p.shift);
+  const float a = log2_decay(p.log_decay, h);
+  const T* q = head_at<T>(p.query, h, p.rep, from);
+  const T* k = head_at<T>(p.key, h, p.rep, from);
+  const T* v = head_at<T>(p.value, h, p.rep, from) + e0;
+  auto load_keys = [&](int i) {
+    load_tile<T, KD>(tiles + i % kSets * kSet + kKeys, k + step * i * kL * p.key.token, step * p.key.token,
+                     min(kL, s.n - i * kL), p.key.dim);
+    copies_commit();
+  };
+  auto load_others = [&](int i) {
+    const int n = min(kL, s.n - i * kL);
+    const int64_t at = step * i * kL;
+    const uint32_t to = tiles + i % kSets * kSet;
+    load_tile<T, KD>(to, q + at * p.query.token, step * p.query.token, n, p.query.dim);
+    load_tile<T, kV>(to + 2 * kKeys, v + at * p.value.token, step * p.value.token, n, p.value.dim - e0);
+    copies_commit();
+  };
+  load_keys(0);
+  load_others(0);
+  if (threadIdx.x < 64) c->decay[threadIdx.x] = threadIdx.x < 32 ? p.mul_inner * power2(a * (float)(31 - (int)threadIdx.x)) : 0.f;
+  State<KD> st;
+  const Stored src = stored(p.states, p.edge, p.Kp, p.Vp, p.K, p.V, p.transposed, (int64_t)slot * p.heads + h,
+                            (int64_t)s.group * p.heads + h);
+  st.get(src.p, src.rs, src.cs, e0, p.K, p.V);
+  const float top_weight = p.mul_key * power2(a * (float)p.shift);
 
-    const bool last = r + 1 == reps;
-    auto room = [&](int i) { return kSets == 2 ? tiles + (i & 1) * kSet + kKeys : state + KD * 128; };
-    auto put = [&](int i, const uint32_t(&w)[16], int pad) {
-      const int64_t tok = from + step * i * kL;
-      put_outputs<T>(room(i), w, Output{(T*)p.out.p + (int64_t)y * p.out.head + tok * p.out.token + e0,
-                                        step * p.out.token, p.out.dim - e0, p.out.wide}, pad);
-    };
-    uint32_t w[16];
-    for (int i = 0; i < chunks; ++i, phase ^= 1) {
-      const int n = min(kL, s.n - i * kL), pad = kL - n;
-      const uint32_t queries = tiles + i % kSets * kSet, keys = queries + kKeys, values = keys + kKeys;
-      const bool more = i + 1 < chunks;
-      copies_wait<0>();
-      const Fit fit = fit_of<T, KD>(c, st, keys, top_weight);
-      st.template to_tile<T>(state, fit.state);
-      publish();
-      before_sync();
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        after_sync();
-        mma_scores<T, KD, false>(tmem, queries, keys, state);
-        commit(smem_u32(&c->done[0]));
-      }
-      if (more && kSets == 2) load_others(i + 1);
-      if (i > 0 && last) put(i - 1, w, 0);
-      wait_done(c, 0, phase);
+  auto room = [&](int i) { return kSets == 2 ? tiles + (i & 1) * kSet + kKeys : state + KD * 128; };
+  auto put = [&](int i, const uint32_t(&w)[16], int pad) {
+    const int64_t tok = from + step * i * kL;
+    put_outputs<T>(room(i), w, Output{(T*)p.out.p + (int64_t)h * p.out.head + tok * p.out.token + e0,
+                                      step * p.out.token, p.out.dim - e0, p.out.wide}, pad);
+  };
+  uint32_t w[16];
+  for (int i = 0; i < chunks; ++i, phase ^= 1) {
+    const int n = min(kL, s.n - i * kL), pad = kL - n;
+    const uint32_t queries = tiles + i % kSets * kSet, keys = queries + kKeys, values = keys + kKeys;
+    const bool more = i + 1 < chunks;
+    copies_wait<0>();
+    const Fit fit = fit_of<T, KD>(c, st, keys, top_weight);
+    st.template to_tile<T>(state, fit.state);
+    publish();
+    before_sync();
+    __syncthreads();
+    if (threadIdx.x == 0) {
       after_sync();
-      if (more) weigh<T, KD, 2>(keys, keys, queries - keys, a, p.shift, p.mul_key * fit.key);
-      decay_scores<T>(tmem, c, a);
-      publish();
-      before_sync();
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        after_sync();
-        mma_inner<T>(tmem, values);
-        commit(smem_u32(&c->done[1]));
-        if (more) {
-          mma_state<T, KD, 2>(tmem + kUpdate, keys, queries - keys, values);
-          commit(smem_u32(&c->done[2]));
-        }
-      }
-      if (more && kSets == 2) load_keys(i + 1);
-      wait_done(c, 1, phase);
+      mma_scores<T, KD, false>(tmem, queries, keys, state);
+      commit(smem_u32(&c->done[0]));
+    }
+    if (more && kSets == 2) load_others(i + 1);
+    if (i > 0 && !fp32) put(i - 1, w, 0);
+    wait_done(c, 0, phase);
+    after_sync();
+    if (more) weigh<T, KD, 2>(keys, keys, queries - keys, a, p.shift, p.mul_key * fit.key);
+    decay_scores<T>(tmem, c, a);
+    publish();
+    before_sync();
+    __syncthreads();
+    if (threadIdx.x == 0) {
       after_sync();
-      const int64_t tok = from + step * i * kL;
-      const Sums sums{reps > 1 ? p.sums + (tok * key_heads + y) * p.Vp + e0 : nullptr, step * key_heads * p.Vp, r == 0,
-                      last};
-      // (rows before the chunk's first token are not there)
-      get_outputs<T>(tmem, p.mul_state * fit.state_back * power2(a * (float)max(row + 1 - p.shift - pad, 0)), sums, pad,
-                     w);
+      mma_inner<T>(tmem, values);
+      commit(smem_u32(&c->done[1]));
       if (more) {
-        wait_done(c, 2, update_phase);
-        update_phase ^= 1;
-        after_sync();
-        if (kSets == 1) {
-          load_keys(i + 1);
-          load_others(i + 1);
-        }
-        st.update(tmem + kUpdate, power2(a * (float)n), fit.key_back);
+        mma_state<T, KD, 2>(tmem + kUpdate, keys, queries - keys, values);
+        commit(smem_u32(&c->done[2]));
       }
     }
-    if (last) put(chunks - 1, w, kL - (s.n - (chunks - 1) * kL));
-    __syncthreads();  // the next head's loads and decays follow
+    if (more && kSets == 2) load_keys(i + 1);
+    wait_done(c, 1, phase);
+    after_sync();
+    const int64_t tok = from + step * i * kL;
+    const Whole whole{fp32 ? p.whole + (tok * p.heads + h) * p.Vp + e0 : nullptr, step * p.heads * p.Vp};
+    // (rows before the chunk's first token are not there)
+    get_outputs<T>(tmem, p.mul_state * fit.state_back * power2(a * (float)max(row + 1 - p.shift - pad, 0)), whole, pad,
+                   w);
+    if (more) {
+      wait_done(c, 2, update_phase);
+      update_phase ^= 1;
+      after_sync();
+      if (kSets == 1) {
+        load_keys(i + 1);
+        load_others(i + 1);
+      }
+      st.update(tmem + kUpdate, power2(a * (float)n), fit.key_back);
+    }
   }
+  if (!fp32) put(chunks - 1, w, kL - (s.n - (chunks - 1) * kL));
 }
 
 template <typename T, int KD>
@@ -939,7 +928,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_out_kernel(const __grid_cons
   const uint32_t tmem = begin<256>(c);
   launch_dependents();
   wait_for_previous();
-  form_outputs<T, KD>(p, blockIdx.x, blockIdx.y, blockIdx.z * kV, c, smem_u32(smem) + 1024, tmem);
+  form_outputs<T, KD, false>(p, blockIdx.x, blockIdx.y, blockIdx.z * kV, c, smem_u32(smem) + 1024, tmem);
   end<256>(tmem);
 }
 
@@ -956,120 +945,117 @@ struct KvArgs {
   const float* states;  // [slots][heads][64][64], NULL: no group has more than one segment
   const float* edge;    // [groups][heads][dim][vdim] or NULL (zeros)
   float scale;
-  float* sums[2];       // [tokens][key heads][64], where rep > 1: of dk, of dv
+  float* whole[2];      // [tokens][heads][64]: instead of dk and dv, in fp32, or NULL
 };
 constexpr int kKvSmem = 1024 + 6 * kBlock + 64 * 128;  // keys and queries twice, values, douts; the state
 
 template <typename T>
-__device__ __forceinline__ void form_kv(const KvArgs& p, int slot, int y, Control* c, uint32_t tiles, uint32_t tmem) {
+__device__ __forceinline__ void form_kv(const KvArgs& p, int slot, int h, Control* c, uint32_t tiles, uint32_t tmem) {
   // Keys and queries in two pairs of tiles in turn: the next chunk's come while this one's
   // last products are formed, its values and douts while its first scores are.  The weighted
   // queries' terms take the places of keys and values when these have been multiplied.  dv
   // and dk leave through a keys' tile that is not in use while the next scores are formed.
   const uint32_t pairs = tiles, values = pairs + 4 * kBlock, douts = values + kBlock, state = douts + kBlock;
   const Span s = span_of(p.split, slot);
-  const int64_t from = s.start + s.n - 1, key_heads = p.heads / p.rep;
+  const int64_t from = s.start + s.n - 1;
   const int chunks = (s.n + kL - 1) / kL;
   const int row = ((int)threadIdx.x >> 5 & 3) * 32 + ((int)threadIdx.x & 31);
   uint32_t update_phase = 0;
+  if (!s.n) return;
 
-  for (int r = 0; r < (s.n ? p.rep : 0); ++r) {
-    const int h = y * p.rep + r;
-    const float a = log2_decay(p.log_decay, h);
-    auto load_keys = [&](int i) {
-      load_tile<T, 64>(pairs + (i & 1) * 2 * kBlock, head_at<T>(p.k, h, p.rep, from - (int64_t)i * kL), -p.k.token,
-                       min(kL, s.n - i * kL), p.k.dim);
-      copies_commit();
-    };
-    auto load_queries = [&](int i) {
-      load_tile<T, 64>(pairs + (i & 1) * 2 * kBlock + kBlock, head_at<T>(p.q, h, p.rep, from - (int64_t)i * kL),
-                       -p.q.token, min(kL, s.n - i * kL), p.q.dim);
-      copies_commit();
-    };
-    auto load_others = [&](int i) {
-      const int n = min(kL, s.n - i * kL);
-      const int64_t at = from - (int64_t)i * kL;
-      load_tile<T, 64>(douts, head_at<T>(p.g, h, p.rep, at), -p.g.token, n, p.g.dim);
-      load_tile<T, 64>(values, head_at<T>(p.v, h, p.rep, at), -p.v.token, n, p.v.dim);
-      copies_commit();
-    };
-    load_queries(0);
-    load_keys(0);
-    load_others(0);
-    if (threadIdx.x < 64) c->decay[threadIdx.x] = threadIdx.x < 32 ? p.scale * power2(a * (float)(31 - (int)threadIdx.x)) : 0.f;
-    State<64> st;
-    const Stored src = stored(p.states, p.edge, 64, 64, p.D, p.E, 0, (int64_t)slot * p.heads + h,
-                              (int64_t)s.group * p.heads + h);
-    st.get(src.p, src.rs, src.cs, 0, p.D, p.E);
-    const float top_weight = p.scale * power2(a);
+  const float a = log2_decay(p.log_decay, h);
+  auto load_keys = [&](int i) {
+    load_tile<T, 64>(pairs + (i & 1) * 2 * kBlock, head_at<T>(p.k, h, p.rep, from - (int64_t)i * kL), -p.k.token,
+                     min(kL, s.n - i * kL), p.k.dim);
+    copies_commit();
+  };
+  auto load_queries = [&](int i) {
+    load_tile<T, 64>(pairs + (i & 1) * 2 * kBlock + kBlock, head_at<T>(p.q, h, p.rep, from - (int64_t)i * kL),
+                     -p.q.token, min(kL, s.n - i * kL), p.q.dim);
+    copies_commit();
+  };
+  auto load_others = [&](int i) {
+    const int n = min(kL, s.n - i * kL);
+    const int64_t at = from - (int64_t)i * kL;
+    load_tile<T, 64>(douts, head_at<T>(p.g, h, p.rep, at), -p.g.token, n, p.g.dim);
+    load_tile<T, 64>(values, head_at<T>(p.v, h, p.rep, at), -p.v.token, n, p.v.dim);
+    copies_commit();
+  };
+  load_queries(0);
+  load_keys(0);
+  load_others(0);
+  if (threadIdx.x < 64) c->decay[threadIdx.x] = threadIdx.x < 32 ? p.scale * power2(a * (float)(31 - (int)threadIdx.x)) : 0.f;
+  State<64> st;
+  const Stored src = stored(p.states, p.edge, 64, 64, p.D, p.E, 0, (int64_t)slot * p.heads + h,
+                            (int64_t)s.group * p.heads + h);
+  st.get(src.p, src.rs, src.cs, 0, p.D, p.E);
+  const float top_weight = p.scale * power2(a);
 
-    const bool last = r + 1 == p.rep;
-    auto put = [&](int i, const uint32_t(&w)[16], const Side& side, uint32_t room, int pad) {
-      put_outputs<T>(room, w, Output{head_at<T>(side, h, p.rep, from - (int64_t)i * kL), -side.token, side.dim, side.wide},
-                     pad);
-    };
-    uint32_t w[16];
-    for (int i = 0; i < chunks; ++i) {
-      const int n = min(kL, s.n - i * kL), pad = kL - n;
-      const bool more = i + 1 < chunks;
-      const uint32_t keys = pairs + (i & 1) * 2 * kBlock, queries = keys + kBlock, other = pairs + (~i & 1) * 2 * kBlock;
-      copies_wait<1>();  // (values and douts may be on their way)
-      const Fit fit = fit_of<T, 64>(c, st, queries, top_weight);
-      st.template to_tile<T>(state, fit.state);
+  const bool rounded = !p.whole[0];
+  auto put = [&](int i, const uint32_t(&w)[16], const Side& side, uint32_t room, int pad) {
+    put_outputs<T>(room, w, Output{head_at<T>(side, h, p.rep, from - (int64_t)i * kL), -side.token, side.dim, side.wide},
+                   pad);
+  };
+  uint32_t w[16];
+  for (int i = 0; i < chunks; ++i) {
+    const int n = min(kL, s.n - i * kL), pad = kL - n;
+    const bool more = i + 1 < chunks;
+    const uint32_t keys = pairs + (i & 1) * 2 * kBlock, queries = keys + kBlock, other = pairs + (~i & 1) * 2 * kBlock;
+    copies_wait<1>();  // (values and douts may be on their way)
+    const Fit fit = fit_of<T, 64>(c, st, queries, top_weight);
+    st.template to_tile<T>(state, fit.state);
+    publish();
+    before_sync();
+    __syncthreads();
+    const float f = fit.state_back * power2(a * (float)max(row - pad, 0));
+    const int64_t at = ((from - (int64_t)i * kL) * p.heads + h) * 64;
+#pragma unroll
+    for (int ph = 0; ph < 2; ++ph) {  // dv, dk: the first two barriers are used twice a chunk
+      if (threadIdx.x == 0) {
+        after_sync();
+        if (ph == 0) mma_scores<T, 64, false>(tmem, keys, queries, state);
+        else mma_scores<T, 64, true>(tmem, values, douts, state);
+        commit(smem_u32(&c->done[0]));
+      }
+      if (ph == 0) {
+        if (more) load_queries(i + 1);
+        else copies_commit();
+      }
+      if (rounded && (ph || i > 0)) put(ph ? i : i - 1, w, ph ? p.dv : p.dk, other, ph ? pad : 0);
+      wait_done(c, 0, ph);
+      after_sync();
+      if (ph == 1 && more) weigh<T, 64, 2>(queries, keys, values - keys, a, 1, p.scale * fit.key);
+      decay_scores<T>(tmem, c, a);
+      if (ph == 0) copies_wait<1>();  // they are there, the next queries may be on their way
       publish();
       before_sync();
       __syncthreads();
-      const float f = fit.state_back * power2(a * (float)max(row - pad, 0));
-      const int64_t sum = ((from - (int64_t)i * kL) * key_heads + y) * 64;
-#pragma unroll
-      for (int ph = 0; ph < 2; ++ph) {  // dv, dk: the first two barriers are used twice a chunk
-        if (threadIdx.x == 0) {
-          after_sync();
-          if (ph == 0) mma_scores<T, 64, false>(tmem, keys, queries, state);
-          else mma_scores<T, 64, true>(tmem, values, douts, state);
-          commit(smem_u32(&c->done[0]));
-        }
-        if (ph == 0) {
-          if (more) load_queries(i + 1);
-          else copies_commit();
-        }
-        if (last && (ph || i > 0)) put(ph ? i : i - 1, w, ph ? p.dv : p.dk, other, ph ? pad : 0);
-        wait_done(c, 0, ph);
+      if (threadIdx.x == 0) {
         after_sync();
-        if (ph == 1 && more) weigh<T, 64, 2>(queries, keys, values - keys, a, 1, p.scale * fit.key);
-        decay_scores<T>(tmem, c, a);
-        if (ph == 0) copies_wait<1>();  // they are there, the next queries may be on their way
-        publish();
-        before_sync();
-        __syncthreads();
-        if (threadIdx.x == 0) {
-          after_sync();
-          mma_inner<T>(tmem, ph ? queries : douts);
-          commit(smem_u32(&c->done[1]));
-          if (ph == 1 && more) {
-            mma_state<T, 64, 2>(tmem + kUpdate, keys, values - keys, douts);
-            commit(smem_u32(&c->done[2]));
-          }
-        }
-        if (ph == 1 && more) load_keys(i + 1);
-        wait_done(c, 1, ph);
-        after_sync();
-        get_outputs<T>(tmem, f, Sums{p.rep > 1 ? p.sums[1 - ph] + sum : nullptr, -key_heads * 64, r == 0, last}, pad, w);
-        if (ph == 0) {
-          before_sync();
-          __syncthreads();  // the sums in TMEM have been read
-        } else if (more) {
-          wait_done(c, 2, update_phase);
-          update_phase ^= 1;
-          after_sync();
-          load_others(i + 1);
-          st.update(tmem + kUpdate, power2(a * (float)n), fit.key_back);
+        mma_inner<T>(tmem, ph ? queries : douts);
+        commit(smem_u32(&c->done[1]));
+        if (ph == 1 && more) {
+          mma_state<T, 64, 2>(tmem + kUpdate, keys, values - keys, douts);
+          commit(smem_u32(&c->done[2]));
         }
       }
+      if (ph == 1 && more) load_keys(i + 1);
+      wait_done(c, 1, ph);
+      after_sync();
+      get_outputs<T>(tmem, f, Whole{rounded ? nullptr : p.whole[1 - ph] + at, -(int64_t)p.heads * 64}, pad, w);
+      if (ph == 0) {
+        before_sync();
+        __syncthreads();  // the sums in TMEM have been read
+      } else if (more) {
+        wait_done(c, 2, update_phase);
+        update_phase ^= 1;
+        after_sync();
+        load_others(i + 1);
+        st.update(tmem + kUpdate, power2(a * (float)n), fit.key_back);
+      }
     }
-    if (last) put(chunks - 1, w, p.dk, pairs + (~chunks & 1) * 2 * kBlock, kL - (s.n - (chunks - 1) * kL));
-    __syncthreads();  // the next head's loads and decays follow
   }
+  if (rounded) put(chunks - 1, w, p.dk, pairs + (~chunks & 1) * 2 * kBlock, kL - (s.n - (chunks - 1) * kL));
 }
 
 // ---- all gradients in one launch ------------------------------------------------------
@@ -1079,7 +1065,7 @@ __device__ __forceinline__ void form_kv(const KvArgs& p, int slot, int y, Contro
 // tokens, 16 heads of 64, bf16: 351 MB, as it is 486) and take longer all the same, 195 us
 // instead of 160: the long ones at the end.  ED, EE: dim and vdim, padded.
 struct GradArgs {
-  int32_t slots, q_heads, k_heads;
+  int32_t slots, heads;
   int32_t first, second;  // where the blocks of a kind end
   OutArgs dq, dk, dv;
   KvArgs both;            // dk and dv of heads of up to 64 channels
@@ -1097,19 +1083,59 @@ __global__ void __launch_bounds__(kThreads, 2) attn_grad_kernel(const __grid_con
   wait_for_previous();
   const int b = blockIdx.x;
   if (b < p.first) {
-    const int at = b / p.slots, y = at % p.k_heads;
+    const int at = b / p.slots, y = at % p.heads;
     if constexpr (ED == 64 && EE == 64) form_kv<T>(p.both, b % p.slots, y, c, tiles, tmem);
-    else form_outputs<T, EE>(p.dk, b % p.slots, y, at / p.k_heads * kV, c, tiles, tmem);
+    else form_outputs<T, EE, true>(p.dk, b % p.slots, y, at / p.heads * kV, c, tiles, tmem);
   } else if (b < p.second) {
     if constexpr (ED != 64 || EE != 64) {
       const int at = (b - p.first) / p.slots;
-      form_outputs<T, ED>(p.dv, (b - p.first) % p.slots, at % p.k_heads, at / p.k_heads * kV, c, tiles, tmem);
+      form_outputs<T, ED, true>(p.dv, (b - p.first) % p.slots, at % p.heads, at / p.heads * kV, c, tiles, tmem);
     }
   } else {
     const int at = (b - p.second) / p.slots;
-    form_outputs<T, EE>(p.dq, (b - p.second) % p.slots, at % p.q_heads, at / p.q_heads * kV, c, tiles, tmem);
+    form_outputs<T, EE, false>(p.dq, (b - p.second) % p.slots, at % p.heads, at / p.heads * kV, c, tiles, tmem);
   }
   end<256>(tmem);
+}
+
+// ---- gradients of shared heads: the sums over their query heads, in their order ----------
+struct JoinArgs {
+  Split split;
+  int32_t heads, rep;     // key heads
+  const float* whole[2];  // [tokens][query heads][padded]
+  int32_t padded[2];
+  Side to[2];
+};
+// Four channels of a token's head a thread.  Bound by the bytes.  (A block that goes through
+// a key head's query heads itself, its sums in memory between them, needs no such kernel,
+// but takes longer: 32640 tokens, 16 heads of 64 over 4, 543 us, in this way
+// 314.)
+template <typename T>
+__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ JoinArgs p) {
+  launch_dependents();
+  wait_for_previous();
+  const int w = blockIdx.y;
+  const Side& to = p.to[w];
+  const int fours = (to.dim + 3) / 4;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, r = i / fours, token = r / p.heads;
+  const int c = (int)(i % fours) * 4, h = (int)(r % p.heads);
+  if (token < offset_of(p.split, 0) || token >= offset_of(p.split, p.split.groups)) return;
+  const float* from = p.whole[w] + r * p.rep * p.padded[w] + c;
+  float4 v = *reinterpret_cast<const float4*>(from);
+  for (int j = 1; j < p.rep; ++j) {
+    const float4 u = *reinterpret_cast<const float4*>(from + j * p.padded[w]);
+    v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+  }
+  T* out = (T*)to.p + token * to.token + h * to.head + c;
+  const uint32_t lo = pair_word<T>(v.x, v.y), hi = pair_word<T>(v.z, v.w);
+  if (to.wide) {
+    *reinterpret_cast<uint2*>(out) = make_uint2(lo, hi);
+  } else {
+    const uint16_t e[4] = {(uint16_t)lo, (uint16_t)(lo >> 16), (uint16_t)hi, (uint16_t)(hi >> 16)};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (c + j < to.dim) reinterpret_cast<uint16_t*>(out)[j] = e[j];
+  }
 }
 
 // ---- rows that start anywhere, copied to padded rows --------------------------------
@@ -1209,18 +1235,18 @@ constexpr int64_t kMaxTokens = ((int64_t)1 << 31) - 1;
 int padded_dim(int32_t dim) { return dim <= 64 ? 64 : 128; }
 
 // Tokens of a segment.  A chunk of the outputs or of the queries' gradients costs two units
-// of time, of the states' sums one, of the keys' and values' gradients four for each query
-// head of a key head; each segment costs one chunk more for its start and its state.  With
-// two blocks an SM, blocks of one kind run in waves; of several kinds about as long as their
-// work takes and half of the longest.  The sums' and the scan's start costs six; where a
-// group is one segment and its last state is not wanted, there are neither.  The groups'
-// lengths are on the device: they are taken as equal, and a lone segment as long as two of
-// them.  (Backward, 32640 tokens, 16 heads of 64: segments of 7 chunks, as chosen, 234 us, of
-// 15 232; 5003 tokens in 7 groups, 8 and 4 heads of 72 and 41: of 2, as chosen, 90, of 3 99.)
+// of time, of the states' sums one, of the keys' and values' gradients four; each segment
+// costs one chunk more for its start and its state.  With two blocks an SM, blocks of one
+// kind run in waves; of several kinds about as long as their work takes and half of the
+// longest.  The sums' and the scan's start costs six; where a group is one segment and its
+// last state is not wanted, there are neither.  The groups' lengths are on the device: they
+// are taken as equal, and a lone segment as long as two of them.  (Backward, 32640 tokens, 16
+// heads of 64: segments of 7 chunks, as chosen, 231 us, of 15 232; 8160 tokens, 16 and 4
+// heads of 64: of 4, as chosen, 94, of 2 104, of 7 111.)
 int32_t segment_tokens(const gs_linear_attn* a, bool backward, bool states) {
   const int64_t chunks = div_up(div_up(a->tokens, a->groups), kL);
   const int64_t longest = a->groups > 1 ? 2 * chunks : chunks;
-  const int64_t resident = (int64_t)device_sms() * 2, rep = a->q_heads / a->k_heads;
+  const int64_t resident = (int64_t)device_sms() * 2;
   const int64_t tiles = padded_dim(a->vdim) / kV, key_tiles = padded_dim(a->dim) / kV;
   int best = 1;
   int64_t cost = INT64_MAX;
@@ -1231,9 +1257,8 @@ int32_t segment_tokens(const gs_linear_attn* a, bool backward, bool states) {
     int64_t c = 0;
     if (!alone || states) c += div_up(sums, resident) * (n + 1) + 6;
     if (backward) {
-      const int64_t q = 2 * (n + 1), kv = 4 * (n * rep + 1);
-      const int64_t work = segments * (a->q_heads * key_tiles * q + a->k_heads * key_tiles * tiles * kv);
-      const int64_t spread = div_up(work, resident) + kv / 2;
+      const int64_t q = 2 * (n + 1), kv = 4 * (n + 1);
+      const int64_t spread = div_up(segments * a->q_heads * key_tiles * (q + tiles * kv), resident) + kv / 2;
       c += spread > kv ? spread : kv;
     } else {
       c += 2 * div_up(sums, resident) * (n + 1);
@@ -1244,7 +1269,7 @@ int32_t segment_tokens(const gs_linear_attn* a, bool backward, bool states) {
 }
 
 struct Room {
-  float *states, *grads, *sums[2];
+  float *states, *grads, *whole[2];  // (whole: where key heads are shared)
   void* rows[4];
   size_t bytes;
   // copied: the inputs (q, k, v, dout) whose rows have to be copied, a bit each
@@ -1258,11 +1283,11 @@ struct Room {
     };
     const size_t d = padded_dim(a->dim), e = padded_dim(a->vdim);
     const size_t one = sizeof(float) * slots * a->q_heads * d * e;
-    const size_t sum = backward && a->q_heads > a->k_heads ? sizeof(float) * a->tokens * a->k_heads : 0;
+    const size_t heads = backward && a->q_heads > a->k_heads ? sizeof(float) * a->tokens * a->q_heads : 0;
     states = take(one);
     grads = take(backward ? one : 0);
-    sums[0] = take(sum * d);
-    sums[1] = take(sum * e);
+    whole[0] = take(heads * d);
+    whole[1] = take(heads * e);
     const size_t row[4] = {(size_t)a->q_heads * div_up(a->dim, 8), (size_t)a->k_heads * div_up(a->dim, 8),
                            (size_t)a->k_heads * div_up(a->vdim, 8), (size_t)a->q_heads * div_up(a->vdim, 8)};
     for (int i = 0; i < 4; ++i) rows[i] = take(copied >> i & 1 ? 16 * row[i] * a->tokens : 0);
@@ -1465,7 +1490,7 @@ gs_status backward(const gs_linear_attn* a, const Call& c, Side (&s)[7], const f
   dq.transposed = 1;
   dq.mul_state = a->scale;
   dq.mul_key = 1.f;
-  o.back = o.shift = o.shared = 1;
+  o.back = o.shift = 1;
   o.mul_state = 1.f;
   o.mul_key = a->scale;
   o.states = scan ? room.grads : nullptr;
@@ -1474,22 +1499,29 @@ gs_status backward(const gs_linear_attn* a, const Call& c, Side (&s)[7], const f
   dk.query = v, dk.key = g, dk.value = q, dk.out = s[5];
   dk.K = a->vdim, dk.V = a->dim, dk.Kp = c.Ep, dk.Vp = c.Dp;
   dk.transposed = 1;
-  dk.sums = room.sums[0];
+  float* const whole[2] = {c.rep > 1 ? room.whole[0] : nullptr, c.rep > 1 ? room.whole[1] : nullptr};
+  dk.whole = whole[0];
   dv.query = k, dv.key = q, dv.value = g, dv.out = s[6];
   dv.K = a->dim, dv.V = a->vdim, dv.Kp = c.Dp, dv.Vp = c.Ep;
-  dv.sums = room.sums[1];
+  dv.whole = whole[1];
 
   const bool small = c.Dp == 64 && c.Ep == 64;
-  const int64_t first = c.slots * a->k_heads * (small ? 1 : c.Dp / kV);
-  const int64_t second = first + (small ? 0 : c.slots * a->k_heads * (c.Ep / kV));
-  const int64_t blocks = second + c.slots * a->q_heads * (c.Dp / kV);
+  const int64_t blocks_a_tile = c.slots * a->q_heads, first = blocks_a_tile * (small ? 1 : c.Dp / kV);
+  const int64_t second = first + (small ? 0 : blocks_a_tile * (c.Ep / kV));
+  const int64_t blocks = second + blocks_a_tile * (c.Dp / kV);
   if (blocks > INT32_MAX) return GS_ERR_INVALID_ARG;
-  const GradArgs p{(int32_t)c.slots, a->q_heads, a->k_heads, (int32_t)first, (int32_t)second, dq, dk, dv,
+  const GradArgs p{(int32_t)c.slots, a->q_heads, (int32_t)first, (int32_t)second, dq, dk, dv,
                    KvArgs{c.split, a->q_heads, c.rep, q, k, v, g, s[5], s[6], a->dim, a->vdim, a->log_decay, o.states,
-                          o.edge, a->scale, {room.sums[0], room.sums[1]}}};
-  if (c.Dp == 64)
-    return c.Ep == 64 ? run_grad_of<T, 64, 64>(p, blocks, st) : run_grad_of<T, 64, 128>(p, blocks, st);
-  return c.Ep == 64 ? run_grad_of<T, 128, 64>(p, blocks, st) : run_grad_of<T, 128, 128>(p, blocks, st);
+                          o.edge, a->scale, {whole[0], whole[1]}}};
+  const gs_status r =
+      c.Dp == 64 ? (c.Ep == 64 ? run_grad_of<T, 64, 64>(p, blocks, st) : run_grad_of<T, 64, 128>(p, blocks, st))
+                 : (c.Ep == 64 ? run_grad_of<T, 128, 64>(p, blocks, st) : run_grad_of<T, 128, 128>(p, blocks, st));
+  if (r != GS_OK || c.rep == 1) return r;
+  const int64_t joins = div_up(a->tokens * a->k_heads * div_up(a->dim > a->vdim ? a->dim : a->vdim, 4), 256);
+  if (joins > INT32_MAX) return GS_ERR_INVALID_ARG;
+  GS_CUDA(launch_overlapped(attn_join_kernel<T>, dim3((unsigned)joins, 2), dim3(256), 0, st,
+                            JoinArgs{c.split, a->k_heads, c.rep, {whole[0], whole[1]}, {c.Dp, c.Ep}, {s[5], s[6]}}));
+  return GS_OK;
 }
 
 }  // namespace
