@@ -802,7 +802,7 @@ struct OutArgs {
   int32_t transposed;    // states are stored [values' channels][keys' channels] (and [Vp][Kp])
   int32_t back, shift;
   float mul_inner, mul_state, mul_key;
-  float* whole;          // [tokens][heads][Vp]: instead of out, in fp32, or NULL
+  float* whole;          // [tokens][heads][Vp]: instead of out, in fp32
 };
 template <int KD>
 constexpr int kOutSets = KD == 64 ? 2 : 1;
@@ -813,7 +813,7 @@ constexpr int kOutSmem = 1024 + kOutSets<KD> * (2 * (KD / 64) + 1) * kBlock + KD
 // forward: 57 us for 273 MB, 4.8 TB/s; no part of the work bounds it alone: taken out by
 // itself, the stores of the outputs are worth 8 us, the decay, the weighing and the state's
 // products 4 or 5 each.  Shared memory is busy for three quarters of a chunk's time.
-// WHOLE: they may be wanted in fp32.
+// WHOLE: in fp32, instead.
 template <typename T, int KD, bool WHOLE>
 __device__ __forceinline__ void form_outputs(const OutArgs& p, int slot, int h, int e0, Control* c, uint32_t tiles,
                                              uint32_t tmem) {
@@ -829,7 +829,6 @@ __device__ __forceinline__ void form_outputs(const OutArgs& p, int slot, int h, 
   const int64_t from = p.back ? s.start + s.n - 1 : s.start, step = p.back ? -1 : 1;
   const int chunks = (s.n + kL - 1) / kL;
   const int row = ((int)threadIdx.x >> 5 & 3) * 32 + ((int)threadIdx.x & 31);
-  const bool fp32 = WHOLE && p.whole;
   uint32_t phase = 0, update_phase = 0;
   if (!s.n) return;
 
@@ -882,7 +881,7 @@ __device__ __forceinline__ void form_outputs(const OutArgs& p, int slot, int h, 
       commit(smem_u32(&c->done[0]));
     }
     if (more && kSets == 2) load_others(i + 1);
-    if (i > 0 && !fp32) put(i - 1, w, 0);
+    if (i > 0 && !WHOLE) put(i - 1, w, 0);
     wait_done(c, 0, phase);
     after_sync();
     if (more) weigh<T, KD, 2>(keys, keys, queries - keys, a, p.shift, p.mul_key * fit.key);
@@ -903,7 +902,7 @@ __device__ __forceinline__ void form_outputs(const OutArgs& p, int slot, int h, 
     wait_done(c, 1, phase);
     after_sync();
     const int64_t tok = from + step * i * kL;
-    const Whole whole{fp32 ? p.whole + (tok * p.heads + h) * p.Vp + e0 : nullptr, step * p.heads * p.Vp};
+    const Whole whole{WHOLE ? p.whole + (tok * p.heads + h) * p.Vp + e0 : nullptr, step * p.heads * p.Vp};
     // (rows before the chunk's first token are not there)
     get_outputs<T>(tmem, p.mul_state * fit.state_back * power2(a * (float)max(row + 1 - p.shift - pad, 0)), whole, pad,
                    w);
@@ -918,7 +917,7 @@ __device__ __forceinline__ void form_outputs(const OutArgs& p, int slot, int h, 
       st.update(tmem + kUpdate, power2(a * (float)n), fit.key_back);
     }
   }
-  if (!fp32) put(chunks - 1, w, kL - (s.n - (chunks - 1) * kL));
+  if (!WHOLE) put(chunks - 1, w, kL - (s.n - (chunks - 1) * kL));
 }
 
 template <typename T, int KD>
@@ -945,11 +944,11 @@ struct KvArgs {
   const float* states;  // [slots][heads][64][64], NULL: no group has more than one segment
   const float* edge;    // [groups][heads][dim][vdim] or NULL (zeros)
   float scale;
-  float* whole[2];      // [tokens][heads][64]: instead of dk and dv, in fp32, or NULL
+  float* whole[2];      // [tokens][heads][64]: instead of dk and dv, in fp32
 };
 constexpr int kKvSmem = 1024 + 6 * kBlock + 64 * 128;  // keys and queries twice, values, douts; the state
 
-template <typename T>
+template <typename T, bool WHOLE>
 __device__ __forceinline__ void form_kv(const KvArgs& p, int slot, int h, Control* c, uint32_t tiles, uint32_t tmem) {
   // Keys and queries in two pairs of tiles in turn: the next chunk's come while this one's
   // last products are formed, its values and douts while its first scores are.  The weighted
@@ -991,7 +990,6 @@ __device__ __forceinline__ void form_kv(const KvArgs& p, int slot, int h, Contro
   st.get(src.p, src.rs, src.cs, 0, p.D, p.E);
   const float top_weight = p.scale * power2(a);
 
-  const bool rounded = !p.whole[0];
   auto put = [&](int i, const uint32_t(&w)[16], const Side& side, uint32_t room, int pad) {
     put_outputs<T>(room, w, Output{head_at<T>(side, h, p.rep, from - (int64_t)i * kL), -side.token, side.dim, side.wide},
                    pad);
@@ -1021,7 +1019,7 @@ __device__ __forceinline__ void form_kv(const KvArgs& p, int slot, int h, Contro
         if (more) load_queries(i + 1);
         else copies_commit();
       }
-      if (rounded && (ph || i > 0)) put(ph ? i : i - 1, w, ph ? p.dv : p.dk, other, ph ? pad : 0);
+      if (!WHOLE && (ph || i > 0)) put(ph ? i : i - 1, w, ph ? p.dv : p.dk, other, ph ? pad : 0);
       wait_done(c, 0, ph);
       after_sync();
       if (ph == 1 && more) weigh<T, 64, 2>(queries, keys, values - keys, a, 1, p.scale * fit.key);
@@ -1042,7 +1040,7 @@ __device__ __forceinline__ void form_kv(const KvArgs& p, int slot, int h, Contro
       if (ph == 1 && more) load_keys(i + 1);
       wait_done(c, 1, ph);
       after_sync();
-      get_outputs<T>(tmem, f, Whole{rounded ? nullptr : p.whole[1 - ph] + at, -(int64_t)p.heads * 64}, pad, w);
+      get_outputs<T>(tmem, f, Whole{WHOLE ? p.whole[1 - ph] + at : nullptr, -(int64_t)p.heads * 64}, pad, w);
       if (ph == 0) {
         before_sync();
         __syncthreads();  // the sums in TMEM have been read
@@ -1055,7 +1053,7 @@ __device__ __forceinline__ void form_kv(const KvArgs& p, int slot, int h, Contro
       }
     }
   }
-  if (rounded) put(chunks - 1, w, p.dk, pairs + (~chunks & 1) * 2 * kBlock, kL - (s.n - (chunks - 1) * kL));
+  if (!WHOLE) put(chunks - 1, w, p.dk, pairs + (~chunks & 1) * 2 * kBlock, kL - (s.n - (chunks - 1) * kL));
 }
 
 // ---- all gradients in one launch ------------------------------------------------------
@@ -1063,7 +1061,8 @@ __device__ __forceinline__ void form_kv(const KvArgs& p, int slot, int h, Contro
 // at the end (5003 tokens in 7 groups, heads of 72 and 41: 91 us in three launches, 51 in
 // one).  A segment's blocks next to one another read a quarter less from memory (32640
 // tokens, 16 heads of 64, bf16: 351 MB, as it is 486) and take longer all the same, 195 us
-// instead of 160: the long ones at the end.  ED, EE: dim and vdim, padded.
+// instead of 160: the long ones at the end.  ED, EE: dim and vdim, padded.  SHARED: key
+// heads are; dk and dv then leave in fp32, for the join.
 struct GradArgs {
   int32_t slots, heads;
   int32_t first, second;  // where the blocks of a kind end
@@ -1074,7 +1073,7 @@ template <int ED, int EE>
 constexpr int kGradSmem = ED == 64 && EE == 64 ? (kKvSmem > kOutSmem<64> ? kKvSmem : kOutSmem<64>)
                                                : (kOutSmem<64> > kOutSmem<128> ? kOutSmem<64> : kOutSmem<128>);
 
-template <typename T, int ED, int EE>
+template <typename T, int ED, int EE, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 2) attn_grad_kernel(const __grid_constant__ GradArgs p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   Control* c = (Control*)smem;
@@ -1084,12 +1083,12 @@ __global__ void __launch_bounds__(kThreads, 2) attn_grad_kernel(const __grid_con
   const int b = blockIdx.x;
   if (b < p.first) {
     const int at = b / p.slots, y = at % p.heads;
-    if constexpr (ED == 64 && EE == 64) form_kv<T>(p.both, b % p.slots, y, c, tiles, tmem);
-    else form_outputs<T, EE, true>(p.dk, b % p.slots, y, at / p.heads * kV, c, tiles, tmem);
+    if constexpr (ED == 64 && EE == 64) form_kv<T, SHARED>(p.both, b % p.slots, y, c, tiles, tmem);
+    else form_outputs<T, EE, SHARED>(p.dk, b % p.slots, y, at / p.heads * kV, c, tiles, tmem);
   } else if (b < p.second) {
     if constexpr (ED != 64 || EE != 64) {
       const int at = (b - p.first) / p.slots;
-      form_outputs<T, ED, true>(p.dv, (b - p.first) % p.slots, at % p.heads, at / p.heads * kV, c, tiles, tmem);
+      form_outputs<T, ED, SHARED>(p.dv, (b - p.first) % p.slots, at % p.heads, at / p.heads * kV, c, tiles, tmem);
     }
   } else {
     const int at = (b - p.second) / p.slots;
@@ -1108,8 +1107,7 @@ struct JoinArgs {
 };
 // Four channels of a token's head a thread.  Bound by the bytes.  (A block that goes through
 // a key head's query heads itself, its sums in memory between them, needs no such kernel,
-// but takes longer: 32640 tokens, 16 heads of 64 over 4, 543 us, in this way
-// 314.)
+// but takes longer: 32640 tokens, 16 heads of 64 over 4, 543 us, in this way 314.)
 template <typename T>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ JoinArgs p) {
   launch_dependents();
@@ -1400,14 +1398,14 @@ gs_status run_out_of(const OutArgs& p, int64_t slots, cudaStream_t st) {
                             kOutSmem<KD>, st, p));
   return GS_OK;
 }
-template <typename T, int ED, int EE>
+template <typename T, int ED, int EE, bool SHARED>
 gs_status run_grad_of(const GradArgs& p, int64_t blocks, cudaStream_t st) {
   static std::atomic<uint64_t> known{0};
-  if (!allow_smem(attn_grad_kernel<T, ED, EE>, known, kGradSmem<ED, EE>)) {
+  if (!allow_smem(attn_grad_kernel<T, ED, EE, SHARED>, known, kGradSmem<ED, EE>)) {
     (void)cudaGetLastError();
     return GS_ERR_CUDA;
   }
-  GS_CUDA(launch_overlapped(attn_grad_kernel<T, ED, EE>, dim3((unsigned)blocks), dim3(kThreads), kGradSmem<ED, EE>, st,
+  GS_CUDA(launch_overlapped(attn_grad_kernel<T, ED, EE, SHARED>, dim3((unsigned)blocks), dim3(kThreads), kGradSmem<ED, EE>, st,
                             p));
   return GS_OK;
 }
@@ -1424,6 +1422,13 @@ struct Call {
     rep = a->q_heads / a->k_heads;
   }
 };
+
+template <typename T, bool SHARED>
+gs_status run_grad_of(const GradArgs& p, const Call& c, int64_t blocks, cudaStream_t st) {
+  if (c.Dp == 64)
+    return c.Ep == 64 ? run_grad_of<T, 64, 64, SHARED>(p, blocks, st) : run_grad_of<T, 64, 128, SHARED>(p, blocks, st);
+  return c.Ep == 64 ? run_grad_of<T, 128, 64, SHARED>(p, blocks, st) : run_grad_of<T, 128, 128, SHARED>(p, blocks, st);
+}
 
 // The states at the segments' starts (and, with two parts, the gradients at their ends).
 template <typename T>
@@ -1466,6 +1471,8 @@ gs_status forward(const gs_linear_attn* a, const Call& c, Side (&s)[4], float* s
 template <typename T>
 gs_status backward(const gs_linear_attn* a, const Call& c, Side (&s)[7], const float* dstate_out,
                    float* dstate, const Room& room, cudaStream_t st) {
+  const int64_t joins = div_up(a->tokens * a->k_heads * div_up(a->dim > a->vdim ? a->dim : a->vdim, 4), 256);
+  if (joins > INT32_MAX) return GS_ERR_INVALID_ARG;
   const gs_status copied = copy_rows(a, s, 4, room, st);
   if (copied != GS_OK) return copied;
   const Side &q = s[0], &k = s[1], &v = s[2], &g = s[3];
@@ -1513,12 +1520,8 @@ gs_status backward(const gs_linear_attn* a, const Call& c, Side (&s)[7], const f
   const GradArgs p{(int32_t)c.slots, a->q_heads, (int32_t)first, (int32_t)second, dq, dk, dv,
                    KvArgs{c.split, a->q_heads, c.rep, q, k, v, g, s[5], s[6], a->dim, a->vdim, a->log_decay, o.states,
                           o.edge, a->scale, {whole[0], whole[1]}}};
-  const gs_status r =
-      c.Dp == 64 ? (c.Ep == 64 ? run_grad_of<T, 64, 64>(p, blocks, st) : run_grad_of<T, 64, 128>(p, blocks, st))
-                 : (c.Ep == 64 ? run_grad_of<T, 128, 64>(p, blocks, st) : run_grad_of<T, 128, 128>(p, blocks, st));
+  const gs_status r = c.rep > 1 ? run_grad_of<T, true>(p, c, blocks, st) : run_grad_of<T, false>(p, c, blocks, st);
   if (r != GS_OK || c.rep == 1) return r;
-  const int64_t joins = div_up(a->tokens * a->k_heads * div_up(a->dim > a->vdim ? a->dim : a->vdim, 4), 256);
-  if (joins > INT32_MAX) return GS_ERR_INVALID_ARG;
   GS_CUDA(launch_overlapped(attn_join_kernel<T>, dim3((unsigned)joins, 2), dim3(256), 0, st,
                             JoinArgs{c.split, a->k_heads, c.rep, {whole[0], whole[1]}, {c.Dp, c.Ep}, {s[5], s[6]}}));
   return GS_OK;
