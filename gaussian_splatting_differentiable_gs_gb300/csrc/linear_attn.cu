@@ -810,7 +810,7 @@ template <int KD>
 constexpr int kOutSmem = 1024 + kOutSets<KD> * (2 * (KD / 64) + 1) * kBlock + KD * 128 + (KD == 64 ? 0 : kBlock);
 
 // One pass over a segment's queries, keys and values.  32640 tokens, 16 heads of 64, bf16,
-// forward: 57 us for 273 MB, 4.8 TB/s; no part of the work bounds it alone: taken out by
+// forward: 58 us for 273 MB, 4.7 TB/s; no part of the work bounds it alone: taken out by
 // itself, the stores of the outputs are worth 8 us, the decay, the weighing and the state's
 // products 4 or 5 each.  Shared memory is busy for three quarters of a chunk's time.
 // WHOLE: in fp32, instead.
@@ -1107,7 +1107,7 @@ struct JoinArgs {
 };
 // Four channels of a token's head a thread.  Bound by the bytes.  (A block that goes through
 // a key head's query heads itself, its sums in memory between them, needs no such kernel,
-// but takes longer: 32640 tokens, 16 heads of 64 over 4, 543 us, in this way 314.)
+// but takes longer: 32640 tokens, 16 heads of 64 over 4, 543 us, in this way 309.)
 template <typename T>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ JoinArgs p) {
   launch_dependents();
