@@ -300,8 +300,9 @@ typedef struct gs_attn_heads {   /* [tokens][heads][channels]                 */
  *   workspace   at most gs_linear_attn_workspace_bytes(a, backward) bytes (0:
  *               refused; rows of q, k, v and dout that do not start on 16-byte
  *               boundaries, or are no multiple of 8 long, are copied there
- *               first), 16-byte aligned, no initialisation; calls on one
- *               workspace must not overlap */
+ *               first; in the backward pass of shared key heads, dk and dv of each
+ *               query head in fp32), 16-byte aligned, no initialisation; calls
+ *               on one workspace must not overlap */
 size_t gs_linear_attn_workspace_bytes(const gs_linear_attn* a, int32_t backward);
 gs_status gs_linear_attn_fwd(const gs_linear_attn* a, const gs_attn_heads* heads,
                              float* state_out, void* workspace, size_t ws_bytes, void* stream);
