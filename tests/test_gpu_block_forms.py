@@ -382,6 +382,31 @@ def test_attention_past_two_to_the_31_elements(gs):
     gs.gs_linear_attn_status()
 
 
+def test_shared_heads_past_two_to_the_31_elements(gs):
+    """2.2e9 elements of the query heads' gradients: the last and the first tokens' beside those of a call on the last
+    ones alone, and of one on the first with the state gradient that the others leave."""
+    T, H, K, D = 2200000, 16, 2, 64
+    cut = T - 1000
+    q, do = (torch.empty(T, H, D, dtype=torch.bfloat16, device="cuda").normal_() for _ in range(2))
+    k, v = (torch.empty(T, K, D, dtype=torch.bfloat16, device="cuda").normal_() for _ in range(2))
+    a = -torch.exp2(-8.0 * torch.arange(1, H + 1, device="cuda") / H)
+    ws = _attn_ws(gs, T, H, K, D, D)
+    close = lambda x, y: (x.float() - y.float()).norm() <= 2 * EPS[q.dtype] * y.float().norm()  # noqa: E731
+    dq, dk, dv = (torch.empty_like(t) for t in (q, k, v))
+    gs.gs_linear_attn_bwd(q, k, v, a, do, dq, dk, dv, workspace=ws)
+    tail = [torch.empty_like(t[cut:]) for t in (q, k, v)]
+    gs.gs_linear_attn_bwd(q[cut:], k[cut:], v[cut:], a, do[cut:], *tail, workspace=ws)
+    assert close(dk[cut:], tail[1]) and close(dv[cut:], tail[2])
+    mid = torch.empty(1, H, D, D, device="cuda")
+    rest = [torch.empty_like(t[1000:]) for t in (q, k, v)]
+    gs.gs_linear_attn_bwd(q[1000:], k[1000:], v[1000:], a, do[1000:], *rest, dstate=mid, workspace=ws)
+    first = [torch.empty_like(t[:1000]) for t in (q, k, v)]
+    gs.gs_linear_attn_bwd(q[:1000], k[:1000], v[:1000], a, do[:1000], *first, dstate_out=mid, workspace=ws)
+    for x, y in zip((dq, dk, dv), first):
+        assert close(x[:1000], y)
+    gs.gs_linear_attn_status()
+
+
 def test_many_groups(gs):
     """Thousands of short groups, some empty, against each alone in a few."""
     G, H, D = 5000, 2, 16
