@@ -20,7 +20,8 @@
 // Tokens are split into segments.  One kernel sums each segment's own part of the state,
 // a second one goes through the segments' parts and leaves each one's state at its start
 // and a group's last state, a third one forms the outputs, segment by segment, with the
-// state in registers (fp32) between a segment's chunks.
+// state in registers (fp32) between a segment's chunks.  Where query heads share a key
+// head, its gradients leave in fp32 for each of them and a fourth kernel sums these.
 //
 // Products are on the tensor cores (tcgen05, 128 rows), sums and states fp32.  What is
 // rounded to the inputs' type on the way: the decayed products q_i k_j, and the state
