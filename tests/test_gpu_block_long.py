@@ -1,0 +1,188 @@
+"""Linear attention with several chunks a segment, and the feed-forward block's sums that are
+shared out, against 64-bit forms: what large calls use.
+
+Tolerances come from the arithmetic.  Linear attention: as in test_gpu_linear_attn.py (EPS of
+the magnitudes for the two roundings to the type and half a step of the result); states are
+sums in fp32 of chunks of 128 tokens, whose keys are 3 terms at most (24 cuts of 2^-23 on the
+tensor cores) with weights of up to nine powers (2^-22 each), decayed once a chunk.
+Feed-forward block: test_gpu_ffn.py's bounds."""
+import pytest
+import torch
+
+import test_gpu_ffn as few
+
+pytestmark = pytest.mark.gpu
+
+EPS = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
+TINY = {torch.bfloat16: 1e-38, torch.float16: 2.0 ** -24}
+CHUNK = 128
+PARTIALS = 4 * 128 * 256 * 4 * 96  # bytes of the partial sums of dw, the workspace's last part
+
+
+@pytest.fixture(scope="module")
+def gs():
+    import __graft_entry__
+    __graft_entry__.build()
+    import gaussian_splatting_differentiable_gs_gb300 as gs
+    return gs
+
+
+def _close(got, want, bound, what):
+    got = got.double()
+    assert got.shape == want.shape
+    over = ~((got - want).abs() <= bound)
+    assert not over.any(), (what, int(over.sum()), float((got - want).abs().max()),
+                            float(((got - want).abs() / bound).max()))
+
+
+def _attn(q, k, v, a, offsets, state, scale):
+    """(out, last states) of [T, h, D] heads, every pair of tokens at once; differentiable."""
+    T, h, _ = q.shape
+    rep = h // k.shape[1]
+    q, k, v = (x.transpose(0, 1) for x in (q, k.repeat_interleave(rep, 1), v.repeat_interleave(rep, 1)))
+    off = torch.tensor(offsets, device=q.device)
+    at = torch.arange(T, device=q.device)
+    of = torch.searchsorted(off[1:].contiguous(), at, right=True)  # a token's group; past the last: none
+    inside = of < len(offsets) - 1
+    gap = at[:, None] - at
+    a = a.double()[:, None, None]
+    decay = torch.where((gap >= 0) & (of[:, None] == of) & inside, torch.exp(a * gap.clamp(min=0)), 0.0)
+    of = of.clamp(max=len(offsets) - 2)
+    out = ((q @ k.transpose(1, 2)) * decay) @ v
+    left = torch.where(inside, torch.exp(a[:, 0] * (off[1:][of] - 1 - at).clamp(min=0)), 0.0)
+    part = k * left[..., None]
+    last = torch.stack([part[:, b:e].transpose(1, 2) @ v[:, b:e] for b, e in zip(offsets, offsets[1:])])
+    if state is not None:
+        since = torch.where(inside, torch.exp(a[:, 0] * (at - off[:-1][of] + 1)), 0.0)
+        out = out + since[..., None] * (q[:, :, None] @ state.transpose(0, 1)[:, of])[:, :, 0]
+        last = last + torch.exp(a[None] * (off[1:] - off[:-1])[:, None, None, None]) * state
+    return scale * out.transpose(0, 1), last
+
+
+def _results(q, k, v, a, offsets, state, scale, do, dlast):
+    """out, last states, dq, dk, dv, dstate."""
+    leaves = [x.detach().clone().requires_grad_(True) for x in (q, k, v, state)]
+    out, last = _attn(*leaves[:3], a, offsets, leaves[3], scale)
+    return [out.detach(), last.detach()] + list(
+        torch.autograd.grad((out * do).sum() + (last * dlast).sum(), leaves))
+
+
+def _check_attn(call, dt, T, H, K, D, E, offsets, seed, pick):
+    """`call` runs both directions; the key heads `pick` and their query heads are looked at."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    q, do = rand(T, H, D).to(dt), rand(T, H, E).to(dt)
+    k, v = rand(T, K, D).to(dt), rand(T, K, E).to(dt)
+    off = [0, T] if offsets is None else offsets
+    G, scale, rep, end = len(off) - 1, D ** -0.5, H // K, off[-1]
+    a = -torch.exp2(-12.0 * torch.rand(H, generator=g, device="cuda"))
+    a[::5] = 0.0
+    s0, ds = rand(G, H, D, E), rand(G, H, D, E)
+    out, dq, dk, dv = (torch.full_like(x, 9.0) for x in (do, q, k, v))
+    last, d0 = (torch.full_like(s0, 9.0) for _ in range(2))
+    offs = None if offsets is None else torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    call(q, k, v, a, offs, s0, scale, out, last, do, dq, dk, dv, ds, d0)
+    for x in (out, dq, dk, dv):
+        assert (x[end:] == 9.0).all()
+    eps, chunks = EPS[dt], -(-T // CHUNK)
+    for key in pick:
+        hs, ks = slice(key * rep, (key + 1) * rep), slice(key, key + 1)
+        ins = [x.double() for x in (q[:, hs], k[:, ks], v[:, ks], a[hs])], [x.double() for x in (
+            s0[:, hs], do[:, hs], ds[:, hs])]
+        want = _results(*ins[0], off, ins[1][0], scale, *ins[1][1:])
+        mag = _results(*[x.abs() for x in ins[0][:3]], ins[0][3], off, ins[1][0].abs(), scale,
+                       *[x.abs() for x in ins[1][1:]])
+        got = [out[:, hs], last[:, hs], dq[:, hs], dk[:, ks], dv[:, ks], d0[:, hs]]
+        for i, name in enumerate(("out", "last states", "dq", "dk", "dv", "dstate")):
+            if i in (1, 5):
+                _close(got[i], want[i], (2.0 ** -17 + chunks * 2.0 ** -20) * mag[i] + 1e-37, (name, key))
+            else:
+                _close(got[i][:end], want[i][:end], (want[i].abs() * eps + (eps * 1.01 + 2.0 ** -14) * mag[i]
+                                                     + TINY[dt] * (1 + mag[i]))[:end], (name, key))
+
+
+# (dim, vdim), tokens, query heads, key heads, groups: heads so many that segments of several
+# chunks are chosen
+LONG = [
+    (64, 64, 700, 256, 256, None),
+    (64, 64, 1000, 160, 40, None),
+    (72, 41, 700, 160, 40, None),
+    (72, 41, 650, 96, 96, [0, 130, 130, 641]),
+    (64, 128, 700, 96, 96, None),
+    (128, 64, 1000, 64, 16, None),
+    (128, 128, 700, 128, 32, None),
+    (128, 128, 1000, 64, 64, [0, 999]),
+]
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("D,E,T,H,K,offsets", LONG)
+def test_attention_of_many_heads(gs, dt, D, E, T, H, K, offsets):
+    G = 1 if offsets is None else len(offsets) - 1
+    ws = torch.full((gs.gs_linear_attn_workspace_bytes(T, H, K, D, E, G),), 0xff, dtype=torch.uint8, device="cuda")
+
+    def call(q, k, v, a, offs, s0, scale, out, last, do, dq, dk, dv, ds, d0):
+        kw = dict(group_offsets=offs, state=s0, scale=scale, workspace=ws)
+        gs.gs_linear_attn_fwd(q, k, v, a, out, state_out=last, **kw)
+        gs.gs_linear_attn_bwd(q, k, v, a, do, dq, dk, dv, dstate_out=ds, dstate=d0, **kw)
+
+    _check_attn(call, dt, T, H, K, D, E, offsets, T + D, (0, 1, K // 2, K - 1))
+    gs.gs_linear_attn_status()
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("T,C,F,pad,offset,shared", [
+    (1400, 64, 64, 0, 0, True),        # one tile of dw, shared by several pairs
+    (2000, 130, 97, 3, 1, True),       # odd channels and hidden, rows that start anywhere
+    (3000, 520, 300, 0, 0, True),
+    (1300, 1500, 1801, 0, 0, False),   # more tiles of dw than pairs, too short to be shared
+    (1700, 1500, 1801, 0, 0, True),    # and with a rest that is
+    (2600, 776, 2500, 8, 0, True),
+])
+def test_shared_sums_of_the_weight_gradient(gs, dt, T, C, F, pad, offset, shared):
+    g = torch.Generator().manual_seed(T + C)
+    x, xd = few._mat(T, C, dt, g, pad=pad, offset=offset)
+    w, wd = few._mat(2 * F, C, dt, g, std=C ** -0.5, pad=pad, offset=offset)
+    dh, dhd = few._mat(T, F, dt, g, pad=pad, offset=offset)
+    ws = torch.zeros(gs.gs_ffn_workspace_bytes(T, C, F), dtype=torch.uint8, device="cuda")
+    ws[256:] = 0xff
+    want = few._bounds(xd, wd, dhd, "silu", dt)
+    h, _ = few._empty(T, F, dt, pad, offset)
+    gs.gs_ffn_fwd(x, w, h, ws)
+    few._close(h, *want["h"], "h")
+    for dw_dt in (dt, torch.float32):
+        dx, dx_all = few._empty(T, C, dt, pad, offset)
+        dw, dw_all = few._empty(2 * F, C, dw_dt, pad, offset)
+        gs.gs_ffn_bwd(x, w, dh, dx, dw, ws)
+        few._close(dx, *few._stored(*want["dx"], dt), "dx")
+        few._close(dw, *few._stored(*want["dw"], dw_dt), "dw")
+        if dw_dt is torch.float32:
+            start = torch.randn(2 * F, C, generator=g)
+            added, added_all = few._empty(2 * F, C, dw_dt, pad, offset)
+            added.copy_(start)
+            gs.gs_ffn_bwd(x, w, dh, None, added, ws, accumulate=True)
+            assert torch.equal(added, start.cuda() + dw)
+            added.fill_(9.0)
+            assert (added_all == 9.0).all()
+        dx.fill_(9.0)
+        dw.fill_(9.0)
+        assert (dx_all == 9.0).all() and (dw_all == 9.0).all()
+    assert bool((ws[-PARTIALS:] != 0xff).any()) == shared
+    assert gs.gs_workspace_status(ws) == gs.GS_OK
+
+
+def test_many_tiles_a_pair(gs):
+    """Forward and dx of over twice as many tiles as there are pairs."""
+    dt, T, C, F = torch.bfloat16, 5300, 2060, 1100
+    g = torch.Generator().manual_seed(1)
+    x, xd = few._mat(T, C, dt, g)
+    w, wd = few._mat(2 * F, C, dt, g, std=C ** -0.5)
+    dh, dhd = few._mat(T, F, dt, g)
+    ws = torch.zeros(gs.gs_ffn_workspace_bytes(T, C, F), dtype=torch.uint8, device="cuda")
+    want = few._bounds(xd, wd, dhd, "gelu", dt)
+    h, dx = torch.empty(T, F, dtype=dt, device="cuda"), torch.empty(T, C, dtype=dt, device="cuda")
+    gs.gs_ffn_fwd(x, w, h, ws, act="gelu")
+    few._close(h, *want["h"], "h")
+    gs.gs_ffn_bwd(x, w, dh, dx, None, ws, act="gelu")
+    few._close(dx, *few._stored(*want["dx"], dt), "dx")
+    assert gs.gs_workspace_status(ws) == gs.GS_OK
