@@ -58,6 +58,7 @@ struct Split {  // tokens in groups, groups in segments
   int64_t tokens;
   const int32_t* offsets;  // NULL: one group
   int32_t groups, seg;
+  int64_t from, upto;      // only segments that start in these tokens
 };
 
 // Segment `slot` of the groups one after the other.  Group g's segments begin at slot
@@ -82,7 +83,18 @@ __device__ __forceinline__ Span span_of(const Split& s, int64_t slot) {
   }
   const int64_t in = slot - first_slot(s, lo), begin = offset_of(s, lo), end = offset_of(s, lo + 1);
   const int64_t start = begin + in * s.seg, left = end - start;
-  return Span{lo, start, in < 0 || left <= 0 ? 0 : (int)(left < s.seg ? left : s.seg)};
+  return Span{lo, start, in < 0 || left <= 0 || start < s.from || start >= s.upto ? 0 : (int)(left < s.seg ? left : s.seg)};
+}
+// The first token of the segment that a token of the groups is in.
+__device__ __forceinline__ int64_t segment_start(const Split& s, int64_t token) {
+  int lo = 0, hi = s.groups - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (offset_of(s, mid) <= token) lo = mid;
+    else hi = mid - 1;
+  }
+  const int64_t begin = offset_of(s, lo);
+  return begin + (token - begin) / s.seg * s.seg;
 }
 
 // Set where a wait for the tensor core ran out (gs_linear_attn_status).
@@ -803,7 +815,7 @@ struct OutArgs {
   int32_t transposed;    // states are stored [values' channels][keys' channels] (and [Vp][Kp])
   int32_t back, shift;
   float mul_inner, mul_state, mul_key;
-  float* whole;          // [tokens][heads][Vp]: instead of out, in fp32
+  float* whole;          // [tokens from split.from][heads][Vp]: instead of out, in fp32
 };
 template <int KD>
 constexpr int kOutSets = KD == 64 ? 2 : 1;
@@ -903,7 +915,8 @@ __device__ __forceinline__ void form_outputs(const OutArgs& p, int slot, int h, 
     wait_done(c, 1, phase);
     after_sync();
     const int64_t tok = from + step * i * kL;
-    const Whole whole{WHOLE ? p.whole + (tok * p.heads + h) * p.Vp + e0 : nullptr, step * p.heads * p.Vp};
+    const Whole whole{WHOLE ? p.whole + ((tok - p.split.from) * p.heads + h) * p.Vp + e0 : nullptr,
+                      step * p.heads * p.Vp};
     // (rows before the chunk's first token are not there)
     get_outputs<T>(tmem, p.mul_state * fit.state_back * power2(a * (float)max(row + 1 - p.shift - pad, 0)), whole, pad,
                    w);
@@ -945,7 +958,7 @@ struct KvArgs {
   const float* states;  // [slots][heads][64][64], NULL: no group has more than one segment
   const float* edge;    // [groups][heads][dim][vdim] or NULL (zeros)
   float scale;
-  float* whole[2];      // [tokens][heads][64]: instead of dk and dv, in fp32
+  float* whole[2];      // [tokens from split.from][heads][64]: instead of dk and dv, in fp32
 };
 constexpr int kKvSmem = 1024 + 6 * kBlock + 64 * 128;  // keys and queries twice, values, douts; the state
 
@@ -1007,7 +1020,7 @@ __device__ __forceinline__ void form_kv(const KvArgs& p, int slot, int h, Contro
     before_sync();
     __syncthreads();
     const float f = fit.state_back * power2(a * (float)max(row - pad, 0));
-    const int64_t at = ((from - (int64_t)i * kL) * p.heads + h) * 64;
+    const int64_t at = ((from - p.split.from - (int64_t)i * kL) * p.heads + h) * 64;
 #pragma unroll
     for (int ph = 0; ph < 2; ++ph) {  // dv, dk: the first two barriers are used twice a chunk
       if (threadIdx.x == 0) {
@@ -1065,7 +1078,7 @@ __device__ __forceinline__ void form_kv(const KvArgs& p, int slot, int h, Contro
 // instead of 160: the long ones at the end.  ED, EE: dim and vdim, padded.  SHARED: key
 // heads are; dk and dv then leave in fp32, for the join.
 struct GradArgs {
-  int32_t slots, heads;
+  int32_t slot0, slots, heads;
   int32_t first, second;  // where the blocks of a kind end
   OutArgs dq, dk, dv;
   KvArgs both;            // dk and dv of heads of up to 64 channels
@@ -1081,19 +1094,16 @@ __global__ void __launch_bounds__(kThreads, 2) attn_grad_kernel(const __grid_con
   const uint32_t tmem = begin<256>(c), tiles = smem_u32(smem) + 1024;
   launch_dependents();
   wait_for_previous();
-  const int b = blockIdx.x;
-  if (b < p.first) {
-    const int at = b / p.slots, y = at % p.heads;
-    if constexpr (ED == 64 && EE == 64) form_kv<T, SHARED>(p.both, b % p.slots, y, c, tiles, tmem);
-    else form_outputs<T, EE, SHARED>(p.dk, b % p.slots, y, at / p.heads * kV, c, tiles, tmem);
-  } else if (b < p.second) {
-    if constexpr (ED != 64 || EE != 64) {
-      const int at = (b - p.first) / p.slots;
-      form_outputs<T, ED, SHARED>(p.dv, (b - p.first) % p.slots, at % p.heads, at / p.heads * kV, c, tiles, tmem);
-    }
+  const int kind = (int)blockIdx.x < p.first ? 0 : (int)blockIdx.x < p.second ? 1 : 2;
+  const int b = blockIdx.x - (kind == 0 ? 0 : kind == 1 ? p.first : p.second);
+  const int at = b / p.slots, slot = p.slot0 + b % p.slots, h = at % p.heads, e0 = at / p.heads * kV;
+  if (kind == 0) {
+    if constexpr (ED == 64 && EE == 64) form_kv<T, SHARED>(p.both, slot, h, c, tiles, tmem);
+    else form_outputs<T, EE, SHARED>(p.dk, slot, h, e0, c, tiles, tmem);
+  } else if (kind == 1) {
+    if constexpr (ED != 64 || EE != 64) form_outputs<T, ED, SHARED>(p.dv, slot, h, e0, c, tiles, tmem);
   } else {
-    const int at = (b - p.second) / p.slots;
-    form_outputs<T, EE, false>(p.dq, (b - p.second) % p.slots, at % p.heads, at / p.heads * kV, c, tiles, tmem);
+    form_outputs<T, EE, false>(p.dq, slot, h, e0, c, tiles, tmem);
   }
   end<256>(tmem);
 }
@@ -1102,7 +1112,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_grad_kernel(const __grid_con
 struct JoinArgs {
   Split split;
   int32_t heads, rep;     // key heads
-  const float* whole[2];  // [tokens][query heads][padded]
+  const float* whole[2];  // [tokens from split.from][query heads][padded]
   int32_t padded[2];
   Side to[2];
 };
@@ -1116,9 +1126,14 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   const int w = blockIdx.y;
   const Side& to = p.to[w];
   const int fours = (to.dim + 3) / 4;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, r = i / fours, token = r / p.heads;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, r = i / fours, token = p.split.from + r / p.heads;
   const int c = (int)(i % fours) * 4, h = (int)(r % p.heads);
   if (token < offset_of(p.split, 0) || token >= offset_of(p.split, p.split.groups)) return;
+  // a segment at an end of the range belongs to the one that it starts in
+  if (token >= p.split.upto || (p.split.from && token < p.split.from + p.split.seg)) {
+    const int64_t start = segment_start(p.split, token);
+    if (start < p.split.from || start >= p.split.upto) return;
+  }
   const float* from = p.whole[w] + r * p.rep * p.padded[w] + c;
   float4 v = *reinterpret_cast<const float4*>(from);
   for (int j = 1; j < p.rep; ++j) {
@@ -1233,6 +1248,42 @@ constexpr int64_t kMaxTokens = ((int64_t)1 << 31) - 1;
 
 int padded_dim(int32_t dim) { return dim <= 64 ? 64 : 128; }
 
+// Backward with shared key heads: the gradients of keys and values wait in fp32, one for each
+// query head, for their sum.  That is as much as two states for each 64 tokens, so they are
+// formed in ranges of tokens for which there is room.  A range's segments start in it; where
+// groups start anywhere, the last ones reach beyond it by less than a segment.  (32640 tokens,
+// 16 heads of 64 over 4, bf16: in one range 304 us, in two 316, in four 345; 8160 tokens: 93,
+// 107 and 133; 2000 tokens, 16 over 2: 39, 58 and 85.)
+size_t two_states(const gs_linear_attn* a, int64_t seg) {  // for each seg tokens, and each group's rest
+  return sizeof(float) * 2 * (a->tokens / seg + a->groups) * a->q_heads * padded_dim(a->dim) * padded_dim(a->vdim);
+}
+// Tokens that there is room for in so many bytes.
+int64_t room_for(const gs_linear_attn* a, size_t bytes) {
+  const int64_t n = (int64_t)(bytes / (sizeof(float) * a->q_heads * (padded_dim(a->dim) + padded_dim(a->vdim))));
+  return n < a->tokens ? n : a->tokens;
+}
+// Tokens of a range, all of about the same length (0: there is no room for one).
+int64_t range_of(const gs_linear_attn* a, bool anywhere, int64_t seg, int64_t room) {
+  if (room >= a->tokens) return a->tokens;
+  const int64_t most = anywhere ? room - seg : room / seg * seg;
+  if (most <= 0) return 0;
+  const int64_t even = div_up(a->tokens, div_up(a->tokens, most));
+  return anywhere ? even : div_up(even, seg) * seg;
+}
+// The bytes that states and ranges should do with: two states of the wider head for each 64
+// tokens and each group, and two more.
+size_t modest(const gs_linear_attn* a) {
+  gs_linear_attn square = *a;
+  square.dim = square.vdim = a->dim > a->vdim ? a->dim : a->vdim;
+  square.groups = a->groups + 1;
+  return two_states(&square, 64);
+}
+bool in_two_ranges(const gs_linear_attn* a, int64_t seg) {
+  const size_t all = modest(a), states = two_states(a, seg);
+  const int64_t range = range_of(a, a->groups > 1, seg, room_for(a, all > states ? all - states : 0));
+  return !a->tokens || (range && div_up(a->tokens, range) <= 2);
+}
+
 // Tokens of a segment.  A chunk of the outputs or of the queries' gradients costs two units
 // of time, of the states' sums one, of the keys' and values' gradients four; each segment
 // costs one chunk more for its start and its state.  With two blocks an SM, blocks of one
@@ -1247,9 +1298,11 @@ int32_t segment_tokens(const gs_linear_attn* a, bool backward, bool states) {
   const int64_t longest = a->groups > 1 ? 2 * chunks : chunks;
   const int64_t resident = (int64_t)device_sms() * 2;
   const int64_t tiles = padded_dim(a->vdim) / kV, key_tiles = padded_dim(a->dim) / kV;
-  int best = 1;
+  const bool shared = backward && a->q_heads > a->k_heads;
+  int best = 16;
   int64_t cost = INT64_MAX;
   for (int m = 1; m <= 16; ++m) {
+    if (shared && !in_two_ranges(a, m * kL)) continue;  // (states of longer segments take less room)
     const bool alone = longest <= m;
     const int64_t n = alone ? longest : m, segments = a->groups * (alone ? 1 : div_up(chunks, m));
     const int64_t sums = segments * a->q_heads * tiles * (backward ? 2 : 1);
@@ -1268,11 +1321,12 @@ int32_t segment_tokens(const gs_linear_attn* a, bool backward, bool states) {
 }
 
 struct Room {
-  float *states, *grads, *whole[2];  // (whole: where key heads are shared)
+  float *states, *grads, *whole[2];
   void* rows[4];
   size_t bytes;
-  // copied: the inputs (q, k, v, dout) whose rows have to be copied, a bit each
-  Room(void* ws, const gs_linear_attn* a, int64_t slots, bool backward, int copied) {
+  // copied: the inputs (q, k, v, dout) whose rows have to be copied, a bit each; joined: tokens
+  // whose gradients of keys and values wait for their sum over the query heads
+  Room(void* ws, const gs_linear_attn* a, int64_t slots, bool backward, int copied, int64_t joined) {
     char* base = (char*)ws;
     size_t at = 0;
     auto take = [&](size_t n) {
@@ -1282,7 +1336,7 @@ struct Room {
     };
     const size_t d = padded_dim(a->dim), e = padded_dim(a->vdim);
     const size_t one = sizeof(float) * slots * a->q_heads * d * e;
-    const size_t heads = backward && a->q_heads > a->k_heads ? sizeof(float) * a->tokens * a->q_heads : 0;
+    const size_t heads = sizeof(float) * joined * a->q_heads;
     states = take(one);
     grads = take(backward ? one : 0);
     whole[0] = take(heads * d);
@@ -1416,7 +1470,7 @@ struct Call {
   int64_t slots;
   int Dp, Ep, rep;
   Call(const gs_linear_attn* a, bool backward, bool states) {
-    split = Split{a->tokens, a->group_offsets, a->groups, segment_tokens(a, backward, states)};
+    split = Split{a->tokens, a->group_offsets, a->groups, segment_tokens(a, backward, states), 0, a->tokens};
     slots = a->tokens / split.seg + a->groups;
     Dp = padded_dim(a->dim);
     Ep = padded_dim(a->vdim);
@@ -1471,9 +1525,14 @@ gs_status forward(const gs_linear_attn* a, const Call& c, Side (&s)[4], float* s
 
 template <typename T>
 gs_status backward(const gs_linear_attn* a, const Call& c, Side (&s)[7], const float* dstate_out,
-                   float* dstate, const Room& room, cudaStream_t st) {
-  const int64_t joins = div_up(a->tokens * a->k_heads * div_up(a->dim > a->vdim ? a->dim : a->vdim, 4), 256);
-  if (joins > INT32_MAX) return GS_ERR_INVALID_ARG;
+                   float* dstate, const Room& room, int64_t range, cudaStream_t st) {
+  // the largest launches
+  const bool small = c.Dp == 64 && c.Ep == 64;
+  auto slots_of = [&](int64_t from, int64_t upto) { return (upto - 1) / c.split.seg + a->groups - from / c.split.seg; };
+  const int64_t kinds = (small ? 1 : c.Dp / kV + c.Ep / kV) + c.Dp / kV;
+  const int64_t fours = a->k_heads * div_up(a->dim > a->vdim ? a->dim : a->vdim, 4);
+  if (slots_of(0, a->tokens) * a->q_heads * kinds > INT32_MAX || div_up((range + c.split.seg) * fours, 256) > INT32_MAX)
+    return GS_ERR_INVALID_ARG;
   const gs_status copied = copy_rows(a, s, 4, room, st);
   if (copied != GS_OK) return copied;
   const Side &q = s[0], &k = s[1], &v = s[2], &g = s[3];
@@ -1484,47 +1543,53 @@ gs_status backward(const gs_linear_attn* a, const Call& c, Side (&s)[7], const f
                      {Scan{a->state, nullptr, room.states, 0}, Scan{dstate_out, dstate, room.grads, 1}}, 2, st);
     if (r != GS_OK) return r;
   }
-  OutArgs o{};
-  o.split = c.split;
-  o.heads = a->q_heads;
-  o.rep = c.rep;
-  o.log_decay = a->log_decay;
-  o.mul_inner = a->scale;
-  OutArgs dq = o;
-  dq.query = g, dq.key = v, dq.value = k, dq.out = s[4];
-  dq.K = a->vdim, dq.V = a->dim, dq.Kp = c.Ep, dq.Vp = c.Dp;
-  dq.states = scan ? room.states : nullptr;
-  dq.edge = a->state;
-  dq.transposed = 1;
-  dq.mul_state = a->scale;
-  dq.mul_key = 1.f;
-  o.back = o.shift = 1;
-  o.mul_state = 1.f;
-  o.mul_key = a->scale;
-  o.states = scan ? room.grads : nullptr;
-  o.edge = dstate_out;
-  OutArgs dk = o, dv = o;
-  dk.query = v, dk.key = g, dk.value = q, dk.out = s[5];
-  dk.K = a->vdim, dk.V = a->dim, dk.Kp = c.Ep, dk.Vp = c.Dp;
-  dk.transposed = 1;
-  float* const whole[2] = {c.rep > 1 ? room.whole[0] : nullptr, c.rep > 1 ? room.whole[1] : nullptr};
-  dk.whole = whole[0];
-  dv.query = k, dv.key = q, dv.value = g, dv.out = s[6];
-  dv.K = a->dim, dv.V = a->vdim, dv.Kp = c.Dp, dv.Vp = c.Ep;
-  dv.whole = whole[1];
+  for (int64_t from = 0; from < a->tokens; from += range) {
+    OutArgs o{};
+    o.split = c.split;
+    o.split.from = from;
+    o.split.upto = from + range < a->tokens ? from + range : a->tokens;
+    o.heads = a->q_heads;
+    o.rep = c.rep;
+    o.log_decay = a->log_decay;
+    o.mul_inner = a->scale;
+    OutArgs dq = o;
+    dq.query = g, dq.key = v, dq.value = k, dq.out = s[4];
+    dq.K = a->vdim, dq.V = a->dim, dq.Kp = c.Ep, dq.Vp = c.Dp;
+    dq.states = scan ? room.states : nullptr;
+    dq.edge = a->state;
+    dq.transposed = 1;
+    dq.mul_state = a->scale;
+    dq.mul_key = 1.f;
+    o.back = o.shift = 1;
+    o.mul_state = 1.f;
+    o.mul_key = a->scale;
+    o.states = scan ? room.grads : nullptr;
+    o.edge = dstate_out;
+    OutArgs dk = o, dv = o;
+    dk.query = v, dk.key = g, dk.value = q, dk.out = s[5];
+    dk.K = a->vdim, dk.V = a->dim, dk.Kp = c.Ep, dk.Vp = c.Dp;
+    dk.transposed = 1;
+    float* const whole[2] = {c.rep > 1 ? room.whole[0] : nullptr, c.rep > 1 ? room.whole[1] : nullptr};
+    dk.whole = whole[0];
+    dv.query = k, dv.key = q, dv.value = g, dv.out = s[6];
+    dv.K = a->dim, dv.V = a->vdim, dv.Kp = c.Dp, dv.Vp = c.Ep;
+    dv.whole = whole[1];
 
-  const bool small = c.Dp == 64 && c.Ep == 64;
-  const int64_t blocks_a_tile = c.slots * a->q_heads, first = blocks_a_tile * (small ? 1 : c.Dp / kV);
-  const int64_t second = first + (small ? 0 : blocks_a_tile * (c.Ep / kV));
-  const int64_t blocks = second + blocks_a_tile * (c.Dp / kV);
-  if (blocks > INT32_MAX) return GS_ERR_INVALID_ARG;
-  const GradArgs p{(int32_t)c.slots, a->q_heads, (int32_t)first, (int32_t)second, dq, dk, dv,
-                   KvArgs{c.split, a->q_heads, c.rep, q, k, v, g, s[5], s[6], a->dim, a->vdim, a->log_decay, o.states,
-                          o.edge, a->scale, {whole[0], whole[1]}}};
-  const gs_status r = c.rep > 1 ? run_grad_of<T, true>(p, c, blocks, st) : run_grad_of<T, false>(p, c, blocks, st);
-  if (r != GS_OK || c.rep == 1) return r;
-  GS_CUDA(launch_overlapped(attn_join_kernel<T>, dim3((unsigned)joins, 2), dim3(256), 0, st,
-                            JoinArgs{c.split, a->k_heads, c.rep, {whole[0], whole[1]}, {c.Dp, c.Ep}, {s[5], s[6]}}));
+    const int64_t slots = slots_of(from, o.split.upto), blocks_a_tile = slots * a->q_heads;
+    const int64_t first = blocks_a_tile * (small ? 1 : c.Dp / kV);
+    const int64_t second = first + (small ? 0 : blocks_a_tile * (c.Ep / kV));
+    const GradArgs p{(int32_t)(from / c.split.seg), (int32_t)slots, a->q_heads, (int32_t)first, (int32_t)second, dq, dk, dv,
+                     KvArgs{o.split, a->q_heads, c.rep, q, k, v, g, s[5], s[6], a->dim, a->vdim, a->log_decay, o.states,
+                            o.edge, a->scale, {whole[0], whole[1]}}};
+    const int64_t blocks = blocks_a_tile * kinds;
+    const gs_status r = c.rep > 1 ? run_grad_of<T, true>(p, c, blocks, st) : run_grad_of<T, false>(p, c, blocks, st);
+    if (r != GS_OK) return r;
+    if (c.rep == 1) continue;
+    const int64_t reach = o.split.upto + (a->group_offsets ? c.split.seg : 0);
+    const int64_t joins = div_up(((reach < a->tokens ? reach : a->tokens) - from) * fours, 256);
+    GS_CUDA(launch_overlapped(attn_join_kernel<T>, dim3((unsigned)joins, 2), dim3(256), 0, st,
+                              JoinArgs{o.split, a->k_heads, c.rep, {whole[0], whole[1]}, {c.Dp, c.Ep}, {s[5], s[6]}}));
+  }
   return GS_OK;
 }
 
@@ -1538,7 +1603,13 @@ extern "C" size_t gs_linear_attn_workspace_bytes(const gs_linear_attn* a, int32_
   size_t most = 0;
   for (int states = 0; states < 2; ++states) {
     const Call c(a, backward != 0, states != 0);
-    const size_t n = Room(nullptr, a, c.slots, backward != 0, backward ? 15 : 7).bytes;
+    size_t n = Room(nullptr, a, c.slots, backward != 0, backward ? 15 : 7, 0).bytes;
+    if (backward && c.rep > 1) {
+      // as few ranges as a modest room allows, four at most
+      const int64_t left = room_for(a, modest(a) > n ? modest(a) - n : 0), least = div_up(a->tokens, 4) + 2 * c.split.seg;
+      const int64_t joined = left > least ? left : least;
+      n = Room(nullptr, a, c.slots, true, 15, joined < a->tokens ? joined : a->tokens).bytes;
+    }
     if (n > most) most = n;
   }
   return most;
@@ -1552,7 +1623,7 @@ extern "C" gs_status gs_linear_attn_fwd(const gs_linear_attn* a, const gs_attn_h
   if (a->tokens > 0 && (!side(&s[0], a, &heads[0], a->dim, false, false) || !side(&s[1], a, &heads[1], a->dim, true, false) ||
                         !side(&s[2], a, &heads[2], a->vdim, true, false) || !side(&s[3], a, &heads[3], a->vdim, false, true)))
     return GS_ERR_INVALID_ARG;
-  const Room room(workspace, a, c.slots, false, a->tokens > 0 ? to_copy(s, 3) : 0);
+  const Room room(workspace, a, c.slots, false, a->tokens > 0 ? to_copy(s, 3) : 0, 0);
   if (!workspace || !aligned16(workspace) || ws_bytes < room.bytes) return GS_ERR_INVALID_ARG;
   cudaStream_t st = (cudaStream_t)stream;
   if (a->tokens == 0 && !state_out) return GS_OK;
@@ -1576,16 +1647,20 @@ extern "C" gs_status gs_linear_attn_bwd(const gs_linear_attn* a, const gs_attn_h
        !side(&s[4], a, &heads[4], a->dim, false, true) || !side(&s[5], a, &heads[5], a->dim, true, true) ||
        !side(&s[6], a, &heads[6], a->vdim, true, true)))
     return GS_ERR_INVALID_ARG;
-  const Room room(workspace, a, c.slots, true, a->tokens > 0 ? to_copy(s, 4) : 0);
-  if (!workspace || !aligned16(workspace) || ws_bytes < room.bytes) return GS_ERR_INVALID_ARG;
+  const int copied = a->tokens > 0 ? to_copy(s, 4) : 0;
+  const size_t others = Room(nullptr, a, c.slots, true, copied, 0).bytes;
+  const int64_t joined = c.rep > 1 ? room_for(a, ws_bytes > others ? ws_bytes - others : 0) : 0;
+  const int64_t range = c.rep > 1 ? range_of(a, a->group_offsets != nullptr, c.split.seg, joined) : a->tokens;
+  const Room room(workspace, a, c.slots, true, copied, joined);
+  if (!workspace || !aligned16(workspace) || ws_bytes < room.bytes || (a->tokens > 0 && range == 0)) return GS_ERR_INVALID_ARG;
   cudaStream_t st = (cudaStream_t)stream;
   if (a->tokens == 0 && !dstate) return GS_OK;
   if (a->tokens == 0) {
     return run_scan(ScanArgs{c.split, a->q_heads, a->dim, a->vdim, c.Dp, c.Ep, a->log_decay,
                              {Scan{dstate_out, dstate, room.grads, 1}, Scan{}}, 1}, st);
   }
-  return a->dtype == GS_BF16 ? backward<__nv_bfloat16>(a, c, s, dstate_out, dstate, room, st)
-                             : backward<__half>(a, c, s, dstate_out, dstate, room, st);
+  return a->dtype == GS_BF16 ? backward<__nv_bfloat16>(a, c, s, dstate_out, dstate, room, range, st)
+                             : backward<__half>(a, c, s, dstate_out, dstate, room, range, st);
 }
 
 extern "C" gs_status gs_linear_attn_status(void* stream) {

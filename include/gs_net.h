@@ -300,9 +300,12 @@ typedef struct gs_attn_heads {   /* [tokens][heads][channels]                 */
  *   workspace   at most gs_linear_attn_workspace_bytes(a, backward) bytes (0:
  *               refused; rows of q, k, v and dout that do not start on 16-byte
  *               boundaries, or are no multiple of 8 long, are copied there
- *               first; in the backward pass of shared key heads, dk and dv of each
- *               query head in fp32), 16-byte aligned, no initialisation; calls
- *               on one workspace must not overlap */
+ *               first), 16-byte aligned, no initialisation; calls on one
+ *               workspace must not overlap.  In the backward pass of shared
+ *               key heads dk and dv of each query head lie there in fp32, for
+ *               as many tokens at a time as there is room for: with less room
+ *               (two segments of at most 2048 tokens at least) there are more
+ *               launches, and the same results */
 size_t gs_linear_attn_workspace_bytes(const gs_linear_attn* a, int32_t backward);
 gs_status gs_linear_attn_fwd(const gs_linear_attn* a, const gs_attn_heads* heads,
                              float* state_out, void* workspace, size_t ws_bytes, void* stream);

@@ -186,3 +186,44 @@ def test_many_tiles_a_pair(gs):
     gs.gs_ffn_bwd(x, w, dh, dx, None, ws, act="gelu")
     few._close(dx, *few._stored(*want["dx"], dt), "dx")
     assert gs.gs_workspace_status(ws) == gs.GS_OK
+
+
+@pytest.mark.parametrize("dt,D,E,offsets", [
+    (torch.bfloat16, 64, 64, None),
+    (torch.float16, 64, 64, [0, 333, 333, 901, 1400]),
+    (torch.float16, 72, 41, [0, 7, 650, 1500]),
+    (torch.bfloat16, 40, 128, [3, 129, 131, 1111, 1499]),
+    (torch.bfloat16, 128, 128, None),
+])
+def test_shared_heads_with_little_room(gs, dt, D, E, offsets):
+    """Gradients of shared heads with room for all tokens and for ever fewer: the same bits,
+    nothing beside the room, until the call is refused."""
+    T, H, K = 1500, 8, 2
+    g = torch.Generator(device="cuda").manual_seed(D)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    q, k, v, do = (rand(T, h, d).to(dt) for h, d in ((H, D), (K, D), (K, E), (H, E)))
+    G = 1 if offsets is None else len(offsets) - 1
+    a, s0, ds = -torch.exp2(-rand(H).abs() * 8), rand(G, H, D, E), rand(G, H, D, E)
+    offs = None if offsets is None else torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    token = 4 * H * sum(64 if d <= 64 else 128 for d in (D, E))
+    asked = gs.gs_linear_attn_workspace_bytes(T, H, K, D, E, G)
+    room = torch.empty(asked + T * token, dtype=torch.uint8, device="cuda")
+
+    def run(size):
+        room.fill_(0xff)
+        out = [torch.full_like(x, 9.0) for x in (q, k, v, s0)]
+        gs.gs_linear_attn_bwd(q, k, v, a, do, *out[:3], group_offsets=offs, state=s0, dstate_out=ds, dstate=out[3],
+                              workspace=room[:size])
+        assert (room[size:] == 0xff).all()
+        return out
+
+    want = run(room.numel())
+    assert all(torch.equal(x, y) for x, y in zip(want, run(asked)))
+    sizes, size = 0, asked
+    try:
+        while size > 0:
+            assert all(torch.equal(x, y) for x, y in zip(want, run(size))), size
+            sizes, size = sizes + 1, size - 100 * token
+    except gs.GSError:
+        pass
+    assert sizes >= 3 and size > 0
