@@ -44,6 +44,11 @@ constexpr int kThreads = 256;
 constexpr int kBlock = kL * 128;  // bytes of 64 channels of a chunk
 constexpr unsigned int kErrTimeout = 1u;
 constexpr int64_t kWaitNs = 2000000000;
+// What the products of a block are limited to: in the self-test fewer than it waits for.
+struct Limits {
+  uint32_t products;  // sets of products
+  int64_t wait_ns;    // after a block's first wait, its last one gives up
+};
 // The keys' channels are padded to KD = 64 or 128.
 
 struct Side {  // heads that are read or written
@@ -59,6 +64,7 @@ struct Split {  // tokens in groups, groups in segments
   const int32_t* offsets;  // NULL: one group
   int32_t groups, seg;
   int64_t from, upto;      // only segments that start in these tokens
+  Limits limits;
 };
 
 // Segment `slot` of the groups one after the other.  Group g's segments begin at slot
@@ -131,9 +137,6 @@ __device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uin
       "r"((uint32_t)add)
       : "memory");
 }
-__device__ __forceinline__ void commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
 __device__ __forceinline__ void before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 // What this thread wrote to shared memory is there for the tensor core (after a barrier).
@@ -141,30 +144,57 @@ __device__ __forceinline__ void publish() { asm volatile("fence.proxy.async.shar
 
 struct Control {
   uint64_t done[3];
+  uint32_t issued[3];         // 1 + the phase that the last products issued end, or 0
   uint32_t tmem;
-  volatile uint32_t abort;
+  volatile int64_t until;     // when waiting ends; 0: nothing has been waited for
+  volatile uint32_t abort;    // a wait gave up
   float top[2][kThreads / 32];
   alignas(16) float decay[64];  // mul d^(31 - i), then zeros
 };
 static_assert(sizeof(Control) <= 1024, "control");
-// Waits for products; at most two seconds in all, after which nothing is waited for any
-// more, the results are undefined and the error is on record.
-__device__ __forceinline__ void wait_done(Control* c, int which, uint32_t parity) {
-  const uint32_t bar = smem_u32(&c->done[which]);
-  if (!mbar_try(bar, parity)) {
-    const int64_t t0 = now_ns();
-    while (!mbar_try(bar, parity) && !c->abort)
-      if (now_ns() - t0 > kWaitNs) {
-        c->abort = 1;
-        atomicOr(&attn_timeouts, kErrTimeout);
-      }
+// Products by one thread; once a wait of its has given up, or the limit is reached, none are
+// issued any more.
+struct Products {
+  Control* c;
+  int64_t wait_ns;
+  uint32_t left;
+  __device__ __forceinline__ Products(Control* control, const Limits& l) : c(control), wait_ns(l.wait_ns), left(l.products) {}
+  __device__ __forceinline__ bool issues() {  // (of thread 0)
+    if (!left) return false;
+    --left;
+    return true;
   }
-  __syncwarp();  // the warp's accesses to TMEM are in step
-}
+  __device__ __forceinline__ void commit(int which, uint32_t parity) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&c->done[which]))
+                 : "memory");
+    c->issued[which] = parity + 1;
+  }
+  // Waits for products; at most two seconds from the block's first wait on, after which nothing
+  // is waited for any more, the results are undefined and the error is on record.
+  __device__ __forceinline__ void wait(int which, uint32_t parity) {
+    const uint32_t bar = smem_u32(&c->done[which]);
+    if (!mbar_try(bar, parity)) {
+      int64_t until = c->until;
+      if (!until) c->until = until = now_ns() + wait_ns;  // (threads that do so together mean the same)
+      while (!mbar_try(bar, parity)) {
+        if (c->abort) {
+          left = 0;
+          break;
+        }
+        if (now_ns() > until) {
+          c->abort = 1;
+          atomicOr(&attn_timeouts, kErrTimeout);
+        }
+      }
+    }
+    __syncwarp();  // the warp's accesses to TMEM are in step
+  }
+};
 template <int COLUMNS>
 __device__ __forceinline__ uint32_t begin(Control* c) {
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&c->done[i]), 1);
+    for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&c->done[i]), 1), c->issued[i] = 0;
+    c->until = 0;
     c->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -179,11 +209,23 @@ __device__ __forceinline__ uint32_t begin(Control* c) {
   after_sync();
   return c->tmem;
 }
+// After giving up, nothing is under way when the block ends that writes its shared memory or
+// TMEM: its threads wait for their own copies, one of them, again for two seconds at most, for
+// the products that were issued and their arrivals (one at most on each barrier).
 template <int COLUMNS>
-__device__ __forceinline__ void end(uint32_t tmem) {
+__device__ __forceinline__ void end(Control* c, const Limits& limits, uint32_t tmem) {
   before_sync();
   __syncthreads();
   after_sync();
+  if (c->abort) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (threadIdx.x == 0) {
+      const int64_t until = now_ns() + limits.wait_ns;
+      for (int i = 0; i < 3; ++i)
+        while (c->issued[i] && !mbar_try(smem_u32(&c->done[i]), c->issued[i] - 1) && now_ns() < until) {}
+    }
+    __syncthreads();
+  }
   if (threadIdx.x >> 5 == 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(COLUMNS));
 }
@@ -510,6 +552,7 @@ __device__ __forceinline__ void sum_part(const PartsArgs& p, const Part& part, i
                        min(kL, s.n - i * kL), part.value.dim - e0);
     copies_commit();
   };
+  Products products(c, p.split.limits);
   State<KD> st;
   st.zero();
 #pragma unroll
@@ -536,13 +579,13 @@ __device__ __forceinline__ void sum_part(const PartsArgs& p, const Part& part, i
     publish();
     before_sync();
     __syncthreads();
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0 && products.issues()) {
       after_sync();
       mma_state<T, KD, TERMS>(tmem, terms, kTerm, values_of(i));
-      commit(smem_u32(&c->done[0]));
+      products.commit(0, i & 1);
     }
     if (kSets == 2) load_keys(i + kSets);
-    wait_done(c, 0, i & 1);
+    products.wait(0, i & 1);
     after_sync();
     if (kSets == 1) load_keys(i + kSets);
     load_values(i + kSets);
@@ -566,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_parts_kernel(const __grid_co
   const Part& part = p.part[blockIdx.z / blocks];
   if (TERMS == 2 || !part.exact) sum_part<T, KD, 2>(p, part, e0, c, smem_u32(smem) + 1024, tmem);
   else sum_part<T, KD, TERMS>(p, part, e0, c, smem_u32(smem) + 1024, tmem);
-  end<64>(tmem);
+  end<64>(c, p.split.limits, tmem);
 }
 
 
@@ -844,6 +887,7 @@ __device__ __forceinline__ void form_outputs(const OutArgs& p, int slot, int h, 
   const int row = ((int)threadIdx.x >> 5 & 3) * 32 + ((int)threadIdx.x & 31);
   uint32_t phase = 0, update_phase = 0;
   if (!s.n) return;
+  Products products(c, p.split.limits);
 
   const float a = log2_decay(p.log_decay, h);
   const T* q = head_at<T>(p.query, h, p.rep, from);
@@ -888,31 +932,31 @@ __device__ __forceinline__ void form_outputs(const OutArgs& p, int slot, int h, 
     publish();
     before_sync();
     __syncthreads();
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0 && products.issues()) {
       after_sync();
       mma_scores<T, KD, false>(tmem, queries, keys, state);
-      commit(smem_u32(&c->done[0]));
+      products.commit(0, phase);
     }
     if (more && kSets == 2) load_others(i + 1);
     if (i > 0 && !WHOLE) put(i - 1, w, 0);
-    wait_done(c, 0, phase);
+    products.wait(0, phase);
     after_sync();
     if (more) weigh<T, KD, 2>(keys, keys, queries - keys, a, p.shift, p.mul_key * fit.key);
     decay_scores<T>(tmem, c, a);
     publish();
     before_sync();
     __syncthreads();
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0 && products.issues()) {
       after_sync();
       mma_inner<T>(tmem, values);
-      commit(smem_u32(&c->done[1]));
+      products.commit(1, phase);
       if (more) {
         mma_state<T, KD, 2>(tmem + kUpdate, keys, queries - keys, values);
-        commit(smem_u32(&c->done[2]));
+        products.commit(2, update_phase);
       }
     }
     if (more && kSets == 2) load_keys(i + 1);
-    wait_done(c, 1, phase);
+    products.wait(1, phase);
     after_sync();
     const int64_t tok = from + step * i * kL;
     const Whole whole{WHOLE ? p.whole + ((tok - p.split.from) * p.heads + h) * p.Vp + e0 : nullptr,
@@ -921,7 +965,7 @@ __device__ __forceinline__ void form_outputs(const OutArgs& p, int slot, int h, 
     get_outputs<T>(tmem, p.mul_state * fit.state_back * power2(a * (float)max(row + 1 - p.shift - pad, 0)), whole, pad,
                    w);
     if (more) {
-      wait_done(c, 2, update_phase);
+      products.wait(2, update_phase);
       update_phase ^= 1;
       after_sync();
       if (kSets == 1) {
@@ -942,7 +986,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_out_kernel(const __grid_cons
   launch_dependents();
   wait_for_previous();
   form_outputs<T, KD, false>(p, blockIdx.x, blockIdx.y, blockIdx.z * kV, c, smem_u32(smem) + 1024, tmem);
-  end<256>(tmem);
+  end<256>(c, p.split.limits, tmem);
 }
 
 // ---- the gradients of keys and values together -----------------------------------
@@ -975,6 +1019,7 @@ __device__ __forceinline__ void form_kv(const KvArgs& p, int slot, int h, Contro
   const int row = ((int)threadIdx.x >> 5 & 3) * 32 + ((int)threadIdx.x & 31);
   uint32_t update_phase = 0;
   if (!s.n) return;
+  Products products(c, p.split.limits);
 
   const float a = log2_decay(p.log_decay, h);
   auto load_keys = [&](int i) {
@@ -1023,18 +1068,18 @@ __device__ __forceinline__ void form_kv(const KvArgs& p, int slot, int h, Contro
     const int64_t at = ((from - p.split.from - (int64_t)i * kL) * p.heads + h) * 64;
 #pragma unroll
     for (int ph = 0; ph < 2; ++ph) {  // dv, dk: the first two barriers are used twice a chunk
-      if (threadIdx.x == 0) {
+      if (threadIdx.x == 0 && products.issues()) {
         after_sync();
         if (ph == 0) mma_scores<T, 64, false>(tmem, keys, queries, state);
         else mma_scores<T, 64, true>(tmem, values, douts, state);
-        commit(smem_u32(&c->done[0]));
+        products.commit(0, ph);
       }
       if (ph == 0) {
         if (more) load_queries(i + 1);
         else copies_commit();
       }
       if (!WHOLE && (ph || i > 0)) put(ph ? i : i - 1, w, ph ? p.dv : p.dk, other, ph ? pad : 0);
-      wait_done(c, 0, ph);
+      products.wait(0, ph);
       after_sync();
       if (ph == 1 && more) weigh<T, 64, 2>(queries, keys, values - keys, a, 1, p.scale * fit.key);
       decay_scores<T>(tmem, c, a);
@@ -1042,24 +1087,24 @@ __device__ __forceinline__ void form_kv(const KvArgs& p, int slot, int h, Contro
       publish();
       before_sync();
       __syncthreads();
-      if (threadIdx.x == 0) {
+      if (threadIdx.x == 0 && products.issues()) {
         after_sync();
         mma_inner<T>(tmem, ph ? queries : douts);
-        commit(smem_u32(&c->done[1]));
+        products.commit(1, ph);
         if (ph == 1 && more) {
           mma_state<T, 64, 2>(tmem + kUpdate, keys, values - keys, douts);
-          commit(smem_u32(&c->done[2]));
+          products.commit(2, update_phase);
         }
       }
       if (ph == 1 && more) load_keys(i + 1);
-      wait_done(c, 1, ph);
+      products.wait(1, ph);
       after_sync();
       get_outputs<T>(tmem, f, Whole{WHOLE ? p.whole[1 - ph] + at : nullptr, -(int64_t)p.heads * 64}, pad, w);
       if (ph == 0) {
         before_sync();
         __syncthreads();  // the sums in TMEM have been read
       } else if (more) {
-        wait_done(c, 2, update_phase);
+        products.wait(2, update_phase);
         update_phase ^= 1;
         after_sync();
         load_others(i + 1);
@@ -1105,7 +1150,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_grad_kernel(const __grid_con
   } else {
     form_outputs<T, EE, false>(p.dq, slot, h, e0, c, tiles, tmem);
   }
-  end<256>(tmem);
+  end<256>(c, p.dq.split.limits, tmem);
 }
 
 // ---- gradients of shared heads: the sums over their query heads, in their order ----------
@@ -1469,8 +1514,10 @@ struct Call {
   Split split;
   int64_t slots;
   int Dp, Ep, rep;
-  Call(const gs_linear_attn* a, bool backward, bool states) {
-    split = Split{a->tokens, a->group_offsets, a->groups, segment_tokens(a, backward, states), 0, a->tokens};
+  // chunks: of a segment; 0: as many as is best
+  Call(const gs_linear_attn* a, bool backward, bool states, int32_t chunks = 0, Limits limits = {UINT32_MAX, kWaitNs}) {
+    split = Split{a->tokens, a->group_offsets, a->groups, chunks ? chunks * kL : segment_tokens(a, backward, states), 0,
+                  a->tokens, limits};
     slots = a->tokens / split.seg + a->groups;
     Dp = padded_dim(a->dim);
     Ep = padded_dim(a->vdim);
@@ -1593,6 +1640,51 @@ gs_status backward(const gs_linear_attn* a, const Call& c, Side (&s)[7], const f
   return GS_OK;
 }
 
+bool chunked_ok(const gs_linear_attn* a, const gs_attn_heads* heads) {
+  return a && heads && shape_ok(a) && aligned_or_none(a) && (a->group_offsets || a->groups == 1);
+}
+
+gs_status forward(const gs_linear_attn* a, const Call& c, const gs_attn_heads* heads, float* state_out, void* workspace,
+                  size_t ws_bytes, cudaStream_t st) {
+  Side s[4] = {};
+  if (a->tokens > 0 && (!side(&s[0], a, &heads[0], a->dim, false, false) || !side(&s[1], a, &heads[1], a->dim, true, false) ||
+                        !side(&s[2], a, &heads[2], a->vdim, true, false) || !side(&s[3], a, &heads[3], a->vdim, false, true)))
+    return GS_ERR_INVALID_ARG;
+  const Room room(workspace, a, c.slots, false, a->tokens > 0 ? to_copy(s, 3) : 0, 0);
+  if (!workspace || !aligned16(workspace) || ws_bytes < room.bytes) return GS_ERR_INVALID_ARG;
+  if (a->tokens == 0 && !state_out) return GS_OK;
+  if (a->tokens == 0) {
+    return run_scan(ScanArgs{c.split, a->q_heads, a->dim, a->vdim, c.Dp, c.Ep, a->log_decay,
+                             {Scan{a->state, state_out, room.states, 0}, Scan{}}, 1}, st);
+  }
+  return a->dtype == GS_BF16 ? forward<__nv_bfloat16>(a, c, s, state_out, room, st)
+                             : forward<__half>(a, c, s, state_out, room, st);
+}
+
+gs_status backward(const gs_linear_attn* a, const Call& c, const gs_attn_heads* heads, const float* dstate_out,
+                   float* dstate, void* workspace, size_t ws_bytes, cudaStream_t st) {
+  Side s[7] = {};
+  if (a->tokens > 0 &&
+      (!side(&s[0], a, &heads[0], a->dim, false, false) || !side(&s[1], a, &heads[1], a->dim, true, false) ||
+       !side(&s[2], a, &heads[2], a->vdim, true, false) || !side(&s[3], a, &heads[3], a->vdim, false, false) ||
+       !side(&s[4], a, &heads[4], a->dim, false, true) || !side(&s[5], a, &heads[5], a->dim, true, true) ||
+       !side(&s[6], a, &heads[6], a->vdim, true, true)))
+    return GS_ERR_INVALID_ARG;
+  const int copied = a->tokens > 0 ? to_copy(s, 4) : 0;
+  const size_t others = Room(nullptr, a, c.slots, true, copied, 0).bytes;
+  const int64_t joined = c.rep > 1 ? room_for(a, ws_bytes > others ? ws_bytes - others : 0) : 0;
+  const int64_t range = c.rep > 1 ? range_of(a, a->group_offsets != nullptr, c.split.seg, joined) : a->tokens;
+  const Room room(workspace, a, c.slots, true, copied, joined);
+  if (!workspace || !aligned16(workspace) || ws_bytes < room.bytes || (a->tokens > 0 && range == 0)) return GS_ERR_INVALID_ARG;
+  if (a->tokens == 0 && !dstate) return GS_OK;
+  if (a->tokens == 0) {
+    return run_scan(ScanArgs{c.split, a->q_heads, a->dim, a->vdim, c.Dp, c.Ep, a->log_decay,
+                             {Scan{dstate_out, dstate, room.grads, 1}, Scan{}}, 1}, st);
+  }
+  return a->dtype == GS_BF16 ? backward<__nv_bfloat16>(a, c, s, dstate_out, dstate, room, range, st)
+                             : backward<__half>(a, c, s, dstate_out, dstate, room, range, st);
+}
+
 }  // namespace
 }  // namespace gs
 
@@ -1617,50 +1709,31 @@ extern "C" size_t gs_linear_attn_workspace_bytes(const gs_linear_attn* a, int32_
 
 extern "C" gs_status gs_linear_attn_fwd(const gs_linear_attn* a, const gs_attn_heads* heads, float* state_out,
                                         void* workspace, size_t ws_bytes, void* stream) {
-  if (!a || !heads || !shape_ok(a) || !aligned_or_none(a) || (!a->group_offsets && a->groups != 1)) return GS_ERR_INVALID_ARG;
-  const Call c(a, false, state_out != nullptr);
-  Side s[4] = {};
-  if (a->tokens > 0 && (!side(&s[0], a, &heads[0], a->dim, false, false) || !side(&s[1], a, &heads[1], a->dim, true, false) ||
-                        !side(&s[2], a, &heads[2], a->vdim, true, false) || !side(&s[3], a, &heads[3], a->vdim, false, true)))
-    return GS_ERR_INVALID_ARG;
-  const Room room(workspace, a, c.slots, false, a->tokens > 0 ? to_copy(s, 3) : 0, 0);
-  if (!workspace || !aligned16(workspace) || ws_bytes < room.bytes) return GS_ERR_INVALID_ARG;
-  cudaStream_t st = (cudaStream_t)stream;
-  if (a->tokens == 0 && !state_out) return GS_OK;
-  if (a->tokens == 0) {
-    return run_scan(ScanArgs{c.split, a->q_heads, a->dim, a->vdim, c.Dp, c.Ep, a->log_decay,
-                             {Scan{a->state, state_out, room.states, 0}, Scan{}}, 1}, st);
-  }
-  return a->dtype == GS_BF16 ? forward<__nv_bfloat16>(a, c, s, state_out, room, st)
-                             : forward<__half>(a, c, s, state_out, room, st);
+  if (!chunked_ok(a, heads)) return GS_ERR_INVALID_ARG;
+  return forward(a, Call(a, false, state_out != nullptr), heads, state_out, workspace, ws_bytes, (cudaStream_t)stream);
 }
 
 extern "C" gs_status gs_linear_attn_bwd(const gs_linear_attn* a, const gs_attn_heads* heads,
                                         const float* dstate_out, float* dstate, void* workspace, size_t ws_bytes,
                                         void* stream) {
-  if (!a || !heads || !shape_ok(a) || !aligned_or_none(a) || (!a->group_offsets && a->groups != 1)) return GS_ERR_INVALID_ARG;
-  const Call c(a, true, dstate != nullptr);
-  Side s[7] = {};
-  if (a->tokens > 0 &&
-      (!side(&s[0], a, &heads[0], a->dim, false, false) || !side(&s[1], a, &heads[1], a->dim, true, false) ||
-       !side(&s[2], a, &heads[2], a->vdim, true, false) || !side(&s[3], a, &heads[3], a->vdim, false, false) ||
-       !side(&s[4], a, &heads[4], a->dim, false, true) || !side(&s[5], a, &heads[5], a->dim, true, true) ||
-       !side(&s[6], a, &heads[6], a->vdim, true, true)))
-    return GS_ERR_INVALID_ARG;
-  const int copied = a->tokens > 0 ? to_copy(s, 4) : 0;
-  const size_t others = Room(nullptr, a, c.slots, true, copied, 0).bytes;
-  const int64_t joined = c.rep > 1 ? room_for(a, ws_bytes > others ? ws_bytes - others : 0) : 0;
-  const int64_t range = c.rep > 1 ? range_of(a, a->group_offsets != nullptr, c.split.seg, joined) : a->tokens;
-  const Room room(workspace, a, c.slots, true, copied, joined);
-  if (!workspace || !aligned16(workspace) || ws_bytes < room.bytes || (a->tokens > 0 && range == 0)) return GS_ERR_INVALID_ARG;
-  cudaStream_t st = (cudaStream_t)stream;
-  if (a->tokens == 0 && !dstate) return GS_OK;
-  if (a->tokens == 0) {
-    return run_scan(ScanArgs{c.split, a->q_heads, a->dim, a->vdim, c.Dp, c.Ep, a->log_decay,
-                             {Scan{dstate_out, dstate, room.grads, 1}, Scan{}}, 1}, st);
-  }
-  return a->dtype == GS_BF16 ? backward<__nv_bfloat16>(a, c, s, dstate_out, dstate, room, range, st)
-                             : backward<__half>(a, c, s, dstate_out, dstate, room, range, st);
+  if (!chunked_ok(a, heads)) return GS_ERR_INVALID_ARG;
+  return backward(a, Call(a, true, dstate != nullptr), heads, dstate_out, dstate, workspace, ws_bytes,
+                  (cudaStream_t)stream);
+}
+
+extern "C" int32_t gs_selftest_linear_attn_chunks(const gs_linear_attn* a, int32_t backward, int32_t states) {
+  return a && shape_ok(a) ? Call(a, backward != 0, states != 0).split.seg / kL : 0;
+}
+
+extern "C" gs_status gs_selftest_linear_attn(const gs_linear_attn* a, const gs_attn_heads* heads, int32_t backward_pass,
+                                             const float* dstate_out, float* state_out, void* workspace, size_t ws_bytes,
+                                             int32_t chunks, int32_t products, void* stream) {
+  if (!chunked_ok(a, heads) || chunks < 0 || chunks > 16) return GS_ERR_INVALID_ARG;
+  const Limits limits = products < 0 ? Limits{UINT32_MAX, kWaitNs} : Limits{(uint32_t)products, 20000000};
+  const Call c(a, backward_pass != 0, state_out != nullptr, chunks, limits);
+  const gs_status s = backward_pass ? backward(a, c, heads, dstate_out, state_out, workspace, ws_bytes, (cudaStream_t)stream)
+                                    : forward(a, c, heads, state_out, workspace, ws_bytes, (cudaStream_t)stream);
+  return s != GS_OK ? s : gs_linear_attn_status(stream);
 }
 
 extern "C" gs_status gs_linear_attn_status(void* stream) {

@@ -325,11 +325,24 @@ gs_status gs_linear_attn_bwd(const gs_linear_attn* a, const gs_attn_heads* heads
 gs_status gs_linear_attn_step(const gs_linear_attn* a, const gs_attn_heads* heads, float* state,
                               void* stream);
 
-/* Every wait of the chunked kernels for the tensor cores is bounded (two seconds
- * a block, after which results are undefined).  gs_linear_attn_status
- * synchronises the stream and returns GS_ERR_TIMEOUT if one ran out on the
- * current device since the last such call. */
+/* Every wait of the chunked kernels for the tensor cores is bounded: a block waits
+ * for two seconds in all, then issues no more products, waits (again for two
+ * seconds at most) for its copies and products under way and ends; results are
+ * undefined.  gs_linear_attn_status synchronises the stream and returns
+ * GS_ERR_TIMEOUT if that happened on the current device, on any stream, since the
+ * last such call. */
 gs_status gs_linear_attn_status(void* stream);
+
+/* Self-test: gs_linear_attn_fwd (or, backward != 0, _bwd, with state_out its dstate)
+ * with segments of `chunks` chunks of 128 tokens (1 to 16; 0: as many as
+ * gs_selftest_linear_attn_chunks says are chosen).  products >= 0: each block's tensor
+ * cores get no more than that many sets of products, so that its waits run out, after
+ * 20 ms instead of two seconds.  Synchronises, and returns what gs_linear_attn_status does;
+ * after GS_ERR_TIMEOUT the results are undefined, the context stays usable. */
+int32_t gs_selftest_linear_attn_chunks(const gs_linear_attn* a, int32_t backward, int32_t states);
+gs_status gs_selftest_linear_attn(const gs_linear_attn* a, const gs_attn_heads* heads, int32_t backward,
+                                  const float* dstate_out, float* state_out, void* workspace,
+                                  size_t ws_bytes, int32_t chunks, int32_t products, void* stream);
 
 #ifdef __cplusplus
 }

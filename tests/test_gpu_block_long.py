@@ -6,6 +6,8 @@ the magnitudes for the two roundings to the type and half a step of the result);
 sums in fp32 of chunks of 128 tokens, whose keys are 3 terms at most (24 cuts of 2^-23 on the
 tensor cores) with weights of up to nine powers (2^-22 each), decayed once a chunk.
 Feed-forward block: test_gpu_ffn.py's bounds."""
+import ctypes as C
+
 import pytest
 import torch
 
@@ -25,6 +27,22 @@ def gs():
     __graft_entry__.build()
     import gaussian_splatting_differentiable_gs_gb300 as gs
     return gs
+
+
+def _selftest(gs):
+    L, vp = gs.lib(), C.c_void_p
+    L.gs_selftest_linear_attn.argtypes = [vp, vp, C.c_int32, vp, vp, vp, C.c_size_t, C.c_int32, C.c_int32, vp]
+    L.gs_selftest_linear_attn_chunks.argtypes = [vp, C.c_int32, C.c_int32]
+    return L
+
+
+def _packed(gs, q, k, v, a, offs, state, scale, *others):
+    """The C call's structure, and the heads of q, k, v and the others."""
+    (T, H, D), K, E = q.shape, k.shape[1], v.shape[2]
+    x = gs.net._ATTN.pack(T, H, K, D, E, 1 if offs is None else offs.numel() - 1, gs.net.DTYPES[q.dtype], scale,
+                          a.data_ptr(), 0 if offs is None else offs.data_ptr(), 0 if state is None else state.data_ptr())
+    heads = [n for t in (q, k, v) + others for n in (t.data_ptr(), t.stride(0), t.stride(1))]
+    return x, (gs.net._ATTN_HEADS4 if len(others) == 1 else gs.net._ATTN_HEADS7).pack(*heads)
 
 
 def _close(got, want, bound, what):
@@ -120,6 +138,8 @@ LONG = [
 def test_attention_of_many_heads(gs, dt, D, E, T, H, K, offsets):
     G = 1 if offsets is None else len(offsets) - 1
     ws = torch.full((gs.gs_linear_attn_workspace_bytes(T, H, K, D, E, G),), 0xff, dtype=torch.uint8, device="cuda")
+    shape = gs.net._ATTN.pack(T, H, K, D, E, G, gs.net.DTYPES[dt], 1.0, 0, 0, 0)
+    assert all(_selftest(gs).gs_selftest_linear_attn_chunks(shape, back, 1) >= 2 for back in (0, 1))
 
     def call(q, k, v, a, offs, s0, scale, out, last, do, dq, dk, dv, ds, d0):
         kw = dict(group_offsets=offs, state=s0, scale=scale, workspace=ws)
@@ -128,6 +148,68 @@ def test_attention_of_many_heads(gs, dt, D, E, T, H, K, offsets):
 
     _check_attn(call, dt, T, H, K, D, E, offsets, T + D, (0, 1, K // 2, K - 1))
     gs.gs_linear_attn_status()
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("chunks", [2, 3, 5])
+@pytest.mark.parametrize("D,E,H,K,offsets", [
+    (64, 64, 3, 3, None),
+    (64, 64, 4, 1, [0, 640, 641, 641, 1297]),
+    (72, 41, 2, 2, [0, 511, 1270]),
+    (72, 41, 4, 2, None),
+    (40, 128, 2, 1, [0, 129, 1300]),
+    (64, 128, 2, 2, None),
+    (128, 32, 3, 1, None),
+    (128, 128, 2, 2, [0, 300, 1200]),
+    (128, 128, 2, 1, None),
+])
+def test_segments_of_several_chunks(gs, dt, chunks, D, E, H, K, offsets):
+    """Segments as long as is asked for, the last one of a group ragged."""
+    T, L = 1300, _selftest(gs)
+    ws = torch.full((1 << 27,), 0xff, dtype=torch.uint8, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+
+    def call(q, k, v, a, offs, s0, scale, out, last, do, dq, dk, dv, ds, d0):
+        x, heads = _packed(gs, q, k, v, a, offs, s0, scale, out)
+        assert L.gs_selftest_linear_attn(x, heads, 0, None, last.data_ptr(), ws.data_ptr(), ws.numel(), chunks, -1,
+                                         stream) == gs.GS_OK
+        x, heads = _packed(gs, q, k, v, a, offs, s0, scale, do, dq, dk, dv)
+        assert L.gs_selftest_linear_attn(x, heads, 1, ds.data_ptr(), d0.data_ptr(), ws.data_ptr(), ws.numel(), chunks, -1,
+                                         stream) == gs.GS_OK
+
+    _check_attn(call, dt, T, H, K, D, E, offsets, chunks + D, range(K))
+
+
+@pytest.mark.parametrize("D,E,H,K", [(64, 64, 4, 4), (64, 64, 4, 2), (128, 128, 2, 2), (72, 41, 2, 1)])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+def test_the_attention_gives_up_and_the_context_survives(gs, dt, D, E, H, K):
+    """Products that never come: the waits run out (20 ms), the blocks wait for what is under
+    way, flag the error and end; the next call is right."""
+    T, L = 700, _selftest(gs)
+    g = torch.Generator(device="cuda").manual_seed(D)
+    q, k, v, do = (torch.randn(T, h, d, generator=g, device="cuda").to(dt) for h, d in ((H, D), (K, D), (K, E), (H, E)))
+    a = torch.full((H,), -0.01, device="cuda")
+    ws = torch.full((1 << 27,), 0xff, dtype=torch.uint8, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    out, grads = torch.empty_like(do), [torch.empty_like(x) for x in (q, k, v)]
+    s, ds = (torch.empty(1, H, D, E, device="cuda") for _ in range(2))
+    fwd, bwd = _packed(gs, q, k, v, a, None, None, 0.1, out), _packed(gs, q, k, v, a, None, None, 0.1, do, *grads)
+
+    def run(products):
+        res = [L.gs_selftest_linear_attn(*fwd, 0, None, s.data_ptr(), ws.data_ptr(), ws.numel(), 3, products, stream)]
+        res.append(L.gs_selftest_linear_attn(*bwd, 1, None, ds.data_ptr(), ws.data_ptr(), ws.numel(), 3, products, stream))
+        return res
+
+    assert run(-1) == [gs.GS_OK] * 2
+    want = [x.clone() for x in (out, s, *grads, ds)]
+    for products in (0, 1, 2, 3, 5):  # (a chunk of the sums takes one, of the outputs two, of the gradients two or four)
+        assert run(products) == [gs.GS_ERR_TIMEOUT] * 2, products
+        gs.gs_linear_attn_status()  # read and cleared
+        for x in (out, s, *grads, ds):
+            x.fill_(7.0)
+        assert run(-1) == [gs.GS_OK] * 2
+        assert all(torch.equal(x, y) for x, y in zip(want, (out, s, *grads, ds))), products
+    assert run(1 << 20) == [gs.GS_OK] * 2
 
 
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
