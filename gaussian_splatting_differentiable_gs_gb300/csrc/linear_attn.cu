@@ -1202,7 +1202,7 @@ struct RowsArgs {
   Side from[4];
   void* to[4];        // [tokens][heads][dim rounded up to 8]
   int32_t heads[4];
-  int64_t tokens;
+  Split split;
 };
 template <typename W>
 __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ RowsArgs p) {
@@ -1212,7 +1212,7 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ 
   const int heads = p.heads[blockIdx.y], granules = (s.dim + 7) / 8;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, r = i / granules, token = r / heads;
   const int c = (int)(i % granules) * 8, h = (int)(r % heads);
-  if (token >= p.tokens) return;
+  if (token < offset_of(p.split, 0) || token >= offset_of(p.split, p.split.groups)) return;
   const W* from = (const W*)s.p + token * s.token + h * s.head + c;
   Pack<W, 8> v;
 #pragma unroll
@@ -1438,9 +1438,9 @@ int to_copy(const Side* s, int n) {
   for (int i = 0; i < n; ++i) bits |= (s[i].wide ? 0 : 1) << i;
   return bits;
 }
-gs_status copy_rows(const gs_linear_attn* a, Side* s, int n, const Room& room, cudaStream_t st) {
+gs_status copy_rows(const gs_linear_attn* a, const Split& split, Side* s, int n, const Room& room, cudaStream_t st) {
   RowsArgs p{};
-  p.tokens = a->tokens;
+  p.split = split;
   int count = 0;
   int64_t most = 0;
   for (int i = 0; i < n; ++i) {
@@ -1546,7 +1546,7 @@ template <typename T>
 gs_status forward(const gs_linear_attn* a, const Call& c, Side (&s)[4], float* state_out, const Room& room,
                   cudaStream_t st) {
   const bool scan = a->tokens > c.split.seg || state_out;
-  const gs_status copied = copy_rows(a, s, 3, room, st);
+  const gs_status copied = copy_rows(a, c.split, s, 3, room, st);
   if (copied != GS_OK) return copied;
   if (scan) {
     const gs_status r = states_of<T>(a, c, {Part{s[1], s[2], 1.f, 0, 0, state_out != nullptr, room.states}, Part{}},
@@ -1580,7 +1580,7 @@ gs_status backward(const gs_linear_attn* a, const Call& c, Side (&s)[7], const f
   const int64_t fours = a->k_heads * div_up(a->dim > a->vdim ? a->dim : a->vdim, 4);
   if (slots_of(0, a->tokens) * a->q_heads * kinds > INT32_MAX || div_up((range + c.split.seg) * fours, 256) > INT32_MAX)
     return GS_ERR_INVALID_ARG;
-  const gs_status copied = copy_rows(a, s, 4, room, st);
+  const gs_status copied = copy_rows(a, c.split, s, 4, room, st);
   if (copied != GS_OK) return copied;
   const Side &q = s[0], &k = s[1], &v = s[2], &g = s[3];
   const bool scan = a->tokens > c.split.seg || dstate;

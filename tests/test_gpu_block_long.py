@@ -309,3 +309,25 @@ def test_shared_heads_with_little_room(gs, dt, D, E, offsets):
     except gs.GSError:
         pass
     assert sizes >= 3 and size > 0
+
+
+@pytest.mark.parametrize("back", [False, True])
+def test_tokens_outside_the_groups_are_not_read(gs, back):
+    """Rows that are copied first: a value that only tokens outside the groups hold is nowhere
+    in the workspace."""
+    T, H, D, dt, mark = 120, 2, 41, torch.float16, 1234.0
+    q, k, v, do = (few._empty(T, H * D, dt, 3, 1)[0].unflatten(1, (H, D)) for _ in range(4))
+    offs = torch.tensor([5, 60, 101], dtype=torch.int32, device="cuda")
+    a = torch.full((H,), -0.1, device="cuda")
+    for x in (q, k, v, do):
+        x.copy_(torch.rand(T, H, D, device="cuda"))
+        x[:5], x[101:] = mark, mark
+    ws = torch.zeros(gs.gs_linear_attn_workspace_bytes(T, H, H, D, D, 2), dtype=torch.uint8, device="cuda")
+    out = [torch.full_like(q, 9.0) for _ in range(4)]
+    if back:
+        gs.gs_linear_attn_bwd(q, k, v, a, do, *out[:3], group_offsets=offs, workspace=ws)
+    else:
+        gs.gs_linear_attn_fwd(q, k, v, a, out[0], group_offsets=offs, workspace=ws)
+    used = ws[:ws.numel() // 2 * 2].view(dt)
+    assert (used != 0).any() and not (used == mark).any()
+    assert all((x[:5] == 9.0).all() and (x[101:] == 9.0).all() for x in out)
