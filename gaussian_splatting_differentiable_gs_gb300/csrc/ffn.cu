@@ -1016,7 +1016,8 @@ gs_status forward(const Args& a, void* h, int64_t h_stride, void* workspace, siz
   const Room room(workspace, a.tokens, a.channels, a.hidden, false);
   if (!workspace || !aligned16(workspace) || ws_bytes < room.bytes) return GS_ERR_INVALID_ARG;
   if (a.tokens == 0) return GS_OK;
-  if (!matrix_ok(h, a.tokens, a.hidden, h_stride, 2, true)) return GS_ERR_INVALID_ARG;
+  // (an output at the address of an input that is still read while it is written)
+  if (!matrix_ok(h, a.tokens, a.hidden, h_stride, 2, true) || h == a.x || h == a.w) return GS_ERR_INVALID_ARG;
   if (few(a) && load_steps == UINT32_MAX) return few_tokens(a, h, h_stride, st);
   const int clusters = resident_clusters();
   if (!clusters) {
@@ -1054,7 +1055,8 @@ gs_status backward(const Args& a, const void* dh, int64_t dh_stride, void* dx, i
     return GS_OK;
   }
   if (!matrix_ok(dh, a.tokens, a.hidden, dh_stride, 2, false) ||
-      (dx && !matrix_ok(dx, a.tokens, a.channels, dx_stride, 2, true)))
+      (dx && (!matrix_ok(dx, a.tokens, a.channels, dx_stride, 2, true) || dx == a.x || dx == a.w || dx == dw)) ||
+      (dw && dw == a.x))
     return GS_ERR_INVALID_ARG;
   if (!dx && !dw) return GS_OK;
   const int clusters = resident_clusters();

@@ -1403,21 +1403,39 @@ bool aligned_or_none(const gs_linear_attn* a) {
   return a->log_decay && aligned_to(a->log_decay, 4) && aligned_to(a->group_offsets, 4) && aligned_to(a->state, 4);
 }
 
+// No two elements of the heads in one place.
+bool apart(const gs_linear_attn* a, int64_t token, int64_t head, int32_t heads, int32_t dim) {
+  const int64_t t = token < 0 ? -token : token, e = head < 0 ? -head : head;
+  const bool many = a->tokens > 1;
+  if ((heads > 1 && e < dim) || (many && t < dim)) return false;
+  return heads < 2 || !many || t >= e * (heads - 1) + dim || e >= t * (a->tokens - 1) + dim;
+}
 bool side(Side* s, const gs_linear_attn* a, const gs_attn_heads* h, int32_t dim, bool of_key, bool output) {
   if (!h->p || !aligned_to(h->p, 2)) return false;
   constexpr int64_t kMost = (int64_t)1 << 40;
   if (h->token >= kMost || h->token <= -kMost || h->head >= kMost || h->head <= -kMost) return false;
   const int32_t heads = of_key ? a->k_heads : a->q_heads;
-  if (output) {  // no two elements in one place
-    const int64_t t = h->token < 0 ? -h->token : h->token, e = h->head < 0 ? -h->head : h->head;
-    const bool many = a->tokens > 1;
-    if ((heads > 1 && e < dim) || (many && t < dim)) return false;
-    if (heads > 1 && many && !(t >= e * (heads - 1) + dim || e >= t * (a->tokens - 1) + dim)) return false;
-  }
+  if (output && !apart(a, h->token, h->head, heads, dim)) return false;
   *s = Side{h->p, h->token, h->head, dim, of_key ? 1 : 0,
             dim % 8 == 0 && aligned16(h->p) && (a->tokens < 2 || h->token % 8 == 0) && (heads < 2 || h->head % 8 == 0)
                 ? 1 : 0};
   return true;
+}
+
+// Outputs at an input's address, or at one another's: other blocks would still read there.
+bool in_place(const Side* s, int inputs, int all) {
+  for (int o = inputs; o < all; ++o)
+    for (int i = 0; i < o; ++i)
+      if (s[i].p == s[o].p) return true;
+  return false;
+}
+// A single token's output at an input's address is its block's own, if both have the same
+// heads: read before it is written.
+bool own_place(const gs_linear_attn* a, const Side& in, const Side& out) {
+  if (in.p != out.p) return true;
+  return (!in.of_key || a->q_heads == a->k_heads) && (a->tokens < 2 || in.token == out.token) &&
+         (a->q_heads < 2 || in.head == out.head) &&
+         apart(a, in.token, in.head, a->q_heads, in.dim > out.dim ? in.dim : out.dim);
 }
 
 // Dynamic shared memory beyond 48 KB, asked for once per kernel and device.
@@ -1648,7 +1666,8 @@ gs_status forward(const gs_linear_attn* a, const Call& c, const gs_attn_heads* h
                   size_t ws_bytes, cudaStream_t st) {
   Side s[4] = {};
   if (a->tokens > 0 && (!side(&s[0], a, &heads[0], a->dim, false, false) || !side(&s[1], a, &heads[1], a->dim, true, false) ||
-                        !side(&s[2], a, &heads[2], a->vdim, true, false) || !side(&s[3], a, &heads[3], a->vdim, false, true)))
+                        !side(&s[2], a, &heads[2], a->vdim, true, false) || !side(&s[3], a, &heads[3], a->vdim, false, true) ||
+                        in_place(s, 3, 4)))
     return GS_ERR_INVALID_ARG;
   const Room room(workspace, a, c.slots, false, a->tokens > 0 ? to_copy(s, 3) : 0, 0);
   if (!workspace || !aligned16(workspace) || ws_bytes < room.bytes) return GS_ERR_INVALID_ARG;
@@ -1668,7 +1687,7 @@ gs_status backward(const gs_linear_attn* a, const Call& c, const gs_attn_heads* 
       (!side(&s[0], a, &heads[0], a->dim, false, false) || !side(&s[1], a, &heads[1], a->dim, true, false) ||
        !side(&s[2], a, &heads[2], a->vdim, true, false) || !side(&s[3], a, &heads[3], a->vdim, false, false) ||
        !side(&s[4], a, &heads[4], a->dim, false, true) || !side(&s[5], a, &heads[5], a->dim, true, true) ||
-       !side(&s[6], a, &heads[6], a->vdim, true, true)))
+       !side(&s[6], a, &heads[6], a->vdim, true, true) || in_place(s, 4, 7)))
     return GS_ERR_INVALID_ARG;
   const int copied = a->tokens > 0 ? to_copy(s, 4) : 0;
   const size_t others = Room(nullptr, a, c.slots, true, copied, 0).bytes;
@@ -1755,7 +1774,8 @@ extern "C" gs_status gs_linear_attn_step(const gs_linear_attn* a, const gs_attn_
   StepArgs p{};
   if (!state || !aligned_to(state, 4) || !side(&p.q, a, &heads[0], a->dim, false, false) ||
       !side(&p.k, a, &heads[1], a->dim, true, false) || !side(&p.v, a, &heads[2], a->vdim, true, false) ||
-      !side(&p.out, a, &heads[3], a->vdim, false, true))
+      !side(&p.out, a, &heads[3], a->vdim, false, true) || !own_place(a, p.q, p.out) || !own_place(a, p.k, p.out) ||
+      !own_place(a, p.v, p.out))
     return GS_ERR_INVALID_ARG;
   p.heads = a->q_heads;
   p.rep = a->q_heads / a->k_heads;

@@ -225,7 +225,8 @@ gs_status gs_selftest_wgrad_timeout(int64_t tokens, int32_t rows, int32_t channe
  *   gate = x w_gate^T, up = x w_up^T, h = act(gate) * up
  * Neither gate nor up is written; gs_ffn_bwd forms them again from x.  x, w,
  * h, dh and dx are of one type, GS_BF16 or GS_F16; sums are fp32.  h may not
- * overlap the inputs, nor may dx or dw.
+ * overlap the inputs, nor may dx or dw overlap them or one another (an address
+ * that is still read while it would be written is refused).
  *   workspace   gs_ffn_workspace_bytes(...) bytes (0: refused), 16-byte
  *               aligned; its first 256 bytes must be zero before the first
  *               call (gs_workspace_status reads them) and calls on one
@@ -293,7 +294,8 @@ typedef struct gs_attn_heads {   /* [tokens][heads][channels]                 */
 } gs_attn_heads;
 
 /* gs_linear_attn_fwd -- all tokens of the groups, in chunks.
- *   heads       (host) four: q, k, v, out; out may not overlap the inputs
+ *   heads       (host) four: q, k, v, out; out may not overlap the inputs (the
+ *               same address is refused)
  *   state_out   [groups][q_heads][dim][vdim] fp32: the states after the
  *               groups' last tokens (a group's own state where it has none),
  *               or NULL; may equal state
@@ -310,7 +312,8 @@ size_t gs_linear_attn_workspace_bytes(const gs_linear_attn* a, int32_t backward)
 gs_status gs_linear_attn_fwd(const gs_linear_attn* a, const gs_attn_heads* heads,
                              float* state_out, void* workspace, size_t ws_bytes, void* stream);
 
-/* gs_linear_attn_bwd -- heads (host): q, k, v, dout, dq, dk, dv.  From the
+/* gs_linear_attn_bwd -- heads (host): q, k, v, dout, dq, dk, dv; dq, dk and dv
+ * may not overlap the inputs or one another (the same address is refused).  From the
  * gradients of the outputs and (dstate_out, or NULL: 0) of the last states: dq,
  * dk, dv (summed over the query heads that share a key head) and dstate, the
  * gradient of the first states (or NULL; may equal dstate_out).  The decays get
@@ -321,7 +324,9 @@ gs_status gs_linear_attn_bwd(const gs_linear_attn* a, const gs_attn_heads* heads
 
 /* gs_linear_attn_step -- one token of each of a->tokens streams; heads (host):
  * q, k, v, out; state [tokens][q_heads][dim][vdim] fp32, read and updated in
- * place.  a->state and a->group_offsets are not used. */
+ * place.  out may lie where q does, or k or v where key heads are not shared,
+ * with the same strides; else it may not overlap them.  a->state and
+ * a->group_offsets are not used. */
 gs_status gs_linear_attn_step(const gs_linear_attn* a, const gs_attn_heads* heads, float* state,
                               void* stream);
 
