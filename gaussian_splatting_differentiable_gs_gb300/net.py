@@ -487,7 +487,7 @@ def _attn(q, k, v, out, name, log_decay, group_offsets, state, scale):
         tv, hv, vdim = v.shape
         (qa, qb, q1), (ka, kb, k1), (va, vb, v1), (oa, ob, o1) = q.stride(), k.stride(), v.stride(), out.stride()
         if ((dt is torch.bfloat16 or dt is torch.float16) and k.dtype is dt and v.dtype is dt and out.dtype is dt
-                and tk == tokens == tv and dk == dim and hk == hv and hk and hq and not hq % hk
+                and tk == tokens == tv and dk == dim and dim and hk == hv and hk and hq and not hq % hk
                 and out.shape == (tokens, hq, vdim)
                 and device == k.get_device() == v.get_device() == out.get_device() >= 0
                 and ((q1 == k1 == v1 == o1 == 1) or not tokens
@@ -516,6 +516,8 @@ def _attn(q, k, v, out, name, log_decay, group_offsets, state, scale):
     hk, vdim = k.shape[1], v.shape[2]
     if not hk or not hq or hq % hk:
         raise ValueError("%d query heads do not share %d key heads evenly" % (hq, hk))
+    if not dim:
+        raise ValueError("q: heads without channels")
     for t, n, shape in ((q, "q", (tokens, hq, dim)), (k, "k", (tokens, hk, dim)), (v, "v", (tokens, hk, vdim)),
                         (out, name, (tokens, hq, vdim))):
         _attn_heads(t, n, shape, q.dtype, q.get_device())

@@ -80,3 +80,18 @@ def test_single_tokens_over_shared_heads_are_refused(gs):
     with pytest.raises(gs.GSError):
         gs.gs_linear_attn_step(q, kv.clone(), kv, a, s, room)
     gs.gs_linear_attn_step(q, kv, kv, a, s, q)
+
+
+def test_heads_without_channels_are_refused(gs):
+    q, v, a = _rand(4, 2, 0), _rand(4, 2, 8), torch.zeros(2, device="cuda")
+    ws, s = torch.empty(1 << 20, dtype=torch.uint8, device="cuda"), torch.empty(4, 2, 0, 8, device="cuda")
+    out = torch.empty_like(v)
+    for scale in (None, 1.0):
+        with pytest.raises(ValueError):
+            gs.gs_linear_attn_fwd(q, q, v, a, out, scale=scale, workspace=ws)
+        with pytest.raises(ValueError):
+            gs.gs_linear_attn_bwd(q, q, v, a, out, q, q, v.clone(), scale=scale, workspace=ws)
+        with pytest.raises(ValueError):
+            gs.gs_linear_attn_step(q, q, v, a, s, out, scale=scale)
+        with pytest.raises((ValueError, gs.GSError)):
+            gs.gs_linear_attn_fwd(v, v, q, a, q, scale=scale, workspace=ws)
