@@ -253,6 +253,28 @@ def test_shared_sums_of_the_weight_gradient(gs, dt, T, C, F, pad, offset, shared
     assert gs.gs_workspace_status(ws) == gs.GS_OK
 
 
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("T,C,F", [(32640, 1024, 2432), (200000, 64, 64)])
+def test_long_sums_of_the_weight_gradient(gs, dt, T, C, F):
+    """dw in fp32 after many tokens, of which the tensor cores sum 2048 at a time.  The gate's
+    half, with gate = 0 and up = 2: dgate is dh, exactly, and dw dh^T x.  All terms are positive
+    and of alike size, so that a run's partial sums are half of its last one on average: (2048 / 8 + 4)
+    cuts of 2^-23 of that; each run, and each pair's share of a tile, is added with a rounding."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x = (torch.rand(T, C, generator=g, device="cuda") / 2 + 0.5).to(dt)
+    x[:, 0] = 2.0
+    dh = (torch.rand(T, F, generator=g, device="cuda") / 2 + 0.5).to(dt)
+    w = torch.zeros(2 * F, C, dtype=dt, device="cuda")
+    w[F:, 0] = 1.0
+    dw = torch.empty(2 * F, C, device="cuda")
+    ws = torch.zeros(gs.gs_ffn_workspace_bytes(T, C, F), dtype=torch.uint8, device="cuda")
+    gs.gs_ffn_bwd(x, w, dh, None, dw, ws)
+    want = dh.double().t() @ x.double()
+    err = ((dw[:F].double() - want) / want).abs()
+    assert float(err.max()) <= 130 * 2.0 ** -23 + (T / 2048 + 77) * 2.0 ** -24, (float(err.max()), float(err.mean()))
+    assert (dw[F:] == 0).all()
+
+
 def test_many_tiles_a_pair(gs):
     """Forward and dx of over twice as many tiles as there are pairs."""
     dt, T, C, F = torch.bfloat16, 5300, 2060, 1100
