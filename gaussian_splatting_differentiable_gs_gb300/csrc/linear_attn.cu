@@ -388,11 +388,16 @@ __device__ __forceinline__ void weigh(uint32_t keys, uint32_t first_term, uint32
     w *= next;
   }
 }
-// fp16: the largest magnitude among the thread's own granules of the keys, in the warp.
+// fp16: the largest finite magnitude among the thread's own granules of the keys, in the warp.
+// (An infinity must not set the range in which the others are kept.)
 template <int KD>
 __device__ __forceinline__ float top_key(uint32_t keys) {
   const Rows<KD> k;
   uint32_t top = 0;  // magnitudes compare as whole numbers
+  auto in_warp = [&] {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  };
 #pragma unroll
   for (int i = 0; i < k.kCount; ++i) {
     const uint4 v = get_granule(keys + k.at + i * k.kRows * 128);
@@ -400,8 +405,17 @@ __device__ __forceinline__ float top_key(uint32_t keys) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) top = max(top, max(in[j] & 0x7fffu, in[j] >> 16 & 0x7fffu));
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  in_warp();
+  if (top >= 0x7c00u) {
+    top = 0;
+#pragma unroll 1
+    for (int i = 0; i < k.kCount * 8; ++i) {
+      uint16_t v;
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(keys + k.at + (i / 8) * k.kRows * 128 + i % 8 * 2) : "memory");
+      if ((v & 0x7fffu) < 0x7c00u) top = max(top, v & 0x7fffu);
+    }
+    in_warp();
+  }
   return __half2float(__ushort_as_half((unsigned short)top));
 }
 
@@ -445,14 +459,28 @@ struct State {
       for (int j = 0; j < 16; j += 2)
         *reinterpret_cast<float2*>(to + row(m, j) * stride + col(j)) = make_float2(v[m][j], v[m][j + 1]);
   }
+  // The largest finite magnitude in the warp.
   __device__ __forceinline__ float top() const {
+    constexpr float kMost = 3.402823466e38f;
     float x = 0.f;
+    auto in_warp = [&] {
+#pragma unroll
+      for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    };
 #pragma unroll
     for (int m = 0; m < kM; ++m)
 #pragma unroll
       for (int j = 0; j < 16; ++j) x = fmaxf(x, fabsf(v[m][j]));
+    in_warp();
+    if (x > kMost) {
+      x = 0.f;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+      for (int m = 0; m < kM; ++m)
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (fabsf(v[m][j]) <= kMost) x = fmaxf(x, fabsf(v[m][j]));
+      in_warp();
+    }
     return x;
   }
   // As the products take it: rows of 64 T.
