@@ -26,7 +26,11 @@
 // Products are on the tensor cores (tcgen05, 128 rows), sums and states fp32.  What is
 // rounded to the inputs' type on the way: the decayed products q_i k_j, and the state
 // where it is multiplied by a query (not where it is kept); each of the two parts of an
-// output is rounded once there and once more as the output.  The decayed keys of a
+// output is rounded once there and once more as the output.  In fp16 both, and the decayed
+// keys, are brought into its range by a power of two for each chunk, from the largest finite
+// state, query and key (32640 tokens, 16 heads of 64: with the products' range 103 us
+// forward and 249 backward, with the other two alone 102 and 242; products past 65504 were
+// infinities then, and those below 2^-14 had fewer bits).  The decayed keys of a
 // state's sum are taken as 3 (bf16) or 2 (fp16) terms, exact to fp32's rounding, for the
 // states that are handed on, and as 2 terms for the others.
 #include <atomic>
@@ -148,8 +152,8 @@ struct Control {
   uint32_t tmem;
   volatile int64_t until;     // when waiting ends; 0: nothing has been waited for
   volatile uint32_t abort;    // a wait gave up
-  float top[2][kThreads / 32];
-  alignas(16) float decay[64];  // mul d^(31 - i), then zeros
+  alignas(16) uint32_t top[4][kThreads / 32];  // the warps' largest magnitudes (floats' bits)
+  alignas(16) float decay[64];  // mul d^(31 - i) (fp16: in the scores' range), then zeros
 };
 static_assert(sizeof(Control) <= 1024, "control");
 // Products by one thread; once a wait of its has given up, or the limit is reached, none are
@@ -388,35 +392,44 @@ __device__ __forceinline__ void weigh(uint32_t keys, uint32_t first_term, uint32
     w *= next;
   }
 }
+// Magnitudes compare as whole numbers, so that a warp's largest takes one instruction.
+__device__ __forceinline__ uint32_t warp_top(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
+// A block's, by way of shared memory: the warps leave theirs before a barrier.
+__device__ __forceinline__ void leave_top(Control* c, int which, float x) {
+  if ((threadIdx.x & 31) == 0) c->top[which][threadIdx.x >> 5] = __float_as_uint(x);
+}
+__device__ __forceinline__ float top_of(const Control* c, int which) {
+  const uint4 a = reinterpret_cast<const uint4*>(c->top[which])[0], b = reinterpret_cast<const uint4*>(c->top[which])[1];
+  return __uint_as_float(max(max(max(a.x, a.y), max(a.z, a.w)), max(max(b.x, b.y), max(b.z, b.w))));
+}
+static_assert(kThreads == 256, "eight warps");
 // fp16: the largest finite magnitude among the thread's own granules of the keys, in the warp.
-// (An infinity must not set the range in which the others are kept.)
+// (An infinity must not set the range in which the others are kept; a maximum passes over
+// NaN.)
 template <int KD>
 __device__ __forceinline__ float top_key(uint32_t keys) {
   const Rows<KD> k;
-  uint32_t top = 0;  // magnitudes compare as whole numbers
-  auto in_warp = [&] {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-  };
+  __half2 most = __float2half2_rn(0.f);
 #pragma unroll
   for (int i = 0; i < k.kCount; ++i) {
     const uint4 v = get_granule(keys + k.at + i * k.kRows * 128);
     const uint32_t in[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) top = max(top, max(in[j] & 0x7fffu, in[j] >> 16 & 0x7fffu));
+    for (int j = 0; j < 4; ++j) most = __hmax2(most, __habs2(*reinterpret_cast<const __half2*>(&in[j])));
   }
-  in_warp();
-  if (top >= 0x7c00u) {
-    top = 0;
+  const float2 two = __half22float2(most);
+  uint32_t top = warp_top(__float_as_uint(fmaxf(two.x, two.y)));
+  if (top >= 0x7f800000u) {
+    float x = 0.f;
 #pragma unroll 1
     for (int i = 0; i < k.kCount * 8; ++i) {
       uint16_t v;
       asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(keys + k.at + (i / 8) * k.kRows * 128 + i % 8 * 2) : "memory");
-      if ((v & 0x7fffu) < 0x7c00u) top = max(top, v & 0x7fffu);
+      if ((v & 0x7fffu) < 0x7c00u) x = fmaxf(x, __half2float(__ushort_as_half(v & 0x7fffu)));
     }
-    in_warp();
+    top = warp_top(__float_as_uint(x));
   }
-  return __half2float(__ushort_as_half((unsigned short)top));
+  return __uint_as_float(top);
 }
 
 // ---- the state: [KD][64] in the products' layout, half of the columns a half of the warps.
@@ -463,10 +476,7 @@ struct State {
   __device__ __forceinline__ float top() const {
     constexpr float kMost = 3.402823466e38f;
     float x = 0.f;
-    auto in_warp = [&] {
-#pragma unroll
-      for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-    };
+    auto in_warp = [&] { x = __uint_as_float(warp_top(__float_as_uint(x))); };
 #pragma unroll
     for (int m = 0; m < kM; ++m)
 #pragma unroll
@@ -556,7 +566,7 @@ __device__ __forceinline__ void sum_part(const PartsArgs& p, const Part& part, i
   constexpr int kSets = KD == 64 ? 2 : 1;
   constexpr uint32_t kTerm = KD / 64 * kBlock, kSet = kTerm + kBlock;
   const uint32_t terms = kSets == 2 ? tiles + 2 * kSet : tiles;
-  const int h = blockIdx.y, warp = threadIdx.x >> 5;
+  const int h = blockIdx.y;
   const Span s = span_of(p.split, blockIdx.x);
   const float a = log2_decay(p.log_decay, h);
   const int64_t from = part.back ? s.start + s.n - 1 : s.start;
@@ -593,13 +603,9 @@ __device__ __forceinline__ void sum_part(const PartsArgs& p, const Part& part, i
     copies_wait<2 * (kSets - 1)>();
     float mul = part.mul, back = 1.f;
     if constexpr (kHalfType) {
-      const float m = top_key<KD>(keys);
-      if ((threadIdx.x & 31) == 0) c->top[i & 1][warp] = m;
+      leave_top(c, i & 1, top_key<KD>(keys));
       __syncthreads();
-      float x = 0.f;
-#pragma unroll
-      for (int w = 0; w < kThreads / 32; ++w) x = fmaxf(x, c->top[i & 1][w]);
-      const int e = exponent_of(x * fabsf(part.mul) * power2(a * (float)part.shift));
+      const int e = exponent_of(top_of(c, i & 1) * fabsf(part.mul) * power2(a * (float)part.shift));
       mul *= power_of_two(-e);
       back = power_of_two(e);
     }
@@ -793,9 +799,10 @@ struct Whole {  // outputs in fp32, or NULL
   float* p;             // as Output::p
   int64_t stride;
 };
-// inner + f outer of half a row: to memory in fp32, or as 32 T.
+// back inner (fp16, else inner) + f outer of half a row: to memory in fp32, or as 32 T.
 template <typename T>
-__device__ __forceinline__ void get_outputs(uint32_t tmem, float f, const Whole& whole, int pad, uint32_t (&w)[16]) {
+__device__ __forceinline__ void get_outputs(uint32_t tmem, float back, float f, const Whole& whole, int pad,
+                                            uint32_t (&w)[16]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = warp >> 2, row = (warp & 3) * 32 + lane;
   const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * 32;
   float x[32], y[32];
@@ -805,7 +812,9 @@ __device__ __forceinline__ void get_outputs(uint32_t tmem, float f, const Whole&
   loaded(y);
 #pragma unroll
   for (int j = 0; j < 32; j += 2) {
-    const float2 v = fma2(make_float2(y[j], y[j + 1]), both(f), make_float2(x[j], x[j + 1]));
+    float2 u = make_float2(x[j], x[j + 1]);
+    if (std::is_same<T, __half>::value) u = mul2(u, both(back));
+    const float2 v = fma2(make_float2(y[j], y[j + 1]), both(f), u);
     x[j] = v.x, x[j + 1] = v.y;
   }
   if (whole.p) {
@@ -854,23 +863,36 @@ __device__ __forceinline__ void put_outputs(uint32_t room, const uint32_t (&w)[1
   __syncwarp();
 }
 
-// fp16: powers of two that keep the state and the weighted keys in range, from the block's
-// largest ones; nothing for bf16.  Takes a barrier.
+// fp16: powers of two that keep the state, the weighted keys and the decayed scores in range,
+// from the block's largest ones; nothing for bf16.  A score is a sum of `channels` products,
+// and none is beyond that many times the largest query and key.
 struct Fit {
-  float state, state_back, key, key_back;
+  float state = 1.f, state_back = 1.f, key = 1.f, key_back = 1.f, score = 1.f, score_back = 1.f;
 };
+__device__ __forceinline__ void fit_scores(Fit& f, float top_query, float top_key, float channels) {
+  const int e = exponent_of(top_query * top_key * channels);
+  f.score = power_of_two(-e), f.score_back = power_of_two(e);
+}
+// Control::decay, which is read after a barrier.
+__device__ __forceinline__ void leave_decay(Control* c, float mul, float a) {
+  if (threadIdx.x < 32) c->decay[threadIdx.x] = mul * power2(a * (float)(31 - (int)threadIdx.x));
+}
+// keys: those that are weighted; score_weight: what the scores are multiplied by, times their
+// channels.  Takes a barrier.
 template <typename T, int KD>
-__device__ __forceinline__ Fit fit_of(Control* c, const State<KD>& st, uint32_t keys, float top_weight) {
-  Fit f{1.f, 1.f, 1.f, 1.f};
+__device__ __forceinline__ Fit fit_of(Control* c, const State<KD>& st, uint32_t keys, float top_weight, uint32_t queries,
+                                      float score_weight) {
+  Fit f;
   if constexpr (std::is_same<T, __half>::value) {
-    const float s = st.top(), k = top_key<KD>(keys);
-    if ((threadIdx.x & 31) == 0) c->top[0][threadIdx.x >> 5] = s, c->top[1][threadIdx.x >> 5] = k;
+    leave_top(c, 0, st.top());
+    leave_top(c, 1, top_key<KD>(keys));
+    leave_top(c, 2, top_key<KD>(queries));
     __syncthreads();
-    float x = 0.f, y = 0.f;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) x = fmaxf(x, c->top[0][w]), y = fmaxf(y, c->top[1][w]);
-    const int e = exponent_of(x), ke = exponent_of(y * fabsf(top_weight));
-    f = Fit{power_of_two(-e), power_of_two(e), power_of_two(-ke), power_of_two(ke)};
+    const float key = top_of(c, 1);
+    const int e = exponent_of(top_of(c, 0)), ke = exponent_of(key * fabsf(top_weight));
+    f.state = power_of_two(-e), f.state_back = power_of_two(e);
+    f.key = power_of_two(-ke), f.key_back = power_of_two(ke);
+    fit_scores(f, top_of(c, 2), key, fabsf(score_weight));
   }
   return f;
 }
@@ -907,6 +929,7 @@ __device__ __forceinline__ void form_outputs(const OutArgs& p, int slot, int h, 
   // a chunk comes while the one before is worked on, whose outputs leave through its keys'
   // tile while the next one's scores are formed; with 128 one set, and a tile for the
   // outputs, leave room for two blocks an SM instead.
+  constexpr bool kHalfType = std::is_same<T, __half>::value;
   constexpr uint32_t kSets = kOutSets<KD>, kSet = 2 * kKeys + kBlock;  // queries, keys, values
   const uint32_t state = tiles + kSets * kSet;
   const Span s = span_of(p.split, slot);
@@ -936,7 +959,8 @@ __device__ __forceinline__ void form_outputs(const OutArgs& p, int slot, int h, 
   };
   load_keys(0);
   load_others(0);
-  if (threadIdx.x < 64) c->decay[threadIdx.x] = threadIdx.x < 32 ? p.mul_inner * power2(a * (float)(31 - (int)threadIdx.x)) : 0.f;
+  if (threadIdx.x < 32) c->decay[32 + threadIdx.x] = 0.f;
+  if (!kHalfType) leave_decay(c, p.mul_inner, a);
   State<KD> st;
   const Stored src = stored(p.states, p.edge, p.Kp, p.Vp, p.K, p.V, p.transposed, (int64_t)slot * p.heads + h,
                             (int64_t)s.group * p.heads + h);
@@ -955,7 +979,8 @@ __device__ __forceinline__ void form_outputs(const OutArgs& p, int slot, int h, 
     const uint32_t queries = tiles + i % kSets * kSet, keys = queries + kKeys, values = keys + kKeys;
     const bool more = i + 1 < chunks;
     copies_wait<0>();
-    const Fit fit = fit_of<T, KD>(c, st, keys, top_weight);
+    const Fit fit = fit_of<T, KD>(c, st, keys, top_weight, queries, p.mul_inner * (float)p.K);
+    if (kHalfType) leave_decay(c, p.mul_inner * fit.score, a);
     st.template to_tile<T>(state, fit.state);
     publish();
     before_sync();
@@ -990,8 +1015,8 @@ __device__ __forceinline__ void form_outputs(const OutArgs& p, int slot, int h, 
     const Whole whole{WHOLE ? p.whole + ((tok - p.split.from) * p.heads + h) * p.Vp + e0 : nullptr,
                       step * p.heads * p.Vp};
     // (rows before the chunk's first token are not there)
-    get_outputs<T>(tmem, p.mul_state * fit.state_back * power2(a * (float)max(row + 1 - p.shift - pad, 0)), whole, pad,
-                   w);
+    get_outputs<T>(tmem, fit.score_back, p.mul_state * fit.state_back * power2(a * (float)max(row + 1 - p.shift - pad, 0)),
+                   whole, pad, w);
     if (more) {
       products.wait(2, update_phase);
       update_phase ^= 1;
@@ -1036,6 +1061,7 @@ constexpr int kKvSmem = 1024 + 6 * kBlock + 64 * 128;  // keys and queries twice
 
 template <typename T, bool WHOLE>
 __device__ __forceinline__ void form_kv(const KvArgs& p, int slot, int h, Control* c, uint32_t tiles, uint32_t tmem) {
+  constexpr bool kHalfType = std::is_same<T, __half>::value;
   // Keys and queries in two pairs of tiles in turn: the next chunk's come while this one's
   // last products are formed, its values and douts while its first scores are.  The weighted
   // queries' terms take the places of keys and values when these have been multiplied.  dv
@@ -1070,7 +1096,8 @@ __device__ __forceinline__ void form_kv(const KvArgs& p, int slot, int h, Contro
   load_queries(0);
   load_keys(0);
   load_others(0);
-  if (threadIdx.x < 64) c->decay[threadIdx.x] = threadIdx.x < 32 ? p.scale * power2(a * (float)(31 - (int)threadIdx.x)) : 0.f;
+  if (threadIdx.x < 32) c->decay[32 + threadIdx.x] = 0.f;
+  if (!kHalfType) leave_decay(c, p.scale, a);
   State<64> st;
   const Stored src = stored(p.states, p.edge, 64, 64, p.D, p.E, 0, (int64_t)slot * p.heads + h,
                             (int64_t)s.group * p.heads + h);
@@ -1087,7 +1114,8 @@ __device__ __forceinline__ void form_kv(const KvArgs& p, int slot, int h, Contro
     const bool more = i + 1 < chunks;
     const uint32_t keys = pairs + (i & 1) * 2 * kBlock, queries = keys + kBlock, other = pairs + (~i & 1) * 2 * kBlock;
     copies_wait<1>();  // (values and douts may be on their way)
-    const Fit fit = fit_of<T, 64>(c, st, queries, top_weight);
+    Fit fit = fit_of<T, 64>(c, st, queries, top_weight, keys, p.scale * (float)p.D);
+    if (kHalfType) leave_decay(c, p.scale * fit.score, a);
     st.template to_tile<T>(state, fit.state);
     publish();
     before_sync();
@@ -1112,6 +1140,7 @@ __device__ __forceinline__ void form_kv(const KvArgs& p, int slot, int h, Contro
       if (ph == 1 && more) weigh<T, 64, 2>(queries, keys, values - keys, a, 1, p.scale * fit.key);
       decay_scores<T>(tmem, c, a);
       if (ph == 0) copies_wait<1>();  // they are there, the next queries may be on their way
+      if (ph == 0 && kHalfType) leave_top(c, 0, top_key<64>(values)), leave_top(c, 1, top_key<64>(douts));
       publish();
       before_sync();
       __syncthreads();
@@ -1127,8 +1156,12 @@ __device__ __forceinline__ void form_kv(const KvArgs& p, int slot, int h, Contro
       if (ph == 1 && more) load_keys(i + 1);
       products.wait(1, ph);
       after_sync();
-      get_outputs<T>(tmem, f, Whole{WHOLE ? p.whole[1 - ph] + at : nullptr, -(int64_t)p.heads * 64}, pad, w);
+      get_outputs<T>(tmem, fit.score_back, f, Whole{WHOLE ? p.whole[1 - ph] + at : nullptr, -(int64_t)p.heads * 64}, pad, w);
       if (ph == 0) {
+        if (kHalfType) {
+          fit_scores(fit, top_of(c, 0), top_of(c, 1), fabsf(p.scale) * (float)p.E);
+          leave_decay(c, p.scale * fit.score, a);
+        }
         before_sync();
         __syncthreads();  // the sums in TMEM have been read
       } else if (more) {

@@ -224,7 +224,9 @@ gs_status gs_selftest_wgrad_timeout(int64_t tokens, int32_t rows, int32_t channe
  * the gate's rows and then up's:
  *   gate = x w_gate^T, up = x w_up^T, h = act(gate) * up
  * Neither gate nor up is written; gs_ffn_bwd forms them again from x.  x, w,
- * h, dh and dx are of one type, GS_BF16 or GS_F16; sums are fp32.  h may not
+ * h, dh and dx are of one type, GS_BF16 or GS_F16; sums are fp32 (the tensor
+ * cores cut them, by 2^-23 at most after every 16 terms; dw's in runs of 2048
+ * tokens, which are added with rounding).  h may not
  * overlap the inputs, nor may dx or dw overlap them or one another (an address
  * that is still read while it would be written is refused).
  *   workspace   gs_ffn_workspace_bytes(...) bytes (0: refused), 16-byte
@@ -270,10 +272,14 @@ gs_status gs_selftest_ffn_timeout(int64_t tokens, int32_t channels, int32_t hidd
  * k_heads), and has a decay and a state of its own.  Tokens outside the
  * groups (behind the last one) are neither read nor written.
  * q, k, v and what is written for them are of one type, GS_BF16 or GS_F16;
- * states and sums are fp32.  In fp16, products scale * q k and dout v (and
- * outputs) beyond 65504 become infinities; an infinity or a NaN in a token
- * spreads to the outputs and gradients of its group, some of those before it
- * among them.  1 <= dim, vdim <= GS_LINEAR_ATTN_MAX_DIM. */
+ * states and sums are fp32.  The chunked calls round two things to the type on
+ * the way, once each: the decayed products of queries and keys (backward also
+ * of values and dout), and the states where they are multiplied by a query or
+ * by dout, both in fp16 brought into its range by powers of two.  Outputs and
+ * gradients are then off by about sqrt(2) times their last rounding; states that
+ * are handed on have no such rounding.  An infinity or a NaN in a token spreads
+ * to the outputs and gradients of its group, some of those before it among
+ * them.  1 <= dim, vdim <= GS_LINEAR_ATTN_MAX_DIM. */
 #define GS_LINEAR_ATTN_MAX_DIM 128
 
 typedef struct gs_linear_attn {

@@ -79,3 +79,23 @@ def test_a_broken_channel_leaves_the_others(gs, dt, bad, T, D, E):
     long._close(got["d0"], want["d0"], tol["d0"], "d0")
     early = slice(0, at)  # (a key has no part in the outputs before it)
     long._close(got["out"][early], want["out"][early], tol["out"][early], "out")
+
+
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("D,E", [(64, 64), (128, 128), (72, 41)])
+@pytest.mark.parametrize("qs,ks,vs,dos", [
+    (300.0, 300.0, 2.0 ** -10, 2.0 ** -10),        # products of queries and keys past 65504
+    (2.0 ** -10, 2.0 ** -10, 2.0 ** 8, 2.0 ** -6),  # and below 2^-14
+    (2.0 ** -6, 2.0 ** -6, 300.0, 300.0),          # of values and their outputs' gradients
+    (2.0 ** 6, 2.0 ** 4, 2.0 ** -12, 2.0 ** -8),
+])
+def test_products_beyond_the_types_range(gs, dt, D, E, qs, ks, vs, dos):
+    """Outputs and gradients are in the type's range; the products on their way are not."""
+    T, H, scale = 300, 2, D ** -0.5
+    q, k, v, do, s0, ds, a = _inputs(T, H, D, E, dt, E)
+    q, k, v, do = ((x.float() * s).to(dt) for x, s in ((q, qs), (k, ks), (v, vs), (do, dos)))
+    want, tol = _bounds(q, k, v, do, s0, ds, a, scale, dt)
+    got = _run(gs, q, k, v, do, s0, ds, a, scale)
+    assert all(float(want[n].abs().max()) < 60000 for n in ("out", "dq", "dk", "dv"))
+    for n in want:
+        long._close(got[n], want[n], tol[n], n)
