@@ -1032,7 +1032,8 @@ gs_status few_of(const Few& p, bool wide, cudaStream_t st) {
                                                                          : few_of<T, ACT, 4>(p, wide, st);
 }
 // (1024 x 2816, 16 and 32 tokens: 5.7 and 7.9 us, on the tensor cores' tiles 8.9;
-// 2048 x 5632: 14.4 and 19.7, 14.0)
+// 2048 x 5632: 14.4 and 19.7, 14.0.  Rows that start anywhere, which the tiles have copied
+// first: 1023 x 2815, 15.2 and 14.6, 16.4; 2047 x 5631, 16 tokens 42, on the tiles 40.)
 bool few(const Args& a) {
   return a.tokens <= 16 || (a.tokens <= 32 && (int64_t)a.channels * a.hidden <= (1 << 22));
 }

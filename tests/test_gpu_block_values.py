@@ -99,3 +99,23 @@ def test_products_beyond_the_types_range(gs, dt, D, E, qs, ks, vs, dos):
     assert all(float(want[n].abs().max()) < 60000 for n in ("out", "dq", "dk", "dv"))
     for n in want:
         long._close(got[n], want[n], tol[n], n)
+
+
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("D,E", [(64, 64), (128, 128)])
+def test_decays_that_leave_nothing(gs, dt, D, E):
+    """log_decay of minus infinity: a token's output is its own product, and the state its own
+    key and value; beside it a head without a decay."""
+    T, H, scale = 300, 2, D ** -0.5
+    q, k, v, do, s0, ds, _ = _inputs(T, H, D, E, dt, D)
+    a = torch.tensor([float("-inf"), 0.0], device="cuda")
+    want, tol = _bounds(q, k, v, do, s0, ds, a.clamp(min=-1e9), scale, dt)
+    got = _run(gs, q, k, v, do, s0, ds, a, scale)
+    for n in want:
+        long._close(got[n], want[n], tol[n], n)
+    own = scale * (q.double() * k.double()).sum(-1, keepdim=True) * v.double()
+    assert (got["out"][:, 0].double() - own[:, 0]).norm() <= 2 * EPS[dt] * own[:, 0].norm()
+    s, out = s0.clone(), torch.empty_like(do[:1])
+    gs.gs_linear_attn_step(q[:1], k[:1], v[:1], a, s, out, scale=scale)
+    assert torch.equal(s[0, 0], k[0, 0, :, None].float() * v[0, 0].float())
+    assert (out[0, 0].double() - own[0, 0]).norm() <= 2 * EPS[dt] * own[0, 0].norm()
