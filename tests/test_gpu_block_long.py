@@ -353,3 +353,45 @@ def test_tokens_outside_the_groups_are_not_read(gs, back):
     used = ws[:ws.numel() // 2 * 2].view(dt)
     assert (used != 0).any() and not (used == mark).any()
     assert all((x[:5] == 9.0).all() and (x[101:] == 9.0).all() for x in out)
+
+
+def test_ranges_captured_and_on_another_stream(gs):
+    """Shared heads with little room: replayed with other inputs, and on a stream beside one that
+    is busy with the same inputs and a workspace of its own."""
+    T, H, K, D, dt = 1500, 8, 2, 64, torch.bfloat16
+    g = torch.Generator(device="cuda").manual_seed(2)
+    q, k, v, do = (torch.randn(T, h, D, generator=g, device="cuda").to(dt) for h in (H, K, K, H))
+    a = torch.linspace(-1.0, 0.0, H, device="cuda")
+    offs = torch.tensor([0, 300, 1450], dtype=torch.int32, device="cuda")
+    size = gs.gs_linear_attn_workspace_bytes(T, H, K, D, D, 2)
+    small = size - 500 * 4 * H * 128
+    rooms = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(2)]
+
+    def run(out, room, n, stream=None):
+        gs.gs_linear_attn_bwd(q, k, v, a, do, *out, group_offsets=offs, workspace=room[:n], stream=stream)
+
+    new = lambda: [torch.zeros_like(x) for x in (q, k, v)]  # noqa: E731
+    want, got, other = new(), new(), new()
+    run(got, rooms[0], small)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(got, rooms[0], small)
+    for _ in range(3):
+        for x in (q, k, v, do):
+            x.copy_(x.flip(0))
+        run(want, rooms[0], size)
+        for x in got:
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(want, got))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for x in got:
+        x.zero_()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        run(got, rooms[0], small)
+        run(other, rooms[1], small, stream=side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) and torch.equal(x, z) for x, y, z in zip(want, got, other))
