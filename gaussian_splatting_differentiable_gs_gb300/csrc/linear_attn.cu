@@ -1384,10 +1384,11 @@ size_t modest(const gs_linear_attn* a) {
   square.groups = a->groups + 1;
   return two_states(&square, 64);
 }
-bool in_two_ranges(const gs_linear_attn* a, int64_t seg) {
+// How many ranges that makes.
+int64_t modest_ranges(const gs_linear_attn* a, int64_t seg) {
   const size_t all = modest(a), states = two_states(a, seg);
   const int64_t range = range_of(a, a->groups > 1, seg, room_for(a, all > states ? all - states : 0));
-  return !a->tokens || (range && div_up(a->tokens, range) <= 2);
+  return range ? div_up(a->tokens, range) : a->tokens ? INT64_MAX : 1;
 }
 
 // Tokens of a segment.  A chunk of the outputs or of the queries' gradients costs two units
@@ -1408,7 +1409,7 @@ int32_t segment_tokens(const gs_linear_attn* a, bool backward, bool states) {
   int best = 16;
   int64_t cost = INT64_MAX;
   for (int m = 1; m <= 16; ++m) {
-    if (shared && !in_two_ranges(a, m * kL)) continue;  // (states of longer segments take less room)
+    if (shared && modest_ranges(a, m * kL) > 4) continue;
     const bool alone = longest <= m;
     const int64_t n = alone ? longest : m, segments = a->groups * (alone ? 1 : div_up(chunks, m));
     const int64_t sums = segments * a->q_heads * tiles * (backward ? 2 : 1);
@@ -1423,6 +1424,11 @@ int32_t segment_tokens(const gs_linear_attn* a, bool backward, bool states) {
     }
     if (c < cost) cost = c, best = m;
   }
+  // Few tokens in groups, whose gradients would take several ranges, are a segment a group: no
+  // sums, no scan, one range.  (262 tokens in 2 groups, 32 heads of 32 over 8: 31 us, in segments
+  // of a chunk 70, or 45 with more room; 700 tokens, 8 heads of 64 over 4: 41, 64 and 44; launched and
+  // waited for.)
+  if (shared && a->groups > 1 && a->tokens <= 6 * kL && modest_ranges(a, best * kL) > 1) best = (int)div_up(a->tokens, kL);
   return best * kL;
 }
 
@@ -1777,8 +1783,9 @@ extern "C" size_t gs_linear_attn_workspace_bytes(const gs_linear_attn* a, int32_
     const Call c(a, backward != 0, states != 0);
     size_t n = Room(nullptr, a, c.slots, backward != 0, backward ? 15 : 7, 0).bytes;
     if (backward && c.rep > 1) {
-      // as few ranges as a modest room allows, four at most
-      const int64_t left = room_for(a, modest(a) > n ? modest(a) - n : 0), least = div_up(a->tokens, 4) + 2 * c.split.seg;
+      // as few ranges as a modest room allows, four at most, and one of up to 4096 tokens
+      const int64_t left = room_for(a, modest(a) > n ? modest(a) - n : 0);
+      const int64_t quarter = div_up(a->tokens, 4) + 2 * c.split.seg, least = quarter > 4096 ? quarter : 4096;
       const int64_t joined = left > least ? left : least;
       n = Room(nullptr, a, c.slots, true, 15, joined < a->tokens ? joined : a->tokens).bytes;
     }
