@@ -358,8 +358,8 @@ __device__ __forceinline__ int64_t dw_row(const Job& p, int64_t n) {
 //
 // Bound by the tensor cores, and in long loops by the power that they may take.  32640 tokens
 // x 1024 channels x 2816 hidden, bf16, 188.3 GFLOP each: forward 195 us (tensor cores 96 % of
-// the cycles; 220 in long loops), dx 204 (95 %; 416 MB read), dW 204 (94 %; 650 MB read),
-// recompute 235 (83 %: its tiles' way out, dh in and dgate and dup out by way of shared
+// the cycles; 220 in long loops), dx 208 (95 %; 416 MB read), dW 212 (93 %; 653 MB read),
+// recompute 240 (81 %: its tiles' way out, dh in and dgate and dup out by way of shared
 // memory, takes longer than the next tile's products).  5003 x 997 x 1361, fp16: 34, 30 and 28 us, half of them
 // start, end and the shares of 80 tiles among 76 pairs.
 template <typename T, typename TO, int MODE, int ACT>

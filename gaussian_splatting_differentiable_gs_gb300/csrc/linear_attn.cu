@@ -1224,7 +1224,7 @@ struct JoinArgs {
 };
 // Four channels of a token's head a thread.  Bound by the bytes.  (A block that goes through
 // a key head's query heads itself, its sums in memory between them, needs no such kernel,
-// but takes longer: 32640 tokens, 16 heads of 64 over 4, 543 us, in this way 309.)
+// but takes longer: 32640 tokens, 16 heads of 64 over 4, 543 us, in this way 306.)
 template <typename T>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ JoinArgs p) {
   launch_dependents();

@@ -219,8 +219,8 @@ gs_status gs_selftest_wgrad_timeout(int64_t tokens, int32_t rows, int32_t channe
                                     void* workspace, size_t ws_bytes, int32_t steps, void* stream);
 
 /* ---------------------------------------------------------------------- */
-/* The gated feed-forward block: both projections, the activation and the
- * product in one kernel on the tensor cores.  With w [2 hidden][channels],
+/* The gated feed-forward block up to its last projection: both first ones, the
+ * activation and the product in one kernel on the tensor cores.  With w [2 hidden][channels],
  * the gate's rows and then up's:
  *   gate = x w_gate^T, up = x w_up^T, h = act(gate) * up
  * Neither gate nor up is written; gs_ffn_bwd forms them again from x.  x, w,
