@@ -1368,11 +1368,11 @@ int64_t room_for(const gs_linear_attn* a, size_t bytes) {
   const int64_t n = (int64_t)(bytes / (sizeof(float) * a->q_heads * (padded_dim(a->dim) + padded_dim(a->vdim))));
   return n < a->tokens ? n : a->tokens;
 }
-// Tokens of a range, all of about the same length (0: there is no room for one).
+// Tokens of a range, a segment at least, all of about the same length (0: there is no room).
 int64_t range_of(const gs_linear_attn* a, bool anywhere, int64_t seg, int64_t room) {
   if (room >= a->tokens) return a->tokens;
   const int64_t most = anywhere ? room - seg : room / seg * seg;
-  if (most <= 0) return 0;
+  if (most < seg) return 0;
   const int64_t even = div_up(a->tokens, div_up(a->tokens, most));
   return anywhere ? even : div_up(even, seg) * seg;
 }
